@@ -954,6 +954,109 @@ int repops_rope_f32(int64_t rows, int64_t heads, int64_t pairs, float *x, int64_
                     const float *cos_tab, const float *sin_tab, int64_t positions, int64_t first,
                     int64_t period, int inverse, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Rows in 8 bits                                                            */
+/* "Verde与RepOps" §5.3 (lower-precision training as future work), §4.3      */
+/* (training: the activations a backward pass needs).  The pages fix no      */
+/* format; the library's: whole numbers q in [-127, 127] with a binary32     */
+/* scale for every `group` consecutive columns of a row (the last group may  */
+/* be shorter), or for the whole row (group 0); q stands for fl(q * scale).  */
+/* group is 0, 32, 64, 128 or 256.  Scales: rows x groups, pitch lds >=      */
+/* groups = ceil(cols / group), or 1.                                        */
+/* ------------------------------------------------------------------------ */
+
+/* q, scale <- the rows of x (stored as x_type, widened exactly), for every
+ * group, each step one binary32 rounding:
+ *   amax = max |x|,  a = max(amax, 2^-100),
+ *   scale = fl(a / 127),  q = rint(fl(x * fl(127 / a))), ties to even.
+ * A group that holds an infinity or a NaN gets scale NaN and q = 0.  A finite
+ * value comes back within scale * (1/2 + 2^-14) (the floor 2^-100 keeps 127 / a
+ * finite; a group of zeros stays zeros).  x, q, scale: device, row pitches ldx, ldq >= cols and
+ * lds; outputs must not overlap x or each other (ALIAS).  INVALID_ARG for
+ * negative sizes, cols above 2^31 - 1, unknown types or groups, null pointers
+ * or short pitches. */
+int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
+                            int64_t group, int8_t *q, int64_t ldq, float *scale, int64_t lds,
+                            cudaStream_t stream);
+
+/* x = fl(q * scale), narrowed once to x_type.  x must not overlap q or scale
+ * (ALIAS); other errors as repops_quantize_rows_i8. */
+int repops_dequantize_rows_i8(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq,
+                              const float *scale, int64_t lds, int64_t group, void *x, int x_type,
+                              int64_t ldx, cudaStream_t stream);
+
+/* repops_swiglu_backward_f32 with g and u in 8 bits (the same group): the bits
+ * of that call on the restored rows.  h (optional): also the forward's
+ * fl(SiLU(g) * u).  One of dg, du, h may be dh itself (same pointer and
+ * pitch); any other overlap of an output with an input or another output is
+ * ALIAS. */
+int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_t *g, int64_t ldg,
+                              const float *g_scale, int64_t ldgs, const int8_t *u, int64_t ldu,
+                              const float *u_scale, int64_t ldus, int64_t group, const float *dh,
+                              int64_t lddh, float *dg, int64_t lddg, float *du, int64_t lddu,
+                              float *h, int64_t ldh, cudaStream_t stream);
+
+/* repops_rmsnorm_backward_f32 with x in 8 bits, and its column sum: dx (+ res)
+ * and dgamma = repops_colsum_f32 of dy * xhat, the bits of those calls on the
+ * restored rows, without dy * xhat passing through memory.  h (optional): also
+ * the forward's (x * inv) * gamma.  dgamma: cols floats.  ws: device scratch of
+ * ..._workspace_bytes(rows, cols) bytes on a 16-byte boundary (a shorter one is
+ * INVALID_ARG), or NULL to take it from the scratch pool on `stream` (ALLOC
+ * when refused); its contents before and after mean nothing.  dx may be res
+ * itself (same pitch); any other overlap is ALIAS.  cols up to 393216
+ * (UNSUPPORTED beyond). */
+uint64_t repops_rmsnorm_backward_i8_workspace_bytes(int64_t rows, int64_t cols);
+int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int64_t ldx,
+                               const float *x_scale, int64_t lds, int64_t group, const float *gamma,
+                               float eps, const float *dy, int64_t lddy, const float *res,
+                               int64_t ldres, float *dx, int64_t lddx, float *h, int64_t ldh,
+                               float *dgamma, void *ws, uint64_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The edge between two blocks                                               */
+/* "Verde与RepOps" §4.3 (Llama-style training): the norm after a block, its  */
+/* gate and residual scale, the residual sum and the norm before the next    */
+/* block, fused.  Composition of the operators above, bit for bit.           */
+/* ------------------------------------------------------------------------ */
+
+/* For every row r, every step one binary32 rounding:
+ *   p = RMSNorm(f; post_gain) as repops_rmsnorm_rows_f32   (post_gain NULL: p = f)
+ *   t = fl(p * gate[r / gate_rows][j])                     (gate NULL: t = p)
+ *   y = fl(x + fl(alpha * t))
+ *   h = RMSNorm(y; pre_gain)                               (pre_gain NULL: no h)
+ * x, f, y, h: rows x cols with their own pitches; gains: cols floats; gate:
+ * rows / gate_rows rows at pitch ldgate, each for gate_rows consecutive rows
+ * (gate_rows must divide rows).  y and h may each be x or f itself (same
+ * pointer and pitch); they must not overlap each other, nor an input otherwise
+ * (ALIAS).  INVALID_ARG also when only one of pre_gain and h is NULL; cols up
+ * to 393216 (UNSUPPORTED beyond). */
+int repops_rmsnorm_residual_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx,
+                                const float *f, int64_t ldf, const float *post_gain,
+                                const float *gate, int64_t ldgate, int64_t gate_rows, float alpha,
+                                const float *pre_gain, float eps, float *y, int64_t ldy, float *h,
+                                int64_t ldh, cudaStream_t stream);
+
+/* Its backward from f and the forward's y, given dy = dL/dy (past the norm;
+ * NULL: none) and dh = dL/dh (NULL exactly when pre_gain, y and dpre are):
+ *   dx  = RMSNorm'(y; dh) + dy          as repops_rmsnorm_backward_f32 with res = dy
+ *   dp  = fl(fl(dx * alpha) * gate)
+ *   df  = RMSNorm'(f; dp)               (post_gain NULL: df = dp)
+ *   dpre  = colsum(dh * yhat),  dpost = colsum(dp * fhat)
+ *   dgate[g] = colsum over the rows of gate row g of fl(fl(dx * alpha) * p)
+ * (a sum as repops_colsum_f32 of those rows' terms).  dpre, dpost: cols floats
+ * (dpost NULL exactly when post_gain is); dgate: rows / gate_rows x cols at
+ * pitch lddgate (NULL exactly when gate is).  ws as
+ * repops_rmsnorm_backward_i8, of ..._workspace_bytes(rows, cols, gate rows)
+ * bytes (0 gate rows without a gate).  dx may be dy itself (same pitch); any
+ * other overlap is ALIAS.  Limits as the forward's. */
+uint64_t repops_rmsnorm_residual_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t gates);
+int repops_rmsnorm_residual_backward_f32(
+    int64_t rows, int64_t cols, const float *dy, int64_t lddy, const float *dh, int64_t lddh,
+    const float *y, int64_t ldy, const float *f, int64_t ldf, const float *post_gain,
+    const float *gate, int64_t ldgate, int64_t gate_rows, float alpha, const float *pre_gain,
+    float eps, float *dx, int64_t lddx, float *df, int64_t lddf, float *dpre, float *dpost,
+    float *dgate, int64_t lddgate, void *ws, uint64_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,12 @@ memory and streams.
   swiglu / swiglu_backward /        SiLU-gated MLP activation and rotary
   rope_frequencies / rope_table /   position embeddings of a Llama-style layer
   rope                              ("Verde与RepOps" §4.3)
+  quantize_rows / dequantize_rows   rows in 8 bits with a scale a group: activation
+                                    checkpoints, and gemm_i8's operands
+  swiglu_backward_i8 /              backward operators that read such rows
+  rmsnorm_backward_i8               ("Verde与RepOps" §4.3, §5.3)
+  rmsnorm_residual /                the edge between two blocks in one pass: norm,
+  rmsnorm_residual_backward         gate, residual scale and sum, next norm
   host_empty(shape, dtype)          page-locked host memory in huge pages for the
                                     host-buffer calls (gemm_host, ..._host)
 """
@@ -44,6 +50,8 @@ __all__ = ["load", "version", "scratch_set_keep_bytes", "scratch_release", "scra
            "softmax_rows", "layernorm_rows", "rmsnorm_rows", "gelu", "gemm_batched",
            "convert", "gemm_typed", "rolling_hash", "TYPE_F32", "TYPE_F16", "TYPE_BF16",
            "colsum", "gelu_backward", "rmsnorm_backward", "softmax_backward",
+           "quantize_rows", "dequantize_rows", "swiglu_backward_i8", "rmsnorm_backward_i8",
+           "rmsnorm_residual", "rmsnorm_residual_backward",
            "swiglu", "swiglu_backward", "rope_frequencies", "rope_table", "rope",
            "device_status", "set_thread_status_word", "RepopsError", "ACT_NONE", "ACT_GELU",
            "LOADER_AUTO", "LOADER_TMA", "LOADER_CPASYNC", "LOADER_DIRECT", "MEAN_MAX_CONTRIBUTORS"]
@@ -931,3 +939,243 @@ def rope(x, heads: int, cos, sin, *, first: int = 0, period: int = None, inverse
                                 int(first), per, int(bool(inverse)), _stream_handle(stream))
     _capi.check(rc, "repops_rope_f32")
     return x
+
+
+def _on_device(**tensors):
+    """Every given tensor (None skipped) must live on the current CUDA device,
+    where the call's kernels run."""
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError("%s must be a tensor on the current CUDA device" % name)
+
+
+def _groups(cols, group):
+    if group not in (0, 32, 64, 128, 256):
+        raise ValueError("group must be 0 (one scale a row), 32, 64, 128 or 256")
+    return -(-cols // group) if group else 1
+
+
+def _rows_i8(q, scale, group, name):
+    """(pointer, pitch, scale pointer, scale pitch) of rows in 8 bits: q int8
+    (rows, cols) and scale float32 (rows, groups), unit column strides (a
+    column block of wider rows is fine where it starts on a group)."""
+    import torch
+    if q.dtype != torch.int8 or q.dim() != 2 or (q.shape[1] > 1 and q.stride(1) != 1):
+        raise ValueError("%s must be a 2-D int8 CUDA tensor with unit column stride" % name)
+    n = _groups(q.shape[1], group)
+    if scale.dtype != torch.float32 or tuple(scale.shape) != (q.shape[0], n) or (n > 1 and scale.stride(1) != 1):
+        raise ValueError("the scales of %s must be float32 of shape (rows, %d) with unit column stride" % (name, n))
+    return q.data_ptr(), max(q.stride(0), q.shape[1], 1), scale.data_ptr(), max(scale.stride(0), n, 1)
+
+
+def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
+    """(q, scale): the rows of x (2-D float32, float16 or bfloat16 CUDA, unit
+    column stride) in 8 bits (repops_quantize_rows_i8): q int8 like x, scale
+    float32 (rows, groups) with one value for every `group` columns (32, 64,
+    128, 256) or a row (0).  q * scale stands for x."""
+    import torch
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a 2-D CUDA tensor with unit column stride")
+    t = _storage_type(x.dtype)
+    rows, cols = x.shape
+    n = _groups(cols, group)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((rows, n), dtype=torch.float32, device=x.device)
+    _on_device(x=x, out=out, scale=scale)
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError("out must have the shape of x")
+    pq, ldq, ps, lds = _rows_i8(out, scale, group, "out")
+    rc = load().repops_quantize_rows_i8(rows, cols, x.data_ptr(), t, max(x.stride(0), cols, 1), group, pq, ldq, ps, lds,
+                                        _stream_handle(stream))
+    _capi.check(rc, "repops_quantize_rows_i8")
+    return out, scale
+
+
+def dequantize_rows(q, scale, *, group: int = 0, dtype=None, out=None, stream=None):
+    """The values rows in 8 bits stand for, fl(q * scale), as float32 (default),
+    float16 or bfloat16 (repops_dequantize_rows_i8)."""
+    import torch
+    pq, ldq, ps, lds = _rows_i8(q, scale, group, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype or torch.float32, device=q.device)
+    if tuple(out.shape) != tuple(q.shape) or (dtype is not None and out.dtype != dtype) or \
+            (out.shape[1] > 1 and out.stride(1) != 1):
+        raise ValueError("out must have the shape of q, the dtype asked for and unit column stride")
+    _on_device(q=q, scale=scale, out=out)
+    rc = load().repops_dequantize_rows_i8(q.shape[0], q.shape[1], pq, ldq, ps, lds, group, out.data_ptr(),
+                                          _storage_type(out.dtype), max(out.stride(0), q.shape[1], 1),
+                                          _stream_handle(stream))
+    _capi.check(rc, "repops_dequantize_rows_i8")
+    return out
+
+
+def _row_like(t, shape, name):
+    """(pointer, pitch) of an optional float32 operand of `shape`."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
+    return _row_operand(t, name)
+
+
+def _gain(t, cols, name):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != cols or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 vector of one value per column" % name)
+    return t.data_ptr()
+
+
+def swiglu_backward_i8(g, g_scale, u, u_scale, dh, dg=None, du=None, *, group: int, h=None, stream=None):
+    """(dg, du) of h = SiLU(g) * u with g and u in 8 bits: swiglu_backward of the
+    restored rows, bit for bit (repops_swiglu_backward_i8).  h: an optional
+    tensor that receives swiglu(g, u) as well.  One of dg, du, h may be dh."""
+    import torch
+    pg, ldg, pgs, ldgs = _rows_i8(g, g_scale, group, "g")
+    pu, ldu, pus, ldus = _rows_i8(u, u_scale, group, "u")
+    if tuple(u.shape) != tuple(g.shape):
+        raise ValueError("g and u differ in shape")
+    pd, ldd = _row_like(dh, g.shape, "dh")
+    dg = torch.empty(g.shape, dtype=torch.float32, device=g.device) if dg is None else dg
+    du = torch.empty(g.shape, dtype=torch.float32, device=g.device) if du is None else du
+    pdg, lddg = _row_like(dg, g.shape, "dg")
+    pdu, lddu = _row_like(du, g.shape, "du")
+    ph, ldh = _row_like(h, g.shape, "h")
+    _on_device(g=g, g_scale=g_scale, u=u, u_scale=u_scale, dh=dh, dg=dg, du=du, h=h)
+    rc = load().repops_swiglu_backward_i8(g.shape[0], g.shape[1], pg, ldg, pgs, ldgs, pu, ldu, pus, ldus, group, pd, ldd,
+                                          pdg, lddg, pdu, lddu, ph, ldh, _stream_handle(stream))
+    _capi.check(rc, "repops_swiglu_backward_i8")
+    return dg, du
+
+
+def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, group: int, res=None, h=None, stream=None):
+    """(dx, dgamma) of RMSNorm rows whose input x is kept in 8 bits: the bits of
+    rmsnorm_backward on the restored rows and of colsum(dy * xhat)
+    (repops_rmsnorm_backward_i8).  res: added to dx (may be dx); h: an optional
+    tensor that receives the norm's output again."""
+    import torch
+    px, ldx, pxs, lds = _rows_i8(x, x_scale, group, "x")
+    rows, cols = x.shape
+    pd, ldd = _row_like(dy, x.shape, "dy")
+    pr, ldr = _row_like(res, x.shape, "res")
+    dx = torch.empty(x.shape, dtype=torch.float32, device=x.device) if dx is None else dx
+    dgamma = torch.empty(cols, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
+    pdx, lddx = _row_like(dx, x.shape, "dx")
+    ph, ldh = _row_like(h, x.shape, "h")
+    _on_device(x=x, x_scale=x_scale, gamma=gamma, dy=dy, res=res, dx=dx, h=h, dgamma=dgamma)
+    if rows == 0 or cols == 0:
+        return dx, dgamma.zero_()
+    L = load()
+    need = L.repops_rmsnorm_backward_i8_workspace_bytes(rows, cols)
+    ws = _workspace(need, x.device, stream)
+    rc = L.repops_rmsnorm_backward_i8(rows, cols, px, ldx, pxs, lds, group, _gain(gamma, cols, "gamma"),
+                                      ctypes.c_float(eps), pd, ldd, pr, ldr, pdx, lddx, ph, ldh,
+                                      _gain(dgamma, cols, "dgamma"), ws.data_ptr() if ws is not None else None, need,
+                                      _stream_handle(stream))
+    _capi.check(rc, "repops_rmsnorm_backward_i8")
+    return dx, dgamma
+
+
+def _gate_rows(gate, rows, cols):
+    """(pointer, pitch, rows that share a gate row, gate rows)."""
+    if gate is None:
+        return None, 0, 1, 0
+    g = gate.view(1, -1) if gate.dim() == 1 else gate
+    if g.dim() != 2 or g.shape[1] != cols or g.shape[0] < 1 or rows % g.shape[0]:
+        raise ValueError("gate must be (cols,) or (G, cols) with G dividing the rows")
+    p, ld = _row_operand(g, "gate")
+    return p, ld, max(rows // g.shape[0], 1), g.shape[0]
+
+
+def rmsnorm_residual(x, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=None, alpha: float = 1.0, y=None,
+                     h=None, stream=None):
+    """(y, h) of the edge between two blocks (repops_rmsnorm_residual_f32):
+
+        y = x + alpha * (gate * RMSNorm(f; post_gain)),   h = RMSNorm(y; pre_gain)
+
+    x, f: 2-D float32 CUDA, unit column stride.  post_gain, gate, pre_gain may
+    be None (no norm of f, no gate, no h: h is then returned as None).  gate:
+    (cols,), or (G, cols) with one row for each G-th of the rows in order (a
+    gate a sequence, or with G = rows a gate a token).  y and h may each be x or
+    f itself."""
+    import torch
+    rows, cols = x.shape
+    px, ldx = _row_operand(x, "x")
+    pf, ldf = _row_like(f, x.shape, "f")
+    pg, ldg, per, _ = _gate_rows(gate, rows, cols)
+    y = torch.empty(x.shape, dtype=torch.float32, device=x.device) if y is None else y
+    if pre_gain is None:
+        if h is not None:
+            raise ValueError("h needs pre_gain")
+    elif h is None:
+        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+    py, ldy = _row_like(y, x.shape, "y")
+    ph, ldh = _row_like(h, x.shape, "h")
+    _on_device(x=x, f=f, pre_gain=pre_gain, post_gain=post_gain, gate=gate, y=y, h=h)
+    rc = load().repops_rmsnorm_residual_f32(rows, cols, px, ldx, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg,
+                                            per, ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"),
+                                            ctypes.c_float(eps), py, ldy, ph, ldh, _stream_handle(stream))
+    _capi.check(rc, "repops_rmsnorm_residual_f32")
+    return y, h
+
+
+def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=None,
+                              alpha: float = 1.0, dx=None, df=None, dpre=None, dpost=None, dgate=None, stream=None):
+    """(dx, df, dpre_gain, dpost_gain, dgate) of rmsnorm_residual given its y, f
+    and the gradients dy (past the norm; None: none) and dh of its results
+    (repops_rmsnorm_residual_backward_f32); an entry is None where the forward
+    had no such operand.  dx may be dy.  pre_gain None: dh and y are not used."""
+    import torch
+    if pre_gain is None:
+        dh = y = dpre = None
+        if dy is None:
+            raise ValueError("without pre_gain, dy is the only gradient and must be given")
+    elif dh is None or y is None:
+        raise ValueError("with pre_gain, dh and y must be given")
+    rows, cols = f.shape
+    pf, ldf = _row_operand(f, "f")
+    pdy, lddy = _row_like(dy, f.shape, "dy")
+    pdh, lddh = _row_like(dh, f.shape, "dh")
+    py, ldy = _row_like(y, f.shape, "y")
+    pg, ldg, per, gates = _gate_rows(gate, rows, cols)
+
+    def new(*shape):
+        return torch.empty(shape, dtype=torch.float32, device=f.device)
+
+    dx = new(rows, cols) if dx is None else dx
+    df = new(rows, cols) if df is None else df
+    dpre = new(cols) if dpre is None and pre_gain is not None else dpre
+    if post_gain is None:
+        dpost = None
+    elif dpost is None:
+        dpost = new(cols)
+    if gate is None:
+        dgate = None
+    elif dgate is None:
+        dgate = torch.empty(gate.shape, dtype=torch.float32, device=f.device)
+    elif tuple(dgate.shape) != tuple(gate.shape):
+        raise ValueError("dgate must have the shape of gate")
+    pdx, lddx = _row_like(dx, f.shape, "dx")
+    pdf, lddf = _row_like(df, f.shape, "df")
+    pdg, lddg, _, _ = _gate_rows(dgate, rows, cols)
+    _on_device(dy=dy, dh=dh, y=y, f=f, pre_gain=pre_gain, post_gain=post_gain, gate=gate, dx=dx, df=df, dpre=dpre,
+               dpost=dpost, dgate=dgate)
+    if rows == 0 or cols == 0:
+        for t in (dpre, dpost, dgate):
+            if t is not None:
+                t.zero_()
+        return dx, df, dpre, dpost, dgate
+    L = load()
+    need = L.repops_rmsnorm_residual_backward_workspace_bytes(rows, cols, gates)
+    ws = _workspace(need, f.device, stream)
+    rc = L.repops_rmsnorm_residual_backward_f32(
+        rows, cols, pdy, lddy, pdh, lddh, py, ldy, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg, per,
+        ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"), ctypes.c_float(eps), pdx, lddx, pdf, lddf,
+        _gain(dpre, cols, "dpre"), _gain(dpost, cols, "dpost"), pdg, lddg, ws.data_ptr() if ws is not None else None,
+        need, _stream_handle(stream))
+    _capi.check(rc, "repops_rmsnorm_residual_backward_f32")
+    return dx, df, dpre, dpost, dgate

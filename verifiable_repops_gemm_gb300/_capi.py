@@ -37,6 +37,19 @@ SIGNATURES = {
     "repops_scratch_set_keep_bytes": (_i32, [ctypes.c_uint64]),
     "repops_scratch_release": (_i32, []),
     "repops_scratch_reserved_bytes": (_i32, [_vp]),
+    "repops_quantize_rows_i8": (_i32, [_i64, _i64, _vp, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "repops_dequantize_rows_i8": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _vp]),
+    "repops_swiglu_backward_i8": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                         _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "repops_rmsnorm_backward_i8_workspace_bytes": (_u64, [_i64, _i64]),
+    "repops_rmsnorm_backward_i8": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _f32, _vp, _i64, _vp, _i64,
+                                          _vp, _i64, _vp, _i64, _vp, _vp, _u64, _vp]),
+    "repops_rmsnorm_residual_f32": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _f32,
+                                           _vp, _i64, _vp, _i64, _vp]),
+    "repops_rmsnorm_residual_backward_workspace_bytes": (_u64, [_i64, _i64, _i64]),
+    "repops_rmsnorm_residual_backward_f32": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                                    _i64, _i64, _f32, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                                    _i64, _vp, _u64, _vp]),
     "repops_host_alloc": (_i32, [_u64, _vp]),
     "repops_host_free": (_i32, [_vp]),
     "repops_set_thread_status_word": (_i32, [_vp]),

@@ -1,0 +1,1031 @@
+// blockedge.cu -- the edge between two blocks of a pre-norm transformer in one
+// pass: the norm after a block, its gate and residual scale, the residual sum,
+// and the norm before the next block; its backward pass; and RMSNorm's backward
+// from an input kept in 8 bits.
+//
+//   p = RMSNorm(f; post),  y = x + alpha * (gate * p),  h = RMSNorm(y; pre)
+//
+// Every step is the one the separate operators take (rowops.cu): one binary32
+// rounding each, row sums over the 32-ary tree, column sums over the tree of
+// colsum, so the bits equal the separate operators' and only the memory
+// traffic changes: forward 16 bytes an element (x, f in; y, h out) instead of
+// 36, backward 24 (y, f, dy, dh in; dx, df out) plus what the column sums read.
+//
+// Row kernels: T threads a row, a warp for each slab of 1024 columns.  The
+// rows arrive by cp.async in the swizzled stage; element-wise steps take the
+// slab in memory order (coalesced, parameters straight from the cache) and the
+// tree takes it in run order, a run a lane, both from the stage.  Memory order
+// keeps the parameters out of registers and shared memory, so more rows are
+// in flight per SM than with a run's values held by the lane that folds it.
+//
+// Column sums (the gradients of the gains and the gate) need their terms
+// folded in row order, a run of 32 rows at a time: a second kernel, a thread
+// for each column (four with 16-byte rows) and run, forms the terms again from
+// the rows and the row's 1/rms that the row kernel left, and a last one folds
+// the run results.  Writing the terms and summing them afterwards would move 8
+// bytes an element for each of the three sums instead of 16 for all.
+#include <algorithm>
+
+#include "internal.cuh"
+#include "rows8.cuh"
+#include "rowtree.cuh"
+
+namespace repops {
+namespace {
+
+constexpr int64_t MAX_STAGED_COLS = 8192;       // 256 threads, a run each
+constexpr int64_t MAX_FOLD_ROWS = RUN * RUN;    // run results the last fold takes
+
+// ------------------------------------------------------------- row slabs ----
+// A warp's slab: step k (of 8) covers four values a lane.  With 16-byte rows
+// (VEC) they are columns 128k + 4*lane .. + 3 of the slab; else columns
+// 128k + lane + {0, 32, 64, 96}.
+
+template <bool VEC>
+__device__ __forceinline__ int64_t slab_col(int k, int t) {
+    const int lane = threadIdx.x & 31, slab = (threadIdx.x >> 5) * 1024;
+    return VEC ? slab + 128 * k + 4 * lane + t : slab + 128 * k + 32 * t + lane;
+}
+
+template <bool VEC>
+__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int k, int64_t n) {
+    if constexpr (VEC) {
+        const int64_t c = slab_col<VEC>(k, 0);
+        if (c + 4 <= n) return __ldg(reinterpret_cast<const float4 *>(row + c));
+        return make_float4(c < n ? row[c] : 0.0f, c + 1 < n ? row[c + 1] : 0.0f, c + 2 < n ? row[c + 2] : 0.0f, 0.0f);
+    } else {
+        const int64_t c = slab_col<VEC>(k, 0);
+        return make_float4(c < n ? row[c] : 0.0f, c + 32 < n ? row[c + 32] : 0.0f, c + 64 < n ? row[c + 64] : 0.0f,
+                           c + 96 < n ? row[c + 96] : 0.0f);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void row_store(float *row, int k, int64_t n, float4 v) {
+    const int64_t c = slab_col<VEC>(k, 0);
+    if constexpr (VEC) {
+        if (c + 4 <= n) {
+            *reinterpret_cast<float4 *>(row + c) = v;
+        } else {
+            if (c < n) row[c] = v.x;
+            if (c + 1 < n) row[c + 1] = v.y;
+            if (c + 2 < n) row[c + 2] = v.z;
+        }
+    } else {
+        if (c < n) row[c] = v.x;
+        if (c + 32 < n) row[c + 32] = v.y;
+        if (c + 64 < n) row[c + 64] = v.z;
+        if (c + 96 < n) row[c + 96] = v.w;
+    }
+}
+
+// A slab step's place in the stage.
+template <bool VEC>
+__device__ __forceinline__ int stage_float(int k, int t) {
+    const int lane = threadIdx.x & 31, u0 = (threadIdx.x >> 5) * 32 + 4 * k;
+    if constexpr (VEC) return 4 * stage_slot(u0 + (lane >> 3), lane & 7) + t;
+    else return 4 * stage_slot(u0 + t, lane >> 2) + (lane & 3);
+}
+
+template <bool VEC>
+__device__ __forceinline__ float4 stage_load(const float4 *stage, int k) {
+    const float *s = reinterpret_cast<const float *>(stage);
+    if constexpr (VEC) return *reinterpret_cast<const float4 *>(s + stage_float<VEC>(k, 0));
+    else
+        return make_float4(s[stage_float<VEC>(k, 0)], s[stage_float<VEC>(k, 1)], s[stage_float<VEC>(k, 2)],
+                           s[stage_float<VEC>(k, 3)]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void stage_store(float4 *stage, int k, float4 v) {
+    float *s = reinterpret_cast<float *>(stage);
+    if constexpr (VEC) {
+        *reinterpret_cast<float4 *>(s + stage_float<VEC>(k, 0)) = v;
+    } else {
+        s[stage_float<VEC>(k, 0)] = v.x;
+        s[stage_float<VEC>(k, 1)] = v.y;
+        s[stage_float<VEC>(k, 2)] = v.z;
+        s[stage_float<VEC>(k, 3)] = v.w;
+    }
+}
+
+// Starts the copy of the warp's slab of a row into the stage.
+template <bool VEC>
+__device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict__ row, int64_t n) {
+    float *s = reinterpret_cast<float *>(stage);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if constexpr (VEC) {
+            const int64_t c = slab_col<VEC>(k, 0);
+            if (c < n) cp_async_16(s + stage_float<VEC>(k, 0), row + c, uint32_t(imin64(4, n - c)) * 4u);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int64_t c = slab_col<VEC>(k, t);
+                if (c < n) cp_async_4(s + stage_float<VEC>(k, t), row + c, 4u);
+            }
+        }
+    }
+}
+
+// The warp's group result of the tree over the staged values f(v): each lane
+// folds its run, every lane folds the lanes' results in order.
+template <class F>
+__device__ __forceinline__ float slab_fold(const float4 *stage, int64_t n, F f) {
+    const int u = threadIdx.x, warp0 = u & ~31;
+    const int64_t s = int64_t(u) * RUN;
+    const int len = s < n ? int(imin64(RUN, n - s)) : 0;
+    float v[RUN];
+#pragma unroll
+    for (int c = 0; c < RUN / 4; ++c) {
+        const float4 w = stage[stage_slot(u, c)];
+        v[4 * c] = w.x; v[4 * c + 1] = w.y; v[4 * c + 2] = w.z; v[4 * c + 3] = w.w;
+    }
+    float acc = f(v[0]);
+    if (len == RUN) {
+#pragma unroll
+        for (int i = 1; i < RUN; ++i) acc = __fadd_rn(acc, f(v[i]));
+    } else {
+#pragma unroll
+        for (int i = 1; i < RUN; ++i)
+            if (i < len) acc = __fadd_rn(acc, f(v[i]));
+    }
+    const int have = int((n + RUN - 1) / RUN) - warp0;     // runs present from this warp on
+    float g = __shfl_sync(0xffffffffu, acc, 0);
+    if (have >= RUN) {
+#pragma unroll
+        for (int i = 1; i < RUN; ++i) g = __fadd_rn(g, __shfl_sync(0xffffffffu, acc, i));
+    } else {
+#pragma unroll
+        for (int i = 1; i < RUN; ++i) {
+            const float o = __shfl_sync(0xffffffffu, acc, i);
+            if (i < have) g = __fadd_rn(g, o);
+        }
+    }
+    return g;
+}
+
+// The tree's root from the warps' group results (one barrier).  gbuf has two
+// halves used in turn, so that a thread still reading one reduction's half
+// never races the next one's writes.
+template <int T, int NV>
+struct GroupBuf {
+    float g[2][NV][8];
+};
+
+template <int T, int NV>
+__device__ __forceinline__ void slab_roots(float (&v)[NV], GroupBuf<T, NV> &gb, int &phase, int64_t n) {
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) gb.g[phase][j][threadIdx.x >> 5] = v[j];
+        }
+        __syncthreads();
+        const int G = int((n + 1023) / 1024);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            v[j] = gb.g[phase][j][0];
+            for (int k = 1; k < G; ++k) v[j] = __fadd_rn(v[j], gb.g[phase][j][k]);
+        }
+        phase ^= 1;
+    }
+}
+
+__device__ __forceinline__ float rms_inv(float sum, float nf, float eps) {
+    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, nf), eps)));
+}
+
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+    return make_float4(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y), __fmul_rn(a.z, b.z), __fmul_rn(a.w, b.w));
+}
+__device__ __forceinline__ float4 mul4(float4 a, float s) { return mul4(a, make_float4(s, s, s, s)); }
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
+}
+__device__ __forceinline__ float4 sub4(float4 a, float4 b) {
+    return make_float4(__fsub_rn(a.x, b.x), __fsub_rn(a.y, b.y), __fsub_rn(a.z, b.z), __fsub_rn(a.w, b.w));
+}
+
+struct Ident {
+    __device__ __forceinline__ float operator()(float x) const { return x; }
+};
+
+// --------------------------------------------------------------- forward ----
+
+struct EdgeArgs {
+    int64_t rows, n;
+    const float *x, *f;
+    int64_t ldx, ldf;
+    const float *post, *gate, *pre;    // each may be null
+    int64_t ldgate, gate_rows;
+    float alpha, eps;
+    float *y, *h;
+    int64_t ldy, ldh;
+};
+
+// Two stages of rows where they leave room for a few CTAs.
+template <int T>
+constexpr bool kEdgePrefetch = T <= 128;
+
+template <int T, bool VEC>
+__global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
+    extern __shared__ float4 stage_mem[];
+    __shared__ GroupBuf<T, 1> gb;
+    int phase = 0;
+    constexpr int Q = T * RUN / 4;
+    constexpr bool PF = kEdgePrefetch<T>;
+    const float nf = float(p.n);
+    int cur = 0;
+    int64_t row = blockIdx.x;
+    if (row < p.rows) {
+        stage_row<VEC>(stage_mem, p.f + row * p.ldf, p.n);
+        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, p.n);
+    }
+    cp_async_commit();
+    for (; row < p.rows; row += gridDim.x) {
+        const int64_t next = row + gridDim.x;
+        float4 *sf = stage_mem + cur * 2 * Q, *sx = sf + Q;
+        if constexpr (PF) {
+            cur ^= 1;
+            if (next < p.rows) {
+                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, p.n);
+                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, p.n);
+            }
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+        __syncwarp();
+        float inv_f = 0.0f;
+        if (p.post) {
+            float s[1] = {slab_fold(sf, p.n, Square())};
+            slab_roots<T, 1>(s, gb, phase, p.n);
+            inv_f = rms_inv(s[0], nf, p.eps);
+        }
+        const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+        float *yr = p.y + row * p.ldy;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float4 v = stage_load<VEC>(sf, k);
+            if (p.post) v = mul4(mul4(v, inv_f), row_load<VEC>(p.post, k, p.n));
+            if (gate) v = mul4(v, row_load<VEC>(gate, k, p.n));
+            v = add4(stage_load<VEC>(sx, k), mul4(v, p.alpha));
+            row_store<VEC>(yr, k, p.n, v);
+            if (p.pre) stage_store<VEC>(sx, k, v);
+        }
+        if (p.pre) {
+            __syncwarp();
+            float s[1] = {slab_fold(sx, p.n, Square())};
+            slab_roots<T, 1>(s, gb, phase, p.n);
+            const float inv_y = rms_inv(s[0], nf, p.eps);
+            float *hr = p.h + row * p.ldh;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                row_store<VEC>(hr, k, p.n, mul4(mul4(stage_load<VEC>(sx, k), inv_y), row_load<VEC>(p.pre, k, p.n)));
+        }
+        __syncwarp();                       // the stage is read before it is filled again
+        if constexpr (!PF) {
+            if (next < p.rows) {
+                stage_row<VEC>(sf, p.f + next * p.ldf, p.n);
+                stage_row<VEC>(sx, p.x + next * p.ldx, p.n);
+            }
+            cp_async_commit();
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// Rows of more than 8192 values: each phase reads the row again.
+__global__ void __launch_bounds__(256) edge_forward_long_kernel(EdgeArgs p) {
+    extern __shared__ float buf[];
+    __shared__ float bcast;
+    const int runs = int((p.n + RUN - 1) / RUN);
+    float *buf2 = buf + runs;
+    const float nf = float(p.n);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const float *xr = p.x + row * p.ldx, *fr = p.f + row * p.ldf;
+        const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+        float *yr = p.y + row * p.ldy;
+        float inv_f = 0.0f;
+        if (p.post)
+            inv_f = rms_inv(generic_reduce_idx<Op::Sum>(
+                                p.n, [&](int64_t i) { return __fmul_rn(fr[i], fr[i]); }, buf, buf2, &bcast),
+                            nf, p.eps);
+        for (int64_t i = threadIdx.x; i < p.n; i += 256) {
+            float v = fr[i];
+            if (p.post) v = __fmul_rn(__fmul_rn(v, inv_f), p.post[i]);
+            if (gate) v = __fmul_rn(v, gate[i]);
+            yr[i] = __fadd_rn(xr[i], __fmul_rn(p.alpha, v));
+        }
+        __syncthreads();
+        if (p.pre) {
+            const float inv_y = rms_inv(generic_reduce_idx<Op::Sum>(
+                                            p.n, [&](int64_t i) { return __fmul_rn(yr[i], yr[i]); }, buf, buf2, &bcast),
+                                        nf, p.eps);
+            float *hr = p.h + row * p.ldh;
+            for (int64_t i = threadIdx.x; i < p.n; i += 256) hr[i] = __fmul_rn(__fmul_rn(yr[i], inv_y), p.pre[i]);
+        }
+        __syncthreads();
+    }
+}
+
+// -------------------------------------------------------------- backward ----
+
+struct EdgeBackArgs {
+    int64_t rows, n;
+    // the norm before the next block: its input y (or q, s: 8 bits), the
+    // gradient dh of its output, and the gradient dy arriving past it
+    const float *y;
+    int64_t ldy;
+    const int8_t *q;
+    int64_t ldq;
+    const float *s;
+    int64_t lds;
+    int shift;
+    const float *dh, *dy;              // either may be null
+    int64_t lddh, lddy;
+    const float *pre;
+    // the block's output, its norm and gate (only with F)
+    const float *f;
+    int64_t ldf;
+    const float *post, *gate;          // each may be null
+    int64_t ldgate, gate_rows;
+    float alpha, eps;
+    float *dx, *df, *h;                // h: the norm's output again, only from 8 bits
+    int64_t lddx, lddf, ldh;
+    float *inv_y, *inv_f;              // a row's 1/rms, for the column sums
+};
+
+template <bool VEC>
+__device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, int k) {
+    const int64_t c = slab_col<VEC>(k, 0);
+    const int8_t *q = p.q + row * p.ldq;
+    const float *s = p.s + row * p.lds;
+    if constexpr (VEC) {
+        // a group is a multiple of 4 columns, and so is n
+        return c < p.n ? unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(q + c)), __ldg(s + (c >> p.shift)))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+        float v[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int64_t i = c + 32 * t;
+            v[t] = i < p.n ? __fmul_rn(float(q[i]), __ldg(s + (i >> p.shift))) : 0.0f;
+        }
+        return make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
+// after the block.  Q8: y comes in 8 bits, and h may be written again.
+template <int T, bool VEC, bool Q8, bool F>
+__global__ void __launch_bounds__(T) edge_backward_kernel(EdgeBackArgs p) {
+    extern __shared__ float4 stage_mem[];
+    __shared__ GroupBuf<T, 2> gb2;
+    __shared__ GroupBuf<T, 1> gb1;
+    int phase1 = 0, phase2 = 0;
+    constexpr int Q = T * RUN / 4;
+    float4 *sy = stage_mem, *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
+    const float nf = float(p.n);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        if (p.dh) {
+            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, p.n);
+            stage_row<VEC>(sh, p.dh + row * p.lddh, p.n);
+        }
+        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, p.n);
+        cp_async_commit();
+        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, p.n);
+        cp_async_commit();
+        if constexpr (Q8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, k, row8_load<VEC>(p, row, k));
+        }
+        cp_async_wait<1>();
+        __syncwarp();
+        float r2[2] = {0.0f, 0.0f};
+        if (p.dh) r2[0] = slab_fold(sy, p.n, Square());
+        if constexpr (F) {
+            if (p.post) r2[1] = slab_fold(sf, p.n, Square());
+        }
+        slab_roots<T, 2>(r2, gb2, phase2, p.n);
+        const float inv_y = rms_inv(r2[0], nf, p.eps), inv_f = rms_inv(r2[1], nf, p.eps);
+        if (threadIdx.x == 0) {
+            if (p.dh) p.inv_y[row] = inv_y;
+            if constexpr (F) {
+                if (p.post) p.inv_f[row] = inv_f;
+            }
+        }
+        float4 e[8];                              // dx
+        if (p.dh) {
+            // sy <- xh, sh <- gy after their products are summed from sh
+            float4 gy[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 g = row_load<VEC>(p.pre, k, p.n);
+                e[k] = mul4(stage_load<VEC>(sy, k), inv_y);
+                gy[k] = mul4(stage_load<VEC>(sh, k), g);
+                if constexpr (Q8) {
+                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, p.n, mul4(e[k], g));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) stage_store<VEC>(sh, k, mul4(gy[k], e[k]));
+            __syncwarp();
+            float r1[1] = {slab_fold(sh, p.n, Ident())};
+            slab_roots<T, 1>(r1, gb1, phase1, p.n);
+            const float c = __fdiv_rn(r1[0], nf);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(gy[k], mul4(e[k], c)), inv_y);
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+        if (p.dy) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 d = stage_load<VEC>(sr, k);
+                e[k] = p.dh ? add4(e[k], d) : d;
+            }
+        }
+        float *dxr = p.dx + row * p.lddx;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, k, p.n, e[k]);
+        if constexpr (F) {
+            float *dfr = p.df + row * p.lddf;
+            const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                e[k] = mul4(e[k], p.alpha);
+                if (gate) e[k] = mul4(e[k], row_load<VEC>(gate, k, p.n));
+            }
+            if (p.post) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    e[k] = mul4(e[k], row_load<VEC>(p.post, k, p.n));
+                    stage_store<VEC>(sr, k, mul4(e[k], mul4(stage_load<VEC>(sf, k), inv_f)));
+                }
+                __syncwarp();
+                float r1[1] = {slab_fold(sr, p.n, Ident())};
+                slab_roots<T, 1>(r1, gb1, phase1, p.n);
+                const float c = __fdiv_rn(r1[0], nf);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    e[k] = mul4(sub4(e[k], mul4(mul4(stage_load<VEC>(sf, k), inv_f), c)), inv_f);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, k, p.n, e[k]);
+        }
+        __syncwarp();
+    }
+}
+
+// Rows of more than 8192 values: each phase reads the row again.
+template <bool Q8, bool F>
+__global__ void __launch_bounds__(256) edge_backward_long_kernel(EdgeBackArgs p) {
+    extern __shared__ float buf[];
+    __shared__ float bcast;
+    const int runs = int((p.n + RUN - 1) / RUN);
+    float *buf2 = buf + runs;
+    const float nf = float(p.n);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        auto yv = [&](int64_t i) {
+            if constexpr (Q8) return __fmul_rn(float(p.q[row * p.ldq + i]), p.s[row * p.lds + (i >> p.shift)]);
+            else return p.y[row * p.ldy + i];
+        };
+        const float *dhr = p.dh + row * p.lddh, *dyr = p.dy + row * p.lddy;
+        float *dxr = p.dx + row * p.lddx;
+        float inv_y = 0.0f, c = 0.0f;
+        if (p.dh) {
+            inv_y = rms_inv(generic_reduce_idx<Op::Sum>(
+                                p.n, [&](int64_t i) { const float v = yv(i); return __fmul_rn(v, v); }, buf, buf2,
+                                &bcast), nf, p.eps);
+            c = __fdiv_rn(generic_reduce_idx<Op::Sum>(p.n, [&](int64_t i) {
+                return __fmul_rn(__fmul_rn(dhr[i], p.pre[i]), __fmul_rn(yv(i), inv_y));
+            }, buf, buf2, &bcast), nf);
+            if (threadIdx.x == 0) p.inv_y[row] = inv_y;
+        }
+        for (int64_t i = threadIdx.x; i < p.n; i += 256) {
+            float d = 0.0f;
+            if (p.dh) {
+                const float xh = __fmul_rn(yv(i), inv_y);
+                d = __fmul_rn(inv_y, __fsub_rn(__fmul_rn(dhr[i], p.pre[i]), __fmul_rn(xh, c)));
+                if constexpr (Q8) {
+                    if (p.h) p.h[row * p.ldh + i] = __fmul_rn(xh, p.pre[i]);
+                }
+            }
+            if (p.dy) d = p.dh ? __fadd_rn(d, dyr[i]) : dyr[i];
+            dxr[i] = d;
+        }
+        __syncthreads();
+        if constexpr (F) {
+            const float *fr = p.f + row * p.ldf;
+            const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+            float *dfr = p.df + row * p.lddf;
+            auto dp = [&](int64_t i) {
+                float d = __fmul_rn(dxr[i], p.alpha);
+                if (gate) d = __fmul_rn(d, gate[i]);
+                return p.post ? __fmul_rn(d, p.post[i]) : d;
+            };
+            float inv_f = 0.0f, cf = 0.0f;
+            if (p.post) {
+                inv_f = rms_inv(generic_reduce_idx<Op::Sum>(
+                                    p.n, [&](int64_t i) { return __fmul_rn(fr[i], fr[i]); }, buf, buf2, &bcast),
+                                nf, p.eps);
+                cf = __fdiv_rn(generic_reduce_idx<Op::Sum>(
+                                   p.n, [&](int64_t i) { return __fmul_rn(dp(i), __fmul_rn(fr[i], inv_f)); }, buf, buf2,
+                                   &bcast), nf);
+                if (threadIdx.x == 0) p.inv_f[row] = inv_f;
+            }
+            for (int64_t i = threadIdx.x; i < p.n; i += 256) {
+                const float d = dp(i);
+                dfr[i] = p.post ? __fmul_rn(inv_f, __fsub_rn(d, __fmul_rn(__fmul_rn(fr[i], inv_f), cf))) : d;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ------------------------------------------------------------ column sums ----
+
+struct ColArgs {
+    EdgeBackArgs e;
+    int64_t block_rows;     // rows of a block: its runs of 32 start at its first row
+    int64_t block_runs;     // runs of a block
+    int64_t runs;           // runs in all
+    float *pre, *post, *gate;   // run results, runs x n each; null: not wanted
+    int64_t ldg;                // pitch of gate's (the others are packed)
+};
+
+// A thread forms and folds the terms of W columns over a run of 32 rows:
+//   pre:  dh * (y * inv_y)
+//   post: ((alpha * dx) * gate) * (f * inv_f)
+//   gate: (alpha * dx) * ((f * inv_f) * post)
+template <int W, bool Q8, bool F>
+__global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
+    const EdgeBackArgs &p = a.e;
+    const int64_t c = (blockIdx.x * int64_t(128) + threadIdx.x) * W;
+    if (c >= p.n) return;
+    struct V { float v[W]; };
+    auto ld = [&](const float *q) {
+        V r;
+        if constexpr (W == 4) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(q + c));
+            r.v[0] = w.x; r.v[1] = w.y; r.v[2] = w.z; r.v[3] = w.w;
+        } else {
+            r.v[0] = __ldg(q + c);
+        }
+        return r;
+    };
+    auto st = [&](float *q, const V &r) {
+        if constexpr (W == 4) *reinterpret_cast<float4 *>(q + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        else q[c] = r.v[0];
+    };
+    V post;
+    if (F && a.gate && p.post) post = ld(p.post);
+    for (int64_t run = blockIdx.y; run < a.runs; run += gridDim.y) {
+        const int64_t b = run / a.block_runs, first = b * a.block_rows + (run - b * a.block_runs) * RUN;
+        const int64_t last = imin64(first + RUN, (b + 1) * a.block_rows);
+        V s_pre, s_post, s_gate;
+        V gate;
+        int64_t gate_left = 0;      // rows until the next gate row begins
+        const float *gate_row = nullptr;
+        if (F && a.post && p.gate) {
+            gate_row = p.gate + (first / p.gate_rows) * p.ldgate;
+            gate_left = p.gate_rows - first % p.gate_rows;
+            gate = ld(gate_row);
+        }
+#pragma unroll 4
+        for (int64_t r = first; r < last; ++r) {
+            const bool start = r == first;
+            if (a.pre) {
+                V y;
+                if constexpr (Q8) {
+                    const float s = __ldg(p.s + r * p.lds + (c >> p.shift));
+                    if constexpr (W == 4) {
+                        const float4 w = unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
+                        y.v[0] = w.x; y.v[1] = w.y; y.v[2] = w.z; y.v[3] = w.w;
+                    } else {
+                        y.v[0] = __fmul_rn(float(p.q[r * p.ldq + c]), s);
+                    }
+                } else {
+                    y = ld(p.y + r * p.ldy);
+                }
+                const V d = ld(p.dh + r * p.lddh);
+                const float inv = __ldg(p.inv_y + r);
+#pragma unroll
+                for (int t = 0; t < W; ++t) {
+                    const float v = __fmul_rn(d.v[t], __fmul_rn(y.v[t], inv));
+                    s_pre.v[t] = start ? v : __fadd_rn(s_pre.v[t], v);
+                }
+            }
+            if constexpr (F) {
+                if (a.post || a.gate) {
+                    const V dx = ld(p.dx + r * p.lddx), f = ld(p.f + r * p.ldf);
+                    const float inv = p.post ? __ldg(p.inv_f + r) : 0.0f;
+                    if (a.post && p.gate) {
+                        if (gate_left == 0) {
+                            gate_row += p.ldgate;
+                            gate_left = p.gate_rows;
+                            gate = ld(gate_row);
+                        }
+                        --gate_left;
+                    }
+#pragma unroll
+                    for (int t = 0; t < W; ++t) {
+                        const float dt = __fmul_rn(dx.v[t], p.alpha);
+                        const float fh = p.post ? __fmul_rn(f.v[t], inv) : f.v[t];
+                        if (a.post) {
+                            const float v = __fmul_rn(p.gate ? __fmul_rn(dt, gate.v[t]) : dt, fh);
+                            s_post.v[t] = start ? v : __fadd_rn(s_post.v[t], v);
+                        }
+                        if (a.gate) {
+                            const float v = __fmul_rn(dt, p.post ? __fmul_rn(fh, post.v[t]) : fh);
+                            s_gate.v[t] = start ? v : __fadd_rn(s_gate.v[t], v);
+                        }
+                    }
+                }
+            }
+        }
+        if (a.pre) st(a.pre + run * p.n, s_pre);
+        if (F && a.post) st(a.post + run * p.n, s_post);
+        if (F && a.gate) st(a.gate + run * a.ldg, s_gate);
+    }
+}
+
+struct FoldSet {
+    const float *in;        // blocks x runs x n run results
+    float *out;             // blocks x n, pitch ldo
+    int64_t blocks, runs, ldo;
+};
+struct FoldArgs {
+    FoldSet s[3];
+    int64_t n;
+};
+
+// The two levels of the tree over up to 1024 run results: 32 columns a CTA, a
+// warp for each run of 32 results.
+__global__ void __launch_bounds__(1024) edge_fold_kernel(FoldArgs a) {
+    __shared__ float part[RUN][RUN + 1];
+    const FoldSet s = a.s[blockIdx.z];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = blockIdx.x * int64_t(RUN) + tx;
+    const int groups = int((s.runs + RUN - 1) / RUN);
+    for (int64_t b = blockIdx.y; b < s.blocks; b += gridDim.y) {
+        const int64_t r0 = int64_t(ty) * RUN, r1 = imin64(r0 + RUN, s.runs);
+        if (c < a.n && r0 < r1) {
+            const float *in = s.in + (b * s.runs + r0) * a.n + c;
+            float acc = in[0];
+            const int m = int(r1 - r0);
+            if (m == RUN) {
+#pragma unroll
+                for (int i = 1; i < RUN; ++i) acc = __fadd_rn(acc, in[int64_t(i) * a.n]);
+            } else {
+                for (int i = 1; i < m; ++i) acc = __fadd_rn(acc, in[int64_t(i) * a.n]);
+            }
+            part[ty][tx] = acc;
+        }
+        __syncthreads();
+        if (ty == 0 && c < a.n) {
+            float acc = part[0][tx];
+            for (int g = 1; g < groups; ++g) acc = __fadd_rn(acc, part[g][tx]);
+            s.out[b * s.ldo + c] = acc;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------- host ----
+
+bool vec_row(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
+
+// The column sums' scratch in floats, each array starting on 16 bytes: two
+// columns of 1/rms, the run results of the two gains, those of the gate (none
+// where a gate row has a single run: that run's result is the gradient), and
+// further levels where a block has more than 1024 runs.
+struct Scratch {
+    int64_t runs;                   // run results of a gain
+    int64_t gate_per, gate_runs;    // runs of one gate row; run results kept for the gate
+    int64_t level;                  // rows of the further levels
+    int64_t n4;
+    uint64_t floats(int64_t rows) const {
+        return uint64_t(2 * pad4(rows)) + uint64_t(2 * runs + gate_runs + level) * uint64_t(n4);
+    }
+};
+
+Scratch scratch_plan(int64_t rows, int64_t cols, int64_t gates) {
+    Scratch s;
+    s.n4 = pad4(cols);
+    s.runs = ceil_div(rows, RUN);
+    s.gate_per = gates > 0 ? ceil_div(rows / gates, RUN) : 0;
+    s.gate_runs = s.gate_per > 1 ? gates * s.gate_per : 0;
+    // a level of r run results has at most r/32 + 1 a block, the blocks have
+    // more than 1024 each, and each level is a 32nd of the one below: under
+    // 1.1 * r/32 + 8 for each of three sums
+    const int64_t most = std::max(s.runs > MAX_FOLD_ROWS ? s.runs : 0, s.gate_per > MAX_FOLD_ROWS ? s.gate_runs : 0);
+    s.level = most ? 4 * ceil_div(most, RUN) + 64 : 0;
+    return s;
+}
+
+// Scratch of a call: the caller's, or the library's pool.
+struct Workspace {
+    float *p = nullptr;
+    bool pool = false;
+    cudaStream_t stream;
+    int get(void *ws, uint64_t ws_bytes, uint64_t need, cudaStream_t s) {
+        stream = s;
+        if (ws) {
+            if (ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return REPOPS_ERR_INVALID_ARG;
+            p = static_cast<float *>(ws);
+            return REPOPS_OK;
+        }
+        if (scratch_malloc(reinterpret_cast<void **>(&p), size_t(need), s) != cudaSuccess) {
+            cudaGetLastError();
+            return REPOPS_ERR_ALLOC;
+        }
+        pool = true;
+        return REPOPS_OK;
+    }
+    int release(int rc) {
+        if (pool && p) {
+            const cudaError_t e = cudaFreeAsync(p, stream);
+            if (rc == REPOPS_OK && e != cudaSuccess) rc = set_cuda_error(e);
+        }
+        return rc;
+    }
+};
+
+template <bool VEC>
+int launch_forward(const EdgeArgs &a, cudaStream_t s) {
+    auto go = [&](auto kern, int T, bool pf) {
+        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (pf ? 4 : 2), a.rows, s, a);
+    };
+    if (a.n <= 1024) return go(edge_forward_kernel<32, VEC>, 32, kEdgePrefetch<32>);
+    if (a.n <= 2048) return go(edge_forward_kernel<64, VEC>, 64, kEdgePrefetch<64>);
+    if (a.n <= 4096) return go(edge_forward_kernel<128, VEC>, 128, kEdgePrefetch<128>);
+    return go(edge_forward_kernel<256, VEC>, 256, kEdgePrefetch<256>);
+}
+
+size_t long_row_smem(int64_t n) {
+    const int64_t runs = ceil_div(n, RUN);
+    return size_t(runs + ceil_div(runs, RUN)) * sizeof(float);
+}
+
+template <class Kern, class Args>
+int launch_long(Kern kern, const Args &a, int64_t rows, int64_t n, cudaStream_t s) {
+    const size_t smem = long_row_smem(n);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return set_cuda_error(e);
+    kern<<<grid_for_rows(rows), 256, smem, s>>>(a);
+    return check_launch();
+}
+
+template <bool VEC, bool Q8, bool F>
+int launch_rows(const EdgeBackArgs &a, cudaStream_t s) {
+    auto go = [&](auto kern, int T) {
+        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (F ? 4 : 3), a.rows, s, a);
+    };
+    if (a.n <= 1024) return go(edge_backward_kernel<32, VEC, Q8, F>, 32);
+    if (a.n <= 2048) return go(edge_backward_kernel<64, VEC, Q8, F>, 64);
+    if (a.n <= 4096) return go(edge_backward_kernel<128, VEC, Q8, F>, 128);
+    return go(edge_backward_kernel<256, VEC, Q8, F>, 256);
+}
+
+template <bool Q8, bool F>
+int launch_columns(const ColArgs &a, bool vec, cudaStream_t s) {
+    const int64_t threads = vec ? a.e.n / 4 : a.e.n;
+    const dim3 grid(unsigned(ceil_div(threads, 128)), unsigned(std::min<int64_t>(a.runs, 65535)));
+    if (vec) edge_columns_kernel<4, Q8, F><<<grid, 128, 0, s>>>(a);
+    else edge_columns_kernel<1, Q8, F><<<grid, 128, 0, s>>>(a);
+    return check_launch();
+}
+
+// The row kernel, the column terms and their folds.  dpre, dpost: n floats;
+// dgate: gates x n at pitch lddgate; null where there is none.
+template <bool Q8, bool F>
+int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_t lddgate, float *ws, bool vec,
+                 cudaStream_t s) {
+    const int64_t gates = dgate ? e.rows / e.gate_rows : 0;
+    const Scratch sc = scratch_plan(e.rows, e.n, gates);
+    e.inv_y = ws;
+    e.inv_f = e.inv_y + pad4(e.rows);
+    float *part = e.inv_f + pad4(e.rows);
+    float *ppre = part, *ppost = ppre + sc.runs * sc.n4, *pgate = ppost + sc.runs * sc.n4;
+    float *level = pgate + sc.gate_runs * sc.n4;
+    int rc;
+    if (e.n > MAX_STAGED_COLS) rc = launch_long(edge_backward_long_kernel<Q8, F>, e, e.rows, e.n, s);
+    else if (vec) rc = launch_rows<true, Q8, F>(e, s);
+    else rc = launch_rows<false, Q8, F>(e, s);
+    if (rc != REPOPS_OK) return rc;
+    if (!dpre && !dpost && !dgate) return REPOPS_OK;
+    // a gate's runs coincide with the gains' where its rows are whole runs:
+    // one pass makes all three sums
+    float *gate_out = sc.gate_per == 1 ? dgate : pgate;
+    const int64_t gate_ld = sc.gate_per == 1 ? lddgate : e.n;
+    const bool together = dgate && (dpre || dpost) && (gates == 1 || e.gate_rows % RUN == 0);
+    if (dpre || dpost) {
+        const ColArgs c{e, e.rows, sc.runs, sc.runs, dpre ? ppre : nullptr, dpost ? ppost : nullptr,
+                        together ? gate_out : nullptr, gate_ld};
+        rc = launch_columns<Q8, F>(c, vec, s);
+        if (rc != REPOPS_OK) return rc;
+    }
+    if (dgate && !together) {
+        const ColArgs c{e, e.gate_rows, sc.gate_per, gates * sc.gate_per, nullptr, nullptr, gate_out, gate_ld};
+        rc = launch_columns<Q8, F>(c, vec, s);
+        if (rc != REPOPS_OK) return rc;
+    }
+    FoldArgs f{};
+    f.n = e.n;
+    int sets = 0;
+    int64_t blocks = 1;
+    auto add = [&](const float *in, float *out, int64_t nb, int64_t runs, int64_t ldo) {
+        // one further level first for more than 1024 run results (twice for
+        // more than 32768 of them, and so on): a column sum's pass per block
+        while (rc == REPOPS_OK && runs > MAX_FOLD_ROWS) {
+            const int64_t up = ceil_div(runs, RUN);
+            const dim3 grid(unsigned(std::min<int64_t>(ceil_div(e.n, 256), 64)), unsigned(std::min<int64_t>(up, 65535)));
+            for (int64_t b = 0; b < nb && rc == REPOPS_OK; ++b) {
+                colsum_pass_kernel<<<grid, 256, 0, s>>>(runs, e.n, in + b * runs * e.n, e.n, level + b * up * e.n, e.n);
+                rc = check_launch();
+            }
+            in = level;
+            level += nb * up * sc.n4;
+            runs = up;
+        }
+        f.s[sets++] = FoldSet{in, out, nb, runs, ldo};
+        blocks = std::max(blocks, nb);
+    };
+    if (dpre) add(ppre, dpre, 1, sc.runs, e.n);
+    if (dpost) add(ppost, dpost, 1, sc.runs, e.n);
+    if (dgate && sc.gate_per > 1) add(pgate, dgate, gates, sc.gate_per, lddgate);
+    if (rc != REPOPS_OK || sets == 0) return rc;
+    const dim3 grid(unsigned(ceil_div(e.n, RUN)), unsigned(std::min<int64_t>(blocks, 65535)), unsigned(sets));
+    edge_fold_kernel<<<grid, 1024, 0, s>>>(f);
+    return check_launch();
+}
+
+}  // namespace
+}  // namespace repops
+
+using namespace repops;
+
+namespace {
+
+struct Span {
+    const void *p;
+    uint64_t bytes;
+};
+
+bool overlaps_any(Span o, std::initializer_list<Span> others) {
+    if (!o.p) return false;
+    for (const Span &t : others)
+        if (t.p && ranges_overlap(o.p, o.bytes, t.p, t.bytes)) return true;
+    return false;
+}
+
+bool too_long(int64_t cols) { return ceil_div(cols, RUN) > MAX_GENERIC_RUNS; }
+
+}  // namespace
+
+extern "C" int repops_rmsnorm_residual_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx, const float *f,
+                                           int64_t ldf, const float *post_gain, const float *gate, int64_t ldgate,
+                                           int64_t gate_rows, float alpha, const float *pre_gain, float eps, float *y,
+                                           int64_t ldy, float *h, int64_t ldh, cudaStream_t stream) {
+    if (rows < 0 || cols < 0) return REPOPS_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return REPOPS_OK;
+    if (!x || !f || !y || (pre_gain != nullptr) != (h != nullptr)) return REPOPS_ERR_INVALID_ARG;
+    if (gate && (gate_rows < 1 || rows % gate_rows != 0)) return REPOPS_ERR_INVALID_ARG;
+    if (too_long(cols)) return REPOPS_ERR_UNSUPPORTED;
+    uint64_t xb, fb, yb, hb = 0, gb = 0;
+    if (!rows_span(rows, cols, ldx, &xb) || !rows_span(rows, cols, ldf, &fb) || !rows_span(rows, cols, ldy, &yb) ||
+        (h && !rows_span(rows, cols, ldh, &hb)) || (gate && !rows_span(rows / gate_rows, cols, ldgate, &gb)))
+        return REPOPS_ERR_INVALID_ARG;
+    // a row is read before either output of it is written: y or h may be x or
+    // f themselves (the same pitch), but not both the same
+    const uint64_t vb = uint64_t(cols) * 4u;
+    const struct { float *p; uint64_t b; int64_t ld; } outs[2] = {{y, yb, ldy}, {h, hb, ldh}};
+    for (const auto &o : outs) {
+        if (!o.p) continue;
+        if (overlaps_any({o.p, o.b}, {{post_gain, vb}, {gate, gb}, {pre_gain, vb}})) return REPOPS_ERR_ALIAS;
+        if (!(o.p == x && o.ld == ldx) && ranges_overlap(o.p, o.b, x, xb)) return REPOPS_ERR_ALIAS;
+        if (!(o.p == f && o.ld == ldf) && ranges_overlap(o.p, o.b, f, fb)) return REPOPS_ERR_ALIAS;
+    }
+    if (h && ranges_overlap(y, yb, h, hb)) return REPOPS_ERR_ALIAS;
+    const EdgeArgs a{rows, cols, x, f, ldx, ldf, post_gain, gate, pre_gain, ldgate, gate ? gate_rows : 1, alpha, eps,
+                     y, h, ldy, ldh};
+    if (cols > MAX_STAGED_COLS) return launch_long(edge_forward_long_kernel, a, rows, cols, stream);
+    const bool vec = vec_row(x, ldx) && vec_row(f, ldf) && vec_row(y, ldy) && (!h || vec_row(h, ldh)) &&
+                     vec_row(post_gain, 0) && vec_row(pre_gain, 0) && (!gate || vec_row(gate, ldgate));
+    return vec ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
+}
+
+extern "C" uint64_t repops_rmsnorm_residual_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t gates) {
+    if (rows <= 0 || cols <= 0 || gates < 0 || (gates > 0 && rows % gates != 0) || rows > (int64_t(1) << 40) ||
+        cols > (int64_t(1) << 24))
+        return 0;
+    return scratch_plan(rows, cols, gates).floats(rows) * 4u;
+}
+
+extern "C" int repops_rmsnorm_residual_backward_f32(
+    int64_t rows, int64_t cols, const float *dy, int64_t lddy, const float *dh, int64_t lddh, const float *y,
+    int64_t ldy, const float *f, int64_t ldf, const float *post_gain, const float *gate, int64_t ldgate,
+    int64_t gate_rows, float alpha, const float *pre_gain, float eps, float *dx, int64_t lddx, float *df,
+    int64_t lddf, float *dpre, float *dpost, float *dgate, int64_t lddgate, void *ws, uint64_t ws_bytes,
+    cudaStream_t stream) {
+    if (rows < 0 || cols < 0) return REPOPS_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return REPOPS_OK;
+    const bool pre = pre_gain != nullptr;
+    if (!f || !dx || !df || (!dy && !dh) || pre != (dh != nullptr) || pre != (y != nullptr) ||
+        pre != (dpre != nullptr) || (post_gain != nullptr) != (dpost != nullptr) ||
+        (gate != nullptr) != (dgate != nullptr))
+        return REPOPS_ERR_INVALID_ARG;
+    if (gate && (gate_rows < 1 || rows % gate_rows != 0)) return REPOPS_ERR_INVALID_ARG;
+    if (too_long(cols)) return REPOPS_ERR_UNSUPPORTED;
+    const int64_t gates = gate ? rows / gate_rows : 0;
+    uint64_t dyb = 0, dhb = 0, yb = 0, fb, gb = 0, dxb, dfb, dgb = 0;
+    if ((dy && !rows_span(rows, cols, lddy, &dyb)) || (dh && !rows_span(rows, cols, lddh, &dhb)) ||
+        (y && !rows_span(rows, cols, ldy, &yb)) || !rows_span(rows, cols, ldf, &fb) ||
+        (gate && (!rows_span(gates, cols, ldgate, &gb) || !rows_span(gates, cols, lddgate, &dgb))) ||
+        !rows_span(rows, cols, lddx, &dxb) || !rows_span(rows, cols, lddf, &dfb))
+        return REPOPS_ERR_INVALID_ARG;
+    const uint64_t vb = uint64_t(cols) * 4u, need = repops_rmsnorm_residual_backward_workspace_bytes(rows, cols, gates);
+    // dx may be dy itself; the column sums read the other inputs after the
+    // rows have been written
+    const Span in_dy{dx == dy && lddx == lddy ? nullptr : dy, dyb};
+    const Span outs[5] = {{dx, dxb}, {df, dfb}, {dpre, vb}, {dpost, vb}, {dgate, dgb}};
+    for (int i = 0; i < 5; ++i) {
+        if (overlaps_any(outs[i], {i == 0 ? in_dy : Span{dy, dyb}, {dh, dhb}, {y, yb}, {f, fb}, {post_gain, vb},
+                                   {gate, gb}, {pre_gain, vb}, {ws, ws ? ws_bytes : 0}}))
+            return REPOPS_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps_any(outs[i], {outs[j]})) return REPOPS_ERR_ALIAS;
+    }
+    if (need == 0) return REPOPS_ERR_UNSUPPORTED;
+    Workspace w;
+    int rc = w.get(ws, ws_bytes, need, stream);
+    if (rc != REPOPS_OK) return rc;
+    EdgeBackArgs e{};
+    e.rows = rows; e.n = cols;
+    e.y = y; e.ldy = ldy;
+    e.dh = dh; e.lddh = lddh; e.dy = dy; e.lddy = lddy;
+    e.pre = pre_gain;
+    e.f = f; e.ldf = ldf;
+    e.post = post_gain; e.gate = gate; e.ldgate = ldgate; e.gate_rows = gate ? gate_rows : 1;
+    e.alpha = alpha; e.eps = eps;
+    e.dx = dx; e.lddx = lddx; e.df = df; e.lddf = lddf;
+    const bool vec = cols % 4 == 0 && (!dy || vec_row(dy, lddy)) && (!dh || vec_row(dh, lddh)) &&
+                     (!y || vec_row(y, ldy)) && vec_row(f, ldf) && vec_row(post_gain, 0) && vec_row(pre_gain, 0) &&
+                     (!gate || (vec_row(gate, ldgate) && vec_row(dgate, lddgate))) && vec_row(dx, lddx) &&
+                     vec_row(df, lddf);
+    return w.release(run_backward<false, true>(e, dpre, dpost, dgate, lddgate, w.p, vec, stream));
+}
+
+extern "C" uint64_t repops_rmsnorm_backward_i8_workspace_bytes(int64_t rows, int64_t cols) {
+    return repops_rmsnorm_residual_backward_workspace_bytes(rows, cols, 0);
+}
+
+extern "C" int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int64_t ldx,
+                                          const float *x_scale, int64_t lds, int64_t group, const float *gamma,
+                                          float eps, const float *dy, int64_t lddy, const float *res, int64_t ldres,
+                                          float *dx, int64_t lddx, float *h, int64_t ldh, float *dgamma, void *ws,
+                                          uint64_t ws_bytes, cudaStream_t stream) {
+    if (rows < 0 || cols < 0 || !known_group(group)) return REPOPS_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return REPOPS_OK;
+    if (!x || !x_scale || !gamma || !dy || !dx || !dgamma) return REPOPS_ERR_INVALID_ARG;
+    if (too_long(cols)) return REPOPS_ERR_UNSUPPORTED;
+    uint64_t xb, sb, dyb, rb = 0, dxb, hb = 0;
+    if (!span_bytes(rows, cols, ldx, 1, &xb) || !span_bytes(rows, group_count(cols, group), lds, 4, &sb) ||
+        !rows_span(rows, cols, lddy, &dyb) || (res && !rows_span(rows, cols, ldres, &rb)) ||
+        !rows_span(rows, cols, lddx, &dxb) || (h && !rows_span(rows, cols, ldh, &hb)))
+        return REPOPS_ERR_INVALID_ARG;
+    const uint64_t vb = uint64_t(cols) * 4u, need = repops_rmsnorm_backward_i8_workspace_bytes(rows, cols);
+    const Span in_res{dx == res && lddx == ldres ? nullptr : res, rb};
+    const Span outs[3] = {{dx, dxb}, {h, hb}, {dgamma, vb}};
+    for (int i = 0; i < 3; ++i) {
+        if (overlaps_any(outs[i], {{x, xb}, {x_scale, sb}, {gamma, vb}, {dy, dyb}, i == 0 ? in_res : Span{res, rb},
+                                   {ws, ws ? ws_bytes : 0}}))
+            return REPOPS_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps_any(outs[i], {outs[j]})) return REPOPS_ERR_ALIAS;
+    }
+    if (need == 0) return REPOPS_ERR_UNSUPPORTED;
+    Workspace w;
+    int rc = w.get(ws, ws_bytes, need, stream);
+    if (rc != REPOPS_OK) return rc;
+    EdgeBackArgs e{};
+    e.rows = rows; e.n = cols;
+    e.q = x; e.ldq = ldx; e.s = x_scale; e.lds = lds; e.shift = group_shift(group);
+    e.dh = dy; e.lddh = lddy; e.dy = res; e.lddy = ldres;
+    e.pre = gamma;
+    e.gate_rows = 1;
+    e.eps = eps;
+    e.dx = dx; e.lddx = lddx; e.h = h; e.ldh = ldh;
+    const bool vec = cols % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 4 == 0 && ldx % 4 == 0 && vec_row(gamma, 0) &&
+                     vec_row(dy, lddy) && (!res || vec_row(res, ldres)) && vec_row(dx, lddx) &&
+                     (!h || vec_row(h, ldh));
+    return w.release(run_backward<true, false>(e, dgamma, nullptr, nullptr, 0, w.p, vec, stream));
+}

@@ -34,15 +34,12 @@
 
 #include "fixed_math.cuh"
 #include "internal.cuh"
+#include "rowtree.cuh"
 
 namespace repops {
 namespace {
 
-constexpr int RUN = 32;
-
-__device__ __forceinline__ int64_t imin64(int64_t a, int64_t b) { return a < b ? a : b; }
 constexpr int MAX_FAST_RUNS = 256 * 4;          // register-resident rows: up to 32768 values
-constexpr int MAX_GENERIC_RUNS = 12288;         // run results in 48 KB of shared memory
 
 // Resident CTAs per SM the staged backward kernels ask the compiler for.
 // Softmax backward: 10 warps (about 100 registers a thread for its p and dp
@@ -54,41 +51,6 @@ constexpr int kBwdRowBlocks = T == 32 ? 16 : 640 / T;
 // RMSNorm backward: 16 warps (128 registers; x, dy, gamma and res runs live).
 template <int T>
 constexpr int kNormBwdBlocks = T == 32 ? 12 : 512 / T;
-
-// ------------------------------------------------------------ arithmetic ----
-
-enum class Op { Sum, Max };
-
-template <Op OP>
-__device__ __forceinline__ float combine(float acc, float v) {
-    if constexpr (OP == Op::Sum) return __fadd_rn(acc, v);
-    else return v > acc ? v : acc;
-}
-
-// Upper levels of the tree over the m run results in a[] (shared memory),
-// ping-ponging with b[]; every thread of the CTA calls it and receives the
-// root.  Both buffers are clobbered.
-template <Op OP>
-__device__ float tree_upper(float *a, float *b, int m, float *bcast) {
-    __syncthreads();
-    while (m > 1) {
-        const int groups = (m + RUN - 1) / RUN;
-        for (int g = threadIdx.x; g < groups; g += blockDim.x) {
-            const int s = g * RUN, e = min(s + RUN, m);
-            float acc = a[s];
-            for (int i = s + 1; i < e; ++i) acc = combine<OP>(acc, a[i]);
-            b[g] = acc;
-        }
-        __syncthreads();
-        float *t = a; a = b; b = t;
-        m = groups;
-    }
-    if (threadIdx.x == 0) *bcast = a[0];
-    __syncthreads();
-    const float r = *bcast;
-    __syncthreads();
-    return r;
-}
 
 // ------------------------------------------------------ register rows ----
 
@@ -173,12 +135,6 @@ __device__ __forceinline__ void load_run(const float *__restrict__ p, int64_t s,
 }
 
 // ------------------------------------------------ shared-memory stage ----
-
-// Run u of a row occupies 128 bytes of the stage at u*128; its 16-byte chunk c
-// sits in slot c ^ (u & 7).  Eight consecutive lanes then hit eight different
-// bank groups both when they copy eight consecutive chunks of one run and when
-// each reads the same chunk of its own run.
-__device__ __forceinline__ int stage_slot(int u, int c) { return u * 8 + (c ^ (u & 7)); }
 
 // Starts the copy of the row's runs [0, T*R) into the stage; each warp copies
 // the runs its own lanes own (so only __syncwarp is needed before reading).
@@ -323,10 +279,6 @@ __device__ __forceinline__ void exp_minus2(float &a, float &b, float m) {
 struct Ident {
     __device__ __forceinline__ float operator()(float x) const { return x; }
 };
-struct Square {
-    __device__ __forceinline__ float operator()(float x) const { return __fmul_rn(x, x); }
-};
-
 template <int T, int R>
 __global__ void __launch_bounds__(T)
 softmax_rows_kernel(int64_t rows, int64_t n, const float *__restrict__ x, int64_t ldx, float *__restrict__ y,
@@ -700,19 +652,6 @@ gelu_kernel(int64_t n, const float *__restrict__ x, float *__restrict__ y, int v
 // row stays cached between phases), column sums (repeated passes folding runs
 // of 32 rows: the level-by-level tree).
 
-// Tree reduction over i in [0, n) of f(i) (an index functor), as generic_reduce.
-template <Op OP, class F>
-__device__ float generic_reduce_idx(int64_t n, F f, float *buf, float *buf2, float *bcast) {
-    const int runs = int((n + RUN - 1) / RUN);
-    for (int j = threadIdx.x; j < runs; j += blockDim.x) {
-        const int64_t s = int64_t(j) * RUN, e = imin64(s + RUN, n);
-        float acc = f(s);
-        for (int64_t i = s + 1; i < e; ++i) acc = combine<OP>(acc, f(i));
-        buf[j] = acc;
-    }
-    return tree_upper<OP>(buf, buf2, runs, bcast);
-}
-
 __device__ __forceinline__ float gelu_grad_fixed(float x) {
     const float z = __fmul_rn(x, 0.707106769084930419921875f);
     const float e = erfc_pos(fabsf(z));
@@ -927,24 +866,6 @@ softmax_backward_staged_kernel(int64_t rows, int64_t n, const float *p, int64_t 
     }
 }
 
-// One tree level of a column sum: out[q][j] = fold of rows [32q, 32q + 32) of
-// column j (left to right from the first).  Threads run along columns
-// (coalesced), the grid's y dimension along q.
-__global__ void __launch_bounds__(256)
-colsum_pass_kernel(int64_t rows, int64_t cols, const float *__restrict__ x, int64_t ldx, float *__restrict__ out,
-                   int64_t ldo) {
-    const int64_t groups = (rows + RUN - 1) / RUN;
-    for (int64_t q = blockIdx.y; q < groups; q += gridDim.y) {
-        const int64_t r0 = q * RUN, r1 = imin64(r0 + RUN, rows);
-        for (int64_t j = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; j < cols;
-             j += int64_t(gridDim.x) * blockDim.x) {
-            float acc = x[r0 * ldx + j];
-            for (int64_t i = r0 + 1; i < r1; ++i) acc = __fadd_rn(acc, x[i * ldx + j]);
-            out[q * ldo + j] = acc;
-        }
-    }
-}
-
 // ------------------------------------------------------------ host ----
 
 int check_rows(int64_t rows, int64_t cols, const float *x, int64_t ldx, const float *y, int64_t ldy) {
@@ -963,28 +884,6 @@ int check_rows(int64_t rows, int64_t cols, const float *x, int64_t ldx, const fl
 bool rows_vec_ok(const float *x, int64_t ldx, const float *y, int64_t ldy) {
     return reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0 &&
            ldx % 4 == 0 && ldy % 4 == 0;
-}
-
-int grid_for_rows(int64_t rows) {
-    DeviceInfo di;
-    const int sms = current_device_info(&di) == REPOPS_OK ? di.sms : 152;
-    return int(std::min<int64_t>(rows, int64_t(sms) * 32));
-}
-
-// Launches `kern` with as many CTAs as fit on the device at once (at most one
-// per row); each CTA then strides over the rows.
-template <class Kern, class... Args>
-int launch_persistent(Kern kern, int threads, size_t smem, int64_t rows, cudaStream_t s, Args... args) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    DeviceInfo di;
-    const int sms = current_device_info(&di) == REPOPS_OK ? di.sms : 152;
-    const int grid = int(std::min<int64_t>(rows, int64_t(std::max(per_sm, 1)) * sms));
-    kern<<<grid, threads, smem, s>>>(args...);
-    return check_launch();
 }
 
 // kind 0 = softmax, 1 = LayerNorm, 2 = RMSNorm
@@ -1123,16 +1022,6 @@ extern "C" int repops_gelu_backward_f32(int64_t n, const float *x, const float *
     gelu_backward_kernel<<<std::max(grid, 1), 256, 0, stream>>>(n, x, dy, dx, vec);
     return check_launch();
 }
-
-namespace {
-// Span check for a rows x cols operand with pitch ld; false on overflow.
-bool rows_span(int64_t rows, int64_t cols, int64_t ld, uint64_t *bytes) {
-    if (rows == 0 || cols == 0) { *bytes = 0; return true; }
-    if (ld < cols || rows - 1 > (INT64_MAX / 4 - cols) / ld) return false;
-    *bytes = uint64_t((rows - 1) * ld + cols) * 4u;
-    return true;
-}
-}  // namespace
 
 extern "C" int repops_rmsnorm_backward_f32(int64_t rows, int64_t cols, const float *x, int64_t ldx,
                                            const float *gamma, float eps, const float *dy, int64_t lddy,

@@ -1,0 +1,56 @@
+// rows8.cuh -- the 8-bit row format: whole numbers q in [-127, 127] with one
+// binary32 scale for every `group` consecutive columns of a row (group 0: one
+// for the whole row); q stands for fl(q * scale).  Shared by the kernels that
+// write it and those that read it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.cuh"
+
+namespace repops {
+namespace {
+
+// column >> shift is the column's group; group 0 puts every column in group 0
+// (columns are below 2^31)
+inline int group_shift(int64_t group) {
+    int s = 0;
+    if (group == 0) return 31;
+    while ((int64_t(1) << s) < group) ++s;
+    return s;
+}
+
+// Groups are whole runs of the 32-ary tree, so that a run has one scale.
+inline bool known_group(int64_t group) {
+    return group == 0 || group == 32 || group == 64 || group == 128 || group == 256;
+}
+
+inline int64_t group_count(int64_t cols, int64_t group) { return group == 0 ? 1 : (cols + group - 1) / group; }
+
+[[maybe_unused]] inline bool known_storage(int t) {
+    return t == REPOPS_TYPE_F32 || t == REPOPS_TYPE_F16 || t == REPOPS_TYPE_BF16;
+}
+[[maybe_unused]] inline unsigned storage_size(int t) { return t == REPOPS_TYPE_F32 ? 4u : 2u; }
+
+// Bytes spanned by rows x cols elements of `size` bytes at pitch ld; false
+// when ld is short or the span overflows.
+[[maybe_unused]] inline bool span_bytes(int64_t rows, int64_t cols, int64_t ld, unsigned size, uint64_t *bytes) {
+    *bytes = 0;
+    if (ld < cols) return false;
+    if (rows == 0 || cols == 0) return true;
+    if (ld > INT64_MAX / 8 || rows - 1 > (INT64_MAX / 8 - cols) / ld) return false;
+    *bytes = uint64_t((rows - 1) * ld + cols) * size;
+    return true;
+}
+
+// Four whole numbers packed in a word, lowest byte first, each as the value it
+// stands for: one rounding, fl(q * scale).
+__device__ __forceinline__ float4 unpack_q4(uint32_t w, float scale) {
+    const int v = static_cast<int>(w);
+    return make_float4(__fmul_rn(float((v << 24) >> 24), scale), __fmul_rn(float((v << 16) >> 24), scale),
+                       __fmul_rn(float((v << 8) >> 24), scale), __fmul_rn(float(v >> 24), scale));
+}
+
+}  // namespace
+}  // namespace repops
