@@ -1013,6 +1013,40 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
                                float *dgamma, void *ws, uint64_t ws_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Product of 8-bit integers                                                 */
+/* "Verde与RepOps" §3.2: only dimensions whose order matters need a fixed    */
+/* order.  A sum of whole numbers has none, so this product may use the      */
+/* tensor cores and any split of k and still give the same bits.             */
+/* ------------------------------------------------------------------------ */
+
+/* C = A * B^T scaled by row and column, for 8-bit integers (any, -128 too):
+ *   acc = sum over k < K of A[i*lda + k] * B[j*ldb + k]     (exact)
+ *   C[i*ldc + j] = fl(fl(fl(acc) * a_scale[i]) * b_scale[j]), then
+ *                  fl(.. + bias[j]) when bias is not NULL, narrowed once to typeC
+ * A (device): M x K, a row per token; B: N x K, a row per output channel (the
+ * weights of a K x N matrix stored transposed), both with k contiguous and any
+ * pitch and alignment; a_scale: M, b_scale and bias: N floats.  K == 0 gives
+ * the scaled zero (+ bias).
+ * config -1 chooses by size; 0 .. repops_gemm_i8_config_count() - 1 force a
+ * kernel (the same bits): 0 splits k between the warps of a CTA and suits few
+ * rows of A; 1, 2 and 3 run tiles of 128 x 256, 128 x 128 and 128 x 64 on the
+ * tensor cores from operands widened to binary16 in scratch.
+ * ws: device scratch of repops_gemm_i8_workspace_bytes(config, M, N, K) bytes
+ * (0 for config 0) on a 16-byte boundary, or NULL to take it from the scratch
+ * pool on `stream` (ALLOC when refused).
+ * INVALID_ARG for negative sizes, unknown types or configs, null pointers,
+ * short pitches or scratch; ALIAS when C or ws overlaps an operand or each
+ * other; UNSUPPORTED for K above 131071 (acc would leave 32 bits) or more than
+ * 2^30 tiles. */
+int repops_gemm_i8_config_count(void);
+int repops_gemm_i8_auto_config(int64_t M, int64_t N, int64_t K);
+uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_t N, int64_t K);
+int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                   const float *a_scale, const int8_t *B, int64_t ldb, const float *b_scale,
+                   const float *bias, void *C, int typeC, int64_t ldc, void *ws, uint64_t ws_bytes,
+                   cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* The edge between two blocks                                               */
 /* "Verde与RepOps" §4.3 (Llama-style training): the norm after a block, its  */
 /* gate and residual scale, the residual sum and the norm before the next    */

@@ -193,3 +193,30 @@ def test_reference_format_on_known_values():
     assert s[0, 0] == 1.0 and q.tolist() == [[127, -64, 1, 0]]
     q, s = ref.quantize(np.array([[0.0, 0.0]], np.float32), 32)
     assert q.tolist() == [[0, 0]] and s[0, 0] > 0
+
+
+def test_gemm_i8_refusals(L):
+    s = L.repops_gemm_i8
+    assert L.repops_gemm_i8_config_count() == 4
+    ws_bytes = L.repops_gemm_i8_workspace_bytes
+    need = ws_bytes(1, 4, 6, 64)
+    assert need > 0 and ws_bytes(0, 4, 6, 64) == 0 and ws_bytes(9, 4, 6, 64) == 0 and ws_bytes(1, 0, 6, 64) == 0
+    assert L.repops_gemm_i8_auto_config(-1, 1, 1) == -1
+
+    def call(**kw):
+        a = dict(cfg=1, M=4, N=6, K=64, A=A, lda=64, sa=B, B=C, ldb=64, sb=D, bias=E, C=F, tc=0, ldc=6, ws=W, wsb=need)
+        a.update(kw)
+        return s(*a.values(), None)
+
+    assert call(M=-1) == -1 and call(N=-1) == -1 and call(K=-1) == -1
+    assert call(cfg=4) == -1 and call(cfg=-2) == -1 and call(tc=3) == -1
+    for k in ("A", "sa", "B", "sb", "C"):
+        assert call(**{k: None}) == -1
+    assert call(lda=63) == -1 and call(ldb=63) == -1 and call(ldc=5) == -1
+    assert call(wsb=need - 1) == -1 and call(ws=W + 8) == -1
+    for other in (A, B, C, D, E):
+        assert call(C=other) == -2
+        assert call(ws=other) == -2
+    assert call(ws=F) == -2
+    assert call(K=131072, lda=131072, ldb=131072) == -7
+    assert call(M=0) == 0 and call(N=0) == 0

@@ -29,6 +29,9 @@ memory and streams.
   swiglu / swiglu_backward /        SiLU-gated MLP activation and rotary
   rope_frequencies / rope_table /   position embeddings of a Llama-style layer
   rope                              ("Verde与RepOps" §4.3)
+  gemm_i8(A, B, a_scale, b_scale)   product of 8-bit integers, scales for each
+                                    token and channel: exact sums, so any order
+                                    ("Verde与RepOps" §3.2, §5.3)
   quantize_rows / dequantize_rows   rows in 8 bits with a scale a group: activation
                                     checkpoints, and gemm_i8's operands
   swiglu_backward_i8 /              backward operators that read such rows
@@ -50,6 +53,7 @@ __all__ = ["load", "version", "scratch_set_keep_bytes", "scratch_release", "scra
            "softmax_rows", "layernorm_rows", "rmsnorm_rows", "gelu", "gemm_batched",
            "convert", "gemm_typed", "rolling_hash", "TYPE_F32", "TYPE_F16", "TYPE_BF16",
            "colsum", "gelu_backward", "rmsnorm_backward", "softmax_backward",
+           "gemm_i8", "gemm_i8_config_count", "gemm_i8_auto_config",
            "quantize_rows", "dequantize_rows", "swiglu_backward_i8", "rmsnorm_backward_i8",
            "rmsnorm_residual", "rmsnorm_residual_backward",
            "swiglu", "swiglu_backward", "rope_frequencies", "rope_table", "rope",
@@ -1010,6 +1014,60 @@ def dequantize_rows(q, scale, *, group: int = 0, dtype=None, out=None, stream=No
                                           _stream_handle(stream))
     _capi.check(rc, "repops_dequantize_rows_i8")
     return out
+
+
+def _scale_vector(t, n, name):
+    import torch
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of %d values" % (name, n))
+    return t.data_ptr()
+
+
+def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, config: int = -1, stream=None):
+    """out[i][j] = (sum_k A[i][k] * B[k][j]) * a_scale[i] * b_scale[j] (+ bias[j])
+    for int8 CUDA tensors: the sum is exact, each step after it one binary32
+    rounding, narrowed once to out's dtype (repops_gemm_i8).
+
+    A: (M, K), unit column stride.  B: (K, N) with unit row stride: the
+    transposed view W.t() of weights (N, K) stored a row per output channel, as
+    quantize_rows leaves them.  a_scale: M, b_scale and bias: N float32 values.
+    out_dtype: float32 (default), float16 or bfloat16.  config: -1 chooses by
+    size, 0 .. gemm_i8_config_count() - 1 force a kernel (the same bits)."""
+    import torch
+    if A.dtype != torch.int8 or B.dtype != torch.int8 or A.dim() != 2 or B.dim() != 2:
+        raise TypeError("A and B must be 2-D int8 CUDA tensors")
+    M, K = A.shape
+    K2, N = B.shape
+    if K != K2:
+        raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
+    if (K > 1 and (A.stride(1) != 1 or B.stride(0) != 1)) or (M > 1 and A.stride(0) < K) or \
+            (N > 1 and B.stride(1) < K):
+        raise ValueError("k must be contiguous: A with unit column stride, B a transposed view W.t() of (N, K) weights")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
+    if out.dim() != 2 or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1) or \
+            (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be (M, N) with unit column stride and the dtype asked for")
+    _on_device(A=A, B=B, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
+    pa, pb = _scale_vector(a_scale, M, "a_scale"), _scale_vector(b_scale, N, "b_scale")
+    pbias = None if bias is None else _scale_vector(bias, N, "bias")
+    L = load()
+    need = L.repops_gemm_i8_workspace_bytes(config, M, N, K)
+    ws = _workspace(need, A.device, stream) if need else None
+    rc = L.repops_gemm_i8(config, M, N, K, A.data_ptr(), max(A.stride(0), K), pa, B.data_ptr(), max(B.stride(1), K), pb,
+                          pbias, out.data_ptr(), _storage_type(out.dtype), max(out.stride(0), N, 1),
+                          ws.data_ptr() if ws is not None else None, need, _stream_handle(stream))
+    _capi.check(rc, "repops_gemm_i8")
+    return out
+
+
+def gemm_i8_config_count() -> int:
+    return load().repops_gemm_i8_config_count()
+
+
+def gemm_i8_auto_config(M: int, N: int, K: int) -> int:
+    """The kernel the automatic choice runs for M x N x K (see gemm_i8)."""
+    return load().repops_gemm_i8_auto_config(M, N, K)
 
 
 def _row_like(t, shape, name):

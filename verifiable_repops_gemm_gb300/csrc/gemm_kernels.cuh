@@ -863,14 +863,6 @@ gemm_cpasync_kernel(const float *__restrict__ A, int64_t lda, const float *__res
 
 // --------------------------------------------------------------- host ----
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled from the driver (null when unavailable).
-EncodeTiledFn tensor_map_encoder();
-
 // 2-D fp32 tensor map: inner extent `inner`, outer extent `outer`, row pitch
 // `ld` elements, box (box_inner x box_outer), zero fill out of bounds.
 inline bool make_map(CUtensorMap *map, const float *base, int64_t inner, int64_t outer, int64_t ld,
