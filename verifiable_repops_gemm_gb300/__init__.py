@@ -67,7 +67,8 @@ __all__ = ["load", "version", "scratch_set_keep_bytes", "scratch_release", "scra
 def _stream_handle(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: building a Stream object costs 3 us of a small call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -949,8 +950,9 @@ def _on_device(**tensors):
     """Every given tensor (None skipped) must live on the current CUDA device,
     where the call's kernels run."""
     import torch
+    here = torch.cuda.current_device()
     for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+        if t is not None and t.get_device() != here:      # -1 for a CPU tensor
             raise ValueError("%s must be a tensor on the current CUDA device" % name)
 
 

@@ -42,35 +42,38 @@ constexpr int64_t MAX_FOLD_ROWS = RUN * RUN;    // run results the last fold tak
 // 128k + lane + {0, 32, 64, 96}.
 
 template <bool VEC>
-__device__ __forceinline__ int64_t slab_col(int k, int t) {
+__device__ __forceinline__ int slab_col(int k, int t) {
     const int lane = threadIdx.x & 31, slab = (threadIdx.x >> 5) * 1024;
     return VEC ? slab + 128 * k + 4 * lane + t : slab + 128 * k + 32 * t + lane;
 }
 
+// Loads take no branch, so that a slab's are all in flight together: a column
+// past the row's end reads column 0 instead, and its result is never stored or
+// folded.  n is a multiple of 4 with VEC.
 template <bool VEC>
-__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int k, int64_t n) {
+__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int k, int n) {
+    const int c = slab_col<VEC>(k, 0);
     if constexpr (VEC) {
-        const int64_t c = slab_col<VEC>(k, 0);
-        if (c + 4 <= n) return __ldg(reinterpret_cast<const float4 *>(row + c));
-        return make_float4(c < n ? row[c] : 0.0f, c + 1 < n ? row[c + 1] : 0.0f, c + 2 < n ? row[c + 2] : 0.0f, 0.0f);
+        return __ldg(reinterpret_cast<const float4 *>(row + (c < n ? c : 0)));
     } else {
-        const int64_t c = slab_col<VEC>(k, 0);
-        return make_float4(c < n ? row[c] : 0.0f, c + 32 < n ? row[c + 32] : 0.0f, c + 64 < n ? row[c + 64] : 0.0f,
-                           c + 96 < n ? row[c + 96] : 0.0f);
+        return make_float4(__ldg(row + (c < n ? c : 0)), __ldg(row + (c + 32 < n ? c + 32 : 0)),
+                           __ldg(row + (c + 64 < n ? c + 64 : 0)), __ldg(row + (c + 96 < n ? c + 96 : 0)));
     }
 }
 
+// Asks for the warp's slab of a parameter row (may be null) ahead of its use.
 template <bool VEC>
-__device__ __forceinline__ void row_store(float *row, int k, int64_t n, float4 v) {
-    const int64_t c = slab_col<VEC>(k, 0);
+__device__ __forceinline__ void row_prefetch(const float *row, int n) {
+    if (!row) return;
+    const int c = (threadIdx.x >> 5) * 1024 + 32 * (threadIdx.x & 31);     // a 128-byte line a lane
+    if (c < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
+}
+
+template <bool VEC>
+__device__ __forceinline__ void row_store(float *row, int k, int n, float4 v) {
+    const int c = slab_col<VEC>(k, 0);
     if constexpr (VEC) {
-        if (c + 4 <= n) {
-            *reinterpret_cast<float4 *>(row + c) = v;
-        } else {
-            if (c < n) row[c] = v.x;
-            if (c + 1 < n) row[c + 1] = v.y;
-            if (c + 2 < n) row[c + 2] = v.z;
-        }
+        if (c < n) *reinterpret_cast<float4 *>(row + c) = v;
     } else {
         if (c < n) row[c] = v.x;
         if (c + 32 < n) row[c + 32] = v.y;
@@ -111,17 +114,17 @@ __device__ __forceinline__ void stage_store(float4 *stage, int k, float4 v) {
 
 // Starts the copy of the warp's slab of a row into the stage.
 template <bool VEC>
-__device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict__ row, int64_t n) {
+__device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict__ row, int n) {
     float *s = reinterpret_cast<float *>(stage);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if constexpr (VEC) {
-            const int64_t c = slab_col<VEC>(k, 0);
-            if (c < n) cp_async_16(s + stage_float<VEC>(k, 0), row + c, uint32_t(imin64(4, n - c)) * 4u);
+            const int c = slab_col<VEC>(k, 0);
+            if (c < n) cp_async_16(s + stage_float<VEC>(k, 0), row + c, 16u);
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int64_t c = slab_col<VEC>(k, t);
+                const int c = slab_col<VEC>(k, t);
                 if (c < n) cp_async_4(s + stage_float<VEC>(k, t), row + c, 4u);
             }
         }
@@ -131,10 +134,9 @@ __device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict
 // The warp's group result of the tree over the staged values f(v): each lane
 // folds its run, every lane folds the lanes' results in order.
 template <class F>
-__device__ __forceinline__ float slab_fold(const float4 *stage, int64_t n, F f) {
+__device__ __forceinline__ float slab_fold(const float4 *stage, int n, F f) {
     const int u = threadIdx.x, warp0 = u & ~31;
-    const int64_t s = int64_t(u) * RUN;
-    const int len = s < n ? int(imin64(RUN, n - s)) : 0;
+    const int len = min(RUN, n - u * RUN);                 // 0 or less past the end
     float v[RUN];
 #pragma unroll
     for (int c = 0; c < RUN / 4; ++c) {
@@ -150,7 +152,7 @@ __device__ __forceinline__ float slab_fold(const float4 *stage, int64_t n, F f) 
         for (int i = 1; i < RUN; ++i)
             if (i < len) acc = __fadd_rn(acc, f(v[i]));
     }
-    const int have = int((n + RUN - 1) / RUN) - warp0;     // runs present from this warp on
+    const int have = (n + RUN - 1) / RUN - warp0;     // runs present from this warp on
     float g = __shfl_sync(0xffffffffu, acc, 0);
     if (have >= RUN) {
 #pragma unroll
@@ -174,14 +176,14 @@ struct GroupBuf {
 };
 
 template <int T, int NV>
-__device__ __forceinline__ void slab_roots(float (&v)[NV], GroupBuf<T, NV> &gb, int &phase, int64_t n) {
+__device__ __forceinline__ void slab_roots(float (&v)[NV], GroupBuf<T, NV> &gb, int &phase, int n) {
     if constexpr (T > 32) {
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) gb.g[phase][j][threadIdx.x >> 5] = v[j];
         }
         __syncthreads();
-        const int G = int((n + 1023) / 1024);
+        const int G = (n + 1023) / 1024;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             v[j] = gb.g[phase][j][0];
@@ -234,12 +236,13 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     int phase = 0;
     constexpr int Q = T * RUN / 4;
     constexpr bool PF = kEdgePrefetch<T>;
+    const int n = int(p.n);
     const float nf = float(p.n);
     int cur = 0;
     int64_t row = blockIdx.x;
     if (row < p.rows) {
-        stage_row<VEC>(stage_mem, p.f + row * p.ldf, p.n);
-        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, p.n);
+        stage_row<VEC>(stage_mem, p.f + row * p.ldf, n);
+        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, n);
     }
     cp_async_commit();
     for (; row < p.rows; row += gridDim.x) {
@@ -248,47 +251,64 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         if constexpr (PF) {
             cur ^= 1;
             if (next < p.rows) {
-                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, p.n);
-                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, p.n);
+                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, n);
+                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, n);
             }
             cp_async_commit();
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
         }
+        const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+        if (row == blockIdx.x) {            // the parameters are on their way while the first row is
+            row_prefetch<VEC>(p.post, n);
+            row_prefetch<VEC>(gate, n);
+            row_prefetch<VEC>(p.pre, n);
+        }
+        cp_async_wait<PF ? 1 : 0>();
         __syncwarp();
         float inv_f = 0.0f;
         if (p.post) {
-            float s[1] = {slab_fold(sf, p.n, Square())};
-            slab_roots<T, 1>(s, gb, phase, p.n);
+            float s[1] = {slab_fold(sf, n, Square())};
+            slab_roots<T, 1>(s, gb, phase, n);
             inv_f = rms_inv(s[0], nf, p.eps);
         }
-        const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
         float *yr = p.y + row * p.ldy;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float4 v = stage_load<VEC>(sf, k);
-            if (p.post) v = mul4(mul4(v, inv_f), row_load<VEC>(p.post, k, p.n));
-            if (gate) v = mul4(v, row_load<VEC>(gate, k, p.n));
-            v = add4(stage_load<VEC>(sx, k), mul4(v, p.alpha));
-            row_store<VEC>(yr, k, p.n, v);
-            if (p.pre) stage_store<VEC>(sx, k, v);
+        for (int b = 0; b < 8; b += 4) {    // four steps' loads in flight together
+            float4 w[4], g[4];
+            if (p.post) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = row_load<VEC>(p.post, b + k, n);
+            }
+            if (gate) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] = row_load<VEC>(gate, b + k, n);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float4 v = stage_load<VEC>(sf, b + k);
+                if (p.post) v = mul4(mul4(v, inv_f), w[k]);
+                if (gate) v = mul4(v, g[k]);
+                v = add4(stage_load<VEC>(sx, b + k), mul4(v, p.alpha));
+                row_store<VEC>(yr, b + k, n, v);
+                if (p.pre) stage_store<VEC>(sx, b + k, v);
+            }
         }
         if (p.pre) {
             __syncwarp();
-            float s[1] = {slab_fold(sx, p.n, Square())};
-            slab_roots<T, 1>(s, gb, phase, p.n);
+            float s[1] = {slab_fold(sx, n, Square())};
+            slab_roots<T, 1>(s, gb, phase, n);
             const float inv_y = rms_inv(s[0], nf, p.eps);
             float *hr = p.h + row * p.ldh;
+            float4 w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                row_store<VEC>(hr, k, p.n, mul4(mul4(stage_load<VEC>(sx, k), inv_y), row_load<VEC>(p.pre, k, p.n)));
+            for (int k = 0; k < 8; ++k) w[k] = row_load<VEC>(p.pre, k, n);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) row_store<VEC>(hr, k, n, mul4(mul4(stage_load<VEC>(sx, k), inv_y), w[k]));
         }
         __syncwarp();                       // the stage is read before it is filled again
         if constexpr (!PF) {
             if (next < p.rows) {
-                stage_row<VEC>(sf, p.f + next * p.ldf, p.n);
-                stage_row<VEC>(sx, p.x + next * p.ldx, p.n);
+                stage_row<VEC>(sf, p.f + next * p.ldf, n);
+                stage_row<VEC>(sx, p.x + next * p.ldx, n);
             }
             cp_async_commit();
         }
@@ -358,57 +378,61 @@ struct EdgeBackArgs {
 };
 
 template <bool VEC>
-__device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, int k) {
-    const int64_t c = slab_col<VEC>(k, 0);
+__device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, int k, int n) {
+    const int c = slab_col<VEC>(k, 0);
     const int8_t *q = p.q + row * p.ldq;
     const float *s = p.s + row * p.lds;
-    if constexpr (VEC) {
-        // a group is a multiple of 4 columns, and so is n
-        return c < p.n ? unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(q + c)), __ldg(s + (c >> p.shift)))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (VEC) {                   // a group is a multiple of 4 columns
+        const int i = c < n ? c : 0;
+        return unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(q + i)), __ldg(s + (i >> p.shift)));
     } else {
         float v[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int64_t i = c + 32 * t;
-            v[t] = i < p.n ? __fmul_rn(float(q[i]), __ldg(s + (i >> p.shift))) : 0.0f;
+            const int i = c + 32 * t < n ? c + 32 * t : 0;
+            v[t] = __fmul_rn(float(__ldg(q + i)), __ldg(s + (i >> p.shift)));
         }
         return make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
+// Resident CTAs per SM the row kernel asks the compiler for.
+template <int T>
+constexpr int kEdgeBackBlocks = 448 / T;
+
 // dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
 // after the block.  Q8: y comes in 8 bits, and h may be written again.
 template <int T, bool VEC, bool Q8, bool F>
-__global__ void __launch_bounds__(T) edge_backward_kernel(EdgeBackArgs p) {
+__global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(EdgeBackArgs p) {
     extern __shared__ float4 stage_mem[];
     __shared__ GroupBuf<T, 2> gb2;
     __shared__ GroupBuf<T, 1> gb1;
     int phase1 = 0, phase2 = 0;
     constexpr int Q = T * RUN / 4;
     float4 *sy = stage_mem, *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
+    const int n = int(p.n);
     const float nf = float(p.n);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         if (p.dh) {
-            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, p.n);
-            stage_row<VEC>(sh, p.dh + row * p.lddh, p.n);
+            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, n);
+            stage_row<VEC>(sh, p.dh + row * p.lddh, n);
         }
-        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, p.n);
+        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, n);
         cp_async_commit();
-        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, p.n);
+        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, n);
         cp_async_commit();
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, k, row8_load<VEC>(p, row, k));
+            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, k, row8_load<VEC>(p, row, k, n));
         }
         cp_async_wait<1>();
         __syncwarp();
         float r2[2] = {0.0f, 0.0f};
-        if (p.dh) r2[0] = slab_fold(sy, p.n, Square());
+        if (p.dh) r2[0] = slab_fold(sy, n, Square());
         if constexpr (F) {
-            if (p.post) r2[1] = slab_fold(sf, p.n, Square());
+            if (p.post) r2[1] = slab_fold(sf, n, Square());
         }
-        slab_roots<T, 2>(r2, gb2, phase2, p.n);
+        slab_roots<T, 2>(r2, gb2, phase2, n);
         const float inv_y = rms_inv(r2[0], nf, p.eps), inv_f = rms_inv(r2[1], nf, p.eps);
         if (threadIdx.x == 0) {
             if (p.dh) p.inv_y[row] = inv_y;
@@ -418,25 +442,27 @@ __global__ void __launch_bounds__(T) edge_backward_kernel(EdgeBackArgs p) {
         }
         float4 e[8];                              // dx
         if (p.dh) {
-            // sy <- xh, sh <- gy after their products are summed from sh
-            float4 gy[8];
+            // sh <- gy * xh, summed from there
+            float4 g[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(p.pre, k, n);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float4 g = row_load<VEC>(p.pre, k, p.n);
-                e[k] = mul4(stage_load<VEC>(sy, k), inv_y);
-                gy[k] = mul4(stage_load<VEC>(sh, k), g);
+                const float4 xh = mul4(stage_load<VEC>(sy, k), inv_y);
                 if constexpr (Q8) {
-                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, p.n, mul4(e[k], g));
+                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, n, mul4(xh, g[k]));
                 }
+                g[k] = mul4(stage_load<VEC>(sh, k), g[k]);
+                stage_store<VEC>(sh, k, mul4(g[k], xh));
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) stage_store<VEC>(sh, k, mul4(gy[k], e[k]));
+            // only gy stays in registers over the fold
             __syncwarp();
-            float r1[1] = {slab_fold(sh, p.n, Ident())};
-            slab_roots<T, 1>(r1, gb1, phase1, p.n);
+            float r1[1] = {slab_fold(sh, n, Ident())};
+            slab_roots<T, 1>(r1, gb1, phase1, n);
             const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(gy[k], mul4(e[k], c)), inv_y);
+            for (int k = 0; k < 8; ++k)
+                e[k] = mul4(sub4(g[k], mul4(mul4(stage_load<VEC>(sy, k), inv_y), c)), inv_y);
         }
         cp_async_wait<0>();
         __syncwarp();
@@ -449,32 +475,39 @@ __global__ void __launch_bounds__(T) edge_backward_kernel(EdgeBackArgs p) {
         }
         float *dxr = p.dx + row * p.lddx;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, k, p.n, e[k]);
+        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, k, n, e[k]);
         if constexpr (F) {
             float *dfr = p.df + row * p.lddf;
             const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+            float4 g[8];
+            if (gate) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(gate, k, n);
+            }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 e[k] = mul4(e[k], p.alpha);
-                if (gate) e[k] = mul4(e[k], row_load<VEC>(gate, k, p.n));
+                if (gate) e[k] = mul4(e[k], g[k]);
             }
             if (p.post) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(p.post, k, n);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    e[k] = mul4(e[k], row_load<VEC>(p.post, k, p.n));
+                    e[k] = mul4(e[k], g[k]);
                     stage_store<VEC>(sr, k, mul4(e[k], mul4(stage_load<VEC>(sf, k), inv_f)));
                 }
                 __syncwarp();
-                float r1[1] = {slab_fold(sr, p.n, Ident())};
-                slab_roots<T, 1>(r1, gb1, phase1, p.n);
+                float r1[1] = {slab_fold(sr, n, Ident())};
+                slab_roots<T, 1>(r1, gb1, phase1, n);
                 const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     e[k] = mul4(sub4(e[k], mul4(mul4(stage_load<VEC>(sf, k), inv_f), c)), inv_f);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, k, p.n, e[k]);
+            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, k, n, e[k]);
         }
         __syncwarp();
     }
@@ -557,89 +590,107 @@ struct ColArgs {
     int64_t ldg;                // pitch of gate's (the others are packed)
 };
 
+template <int W>
+struct Cols {
+    float v[W];
+};
+
+template <int W>
+__device__ __forceinline__ Cols<W> cols_load(const float *q) {
+    Cols<W> r;
+    if constexpr (W == 4) {
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(q));
+        r.v[0] = w.x; r.v[1] = w.y; r.v[2] = w.z; r.v[3] = w.w;
+    } else {
+        r.v[0] = __ldg(q);
+    }
+    return r;
+}
+
+template <int W>
+__device__ __forceinline__ void cols_store(float *q, const Cols<W> &r) {
+    if constexpr (W == 4) *reinterpret_cast<float4 *>(q) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+    else *q = r.v[0];
+}
+
 // A thread forms and folds the terms of W columns over a run of 32 rows:
 //   pre:  dh * (y * inv_y)
 //   post: ((alpha * dx) * gate) * (f * inv_f)
 //   gate: (alpha * dx) * ((f * inv_f) * post)
-template <int W, bool Q8, bool F>
+// PRE, POST, GATE: the sums wanted; eight rows' loads are in flight together.
+template <int W, bool Q8, bool PRE, bool POST, bool GATE>
 __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
     const EdgeBackArgs &p = a.e;
+    constexpr int B = 8;                 // rows loaded at once; RUN is a multiple
     const int64_t c = (blockIdx.x * int64_t(128) + threadIdx.x) * W;
     if (c >= p.n) return;
-    struct V { float v[W]; };
-    auto ld = [&](const float *q) {
-        V r;
-        if constexpr (W == 4) {
-            const float4 w = __ldg(reinterpret_cast<const float4 *>(q + c));
-            r.v[0] = w.x; r.v[1] = w.y; r.v[2] = w.z; r.v[3] = w.w;
-        } else {
-            r.v[0] = __ldg(q + c);
-        }
-        return r;
-    };
-    auto st = [&](float *q, const V &r) {
-        if constexpr (W == 4) *reinterpret_cast<float4 *>(q + c) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-        else q[c] = r.v[0];
-    };
-    V post;
-    if (F && a.gate && p.post) post = ld(p.post);
+    Cols<W> post{};
+    if (GATE && p.post) post = cols_load<W>(p.post + c);
     for (int64_t run = blockIdx.y; run < a.runs; run += gridDim.y) {
         const int64_t b = run / a.block_runs, first = b * a.block_rows + (run - b * a.block_runs) * RUN;
-        const int64_t last = imin64(first + RUN, (b + 1) * a.block_rows);
-        V s_pre, s_post, s_gate;
-        V gate;
-        int64_t gate_left = 0;      // rows until the next gate row begins
+        const int rows = int(imin64(RUN, (b + 1) * a.block_rows - first));
+        Cols<W> s_pre, s_post, s_gate, gate{};
+        int64_t gate_left = 0;           // rows until the next gate row begins
         const float *gate_row = nullptr;
-        if (F && a.post && p.gate) {
-            gate_row = p.gate + (first / p.gate_rows) * p.ldgate;
+        if (POST && p.gate) {
+            gate_row = p.gate + (first / p.gate_rows) * p.ldgate + c;
             gate_left = p.gate_rows - first % p.gate_rows;
-            gate = ld(gate_row);
+            gate = cols_load<W>(gate_row);
         }
-#pragma unroll 4
-        for (int64_t r = first; r < last; ++r) {
-            const bool start = r == first;
-            if (a.pre) {
-                V y;
-                if constexpr (Q8) {
-                    const float s = __ldg(p.s + r * p.lds + (c >> p.shift));
-                    if constexpr (W == 4) {
-                        const float4 w = unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
-                        y.v[0] = w.x; y.v[1] = w.y; y.v[2] = w.z; y.v[3] = w.w;
-                    } else {
-                        y.v[0] = __fmul_rn(float(p.q[r * p.ldq + c]), s);
-                    }
-                } else {
-                    y = ld(p.y + r * p.ldy);
-                }
-                const V d = ld(p.dh + r * p.lddh);
-                const float inv = __ldg(p.inv_y + r);
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += B) {
+            Cols<W> y[B], d[B], dx[B], f[B];
+            float iy[B], jf[B];
 #pragma unroll
-                for (int t = 0; t < W; ++t) {
-                    const float v = __fmul_rn(d.v[t], __fmul_rn(y.v[t], inv));
-                    s_pre.v[t] = start ? v : __fadd_rn(s_pre.v[t], v);
+            for (int i = 0; i < B; ++i) {
+                const int64_t r = first + min(r0 + i, rows - 1);     // past the run: its last row, not folded
+                if constexpr (PRE) {
+                    if constexpr (Q8) {
+                        const float s = __ldg(p.s + r * p.lds + (c >> p.shift));
+                        if constexpr (W == 4) {
+                            const float4 w = unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
+                            y[i].v[0] = w.x; y[i].v[1] = w.y; y[i].v[2] = w.z; y[i].v[3] = w.w;
+                        } else {
+                            y[i].v[0] = __fmul_rn(float(__ldg(p.q + r * p.ldq + c)), s);
+                        }
+                    } else {
+                        y[i] = cols_load<W>(p.y + r * p.ldy + c);
+                    }
+                    d[i] = cols_load<W>(p.dh + r * p.lddh + c);
+                    iy[i] = __ldg(p.inv_y + r);
+                }
+                if constexpr (POST || GATE) {
+                    dx[i] = cols_load<W>(p.dx + r * p.lddx + c);
+                    f[i] = cols_load<W>(p.f + r * p.ldf + c);
+                    jf[i] = p.post ? __ldg(p.inv_f + r) : 0.0f;
                 }
             }
-            if constexpr (F) {
-                if (a.post || a.gate) {
-                    const V dx = ld(p.dx + r * p.lddx), f = ld(p.f + r * p.ldf);
-                    const float inv = p.post ? __ldg(p.inv_f + r) : 0.0f;
-                    if (a.post && p.gate) {
-                        if (gate_left == 0) {
-                            gate_row += p.ldgate;
-                            gate_left = p.gate_rows;
-                            gate = ld(gate_row);
-                        }
-                        --gate_left;
-                    }
 #pragma unroll
-                    for (int t = 0; t < W; ++t) {
-                        const float dt = __fmul_rn(dx.v[t], p.alpha);
-                        const float fh = p.post ? __fmul_rn(f.v[t], inv) : f.v[t];
-                        if (a.post) {
+            for (int i = 0; i < B; ++i) {
+                if (r0 + i >= rows) break;
+                const bool start = r0 + i == 0;
+                if (POST && p.gate) {
+                    if (gate_left == 0) {
+                        gate_row += p.ldgate;
+                        gate_left = p.gate_rows;
+                        gate = cols_load<W>(gate_row);
+                    }
+                    --gate_left;
+                }
+#pragma unroll
+                for (int t = 0; t < W; ++t) {
+                    if constexpr (PRE) {
+                        const float v = __fmul_rn(d[i].v[t], __fmul_rn(y[i].v[t], iy[i]));
+                        s_pre.v[t] = start ? v : __fadd_rn(s_pre.v[t], v);
+                    }
+                    if constexpr (POST || GATE) {
+                        const float dt = __fmul_rn(dx[i].v[t], p.alpha);
+                        const float fh = p.post ? __fmul_rn(f[i].v[t], jf[i]) : f[i].v[t];
+                        if constexpr (POST) {
                             const float v = __fmul_rn(p.gate ? __fmul_rn(dt, gate.v[t]) : dt, fh);
                             s_post.v[t] = start ? v : __fadd_rn(s_post.v[t], v);
                         }
-                        if (a.gate) {
+                        if constexpr (GATE) {
                             const float v = __fmul_rn(dt, p.post ? __fmul_rn(fh, post.v[t]) : fh);
                             s_gate.v[t] = start ? v : __fadd_rn(s_gate.v[t], v);
                         }
@@ -647,9 +698,9 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
                 }
             }
         }
-        if (a.pre) st(a.pre + run * p.n, s_pre);
-        if (F && a.post) st(a.post + run * p.n, s_post);
-        if (F && a.gate) st(a.gate + run * a.ldg, s_gate);
+        if constexpr (PRE) cols_store<W>(a.pre + run * p.n + c, s_pre);
+        if constexpr (POST) cols_store<W>(a.post + run * p.n + c, s_post);
+        if constexpr (GATE) cols_store<W>(a.gate + run * a.ldg + c, s_gate);
     }
 }
 
@@ -799,9 +850,19 @@ template <bool Q8, bool F>
 int launch_columns(const ColArgs &a, bool vec, cudaStream_t s) {
     const int64_t threads = vec ? a.e.n / 4 : a.e.n;
     const dim3 grid(unsigned(ceil_div(threads, 128)), unsigned(std::min<int64_t>(a.runs, 65535)));
-    if (vec) edge_columns_kernel<4, Q8, F><<<grid, 128, 0, s>>>(a);
-    else edge_columns_kernel<1, Q8, F><<<grid, 128, 0, s>>>(a);
-    return check_launch();
+    auto go = [&](auto kern4, auto kern1) {
+        if (vec) kern4<<<grid, 128, 0, s>>>(a);
+        else kern1<<<grid, 128, 0, s>>>(a);
+        return check_launch();
+    };
+#define REPOPS_COLUMNS(PRE, POST, GATE) \
+    go(edge_columns_kernel<4, Q8, PRE, POST, GATE>, edge_columns_kernel<1, Q8, PRE, POST, GATE>)
+    if constexpr (!F) return REPOPS_COLUMNS(true, false, false);
+    else if (a.pre && a.post) return a.gate ? REPOPS_COLUMNS(true, true, true) : REPOPS_COLUMNS(true, true, false);
+    else if (a.pre) return a.gate ? REPOPS_COLUMNS(true, false, true) : REPOPS_COLUMNS(true, false, false);
+    else if (a.post) return a.gate ? REPOPS_COLUMNS(false, true, true) : REPOPS_COLUMNS(false, true, false);
+    else return REPOPS_COLUMNS(false, false, true);
+#undef REPOPS_COLUMNS
 }
 
 // The row kernel, the column terms and their folds.  dpre, dpost: n floats;
@@ -918,7 +979,7 @@ extern "C" int repops_rmsnorm_residual_f32(int64_t rows, int64_t cols, const flo
     const EdgeArgs a{rows, cols, x, f, ldx, ldf, post_gain, gate, pre_gain, ldgate, gate ? gate_rows : 1, alpha, eps,
                      y, h, ldy, ldh};
     if (cols > MAX_STAGED_COLS) return launch_long(edge_forward_long_kernel, a, rows, cols, stream);
-    const bool vec = vec_row(x, ldx) && vec_row(f, ldf) && vec_row(y, ldy) && (!h || vec_row(h, ldh)) &&
+    const bool vec = cols % 4 == 0 && vec_row(x, ldx) && vec_row(f, ldf) && vec_row(y, ldy) && (!h || vec_row(h, ldh)) &&
                      vec_row(post_gain, 0) && vec_row(pre_gain, 0) && (!gate || vec_row(gate, ldgate));
     return vec ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
