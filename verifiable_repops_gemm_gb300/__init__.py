@@ -344,9 +344,14 @@ def sort_ids(ids) -> list:
     return [int(order[i]) for i in range(n)]
 
 
+_STORAGE_TYPES = {}
+
+
 def _storage_type(dtype):
     import torch
-    t = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}.get(dtype)
+    if not _STORAGE_TYPES:
+        _STORAGE_TYPES.update({torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16})
+    t = _STORAGE_TYPES.get(dtype)
     if t is None:
         raise TypeError("storage type must be float32, float16 or bfloat16, not %s" % dtype)
     return t
@@ -625,9 +630,14 @@ def replay(grads_per_step, orders, etas, theta, leaf: int = 4096, *, roots=None,
 
 def _row_operand(x, name):
     import torch
-    if x.dtype != torch.float32 or x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+    shape = x.shape
+    if x.dtype != torch.float32 or len(shape) != 2 or not x.is_cuda:
         raise ValueError("%s must be a 2-D float32 CUDA tensor with unit column stride" % name)
-    return x.data_ptr(), max(x.stride(0), x.shape[1], 1)
+    ld, unit = x.stride()
+    cols = shape[1]
+    if cols > 1 and unit != 1:
+        raise ValueError("%s must be a 2-D float32 CUDA tensor with unit column stride" % name)
+    return x.data_ptr(), ld if ld >= cols and ld > 0 else max(cols, 1)
 
 
 def _row_out(x, out):
@@ -946,14 +956,14 @@ def rope(x, heads: int, cos, sin, *, first: int = 0, period: int = None, inverse
     return x
 
 
-def _on_device(**tensors):
+def _on_device(*tensors):
     """Every given tensor (None skipped) must live on the current CUDA device,
     where the call's kernels run."""
     import torch
     here = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.get_device() != here:      # -1 for a CPU tensor
-            raise ValueError("%s must be a tensor on the current CUDA device" % name)
+            raise ValueError("every tensor must be on the current CUDA device (%d)" % here)
 
 
 def _groups(cols, group):
@@ -967,12 +977,14 @@ def _rows_i8(q, scale, group, name):
     (rows, cols) and scale float32 (rows, groups), unit column strides (a
     column block of wider rows is fine where it starts on a group)."""
     import torch
-    if q.dtype != torch.int8 or q.dim() != 2 or (q.shape[1] > 1 and q.stride(1) != 1):
+    shape = q.shape
+    if q.dtype != torch.int8 or len(shape) != 2 or (shape[1] > 1 and q.stride(1) != 1):
         raise ValueError("%s must be a 2-D int8 CUDA tensor with unit column stride" % name)
-    n = _groups(q.shape[1], group)
-    if scale.dtype != torch.float32 or tuple(scale.shape) != (q.shape[0], n) or (n > 1 and scale.stride(1) != 1):
+    rows, cols = shape
+    n = _groups(cols, group)
+    if scale.dtype != torch.float32 or scale.shape != (rows, n) or (n > 1 and scale.stride(1) != 1):
         raise ValueError("the scales of %s must be float32 of shape (rows, %d) with unit column stride" % (name, n))
-    return q.data_ptr(), max(q.stride(0), q.shape[1], 1), scale.data_ptr(), max(scale.stride(0), n, 1)
+    return q.data_ptr(), max(q.stride(0), cols, 1), scale.data_ptr(), max(scale.stride(0), n, 1)
 
 
 def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
@@ -990,7 +1002,7 @@ def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
         out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty((rows, n), dtype=torch.float32, device=x.device)
-    _on_device(x=x, out=out, scale=scale)
+    _on_device(x, out, scale)
     if tuple(out.shape) != (rows, cols):
         raise ValueError("out must have the shape of x")
     pq, ldq, ps, lds = _rows_i8(out, scale, group, "out")
@@ -1010,7 +1022,7 @@ def dequantize_rows(q, scale, *, group: int = 0, dtype=None, out=None, stream=No
     if tuple(out.shape) != tuple(q.shape) or (dtype is not None and out.dtype != dtype) or \
             (out.shape[1] > 1 and out.stride(1) != 1):
         raise ValueError("out must have the shape of q, the dtype asked for and unit column stride")
-    _on_device(q=q, scale=scale, out=out)
+    _on_device(q, scale, out)
     rc = load().repops_dequantize_rows_i8(q.shape[0], q.shape[1], pq, ldq, ps, lds, group, out.data_ptr(),
                                           _storage_type(out.dtype), max(out.stride(0), q.shape[1], 1),
                                           _stream_handle(stream))
@@ -1042,24 +1054,24 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
     K2, N = B.shape
     if K != K2:
         raise ValueError("inner dimensions differ: %d vs %d" % (K, K2))
-    if (K > 1 and (A.stride(1) != 1 or B.stride(0) != 1)) or (M > 1 and A.stride(0) < K) or \
-            (N > 1 and B.stride(1) < K):
+    (lda, ua), (ub, ldb) = A.stride(), B.stride()
+    if (K > 1 and (ua != 1 or ub != 1)) or (M > 1 and lda < K) or (N > 1 and ldb < K):
         raise ValueError("k must be contiguous: A with unit column stride, B a transposed view W.t() of (N, K) weights")
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
-    if out.dim() != 2 or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1) or \
-            (out_dtype is not None and out.dtype != out_dtype):
+    elif out.shape != (M, N) or (N > 1 and out.stride(1) != 1) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be (M, N) with unit column stride and the dtype asked for")
-    _on_device(A=A, B=B, a_scale=a_scale, b_scale=b_scale, bias=bias, out=out)
-    pa, pb = _scale_vector(a_scale, M, "a_scale"), _scale_vector(b_scale, N, "b_scale")
-    pbias = None if bias is None else _scale_vector(bias, N, "bias")
+    _on_device(A, B, a_scale, b_scale, bias, out)
     L = load()
     need = L.repops_gemm_i8_workspace_bytes(config, M, N, K)
     ws = _workspace(need, A.device, stream) if need else None
-    rc = L.repops_gemm_i8(config, M, N, K, A.data_ptr(), max(A.stride(0), K), pa, B.data_ptr(), max(B.stride(1), K), pb,
-                          pbias, out.data_ptr(), _storage_type(out.dtype), max(out.stride(0), N, 1),
-                          ws.data_ptr() if ws is not None else None, need, _stream_handle(stream))
-    _capi.check(rc, "repops_gemm_i8")
+    rc = L.repops_gemm_i8(config, M, N, K, A.data_ptr(), max(lda, K), _scale_vector(a_scale, M, "a_scale"), B.data_ptr(),
+                          max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
+                          None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
+                          _storage_type(out.dtype), max(out.stride(0), N, 1), ws.data_ptr() if ws is not None else None,
+                          need, _stream_handle(stream))
+    if rc:
+        _capi.check(rc, "repops_gemm_i8")
     return out
 
 
@@ -1076,7 +1088,7 @@ def _row_like(t, shape, name):
     """(pointer, pitch) of an optional float32 operand of `shape`."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
     return _row_operand(t, name)
 
@@ -1105,7 +1117,7 @@ def swiglu_backward_i8(g, g_scale, u, u_scale, dh, dg=None, du=None, *, group: i
     pdg, lddg = _row_like(dg, g.shape, "dg")
     pdu, lddu = _row_like(du, g.shape, "du")
     ph, ldh = _row_like(h, g.shape, "h")
-    _on_device(g=g, g_scale=g_scale, u=u, u_scale=u_scale, dh=dh, dg=dg, du=du, h=h)
+    _on_device(g, g_scale, u, u_scale, dh, dg, du, h)
     rc = load().repops_swiglu_backward_i8(g.shape[0], g.shape[1], pg, ldg, pgs, ldgs, pu, ldu, pus, ldus, group, pd, ldd,
                                           pdg, lddg, pdu, lddu, ph, ldh, _stream_handle(stream))
     _capi.check(rc, "repops_swiglu_backward_i8")
@@ -1126,7 +1138,7 @@ def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, gro
     dgamma = torch.empty(cols, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
     pdx, lddx = _row_like(dx, x.shape, "dx")
     ph, ldh = _row_like(h, x.shape, "h")
-    _on_device(x=x, x_scale=x_scale, gamma=gamma, dy=dy, res=res, dx=dx, h=h, dgamma=dgamma)
+    _on_device(x, x_scale, gamma, dy, res, dx, h, dgamma)
     if rows == 0 or cols == 0:
         return dx, dgamma.zero_()
     L = load()
@@ -1175,7 +1187,7 @@ def rmsnorm_residual(x, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=
         h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     py, ldy = _row_like(y, x.shape, "y")
     ph, ldh = _row_like(h, x.shape, "h")
-    _on_device(x=x, f=f, pre_gain=pre_gain, post_gain=post_gain, gate=gate, y=y, h=h)
+    _on_device(x, f, pre_gain, post_gain, gate, y, h)
     rc = load().repops_rmsnorm_residual_f32(rows, cols, px, ldx, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg,
                                             per, ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"),
                                             ctypes.c_float(eps), py, ldy, ph, ldh, _stream_handle(stream))
@@ -1222,8 +1234,7 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
     pdx, lddx = _row_like(dx, f.shape, "dx")
     pdf, lddf = _row_like(df, f.shape, "df")
     pdg, lddg, _, _ = _gate_rows(dgate, rows, cols)
-    _on_device(dy=dy, dh=dh, y=y, f=f, pre_gain=pre_gain, post_gain=post_gain, gate=gate, dx=dx, df=df, dpre=dpre,
-               dpost=dpost, dgate=dgate)
+    _on_device(dy, dh, y, f, pre_gain, post_gain, gate, dx, df, dpre, dpost, dgate)
     if rows == 0 or cols == 0:
         for t in (dpre, dpost, dgate):
             if t is not None:

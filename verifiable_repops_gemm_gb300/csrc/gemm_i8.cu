@@ -15,16 +15,19 @@
 // loads: which k a lane holds does not matter as long as both operands agree,
 // so lane q of a quad loads k = 16q .. 16q + 15 of a 64-k step and feeds words
 // 0, 1 to one instruction and 2, 3 to the next.  The warps of a CTA split k and
-// add their sums in shared memory.
+// add their sums in shared memory.  The instruction's rate here is 130 TOPS
+// (measured), enough for 8 tokens at the memory's rate; widening to binary16
+// in registers for the faster-looking m16n8k16.f16 took 31 us where this takes
+// 13 (16384 channels, 2048 k, 13 tokens).
 //
 // Many rows: the operands are widened once to binary16 (exact: 8 bits fit its
-// 11) and multiplied by tcgen05 with binary32 accumulators in tensor memory,
-// because this chip's integer tensor rate is a small part of its binary16 rate.
-// Every product and every partial sum of up to 512 of them is a whole number
-// below 2^23 in magnitude, so binary32 accumulation is exact whatever its
-// order; after each 512 of k the accumulators are added to 32-bit integers in
+// 11) in scratch and multiplied by tcgen05 with binary32 accumulators in tensor
+// memory.  Every product and every partial sum of up to 512 of them is a whole
+// number of at most 2^23, so binary32 accumulation is exact whatever its order;
+// after each 512 of k the accumulators are added to 32-bit integers in
 // registers while the tensor core fills the other half of tensor memory.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -105,6 +108,14 @@ __device__ __forceinline__ float scale_bias(float v, float sb, const float *bias
 
 // ---------------------------------------------------------------- few rows ----
 
+// Whole numbers as binary16: with the sign bit flipped a byte is q + 128, the
+// low mantissa bits of 1024 + (q + 128); subtracting 1152 is exact.
+__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t selector) {
+    const uint32_t h = __byte_perm(w, 0x64646464u, selector);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -113,57 +124,98 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 * MT channels x 8 * NT tokens a CTA of 8 warps; warp w takes the 64-k
-// steps w, w + 8, ...
-template <int TY, int MT, int NT, bool VEC>
+// One or two (NT) tokens: a warp takes R channels, its lanes 512 consecutive bytes
+// of each at once, and multiplies by dp4a: the tensor instruction's rate would
+// be spent on columns that are not there (at 8192 x 8192 its eight take 8 of the
+// 10 us that reading B takes).
+template <int TY, int R, int NT, bool VEC>
+__global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t j0 = (blockIdx.x * int64_t(8) + (threadIdx.x >> 5)) * R;
+    if (j0 >= p.N) return;
+    int acc[R][NT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) acc[r][m] = 0;
+    const int K = int(p.K);
+#pragma unroll 8 / R
+    for (int k = 16 * lane; k < K; k += 512) {
+        uint4 w[R], x[NT];
+        // a channel or token past the end repeats the last one, and is not stored
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = load_k16<VEC>(p.B + min(j0 + r, p.N - 1) * p.ldb, k, K, p.B, p.b_end);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) x[m] = load_k16<VEC>(p.A + min(int64_t(m), p.M - 1) * p.lda, k, K, p.A, p.a_end);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                acc[r][m] = __dp4a(int(w[r].x), int(x[m].x), acc[r][m]);
+                acc[r][m] = __dp4a(int(w[r].y), int(x[m].y), acc[r][m]);
+                acc[r][m] = __dp4a(int(w[r].z), int(x[m].z), acc[r][m]);
+                acc[r][m] = __dp4a(int(w[r].w), int(x[m].w), acc[r][m]);
+            }
+    }
+    int mine = 0;                      // lane r * NT + m keeps channel r, token m
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+            const int v = __reduce_add_sync(0xffffffffu, acc[r][m]);
+            if (lane == r * NT + m) mine = v;
+        }
+    const int64_t j = j0 + lane / NT, m = lane % NT;
+    if (lane < R * NT && j < p.N && m < p.M) {
+        const float v = __fmul_rn(__int2float_rn(mine), __ldg(p.sa + m));
+        store_c<TY>(p.C, m * p.ldc + j, scale_bias(v, __ldg(p.sb + j), p.bias, j));
+    }
+}
+
+// 16 channels x 8 * NT tokens a CTA of 8 warps; warp w takes the 64-k steps w,
+// w + 8, ...  (Two tiles of channels a warp were slower at every size but one.)
+template <int TY, int NT, bool VEC>
 __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
-    constexpr int CH = 16 * MT, TK = 8 * NT;
-    __shared__ int sum[TK][CH + 1];
+    constexpr int CH = 16, TK = 8 * NT, PITCH = CH + 4;         // 2 * PITCH = 8 (mod 32): the adds hit 32 banks
+    constexpr int UNROLL = NT <= 2 ? 4 : 2;
+    __shared__ int sum[TK][PITCH];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int64_t n0 = int64_t(blockIdx.x) * CH, m0 = int64_t(blockIdx.y) * TK;
-    for (int i = threadIdx.x; i < TK * (CH + 1); i += 256) (&sum[0][0])[i] = 0;
-    int d[MT][NT][4];
+    for (int i = threadIdx.x; i < TK * PITCH; i += 256) (&sum[0][0])[i] = 0;
+    int d[NT][4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[t][u][i] = 0;
+        for (int i = 0; i < 4; ++i) d[u][i] = 0;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const int64_t steps = (p.K + 63) / 64;
-#pragma unroll 2
-    for (int64_t s = warp; s < steps; s += 8) {
-        const int64_t k = s * 64 + 16 * q;
-        uint4 w[MT][2], x[NT];
+    const int steps = int((p.K + 63) / 64);
+#pragma unroll UNROLL
+    for (int s = warp; s < steps; s += 8) {
+        const int64_t k = int64_t(s) * 64 + 16 * q;
+        uint4 w[2], x[NT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t j = n0 + 16 * t + 8 * h + g;
-                w[t][h] = j < p.N && k < p.K ? load_k16<VEC>(p.B + j * p.ldb, k, p.K, p.B, p.b_end) : zero;
-            }
+        for (int h = 0; h < 2; ++h) {
+            const int64_t j = n0 + 8 * h + g;
+            w[h] = j < p.N && k < p.K ? load_k16<VEC>(p.B + j * p.ldb, k, p.K, p.B, p.b_end) : zero;
+        }
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const int64_t i = m0 + 8 * u + g;
             x[u] = i < p.M && k < p.K ? load_k16<VEC>(p.A + i * p.lda, k, p.K, p.A, p.a_end) : zero;
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                mma_s8(d[t][u], w[t][0].x, w[t][1].x, w[t][0].y, w[t][1].y, x[u].x, x[u].y);
-                mma_s8(d[t][u], w[t][0].z, w[t][1].z, w[t][0].w, w[t][1].w, x[u].z, x[u].w);
-            }
+        for (int u = 0; u < NT; ++u) {
+            mma_s8(d[u], w[0].x, w[1].x, w[0].y, w[1].y, x[u].x, x[u].y);
+            mma_s8(d[u], w[0].z, w[1].z, w[0].w, w[1].w, x[u].z, x[u].w);
+        }
     }
     __syncthreads();
     // lane: channels g and g + 8, tokens 2q and 2q + 1 of each tile
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                atomicAdd(&sum[8 * u + 2 * q + (i & 1)][16 * t + 8 * (i >> 1) + g], d[t][u][i]);
+        for (int i = 0; i < 4; ++i)
+            atomicAdd(&sum[8 * u + 2 * q + (i & 1)][8 * (i >> 1) + g], d[u][i]);
     __syncthreads();
     for (int i = threadIdx.x; i < TK * CH; i += 256) {
         const int64_t m = m0 + i / CH, n = n0 + i % CH;
@@ -177,14 +229,6 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
 
 constexpr int BM = 128, BK = 64;          // BK binary16 = one 128-byte swizzled row
 constexpr int kChunkSteps = 8;            // k-steps between two drains: 512 of k
-
-// Whole numbers as binary16: with the sign bit flipped a byte is q + 128, the
-// low mantissa bits of 1024 + (q + 128); subtracting 1152 is exact.
-__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t selector) {
-    const uint32_t h = __byte_perm(w, 0x64646464u, selector);
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&h), __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
 
 // The rows of A, then those of B, as binary16 rows of Kp (a multiple of 64)
 // values, zeros past K: 16 values a thread.
@@ -207,7 +251,7 @@ template <int BN>
 struct TileCfg {
     static constexpr int STAGE_BYTES = (BM + BN) * BK * 2;
     static constexpr int STAGES = 196608 / STAGE_BYTES;          // 4, 6 or 8
-    static constexpr int WARP_STAGE = 32 * 32 * 4;               // an epilogue warp's 32 x 32 block
+    static constexpr int WARP_STAGE = 32 * 128;                  // an epilogue warp's block: 32 rows of 128 bytes
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * WARP_STAGE;
     static constexpr uint32_t TMEM_COLS = 2 * BN;
     static constexpr int COLS = BN / 2;                          // an epilogue warp's columns
@@ -225,16 +269,91 @@ struct TileMap {
     }
 };
 
+// Scales (or biases) of columns col .. col + 7: one value for the whole warp
+// each, a column past the end repeating the last one.
+__device__ __forceinline__ void column_values(const float *v, int64_t col, int64_t n, bool vec, float (&out)[8]) {
+    if (vec && col + 8 <= n) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(v + col)), b = __ldg(reinterpret_cast<const float4 *>(v + col) + 1);
+        out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
+        out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = __ldg(v + min(col + i, n - 1));
+    }
+}
+
+// C's tile: sums x scales, through the warp's block of shared memory.  c_tma:
+// C can be stored by TMA (a block of 32 rows x 128 bytes at a time, clipped at
+// C's edges); else lanes store single values.  s_vec: scales and bias are on
+// 16-byte boundaries.
+template <int TY, int COLS>
+__device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *map_c, const int (&acc)[COLS], float sa,
+                                           int64_t row0, int64_t col0, uint8_t *block, bool c_tma, bool s_vec) {
+    constexpr int W = TY == REPOPS_TYPE_F32 ? 32 : COLS < 64 ? COLS : 64;    // columns of a block
+    const int lane = threadIdx.x & 31;
+    uint4 *chunk = reinterpret_cast<uint4 *>(block);           // 16-byte chunk c of row r in slot c ^ (r & 7)
+#pragma unroll
+    for (int j = 0; j < COLS; j += W) {
+        if (col0 + j >= p.N) break;
+        if (c_tma && lane == 0) tma_store_wait_read();         // the block's previous contents have left
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < W; c += 8) {
+            float v[8], sb[8];
+            column_values(p.sb, col0 + j + c, p.N, s_vec, sb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j + c + i]), sa), sb[i]);
+            if (p.bias) {
+                column_values(p.bias, col0 + j + c, p.N, s_vec, sb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], sb[i]);
+            }
+            if constexpr (TY == REPOPS_TYPE_F32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    chunk[lane * 8 + ((c / 4 + h) ^ (lane & 7))] =
+                        make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                                   __float_as_uint(v[4 * h + 3]));
+            } else {
+                chunk[lane * 8 + ((c / 8) ^ (lane & 7))] = make_uint4(pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]),
+                                                                      pack_c<TY>(v[4], v[5]), pack_c<TY>(v[6], v[7]));
+            }
+        }
+        if (c_tma) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && row0 < p.M) tma_store_2d(map_c, block, int32_t(col0 + j), int32_t(row0));
+        } else {
+            __syncwarp();
+            using E = typename std::conditional<TY == REPOPS_TYPE_F32, float, uint16_t>::type;
+            constexpr int PER = 16 / int(sizeof(E));           // values of a chunk
+            const E *e = reinterpret_cast<const E *>(block);
+#pragma unroll 1
+            for (int r = 0; r < 32 && row0 + r < p.M; ++r)
+#pragma unroll
+                for (int c = lane; c < W; c += 32)
+                    if (col0 + j + c < p.N)
+                        static_cast<E *>(p.C)[(row0 + r) * p.ldc + col0 + j + c] =
+                            e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
+            __syncwarp();
+        }
+    }
+}
+
 template <int TY, int BN>
 __global__ void __launch_bounds__(kTileThreads, 1)
-gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, I8Args p,
-                    TileMap tm, int ksteps, int c_vec, unsigned *status) {
+gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma, int s_vec,
+                    unsigned *status) {
     using T = TileCfg<BN>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // from a shuffle the compiler knows that a warp's role is uniform: a product
+    // then takes its 64 (128 columns) or 128 cycles instead of the 111 that
+    // issuing it from a branch it must assume divergent costs
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int tiles = tm.tiles_m * tm.tiles_n;
     const int chunks = (ksteps + kChunkSteps - 1) / kChunkSteps;
     if (threadIdx.x == 0) {
@@ -259,17 +378,17 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     // status word, waits (again with a limit) for its own copies or products in
     // flight and leaves; the others run into their own limits.
     if (warp == 8) {
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tensormap(&map_a);
             prefetch_tensormap(&map_b);
-            int issued = 0;
+            int issued = 0, s = 0;
+            uint32_t phase = 1;                                // the wait before the ring's first use passes
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 int m, n;
                 tm.at(t, m, n);
                 for (int k = 0; k < ksteps; ++k, ++issued) {
-                    const int s = issued % T::STAGES;
-                    if (issued >= T::STAGES && !mbar_wait_bounded(&empty[s], uint32_t(issued / T::STAGES - 1) & 1u)) {
+                    if (!mbar_wait_bounded(&empty[s], phase)) {
                         ok = false;
                         break;
                     }
@@ -277,6 +396,10 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                     mbar_arrive_expect_tx(&full[s], T::STAGE_BYTES);
                     tma_load_2d(st, &map_a, &full[s], k * BK, m * BM);
                     tma_load_2d(st + BM * BK * 2, &map_b, &full[s], k * BK, n * BN);
+                    if (++s == T::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             if (!ok) {
@@ -286,34 +409,40 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = idesc_f16(BM, BN);
-            int used = 0, filled = 0;
+            const uint32_t base = smem_addr(stages);
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 1;
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                for (int c = 0; c < chunks && ok; ++c, ++filled) {
-                    const int b = filled & 1;
-                    if (filled >= 2 && !mbar_wait_bounded(&acc_empty[b], uint32_t(filled / 2 - 1) & 1u)) {
+                for (int c = 0; c < chunks && ok; ++c) {
+                    if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int k1 = min(ksteps, (c + 1) * kChunkSteps);
-                    for (int k = c * kChunkSteps; k < k1; ++k, ++used) {
-                        const int s = used % T::STAGES;
-                        if (!mbar_wait_bounded(&full[s], uint32_t(used / T::STAGES) & 1u)) {
+                    const int steps = min(kChunkSteps, ksteps - c * kChunkSteps);
+                    for (int k = 0; k < steps; ++k) {
+                        if (!mbar_wait_bounded(&full[s], phase)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t st = smem_addr(stages + s * T::STAGE_BYTES);
+                        const uint32_t st = base + s * T::STAGE_BYTES;
                         const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + BM * BK * 2);
 #pragma unroll
                         for (int j = 0; j < BK / 16; ++j)      // 32 bytes of k a step within the swizzled row
-                            tc_mma_f16(tmem + b * BN, da + 2 * j, db + 2 * j, idesc, k > c * kChunkSteps || j > 0);
+                            tc_mma_f16(tmem + b * BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
                         tc_commit(&empty[s]);
+                        if (++s == T::STAGES) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
                     if (ok) tc_commit(&acc_full[b]);
+                    b ^= 1;
+                    if (b == 0) acc_phase ^= 1u;
                 }
             }
             if (!ok) {
@@ -325,96 +454,42 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     } else {
         const int half = warp >> 2;                            // columns half * COLS .. of the tile
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-        float4 *block = reinterpret_cast<float4 *>(stages + T::STAGES * T::STAGE_BYTES + warp * T::WARP_STAGE);
-        int drains = 0;
+        uint8_t *block = stages + T::STAGES * T::STAGE_BYTES + warp * T::WARP_STAGE;
+        int b = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
             int tile_m, tile_n;
             tm.at(t, tile_m, tile_n);
             const int64_t row0 = int64_t(tile_m) * BM + 32 * (warp & 3), col0 = int64_t(tile_n) * BN + half * T::COLS;
-            const float sa = row0 + lane < p.M ? __ldg(p.sa + row0 + lane) : 0.0f;
+            const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
             int acc[T::COLS];
 #pragma unroll
             for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
-            for (int c = 0; c < chunks; ++c, ++drains) {
-                const int b = drains & 1;
-                if (!mbar_wait_bounded(&acc_full[b], uint32_t(drains / 2) & 1u)) {
-                    ok = false;
-                    break;
-                }
+            for (int c = 0; c < chunks; ++c) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], phase));
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < T::COLS / 32; ++j) {
-                    uint32_t v[32];
-                    tmem_load32(tmem + lanes + b * BN + half * T::COLS + 32 * j, v);
+                for (int j = 0; j < T::COLS; j += 16) {
+                    uint32_t v[16];
+                    tmem_load16(tmem + lanes + b * BN + half * T::COLS + j, v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[32 * j + i] += __float2int_rn(__uint_as_float(v[i]));
+                    for (int i = 0; i < 16; ++i) acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[b]);
+                b ^= 1;
+                if (b == 0) phase ^= 1u;
             }
             if (!ok) {
                 if (lane == 0) atomicOr(status, 1u);
                 break;
             }
-            // 32 columns at a time through the warp's block (16-byte chunk c of
-            // row r in slot c ^ (r & 7)): a lane writes its row, then eight
-            // lanes read a row's 128 bytes, so the stores are whole lines
-#pragma unroll
-            for (int j = 0; j < T::COLS / 32; ++j) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int *a = acc + 32 * j + 4 * c;
-                    block[lane * 8 + (c ^ (lane & 7))] =
-                        make_float4(__fmul_rn(__int2float_rn(a[0]), sa), __fmul_rn(__int2float_rn(a[1]), sa),
-                                    __fmul_rn(__int2float_rn(a[2]), sa), __fmul_rn(__int2float_rn(a[3]), sa));
-                }
-                __syncwarp();
-                constexpr int W = TY == REPOPS_TYPE_F32 ? 4 : 8;      // columns a lane stores at once
-                constexpr int PER_ROW = 32 / W, ROWS = 32 / PER_ROW;
-                const int cl = (lane % PER_ROW) * W;
-                const int64_t col = col0 + 32 * j + cl;
-                float sb[W], bi[W];
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    sb[i] = col + i < p.N ? __ldg(p.sb + col + i) : 0.0f;
-                    bi[i] = p.bias && col + i < p.N ? __ldg(p.bias + col + i) : 0.0f;
-                }
-#pragma unroll
-                for (int r0 = 0; r0 < 32; r0 += ROWS) {
-                    const int r = r0 + lane / PER_ROW;
-                    float v[W];
-#pragma unroll
-                    for (int i = 0; i < W / 4; ++i) {
-                        const float4 f = block[r * 8 + ((cl / 4 + i) ^ (r & 7))];
-                        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        v[i] = __fmul_rn(v[i], sb[i]);
-                        if (p.bias) v[i] = __fadd_rn(v[i], bi[i]);
-                    }
-                    const int64_t row = row0 + r;
-                    if (row >= p.M) continue;
-                    const int64_t at = row * p.ldc + col;
-                    if (c_vec && col + W <= p.N) {
-                        if constexpr (TY == REPOPS_TYPE_F32) {
-                            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + at) = make_float4(v[0], v[1], v[2], v[3]);
-                        } else {
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.C) + at) =
-                                make_uint4(pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]), pack_c<TY>(v[4], v[5]),
-                                           pack_c<TY>(v[6], v[7]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < W; ++i)
-                            if (col + i < p.N) store_c<TY>(p.C, at + i, v[i]);
-                    }
-                }
-                __syncwarp();
-            }
+            store_tile<TY, T::COLS>(p, &map_c, acc, sa, row0, col0, block, c_tma != 0, s_vec != 0);
         }
+        if (c_tma && lane == 0) tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -445,29 +520,52 @@ int auto_config(int64_t M, int64_t N, int64_t K) {
 
 bool operand_vec(const int8_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
 
-template <int TY, int MT, int NT>
+template <int TY, int R, int NT>
+int launch_dot(const I8Args &a, cudaStream_t s) {
+    const unsigned grid = unsigned(ceil_div(a.N, 8 * R));
+    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) gemm_i8_dot_kernel<TY, R, NT, true><<<grid, 256, 0, s>>>(a);
+    else gemm_i8_dot_kernel<TY, R, NT, false><<<grid, 256, 0, s>>>(a);
+    return check_launch();
+}
+
+template <int TY, int R>
+int launch_dot_r(const I8Args &a, cudaStream_t s) {
+    return a.M == 1 ? launch_dot<TY, R, 1>(a, s) : launch_dot<TY, R, 2>(a, s);
+}
+
+template <int TY, int NT>
 int launch_rows_nt(const I8Args &a, cudaStream_t s) {
-    const dim3 grid(unsigned(ceil_div(a.N, 16 * MT)), unsigned(ceil_div(a.M, 8 * NT)));
-    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) gemm_i8_rows_kernel<TY, MT, NT, true><<<grid, 256, 0, s>>>(a);
-    else gemm_i8_rows_kernel<TY, MT, NT, false><<<grid, 256, 0, s>>>(a);
+    const dim3 grid(unsigned(ceil_div(a.N, 16)), unsigned(ceil_div(a.M, 8 * NT)));
+    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) gemm_i8_rows_kernel<TY, NT, true><<<grid, 256, 0, s>>>(a);
+    else gemm_i8_rows_kernel<TY, NT, false><<<grid, 256, 0, s>>>(a);
     return check_launch();
 }
 
 template <int TY>
 int launch_rows(const I8Args &a, cudaStream_t s) {
-    if (a.M <= 8) return launch_rows_nt<TY, 1, 1>(a, s);
-    if (a.M <= 16) return launch_rows_nt<TY, 1, 2>(a, s);
-    if (a.M <= 32) return launch_rows_nt<TY, 1, 4>(a, s);
-    return launch_rows_nt<TY, 1, 8>(a, s);
+    if (a.M <= 2) {
+        // channels a warp: as many as leave 16 warps an SM
+        const int64_t warps = int64_t(sm_count()) * 16;
+        if (a.N >= 4 * warps) return launch_dot_r<TY, 4>(a, s);
+        if (a.N >= 2 * warps) return launch_dot_r<TY, 2>(a, s);
+        return launch_dot_r<TY, 1>(a, s);
+    }
+    if (a.M <= 8) return launch_rows_nt<TY, 1>(a, s);
+    if (a.M <= 16) return launch_rows_nt<TY, 2>(a, s);
+    if (a.M <= 32) return launch_rows_nt<TY, 4>(a, s);
+    return launch_rows_nt<TY, 8>(a, s);
 }
 
-bool make_map(CUtensorMap *map, const __half *base, int64_t Kp, int64_t rows, int box_rows) {
+// A 2-D map of `rows` rows of `inner` values at pitch `ld`, a box of box_rows
+// rows of 128 bytes under the 128-byte swizzle.
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, unsigned size, const void *base, int64_t inner, int64_t rows,
+              int64_t ld, int box_inner, int box_rows) {
     gemm::EncodeTiledFn enc = gemm::tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(Kp), cuuint64_t(rows)}, strides[1] = {cuuint64_t(Kp) * 2u};
-    const cuuint32_t box[2] = {cuuint32_t(BK), cuuint32_t(box_rows)}, estr[2] = {1u, 1u};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld) * size};
+    const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_rows)}, estr[2] = {1u, 1u};
+    return enc(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -481,8 +579,20 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
     int rc = check_launch();
     if (rc != REPOPS_OK) return rc;
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, ws, Kp, a.M, BM) || !make_map(&mb, ws + a.M * Kp, Kp, a.N, BN)) return REPOPS_ERR_UNSUPPORTED;
+    constexpr CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap ma, mb, mc;
+    if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, BN))
+        return REPOPS_ERR_UNSUPPORTED;
+    // C by TMA where its rows start on 16 bytes and a block's rows fill 128 bytes
+    constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
+    constexpr CUtensorMapDataType ctype = TY == REPOPS_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                          : TY == REPOPS_TYPE_F16 ? F16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr int wide = 128 / int(csize);                             // columns of a stored block
+    const int c_tma = wide <= T::COLS && reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && uint64_t(a.ldc) * csize % 16 == 0 &&
+                      a.ldc < (int64_t(1) << 37) && make_map(&mc, ctype, csize, a.C, a.N, a.M, a.ldc, wide, 32);
+    if (!c_tma) mc = ma;
+    const int s_vec = reinterpret_cast<uintptr_t>(a.sb) % 16 == 0 && (!a.bias || reinterpret_cast<uintptr_t>(a.bias) % 16 == 0);
     unsigned *status = nullptr;
     if ((rc = status_word_address(&status)) != REPOPS_OK) return rc;
     auto kern = gemm_i8_tile_kernel<TY, BN>;
@@ -490,10 +600,8 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     if (e != cudaSuccess) return set_cuda_error(e);
     const TileMap tm{int(ceil_div(a.M, BM)), int(ceil_div(a.N, BN)), 16};
     const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
-    const unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
-    const int c_vec = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && uint64_t(a.ldc) * csize % 16 == 0;
-    kern<<<unsigned(std::min<int64_t>(tiles, sm_count())), kTileThreads, T::SMEM, s>>>(ma, mb, a, tm, int(Kp / BK),
-                                                                                      c_vec, status);
+    kern<<<unsigned(std::min<int64_t>(tiles, sm_count())), kTileThreads, T::SMEM, s>>>(ma, mb, mc, a, tm, int(Kp / BK),
+                                                                                      c_tma, s_vec, status);
     return check_launch();
 }
 

@@ -71,149 +71,153 @@ __device__ __forceinline__ void store_four(void *p, int64_t i, float4 v) {
     }
 }
 
-// The larger magnitude, a NaN winning over everything: magnitudes are compared
-// as their bit patterns, which order non-negative values, infinity and NaN.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t mag4(uint32_t m, float4 v) {
-    return max(max(max(mag(v.x), mag(v.y)), max(mag(v.z), mag(v.w))), m);
+// The larger magnitude, a NaN winning over everything.
+__device__ __forceinline__ float max_mag(float m, float v) {
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v)));
+    return m;
+}
+__device__ __forceinline__ float max_mag4(float m, float4 v) {
+    return max_mag(max_mag(max_mag(max_mag(m, v.x), v.y), v.z), v.w);
 }
 
 struct GroupScale {
     float scale, inv;
+    uint32_t keep;      // all bits, or none for a group with an infinity or a NaN
 };
 
-__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits) {
-    if (amax_bits >= 0x7f800000u) return {__uint_as_float(0x7fffffffu), 0.0f};
-    const float a = fmaxf(__uint_as_float(amax_bits), kScaleFloor);
-    return {__fdiv_rn(a, 127.0f), __fdiv_rn(127.0f, a)};
+__device__ __forceinline__ GroupScale group_scale(float amax) {
+    if (!(amax <= 3.402823466e38f)) return {__uint_as_float(0x7fffffffu), 0.0f, 0u};
+    const float a = fmaxf(amax, kScaleFloor);
+    return {__fdiv_rn(a, 127.0f), __fdiv_rn(127.0f, a), 0xffffffffu};
 }
 
-// A non-finite group has inv 0: its q is 0 for the finite values, and for the
-// others (inf * 0 = NaN) the conversion of NaN, which is 0 as well.
-__device__ __forceinline__ int quant1(float x, float inv) { return __float2int_rn(__fmul_rn(x, inv)); }
-
-__device__ __forceinline__ uint32_t quant4(float4 v, float inv) {
-    return (uint32_t(quant1(v.x, inv)) & 0xffu) | ((uint32_t(quant1(v.y, inv)) & 0xffu) << 8) |
-           ((uint32_t(quant1(v.z, inv)) & 0xffu) << 16) | (uint32_t(quant1(v.w, inv)) << 24);
+// rint(fl(x * inv)) in the low byte: adding 1.5 * 2^23 rounds to a whole number
+// (ties to even) and leaves it, two's complement, in the low mantissa bits.
+__device__ __forceinline__ uint32_t quant1(float x, float inv) {
+    return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.0f));
 }
 
-// Groups of 32 .. 256 columns: a warp takes 256 columns of a row as two loads
-// of four values a lane (columns 4*lane and 128 + 4*lane), so a group is 8, 16
-// or 32 lanes of one load, or both loads: its maximum is 3 to 5 shuffles.
+__device__ __forceinline__ uint32_t quant4(float4 v, const GroupScale &g) {
+    const uint32_t lo = __byte_perm(quant1(v.x, g.inv), quant1(v.y, g.inv), 0x0040);
+    const uint32_t hi = __byte_perm(quant1(v.z, g.inv), quant1(v.w, g.inv), 0x0040);
+    return __byte_perm(lo, hi, 0x5410) & g.keep;
+}
+
+// Groups of 32 .. 256 columns: 16 values a lane, so a group is 2 to 16 lanes
+// and its maximum 1 to 4 shuffles; a warp takes 512 columns of a row.  Value i
+// = 4j + t of lane l of a group is its column 4 * (l + lanes * j) + t with
+// 16-byte rows (VEC), else l + lanes * i, so that neighbouring lanes hold
+// neighbouring columns.  Loads take no branch: a column past the row reads its
+// group's first (or the row's, for a group past it), which changes no maximum.
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256)
-quantize_groups_kernel(int64_t rows, int64_t cols, const void *__restrict__ x, int64_t ldx, int group,
+quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t ldx, int group,
                        int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale, int64_t lds) {
-    const int lane = threadIdx.x & 31;
-    const int64_t segs = (cols + 255) / 256;
+    const int lane = threadIdx.x & 31, lanes = group / 16, l = lane & (lanes - 1);
+    const int segs = (cols + 511) / 512;
     const int64_t items = rows * segs, stride = int64_t(gridDim.x) * 8;
-    const int width = min(group, 128) / 4;          // lanes of a group within one load
     for (int64_t it = blockIdx.x * int64_t(8) + (threadIdx.x >> 5); it < items; it += stride) {
-        const int64_t r = it / segs, c0 = (it - r * segs) * 256 + 4 * lane;
-        float4 v[2];
-        uint32_t m[2];
+        const int64_t r = items <= UINT32_MAX ? uint32_t(it) / uint32_t(segs) : it / segs;
+        const int g0 = int(it - r * segs) * 512 + (lane - l) * 16;      // the group's first column
+        const int safe = g0 < cols ? g0 : 0;
+        const int64_t base = r * ldx;
+        float4 v[4];
+        float m = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int64_t c = c0 + 128 * s, base = r * ldx + c;
+        for (int j = 0; j < 4; ++j) {
             if constexpr (VEC) {
-                v[s] = c < cols ? load_four<TY>(x, base) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const int c = g0 + 4 * (l + lanes * j);
+                v[j] = load_four<TY>(x, base + (c < cols ? c : safe));
             } else {
-                v[s].x = c < cols ? load_one<TY>(x, base) : 0.0f;
-                v[s].y = c + 1 < cols ? load_one<TY>(x, base + 1) : 0.0f;
-                v[s].z = c + 2 < cols ? load_one<TY>(x, base + 2) : 0.0f;
-                v[s].w = c + 3 < cols ? load_one<TY>(x, base + 3) : 0.0f;
+                const int c = g0 + l + 4 * lanes * j;
+                v[j].x = load_one<TY>(x, base + (c < cols ? c : safe));
+                v[j].y = load_one<TY>(x, base + (c + lanes < cols ? c + lanes : safe));
+                v[j].z = load_one<TY>(x, base + (c + 2 * lanes < cols ? c + 2 * lanes : safe));
+                v[j].w = load_one<TY>(x, base + (c + 3 * lanes < cols ? c + 3 * lanes : safe));
             }
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) m[s] = mag4(0u, v[s]);
-        if (group == 256) m[0] = m[1] = max(m[0], m[1]);
-        for (int o = width / 2; o > 0; o >>= 1) {
-            m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-            m[1] = max(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
-        }
+        for (int j = 0; j < 4; ++j) m = max_mag4(m, v[j]);
+        for (int o = lanes / 2; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const GroupScale gs = group_scale(m);
+        int8_t *o = q + r * ldq;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int64_t c = c0 + 128 * s;
-            if (c >= cols) continue;
-            const GroupScale gs = group_scale(m[s]);
-            const uint32_t w = quant4(v[s], gs.inv);
-            int8_t *o = q + r * ldq + c;
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = quant4(v[j], gs);
             if constexpr (VEC) {
-                __stcs(reinterpret_cast<uint32_t *>(o), w);
+                const int c = g0 + 4 * (l + lanes * j);
+                if (c < cols) *reinterpret_cast<uint32_t *>(o + c) = w;
             } else {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    if (c + t < cols) o[t] = int8_t(w >> (8 * t));
+                for (int t = 0; t < 4; ++t) {
+                    const int c = g0 + l + lanes * (4 * j + t);
+                    if (c < cols) o[c] = int8_t(w >> (8 * t));
+                }
             }
-            if (c % group == 0) scale[r * lds + c / group] = gs.scale;
         }
+        if (l == 0 && g0 < cols) scale[r * lds + g0 / group] = gs.scale;
     }
 }
 
-// One scale a row: T threads a row (a warp, or the CTA), each keeping up to
-// 4 * KEEP of the row's values in registers between the maximum and the
-// quantisation; longer rows are read again from the cache.
+// One scale a row: T threads a row (a warp, or the CTA), each keeping up to 32
+// of the row's values in registers between the maximum and the quantisation;
+// longer rows are read again from the cache.
 template <int TY, bool VEC, int T>
 __global__ void __launch_bounds__(256)
-quantize_rows_kernel(int64_t rows, int64_t cols, const void *__restrict__ x, int64_t ldx, int8_t *__restrict__ q,
+quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t ldx, int8_t *__restrict__ q,
                      int64_t ldq, float *__restrict__ scale, int64_t lds) {
-    constexpr int KEEP = 8, ROWS = 256 / T, STEP = VEC ? 4 * T : T;
-    __shared__ uint32_t part[8];
+    constexpr int KEEP = 8, ROWS = 256 / T;
+    __shared__ float part[8];
     const int t = threadIdx.x % T;
+    const int steps = (cols + 4 * T - 1) / (4 * T);
     for (int64_t r0 = blockIdx.x * int64_t(ROWS); r0 < rows; r0 += int64_t(gridDim.x) * ROWS) {
-        const int64_t r = r0 + threadIdx.x / T;
-        const bool live = r < rows;
-        const int64_t base = r * ldx;
-        // step k covers columns [k * STEP, (k + 1) * STEP): VEC four a thread,
-        // else one a thread (four steps make one float4 here)
-        float4 v[KEEP];
-        auto load = [&](int64_t k) {
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool live = r0 + threadIdx.x / T < rows;
+        const int64_t r = live ? r0 + threadIdx.x / T : rows - 1, base = r * ldx;
+        // step k covers columns [4T * k, 4T * (k + 1)): four in a row a thread
+        // with 16-byte rows, else four T apart; past the end column 0 is read
+        auto load = [&](int k) {
             if constexpr (VEC) {
-                const int64_t c = k * STEP + 4 * t;
-                if (c < cols) w = load_four<TY>(x, base + c);
+                const int c = 4 * T * k + 4 * t;
+                return load_four<TY>(x, base + (c < cols ? c : 0));
             } else {
-                const int64_t c = 4 * k * STEP + t;
-                if (c < cols) w.x = load_one<TY>(x, base + c);
-                if (c + STEP < cols) w.y = load_one<TY>(x, base + c + STEP);
-                if (c + 2 * STEP < cols) w.z = load_one<TY>(x, base + c + 2 * STEP);
-                if (c + 3 * STEP < cols) w.w = load_one<TY>(x, base + c + 3 * STEP);
+                const int c = 4 * T * k + t;
+                return make_float4(load_one<TY>(x, base + (c < cols ? c : 0)),
+                                   load_one<TY>(x, base + (c + T < cols ? c + T : 0)),
+                                   load_one<TY>(x, base + (c + 2 * T < cols ? c + 2 * T : 0)),
+                                   load_one<TY>(x, base + (c + 3 * T < cols ? c + 3 * T : 0)));
             }
-            return w;
         };
-        const int64_t steps = (cols + 4 * T - 1) / (4 * T);
-        uint32_t m = 0;
-        if (live) {
+        float4 v[KEEP];
+        float m = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KEEP; ++k)
-                if (k < steps) v[k] = load(k);
+        for (int k = 0; k < KEEP; ++k)
+            if (k < steps) v[k] = load(k);
 #pragma unroll
-            for (int k = 0; k < KEEP; ++k)
-                if (k < steps) m = mag4(m, v[k]);
-            for (int64_t k = KEEP; k < steps; ++k) m = mag4(m, load(k));
-        }
+        for (int k = 0; k < KEEP; ++k)
+            if (k < steps) m = max_mag4(m, v[k]);
+        for (int k = KEEP; k < steps; ++k) m = max_mag4(m, load(k));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 16; o > 0; o >>= 1) m = max_mag(m, __shfl_xor_sync(0xffffffffu, m, o));
         if constexpr (T > 32) {
             if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < T / 32; ++w) m = max(m, part[w]);
+            for (int w = 0; w < T / 32; ++w) m = max_mag(m, part[w]);
             __syncthreads();
         }
         if (!live) continue;
         const GroupScale gs = group_scale(m);
         if (t == 0) scale[r * lds] = gs.scale;
         int8_t *o = q + r * ldq;
-        auto store = [&](int64_t k, float4 f) {
-            const uint32_t w = quant4(f, gs.inv);
+        auto store = [&](int k, float4 f) {
+            const uint32_t w = quant4(f, gs);
             if constexpr (VEC) {
-                const int64_t c = k * STEP + 4 * t;
+                const int c = 4 * T * k + 4 * t;
                 if (c < cols) *reinterpret_cast<uint32_t *>(o + c) = w;
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t c = (4 * k + j) * STEP + t;
+                    const int c = 4 * T * k + T * j + t;
                     if (c < cols) o[c] = int8_t(w >> (8 * j));
                 }
             }
@@ -221,26 +225,35 @@ quantize_rows_kernel(int64_t rows, int64_t cols, const void *__restrict__ x, int
 #pragma unroll
         for (int k = 0; k < KEEP; ++k)
             if (k < steps) store(k, v[k]);
-        for (int64_t k = KEEP; k < steps; ++k) store(k, load(k));
+        for (int k = KEEP; k < steps; ++k) store(k, load(k));
     }
 }
 
-// Threads along columns (four each, or one), the grid's y along rows.
+// A CTA takes 4 * 256 units of a row (a unit: four columns with aligned rows,
+// else one), four a thread in flight together; the grid's y runs along rows.
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256)
-dequantize_kernel(int64_t rows, int64_t cols, const int8_t *__restrict__ q, int64_t ldq,
+dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t ldq,
                   const float *__restrict__ scale, int64_t lds, int shift, void *__restrict__ x, int64_t ldx) {
-    const int64_t units = VEC ? cols / 4 : cols;
+    const int units = VEC ? cols / 4 : cols;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const int8_t *qr = q + r * ldq;
         const float *sr = scale + r * lds;
-        for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < units;
-             i += int64_t(gridDim.x) * blockDim.x) {
-            if constexpr (VEC) {
-                const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(qr) + i);
-                store_four<TY>(x, r * ldx + 4 * i, unpack_q4(w, __ldg(sr + ((4 * i) >> shift))));
-            } else {
-                store_one<TY>(x, r * ldx + i, __fmul_rn(float(qr[i]), __ldg(sr + (i >> shift))));
+        for (int64_t i0 = blockIdx.x * int64_t(1024) + threadIdx.x; i0 < units; i0 += int64_t(gridDim.x) * 1024) {
+            uint32_t w[4];
+            float s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t i = i0 + 256 * j < units ? i0 + 256 * j : 0;
+                w[j] = VEC ? __ldcs(reinterpret_cast<const uint32_t *>(qr) + i) : uint32_t(int(__ldg(qr + i)));
+                s[j] = __ldg(sr + ((VEC ? 4 * i : i) >> shift));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t i = i0 + 256 * j;
+                if (i >= units) continue;
+                if constexpr (VEC) store_four<TY>(x, r * ldx + 4 * i, unpack_q4(w[j], s[j]));
+                else store_one<TY>(x, r * ldx + i, __fmul_rn(float(int(w[j])), s[j]));
             }
         }
     }
@@ -323,11 +336,11 @@ dim3 grid_2d(int64_t units, int64_t rows) {
 }
 
 template <int TY>
-int launch_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx, int64_t group, int8_t *q, int64_t ldq,
+int launch_quantize(int64_t rows, int cols, const void *x, int64_t ldx, int64_t group, int8_t *q, int64_t ldq,
                     float *scale, int64_t lds, cudaStream_t s) {
     const bool vec = cols % 4 == 0 && aligned(x, ldx, storage_size(TY), 4 * storage_size(TY)) && aligned(q, ldq, 1, 4);
     if (group > 0) {
-        const int64_t items = rows * ((cols + 255) / 256);
+        const int64_t items = rows * ((int64_t(cols) + 511) / 512);
         const unsigned grid = unsigned(std::min<int64_t>((items + 7) / 8, int64_t(sm_count()) * 32));
         if (vec)
             quantize_groups_kernel<TY, true><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds);
@@ -350,13 +363,13 @@ int launch_quantize(int64_t rows, int64_t cols, const void *x, int64_t ldx, int6
 }
 
 template <int TY>
-int launch_dequantize(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq, const float *scale, int64_t lds,
-                      int shift, void *x, int64_t ldx, cudaStream_t s) {
+int launch_dequantize(int64_t rows, int cols, const int8_t *q, int64_t ldq, const float *scale, int64_t lds, int shift,
+                      void *x, int64_t ldx, cudaStream_t s) {
     const bool vec = cols % 4 == 0 && aligned(x, ldx, storage_size(TY), 4 * storage_size(TY)) && aligned(q, ldq, 1, 4);
-    if (vec)
-        dequantize_kernel<TY, true><<<grid_2d(cols / 4, rows), 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
-    else
-        dequantize_kernel<TY, false><<<grid_2d(cols, rows), 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
+    const int64_t units = vec ? cols / 4 : cols;
+    const dim3 grid(unsigned((units + 1023) / 1024), unsigned(std::min<int64_t>(rows, 65535)));
+    if (vec) dequantize_kernel<TY, true><<<grid, 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
+    else dequantize_kernel<TY, false><<<grid, 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
     return check_launch();
 }
 
@@ -368,7 +381,7 @@ using namespace repops;
 extern "C" int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
                                        int64_t group, int8_t *q, int64_t ldq, float *scale, int64_t lds,
                                        cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || cols > INT32_MAX || !known_storage(x_type) || !known_group(group))
+    if (rows < 0 || cols < 0 || cols > (int64_t(1) << 30) || !known_storage(x_type) || !known_group(group))
         return REPOPS_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return REPOPS_OK;
     if (!x || !q || !scale) return REPOPS_ERR_INVALID_ARG;
@@ -380,18 +393,18 @@ extern "C" int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x
         return REPOPS_ERR_ALIAS;
     switch (x_type) {
         case REPOPS_TYPE_F32:
-            return launch_quantize<REPOPS_TYPE_F32>(rows, cols, x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_F32>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
         case REPOPS_TYPE_F16:
-            return launch_quantize<REPOPS_TYPE_F16>(rows, cols, x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_F16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
         default:
-            return launch_quantize<REPOPS_TYPE_BF16>(rows, cols, x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_BF16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
     }
 }
 
 extern "C" int repops_dequantize_rows_i8(int64_t rows, int64_t cols, const int8_t *q, int64_t ldq,
                                          const float *scale, int64_t lds, int64_t group, void *x, int x_type,
                                          int64_t ldx, cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || cols > INT32_MAX || !known_storage(x_type) || !known_group(group))
+    if (rows < 0 || cols < 0 || cols > (int64_t(1) << 30) || !known_storage(x_type) || !known_group(group))
         return REPOPS_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return REPOPS_OK;
     if (!x || !q || !scale) return REPOPS_ERR_INVALID_ARG;
@@ -403,11 +416,11 @@ extern "C" int repops_dequantize_rows_i8(int64_t rows, int64_t cols, const int8_
     const int shift = group_shift(group);
     switch (x_type) {
         case REPOPS_TYPE_F32:
-            return launch_dequantize<REPOPS_TYPE_F32>(rows, cols, q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_F32>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
         case REPOPS_TYPE_F16:
-            return launch_dequantize<REPOPS_TYPE_F16>(rows, cols, q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_F16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
         default:
-            return launch_dequantize<REPOPS_TYPE_BF16>(rows, cols, q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_BF16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
     }
 }
 
@@ -416,7 +429,7 @@ extern "C" int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_
                                          const float *u_scale, int64_t ldus, int64_t group, const float *dh,
                                          int64_t lddh, float *dg, int64_t lddg, float *du, int64_t lddu, float *h,
                                          int64_t ldh, cudaStream_t stream) {
-    if (rows < 0 || cols < 0 || cols > INT32_MAX || !known_group(group)) return REPOPS_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0 || cols > (int64_t(1) << 30) || !known_group(group)) return REPOPS_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return REPOPS_OK;
     if (!g || !g_scale || !u || !u_scale || !dh || !dg || !du) return REPOPS_ERR_INVALID_ARG;
     const int64_t ng = group_count(cols, group);
