@@ -22,10 +22,12 @@
 //
 // Many rows: the operands are widened once to binary16 (exact: 8 bits fit its
 // 11) in scratch and multiplied by tcgen05 with binary32 accumulators in tensor
-// memory.  Every product and every partial sum of up to 512 of them is a whole
-// number of at most 2^23, so binary32 accumulation is exact whatever its order;
-// after each 512 of k the accumulators are added to 32-bit integers in
-// registers while the tensor core fills the other half of tensor memory.
+// memory.  Every product and every partial sum of up to 1024 of them is a whole
+// number of at most 2^24, so binary32 accumulation is exact whatever its order;
+// after each 1024 of k the accumulators are added to 32-bit integers in
+// registers while the tensor core fills the other half of tensor memory.  (A
+// conversion to integer takes 8 cycles a warp: 2300 cycles for a drain, against
+// 8200 of products.)
 #include <algorithm>
 #include <type_traits>
 
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
 // --------------------------------------------------------------- many rows ----
 
 constexpr int BM = 128, BK = 64;          // BK binary16 = one 128-byte swizzled row
-constexpr int kChunkSteps = 8;            // k-steps between two drains: 512 of k
+constexpr int kChunkSteps = 16;           // k-steps between two drains: 1024 of k
 
 // The rows of A, then those of B, as binary16 rows of Kp (a multiple of 64)
 // values, zeros past K: 16 values a thread.
@@ -269,26 +271,14 @@ struct TileMap {
     }
 };
 
-// Scales (or biases) of columns col .. col + 7: one value for the whole warp
-// each, a column past the end repeating the last one.
-__device__ __forceinline__ void column_values(const float *v, int64_t col, int64_t n, bool vec, float (&out)[8]) {
-    if (vec && col + 8 <= n) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(v + col)), b = __ldg(reinterpret_cast<const float4 *>(v + col) + 1);
-        out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
-        out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = __ldg(v + min(col + i, n - 1));
-    }
-}
-
-// C's tile: sums x scales, through the warp's block of shared memory.  c_tma:
-// C can be stored by TMA (a block of 32 rows x 128 bytes at a time, clipped at
-// C's edges); else lanes store single values.  s_vec: scales and bias are on
-// 16-byte boundaries.
+// C's tile: sums x scales, through the warp's block of shared memory.  Lane l
+// holds the scales (and biases) of columns l, l + 32, ...  c_tma: C can be
+// stored by TMA (a block of 32 rows x 128 bytes at a time, clipped at C's
+// edges); else lanes store single values.
 template <int TY, int COLS>
 __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *map_c, const int (&acc)[COLS], float sa,
-                                           int64_t row0, int64_t col0, uint8_t *block, bool c_tma, bool s_vec) {
+                                           const float (&sb)[COLS / 32], const float (&bias)[COLS / 32], int64_t row0,
+                                           int64_t col0, uint8_t *block, bool c_tma) {
     constexpr int W = TY == REPOPS_TYPE_F32 ? 32 : COLS < 64 ? COLS : 64;    // columns of a block
     const int lane = threadIdx.x & 31;
     uint4 *chunk = reinterpret_cast<uint4 *>(block);           // 16-byte chunk c of row r in slot c ^ (r & 7)
@@ -298,25 +288,26 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *m
         if (c_tma && lane == 0) tma_store_wait_read();         // the block's previous contents have left
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < W; c += 8) {
-            float v[8], sb[8];
-            column_values(p.sb, col0 + j + c, p.N, s_vec, sb);
+        for (int c = j; c < j + W; c += 8) {
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(__int2float_rn(acc[j + c + i]), sa), sb[i]);
+            for (int i = 0; i < 8; ++i)
+                v[i] = __fmul_rn(__fmul_rn(__int2float_rn(acc[c + i]), sa),
+                                 __shfl_sync(0xffffffffu, sb[c / 32], (c + i) % 32));
             if (p.bias) {
-                column_values(p.bias, col0 + j + c, p.N, s_vec, sb);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], sb[i]);
+                for (int i = 0; i < 8; ++i)
+                    v[i] = __fadd_rn(v[i], __shfl_sync(0xffffffffu, bias[c / 32], (c + i) % 32));
             }
             if constexpr (TY == REPOPS_TYPE_F32) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    chunk[lane * 8 + ((c / 4 + h) ^ (lane & 7))] =
+                    chunk[lane * 8 + (((c - j) / 4 + h) ^ (lane & 7))] =
                         make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
                                    __float_as_uint(v[4 * h + 3]));
             } else {
-                chunk[lane * 8 + ((c / 8) ^ (lane & 7))] = make_uint4(pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]),
-                                                                      pack_c<TY>(v[4], v[5]), pack_c<TY>(v[6], v[7]));
+                chunk[lane * 8 + (((c - j) / 8) ^ (lane & 7))] = make_uint4(
+                    pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]), pack_c<TY>(v[4], v[5]), pack_c<TY>(v[6], v[7]));
             }
         }
         if (c_tma) {
@@ -328,13 +319,18 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *m
             using E = typename std::conditional<TY == REPOPS_TYPE_F32, float, uint16_t>::type;
             constexpr int PER = 16 / int(sizeof(E));           // values of a chunk
             const E *e = reinterpret_cast<const E *>(block);
-#pragma unroll 1
-            for (int r = 0; r < 32 && row0 + r < p.M; ++r)
+            const int rows = int(min(p.M - row0, int64_t(32)));
 #pragma unroll
-                for (int c = lane; c < W; c += 32)
-                    if (col0 + j + c < p.N)
-                        static_cast<E *>(p.C)[(row0 + r) * p.ldc + col0 + j + c] =
-                            e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
+            for (int h = 0; h < W; h += 32) {
+                const int c = h + lane;
+                E *out = static_cast<E *>(p.C) + row0 * p.ldc + col0 + j + c;
+                const bool mine = col0 + j + c < p.N;
+#pragma unroll 8
+                for (int r = 0; r < 32; ++r) {
+                    const E v = e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
+                    if (mine && r < rows) out[r * p.ldc] = v;
+                }
+            }
             __syncwarp();
         }
     }
@@ -343,7 +339,7 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *m
 template <int TY, int BN>
 __global__ void __launch_bounds__(kTileThreads, 1)
 gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma, int s_vec,
+                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
                     unsigned *status) {
     using T = TileCfg<BN>;
     extern __shared__ uint8_t raw[];
@@ -463,6 +459,13 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             tm.at(t, tile_m, tile_n);
             const int64_t row0 = int64_t(tile_m) * BM + 32 * (warp & 3), col0 = int64_t(tile_n) * BN + half * T::COLS;
             const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
+            float sb[T::COLS / 32], bias[T::COLS / 32];
+#pragma unroll
+            for (int i = 0; i < T::COLS / 32; ++i) {
+                const int64_t col = min(col0 + 32 * i + lane, p.N - 1);    // past the end: not stored
+                sb[i] = __ldg(p.sb + col);
+                bias[i] = p.bias ? __ldg(p.bias + col) : 0.0f;
+            }
             int acc[T::COLS];
 #pragma unroll
             for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
@@ -487,7 +490,7 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 if (lane == 0) atomicOr(status, 1u);
                 break;
             }
-            store_tile<TY, T::COLS>(p, &map_c, acc, sa, row0, col0, block, c_tma != 0, s_vec != 0);
+            store_tile<TY, T::COLS>(p, &map_c, acc, sa, sb, bias, row0, col0, block, c_tma != 0);
         }
         if (c_tma && lane == 0) tma_store_wait();
     }
@@ -592,7 +595,6 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     const int c_tma = wide <= T::COLS && reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && uint64_t(a.ldc) * csize % 16 == 0 &&
                       a.ldc < (int64_t(1) << 37) && make_map(&mc, ctype, csize, a.C, a.N, a.M, a.ldc, wide, 32);
     if (!c_tma) mc = ma;
-    const int s_vec = reinterpret_cast<uintptr_t>(a.sb) % 16 == 0 && (!a.bias || reinterpret_cast<uintptr_t>(a.bias) % 16 == 0);
     unsigned *status = nullptr;
     if ((rc = status_word_address(&status)) != REPOPS_OK) return rc;
     auto kern = gemm_i8_tile_kernel<TY, BN>;
@@ -601,7 +603,7 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     const TileMap tm{int(ceil_div(a.M, BM)), int(ceil_div(a.N, BN)), 16};
     const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
     kern<<<unsigned(std::min<int64_t>(tiles, sm_count())), kTileThreads, T::SMEM, s>>>(ma, mb, mc, a, tm, int(Kp / BK),
-                                                                                      c_tma, s_vec, status);
+                                                                                      c_tma, status);
     return check_launch();
 }
 
