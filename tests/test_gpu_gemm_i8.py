@@ -98,7 +98,7 @@ def test_large_random_rows(rp, config):
     assert torch.equal(got, ref)
 
 
-@pytest.mark.parametrize("config", [0, 1, 3])
+@pytest.mark.parametrize("config", [0, 1, 2, 3])
 def test_rows_outside_are_left(rp, config):
     A, B = ints((70, 200), 3).to(DEV), ints((90, 200), 4).to(DEV)
     sa, sb = torch.ones(70, device=DEV), torch.ones(90, device=DEV)
@@ -122,7 +122,7 @@ def test_empty_and_zero_k(rp):
         assert torch.equal(y, bias.expand(3, 5))
 
 
-@pytest.mark.parametrize("config", [0, 2])
+@pytest.mark.parametrize("config", [0, 1, 2, 3])
 def test_scales_with_nan_and_infinity(rp, config):
     A, B = ints((4, 64), 6, 1, 100).to(DEV), ints((6, 64), 7, 1, 100).to(DEV)
     sa, sb = torch.ones(4, device=DEV), torch.ones(6, device=DEV)

@@ -29,6 +29,7 @@
 // conversion to integer takes 8 cycles a warp: 2300 cycles for a drain, against
 // 8200 of products.)
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -249,9 +250,12 @@ __global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half
     }
 }
 
-template <int BN>
+// CTAS CTAs (1, or a pair) multiply a tile of CTAS * 128 rows by BN columns,
+// each holding 128 rows of A and BN / CTAS of B in a stage.
+template <int BN, int CTAS>
 struct TileCfg {
-    static constexpr int STAGE_BYTES = (BM + BN) * BK * 2;
+    static constexpr int B_ROWS = BN / CTAS;
+    static constexpr int STAGE_BYTES = (BM + B_ROWS) * BK * 2;
     static constexpr int STAGES = 196608 / STAGE_BYTES;          // 4, 6 or 8
     static constexpr int WARP_STAGE = 32 * 128;                  // an epilogue warp's block: 32 rows of 128 bytes
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * WARP_STAGE;
@@ -336,12 +340,10 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *m
     }
 }
 
-template <int TY, int BN>
-__global__ void __launch_bounds__(kTileThreads, 1)
-gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
-                    unsigned *status) {
-    using T = TileCfg<BN>;
+template <int TY, int BN, int CTAS>
+__device__ __forceinline__ void tile_kernel(const CUtensorMap &map_a, const CUtensorMap &map_b, const CUtensorMap &map_c,
+                                            const I8Args &p, const TileMap &tm, int ksteps, int c_tma, unsigned *status) {
+    using T = TileCfg<BN, CTAS>;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
@@ -350,7 +352,8 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     // then takes its 64 (128 columns) or 128 cycles instead of the 111 that
     // issuing it from a branch it must assume divergent costs
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int tiles = tm.tiles_m * tm.tiles_n;
+    const uint32_t rank = CTAS == 1 ? 0u : cluster_rank();
+    const int tiles = tm.tiles_m * tm.tiles_n, first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
     const int chunks = (ksteps + kChunkSteps - 1) / kChunkSteps;
     if (threadIdx.x == 0) {
         for (int s = 0; s < T::STAGES; ++s) {
@@ -359,14 +362,15 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], 8 * CTAS);
         }
         mbar_init(&drained, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc(&tmem_slot, T::TMEM_COLS);
+    if (warp == 9) tmem_alloc<CTAS>(&tmem_slot, T::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -380,18 +384,29 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             int issued = 0, s = 0;
             uint32_t phase = 1;                                // the wait before the ring's first use passes
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = first; t < tiles && ok; t += stride) {
                 int m, n;
                 tm.at(t, m, n);
+                const int row_a = (m * CTAS + int(rank)) * BM, row_b = n * BN + int(rank) * T::B_ROWS;
                 for (int k = 0; k < ksteps; ++k, ++issued) {
                     if (!mbar_wait_bounded(&empty[s], phase)) {
                         ok = false;
                         break;
                     }
                     uint8_t *st = stages + s * T::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&full[s], T::STAGE_BYTES);
-                    tma_load_2d(st, &map_a, &full[s], k * BK, m * BM);
-                    tma_load_2d(st + BM * BK * 2, &map_b, &full[s], k * BK, n * BN);
+                    // a pair's four copies all signal the first CTA, whose
+                    // barrier is armed for both CTAs' bytes; a copy of the other
+                    // CTA that lands before that leaves the phase open, as the
+                    // arming arrival is still missing
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * T::STAGE_BYTES);
+                    if constexpr (CTAS == 1) {
+                        tma_load_2d(st, &map_a, &full[s], k * BK, row_a);
+                        tma_load_2d(st + BM * BK * 2, &map_b, &full[s], k * BK, row_b);
+                    } else {
+                        const uint32_t bar = cluster_addr(&full[s], 0);
+                        tma_load_2d_pair(st, &map_a, bar, k * BK, row_a);
+                        tma_load_2d_pair(st + BM * BK * 2, &map_b, bar, k * BK, row_b);
+                    }
                     if (++s == T::STAGES) {
                         s = 0;
                         phase ^= 1u;
@@ -400,23 +415,31 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             }
             if (!ok) {
                 atomicOr(status, 1u);
-                for (int i = max(0, issued - T::STAGES); i < issued; ++i)
-                    mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
+                if (rank == 0) {
+                    for (int i = max(0, issued - T::STAGES); i < issued; ++i)
+                        mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
+                } else {
+                    // these copies signal the other CTA: give them the time of
+                    // a copy a thousand times over
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 2000000u) {}
+                }
             }
         }
     } else if (warp == 9) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = idesc_f16(BM, BN);
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = idesc_f16(BM * CTAS, BN);
             const uint32_t base = smem_addr(stages);
             int s = 0, b = 0;
             uint32_t phase = 0, acc_phase = 1;
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = first; t < tiles && ok; t += stride) {
                 for (int c = 0; c < chunks && ok; ++c) {
                     if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
                         ok = false;
                         break;
                     }
+                    if constexpr (CTAS == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                     tc_fence_after();
                     const int steps = min(kChunkSteps, ksteps - c * kChunkSteps);
                     for (int k = 0; k < steps; ++k) {
@@ -429,21 +452,21 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                         const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + BM * BK * 2);
 #pragma unroll
                         for (int j = 0; j < BK / 16; ++j)      // 32 bytes of k a step within the swizzled row
-                            tc_mma_f16(tmem + b * BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
-                        tc_commit(&empty[s]);
+                            tc_mma_f16<CTAS>(tmem + b * BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+                        tc_commit<CTAS>(&empty[s]);
                         if (++s == T::STAGES) {
                             s = 0;
                             phase ^= 1u;
                         }
                     }
-                    if (ok) tc_commit(&acc_full[b]);
+                    if (ok) tc_commit<CTAS>(&acc_full[b]);
                     b ^= 1;
                     if (b == 0) acc_phase ^= 1u;
                 }
             }
             if (!ok) {
                 atomicOr(status, 1u);
-                tc_commit(&drained);
+                tc_commit<CTAS>(&drained);
                 mbar_wait_bounded(&drained, 0u);
             }
         }
@@ -454,10 +477,11 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
         int b = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int t = first; t < tiles && ok; t += stride) {
             int tile_m, tile_n;
             tm.at(t, tile_m, tile_n);
-            const int64_t row0 = int64_t(tile_m) * BM + 32 * (warp & 3), col0 = int64_t(tile_n) * BN + half * T::COLS;
+            const int64_t row0 = (int64_t(tile_m) * CTAS + rank) * BM + 32 * (warp & 3),
+                          col0 = int64_t(tile_n) * BN + half * T::COLS;
             const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
             float sb[T::COLS / 32], bias[T::COLS / 32];
 #pragma unroll
@@ -482,7 +506,10 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                if (lane == 0) {
+                    if constexpr (CTAS == 1) mbar_arrive(&acc_empty[b]);
+                    else mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+                }
                 b ^= 1;
                 if (b == 0) phase ^= 1u;
             }
@@ -497,13 +524,30 @@ gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync();                   // no CTA leaves while the other may signal it
     tc_fence_after();
-    if (warp == 9) tmem_free(tmem, T::TMEM_COLS);
+    if (warp == 9) tmem_free<CTAS>(tmem, T::TMEM_COLS);
+}
+
+template <int TY, int BN>
+__global__ void __launch_bounds__(kTileThreads, 1)
+gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
+                    unsigned *status) {
+    tile_kernel<TY, BN, 1>(map_a, map_b, map_c, p, tm, ksteps, c_tma, status);
+}
+
+template <int TY>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
+                    unsigned *status) {
+    tile_kernel<TY, 256, 2>(map_a, map_b, map_c, p, tm, ksteps, c_tma, status);
 }
 
 // ------------------------------------------------------------------- host ----
 
-enum I8Config { CFG_AUTO = -1, CFG_ROWS = 0, CFG_TILE256 = 1, CFG_TILE128 = 2, CFG_TILE64 = 3, CFG_COUNT = 4 };
+enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_PAIR, CFG_TILE128, CFG_TILE64, CFG_COUNT };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -516,9 +560,28 @@ int64_t padded_k(int64_t K) { return ceil_div(K, BK) * BK; }
 
 uint64_t tile_workspace(int64_t M, int64_t N, int64_t K) { return uint64_t(M + N) * uint64_t(padded_k(K)) * 2u; }
 
+// The kernel whose estimated time is least.  Few rows: the integer tensor rate
+// (115 TOPS in whole groups of 8 tokens) or the memory's, plus 3 us.  Tiles: 3
+// bytes for each of B's to widen it (5.5 TB/s), 6 us of launches, fill and last
+// store, and the waves of tiles x k-steps of 64 x the time of a step: 0.36 us for
+// a pair's 256 x 256, 0.22 for 128 x 128, 0.19 for 128 x 64 (below that the
+// products' issue, not their size, sets the time).  Measured either side of a
+// choice, in us: M 32, N 16384, K 2048: rows 20, tiles 29; M 64: 39, 30.
+// N = K = 2048, M 1024: pair 22, 128 x 128 16; M 8192: 61, 61.  N 16384, K 2048,
+// M 2048: pair 104, 128 x 128 121; M 128: 36, 30.  N = K = 8192, M 128: 128 x 128
+// 76, 128 x 64 71.
 int auto_config(int64_t M, int64_t N, int64_t K) {
-    if (M <= 64 || K == 0) return CFG_ROWS;
-    return N > 128 ? CFG_TILE256 : N > 64 ? CFG_TILE128 : CFG_TILE64;
+    if (K == 0) return CFG_ROWS;
+    const double nk = double(N) * double(K), sms = 152;
+    const double steps = double(padded_k(K) / BK);
+    auto tiles = [&](int64_t bm, int64_t bn, double slots, double step_us) {
+        return std::ceil(double(ceil_div(M, bm)) * double(ceil_div(N, bn)) / slots) * steps * step_us;
+    };
+    const double t[3] = {tiles(256, 256, sms / 2, 0.36), tiles(128, 128, sms, 0.22), tiles(128, 64, sms, 0.19)};
+    const int best = t[0] <= t[1] && t[0] <= t[2] ? 0 : t[1] <= t[2] ? 1 : 2;
+    const double few = std::max(nk / 6.5e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
+    const double many = 3.0 * (nk + double(M) * double(K)) / 5.5e6 + 6.0 + t[best];
+    return few <= many ? CFG_ROWS : CFG_PAIR + best;
 }
 
 bool operand_vec(const int8_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
@@ -572,9 +635,9 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, unsigned size, const v
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TY, int BN>
+template <int TY, int BN, int CTAS>
 int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
-    using T = TileCfg<BN>;
+    using T = TileCfg<BN, CTAS>;
     const int64_t Kp = padded_k(a.K);
     const int64_t items = (a.M + a.N) * (Kp / 16);
     const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 32));
@@ -584,7 +647,7 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     if (rc != REPOPS_OK) return rc;
     constexpr CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap ma, mb, mc;
-    if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, BN))
+    if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, T::B_ROWS))
         return REPOPS_ERR_UNSUPPORTED;
     // C by TMA where its rows start on 16 bytes and a block's rows fill 128 bytes
     constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
@@ -597,13 +660,13 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     if (!c_tma) mc = ma;
     unsigned *status = nullptr;
     if ((rc = status_word_address(&status)) != REPOPS_OK) return rc;
-    auto kern = gemm_i8_tile_kernel<TY, BN>;
+    auto kern = CTAS == 2 ? gemm_i8_pair_kernel<TY> : gemm_i8_tile_kernel<TY, BN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return set_cuda_error(e);
-    const TileMap tm{int(ceil_div(a.M, BM)), int(ceil_div(a.N, BN)), 16};
+    const TileMap tm{int(ceil_div(a.M, BM * CTAS)), int(ceil_div(a.N, BN)), 16 / CTAS};
     const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
-    kern<<<unsigned(std::min<int64_t>(tiles, sm_count())), kTileThreads, T::SMEM, s>>>(ma, mb, mc, a, tm, int(Kp / BK),
-                                                                                      c_tma, status);
+    kern<<<unsigned(std::min<int64_t>(tiles, sm_count() / CTAS) * CTAS), kTileThreads, T::SMEM, s>>>(
+        ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
     return check_launch();
 }
 
@@ -611,9 +674,9 @@ template <int TY>
 int run_i8(int cfg, const I8Args &a, void *ws, cudaStream_t s) {
     switch (cfg) {
         case CFG_ROWS: return launch_rows<TY>(a, s);
-        case CFG_TILE256: return launch_tile<TY, 256>(a, static_cast<__half *>(ws), s);
-        case CFG_TILE128: return launch_tile<TY, 128>(a, static_cast<__half *>(ws), s);
-        default: return launch_tile<TY, 64>(a, static_cast<__half *>(ws), s);
+        case CFG_PAIR: return launch_tile<TY, 256, 2>(a, static_cast<__half *>(ws), s);
+        case CFG_TILE128: return launch_tile<TY, 128, 1>(a, static_cast<__half *>(ws), s);
+        default: return launch_tile<TY, 64, 1>(a, static_cast<__half *>(ws), s);
     }
 }
 
