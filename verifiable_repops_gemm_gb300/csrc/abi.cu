@@ -179,7 +179,7 @@ using namespace repops;
 
 extern "C" const char *repops_version(void) {
     return "librepops 0.1.0; arch sm_103a; fp32 IEEE-754 round-to-nearest-even, no FMA, no FTZ, "
-           "no tensor cores; gemm tiles 128x128/256t 8x8, 64x128/128t 8x8, 128x64/128t 8x8, "
+           "no tensor cores (gemm_i8 alone uses them: exact integer sums); gemm tiles 128x128/256t 8x8, 64x128/128t 8x8, 128x64/128t 8x8, "
            "64x64/128t 8x4, 32x64/128t 4x4, BK 32, loaders TMA(128B swizzle)+cp.async; "
            "mean+sgd left fold, divide by count; merkle sha256 leaf 0x00 node 0x01 promote-odd; "
            "flags: " REPOPS_BUILD_FLAGS;

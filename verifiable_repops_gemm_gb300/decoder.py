@@ -37,6 +37,21 @@ call (transposed GEMMs, the backward row operators, column sums, the inverse
 rotation); the key and value gradients of a key/value head accumulate its
 query heads in head order through the GEMM's residual epilogue.
 
+Sandwich blocks (post_norm, gated, residual_scale): each block's output passes
+through a norm of its own, a learned gate and a residual scale before the
+residual sum -- x = x + s * (gate * RMSNorm(f)) -- and the edge between the two
+blocks, with the norm before the MLP, is one call (rmsnorm_residual).
+
+8-bit checkpoints: `activations(bits=8)` keeps x, qkv, the attention output
+and the MLP's input to its activation as 8-bit rows with a scale for every 128
+columns (about a quarter of their bytes), and no norm outputs, activations or
+probabilities: `backward` recomputes those from the restored rows.  Its bits are
+those of the binary32 backward on the restored activations.
+
+8-bit weights: `quantize_weights` and `forward_i8` run the layer's four weight
+products on 8-bit rows (a scale a token) and 8-bit weights (a scale a channel)
+for inference (gemm_i8).
+
 Every step is a library call (this module only slices tensors); the bits of
 the result depend on nothing but the inputs.  In the GeLU layer, GeLU runs as
 its own kernel by default: inside the GEMM's epilogue it measured 2.5x its
@@ -52,7 +67,11 @@ from dataclasses import dataclass
 import torch
 
 from . import (gemm, gemm_batched, gelu, rmsnorm_rows, softmax_rows, ACT_GELU, colsum, gelu_backward,
-               rmsnorm_backward, softmax_backward, swiglu, swiglu_backward, rope_frequencies, rope_table, rope)
+               rmsnorm_backward, softmax_backward, swiglu, swiglu_backward, rope_frequencies, rope_table, rope,
+               rmsnorm_residual, rmsnorm_residual_backward, quantize_rows, dequantize_rows, swiglu_backward_i8,
+               rmsnorm_backward_i8, gemm_i8)
+
+CHECKPOINT_GROUP = 128   # columns that share a scale in an 8-bit checkpoint
 
 
 @dataclass(frozen=True)
@@ -65,6 +84,13 @@ class DecoderConfig:
     eps: float = 1e-5
     mlp: str = "swiglu"        # "swiglu" (Llama: gate and up, no biases) or "gelu" (up + bias)
     rope_base: float = 500000.0  # rotary base; 0 turns the rotary embedding off
+    post_norm: bool = False    # a norm after each block (gains p1, p2)
+    gated: bool = False        # a learned gate on each block's output (a1, a2)
+    residual_scale: float = 1.0  # the scale of a block's output in the residual sum
+
+    @property
+    def sandwich(self) -> bool:
+        return self.post_norm or self.gated or self.residual_scale != 1.0
 
     @property
     def d_head(self) -> int:
@@ -90,22 +116,28 @@ def weight_shapes(cfg: DecoderConfig) -> dict:
     """Every weight of a layer and its shape, in a fixed order."""
     d, w, f = cfg.d, cfg.qkv_width, cfg.ffn
     if cfg.mlp == "swiglu":
-        return {"g1": (d,), "w_qkv": (d, w), "w_o": (d, d), "g2": (d,), "w_gu": (d, 2 * f), "w_down": (f, d)}
-    if cfg.mlp == "gelu":
-        return {"g1": (d,), "w_qkv": (d, w), "w_o": (d, d), "g2": (d,), "w_up": (d, f), "b_up": (f,),
-                "w_down": (f, d), "b_down": (d,)}
-    raise ValueError("mlp must be 'swiglu' or 'gelu'")
+        out = {"g1": (d,), "w_qkv": (d, w), "w_o": (d, d), "g2": (d,), "w_gu": (d, 2 * f), "w_down": (f, d)}
+    elif cfg.mlp == "gelu":
+        out = {"g1": (d,), "w_qkv": (d, w), "w_o": (d, d), "g2": (d,), "w_up": (d, f), "b_up": (f,),
+               "w_down": (f, d), "b_down": (d,)}
+    else:
+        raise ValueError("mlp must be 'swiglu' or 'gelu'")
+    if cfg.post_norm:
+        out.update(p1=(d,), p2=(d,))
+    if cfg.gated:
+        out.update(a1=(d,), a2=(d,))
+    return out
 
 
 def init_weights(cfg: DecoderConfig, seed: int, device) -> dict:
-    """Synthetic weights: N(0, 0.02) matrices and biases, norm gains
+    """Synthetic weights: N(0, 0.02) matrices and biases, norm gains and gates
     N(1, 0.1); seeded, generated on `device`."""
     g = torch.Generator(device=device)
     g.manual_seed(seed)
     out = {}
     for name, shape in weight_shapes(cfg).items():
         t = torch.randn(shape, generator=g, device=device, dtype=torch.float32)
-        out[name] = t * 0.1 + 1.0 if name in ("g1", "g2") else t * 0.02
+        out[name] = t * 0.1 + 1.0 if name in ("g1", "g2", "p1", "p2", "a1", "a2") else t * 0.02
     return out
 
 
@@ -235,6 +267,8 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
         raise ValueError("tokens must be a whole number of sequences")
     ws = work if work is not None else workspace(cfg, T, x.device)
     f = cfg.ffn
+    if save is not None and save.get("bits") == 8:
+        return _forward_checkpointed(x, w, cfg, ws, save, fused_attention)
     if save is not None:
         save["x0"].copy_(x)
         h, qkv, attn, a = save["h1"], save["qkv"], save["attn"], save["a"]
@@ -245,6 +279,15 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
     _rotate(qkv, cfg, ws["rope"], inverse=False)
     attention(qkv, cfg, attn, ws["scores"], save["probs"] if save is not None else None, ws.get("streams"),
               fused=fused_attention)
+    if cfg.sandwich:
+        f1 = gemm(attn, w["w_o"], out=save["f1"] if save is not None else ws["tmp_d"])
+        h = save["h2"] if save is not None else h
+        _edge(x, f1, w, cfg, 1, h)
+        if save is not None:
+            save["x1"].copy_(x)
+        f2 = _mlp(h, w, cfg, ws, save, save["f2"] if save is not None else ws["tmp_d"])
+        _edge(x, f2, w, cfg, 2)
+        return x
     if fused:
         gemm_batched(attn, w["w_o"], out=x, residual=x)
     else:
@@ -283,11 +326,146 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
     return x
 
 
-def activations(cfg: DecoderConfig, tokens: int, device) -> dict:
+def _edge(x, f, w, cfg: DecoderConfig, k: int, h=None):
+    """The edge after block k (1 attention, 2 MLP) in place on x; with h, the
+    norm before the MLP into it."""
+    rmsnorm_residual(x, f, w["g2"] if h is not None else None, cfg.eps, post_gain=w.get("p%d" % k),
+                     gate=w.get("a%d" % k), alpha=cfg.residual_scale, y=x, h=h)
+
+
+def _mlp(h, w, cfg: DecoderConfig, ws, save, out):
+    """The MLP of h (without the residual) into `out`, its activations where
+    `save` keeps them."""
+    f = cfg.ffn
+    a = save["a"] if save is not None else ws["a"]
+    if cfg.mlp == "swiglu":
+        gu = save["gu"] if save is not None else ws["gu"]
+        gemm(h, w["w_gu"], out=gu)
+        swiglu(gu[:, :f], gu[:, f:], out=a)
+        return gemm(a, w["w_down"], out=out)
+    pre = save["pre"] if save is not None else a
+    gemm_batched(h, w["w_up"], out=pre, bias=w["b_up"])
+    gelu(pre, out=a)
+    return gemm_batched(a, w["w_down"], out=out, bias=w["b_down"])
+
+
+def _keep(save, name, t):
+    """t's rows in 8 bits into the checkpoint `name`."""
+    q, s = save[name]
+    quantize_rows(t, group=CHECKPOINT_GROUP, out=q, scale=s)
+
+
+def _restore(save, name, out):
+    q, s = save[name]
+    return dequantize_rows(q, s, group=CHECKPOINT_GROUP, out=out)
+
+
+def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused_attention):
+    """forward(save=...) for activations(bits=8): the same x, the activations
+    quantised as they are made."""
+    h, qkv, attn, tmp = ws["h"], ws["qkv"], ws["attn"], ws["tmp_d"]
+    _keep(save, "x0", x)
+    rmsnorm_rows(x, w["g1"], cfg.eps, out=h)
+    gemm(h, w["w_qkv"], out=qkv)
+    _rotate(qkv, cfg, ws["rope"], inverse=False)
+    _keep(save, "qkv", qkv)
+    attention(qkv, cfg, attn, ws["scores"], None, ws.get("streams"), fused=fused_attention)
+    _keep(save, "attn", attn)
+    if cfg.sandwich:
+        f1 = gemm(attn, w["w_o"], out=tmp)
+        _keep(save, "f1", f1)
+        _edge(x, f1, w, cfg, 1, h)
+    else:
+        gemm_batched(attn, w["w_o"], out=x, residual=x)
+        rmsnorm_rows(x, w["g2"], cfg.eps, out=h)
+    _keep(save, "x1", x)
+    if cfg.sandwich:
+        f2 = _mlp(h, w, cfg, ws, None if cfg.mlp == "swiglu" else {"a": ws["a"], "pre": ws["pre"]}, tmp)
+        _keep(save, "f2", f2)
+        _edge(x, f2, w, cfg, 2)
+    elif cfg.mlp == "swiglu":
+        gemm(h, w["w_gu"], out=ws["gu"])
+        swiglu(ws["gu"][:, :cfg.ffn], ws["gu"][:, cfg.ffn:], out=ws["a"])
+        gemm_batched(ws["a"], w["w_down"], out=x, residual=x)
+    else:
+        gemm_batched(h, w["w_up"], out=ws["pre"], bias=w["b_up"])
+        gelu(ws["pre"], out=ws["a"])
+        gemm_batched(ws["a"], w["w_down"], out=x, bias=w["b_down"], residual=x)
+    if cfg.mlp == "swiglu":
+        _keep(save, "g", ws["gu"][:, :cfg.ffn])
+        _keep(save, "u", ws["gu"][:, cfg.ffn:])
+    else:
+        _keep(save, "pre", ws["pre"])
+    return x
+
+
+WEIGHT_MATRICES = ("w_qkv", "w_o", "w_gu", "w_up", "w_down")
+
+
+def quantize_weights(w: dict, cfg: DecoderConfig) -> dict:
+    """The layer's weight matrices in 8 bits for `forward_i8`: name -> (whole
+    numbers (N, K), a row for each output channel; scales (N,))."""
+    out = {}
+    for name in WEIGHT_MATRICES:
+        if name in w:
+            q, s = quantize_rows(w[name].t().contiguous())
+            out[name] = (q, s.view(-1))
+    return out
+
+
+def forward_i8(x, w: dict, w8: dict, cfg: DecoderConfig, *, work: dict = None, fused_attention: bool = False):
+    """The layer on x in place with 8-bit weight products (inference): every
+    operand row is quantised with a scale of its own just before its product
+    (quantize_rows, gemm_i8 with `quantize_weights`' w8); norms, rotary
+    embedding, attention and residual sums stay binary32."""
+    T, f = x.shape[0], cfg.ffn
+    if T % cfg.seq_len:
+        raise ValueError("tokens must be a whole number of sequences")
+    ws = work if work is not None else workspace(cfg, T, x.device)
+
+    def product(rows, name, out, bias=None):
+        q, s = quantize_rows(rows)
+        wq, wscale = w8[name]
+        return gemm_i8(q, wq.t(), s.view(-1), wscale, out=out, bias=bias)
+
+    h = rmsnorm_rows(x, w["g1"], cfg.eps, out=ws["h"])
+    qkv = product(h, "w_qkv", ws["qkv"])
+    _rotate(qkv, cfg, ws["rope"], inverse=False)
+    attention(qkv, cfg, ws["attn"], ws["scores"], None, ws.get("streams"), fused=fused_attention)
+    _edge(x, product(ws["attn"], "w_o", ws["tmp_d"]), w, cfg, 1, h)
+    if cfg.mlp == "swiglu":
+        gu = product(h, "w_gu", ws["gu"])
+        a = swiglu(gu[:, :f], gu[:, f:], out=ws["a"])
+        f2 = product(a, "w_down", ws["tmp_d"])
+    else:
+        a = product(h, "w_up", ws["a"], bias=w["b_up"])
+        f2 = product(gelu(a, out=a), "w_down", ws["tmp_d"], bias=w["b_down"])
+    _edge(x, f2, w, cfg, 2)
+    return x
+
+
+def activations(cfg: DecoderConfig, tokens: int, device, bits: int = 32) -> dict:
     """Buffers for the activations `forward(save=...)` keeps for `backward`
-    (every head's attention probabilities included: seqs * heads * S^2)."""
+    (every head's attention probabilities included: seqs * heads * S^2).
+    bits=8: 8-bit checkpoints instead, (whole numbers, scales) a tensor, of
+    what backward does not recompute."""
     e = dict(dtype=torch.float32, device=device)
     group, S = cfg.heads // cfg.kv_heads, cfg.seq_len
+    if bits == 8:
+        def rows(cols):
+            return (torch.empty(tokens, cols, dtype=torch.int8, device=device),
+                    torch.empty(tokens, -(-cols // CHECKPOINT_GROUP), **e))
+
+        out = {"bits": 8, "x0": rows(cfg.d), "qkv": rows(cfg.qkv_width), "attn": rows(cfg.d), "x1": rows(cfg.d)}
+        if cfg.mlp == "swiglu":
+            out.update(g=rows(cfg.ffn), u=rows(cfg.ffn))
+        else:
+            out["pre"] = rows(cfg.ffn)
+        if cfg.sandwich:
+            out.update(f1=rows(cfg.d), f2=rows(cfg.d))
+        return out
+    if bits != 32:
+        raise ValueError("bits must be 32 or 8")
     out = {"x0": torch.empty(tokens, cfg.d, **e), "h1": torch.empty(tokens, cfg.d, **e),
            "qkv": torch.empty(tokens, cfg.qkv_width, **e), "attn": torch.empty(tokens, cfg.d, **e),
            "probs": torch.empty(tokens // S * cfg.kv_heads, group, S, S, **e),
@@ -297,6 +475,8 @@ def activations(cfg: DecoderConfig, tokens: int, device) -> dict:
         out["gu"] = torch.empty(tokens, 2 * cfg.ffn, **e)
     else:
         out["pre"] = torch.empty(tokens, cfg.ffn, **e)
+    if cfg.sandwich:
+        out.update(f1=torch.empty(tokens, cfg.d, **e), f2=torch.empty(tokens, cfg.d, **e))
     return out
 
 
@@ -325,36 +505,129 @@ def backward(dy, w: dict, cfg: DecoderConfig, saved: dict, *, work: dict = None,
         dq, dk rotated back (the rotary embedding's transpose)
         dW_qkv = h1^T dqkv, dh1 = dqkv W_qkv^T
         dx0 = RMSNorm'(x0; dh1) + dx1, dg1 = colsum(dh1 * xhat1)
+
+    In a sandwich layer the edges' backward (rmsnorm_residual_backward) stands
+    before the MLP's and in the place of RMSNorm'(x1; dh2) + dy: it splits dy
+    into the residual's gradient and the block's, and gives dp2, da2 and dg2, dp1,
+    da1.  From 8-bit checkpoints the norms' and SwiGLU's backward read the kept
+    rows and write the norm outputs and activations the weight gradients need.
     """
     T, f = dy.shape[0], cfg.ffn
-    ws = work if work is not None else backward_workspace(cfg, T, dy.device)
+    kept8 = saved.get("bits") == 8
+    ws = work if work is not None else backward_workspace(cfg, T, dy.device, bits=8 if kept8 else 32)
     g = {}
     o = grads if grads is not None else {}
-    g["w_down"] = gemm(saved["a"].t(), dy, out=o.get("w_down"))
-    da = gemm(dy, w["w_down"].t(), out=ws["t_ffn"])
-    if cfg.mlp == "swiglu":
-        gu = saved["gu"]
-        swiglu_backward(gu[:, :f], gu[:, f:], da, dg=gu[:, :f], du=gu[:, f:])     # gu <- [dg | du]
-        g["w_gu"] = gemm(saved["h2"].t(), gu, out=o.get("w_gu"))
-        dh2 = gemm(gu, w["w_gu"].t(), out=ws["t_d"])
+    dm = dy                                  # the MLP's gradient
+    if cfg.sandwich:
+        f2 = _restore(saved, "f2", ws["t_f"]) if kept8 else saved["f2"]
+        dy, dm = _edge_backward(dy, None, None, f2, w, cfg, 2, g, o, ws["t_e"])
+    if kept8:
+        dgu, dh2, a = _mlp_backward_i8(dm, w, cfg, saved, ws, g, o)
     else:
-        g["b_down"] = colsum(dy, out=o.get("b_down"))
-        dpre = gelu_backward(saved["pre"], da, out=da)
-        g["w_up"] = gemm(saved["h2"].t(), dpre, out=o.get("w_up"))
-        g["b_up"] = colsum(dpre, out=o.get("b_up"))
-        dh2 = gemm(dpre, w["w_up"].t(), out=ws["t_d"])
-    dx1, p2 = rmsnorm_backward(saved["x1"], w["g2"], cfg.eps, dh2, dx=dy, dyxh=ws["t_d2"], res=dy)
-    g["g2"] = colsum(p2, out=o.get("g2"))
-    g["w_o"] = gemm(saved["attn"].t(), dx1, out=o.get("w_o"))
-    dattn = gemm(dx1, w["w_o"].t(), out=ws["t_d"])
+        a = saved["a"]
+        g["w_down"] = gemm(a.t(), dm, out=o.get("w_down"))
+        da = gemm(dm, w["w_down"].t(), out=ws["t_ffn"])
+        if cfg.mlp == "swiglu":
+            gu = saved["gu"]
+            swiglu_backward(gu[:, :f], gu[:, f:], da, dg=gu[:, :f], du=gu[:, f:])     # gu <- [dg | du]
+            g["w_gu"] = gemm(saved["h2"].t(), gu, out=o.get("w_gu"))
+            dh2 = gemm(gu, w["w_gu"].t(), out=ws["t_d"])
+        else:
+            g["b_down"] = colsum(dm, out=o.get("b_down"))
+            dpre = gelu_backward(saved["pre"], da, out=da)
+            g["w_up"] = gemm(saved["h2"].t(), dpre, out=o.get("w_up"))
+            g["b_up"] = colsum(dpre, out=o.get("b_up"))
+            dh2 = gemm(dpre, w["w_up"].t(), out=ws["t_d"])
+    dblock = None
+    if cfg.sandwich:
+        f1 = _restore(saved, "f1", ws["t_f"]) if kept8 else saved["f1"]
+        x1 = _restore(saved, "x1", ws["h"]) if kept8 else saved["x1"]
+        dx1, dblock = _edge_backward(dy, dh2, x1, f1, w, cfg, 1, g, o, ws["t_e"])
+        if kept8:
+            rmsnorm_rows(x1, w["g2"], cfg.eps, out=ws["h"])
+    elif kept8:
+        q, s = saved["x1"]
+        dx1, g["g2"] = rmsnorm_backward_i8(q, s, w["g2"], cfg.eps, dh2, dx=dy, dgamma=o.get("g2"),
+                                           group=CHECKPOINT_GROUP, res=dy, h=ws["h"])
+    else:
+        dx1, p2 = rmsnorm_backward(saved["x1"], w["g2"], cfg.eps, dh2, dx=dy, dyxh=ws["t_d2"], res=dy)
+        g["g2"] = colsum(p2, out=o.get("g2"))
+    if dblock is None:
+        dblock = dx1
+    if kept8:
+        g["w_gu" if cfg.mlp == "swiglu" else "w_up"] = gemm(ws["h"].t(), dgu,
+                                                            out=o.get("w_gu" if cfg.mlp == "swiglu" else "w_up"))
+        attn = _restore(saved, "attn", ws["attn"])
+        saved = _recomputed_attention(saved, cfg, ws)
+    else:
+        attn = saved["attn"]
+    g["w_o"] = gemm(attn.t(), dblock, out=o.get("w_o"))
+    dattn = gemm(dblock, w["w_o"].t(), out=ws["t_d"])
     _attention_backward(dattn, ws["dqkv"], saved, cfg, ws["dp"], ws.get("streams"))
     dqkv = ws["dqkv"]
     _rotate(dqkv, cfg, ws["rope"], inverse=True)
+    if kept8:
+        dh1 = gemm(dqkv, w["w_qkv"].t(), out=ws["t_d"])
+        q, s = saved["x0"]
+        dx0, g["g1"] = rmsnorm_backward_i8(q, s, w["g1"], cfg.eps, dh1, dx=dx1, dgamma=o.get("g1"),
+                                           group=CHECKPOINT_GROUP, res=dx1, h=ws["h"])
+        g["w_qkv"] = gemm(ws["h"].t(), dqkv, out=o.get("w_qkv"))
+        return dx0, g
     g["w_qkv"] = gemm(saved["h1"].t(), dqkv, out=o.get("w_qkv"))
     dh1 = gemm(dqkv, w["w_qkv"].t(), out=ws["t_d"])
     dx0, p1 = rmsnorm_backward(saved["x0"], w["g1"], cfg.eps, dh1, dx=dx1, dyxh=ws["t_d2"], res=dx1)
     g["g1"] = colsum(p1, out=o.get("g1"))
     return dx0, g
+
+
+def _edge_backward(dy, dh, y, f, w, cfg: DecoderConfig, k: int, g: dict, o: dict, df):
+    """(dx in dy's storage, the block's gradient in df) of the edge after block
+    k; its parameters' gradients into g."""
+    post, gate = w.get("p%d" % k), w.get("a%d" % k)
+    pre = w["g2"] if dh is not None else None
+    dx, df, dpre, dpost, dgate = rmsnorm_residual_backward(
+        dy, dh, y, f, pre, cfg.eps, post_gain=post, gate=gate, alpha=cfg.residual_scale, dx=dy, df=df,
+        dpre=o.get("g2") if pre is not None else None, dpost=o.get("p%d" % k), dgate=o.get("a%d" % k))
+    for name, t in (("g2", dpre), ("p%d" % k, dpost), ("a%d" % k, dgate)):
+        if t is not None:
+            g[name] = t
+    return dx, df
+
+
+def _mlp_backward_i8(dm, w, cfg: DecoderConfig, saved, ws, g: dict, o: dict):
+    """(the gradient of the MLP's first product's output, dh2, the activation) of
+    an MLP kept in 8 bits; w_down's (and the biases') gradients into g."""
+    f = cfg.ffn
+    da = gemm(dm, w["w_down"].t(), out=ws["t_ffn"])
+    a = ws["a"]
+    if cfg.mlp == "swiglu":
+        gu = ws["gu"]
+        (gq, gs), (uq, us) = saved["g"], saved["u"]
+        swiglu_backward_i8(gq, gs, uq, us, da, dg=gu[:, :f], du=gu[:, f:], group=CHECKPOINT_GROUP, h=a)
+        g["w_down"] = gemm(a.t(), dm, out=o.get("w_down"))
+        return gu, gemm(gu, w["w_gu"].t(), out=ws["t_d"]), a
+    pre = _restore(saved, "pre", ws["pre"])
+    gelu(pre, out=a)
+    g["w_down"] = gemm(a.t(), dm, out=o.get("w_down"))
+    g["b_down"] = colsum(dm, out=o.get("b_down"))
+    dpre = gelu_backward(pre, da, out=da)
+    g["b_up"] = colsum(dpre, out=o.get("b_up"))
+    return dpre, gemm(dpre, w["w_up"].t(), out=ws["t_d"]), a
+
+
+def _recomputed_attention(saved, cfg: DecoderConfig, ws):
+    """saved with qkv restored and every head's probabilities computed again
+    from it (the forward's product and causal softmax)."""
+    S, dh, kv, H = cfg.seq_len, cfg.d_head, cfg.kv_heads, cfg.heads
+    qkv = _restore(saved, "qkv", ws["qkv"])
+    for s in range(qkv.shape[0] // S):
+        rows = slice(s * S, (s + 1) * S)
+        sc = ws["probs"][s * kv:(s + 1) * kv].view(H, S, S)
+        gemm_batched(_heads(qkv, rows, 0, H, dh), _kv(qkv, rows, cfg.d, kv, dh).transpose(1, 2), out=sc,
+                     alpha=1.0 / float(dh) ** 0.5, causal_first=0)
+        P = sc.view(H * S, S)
+        softmax_rows(P, out=P, causal_first=0, causal_period=S)
+    return dict(saved, qkv=qkv, probs=ws["probs"])
 
 
 def _attention_backward(dattn, dqkv, saved, cfg: DecoderConfig, dp, streams):
@@ -421,14 +694,29 @@ def _attention_backward(dattn, dqkv, saved, cfg: DecoderConfig, dp, streams):
         _after(main, *joined)
 
 
-def backward_workspace(cfg: DecoderConfig, tokens: int, device) -> dict:
+def backward_workspace(cfg: DecoderConfig, tokens: int, device, bits: int = 32) -> dict:
+    """Scratch of `backward`; bits=8 adds what it restores and recomputes from
+    8-bit checkpoints (one layer's, reused by every layer)."""
     e = dict(dtype=torch.float32, device=device)
     group, S = cfg.heads // cfg.kv_heads, cfg.seq_len
     seqs = tokens // S
-    return {"t_ffn": torch.empty(tokens, cfg.ffn, **e), "t_d": torch.empty(tokens, cfg.d, **e),
-            "t_d2": torch.empty(tokens, cfg.d, **e), "dqkv": torch.empty(tokens, cfg.qkv_width, **e),
-            "dp": torch.empty(seqs * cfg.kv_heads, group, S, S, **e), "rope": rope_tables(cfg, device),
-            "streams": side_streams(cfg, tokens, device)}
+    out = {"t_ffn": torch.empty(tokens, cfg.ffn, **e), "t_d": torch.empty(tokens, cfg.d, **e),
+           "t_d2": torch.empty(tokens, cfg.d, **e), "dqkv": torch.empty(tokens, cfg.qkv_width, **e),
+           "dp": torch.empty(seqs * cfg.kv_heads, group, S, S, **e), "rope": rope_tables(cfg, device),
+           "streams": side_streams(cfg, tokens, device)}
+    if cfg.sandwich:
+        out["t_e"] = torch.empty(tokens, cfg.d, **e)
+    if bits == 8:
+        out.update(h=torch.empty(tokens, cfg.d, **e), a=torch.empty(tokens, cfg.ffn, **e),
+                   qkv=torch.empty(tokens, cfg.qkv_width, **e), attn=torch.empty(tokens, cfg.d, **e),
+                   probs=torch.empty(seqs * cfg.kv_heads, group, S, S, **e))
+        if cfg.mlp == "swiglu":
+            out["gu"] = torch.empty(tokens, 2 * cfg.ffn, **e)
+        else:
+            out["pre"] = torch.empty(tokens, cfg.ffn, **e)
+        if cfg.sandwich:
+            out["t_f"] = torch.empty(tokens, cfg.d, **e)
+    return out
 
 
 def workspace(cfg: DecoderConfig, tokens: int, device) -> dict:
@@ -442,4 +730,6 @@ def workspace(cfg: DecoderConfig, tokens: int, device) -> dict:
            "streams": side_streams(cfg, tokens, device)}
     if cfg.mlp == "swiglu":
         out["gu"] = torch.empty(tokens, 2 * cfg.ffn, **e)
+    else:
+        out["pre"] = torch.empty(tokens, cfg.ffn, **e)
     return out

@@ -67,13 +67,16 @@ class Model:
 
 
 class Workspace:
-    """Buffers one contributor's forward and backward reuse."""
+    """Buffers one contributor's forward and backward reuse.  checkpoint_bits=8
+    keeps the layers' activations in 8 bits (decoder.activations): every
+    contributor and every verifier must choose the same, as the gradients' bits
+    depend on it."""
 
-    def __init__(self, model: Model, tokens: int, device):
+    def __init__(self, model: Model, tokens: int, device, checkpoint_bits: int = 32):
         cfg = model.cfg
-        self.saved = [decoder.activations(cfg, tokens, device) for _ in range(model.layers)]
+        self.saved = [decoder.activations(cfg, tokens, device, checkpoint_bits) for _ in range(model.layers)]
         self.fwd = decoder.workspace(cfg, tokens, device)
-        self.bwd = decoder.backward_workspace(cfg, tokens, device)
+        self.bwd = decoder.backward_workspace(cfg, tokens, device, checkpoint_bits)
         self.h = torch.empty(tokens, cfg.d, dtype=torch.float32, device=device)
         self.d = torch.empty(tokens, cfg.d, dtype=torch.float32, device=device)
 
