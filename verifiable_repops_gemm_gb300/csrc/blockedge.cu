@@ -69,6 +69,13 @@ __device__ __forceinline__ void row_prefetch(const float *row, int n) {
     if (c < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
 }
 
+// The same for a row that is read once: into L2.
+__device__ __forceinline__ void row_prefetch_l2(const float *row, int n) {
+    if (!row) return;
+    const int c = (threadIdx.x >> 5) * 1024 + 32 * (threadIdx.x & 31);
+    if (c < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+}
+
 template <bool VEC>
 __device__ __forceinline__ void row_store(float *row, int k, int n, float4 v) {
     const int c = slab_col<VEC>(k, 0);
@@ -398,7 +405,7 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
 
 // Resident CTAs per SM the row kernel asks the compiler for.
 template <int T>
-constexpr int kEdgeBackBlocks = 448 / T;
+constexpr int kEdgeBackBlocks = 512 / T;
 
 // dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
 // after the block.  Q8: y comes in 8 bits, and h may be written again.
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
     __shared__ GroupBuf<T, 1> gb1;
     int phase1 = 0, phase2 = 0;
     constexpr int Q = T * RUN / 4;
-    float4 *sy = stage_mem, *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
+    float4 *sy = stage_mem, *sh = sy + Q, *sf = sh + Q;
     const int n = int(p.n);
     const float nf = float(p.n);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -419,13 +426,14 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
         }
         if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, n);
         cp_async_commit();
-        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, n);
-        cp_async_commit();
+        const float *dyr = p.dy ? p.dy + row * p.lddy : nullptr;
+        row_prefetch_l2(dyr, n);
+        row_prefetch<VEC>(p.dh ? p.pre : nullptr, n);
         if constexpr (Q8) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, k, row8_load<VEC>(p, row, k, n));
         }
-        cp_async_wait<1>();
+        cp_async_wait<0>();
         __syncwarp();
         float r2[2] = {0.0f, 0.0f};
         if (p.dh) r2[0] = slab_fold(sy, n, Square());
@@ -464,14 +472,16 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
             for (int k = 0; k < 8; ++k)
                 e[k] = mul4(sub4(g[k], mul4(mul4(stage_load<VEC>(sy, k), inv_y), c)), inv_y);
         }
-        cp_async_wait<0>();
-        __syncwarp();
-        if (p.dy) {
+        if (dyr) {
+            float4 d[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float4 d = stage_load<VEC>(sr, k);
-                e[k] = p.dh ? add4(e[k], d) : d;
-            }
+            for (int k = 0; k < 8; ++k) d[k] = row_load<VEC>(dyr, k, n);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) e[k] = p.dh ? add4(e[k], d[k]) : d[k];
+        }
+        if constexpr (F) {
+            row_prefetch<VEC>(p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr, n);
+            row_prefetch<VEC>(p.post, n);
         }
         float *dxr = p.dx + row * p.lddx;
 #pragma unroll
@@ -496,10 +506,10 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     e[k] = mul4(e[k], g[k]);
-                    stage_store<VEC>(sr, k, mul4(e[k], mul4(stage_load<VEC>(sf, k), inv_f)));
+                    stage_store<VEC>(sh, k, mul4(e[k], mul4(stage_load<VEC>(sf, k), inv_f)));
                 }
                 __syncwarp();
-                float r1[1] = {slab_fold(sr, n, Ident())};
+                float r1[1] = {slab_fold(sh, n, Ident())};
                 slab_roots<T, 1>(r1, gb1, phase1, n);
                 const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
@@ -838,7 +848,7 @@ int launch_long(Kern kern, const Args &a, int64_t rows, int64_t n, cudaStream_t 
 template <bool VEC, bool Q8, bool F>
 int launch_rows(const EdgeBackArgs &a, cudaStream_t s) {
     auto go = [&](auto kern, int T) {
-        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (F ? 4 : 3), a.rows, s, a);
+        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (F ? 3 : 2), a.rows, s, a);
     };
     if (a.n <= 1024) return go(edge_backward_kernel<32, VEC, Q8, F>, 32);
     if (a.n <= 2048) return go(edge_backward_kernel<64, VEC, Q8, F>, 64);

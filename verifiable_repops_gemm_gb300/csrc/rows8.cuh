@@ -45,11 +45,16 @@ inline int64_t group_count(int64_t cols, int64_t group) { return group == 0 ? 1 
 }
 
 // Four whole numbers packed in a word, lowest byte first, each as the value it
-// stands for: one rounding, fl(q * scale).
+// stands for: one rounding, fl(q * scale).  With its sign bit flipped a byte is
+// q + 128; as the low byte of 2^23's pattern it is 2^23 + q + 128, and taking
+// 2^23 + 128 away is exact -- a permute and an add, where the conversion
+// instruction runs at an eighth of their rate.
 __device__ __forceinline__ float4 unpack_q4(uint32_t w, float scale) {
-    const int v = static_cast<int>(w);
-    return make_float4(__fmul_rn(float((v << 24) >> 24), scale), __fmul_rn(float((v << 16) >> 24), scale),
-                       __fmul_rn(float((v << 8) >> 24), scale), __fmul_rn(float(v >> 24), scale));
+    const uint32_t u = w ^ 0x80808080u;
+    const float a = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540)), b = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541)),
+                c = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7542)), d = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7543));
+    return make_float4(__fmul_rn(__fsub_rn(a, 8388736.0f), scale), __fmul_rn(__fsub_rn(b, 8388736.0f), scale),
+                       __fmul_rn(__fsub_rn(c, 8388736.0f), scale), __fmul_rn(__fsub_rn(d, 8388736.0f), scale));
 }
 
 }  // namespace
