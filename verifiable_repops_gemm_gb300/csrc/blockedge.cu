@@ -50,14 +50,16 @@ __device__ __forceinline__ int slab_col(int k, int t) {
 // Loads take no branch, so that a slab's are all in flight together: a column
 // past the row's end reads column 0 instead, and its result is never stored or
 // folded.  n is a multiple of 4 with VEC.
-template <bool VEC>
-__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int k, int n) {
+// CONST: nothing in the kernel writes the row.
+template <bool VEC, bool CONST = true>
+__device__ __forceinline__ float4 row_load(const float *row, int k, int n) {
     const int c = slab_col<VEC>(k, 0);
+    auto one = [&](int i) { return CONST ? __ldg(row + (i < n ? i : 0)) : row[i < n ? i : 0]; };
     if constexpr (VEC) {
-        return __ldg(reinterpret_cast<const float4 *>(row + (c < n ? c : 0)));
+        const float4 *q = reinterpret_cast<const float4 *>(row + (c < n ? c : 0));
+        return CONST ? __ldg(q) : *q;
     } else {
-        return make_float4(__ldg(row + (c < n ? c : 0)), __ldg(row + (c + 32 < n ? c + 32 : 0)),
-                           __ldg(row + (c + 64 < n ? c + 64 : 0)), __ldg(row + (c + 96 < n ? c + 96 : 0)));
+        return make_float4(one(c), one(c + 32), one(c + 64), one(c + 96));
     }
 }
 
@@ -141,7 +143,7 @@ __device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict
 // The warp's group result of the tree over the staged values f(v): each lane
 // folds its run, every lane folds the lanes' results in order.
 template <class F>
-__device__ __forceinline__ float slab_fold(const float4 *stage, int n, F f) {
+__device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, int n, F f) {
     const int u = threadIdx.x, warp0 = u & ~31;
     const int len = min(RUN, n - u * RUN);                 // 0 or less past the end
     float v[RUN];
@@ -160,16 +162,26 @@ __device__ __forceinline__ float slab_fold(const float4 *stage, int n, F f) {
             if (i < len) acc = __fadd_rn(acc, f(v[i]));
     }
     const int have = (n + RUN - 1) / RUN - warp0;     // runs present from this warp on
-    float g = __shfl_sync(0xffffffffu, acc, 0);
+    // the lanes' results to every lane: a store and eight broadcast reads (31
+    // shuffles cost the shared-memory pipe three times as much)
+    float4 *mine = lanes + (warp0 >> 2);
+    __syncwarp();
+    reinterpret_cast<float *>(mine)[threadIdx.x & 31] = acc;
+    __syncwarp();
+    float r[RUN];
+#pragma unroll
+    for (int c = 0; c < RUN / 4; ++c) {
+        const float4 w = mine[c];
+        r[4 * c] = w.x; r[4 * c + 1] = w.y; r[4 * c + 2] = w.z; r[4 * c + 3] = w.w;
+    }
+    float g = r[0];
     if (have >= RUN) {
 #pragma unroll
-        for (int i = 1; i < RUN; ++i) g = __fadd_rn(g, __shfl_sync(0xffffffffu, acc, i));
+        for (int i = 1; i < RUN; ++i) g = __fadd_rn(g, r[i]);
     } else {
 #pragma unroll
-        for (int i = 1; i < RUN; ++i) {
-            const float o = __shfl_sync(0xffffffffu, acc, i);
-            if (i < have) g = __fadd_rn(g, o);
-        }
+        for (int i = 1; i < RUN; ++i)
+            if (i < have) g = __fadd_rn(g, r[i]);
     }
     return g;
 }
@@ -240,6 +252,7 @@ template <int T, bool VEC>
 __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     extern __shared__ float4 stage_mem[];
     __shared__ GroupBuf<T, 1> gb;
+    __shared__ float4 lanes[T / 4];
     int phase = 0;
     constexpr int Q = T * RUN / 4;
     constexpr bool PF = kEdgePrefetch<T>;
@@ -273,7 +286,7 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         __syncwarp();
         float inv_f = 0.0f;
         if (p.post) {
-            float s[1] = {slab_fold(sf, n, Square())};
+            float s[1] = {slab_fold(sf, lanes, n, Square())};
             slab_roots<T, 1>(s, gb, phase, n);
             inv_f = rms_inv(s[0], nf, p.eps);
         }
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         }
         if (p.pre) {
             __syncwarp();
-            float s[1] = {slab_fold(sx, n, Square())};
+            float s[1] = {slab_fold(sx, lanes, n, Square())};
             slab_roots<T, 1>(s, gb, phase, n);
             const float inv_y = rms_inv(s[0], nf, p.eps);
             float *hr = p.h + row * p.ldh;
@@ -405,7 +418,7 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
 
 // Resident CTAs per SM the row kernel asks the compiler for.
 template <int T>
-constexpr int kEdgeBackBlocks = 512 / T;
+constexpr int kEdgeBackBlocks = 448 / T;
 
 // dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
 // after the block.  Q8: y comes in 8 bits, and h may be written again.
@@ -414,6 +427,7 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
     extern __shared__ float4 stage_mem[];
     __shared__ GroupBuf<T, 2> gb2;
     __shared__ GroupBuf<T, 1> gb1;
+    __shared__ float4 lanes[T / 4];
     int phase1 = 0, phase2 = 0;
     constexpr int Q = T * RUN / 4;
     float4 *sy = stage_mem, *sh = sy + Q, *sf = sh + Q;
@@ -436,9 +450,9 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
         cp_async_wait<0>();
         __syncwarp();
         float r2[2] = {0.0f, 0.0f};
-        if (p.dh) r2[0] = slab_fold(sy, n, Square());
+        if (p.dh) r2[0] = slab_fold(sy, lanes, n, Square());
         if constexpr (F) {
-            if (p.post) r2[1] = slab_fold(sf, n, Square());
+            if (p.post) r2[1] = slab_fold(sf, lanes, n, Square());
         }
         slab_roots<T, 2>(r2, gb2, phase2, n);
         const float inv_y = rms_inv(r2[0], nf, p.eps), inv_f = rms_inv(r2[1], nf, p.eps);
@@ -456,26 +470,24 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
             for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(p.pre, k, n);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float4 xh = mul4(stage_load<VEC>(sy, k), inv_y);
+                e[k] = mul4(stage_load<VEC>(sy, k), inv_y);
                 if constexpr (Q8) {
-                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, n, mul4(xh, g[k]));
+                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, n, mul4(e[k], g[k]));
                 }
                 g[k] = mul4(stage_load<VEC>(sh, k), g[k]);
-                stage_store<VEC>(sh, k, mul4(g[k], xh));
+                stage_store<VEC>(sh, k, mul4(g[k], e[k]));
             }
-            // only gy stays in registers over the fold
             __syncwarp();
-            float r1[1] = {slab_fold(sh, n, Ident())};
+            float r1[1] = {slab_fold(sh, lanes, n, Ident())};
             slab_roots<T, 1>(r1, gb1, phase1, n);
             const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                e[k] = mul4(sub4(g[k], mul4(mul4(stage_load<VEC>(sy, k), inv_y), c)), inv_y);
+            for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(g[k], mul4(e[k], c)), inv_y);
         }
         if (dyr) {
             float4 d[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = row_load<VEC>(dyr, k, n);
+            for (int k = 0; k < 8; ++k) d[k] = row_load<VEC, false>(dyr, k, n);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e[k] = p.dh ? add4(e[k], d[k]) : d[k];
         }
@@ -506,15 +518,15 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     e[k] = mul4(e[k], g[k]);
-                    stage_store<VEC>(sh, k, mul4(e[k], mul4(stage_load<VEC>(sf, k), inv_f)));
+                    g[k] = mul4(stage_load<VEC>(sf, k), inv_f);
+                    stage_store<VEC>(sh, k, mul4(e[k], g[k]));
                 }
                 __syncwarp();
-                float r1[1] = {slab_fold(sh, n, Ident())};
+                float r1[1] = {slab_fold(sh, lanes, n, Ident())};
                 slab_roots<T, 1>(r1, gb1, phase1, n);
                 const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    e[k] = mul4(sub4(e[k], mul4(mul4(stage_load<VEC>(sf, k), inv_f), c)), inv_f);
+                for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, k, n, e[k]);
