@@ -11,12 +11,17 @@
 // traffic changes: forward 16 bytes an element (x, f in; y, h out) instead of
 // 36, backward 24 (y, f, dy, dh in; dx, df out) plus what the column sums read.
 //
-// Row kernels: T threads a row, a warp for each slab of 1024 columns.  The
-// rows arrive by cp.async in the swizzled stage; element-wise steps take the
-// slab in memory order (coalesced, parameters straight from the cache) and the
-// tree takes it in run order, a run a lane, both from the stage.  Memory order
-// keeps the parameters out of registers and shared memory, so more rows are
-// in flight per SM than with a run's values held by the lane that folds it.
+// Row kernels: teams of T threads, a row a team at a time, a warp for each slab
+// of 1024 columns.  The rows arrive by cp.async in a swizzled stage; element-wise
+// steps take a slab in memory order (coalesced) and the tree takes it in run
+// order, a run a lane, both from the stage.  Forward, a CTA is a team and reads
+// the gains and the gate from the caches, with the next row's copies in flight
+// (4096 x 2048: 29 us; a plain copy of as many bytes 23).  Backward, a row passes
+// three dependent sums and takes about 6 us, so what counts is how many rows are
+// in flight and how little each waits for: one CTA an SM holds as many teams as
+// fit its shared memory and, once for all of them, the gains and the gate (read
+// from the caches they were a third of a row's time: 8192 x 2048, 84 -> 67 us; a
+// plain copy of as many bytes 60).
 //
 // Column sums (the gradients of the gains and the gate) need their terms
 // folded in row order, a run of 32 rows at a time: a second kernel, a thread
@@ -39,48 +44,38 @@ constexpr int64_t MAX_FOLD_ROWS = RUN * RUN;    // run results the last fold tak
 // ------------------------------------------------------------- row slabs ----
 // A warp's slab: step k (of 8) covers four values a lane.  With 16-byte rows
 // (VEC) they are columns 128k + 4*lane .. + 3 of the slab; else columns
-// 128k + lane + {0, 32, 64, 96}.
+// 128k + lane + {0, 32, 64, 96}.  `slab` is the slab's first column.
 
 template <bool VEC>
-__device__ __forceinline__ int slab_col(int k, int t) {
-    const int lane = threadIdx.x & 31, slab = (threadIdx.x >> 5) * 1024;
+__device__ __forceinline__ int slab_col(int slab, int k, int t) {
+    const int lane = threadIdx.x & 31;
     return VEC ? slab + 128 * k + 4 * lane + t : slab + 128 * k + 32 * t + lane;
 }
 
 // Loads take no branch, so that a slab's are all in flight together: a column
 // past the row's end reads column 0 instead, and its result is never stored or
 // folded.  n is a multiple of 4 with VEC.
-// CONST: nothing in the kernel writes the row.
-template <bool VEC, bool CONST = true>
-__device__ __forceinline__ float4 row_load(const float *row, int k, int n) {
-    const int c = slab_col<VEC>(k, 0);
-    auto one = [&](int i) { return CONST ? __ldg(row + (i < n ? i : 0)) : row[i < n ? i : 0]; };
+template <bool VEC>
+__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int slab, int k, int n) {
+    const int c = slab_col<VEC>(slab, k, 0);
     if constexpr (VEC) {
-        const float4 *q = reinterpret_cast<const float4 *>(row + (c < n ? c : 0));
-        return CONST ? __ldg(q) : *q;
+        return __ldg(reinterpret_cast<const float4 *>(row + (c < n ? c : 0)));
     } else {
-        return make_float4(one(c), one(c + 32), one(c + 64), one(c + 96));
+        return make_float4(__ldg(row + (c < n ? c : 0)), __ldg(row + (c + 32 < n ? c + 32 : 0)),
+                           __ldg(row + (c + 64 < n ? c + 64 : 0)), __ldg(row + (c + 96 < n ? c + 96 : 0)));
     }
 }
 
 // Asks for the warp's slab of a parameter row (may be null) ahead of its use.
-template <bool VEC>
-__device__ __forceinline__ void row_prefetch(const float *row, int n) {
+__device__ __forceinline__ void row_prefetch(const float *row, int slab, int n) {
     if (!row) return;
-    const int c = (threadIdx.x >> 5) * 1024 + 32 * (threadIdx.x & 31);     // a 128-byte line a lane
+    const int c = slab + 32 * (threadIdx.x & 31);              // a 128-byte line a lane
     if (c < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
 }
 
-// The same for a row that is read once: into L2.
-__device__ __forceinline__ void row_prefetch_l2(const float *row, int n) {
-    if (!row) return;
-    const int c = (threadIdx.x >> 5) * 1024 + 32 * (threadIdx.x & 31);
-    if (c < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
-}
-
 template <bool VEC>
-__device__ __forceinline__ void row_store(float *row, int k, int n, float4 v) {
-    const int c = slab_col<VEC>(k, 0);
+__device__ __forceinline__ void row_store(float *row, int slab, int k, int n, float4 v) {
+    const int c = slab_col<VEC>(slab, k, 0);
     if constexpr (VEC) {
         if (c < n) *reinterpret_cast<float4 *>(row + c) = v;
     } else {
@@ -93,58 +88,74 @@ __device__ __forceinline__ void row_store(float *row, int k, int n, float4 v) {
 
 // A slab step's place in the stage.
 template <bool VEC>
-__device__ __forceinline__ int stage_float(int k, int t) {
-    const int lane = threadIdx.x & 31, u0 = (threadIdx.x >> 5) * 32 + 4 * k;
+__device__ __forceinline__ int stage_float(int slab, int k, int t) {
+    const int lane = threadIdx.x & 31, u0 = slab / RUN + 4 * k;
     if constexpr (VEC) return 4 * stage_slot(u0 + (lane >> 3), lane & 7) + t;
     else return 4 * stage_slot(u0 + t, lane >> 2) + (lane & 3);
 }
 
 template <bool VEC>
-__device__ __forceinline__ float4 stage_load(const float4 *stage, int k) {
+__device__ __forceinline__ float4 stage_load(const float4 *stage, int slab, int k) {
     const float *s = reinterpret_cast<const float *>(stage);
-    if constexpr (VEC) return *reinterpret_cast<const float4 *>(s + stage_float<VEC>(k, 0));
+    if constexpr (VEC) return *reinterpret_cast<const float4 *>(s + stage_float<VEC>(slab, k, 0));
     else
-        return make_float4(s[stage_float<VEC>(k, 0)], s[stage_float<VEC>(k, 1)], s[stage_float<VEC>(k, 2)],
-                           s[stage_float<VEC>(k, 3)]);
+        return make_float4(s[stage_float<VEC>(slab, k, 0)], s[stage_float<VEC>(slab, k, 1)],
+                           s[stage_float<VEC>(slab, k, 2)], s[stage_float<VEC>(slab, k, 3)]);
 }
 
 template <bool VEC>
-__device__ __forceinline__ void stage_store(float4 *stage, int k, float4 v) {
+__device__ __forceinline__ void stage_store(float4 *stage, int slab, int k, float4 v) {
     float *s = reinterpret_cast<float *>(stage);
     if constexpr (VEC) {
-        *reinterpret_cast<float4 *>(s + stage_float<VEC>(k, 0)) = v;
+        *reinterpret_cast<float4 *>(s + stage_float<VEC>(slab, k, 0)) = v;
     } else {
-        s[stage_float<VEC>(k, 0)] = v.x;
-        s[stage_float<VEC>(k, 1)] = v.y;
-        s[stage_float<VEC>(k, 2)] = v.z;
-        s[stage_float<VEC>(k, 3)] = v.w;
+        s[stage_float<VEC>(slab, k, 0)] = v.x;
+        s[stage_float<VEC>(slab, k, 1)] = v.y;
+        s[stage_float<VEC>(slab, k, 2)] = v.z;
+        s[stage_float<VEC>(slab, k, 3)] = v.w;
     }
 }
 
 // Starts the copy of the warp's slab of a row into the stage.
 template <bool VEC>
-__device__ __forceinline__ void stage_row(float4 *stage, const float *__restrict__ row, int n) {
+__device__ __forceinline__ void stage_row(float4 *stage, const float *row, int slab, int n) {
     float *s = reinterpret_cast<float *>(stage);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if constexpr (VEC) {
-            const int c = slab_col<VEC>(k, 0);
-            if (c < n) cp_async_16(s + stage_float<VEC>(k, 0), row + c, 16u);
+            const int c = slab_col<VEC>(slab, k, 0);
+            if (c < n) cp_async_16(s + stage_float<VEC>(slab, k, 0), row + c, 16u);
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int c = slab_col<VEC>(k, t);
-                if (c < n) cp_async_4(s + stage_float<VEC>(k, t), row + c, 4u);
+                const int c = slab_col<VEC>(slab, k, t);
+                if (c < n) cp_async_4(s + stage_float<VEC>(slab, k, t), row + c, 4u);
             }
         }
     }
 }
 
+// The CTA's copy of a parameter row (null: none), in memory order, and a slab
+// step of it.  A barrier follows the copies.
+template <int T>
+__device__ __forceinline__ void param_copy(float *dst, const float *src, int n) {
+    if (!src) return;
+    for (int c = threadIdx.x; c < T * RUN; c += blockDim.x) dst[c] = c < n ? __ldg(src + c) : 0.0f;
+}
+
+template <bool VEC>
+__device__ __forceinline__ float4 param_load(const float *param, int slab, int k) {
+    const int c = slab_col<VEC>(slab, k, 0);
+    if constexpr (VEC) return *reinterpret_cast<const float4 *>(param + c);
+    else return make_float4(param[c], param[c + 32], param[c + 64], param[c + 96]);
+}
+
 // The warp's group result of the tree over the staged values f(v): each lane
-// folds its run, every lane folds the lanes' results in order.
+// folds its run, every lane folds the lanes' results in order.  `lanes`: 32
+// floats of the warp's own.
 template <class F>
-__device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, int n, F f) {
-    const int u = threadIdx.x, warp0 = u & ~31;
+__device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, int slab, int n, F f) {
+    const int lane = threadIdx.x & 31, u = slab / RUN + lane;
     const int len = min(RUN, n - u * RUN);                 // 0 or less past the end
     float v[RUN];
 #pragma unroll
@@ -161,17 +172,16 @@ __device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, i
         for (int i = 1; i < RUN; ++i)
             if (i < len) acc = __fadd_rn(acc, f(v[i]));
     }
-    const int have = (n + RUN - 1) / RUN - warp0;     // runs present from this warp on
+    const int have = (n + RUN - 1) / RUN - slab / RUN;     // runs present from this warp on
     // the lanes' results to every lane: a store and eight broadcast reads (31
     // shuffles cost the shared-memory pipe three times as much)
-    float4 *mine = lanes + (warp0 >> 2);
     __syncwarp();
-    reinterpret_cast<float *>(mine)[threadIdx.x & 31] = acc;
+    reinterpret_cast<float *>(lanes)[lane] = acc;
     __syncwarp();
     float r[RUN];
 #pragma unroll
     for (int c = 0; c < RUN / 4; ++c) {
-        const float4 w = mine[c];
+        const float4 w = lanes[c];
         r[4 * c] = w.x; r[4 * c + 1] = w.y; r[4 * c + 2] = w.z; r[4 * c + 3] = w.w;
     }
     float g = r[0];
@@ -186,27 +196,23 @@ __device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, i
     return g;
 }
 
-// The tree's root from the warps' group results (one barrier).  gbuf has two
-// halves used in turn, so that a thread still reading one reduction's half
-// never races the next one's writes.
+// The tree's roots from the warps' group results (one barrier of the team).
+// buf has two halves used in turn, so that a thread still reading one
+// reduction's half never races the next one's writes.
 template <int T, int NV>
-struct GroupBuf {
-    float g[2][NV][8];
-};
-
-template <int T, int NV>
-__device__ __forceinline__ void slab_roots(float (&v)[NV], GroupBuf<T, NV> &gb, int &phase, int n) {
+__device__ __forceinline__ void slab_roots(float (&v)[NV], float (&buf)[2][2][8], int &phase, int team, int n) {
     if constexpr (T > 32) {
+        const int warp = (threadIdx.x % T) >> 5;
         if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) gb.g[phase][j][threadIdx.x >> 5] = v[j];
+            for (int j = 0; j < NV; ++j) buf[phase][j][warp] = v[j];
         }
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(T) : "memory");
         const int G = (n + 1023) / 1024;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            v[j] = gb.g[phase][j][0];
-            for (int k = 1; k < G; ++k) v[j] = __fadd_rn(v[j], gb.g[phase][j][k]);
+            v[j] = buf[phase][j][0];
+            for (int k = 1; k < G; ++k) v[j] = __fadd_rn(v[j], buf[phase][j][k]);
         }
         phase ^= 1;
     }
@@ -231,6 +237,13 @@ struct Ident {
     __device__ __forceinline__ float operator()(float x) const { return x; }
 };
 
+// Teams of a CTA whose rows take STAGES stages and whose parameters PARAMS: what
+// 224 KB hold, and 15 barriers at most.
+template <int T, int STAGES, int PARAMS, int MAX_THREADS>
+constexpr int kTeams = std::min({(224 * 1024 / (T * RUN * 4) - PARAMS) / STAGES, MAX_THREADS / T, T > 32 ? 15 : 64});
+template <int T, int STAGES, int PARAMS, int TEAMS>
+constexpr size_t kTeamSmem = size_t(T) * RUN * 4 * (PARAMS + STAGES * TEAMS);
+
 // --------------------------------------------------------------- forward ----
 
 struct EdgeArgs {
@@ -251,8 +264,10 @@ constexpr bool kEdgePrefetch = T <= 128;
 template <int T, bool VEC>
 __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     extern __shared__ float4 stage_mem[];
-    __shared__ GroupBuf<T, 1> gb;
-    __shared__ float4 lanes[T / 4];
+    __shared__ float roots[2][2][8];
+    __shared__ float4 lane_mem[T / 4];
+    float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
+    const int slab = (threadIdx.x >> 5) * 1024;
     int phase = 0;
     constexpr int Q = T * RUN / 4;
     constexpr bool PF = kEdgePrefetch<T>;
@@ -261,8 +276,8 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     int cur = 0;
     int64_t row = blockIdx.x;
     if (row < p.rows) {
-        stage_row<VEC>(stage_mem, p.f + row * p.ldf, n);
-        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, n);
+        stage_row<VEC>(stage_mem, p.f + row * p.ldf, slab, n);
+        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, slab, n);
     }
     cp_async_commit();
     for (; row < p.rows; row += gridDim.x) {
@@ -271,23 +286,23 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         if constexpr (PF) {
             cur ^= 1;
             if (next < p.rows) {
-                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, n);
-                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, n);
+                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, slab, n);
+                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
         const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
         if (row == blockIdx.x) {            // the parameters are on their way while the first row is
-            row_prefetch<VEC>(p.post, n);
-            row_prefetch<VEC>(gate, n);
-            row_prefetch<VEC>(p.pre, n);
+            row_prefetch(p.post, slab, n);
+            row_prefetch(gate, slab, n);
+            row_prefetch(p.pre, slab, n);
         }
         cp_async_wait<PF ? 1 : 0>();
         __syncwarp();
         float inv_f = 0.0f;
         if (p.post) {
-            float s[1] = {slab_fold(sf, lanes, n, Square())};
-            slab_roots<T, 1>(s, gb, phase, n);
+            float s[1] = {slab_fold(sf, lanes, slab, n, Square())};
+            slab_roots<T, 1>(s, roots, phase, 0, n);
             inv_f = rms_inv(s[0], nf, p.eps);
         }
         float *yr = p.y + row * p.ldy;
@@ -296,39 +311,39 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
             float4 w[4], g[4];
             if (p.post) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = row_load<VEC>(p.post, b + k, n);
+                for (int k = 0; k < 4; ++k) w[k] = row_load<VEC>(p.post, slab, b + k, n);
             }
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] = row_load<VEC>(gate, b + k, n);
+                for (int k = 0; k < 4; ++k) g[k] = row_load<VEC>(gate, slab, b + k, n);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float4 v = stage_load<VEC>(sf, b + k);
+                float4 v = stage_load<VEC>(sf, slab, b + k);
                 if (p.post) v = mul4(mul4(v, inv_f), w[k]);
                 if (gate) v = mul4(v, g[k]);
-                v = add4(stage_load<VEC>(sx, b + k), mul4(v, p.alpha));
-                row_store<VEC>(yr, b + k, n, v);
-                if (p.pre) stage_store<VEC>(sx, b + k, v);
+                v = add4(stage_load<VEC>(sx, slab, b + k), mul4(v, p.alpha));
+                row_store<VEC>(yr, slab, b + k, n, v);
+                if (p.pre) stage_store<VEC>(sx, slab, b + k, v);
             }
         }
         if (p.pre) {
             __syncwarp();
-            float s[1] = {slab_fold(sx, lanes, n, Square())};
-            slab_roots<T, 1>(s, gb, phase, n);
+            float s[1] = {slab_fold(sx, lanes, slab, n, Square())};
+            slab_roots<T, 1>(s, roots, phase, 0, n);
             const float inv_y = rms_inv(s[0], nf, p.eps);
             float *hr = p.h + row * p.ldh;
             float4 w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = row_load<VEC>(p.pre, k, n);
+            for (int k = 0; k < 8; ++k) w[k] = row_load<VEC>(p.pre, slab, k, n);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC>(hr, k, n, mul4(mul4(stage_load<VEC>(sx, k), inv_y), w[k]));
+            for (int k = 0; k < 8; ++k) row_store<VEC>(hr, slab, k, n, mul4(mul4(stage_load<VEC>(sx, slab, k), inv_y), w[k]));
         }
         __syncwarp();                       // the stage is read before it is filled again
         if constexpr (!PF) {
             if (next < p.rows) {
-                stage_row<VEC>(sf, p.f + next * p.ldf, n);
-                stage_row<VEC>(sx, p.x + next * p.ldx, n);
+                stage_row<VEC>(sf, p.f + next * p.ldf, slab, n);
+                stage_row<VEC>(sx, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
@@ -398,8 +413,8 @@ struct EdgeBackArgs {
 };
 
 template <bool VEC>
-__device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, int k, int n) {
-    const int c = slab_col<VEC>(k, 0);
+__device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, int slab, int k, int n) {
+    const int c = slab_col<VEC>(slab, k, 0);
     const int8_t *q = p.q + row * p.ldq;
     const float *s = p.s + row * p.lds;
     if constexpr (VEC) {                   // a group is a multiple of 4 columns
@@ -416,47 +431,56 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
     }
 }
 
-// Resident CTAs per SM the row kernel asks the compiler for.
-template <int T>
-constexpr int kEdgeBackBlocks = 448 / T;
+// Stages of a row: y, dh, dy, and f with F; parameters: pre, and post and the
+// gate with F (whose rows want 160 registers a thread).
+template <int T, bool F>
+constexpr int kBackTeams = F ? kTeams<T, 4, 3, 384> : kTeams<T, 3, 1, 512>;
 
 // dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
 // after the block.  Q8: y comes in 8 bits, and h may be written again.
 template <int T, bool VEC, bool Q8, bool F>
-__global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(EdgeBackArgs p) {
-    extern __shared__ float4 stage_mem[];
-    __shared__ GroupBuf<T, 2> gb2;
-    __shared__ GroupBuf<T, 1> gb1;
-    __shared__ float4 lanes[T / 4];
-    int phase1 = 0, phase2 = 0;
-    constexpr int Q = T * RUN / 4;
-    float4 *sy = stage_mem, *sh = sy + Q, *sf = sh + Q;
-    const int n = int(p.n);
+__global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(EdgeBackArgs p) {
+    constexpr int Q = T * RUN / 4, TEAMS = kBackTeams<T, F>;
+    extern __shared__ float4 smem[];
+    __shared__ float roots[TEAMS][2][2][8];
+    __shared__ float4 lane_mem[TEAMS * T / 4];
+    const int n = int(p.n), team = threadIdx.x / T, slab = ((threadIdx.x % T) >> 5) * 1024;
     const float nf = float(p.n);
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    float *pre = reinterpret_cast<float *>(smem), *post = pre + T * RUN, *gate1 = post + T * RUN;
+    float4 *sy = smem + (F ? 3 : 1) * Q + team * Q * (F ? 4 : 3), *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
+    float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
+    const bool one_gate = F && p.gate && p.gate_rows >= p.rows;
+    param_copy<T>(pre, p.pre, n);
+    if constexpr (F) {
+        param_copy<T>(post, p.post, n);
+        param_copy<T>(gate1, one_gate ? p.gate : nullptr, n);
+    }
+    __syncthreads();
+    int phase = 0;
+    // rows go to the SMs first, then to their teams
+    for (int64_t row = int64_t(team) * gridDim.x + blockIdx.x; row < p.rows; row += int64_t(gridDim.x) * TEAMS) {
         if (p.dh) {
-            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, n);
-            stage_row<VEC>(sh, p.dh + row * p.lddh, n);
+            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, slab, n);
+            stage_row<VEC>(sh, p.dh + row * p.lddh, slab, n);
         }
-        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, n);
+        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, slab, n);
         cp_async_commit();
-        const float *dyr = p.dy ? p.dy + row * p.lddy : nullptr;
-        row_prefetch_l2(dyr, n);
-        row_prefetch<VEC>(p.dh ? p.pre : nullptr, n);
+        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, slab, n);
+        cp_async_commit();
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, k, row8_load<VEC>(p, row, k, n));
+            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, slab, k, row8_load<VEC>(p, row, slab, k, n));
         }
-        cp_async_wait<0>();
+        cp_async_wait<1>();
         __syncwarp();
         float r2[2] = {0.0f, 0.0f};
-        if (p.dh) r2[0] = slab_fold(sy, lanes, n, Square());
+        if (p.dh) r2[0] = slab_fold(sy, lanes, slab, n, Square());
         if constexpr (F) {
-            if (p.post) r2[1] = slab_fold(sf, lanes, n, Square());
+            if (p.post) r2[1] = slab_fold(sf, lanes, slab, n, Square());
         }
-        slab_roots<T, 2>(r2, gb2, phase2, n);
+        slab_roots<T, 2>(r2, roots[team], phase, team, n);
         const float inv_y = rms_inv(r2[0], nf, p.eps), inv_f = rms_inv(r2[1], nf, p.eps);
-        if (threadIdx.x == 0) {
+        if (threadIdx.x % T == 0) {
             if (p.dh) p.inv_y[row] = inv_y;
             if constexpr (F) {
                 if (p.post) p.inv_f[row] = inv_f;
@@ -467,72 +491,69 @@ __global__ void __launch_bounds__(T, kEdgeBackBlocks<T>) edge_backward_kernel(Ed
             // sh <- gy * xh, summed from there
             float4 g[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(p.pre, k, n);
-#pragma unroll
             for (int k = 0; k < 8; ++k) {
-                e[k] = mul4(stage_load<VEC>(sy, k), inv_y);
+                g[k] = param_load<VEC>(pre, slab, k);
+                e[k] = mul4(stage_load<VEC>(sy, slab, k), inv_y);
                 if constexpr (Q8) {
-                    if (p.h) row_store<VEC>(p.h + row * p.ldh, k, n, mul4(e[k], g[k]));
+                    if (p.h) row_store<VEC>(p.h + row * p.ldh, slab, k, n, mul4(e[k], g[k]));
                 }
-                g[k] = mul4(stage_load<VEC>(sh, k), g[k]);
-                stage_store<VEC>(sh, k, mul4(g[k], e[k]));
+                g[k] = mul4(stage_load<VEC>(sh, slab, k), g[k]);
+                stage_store<VEC>(sh, slab, k, mul4(g[k], e[k]));
             }
             __syncwarp();
-            float r1[1] = {slab_fold(sh, lanes, n, Ident())};
-            slab_roots<T, 1>(r1, gb1, phase1, n);
+            float r1[1] = {slab_fold(sh, lanes, slab, n, Ident())};
+            slab_roots<T, 1>(r1, roots[team], phase, team, n);
             const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
             for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(g[k], mul4(e[k], c)), inv_y);
         }
-        if (dyr) {
-            float4 d[8];
+        cp_async_wait<0>();
+        __syncwarp();
+        if (p.dy) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = row_load<VEC, false>(dyr, k, n);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = p.dh ? add4(e[k], d[k]) : d[k];
-        }
-        if constexpr (F) {
-            row_prefetch<VEC>(p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr, n);
-            row_prefetch<VEC>(p.post, n);
+            for (int k = 0; k < 8; ++k) {
+                const float4 d = stage_load<VEC>(sr, slab, k);
+                e[k] = p.dh ? add4(e[k], d) : d;
+            }
         }
         float *dxr = p.dx + row * p.lddx;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, k, n, e[k]);
+        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, slab, k, n, e[k]);
         if constexpr (F) {
             float *dfr = p.df + row * p.lddf;
-            const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
+            const float *gate = p.gate && !one_gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
             float4 g[8];
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(gate, k, n);
+                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(gate, slab, k, n);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 e[k] = mul4(e[k], p.alpha);
                 if (gate) e[k] = mul4(e[k], g[k]);
+                else if (one_gate) e[k] = mul4(e[k], param_load<VEC>(gate1, slab, k));
             }
             if (p.post) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(p.post, k, n);
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    e[k] = mul4(e[k], g[k]);
-                    g[k] = mul4(stage_load<VEC>(sf, k), inv_f);
-                    stage_store<VEC>(sh, k, mul4(e[k], g[k]));
+                    e[k] = mul4(e[k], param_load<VEC>(post, slab, k));
+                    g[k] = mul4(stage_load<VEC>(sf, slab, k), inv_f);
+                    stage_store<VEC>(sh, slab, k, mul4(e[k], g[k]));
                 }
                 __syncwarp();
-                float r1[1] = {slab_fold(sh, lanes, n, Ident())};
-                slab_roots<T, 1>(r1, gb1, phase1, n);
+                float r1[1] = {slab_fold(sh, lanes, slab, n, Ident())};
+                slab_roots<T, 1>(r1, roots[team], phase, team, n);
                 const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, k, n, e[k]);
+            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, slab, k, n, e[k]);
         }
         __syncwarp();
     }
+    cp_async_wait<0>();
 }
 
 // Rows of more than 8192 values: each phase reads the row again.
@@ -737,7 +758,7 @@ struct FoldArgs {
 };
 
 // The two levels of the tree over up to 1024 run results: 32 columns a CTA, a
-// warp for each run of 32 results.
+// warp for each run of 32 results (as many as the longest sum has).
 __global__ void __launch_bounds__(1024) edge_fold_kernel(FoldArgs a) {
     __shared__ float part[RUN][RUN + 1];
     const FoldSet s = a.s[blockIdx.z];
@@ -832,6 +853,17 @@ struct Workspace {
     }
 };
 
+// One CTA an SM at most (a CTA's teams fill it), a row a team at least.
+template <class Kern, class Args>
+int launch_teams(Kern kern, int threads, size_t smem, const Args &a, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return set_cuda_error(e);
+    DeviceInfo di;
+    const int64_t sms = current_device_info(&di) == REPOPS_OK ? di.sms : 152;
+    kern<<<unsigned(std::min(a.rows, sms)), threads, smem, s>>>(a);
+    return check_launch();
+}
+
 template <bool VEC>
 int launch_forward(const EdgeArgs &a, cudaStream_t s) {
     auto go = [&](auto kern, int T, bool pf) {
@@ -857,15 +889,19 @@ int launch_long(Kern kern, const Args &a, int64_t rows, int64_t n, cudaStream_t 
     return check_launch();
 }
 
+template <int T, bool VEC, bool Q8, bool F>
+int launch_rows_t(const EdgeBackArgs &a, cudaStream_t s) {
+    constexpr int teams = kBackTeams<T, F>;
+    return launch_teams(edge_backward_kernel<T, VEC, Q8, F>, T * teams,
+                        F ? kTeamSmem<T, 4, 3, teams> : kTeamSmem<T, 3, 1, teams>, a, s);
+}
+
 template <bool VEC, bool Q8, bool F>
 int launch_rows(const EdgeBackArgs &a, cudaStream_t s) {
-    auto go = [&](auto kern, int T) {
-        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (F ? 3 : 2), a.rows, s, a);
-    };
-    if (a.n <= 1024) return go(edge_backward_kernel<32, VEC, Q8, F>, 32);
-    if (a.n <= 2048) return go(edge_backward_kernel<64, VEC, Q8, F>, 64);
-    if (a.n <= 4096) return go(edge_backward_kernel<128, VEC, Q8, F>, 128);
-    return go(edge_backward_kernel<256, VEC, Q8, F>, 256);
+    if (a.n <= 1024) return launch_rows_t<32, VEC, Q8, F>(a, s);
+    if (a.n <= 2048) return launch_rows_t<64, VEC, Q8, F>(a, s);
+    if (a.n <= 4096) return launch_rows_t<128, VEC, Q8, F>(a, s);
+    return launch_rows_t<256, VEC, Q8, F>(a, s);
 }
 
 template <bool Q8, bool F>
@@ -924,7 +960,7 @@ int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_
     FoldArgs f{};
     f.n = e.n;
     int sets = 0;
-    int64_t blocks = 1;
+    int64_t blocks = 1, most = 1;
     auto add = [&](const float *in, float *out, int64_t nb, int64_t runs, int64_t ldo) {
         // one further level first for more than 1024 run results (twice for
         // more than 32768 of them, and so on): a column sum's pass per block
@@ -941,13 +977,14 @@ int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_
         }
         f.s[sets++] = FoldSet{in, out, nb, runs, ldo};
         blocks = std::max(blocks, nb);
+        most = std::max(most, runs);
     };
     if (dpre) add(ppre, dpre, 1, sc.runs, e.n);
     if (dpost) add(ppost, dpost, 1, sc.runs, e.n);
     if (dgate && sc.gate_per > 1) add(pgate, dgate, gates, sc.gate_per, lddgate);
     if (rc != REPOPS_OK || sets == 0) return rc;
     const dim3 grid(unsigned(ceil_div(e.n, RUN)), unsigned(std::min<int64_t>(blocks, 65535)), unsigned(sets));
-    edge_fold_kernel<<<grid, 1024, 0, s>>>(f);
+    edge_fold_kernel<<<grid, unsigned(ceil_div(most, RUN) * 32), 0, s>>>(f);
     return check_launch();
 }
 
