@@ -73,11 +73,17 @@ __device__ __forceinline__ void row_prefetch(const float *row, int slab, int n) 
     if (c < n) asm volatile("prefetch.global.L1 [%0];" ::"l"(row + c));
 }
 
-template <bool VEC>
+// KEEP: the row is read again soon (by the column sums); else its lines make
+// way first.
+template <bool VEC, bool KEEP = true>
 __device__ __forceinline__ void row_store(float *row, int slab, int k, int n, float4 v) {
     const int c = slab_col<VEC>(slab, k, 0);
     if constexpr (VEC) {
-        if (c < n) *reinterpret_cast<float4 *>(row + c) = v;
+        if constexpr (KEEP) {
+            if (c < n) *reinterpret_cast<float4 *>(row + c) = v;
+        } else {
+            if (c < n) __stcs(reinterpret_cast<float4 *>(row + c), v);
+        }
     } else {
         if (c < n) row[c] = v.x;
         if (c + 32 < n) row[c + 32] = v.y;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
                 g[k] = param_load<VEC>(pre, slab, k);
                 e[k] = mul4(stage_load<VEC>(sy, slab, k), inv_y);
                 if constexpr (Q8) {
-                    if (p.h) row_store<VEC>(p.h + row * p.ldh, slab, k, n, mul4(e[k], g[k]));
+                    if (p.h) row_store<VEC, false>(p.h + row * p.ldh, slab, k, n, mul4(e[k], g[k]));
                 }
                 g[k] = mul4(stage_load<VEC>(sh, slab, k), g[k]);
                 stage_store<VEC>(sh, slab, k, mul4(g[k], e[k]));
@@ -549,7 +555,7 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
                 for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC>(dfr, slab, k, n, e[k]);
+            for (int k = 0; k < 8; ++k) row_store<VEC, false>(dfr, slab, k, n, e[k]);
         }
         __syncwarp();
     }
@@ -669,7 +675,8 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
     if (c >= p.n) return;
     Cols<W> post{};
     if (GATE && p.post) post = cols_load<W>(p.post + c);
-    for (int64_t run = blockIdx.y; run < a.runs; run += gridDim.y) {
+    // the last rows first: the row kernel has just left them in L2
+    for (int64_t run = a.runs - 1 - blockIdx.y; run >= 0; run -= gridDim.y) {
         const int64_t b = run / a.block_runs, first = b * a.block_rows + (run - b * a.block_runs) * RUN;
         const int rows = int(imin64(RUN, (b + 1) * a.block_rows - first));
         Cols<W> s_pre, s_post, s_gate, gate{};
