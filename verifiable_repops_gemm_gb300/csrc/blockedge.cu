@@ -671,6 +671,7 @@ template <int W, bool Q8, bool PRE, bool POST, bool GATE>
 __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
     const EdgeBackArgs &p = a.e;
     constexpr int B = 8;                 // rows loaded at once; RUN is a multiple
+    grid_release();
     const int64_t c = (blockIdx.x * int64_t(128) + threadIdx.x) * W;
     if (c >= p.n) return;
     Cols<W> post{};
@@ -772,6 +773,7 @@ __global__ void __launch_bounds__(1024) edge_fold_kernel(FoldArgs a) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = blockIdx.x * int64_t(RUN) + tx;
     const int groups = int((s.runs + RUN - 1) / RUN);
+    grid_wait();
     for (int64_t b = blockIdx.y; b < s.blocks; b += gridDim.y) {
         const int64_t r0 = int64_t(ty) * RUN, r1 = imin64(r0 + RUN, s.runs);
         if (c < a.n && r0 < r1) {
@@ -991,8 +993,7 @@ int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_
     if (dgate && sc.gate_per > 1) add(pgate, dgate, gates, sc.gate_per, lddgate);
     if (rc != REPOPS_OK || sets == 0) return rc;
     const dim3 grid(unsigned(ceil_div(e.n, RUN)), unsigned(std::min<int64_t>(blocks, 65535)), unsigned(sets));
-    edge_fold_kernel<<<grid, unsigned(ceil_div(most, RUN) * 32), 0, s>>>(f);
-    return check_launch();
+    return launch_behind(edge_fold_kernel, grid, unsigned(ceil_div(most, RUN) * 32), 0, s, f);
 }
 
 }  // namespace

@@ -237,6 +237,7 @@ constexpr int kChunkSteps = 16;           // k-steps between two drains: 1024 of
 // values, zeros past K: 16 values a thread.
 template <bool VEC>
 __global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half *__restrict__ out) {
+    grid_release();
     const int64_t per = Kp / 16, items = (p.M + p.N) * per, stride = int64_t(gridDim.x) * 256;
     for (int64_t it = blockIdx.x * int64_t(256) + threadIdx.x; it < items; it += stride) {
         const int64_t r = it / per, k = (it - r * per) * 16;
@@ -373,6 +374,7 @@ __device__ __forceinline__ void tile_kernel(const CUtensorMap &map_a, const CUte
     if constexpr (CTAS == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    grid_wait();                                               // the widened operands
 
     // Every wait gives up after its limit: the role that gave up sets the
     // status word, waits (again with a limit) for its own copies or products in
@@ -665,9 +667,8 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     if (e != cudaSuccess) return set_cuda_error(e);
     const TileMap tm{int(ceil_div(a.M, BM * CTAS)), int(ceil_div(a.N, BN)), 16 / CTAS};
     const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
-    kern<<<unsigned(std::min<int64_t>(tiles, sm_count() / CTAS) * CTAS), kTileThreads, T::SMEM, s>>>(
-        ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
-    return check_launch();
+    return launch_behind(kern, dim3(unsigned(std::min<int64_t>(tiles, sm_count() / CTAS) * CTAS)), kTileThreads,
+                         T::SMEM, s, ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
 }
 
 template <int TY>

@@ -116,6 +116,29 @@ __device__ __forceinline__ bool dbg_smem(uint64_t need, unsigned *status) {
 #define REPOPS_DBG_SMEM_OK(need, status) true
 #endif
 
+// A kernel of one call launched behind another of the same call on `stream`:
+// its CTAs may take their places while the earlier kernel ends, and wait there
+// (grid_wait, before they read or write anything of it) until it has ended and
+// its writes are visible.  The earlier kernel calls grid_release.
+template <class... Params, class... Args>
+int launch_behind(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+    return e == cudaSuccess ? REPOPS_OK : set_cuda_error(e);
+}
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Limit for every device-side wait, in nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s
 
