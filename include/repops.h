@@ -1037,8 +1037,8 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
  * pool on `stream` (ALLOC when refused).
  * INVALID_ARG for negative sizes, unknown types or configs, null pointers,
  * short pitches or scratch; ALIAS when C or ws overlaps an operand or each
- * other; UNSUPPORTED for K above 131071 (acc would leave 32 bits) or more than
- * 2^30 tiles. */
+ * other; UNSUPPORTED for K above 131071 (acc would leave 32 bits), M or N above
+ * 2^31 - 1, or more than 2^30 tiles. */
 int repops_gemm_i8_config_count(void);
 int repops_gemm_i8_auto_config(int64_t M, int64_t N, int64_t K);
 uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_t N, int64_t K);

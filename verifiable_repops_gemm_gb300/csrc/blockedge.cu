@@ -30,6 +30,7 @@
 // the run results.  Writing the terms and summing them afterwards would move 8
 // bytes an element for each of the three sums instead of 16 for all.
 #include <algorithm>
+#include <atomic>
 
 #include "internal.cuh"
 #include "rows8.cuh"
@@ -873,15 +874,39 @@ int launch_teams(Kern kern, int threads, size_t smem, const Args &a, cudaStream_
     return check_launch();
 }
 
+// Resident CTAs an SM of the forward kernel, asked for once a device (0: not
+// yet): the question costs a quarter of the host's time in a call for one row.
+// The kernel's shared-memory limit belongs to the context and is set each time
+// where the default (48 KB) does not do.
+template <int T, bool VEC>
+int launch_forward_t(const EdgeArgs &a, cudaStream_t s) {
+    constexpr size_t smem = size_t(T) * RUN * 4 * (kEdgePrefetch<T> ? 4 : 2);
+    static std::atomic<int> resident[64];
+    DeviceInfo di;
+    int rc = current_device_info(&di);
+    if (rc != REPOPS_OK) return rc;
+    auto kern = edge_forward_kernel<T, VEC>;
+    int per_sm = resident[di.device].load(std::memory_order_relaxed);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return set_cuda_error(e);
+    }
+    if (per_sm == 0) {
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, T, smem);
+        if (e != cudaSuccess) return set_cuda_error(e);
+        per_sm = std::max(per_sm, 1);
+        resident[di.device].store(per_sm, std::memory_order_relaxed);
+    }
+    kern<<<unsigned(std::min<int64_t>(a.rows, int64_t(per_sm) * di.sms)), T, smem, s>>>(a);
+    return check_launch();
+}
+
 template <bool VEC>
 int launch_forward(const EdgeArgs &a, cudaStream_t s) {
-    auto go = [&](auto kern, int T, bool pf) {
-        return launch_persistent(kern, T, size_t(T) * RUN * 4 * (pf ? 4 : 2), a.rows, s, a);
-    };
-    if (a.n <= 1024) return go(edge_forward_kernel<32, VEC>, 32, kEdgePrefetch<32>);
-    if (a.n <= 2048) return go(edge_forward_kernel<64, VEC>, 64, kEdgePrefetch<64>);
-    if (a.n <= 4096) return go(edge_forward_kernel<128, VEC>, 128, kEdgePrefetch<128>);
-    return go(edge_forward_kernel<256, VEC>, 256, kEdgePrefetch<256>);
+    if (a.n <= 1024) return launch_forward_t<32, VEC>(a, s);
+    if (a.n <= 2048) return launch_forward_t<64, VEC>(a, s);
+    if (a.n <= 4096) return launch_forward_t<128, VEC>(a, s);
+    return launch_forward_t<256, VEC>(a, s);
 }
 
 size_t long_row_smem(int64_t n) {

@@ -707,7 +707,7 @@ extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const
     if (M < 0 || N < 0 || K < 0 || !known_storage(typeC) || config < CFG_AUTO || config >= CFG_COUNT)
         return REPOPS_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return REPOPS_OK;
-    if (K > kMaxK) return REPOPS_ERR_UNSUPPORTED;
+    if (K > kMaxK || M > INT32_MAX || N > INT32_MAX) return REPOPS_ERR_UNSUPPORTED;
     if ((K > 0 && (!A || !B)) || !a_scale || !b_scale || !C) return REPOPS_ERR_INVALID_ARG;
     uint64_t ab, bb, cb;
     if (!span_bytes(M, K, lda, 1, &ab) || !span_bytes(N, K, ldb, 1, &bb) ||
