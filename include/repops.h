@@ -34,7 +34,8 @@
  *     repops_set_thread_status_word()) and, only where the caller asks for
  *     it, freed scratch its memory pool keeps mapped (see "Scratch memory").
  *   - Floating point is IEEE-754 binary32, round-to-nearest-even, subnormals
- *     kept (no flush-to-zero), no fused multiply-add, no tensor cores.
+ *     kept (no flush-to-zero), no fused multiply-add, no tensor cores (but for
+ *     the whole-number sums of repops_gemm_i8, which they hold exactly).
  *   - NaN results compare equal as a class (payload bits are not pinned);
  *     every other value, including signed zeros and infinities, is bit-exact.
  */

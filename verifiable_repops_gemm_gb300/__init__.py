@@ -956,14 +956,19 @@ def rope(x, heads: int, cos, sin, *, first: int = 0, period: int = None, inverse
     return x
 
 
-def _on_device(*tensors):
-    """Every given tensor (None skipped) must live on the current CUDA device,
-    where the call's kernels run."""
+def _stream_on_device(stream, *tensors):
+    """The handle of `stream` (None: the current one), after checking that every
+    given tensor (None skipped) lives on the current CUDA device, where the
+    call's kernels run.  One function, as each question to torch counts in a
+    call of 15 us."""
     import torch
     here = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:      # -1 for a CPU tensor
             raise ValueError("every tensor must be on the current CUDA device (%d)" % here)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _groups(cols, group):
@@ -1000,15 +1005,15 @@ def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
     n = _groups(cols, group)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    elif out.shape != (rows, cols):
+        raise ValueError("out must have the shape of x")
     if scale is None:
         scale = torch.empty((rows, n), dtype=torch.float32, device=x.device)
-    _on_device(x, out, scale)
-    if tuple(out.shape) != (rows, cols):
-        raise ValueError("out must have the shape of x")
+    h = _stream_on_device(stream, x, out, scale)
     pq, ldq, ps, lds = _rows_i8(out, scale, group, "out")
-    rc = load().repops_quantize_rows_i8(rows, cols, x.data_ptr(), t, max(x.stride(0), cols, 1), group, pq, ldq, ps, lds,
-                                        _stream_handle(stream))
-    _capi.check(rc, "repops_quantize_rows_i8")
+    rc = load().repops_quantize_rows_i8(rows, cols, x.data_ptr(), t, max(x.stride(0), cols, 1), group, pq, ldq, ps, lds, h)
+    if rc:
+        _capi.check(rc, "repops_quantize_rows_i8")
     return out, scale
 
 
@@ -1019,14 +1024,14 @@ def dequantize_rows(q, scale, *, group: int = 0, dtype=None, out=None, stream=No
     pq, ldq, ps, lds = _rows_i8(q, scale, group, "q")
     if out is None:
         out = torch.empty(q.shape, dtype=dtype or torch.float32, device=q.device)
-    if tuple(out.shape) != tuple(q.shape) or (dtype is not None and out.dtype != dtype) or \
+    elif out.shape != q.shape or (dtype is not None and out.dtype != dtype) or \
             (out.shape[1] > 1 and out.stride(1) != 1):
         raise ValueError("out must have the shape of q, the dtype asked for and unit column stride")
-    _on_device(q, scale, out)
+    handle = _stream_on_device(stream, q, scale, out)
     rc = load().repops_dequantize_rows_i8(q.shape[0], q.shape[1], pq, ldq, ps, lds, group, out.data_ptr(),
-                                          _storage_type(out.dtype), max(out.stride(0), q.shape[1], 1),
-                                          _stream_handle(stream))
-    _capi.check(rc, "repops_dequantize_rows_i8")
+                                          _storage_type(out.dtype), max(out.stride(0), q.shape[1], 1), handle)
+    if rc:
+        _capi.check(rc, "repops_dequantize_rows_i8")
     return out
 
 
@@ -1061,7 +1066,7 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
         out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
     elif out.shape != (M, N) or (N > 1 and out.stride(1) != 1) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be (M, N) with unit column stride and the dtype asked for")
-    _on_device(A, B, a_scale, b_scale, bias, out)
+    handle = _stream_on_device(stream, A, B, a_scale, b_scale, bias, out)
     L = load()
     need = L.repops_gemm_i8_workspace_bytes(config, M, N, K)
     ws = _workspace(need, A.device, stream) if need else None
@@ -1069,7 +1074,7 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
                           max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
                           None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
                           _storage_type(out.dtype), max(out.stride(0), N, 1), ws.data_ptr() if ws is not None else None,
-                          need, _stream_handle(stream))
+                          need, handle)
     if rc:
         _capi.check(rc, "repops_gemm_i8")
     return out
@@ -1117,10 +1122,11 @@ def swiglu_backward_i8(g, g_scale, u, u_scale, dh, dg=None, du=None, *, group: i
     pdg, lddg = _row_like(dg, g.shape, "dg")
     pdu, lddu = _row_like(du, g.shape, "du")
     ph, ldh = _row_like(h, g.shape, "h")
-    _on_device(g, g_scale, u, u_scale, dh, dg, du, h)
+    handle = _stream_on_device(stream, g, g_scale, u, u_scale, dh, dg, du, h)
     rc = load().repops_swiglu_backward_i8(g.shape[0], g.shape[1], pg, ldg, pgs, ldgs, pu, ldu, pus, ldus, group, pd, ldd,
-                                          pdg, lddg, pdu, lddu, ph, ldh, _stream_handle(stream))
-    _capi.check(rc, "repops_swiglu_backward_i8")
+                                          pdg, lddg, pdu, lddu, ph, ldh, handle)
+    if rc:
+        _capi.check(rc, "repops_swiglu_backward_i8")
     return dg, du
 
 
@@ -1138,7 +1144,7 @@ def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, gro
     dgamma = torch.empty(cols, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
     pdx, lddx = _row_like(dx, x.shape, "dx")
     ph, ldh = _row_like(h, x.shape, "h")
-    _on_device(x, x_scale, gamma, dy, res, dx, h, dgamma)
+    handle = _stream_on_device(stream, x, x_scale, gamma, dy, res, dx, h, dgamma)
     if rows == 0 or cols == 0:
         return dx, dgamma.zero_()
     L = load()
@@ -1147,8 +1153,9 @@ def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, gro
     rc = L.repops_rmsnorm_backward_i8(rows, cols, px, ldx, pxs, lds, group, _gain(gamma, cols, "gamma"),
                                       ctypes.c_float(eps), pd, ldd, pr, ldr, pdx, lddx, ph, ldh,
                                       _gain(dgamma, cols, "dgamma"), ws.data_ptr() if ws is not None else None, need,
-                                      _stream_handle(stream))
-    _capi.check(rc, "repops_rmsnorm_backward_i8")
+                                      handle)
+    if rc:
+        _capi.check(rc, "repops_rmsnorm_backward_i8")
     return dx, dgamma
 
 
@@ -1156,11 +1163,13 @@ def _gate_rows(gate, rows, cols):
     """(pointer, pitch, rows that share a gate row, gate rows)."""
     if gate is None:
         return None, 0, 1, 0
-    g = gate.view(1, -1) if gate.dim() == 1 else gate
-    if g.dim() != 2 or g.shape[1] != cols or g.shape[0] < 1 or rows % g.shape[0]:
+    shape = gate.shape
+    if len(shape) == 1:
+        gate, shape = gate.unsqueeze(0), (1, shape[0])
+    if len(shape) != 2 or shape[1] != cols or shape[0] < 1 or rows % shape[0]:
         raise ValueError("gate must be (cols,) or (G, cols) with G dividing the rows")
-    p, ld = _row_operand(g, "gate")
-    return p, ld, max(rows // g.shape[0], 1), g.shape[0]
+    p, ld = _row_operand(gate, "gate")
+    return p, ld, max(rows // shape[0], 1), shape[0]
 
 
 def rmsnorm_residual(x, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=None, alpha: float = 1.0, y=None,
@@ -1187,11 +1196,12 @@ def rmsnorm_residual(x, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=
         h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
     py, ldy = _row_like(y, x.shape, "y")
     ph, ldh = _row_like(h, x.shape, "h")
-    _on_device(x, f, pre_gain, post_gain, gate, y, h)
+    handle = _stream_on_device(stream, x, f, pre_gain, post_gain, gate, y, h)
     rc = load().repops_rmsnorm_residual_f32(rows, cols, px, ldx, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg,
                                             per, ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"),
-                                            ctypes.c_float(eps), py, ldy, ph, ldh, _stream_handle(stream))
-    _capi.check(rc, "repops_rmsnorm_residual_f32")
+                                            ctypes.c_float(eps), py, ldy, ph, ldh, handle)
+    if rc:
+        _capi.check(rc, "repops_rmsnorm_residual_f32")
     return y, h
 
 
@@ -1234,7 +1244,7 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
     pdx, lddx = _row_like(dx, f.shape, "dx")
     pdf, lddf = _row_like(df, f.shape, "df")
     pdg, lddg, _, _ = _gate_rows(dgate, rows, cols)
-    _on_device(dy, dh, y, f, pre_gain, post_gain, gate, dx, df, dpre, dpost, dgate)
+    handle = _stream_on_device(stream, dy, dh, y, f, pre_gain, post_gain, gate, dx, df, dpre, dpost, dgate)
     if rows == 0 or cols == 0:
         for t in (dpre, dpost, dgate):
             if t is not None:
@@ -1247,6 +1257,7 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
         rows, cols, pdy, lddy, pdh, lddh, py, ldy, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg, per,
         ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"), ctypes.c_float(eps), pdx, lddx, pdf, lddf,
         _gain(dpre, cols, "dpre"), _gain(dpost, cols, "dpost"), pdg, lddg, ws.data_ptr() if ws is not None else None,
-        need, _stream_handle(stream))
-    _capi.check(rc, "repops_rmsnorm_residual_backward_f32")
+        need, handle)
+    if rc:
+        _capi.check(rc, "repops_rmsnorm_residual_backward_f32")
     return dx, df, dpre, dpost, dgate
