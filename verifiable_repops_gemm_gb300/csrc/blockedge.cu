@@ -43,7 +43,7 @@ constexpr int64_t MAX_STAGED_COLS = 8192;       // 256 threads, a run each
 constexpr int64_t MAX_FOLD_ROWS = RUN * RUN;    // run results the last fold takes
 
 // ------------------------------------------------------------- row slabs ----
-// A warp's slab: step k (of 8) covers four values a lane.  With 16-byte rows
+// A warp's slab: step k (of KS, 8 but for short rows) covers four values a lane.  With 16-byte rows
 // (VEC) they are columns 128k + 4*lane .. + 3 of the slab; else columns
 // 128k + lane + {0, 32, 64, 96}.  `slab` is the slab's first column.
 
@@ -124,11 +124,11 @@ __device__ __forceinline__ void stage_store(float4 *stage, int slab, int k, floa
 }
 
 // Starts the copy of the warp's slab of a row into the stage.
-template <bool VEC>
+template <bool VEC, int KS>
 __device__ __forceinline__ void stage_row(float4 *stage, const float *row, int slab, int n) {
     float *s = reinterpret_cast<float *>(stage);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < KS; ++k) {
         if constexpr (VEC) {
             const int c = slab_col<VEC>(slab, k, 0);
             if (c < n) cp_async_16(s + stage_float<VEC>(slab, k, 0), row + c, 16u);
@@ -144,10 +144,10 @@ __device__ __forceinline__ void stage_row(float4 *stage, const float *row, int s
 
 // The CTA's copy of a parameter row (null: none), in memory order, and a slab
 // step of it.  A barrier follows the copies.
-template <int T>
+template <int LEN>
 __device__ __forceinline__ void param_copy(float *dst, const float *src, int n) {
     if (!src) return;
-    for (int c = threadIdx.x; c < T * RUN; c += blockDim.x) dst[c] = c < n ? __ldg(src + c) : 0.0f;
+    for (int c = threadIdx.x; c < LEN; c += blockDim.x) dst[c] = c < n ? __ldg(src + c) : 0.0f;
 }
 
 template <bool VEC>
@@ -164,10 +164,11 @@ template <class F>
 __device__ __forceinline__ float slab_fold(const float4 *stage, float4 *lanes, int slab, int n, F f) {
     const int lane = threadIdx.x & 31, u = slab / RUN + lane;
     const int len = min(RUN, n - u * RUN);                 // 0 or less past the end
+    const int at = len > 0 ? u : slab / RUN;               // a lane without a run reads one that is there
     float v[RUN];
 #pragma unroll
     for (int c = 0; c < RUN / 4; ++c) {
-        const float4 w = stage[stage_slot(u, c)];
+        const float4 w = stage[stage_slot(at, c)];
         v[4 * c] = w.x; v[4 * c + 1] = w.y; v[4 * c + 2] = w.z; v[4 * c + 3] = w.w;
     }
     float acc = f(v[0]);
@@ -246,10 +247,10 @@ struct Ident {
 
 // Teams of a CTA whose rows take STAGES stages and whose parameters PARAMS: what
 // 224 KB hold, and 15 barriers at most.
-template <int T, int STAGES, int PARAMS, int MAX_THREADS>
-constexpr int kTeams = std::min({(224 * 1024 / (T * RUN * 4) - PARAMS) / STAGES, MAX_THREADS / T, T > 32 ? 15 : 64});
-template <int T, int STAGES, int PARAMS, int TEAMS>
-constexpr size_t kTeamSmem = size_t(T) * RUN * 4 * (PARAMS + STAGES * TEAMS);
+template <int T, int KS, int STAGES, int PARAMS, int MAX_THREADS>
+constexpr int kTeams = std::min({(224 * 1024 / (T * KS * 16) - PARAMS) / STAGES, MAX_THREADS / T, T > 32 ? 15 : 64});
+template <int T, int KS, int STAGES, int PARAMS, int TEAMS>
+constexpr size_t kTeamSmem = size_t(T) * KS * 16 * (PARAMS + STAGES * TEAMS);
 
 // --------------------------------------------------------------- forward ----
 
@@ -268,7 +269,7 @@ struct EdgeArgs {
 template <int T>
 constexpr bool kEdgePrefetch = T <= 128;
 
-template <int T, bool VEC>
+template <int T, int KS, bool VEC>
 __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     extern __shared__ float4 stage_mem[];
     __shared__ float roots[2][2][8];
@@ -276,15 +277,15 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
     float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
     const int slab = (threadIdx.x >> 5) * 1024;
     int phase = 0;
-    constexpr int Q = T * RUN / 4;
+    constexpr int Q = T * KS, KB = KS < 4 ? KS : 4;            // a stage in 16-byte chunks
     constexpr bool PF = kEdgePrefetch<T>;
     const int n = int(p.n);
     const float nf = float(p.n);
     int cur = 0;
     int64_t row = blockIdx.x;
     if (row < p.rows) {
-        stage_row<VEC>(stage_mem, p.f + row * p.ldf, slab, n);
-        stage_row<VEC>(stage_mem + Q, p.x + row * p.ldx, slab, n);
+        stage_row<VEC, KS>(stage_mem, p.f + row * p.ldf, slab, n);
+        stage_row<VEC, KS>(stage_mem + Q, p.x + row * p.ldx, slab, n);
     }
     cp_async_commit();
     for (; row < p.rows; row += gridDim.x) {
@@ -293,8 +294,8 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         if constexpr (PF) {
             cur ^= 1;
             if (next < p.rows) {
-                stage_row<VEC>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, slab, n);
-                stage_row<VEC>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, slab, n);
+                stage_row<VEC, KS>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, slab, n);
+                stage_row<VEC, KS>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
@@ -314,18 +315,18 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
         }
         float *yr = p.y + row * p.ldy;
 #pragma unroll
-        for (int b = 0; b < 8; b += 4) {    // four steps' loads in flight together
-            float4 w[4], g[4];
+        for (int b = 0; b < KS; b += KB) {    // up to four steps' loads in flight together
+            float4 w[KB], g[KB];
             if (p.post) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = row_load<VEC>(p.post, slab, b + k, n);
+                for (int k = 0; k < KB; ++k) w[k] = row_load<VEC>(p.post, slab, b + k, n);
             }
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] = row_load<VEC>(gate, slab, b + k, n);
+                for (int k = 0; k < KB; ++k) g[k] = row_load<VEC>(gate, slab, b + k, n);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < KB; ++k) {
                 float4 v = stage_load<VEC>(sf, slab, b + k);
                 if (p.post) v = mul4(mul4(v, inv_f), w[k]);
                 if (gate) v = mul4(v, g[k]);
@@ -340,17 +341,17 @@ __global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
             slab_roots<T, 1>(s, roots, phase, 0, n);
             const float inv_y = rms_inv(s[0], nf, p.eps);
             float *hr = p.h + row * p.ldh;
-            float4 w[8];
+            float4 w[KS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = row_load<VEC>(p.pre, slab, k, n);
+            for (int k = 0; k < KS; ++k) w[k] = row_load<VEC>(p.pre, slab, k, n);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC>(hr, slab, k, n, mul4(mul4(stage_load<VEC>(sx, slab, k), inv_y), w[k]));
+            for (int k = 0; k < KS; ++k) row_store<VEC>(hr, slab, k, n, mul4(mul4(stage_load<VEC>(sx, slab, k), inv_y), w[k]));
         }
         __syncwarp();                       // the stage is read before it is filled again
         if constexpr (!PF) {
             if (next < p.rows) {
-                stage_row<VEC>(sf, p.f + next * p.ldf, slab, n);
-                stage_row<VEC>(sx, p.x + next * p.ldx, slab, n);
+                stage_row<VEC, KS>(sf, p.f + next * p.ldf, slab, n);
+                stage_row<VEC, KS>(sx, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
@@ -432,7 +433,7 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int i = c + 32 * t < n ? c + 32 * t : 0;
-            v[t] = __fmul_rn(float(__ldg(q + i)), __ldg(s + (i >> p.shift)));
+            v[t] = unpack_q1(__ldg(q + i), __ldg(s + (i >> p.shift)));
         }
         return make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -440,43 +441,43 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
 
 // Stages of a row: y, dh, dy, and f with F; parameters: pre, and post and the
 // gate with F (whose rows want 160 registers a thread).
-template <int T, bool F>
-constexpr int kBackTeams = F ? kTeams<T, 4, 3, 384> : kTeams<T, 3, 1, 512>;
+template <int T, int KS, bool F>
+constexpr int kBackTeams = F ? kTeams<T, KS, 4, 3, KS == 8 ? 384 : 512> : kTeams<T, KS, 3, 1, 512>;
 
 // dx = RMSNorm'(y; dh) + dy, then, with F, df through the gate and the norm
 // after the block.  Q8: y comes in 8 bits, and h may be written again.
-template <int T, bool VEC, bool Q8, bool F>
-__global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(EdgeBackArgs p) {
-    constexpr int Q = T * RUN / 4, TEAMS = kBackTeams<T, F>;
+template <int T, int KS, bool VEC, bool Q8, bool F>
+__global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kernel(EdgeBackArgs p) {
+    constexpr int Q = T * KS, TEAMS = kBackTeams<T, KS, F>;
     extern __shared__ float4 smem[];
     __shared__ float roots[TEAMS][2][2][8];
     __shared__ float4 lane_mem[TEAMS * T / 4];
     const int n = int(p.n), team = threadIdx.x / T, slab = ((threadIdx.x % T) >> 5) * 1024;
     const float nf = float(p.n);
-    float *pre = reinterpret_cast<float *>(smem), *post = pre + T * RUN, *gate1 = post + T * RUN;
+    float *pre = reinterpret_cast<float *>(smem), *post = pre + 4 * Q, *gate1 = post + 4 * Q;
     float4 *sy = smem + (F ? 3 : 1) * Q + team * Q * (F ? 4 : 3), *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
     float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
     const bool one_gate = F && p.gate && p.gate_rows >= p.rows;
-    param_copy<T>(pre, p.pre, n);
+    param_copy<4 * Q>(pre, p.pre, n);
     if constexpr (F) {
-        param_copy<T>(post, p.post, n);
-        param_copy<T>(gate1, one_gate ? p.gate : nullptr, n);
+        param_copy<4 * Q>(post, p.post, n);
+        param_copy<4 * Q>(gate1, one_gate ? p.gate : nullptr, n);
     }
     __syncthreads();
     int phase = 0;
     // rows go to the SMs first, then to their teams
     for (int64_t row = int64_t(team) * gridDim.x + blockIdx.x; row < p.rows; row += int64_t(gridDim.x) * TEAMS) {
         if (p.dh) {
-            if constexpr (!Q8) stage_row<VEC>(sy, p.y + row * p.ldy, slab, n);
-            stage_row<VEC>(sh, p.dh + row * p.lddh, slab, n);
+            if constexpr (!Q8) stage_row<VEC, KS>(sy, p.y + row * p.ldy, slab, n);
+            stage_row<VEC, KS>(sh, p.dh + row * p.lddh, slab, n);
         }
-        if constexpr (F) stage_row<VEC>(sf, p.f + row * p.ldf, slab, n);
+        if constexpr (F) stage_row<VEC, KS>(sf, p.f + row * p.ldf, slab, n);
         cp_async_commit();
-        if (p.dy) stage_row<VEC>(sr, p.dy + row * p.lddy, slab, n);
+        if (p.dy) stage_row<VEC, KS>(sr, p.dy + row * p.lddy, slab, n);
         cp_async_commit();
         if constexpr (Q8) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) stage_store<VEC>(sy, slab, k, row8_load<VEC>(p, row, slab, k, n));
+            for (int k = 0; k < KS; ++k) stage_store<VEC>(sy, slab, k, row8_load<VEC>(p, row, slab, k, n));
         }
         cp_async_wait<1>();
         __syncwarp();
@@ -493,12 +494,12 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
                 if (p.post) p.inv_f[row] = inv_f;
             }
         }
-        float4 e[8];                              // dx
+        float4 e[KS];                             // dx
         if (p.dh) {
             // sh <- gy * xh, summed from there
-            float4 g[8];
+            float4 g[KS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < KS; ++k) {
                 g[k] = param_load<VEC>(pre, slab, k);
                 e[k] = mul4(stage_load<VEC>(sy, slab, k), inv_y);
                 if constexpr (Q8) {
@@ -512,30 +513,30 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
             slab_roots<T, 1>(r1, roots[team], phase, team, n);
             const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(g[k], mul4(e[k], c)), inv_y);
+            for (int k = 0; k < KS; ++k) e[k] = mul4(sub4(g[k], mul4(e[k], c)), inv_y);
         }
         cp_async_wait<0>();
         __syncwarp();
         if (p.dy) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < KS; ++k) {
                 const float4 d = stage_load<VEC>(sr, slab, k);
                 e[k] = p.dh ? add4(e[k], d) : d;
             }
         }
         float *dxr = p.dx + row * p.lddx;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) row_store<VEC>(dxr, slab, k, n, e[k]);
+        for (int k = 0; k < KS; ++k) row_store<VEC>(dxr, slab, k, n, e[k]);
         if constexpr (F) {
             float *dfr = p.df + row * p.lddf;
             const float *gate = p.gate && !one_gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
-            float4 g[8];
+            float4 g[KS];
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = row_load<VEC>(gate, slab, k, n);
+                for (int k = 0; k < KS; ++k) g[k] = row_load<VEC>(gate, slab, k, n);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < KS; ++k) {
                 e[k] = mul4(e[k], p.alpha);
                 if (gate) e[k] = mul4(e[k], g[k]);
                 else if (one_gate) e[k] = mul4(e[k], param_load<VEC>(gate1, slab, k));
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
             if (p.post) {
                 __syncwarp();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < KS; ++k) {
                     e[k] = mul4(e[k], param_load<VEC>(post, slab, k));
                     g[k] = mul4(stage_load<VEC>(sf, slab, k), inv_f);
                     stage_store<VEC>(sh, slab, k, mul4(e[k], g[k]));
@@ -553,10 +554,10 @@ __global__ void __launch_bounds__(T *kBackTeams<T, F>, 1) edge_backward_kernel(E
                 slab_roots<T, 1>(r1, roots[team], phase, team, n);
                 const float c = __fdiv_rn(r1[0], nf);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
+                for (int k = 0; k < KS; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) row_store<VEC, false>(dfr, slab, k, n, e[k]);
+            for (int k = 0; k < KS; ++k) row_store<VEC, false>(dfr, slab, k, n, e[k]);
         }
         __syncwarp();
     }
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
                             const float4 w = unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
                             y[i].v[0] = w.x; y[i].v[1] = w.y; y[i].v[2] = w.z; y[i].v[3] = w.w;
                         } else {
-                            y[i].v[0] = __fmul_rn(float(__ldg(p.q + r * p.ldq + c)), s);
+                            y[i].v[0] = unpack_q1(__ldg(p.q + r * p.ldq + c), s);
                         }
                     } else {
                         y[i] = cols_load<W>(p.y + r * p.ldy + c);
@@ -878,14 +879,14 @@ int launch_teams(Kern kern, int threads, size_t smem, const Args &a, cudaStream_
 // yet): the question costs a quarter of the host's time in a call for one row.
 // The kernel's shared-memory limit belongs to the context and is set each time
 // where the default (48 KB) does not do.
-template <int T, bool VEC>
+template <int T, int KS, bool VEC>
 int launch_forward_t(const EdgeArgs &a, cudaStream_t s) {
-    constexpr size_t smem = size_t(T) * RUN * 4 * (kEdgePrefetch<T> ? 4 : 2);
+    constexpr size_t smem = size_t(T) * KS * 16 * (kEdgePrefetch<T> ? 4 : 2);
     static std::atomic<int> resident[64];
     DeviceInfo di;
     int rc = current_device_info(&di);
     if (rc != REPOPS_OK) return rc;
-    auto kern = edge_forward_kernel<T, VEC>;
+    auto kern = edge_forward_kernel<T, KS, VEC>;
     int per_sm = resident[di.device].load(std::memory_order_relaxed);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -903,10 +904,12 @@ int launch_forward_t(const EdgeArgs &a, cudaStream_t s) {
 
 template <bool VEC>
 int launch_forward(const EdgeArgs &a, cudaStream_t s) {
-    if (a.n <= 1024) return launch_forward_t<32, VEC>(a, s);
-    if (a.n <= 2048) return launch_forward_t<64, VEC>(a, s);
-    if (a.n <= 4096) return launch_forward_t<128, VEC>(a, s);
-    return launch_forward_t<256, VEC>(a, s);
+    if (a.n <= 256) return launch_forward_t<32, 2, VEC>(a, s);
+    if (a.n <= 512) return launch_forward_t<32, 4, VEC>(a, s);
+    if (a.n <= 1024) return launch_forward_t<32, 8, VEC>(a, s);
+    if (a.n <= 2048) return launch_forward_t<64, 8, VEC>(a, s);
+    if (a.n <= 4096) return launch_forward_t<128, 8, VEC>(a, s);
+    return launch_forward_t<256, 8, VEC>(a, s);
 }
 
 size_t long_row_smem(int64_t n) {
@@ -923,19 +926,21 @@ int launch_long(Kern kern, const Args &a, int64_t rows, int64_t n, cudaStream_t 
     return check_launch();
 }
 
-template <int T, bool VEC, bool Q8, bool F>
+template <int T, int KS, bool VEC, bool Q8, bool F>
 int launch_rows_t(const EdgeBackArgs &a, cudaStream_t s) {
-    constexpr int teams = kBackTeams<T, F>;
-    return launch_teams(edge_backward_kernel<T, VEC, Q8, F>, T * teams,
-                        F ? kTeamSmem<T, 4, 3, teams> : kTeamSmem<T, 3, 1, teams>, a, s);
+    constexpr int teams = kBackTeams<T, KS, F>;
+    return launch_teams(edge_backward_kernel<T, KS, VEC, Q8, F>, T * teams,
+                        F ? kTeamSmem<T, KS, 4, 3, teams> : kTeamSmem<T, KS, 3, 1, teams>, a, s);
 }
 
 template <bool VEC, bool Q8, bool F>
 int launch_rows(const EdgeBackArgs &a, cudaStream_t s) {
-    if (a.n <= 1024) return launch_rows_t<32, VEC, Q8, F>(a, s);
-    if (a.n <= 2048) return launch_rows_t<64, VEC, Q8, F>(a, s);
-    if (a.n <= 4096) return launch_rows_t<128, VEC, Q8, F>(a, s);
-    return launch_rows_t<256, VEC, Q8, F>(a, s);
+    if (a.n <= 256) return launch_rows_t<32, 2, VEC, Q8, F>(a, s);
+    if (a.n <= 512) return launch_rows_t<32, 4, VEC, Q8, F>(a, s);
+    if (a.n <= 1024) return launch_rows_t<32, 8, VEC, Q8, F>(a, s);
+    if (a.n <= 2048) return launch_rows_t<64, 8, VEC, Q8, F>(a, s);
+    if (a.n <= 4096) return launch_rows_t<128, 8, VEC, Q8, F>(a, s);
+    return launch_rows_t<256, 8, VEC, Q8, F>(a, s);
 }
 
 template <bool Q8, bool F>

@@ -245,7 +245,7 @@ dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t i = i0 + 256 * j < units ? i0 + 256 * j : 0;
-                w[j] = VEC ? __ldcs(reinterpret_cast<const uint32_t *>(qr) + i) : uint32_t(int(__ldg(qr + i)));
+                w[j] = VEC ? __ldcs(reinterpret_cast<const uint32_t *>(qr) + i) : uint32_t(uint8_t(__ldg(qr + i)));
                 s[j] = __ldg(sr + ((VEC ? 4 * i : i) >> shift));
             }
 #pragma unroll
@@ -253,7 +253,7 @@ dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t 
                 const int64_t i = i0 + 256 * j;
                 if (i >= units) continue;
                 if constexpr (VEC) store_four<TY>(x, r * ldx + 4 * i, unpack_q4(w[j], s[j]));
-                else store_one<TY>(x, r * ldx + i, __fmul_rn(float(int(w[j])), s[j]));
+                else store_one<TY>(x, r * ldx + i, unpack_q1(int8_t(w[j]), s[j]));
             }
         }
     }
@@ -272,46 +272,72 @@ struct SwigluArgs {
     int64_t lddg, lddu, ldh;
 };
 
+// Four values of a row from column c on: consecutive with aligned rows (VEC),
+// else 256 apart (so that neighbouring threads hold neighbouring columns); past
+// the row's end column 0 is read (no branch: the loads are in flight together)
+// and nothing is stored.
+template <bool VEC>
+__device__ __forceinline__ float4 four_q8(const int8_t *q, const float *s, int shift, int c, int n) {
+    if constexpr (VEC) {
+        return unpack_q4(__ldcs(reinterpret_cast<const uint32_t *>(q + c)), __ldg(s + (c >> shift)));
+    } else {
+        float v[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int i = c + 256 * t < n ? c + 256 * t : 0;
+            v[t] = unpack_q1(__ldg(q + i), __ldg(s + (i >> shift)));
+        }
+        return make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ float4 four_f32(const float *p, int c, int n) {
+    if constexpr (VEC) return *reinterpret_cast<const float4 *>(p + c);
+    else
+        return make_float4(p[c < n ? c : 0], p[c + 256 < n ? c + 256 : 0], p[c + 512 < n ? c + 512 : 0],
+                           p[c + 768 < n ? c + 768 : 0]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_four_f32(float *p, int c, int n, float4 v) {
+    if constexpr (VEC) {
+        *reinterpret_cast<float4 *>(p + c) = v;
+    } else {
+        if (c < n) p[c] = v.x;
+        if (c + 256 < n) p[c + 256] = v.y;
+        if (c + 512 < n) p[c + 512] = v.z;
+        if (c + 768 < n) p[c + 768] = v.w;
+    }
+}
+
 // The backward of h = SiLU(g) * u with g and u restored in registers, the
 // operations of swiglu_backward_kernel; with h, the forward's value as well
-// (the activation a weight gradient needs, so that it is not kept).
+// (the activation a weight gradient needs, so that it is not kept).  A CTA takes
+// 1024 columns of a row, four a thread.
 template <bool VEC, bool H>
 __global__ void __launch_bounds__(256) swiglu_backward_i8_kernel(SwigluArgs p) {
-    const int64_t units = VEC ? p.cols / 4 : p.cols;
+    const int n = int(p.cols);
     for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
         const int8_t *gr = p.g + r * p.ldg, *ur = p.u + r * p.ldu;
         const float *gsr = p.gs + r * p.ldgs, *usr = p.us + r * p.ldus, *dr = p.dh + r * p.lddh;
         float *dgr = p.dg + r * p.lddg, *dur = p.du + r * p.lddu, *hr = H ? p.h + r * p.ldh : nullptr;
-        for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < units;
-             i += int64_t(gridDim.x) * blockDim.x) {
-            if constexpr (VEC) {
-                const int64_t grp = (4 * i) >> p.shift;
-                const float4 d = reinterpret_cast<const float4 *>(dr)[i];
-                const float4 a = unpack_q4(__ldcs(reinterpret_cast<const uint32_t *>(gr) + i), __ldg(gsr + grp));
-                const float4 b = unpack_q4(__ldcs(reinterpret_cast<const uint32_t *>(ur) + i), __ldg(usr + grp));
-                float4 og, ou;
-                const float2 s01 = sigmoid_fixed2(a.x, a.y), s23 = sigmoid_fixed2(a.z, a.w);
-                swiglu_grad_s(a.x, b.x, d.x, s01.x, og.x, ou.x);
-                swiglu_grad_s(a.y, b.y, d.y, s01.y, og.y, ou.y);
-                swiglu_grad_s(a.z, b.z, d.z, s23.x, og.z, ou.z);
-                swiglu_grad_s(a.w, b.w, d.w, s23.y, og.w, ou.w);
-                reinterpret_cast<float4 *>(dgr)[i] = og;
-                reinterpret_cast<float4 *>(dur)[i] = ou;
-                if constexpr (H)
-                    reinterpret_cast<float4 *>(hr)[i] =
-                        make_float4(swiglu_s(a.x, b.x, s01.x), swiglu_s(a.y, b.y, s01.y),
-                                    swiglu_s(a.z, b.z, s23.x), swiglu_s(a.w, b.w, s23.y));
-            } else {
-                const int64_t grp = i >> p.shift;
-                const float a = __fmul_rn(float(gr[i]), __ldg(gsr + grp));
-                const float b = __fmul_rn(float(ur[i]), __ldg(usr + grp));
-                float og, ou;
-                const float d = dr[i];
-                swiglu_grad1(a, b, d, og, ou);
-                dgr[i] = og;
-                dur[i] = ou;
-                if constexpr (H) hr[i] = swiglu1(a, b);
-            }
+        for (int c0 = blockIdx.x * 1024; c0 < n; c0 += gridDim.x * 1024) {
+            const int c = c0 + (VEC ? 4 : 1) * threadIdx.x;
+            if (c >= n) continue;
+            const float4 d = four_f32<VEC>(dr, c, n);
+            const float4 a = four_q8<VEC>(gr, gsr, p.shift, c, n), b = four_q8<VEC>(ur, usr, p.shift, c, n);
+            float4 og, ou;
+            const float2 s01 = sigmoid_fixed2(a.x, a.y), s23 = sigmoid_fixed2(a.z, a.w);
+            swiglu_grad_s(a.x, b.x, d.x, s01.x, og.x, ou.x);
+            swiglu_grad_s(a.y, b.y, d.y, s01.y, og.y, ou.y);
+            swiglu_grad_s(a.z, b.z, d.z, s23.x, og.z, ou.z);
+            swiglu_grad_s(a.w, b.w, d.w, s23.y, og.w, ou.w);
+            store_four_f32<VEC>(dgr, c, n, og);
+            store_four_f32<VEC>(dur, c, n, ou);
+            if constexpr (H)
+                store_four_f32<VEC>(hr, c, n, make_float4(swiglu_s(a.x, b.x, s01.x), swiglu_s(a.y, b.y, s01.y),
+                                                          swiglu_s(a.z, b.z, s23.x), swiglu_s(a.w, b.w, s23.y)));
         }
     }
 }
@@ -325,14 +351,6 @@ bool aligned(const void *p, int64_t ld, unsigned size, unsigned bytes) {
 int sm_count() {
     DeviceInfo di;
     return current_device_info(&di) == REPOPS_OK ? di.sms : 152;
-}
-
-// 256-thread CTAs: x over column units, y over rows, about 16 CTAs per SM.
-dim3 grid_2d(int64_t units, int64_t rows) {
-    const int64_t target = int64_t(sm_count()) * 16;
-    const int64_t gx = std::max<int64_t>(1, std::min<int64_t>((units + 255) / 256, target));
-    const int64_t gy = std::max<int64_t>(1, std::min<int64_t>({rows, std::max<int64_t>(1, target / gx), 65535}));
-    return dim3(unsigned(gx), unsigned(gy));
 }
 
 template <int TY>
@@ -457,7 +475,7 @@ extern "C" int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_
                        dg, du, h, lddg, lddu, ldh};
     const bool vec = cols % 4 == 0 && aligned(g, ldg, 1, 4) && aligned(u, ldu, 1, 4) && aligned(dh, lddh, 4, 16) &&
                      aligned(dg, lddg, 4, 16) && aligned(du, lddu, 4, 16) && (!h || aligned(h, ldh, 4, 16));
-    const dim3 grid = grid_2d(vec ? cols / 4 : cols, rows);
+    const dim3 grid(unsigned((cols + 1023) / 1024), unsigned(std::min<int64_t>(rows, 65535)));
     if (vec && h) swiglu_backward_i8_kernel<true, true><<<grid, 256, 0, stream>>>(a);
     else if (vec) swiglu_backward_i8_kernel<true, false><<<grid, 256, 0, stream>>>(a);
     else if (h) swiglu_backward_i8_kernel<false, true><<<grid, 256, 0, stream>>>(a);

@@ -57,5 +57,11 @@ __device__ __forceinline__ float4 unpack_q4(uint32_t w, float scale) {
                        __fmul_rn(__fsub_rn(c, 8388736.0f), scale), __fmul_rn(__fsub_rn(d, 8388736.0f), scale));
 }
 
+// One of them.
+__device__ __forceinline__ float unpack_q1(int8_t q, float scale) {
+    const uint32_t u = 0x4b000000u | (uint32_t(uint8_t(q)) ^ 0x80u);
+    return __fmul_rn(__fsub_rn(__uint_as_float(u), 8388736.0f), scale);
+}
+
 }  // namespace
 }  // namespace repops
