@@ -270,7 +270,7 @@ template <int T>
 constexpr bool kEdgePrefetch = T <= 128;
 
 template <int T, int KS, bool VEC>
-__global__ void __launch_bounds__(T) edge_forward_kernel(EdgeArgs p) {
+__global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
     extern __shared__ float4 stage_mem[];
     __shared__ float roots[2][2][8];
     __shared__ float4 lane_mem[T / 4];

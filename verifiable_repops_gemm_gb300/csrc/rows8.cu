@@ -159,9 +159,9 @@ quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64
     }
 }
 
-// One scale a row: T threads a row (a warp, or the CTA), each keeping up to 32
-// of the row's values in registers between the maximum and the quantisation;
-// longer rows are read again from the cache.
+// One scale a row: T threads a row, each keeping up to 32 of the row's values in
+// registers between the maximum and the quantisation; rows of more than 8192
+// values are read again from the cache.
 template <int TY, bool VEC, int T>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t ldx, int8_t *__restrict__ q,
@@ -202,7 +202,7 @@ quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t
             if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < T / 32; ++w) m = max_mag(m, part[w]);
+            for (int w = 0; w < T / 32; ++w) m = max_mag(m, part[threadIdx.x / T * (T / 32) + w]);
             __syncthreads();
         }
         if (!live) continue;
@@ -229,8 +229,9 @@ quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t
     }
 }
 
-// A CTA takes 4 * 256 units of a row (a unit: four columns with aligned rows,
-// else one), four a thread in flight together; the grid's y runs along rows.
+// A CTA takes four units a thread of a row (a unit: four columns with aligned
+// rows, else one), all in flight together; the grid's y runs along rows.  Short
+// rows get short CTAs (row_threads).
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t ldq,
@@ -239,18 +240,19 @@ dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t 
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const int8_t *qr = q + r * ldq;
         const float *sr = scale + r * lds;
-        for (int64_t i0 = blockIdx.x * int64_t(1024) + threadIdx.x; i0 < units; i0 += int64_t(gridDim.x) * 1024) {
+        const int S = blockDim.x;
+        for (int64_t i0 = blockIdx.x * int64_t(4 * S) + threadIdx.x; i0 < units; i0 += int64_t(gridDim.x) * 4 * S) {
             uint32_t w[4];
             float s[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t i = i0 + 256 * j < units ? i0 + 256 * j : 0;
+                const int64_t i = i0 + S * j < units ? i0 + S * j : 0;
                 w[j] = VEC ? __ldcs(reinterpret_cast<const uint32_t *>(qr) + i) : uint32_t(uint8_t(__ldg(qr + i)));
                 s[j] = __ldg(sr + ((VEC ? 4 * i : i) >> shift));
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t i = i0 + 256 * j;
+                const int64_t i = i0 + S * j;
                 if (i >= units) continue;
                 if constexpr (VEC) store_four<TY>(x, r * ldx + 4 * i, unpack_q4(w[j], s[j]));
                 else store_one<TY>(x, r * ldx + i, unpack_q1(int8_t(w[j]), s[j]));
@@ -273,9 +275,9 @@ struct SwigluArgs {
 };
 
 // Four values of a row from column c on: consecutive with aligned rows (VEC),
-// else 256 apart (so that neighbouring threads hold neighbouring columns); past
-// the row's end column 0 is read (no branch: the loads are in flight together)
-// and nothing is stored.
+// else a CTA's threads apart (so that neighbouring threads hold neighbouring
+// columns); past the row's end column 0 is read (no branch: the loads are in
+// flight together) and nothing is stored.
 template <bool VEC>
 __device__ __forceinline__ float4 four_q8(const int8_t *q, const float *s, int shift, int c, int n) {
     if constexpr (VEC) {
@@ -284,7 +286,7 @@ __device__ __forceinline__ float4 four_q8(const int8_t *q, const float *s, int s
         float v[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int i = c + 256 * t < n ? c + 256 * t : 0;
+            const int i = c + int(blockDim.x) * t < n ? c + int(blockDim.x) * t : 0;
             v[t] = unpack_q1(__ldg(q + i), __ldg(s + (i >> shift)));
         }
         return make_float4(v[0], v[1], v[2], v[3]);
@@ -294,9 +296,9 @@ __device__ __forceinline__ float4 four_q8(const int8_t *q, const float *s, int s
 template <bool VEC>
 __device__ __forceinline__ float4 four_f32(const float *p, int c, int n) {
     if constexpr (VEC) return *reinterpret_cast<const float4 *>(p + c);
-    else
-        return make_float4(p[c < n ? c : 0], p[c + 256 < n ? c + 256 : 0], p[c + 512 < n ? c + 512 : 0],
-                           p[c + 768 < n ? c + 768 : 0]);
+    const int S = blockDim.x;
+    return make_float4(p[c < n ? c : 0], p[c + S < n ? c + S : 0], p[c + 2 * S < n ? c + 2 * S : 0],
+                       p[c + 3 * S < n ? c + 3 * S : 0]);
 }
 
 template <bool VEC>
@@ -304,17 +306,18 @@ __device__ __forceinline__ void store_four_f32(float *p, int c, int n, float4 v)
     if constexpr (VEC) {
         *reinterpret_cast<float4 *>(p + c) = v;
     } else {
+        const int S = blockDim.x;
         if (c < n) p[c] = v.x;
-        if (c + 256 < n) p[c + 256] = v.y;
-        if (c + 512 < n) p[c + 512] = v.z;
-        if (c + 768 < n) p[c + 768] = v.w;
+        if (c + S < n) p[c + S] = v.y;
+        if (c + 2 * S < n) p[c + 2 * S] = v.z;
+        if (c + 3 * S < n) p[c + 3 * S] = v.w;
     }
 }
 
 // The backward of h = SiLU(g) * u with g and u restored in registers, the
 // operations of swiglu_backward_kernel; with h, the forward's value as well
 // (the activation a weight gradient needs, so that it is not kept).  A CTA takes
-// 1024 columns of a row, four a thread.
+// four columns a thread of a row.
 template <bool VEC, bool H>
 __global__ void __launch_bounds__(256) swiglu_backward_i8_kernel(SwigluArgs p) {
     const int n = int(p.cols);
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_i8_kernel(SwigluArgs p) {
         const int8_t *gr = p.g + r * p.ldg, *ur = p.u + r * p.ldu;
         const float *gsr = p.gs + r * p.ldgs, *usr = p.us + r * p.ldus, *dr = p.dh + r * p.lddh;
         float *dgr = p.dg + r * p.lddg, *dur = p.du + r * p.lddu, *hr = H ? p.h + r * p.ldh : nullptr;
-        for (int c0 = blockIdx.x * 1024; c0 < n; c0 += gridDim.x * 1024) {
+        for (int c0 = blockIdx.x * blockDim.x * 4; c0 < n; c0 += gridDim.x * blockDim.x * 4) {
             const int c = c0 + (VEC ? 4 : 1) * threadIdx.x;
             if (c >= n) continue;
             const float4 d = four_f32<VEC>(dr, c, n);
@@ -348,6 +351,9 @@ bool aligned(const void *p, int64_t ld, unsigned size, unsigned bytes) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && uint64_t(ld) * size % bytes == 0;
 }
 
+// Threads of a CTA that takes four of `units` a thread: whole warps, at most 256.
+unsigned row_threads(int64_t units) { return unsigned(std::min<int64_t>(256, ((units + 3) / 4 + 31) / 32 * 32)); }
+
 int sm_count() {
     DeviceInfo di;
     return current_device_info(&di) == REPOPS_OK ? di.sms : 152;
@@ -366,18 +372,17 @@ int launch_quantize(int64_t rows, int cols, const void *x, int64_t ldx, int64_t 
             quantize_groups_kernel<TY, false><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds);
         return check_launch();
     }
-    // a warp a row while the row fits its registers, else the CTA
-    const bool warp = cols <= 1024;
-    const unsigned grid = unsigned(std::min<int64_t>(warp ? (rows + 7) / 8 : rows, int64_t(sm_count()) * 32));
-    if (warp && vec)
-        quantize_rows_kernel<TY, true, 32><<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
-    else if (warp)
-        quantize_rows_kernel<TY, false, 32><<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
-    else if (vec)
-        quantize_rows_kernel<TY, true, 256><<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
-    else
-        quantize_rows_kernel<TY, false, 256><<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
-    return check_launch();
+    // as few threads a row as hold it in registers
+    auto go = [&](auto kv, auto ks, int T) {
+        const unsigned grid = unsigned(std::min<int64_t>((rows + 256 / T - 1) / (256 / T), int64_t(sm_count()) * 32));
+        if (vec) kv<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
+        else ks<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
+        return check_launch();
+    };
+    if (cols <= 1024) return go(quantize_rows_kernel<TY, true, 32>, quantize_rows_kernel<TY, false, 32>, 32);
+    if (cols <= 2048) return go(quantize_rows_kernel<TY, true, 64>, quantize_rows_kernel<TY, false, 64>, 64);
+    if (cols <= 4096) return go(quantize_rows_kernel<TY, true, 128>, quantize_rows_kernel<TY, false, 128>, 128);
+    return go(quantize_rows_kernel<TY, true, 256>, quantize_rows_kernel<TY, false, 256>, 256);
 }
 
 template <int TY>
@@ -385,9 +390,10 @@ int launch_dequantize(int64_t rows, int cols, const int8_t *q, int64_t ldq, cons
                       void *x, int64_t ldx, cudaStream_t s) {
     const bool vec = cols % 4 == 0 && aligned(x, ldx, storage_size(TY), 4 * storage_size(TY)) && aligned(q, ldq, 1, 4);
     const int64_t units = vec ? cols / 4 : cols;
-    const dim3 grid(unsigned((units + 1023) / 1024), unsigned(std::min<int64_t>(rows, 65535)));
-    if (vec) dequantize_kernel<TY, true><<<grid, 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
-    else dequantize_kernel<TY, false><<<grid, 256, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
+    const unsigned threads = row_threads(units);
+    const dim3 grid(unsigned((units + 4 * threads - 1) / (4 * threads)), unsigned(std::min<int64_t>(rows, 65535)));
+    if (vec) dequantize_kernel<TY, true><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
+    else dequantize_kernel<TY, false><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
     return check_launch();
 }
 
@@ -475,10 +481,11 @@ extern "C" int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_
                        dg, du, h, lddg, lddu, ldh};
     const bool vec = cols % 4 == 0 && aligned(g, ldg, 1, 4) && aligned(u, ldu, 1, 4) && aligned(dh, lddh, 4, 16) &&
                      aligned(dg, lddg, 4, 16) && aligned(du, lddu, 4, 16) && (!h || aligned(h, ldh, 4, 16));
-    const dim3 grid(unsigned((cols + 1023) / 1024), unsigned(std::min<int64_t>(rows, 65535)));
-    if (vec && h) swiglu_backward_i8_kernel<true, true><<<grid, 256, 0, stream>>>(a);
-    else if (vec) swiglu_backward_i8_kernel<true, false><<<grid, 256, 0, stream>>>(a);
-    else if (h) swiglu_backward_i8_kernel<false, true><<<grid, 256, 0, stream>>>(a);
-    else swiglu_backward_i8_kernel<false, false><<<grid, 256, 0, stream>>>(a);
+    const unsigned threads = row_threads(cols);
+    const dim3 grid(unsigned((cols + 4 * threads - 1) / (4 * threads)), unsigned(std::min<int64_t>(rows, 65535)));
+    if (vec && h) swiglu_backward_i8_kernel<true, true><<<grid, threads, 0, stream>>>(a);
+    else if (vec) swiglu_backward_i8_kernel<true, false><<<grid, threads, 0, stream>>>(a);
+    else if (h) swiglu_backward_i8_kernel<false, true><<<grid, threads, 0, stream>>>(a);
+    else swiglu_backward_i8_kernel<false, false><<<grid, threads, 0, stream>>>(a);
     return check_launch();
 }
