@@ -27,7 +27,11 @@
 // after each 1024 of k the accumulators are added to 32-bit integers in
 // registers while the tensor core fills the other half of tensor memory.  (A
 // conversion to integer takes 8 cycles a warp: 2300 cycles for a drain, against
-// 8200 of products.)
+// 8200 of products.)  Two CTAs share a tile of 256 x 256 where there are enough
+// (cta_group::2: each reads half of B from its shared memory).  8192 x 8192 x
+// 8192 takes 662 us: 59 to widen (6.8 TB/s), then 1.82 PFLOP/s in the products,
+// bound by the tensor cores at the clock the power limit leaves; 2048 x 16384 x
+// 2048 takes 100 us, 16 of them to widen, 512 tiles in 7 rounds of 76 pairs.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -231,23 +235,59 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
 // --------------------------------------------------------------- many rows ----
 
 constexpr int BM = 128, BK = 64;          // BK binary16 = one 128-byte swizzled row
-constexpr int kChunkSteps = 16;           // k-steps between two drains: 1024 of k
+constexpr int kChunkSteps = 16;           // k-steps between two drains: 1024 of k, the most that stays exact
+
+// Bytes k .. k+7 of a row (zeros from `n` on), as load_k16 loads sixteen.
+template <bool VEC>
+__device__ __forceinline__ uint2 load_k8(const int8_t *__restrict__ row, int64_t k, int64_t n, const int8_t *base,
+                                         const int8_t *end) {
+    const int8_t *p = row + k;
+    if (k + 8 <= n) {
+        if constexpr (VEC) {
+            return __ldg(reinterpret_cast<const uint2 *>(p));
+        } else {
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u);
+            const int8_t *q = p - off;
+            if (q >= base && q + (off ? 12 : 8) <= end) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
+                const uint32_t a = __ldg(w), b = __ldg(w + 1), c = off ? __ldg(w + 2) : 0u;
+                return make_uint2(__funnelshift_r(a, b, 8 * off), __funnelshift_r(b, c, 8 * off));
+            }
+        }
+    }
+    uint32_t r[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < n) r[i >> 2] |= uint32_t(uint8_t(p[i])) << (8 * (i & 3));
+    return make_uint2(r[0], r[1]);
+}
 
 // The rows of A, then those of B, as binary16 rows of Kp (a multiple of 64)
-// values, zeros past K: 16 values a thread.
+// values, zeros past K.  An item is 8 values, so that a warp's store covers 512
+// consecutive bytes (16 values an item, stored as two halves of each 32-byte
+// sector, took a third longer); two items a thread are in flight.
 template <bool VEC>
 __global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half *__restrict__ out) {
     grid_release();
-    const int64_t per = Kp / 16, items = (p.M + p.N) * per, stride = int64_t(gridDim.x) * 256;
-    for (int64_t it = blockIdx.x * int64_t(256) + threadIdx.x; it < items; it += stride) {
-        const int64_t r = it / per, k = (it - r * per) * 16;
-        const bool a = r < p.M;
-        const uint4 w = a ? load_k16<VEC>(p.A + r * p.lda, k, p.K, p.A, p.a_end)
-                          : load_k16<VEC>(p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
-        const uint32_t b[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-        uint4 *o = reinterpret_cast<uint4 *>(out + it * 16);
-        o[0] = make_uint4(widen2(b[0], 0x4140u), widen2(b[0], 0x4342u), widen2(b[1], 0x4140u), widen2(b[1], 0x4342u));
-        o[1] = make_uint4(widen2(b[2], 0x4140u), widen2(b[2], 0x4342u), widen2(b[3], 0x4140u), widen2(b[3], 0x4342u));
+    const uint32_t per = uint32_t(Kp / 8);
+    const int64_t items = (p.M + p.N) * per, stride = int64_t(gridDim.x) * 512;
+    for (int64_t i0 = blockIdx.x * int64_t(512) + threadIdx.x; i0 < items; i0 += stride) {
+        uint2 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t it = min(i0 + 256 * j, items - 1);       // past the end: the last one again
+            const int64_t r = items <= UINT32_MAX ? uint32_t(it) / per : it / per;
+            const int64_t k = (it - r * per) * 8;
+            w[j] = r < p.M ? load_k8<VEC>(p.A + r * p.lda, k, p.K, p.A, p.a_end)
+                           : load_k8<VEC>(p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i0 + 256 * j >= items) continue;
+            const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
+            *reinterpret_cast<uint4 *>(out + (i0 + 256 * j) * 8) =
+                make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+        }
     }
 }
 
@@ -641,8 +681,8 @@ template <int TY, int BN, int CTAS>
 int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     using T = TileCfg<BN, CTAS>;
     const int64_t Kp = padded_k(a.K);
-    const int64_t items = (a.M + a.N) * (Kp / 16);
-    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 32));
+    const int64_t items = (a.M + a.N) * (Kp / 8);
+    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
     if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) widen_kernel<true><<<wgrid, 256, 0, s>>>(a, Kp, ws);
     else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
     int rc = check_launch();
