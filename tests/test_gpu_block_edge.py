@@ -191,3 +191,25 @@ def test_captured_graphs_share_nothing(rp):
     torch.cuda.synchronize()
     for _, outs in graphs:
         assert all(same(a, b) for a, b in zip(outs, want))
+
+
+def test_rows_that_share_memory_are_refused(rp):
+    o = operands(6, 40, 1, True, 130)
+    one = o["x"][:1]
+    for bad in (dict(x=one.expand(6, 40)), dict(f=one.expand(6, 40)), dict(y=one.expand(6, 40))):
+        kw = dict(x=o["x"], f=o["f"], pre_gain=o["pre"], eps=EPS)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            rp.rmsnorm_residual(**kw)
+    with pytest.raises(ValueError):
+        rp.rmsnorm_residual(o["x"], o["f"], o["pre"], EPS, gate=o["gate"].expand(3, 40))
+    A = torch.ones(4, 64, dtype=torch.int8, device=DEV)
+    s = torch.ones(4, device=DEV)
+    with pytest.raises(ValueError):
+        rp.gemm_i8(A[:1].expand(4, 64), A.t(), s, s)
+    with pytest.raises(ValueError):
+        rp.gemm_i8(A, A.t(), s, s, out=torch.empty(1, 4, device=DEV).expand(4, 4))
+    with pytest.raises(ValueError):
+        rp.quantize_rows(one.expand(6, 40))
+    with pytest.raises(ValueError):
+        rp.dequantize_rows(A, s.view(4, 1), out=torch.empty(1, 64, device=DEV).expand(4, 64))

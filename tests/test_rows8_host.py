@@ -92,6 +92,8 @@ def test_rmsnorm_backward_refusals(L):
         for other in (A, B, C, D, W):
             assert call(**{k: other}) == -2, (k, other)
     assert call(dx=E, lddx=68) == -2 and call(h=E) == -2 and call(h=F) == -2 and call(dgamma=F + 8) == -2
+    for other in (A, B, C, D, E):
+        assert call(ws=other) == -2                          # scratch over an input
     assert call(cols=400000, ldx=400000, lds=12500, lddy=400000, ldres=400000, lddx=400000, ldh=400000) == -7
     assert call(rows=0) == 0
 
@@ -156,6 +158,8 @@ def test_edge_backward_refusals(L):
             if p != o:
                 assert call(**{o: ptr[p]}) == -2, (o, p)
     assert call(dx=ptr["dy"], lddx=68) == -2
+    for i in ("dy", "dh", "y", "f", "post", "gate", "pre"):
+        assert call(ws=ptr[i]) == -2, i                      # scratch over an input
     assert call(rows=0) == 0
 
 
@@ -220,3 +224,26 @@ def test_gemm_i8_refusals(L):
     assert call(ws=F) == -2
     assert call(K=131072, lda=131072, ldb=131072) == -7
     assert call(M=0) == 0 and call(N=0) == 0
+
+
+def test_binding_refuses_rows_that_share_memory():
+    """An expanded tensor's rows are one row in memory: reading or writing them at
+    a pitch of their width would leave it."""
+    import torch
+
+    import verifiable_repops_gemm_gb300 as rp
+    q, s = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 2)
+    assert rp._rows_i8(q, s, 32, "q")[1::2] == (64, 2)
+    assert rp._rows_i8(q[:1].expand(1, 64), s[:1], 32, "q")[1] == 64
+    assert rp._rows_i8(q[:, :60], s, 32, "q")[1] == 64
+    with pytest.raises(ValueError):
+        rp._rows_i8(q[:1].expand(4, 64), s, 32, "q")
+    with pytest.raises(ValueError):
+        rp._rows_i8(q, s[:1].expand(4, 2), 32, "q")
+    with pytest.raises(ValueError):
+        rp._pitch(torch.zeros(1).expand(4, 1), "x")
+    with pytest.raises(ValueError):
+        rp._rows_i8(q, s, 48, "q")
+    with pytest.raises(ValueError):
+        rp._rows_i8(q.t(), s, 32, "q")
+    assert rp._pitch(torch.zeros(0, 5).expand(0, 5), "x") == 5

@@ -634,10 +634,14 @@ def _row_operand(x, name):
     if x.dtype != torch.float32 or len(shape) != 2 or not x.is_cuda:
         raise ValueError("%s must be a 2-D float32 CUDA tensor with unit column stride" % name)
     ld, unit = x.stride()
-    cols = shape[1]
+    rows, cols = shape
     if cols > 1 and unit != 1:
         raise ValueError("%s must be a 2-D float32 CUDA tensor with unit column stride" % name)
-    return x.data_ptr(), ld if ld >= cols and ld > 0 else max(cols, 1)
+    if ld < cols or ld < 1:
+        if rows > 1 and cols > 0:            # an expanded or overlapping view: its rows share memory
+            raise ValueError("the rows of %s overlap (row stride %d, %d columns)" % (name, ld, cols))
+        ld = max(cols, 1)
+    return x.data_ptr(), ld
 
 
 def _row_out(x, out):
@@ -977,6 +981,16 @@ def _groups(cols, group):
     return -(-cols // group) if group else 1
 
 
+def _pitch(t, name):
+    """The row pitch of a 2-D tensor whose rows must not share memory."""
+    (rows, cols), ld = t.shape, t.stride(0)
+    if ld < cols or ld < 1:
+        if rows > 1 and cols > 0:
+            raise ValueError("the rows of %s overlap (row stride %d, %d columns)" % (name, ld, cols))
+        return max(cols, 1)
+    return ld
+
+
 def _rows_i8(q, scale, group, name):
     """(pointer, pitch, scale pointer, scale pitch) of rows in 8 bits: q int8
     (rows, cols) and scale float32 (rows, groups), unit column strides (a
@@ -989,7 +1003,7 @@ def _rows_i8(q, scale, group, name):
     n = _groups(cols, group)
     if scale.dtype != torch.float32 or scale.shape != (rows, n) or (n > 1 and scale.stride(1) != 1):
         raise ValueError("the scales of %s must be float32 of shape (rows, %d) with unit column stride" % (name, n))
-    return q.data_ptr(), max(q.stride(0), cols, 1), scale.data_ptr(), max(scale.stride(0), n, 1)
+    return q.data_ptr(), _pitch(q, name), scale.data_ptr(), _pitch(scale, "the scales of " + name)
 
 
 def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
@@ -1011,7 +1025,7 @@ def quantize_rows(x, *, group: int = 0, out=None, scale=None, stream=None):
         scale = torch.empty((rows, n), dtype=torch.float32, device=x.device)
     h = _stream_on_device(stream, x, out, scale)
     pq, ldq, ps, lds = _rows_i8(out, scale, group, "out")
-    rc = load().repops_quantize_rows_i8(rows, cols, x.data_ptr(), t, max(x.stride(0), cols, 1), group, pq, ldq, ps, lds, h)
+    rc = load().repops_quantize_rows_i8(rows, cols, x.data_ptr(), t, _pitch(x, "x"), group, pq, ldq, ps, lds, h)
     if rc:
         _capi.check(rc, "repops_quantize_rows_i8")
     return out, scale
@@ -1029,7 +1043,7 @@ def dequantize_rows(q, scale, *, group: int = 0, dtype=None, out=None, stream=No
         raise ValueError("out must have the shape of q, the dtype asked for and unit column stride")
     handle = _stream_on_device(stream, q, scale, out)
     rc = load().repops_dequantize_rows_i8(q.shape[0], q.shape[1], pq, ldq, ps, lds, group, out.data_ptr(),
-                                          _storage_type(out.dtype), max(out.stride(0), q.shape[1], 1), handle)
+                                          _storage_type(out.dtype), _pitch(out, "out"), handle)
     if rc:
         _capi.check(rc, "repops_dequantize_rows_i8")
     return out
@@ -1073,7 +1087,7 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
     rc = L.repops_gemm_i8(config, M, N, K, A.data_ptr(), max(lda, K), _scale_vector(a_scale, M, "a_scale"), B.data_ptr(),
                           max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
                           None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
-                          _storage_type(out.dtype), max(out.stride(0), N, 1), ws.data_ptr() if ws is not None else None,
+                          _storage_type(out.dtype), _pitch(out, "out"), ws.data_ptr() if ws is not None else None,
                           need, handle)
     if rc:
         _capi.check(rc, "repops_gemm_i8")

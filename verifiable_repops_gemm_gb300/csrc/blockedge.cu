@@ -1126,6 +1126,9 @@ extern "C" int repops_rmsnorm_residual_backward_f32(
             if (overlaps_any(outs[i], {outs[j]})) return REPOPS_ERR_ALIAS;
     }
     if (need == 0) return REPOPS_ERR_UNSUPPORTED;
+    if (overlaps_any({ws, ws ? ws_bytes : 0}, {{dy, dyb}, {dh, dhb}, {y, yb}, {f, fb}, {post_gain, vb}, {gate, gb},
+                                               {pre_gain, vb}}))
+        return REPOPS_ERR_ALIAS;
     Workspace w;
     int rc = w.get(ws, ws_bytes, need, stream);
     if (rc != REPOPS_OK) return rc;
@@ -1174,6 +1177,8 @@ extern "C" int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8
             if (overlaps_any(outs[i], {outs[j]})) return REPOPS_ERR_ALIAS;
     }
     if (need == 0) return REPOPS_ERR_UNSUPPORTED;
+    if (overlaps_any({ws, ws ? ws_bytes : 0}, {{x, xb}, {x_scale, sb}, {gamma, vb}, {dy, dyb}, {res, rb}}))
+        return REPOPS_ERR_ALIAS;
     Workspace w;
     int rc = w.get(ws, ws_bytes, need, stream);
     if (rc != REPOPS_OK) return rc;

@@ -681,12 +681,6 @@ template <int TY, int BN, int CTAS>
 int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
     using T = TileCfg<BN, CTAS>;
     const int64_t Kp = padded_k(a.K);
-    const int64_t items = (a.M + a.N) * (Kp / 8);
-    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
-    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) widen_kernel<true><<<wgrid, 256, 0, s>>>(a, Kp, ws);
-    else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
-    int rc = check_launch();
-    if (rc != REPOPS_OK) return rc;
     constexpr CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap ma, mb, mc;
     if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, T::B_ROWS))
@@ -701,10 +695,18 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
                       a.ldc < (int64_t(1) << 37) && make_map(&mc, ctype, csize, a.C, a.N, a.M, a.ldc, wide, 32);
     if (!c_tma) mc = ma;
     unsigned *status = nullptr;
-    if ((rc = status_word_address(&status)) != REPOPS_OK) return rc;
+    int rc = status_word_address(&status);
+    if (rc != REPOPS_OK) return rc;
     auto kern = CTAS == 2 ? gemm_i8_pair_kernel<TY> : gemm_i8_tile_kernel<TY, BN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return set_cuda_error(e);
+    // nothing has been launched so far: from here on only a launch can fail
+    const int64_t items = (a.M + a.N) * (Kp / 8);
+    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
+    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) widen_kernel<true><<<wgrid, 256, 0, s>>>(a, Kp, ws);
+    else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
+    rc = check_launch();
+    if (rc != REPOPS_OK) return rc;
     const TileMap tm{int(ceil_div(a.M, BM * CTAS)), int(ceil_div(a.N, BN)), 16 / CTAS};
     const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
     return launch_behind(kern, dim3(unsigned(std::min<int64_t>(tiles, sm_count() / CTAS) * CTAS)), kTileThreads,
