@@ -42,6 +42,7 @@ memory and streams.
                                     host-buffer calls (gemm_host, ..._host)
 """
 import ctypes
+import functools
 
 from . import _capi
 from ._capi import (ACT_GELU, ACT_NONE, LOADER_AUTO, LOADER_CPASYNC, LOADER_DIRECT, LOADER_TMA,
@@ -1056,6 +1057,11 @@ def _scale_vector(t, n, name):
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=1024)
+def _gemm_i8_workspace(config, M, N, K):
+    return load().repops_gemm_i8_workspace_bytes(config, M, N, K)
+
+
 def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, config: int = -1, stream=None):
     """out[i][j] = (sum_k A[i][k] * B[k][j]) * a_scale[i] * b_scale[j] (+ bias[j])
     for int8 CUDA tensors: the sum is exact, each step after it one binary32
@@ -1077,18 +1083,18 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
     if (K > 1 and (ua != 1 or ub != 1)) or (M > 1 and lda < K) or (N > 1 and ldb < K):
         raise ValueError("k must be contiguous: A with unit column stride, B a transposed view W.t() of (N, K) weights")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device)
+        out, ldc = torch.empty((M, N), dtype=out_dtype or torch.float32, device=A.device), max(N, 1)
     elif out.shape != (M, N) or (N > 1 and out.stride(1) != 1) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be (M, N) with unit column stride and the dtype asked for")
+    else:
+        ldc = _pitch(out, "out")
     handle = _stream_on_device(stream, A, B, a_scale, b_scale, bias, out)
-    L = load()
-    need = L.repops_gemm_i8_workspace_bytes(config, M, N, K)
+    need = _gemm_i8_workspace(config, M, N, K)
     ws = _workspace(need, A.device, stream) if need else None
-    rc = L.repops_gemm_i8(config, M, N, K, A.data_ptr(), max(lda, K), _scale_vector(a_scale, M, "a_scale"), B.data_ptr(),
-                          max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
-                          None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
-                          _storage_type(out.dtype), _pitch(out, "out"), ws.data_ptr() if ws is not None else None,
-                          need, handle)
+    rc = load().repops_gemm_i8(config, M, N, K, A.data_ptr(), max(lda, K), _scale_vector(a_scale, M, "a_scale"),
+                               B.data_ptr(), max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
+                               None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
+                               _storage_type(out.dtype), ldc, ws.data_ptr() if ws is not None else None, need, handle)
     if rc:
         _capi.check(rc, "repops_gemm_i8")
     return out
@@ -1112,6 +1118,16 @@ def _row_like(t, shape, name):
     return _row_operand(t, name)
 
 
+def _row_out_like(t, shape, device, name):
+    """(tensor, pointer, pitch) of a float32 output of `shape`, allocated when t
+    is None (and then not asked about what it is known to be)."""
+    import torch
+    if t is None:
+        t = torch.empty(shape, dtype=torch.float32, device=device)
+        return t, t.data_ptr(), max(shape[1], 1)
+    return (t,) + _row_like(t, shape, name)
+
+
 def _gain(t, cols, name):
     import torch
     if t is None:
@@ -1125,16 +1141,13 @@ def swiglu_backward_i8(g, g_scale, u, u_scale, dh, dg=None, du=None, *, group: i
     """(dg, du) of h = SiLU(g) * u with g and u in 8 bits: swiglu_backward of the
     restored rows, bit for bit (repops_swiglu_backward_i8).  h: an optional
     tensor that receives swiglu(g, u) as well.  One of dg, du, h may be dh."""
-    import torch
     pg, ldg, pgs, ldgs = _rows_i8(g, g_scale, group, "g")
     pu, ldu, pus, ldus = _rows_i8(u, u_scale, group, "u")
     if tuple(u.shape) != tuple(g.shape):
         raise ValueError("g and u differ in shape")
     pd, ldd = _row_like(dh, g.shape, "dh")
-    dg = torch.empty(g.shape, dtype=torch.float32, device=g.device) if dg is None else dg
-    du = torch.empty(g.shape, dtype=torch.float32, device=g.device) if du is None else du
-    pdg, lddg = _row_like(dg, g.shape, "dg")
-    pdu, lddu = _row_like(du, g.shape, "du")
+    dg, pdg, lddg = _row_out_like(dg, g.shape, g.device, "dg")
+    du, pdu, lddu = _row_out_like(du, g.shape, g.device, "du")
     ph, ldh = _row_like(h, g.shape, "h")
     handle = _stream_on_device(stream, g, g_scale, u, u_scale, dh, dg, du, h)
     rc = load().repops_swiglu_backward_i8(g.shape[0], g.shape[1], pg, ldg, pgs, ldgs, pu, ldu, pus, ldus, group, pd, ldd,
@@ -1154,9 +1167,8 @@ def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, gro
     rows, cols = x.shape
     pd, ldd = _row_like(dy, x.shape, "dy")
     pr, ldr = _row_like(res, x.shape, "res")
-    dx = torch.empty(x.shape, dtype=torch.float32, device=x.device) if dx is None else dx
+    dx, pdx, lddx = _row_out_like(dx, x.shape, x.device, "dx")
     dgamma = torch.empty(cols, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
-    pdx, lddx = _row_like(dx, x.shape, "dx")
     ph, ldh = _row_like(h, x.shape, "h")
     handle = _stream_on_device(stream, x, x_scale, gamma, dy, res, dx, h, dgamma)
     if rows == 0 or cols == 0:
@@ -1197,19 +1209,17 @@ def rmsnorm_residual(x, f, pre_gain, eps: float = 1e-5, *, post_gain=None, gate=
     (cols,), or (G, cols) with one row for each G-th of the rows in order (a
     gate a sequence, or with G = rows a gate a token).  y and h may each be x or
     f itself."""
-    import torch
     rows, cols = x.shape
     px, ldx = _row_operand(x, "x")
     pf, ldf = _row_like(f, x.shape, "f")
     pg, ldg, per, _ = _gate_rows(gate, rows, cols)
-    y = torch.empty(x.shape, dtype=torch.float32, device=x.device) if y is None else y
-    if pre_gain is None:
-        if h is not None:
-            raise ValueError("h needs pre_gain")
-    elif h is None:
-        h = torch.empty(x.shape, dtype=torch.float32, device=x.device)
-    py, ldy = _row_like(y, x.shape, "y")
-    ph, ldh = _row_like(h, x.shape, "h")
+    y, py, ldy = _row_out_like(y, x.shape, x.device, "y")
+    if pre_gain is not None:
+        h, ph, ldh = _row_out_like(h, x.shape, x.device, "h")
+    elif h is not None:
+        raise ValueError("h needs pre_gain")
+    else:
+        ph, ldh = None, 0
     handle = _stream_on_device(stream, x, f, pre_gain, post_gain, gate, y, h)
     rc = load().repops_rmsnorm_residual_f32(rows, cols, px, ldx, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg,
                                             per, ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"),
@@ -1242,8 +1252,8 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
     def new(*shape):
         return torch.empty(shape, dtype=torch.float32, device=f.device)
 
-    dx = new(rows, cols) if dx is None else dx
-    df = new(rows, cols) if df is None else df
+    dx, pdx, lddx = _row_out_like(dx, f.shape, f.device, "dx")
+    df, pdf, lddf = _row_out_like(df, f.shape, f.device, "df")
     dpre = new(cols) if dpre is None and pre_gain is not None else dpre
     if post_gain is None:
         dpost = None
@@ -1255,8 +1265,6 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
         dgate = torch.empty(gate.shape, dtype=torch.float32, device=f.device)
     elif tuple(dgate.shape) != tuple(gate.shape):
         raise ValueError("dgate must have the shape of gate")
-    pdx, lddx = _row_like(dx, f.shape, "dx")
-    pdf, lddf = _row_like(df, f.shape, "df")
     pdg, lddg, _, _ = _gate_rows(dgate, rows, cols)
     handle = _stream_on_device(stream, dy, dh, y, f, pre_gain, post_gain, gate, dx, df, dpre, dpost, dgate)
     if rows == 0 or cols == 0:
