@@ -587,9 +587,311 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     tile_kernel<TY, 256, 2>(map_a, map_b, map_c, p, tm, ksteps, c_tma, status);
 }
 
+// ------------------------------------------------------------ middling rows ----
+
+// Tokens from a couple of dozen to a thousand or so: B streams through once as
+// bytes and is widened on its way into tensor memory, where it is the product's
+// first operand (128 channels x k), so that its binary16 form never passes
+// through shared memory or DRAM.  The tokens, few, are widened to scratch before
+// and loaded by TMA.  All the (tile, 128-k step) pairs form one line that the CTAs share
+// evenly: a tile split between CTAs is added up in 32-bit integers by atomics
+// (whole numbers: any order gives the same bits), and the CTA whose part is the
+// last to be counted stores it.  No CTA waits for another.
+constexpr int kStreamK = 128;             // k of a step: a 128-byte row of B
+constexpr int kStreamChunk = 1024 / kStreamK;
+constexpr int kStreamThreads = 576;       // 8 epilogue warps, 8 widening warps, a TMA warp, an MMA warp
+constexpr int kStreamCtas = 152;
+
+// BT tokens a tile.  Tensor memory: two accumulators of BT columns, then a
+// stage's widened channels (64 columns each).
+template <int BT>
+struct StreamCfg {
+    static constexpr int W_BYTES = BM * kStreamK;
+    static constexpr int BOX_BYTES = BT * 128;                   // BT tokens x 64 of k
+    static constexpr int STAGE_BYTES = W_BYTES + 2 * BOX_BYTES;
+    static constexpr int STAGES = 196608 / STAGE_BYTES;          // 6 or 4
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES;
+    static constexpr int A_COL = 2 * BT;
+    static constexpr int COLS = BT / 2;                          // an epilogue warp's tokens
+    static_assert(A_COL + STAGES * kStreamK / 2 <= 512 && STAGES % 2 == 0);
+};
+
+// The line of steps: tile t = channel tile * tiles_t + token tile takes steps
+// t * ksteps .. + ksteps - 1; CTA c of `ctas` takes [begin(c), begin(c + 1)).
+struct StreamMap {
+    int64_t total;
+    int tiles_t, ksteps, ctas;
+    __device__ __forceinline__ int64_t begin(int c) const { return total * c / ctas; }
+    // the CTA that holds step u
+    __device__ __forceinline__ int owner(int64_t u) const { return int(((u + 1) * ctas - 1) / total); }
+};
+
+// Scratch: the tokens in binary16 (rows of Kp), the sums of split tiles (one for
+// each CTA: the tile that it begins and does not finish), their counts of steps,
+// and B at a 16-byte pitch where TMA cannot read it in place.
+struct StreamScratch {
+    __half *tokens;
+    int *sums, *counts;
+    int8_t *copy;
+};
+
+// Widens the tokens, clears the sums and counts, copies B where COPY.
+template <bool VEC, bool COPY>
+__global__ void __launch_bounds__(256) stream_prepare_kernel(I8Args p, int64_t Kp, StreamScratch w, int64_t clear16) {
+    grid_release();
+    const int64_t i0 = blockIdx.x * int64_t(256) + threadIdx.x, stride = int64_t(gridDim.x) * 256;
+    const int64_t per = Kp / 8;
+    for (int64_t i = i0; i < p.M * per; i += stride) {
+        const int64_t r = i / per;
+        const uint2 v = load_k8<VEC>(p.A + r * p.lda, (i - r * per) * 8, p.K, p.A, p.a_end);
+        const uint32_t a = v.x ^ 0x80808080u, b = v.y ^ 0x80808080u;
+        *reinterpret_cast<uint4 *>(w.tokens + i * 8) =
+            make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+    }
+    uint4 *clear = reinterpret_cast<uint4 *>(w.sums);
+    for (int64_t i = i0; i < clear16; i += stride) clear[i] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (COPY) {
+        const int64_t per16 = Kp / 16;
+        for (int64_t i = i0; i < p.N * per16; i += stride) {
+            const int64_t r = i / per16;
+            reinterpret_cast<uint4 *>(w.copy)[i] =
+                load_k16<false>(p.B + r * p.ldb, (i - r * per16) * 16, p.K, p.B, p.b_end);
+        }
+    }
+}
+
+// The 256 epilogue threads.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int TY, int BT>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w, I8Args p,
+                      StreamMap sm, StreamScratch ws, unsigned *status) {
+    using T = StreamCfg<BT>;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[T::STAGES], ready[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int last;
+    uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int64_t u0 = sm.begin(blockIdx.x), u1 = sm.begin(blockIdx.x + 1);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < T::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&ready[s], 4);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        mbar_init(&drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == 17) tmem_alloc<1>(&tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    grid_wait();                                               // the widened tokens, the cleared sums
+
+    // Every wait gives up after its limit, as in tile_kernel.
+    if (warp == 16) {
+        if (elect_one()) {
+            prefetch_tensormap(&map_w);
+            prefetch_tensormap(&map_t);
+            int64_t tile = u0 / sm.ksteps;
+            int k = int(u0 - tile * sm.ksteps), s = 0, issued = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int64_t u = u0; u < u1; ++u, ++issued) {
+                if (!mbar_wait_bounded(&empty[s], phase)) {
+                    ok = false;
+                    break;
+                }
+                const int ch = int(tile / sm.tiles_t), tok = int(tile - int64_t(ch) * sm.tiles_t);
+                uint8_t *st = stages + s * T::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[s], T::STAGE_BYTES);
+                tma_load_2d(st, &map_w, &full[s], k * kStreamK, ch * BM);
+                tma_load_2d(st + T::W_BYTES, &map_t, &full[s], k * kStreamK, tok * BT);
+                tma_load_2d(st + T::W_BYTES + T::BOX_BYTES, &map_t, &full[s], k * kStreamK + 64, tok * BT);
+                if (++k == sm.ksteps) {
+                    k = 0;
+                    ++tile;
+                }
+                if (++s == T::STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                atomicOr(status, 1u);
+                for (int i = max(0, issued - T::STAGES); i < issued; ++i)
+                    mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
+            }
+        }
+    } else if (warp == 17) {
+        if (elect_one()) {
+            constexpr uint32_t idesc = idesc_f16(BM, BT);
+            const uint32_t base = smem_addr(stages) + T::W_BYTES;
+            int s = 0, b = 0, k = int(u0 % sm.ksteps);
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int64_t u = u0; u < u1 && ok;) {
+                // to the end of a chunk, of the tile or of this CTA's steps
+                const int steps = int(min(min(int64_t(kStreamChunk), int64_t(sm.ksteps - k)), u1 - u));
+                if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int i = 0; i < steps; ++i) {
+                    if (!mbar_wait_bounded(&full[s], phase) || !mbar_wait_bounded(&ready[s], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = tmem + T::A_COL + s * (kStreamK / 2);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t db = smem_desc_sw128(base + s * T::STAGE_BYTES + h * T::BOX_BYTES);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tc_mma_f16_tmem(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc, i > 0 || h > 0 || j > 0);
+                    }
+                    tc_commit<1>(&empty[s]);
+                    if (++s == T::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) tc_commit<1>(&acc_full[b]);
+                b ^= 1;
+                if (b == 0) acc_phase ^= 1u;
+                u += steps;
+                k += steps;
+                if (k == sm.ksteps) k = 0;
+            }
+            if (!ok) {
+                atomicOr(status, 1u);
+                tc_commit<1>(&drained);
+                mbar_wait_bounded(&drained, 0u);
+            }
+        }
+    } else if (warp >= 8) {
+        // four warps widen the even steps, four the odd: a lane its channel
+        const int row = 32 * (warp & 3) + lane, n = int(u1 - u0);
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        int s = (warp - 8) >> 2;
+        uint32_t phase = 0;
+        for (int i = s; i < n; i += 2) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase))) {
+                if (lane == 0) atomicOr(status, 1u);
+                break;
+            }
+            tc_fence_after();                                  // the products that read this stage's columns
+            const uint8_t *st = stages + s * T::STAGE_BYTES + row * kStreamK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(st + (((4 * h + c) ^ (row & 7)) << 4));
+                    const uint32_t q[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[8 * c + 2 * e] = widen2(q[e], 0x4140u);
+                        v[8 * c + 2 * e + 1] = widen2(q[e], 0x4342u);
+                    }
+                }
+                tmem_store32(tmem + lanes + T::A_COL + s * (kStreamK / 2) + 32 * h, v);
+            }
+            tmem_store_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[s]);
+            s += 2;
+            if (s >= T::STAGES) {
+                s -= T::STAGES;
+                phase ^= 1u;
+            }
+        }
+    } else {
+        const int half = warp >> 2;                            // tokens half * COLS .. of the tile
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        int b = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        // a warp that gave up still meets the others at their barriers
+        for (int64_t u = u0; u < u1;) {
+            const int64_t tile = u / sm.ksteps, start = tile * sm.ksteps;
+            const int steps = int(min(start + sm.ksteps, u1) - u);
+            const int ch = int(tile / sm.tiles_t), tok = int(tile - int64_t(ch) * sm.tiles_t);
+            const int64_t n = int64_t(ch) * BM + 32 * (warp & 3) + lane, m0 = int64_t(tok) * BT + half * T::COLS;
+            int acc[T::COLS];
+#pragma unroll
+            for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
+            for (int c = 0; c < steps && ok; c += kStreamChunk) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], phase));
+                if (!ok) {
+                    if (lane == 0) atomicOr(status, 1u);
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < T::COLS; j += 16) {
+                    uint32_t v[16];
+                    tmem_load16(tmem + lanes + b * BT + half * T::COLS + j, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[b]);
+                b ^= 1;
+                if (b == 0) phase ^= 1u;
+            }
+            u += steps;
+            if (steps < sm.ksteps) {
+                const int slot = sm.owner(start);
+                int *sum = ws.sums + (int64_t(slot) * BT + half * T::COLS) * BM + 32 * (warp & 3) + lane;
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < T::COLS; ++i) atomicAdd(sum + i * BM, acc[i]);
+                }
+                __threadfence();
+                epilogue_sync();
+                if (threadIdx.x == 0) last = atomicAdd(ws.counts + slot, steps) + steps == sm.ksteps;
+                epilogue_sync();
+                if (!last) continue;
+                __threadfence();
+#pragma unroll
+                for (int i = 0; i < T::COLS; ++i) acc[i] = __ldcg(sum + i * BM);
+            }
+            if (!ok) continue;
+            float sa[T::COLS / 32];
+#pragma unroll
+            for (int i = 0; i < T::COLS / 32; ++i) sa[i] = __ldg(p.sa + min(m0 + 32 * i + lane, p.M - 1));
+            const int64_t nn = min(n, p.N - 1);                // past the end: not stored
+            const float sb = __ldg(p.sb + nn), bias = p.bias ? __ldg(p.bias + nn) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < T::COLS; ++i) {
+                float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i]), __shfl_sync(0xffffffffu, sa[i / 32], i % 32)), sb);
+                if (p.bias) v = __fadd_rn(v, bias);
+                if (n < p.N && m0 + i < p.M) store_c<TY>(p.C, (m0 + i) * p.ldc + n, v);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 17) tmem_free<1>(tmem, 512);
+}
+
 // ------------------------------------------------------------------- host ----
 
-enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_PAIR, CFG_TILE128, CFG_TILE64, CFG_COUNT };
+enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_PAIR, CFG_TILE128, CFG_TILE64, CFG_STREAM, CFG_COUNT };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -713,13 +1015,78 @@ int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
                          T::SMEM, s, ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
 }
 
+// ---- middling rows
+
+int64_t stream_k(int64_t K) { return ceil_div(K, kStreamK) * kStreamK; }
+
+// Tokens a tile.
+int stream_tokens(int64_t M) { return M <= 64 ? 64 : 128; }
+
+StreamMap stream_map(int64_t M, int64_t N, int64_t K) {
+    StreamMap sm;
+    sm.tiles_t = int(ceil_div(M, stream_tokens(M)));
+    sm.ksteps = int(ceil_div(K, kStreamK));
+    sm.total = ceil_div(N, BM) * sm.tiles_t * sm.ksteps;
+    sm.ctas = int(std::min<int64_t>(kStreamCtas, sm.total));
+    return sm;
+}
+
+// Offsets of the scratch's parts in bytes; the last is its size.
+struct StreamLayout {
+    uint64_t sums, counts, copy, bytes;
+};
+StreamLayout stream_layout(int64_t M, int64_t N, int64_t K) {
+    const uint64_t kp = uint64_t(stream_k(K)), ctas = uint64_t(stream_map(M, N, K).ctas);
+    StreamLayout l;
+    l.sums = uint64_t(M) * kp * 2u;
+    l.counts = l.sums + ctas * BM * uint64_t(stream_tokens(M)) * 4u;
+    l.copy = l.counts + (ctas * 4u + 15u) / 16u * 16u;
+    l.bytes = l.copy + uint64_t(N) * kp;
+    return l;
+}
+
+template <int TY, int BT>
+int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
+    using T = StreamCfg<BT>;
+    const int64_t Kp = stream_k(a.K);
+    const StreamMap sm = stream_map(a.M, a.N, a.K);
+    const StreamLayout l = stream_layout(a.M, a.N, a.K);
+    const StreamScratch w{reinterpret_cast<__half *>(ws), reinterpret_cast<int *>(ws + l.sums),
+                          reinterpret_cast<int *>(ws + l.counts), reinterpret_cast<int8_t *>(ws + l.copy)};
+    const bool in_place = operand_vec(a.B, a.ldb) && a.ldb < (int64_t(1) << 39), vec = operand_vec(a.A, a.lda);
+    CUtensorMap mt, mw;
+    if (!make_map(&mt, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.tokens, Kp, a.M, Kp, 64, BT) ||
+        !(in_place ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.B, a.K, a.N, a.ldb, kStreamK, BM)
+                   : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.copy, Kp, a.N, Kp, kStreamK, BM)))
+        return REPOPS_ERR_UNSUPPORTED;
+    unsigned *status = nullptr;
+    int rc = status_word_address(&status);
+    if (rc != REPOPS_OK) return rc;
+    auto kern = gemm_i8_stream_kernel<TY, BT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    // nothing has been launched so far: from here on only a launch can fail
+    const int64_t clear16 = int64_t((l.copy - l.sums) / 16);
+    const int64_t items = std::max({a.M * (Kp / 8), clear16, in_place ? int64_t(0) : a.N * (Kp / 16)});
+    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 8));
+    auto prep = in_place ? vec ? stream_prepare_kernel<true, false> : stream_prepare_kernel<false, false>
+                         : vec ? stream_prepare_kernel<true, true> : stream_prepare_kernel<false, true>;
+    prep<<<grid, 256, 0, s>>>(a, Kp, w, clear16);
+    rc = check_launch();
+    if (rc != REPOPS_OK) return rc;
+    return launch_behind(kern, dim3(unsigned(sm.ctas)), kStreamThreads, T::SMEM, s, mt, mw, a, sm, w, status);
+}
+
 template <int TY>
 int run_i8(int cfg, const I8Args &a, void *ws, cudaStream_t s) {
     switch (cfg) {
         case CFG_ROWS: return launch_rows<TY>(a, s);
         case CFG_PAIR: return launch_tile<TY, 256, 2>(a, static_cast<__half *>(ws), s);
         case CFG_TILE128: return launch_tile<TY, 128, 1>(a, static_cast<__half *>(ws), s);
-        default: return launch_tile<TY, 64, 1>(a, static_cast<__half *>(ws), s);
+        case CFG_TILE64: return launch_tile<TY, 64, 1>(a, static_cast<__half *>(ws), s);
+        default:
+            return stream_tokens(a.M) == 64 ? launch_stream<TY, 64>(a, static_cast<uint8_t *>(ws), s)
+                                            : launch_stream<TY, 128>(a, static_cast<uint8_t *>(ws), s);
     }
 }
 
@@ -739,7 +1106,9 @@ extern "C" uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_
         M > (int64_t(1) << 40) || N > (int64_t(1) << 40))
         return 0;
     if (config == CFG_AUTO) config = auto_config(M, N, K);
-    return config == CFG_ROWS ? 0 : tile_workspace(M, N, K);
+    return config == CFG_ROWS     ? 0
+           : config == CFG_STREAM ? stream_layout(M, N, K).bytes
+                                  : tile_workspace(M, N, K);
 }
 
 extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
