@@ -593,51 +593,40 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
 // bytes and is widened on its way into tensor memory, where it is the product's
 // first operand (128 channels x k), so that its binary16 form never passes
 // through shared memory or DRAM.  The tokens, few, are widened to scratch before
-// and loaded by TMA.  All the (tile, 128-k step) pairs form one line that the CTAs share
-// evenly: a tile split between CTAs is added up in 32-bit integers by atomics
-// (whole numbers: any order gives the same bits), and the CTA whose part is the
-// last to be counted stores it.  No CTA waits for another.
+// and loaded by TMA.  Where there are fewer tiles than SMs a cluster shares a
+// tile's k: each CTA leaves its 32-bit sums in shared memory, and after the
+// cluster's barrier each adds and stores its share of the tokens (whole numbers:
+// any split gives the same bits).
 constexpr int kStreamK = 128;             // k of a step: a 128-byte row of B
 constexpr int kStreamChunk = 1024 / kStreamK;
-constexpr int kStreamThreads = 576;       // 8 epilogue warps, 8 widening warps, a TMA warp, an MMA warp
-constexpr int kStreamCtas = 152;
+constexpr int kStreamThreads = 608;       // 8 epilogue warps, 8 widening warps, a TMA warp each for B and tokens, an MMA warp
 
-// BT tokens a tile.  Tensor memory: two accumulators of BT columns, then a
-// stage's widened channels (64 columns each).
+// BT tokens a tile.  Three rings: B's bytes (freed once widened), the tokens in
+// shared memory and the widened channels in tensor memory (both freed by the
+// products).  Tensor memory: two accumulators of BT columns, then 64 columns for
+// each stage's widened channels.
 template <int BT>
 struct StreamCfg {
-    static constexpr int W_BYTES = BM * kStreamK;
-    static constexpr int BOX_BYTES = BT * 128;                   // BT tokens x 64 of k
-    static constexpr int STAGE_BYTES = W_BYTES + 2 * BOX_BYTES;
-    static constexpr int STAGES = 196608 / STAGE_BYTES;          // 6 or 4
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES;
+    static constexpr int W_BYTES = BM * kStreamK, BOX_BYTES = BT * 128, T_BYTES = 2 * BOX_BYTES;
+    static constexpr int T_STAGES = 4;
+    static constexpr int W_STAGES = (229376 - T_STAGES * T_BYTES) / W_BYTES;     // 10 or 6
+    static constexpr int SMEM = 1024 + W_STAGES * W_BYTES + T_STAGES * T_BYTES;
     static constexpr int A_COL = 2 * BT;
     static constexpr int COLS = BT / 2;                          // an epilogue warp's tokens
-    static_assert(A_COL + STAGES * kStreamK / 2 <= 512 && STAGES % 2 == 0);
+    static_assert(A_COL + T_STAGES * kStreamK / 2 <= 512 && W_STAGES % 2 == 0 && T_STAGES % 2 == 0);
 };
 
-// The line of steps: tile t = channel tile * tiles_t + token tile takes steps
-// t * ksteps .. + ksteps - 1; CTA c of `ctas` takes [begin(c), begin(c + 1)).
+// Tile t = channel tile * tiles_t + token tile; `parts` CTAs share a tile (its
+// cluster), CTA r the k-steps [first(r), first(r + 1)).
 struct StreamMap {
-    int64_t total;
-    int tiles_t, ksteps, ctas;
-    __device__ __forceinline__ int64_t begin(int c) const { return total * c / ctas; }
-    // the CTA that holds step u
-    __device__ __forceinline__ int owner(int64_t u) const { return int(((u + 1) * ctas - 1) / total); }
+    int tiles, tiles_t, ksteps, parts;
+    __device__ __forceinline__ int first(int r) const { return int(int64_t(ksteps) * r / parts); }
 };
 
-// Scratch: the tokens in binary16 (rows of Kp), the sums of split tiles (one for
-// each CTA: the tile that it begins and does not finish), their counts of steps,
-// and B at a 16-byte pitch where TMA cannot read it in place.
-struct StreamScratch {
-    __half *tokens;
-    int *sums, *counts;
-    int8_t *copy;
-};
-
-// Widens the tokens, clears the sums and counts, copies B where COPY.
+// Widens the tokens (rows of Kp) and copies B to rows of Kp where COPY.
 template <bool VEC, bool COPY>
-__global__ void __launch_bounds__(256) stream_prepare_kernel(I8Args p, int64_t Kp, StreamScratch w, int64_t clear16) {
+__global__ void __launch_bounds__(256)
+stream_prepare_kernel(I8Args p, int64_t Kp, __half *__restrict__ tokens, int8_t *__restrict__ copy) {
     grid_release();
     const int64_t i0 = blockIdx.x * int64_t(256) + threadIdx.x, stride = int64_t(gridDim.x) * 256;
     const int64_t per = Kp / 8;
@@ -645,41 +634,41 @@ __global__ void __launch_bounds__(256) stream_prepare_kernel(I8Args p, int64_t K
         const int64_t r = i / per;
         const uint2 v = load_k8<VEC>(p.A + r * p.lda, (i - r * per) * 8, p.K, p.A, p.a_end);
         const uint32_t a = v.x ^ 0x80808080u, b = v.y ^ 0x80808080u;
-        *reinterpret_cast<uint4 *>(w.tokens + i * 8) =
+        *reinterpret_cast<uint4 *>(tokens + i * 8) =
             make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
     }
-    uint4 *clear = reinterpret_cast<uint4 *>(w.sums);
-    for (int64_t i = i0; i < clear16; i += stride) clear[i] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (COPY) {
         const int64_t per16 = Kp / 16;
         for (int64_t i = i0; i < p.N * per16; i += stride) {
             const int64_t r = i / per16;
-            reinterpret_cast<uint4 *>(w.copy)[i] =
+            reinterpret_cast<uint4 *>(copy)[i] =
                 load_k16<false>(p.B + r * p.ldb, (i - r * per16) * 16, p.K, p.B, p.b_end);
         }
     }
 }
 
-// The 256 epilogue threads.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 template <int TY, int BT>
 __global__ void __launch_bounds__(kStreamThreads, 1)
 gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_constant__ CUtensorMap map_w, I8Args p,
-                      StreamMap sm, StreamScratch ws, unsigned *status) {
+                      StreamMap sm, int b_in_place, int c_vec, unsigned *status) {
     using T = StreamCfg<BT>;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[T::STAGES], ready[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t w_full[T::W_STAGES], w_empty[T::W_STAGES];
+    __shared__ uint64_t ready[T::T_STAGES], used[T::T_STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
-    __shared__ int last;
-    uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    uint8_t *w_ring = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u), *t_ring = w_ring + T::W_STAGES * T::W_BYTES;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int64_t u0 = sm.begin(blockIdx.x), u1 = sm.begin(blockIdx.x + 1);
+    const int rank = sm.parts == 1 ? 0 : int(cluster_rank());
+    const int tile0 = int(blockIdx.x) / sm.parts, stride = int(gridDim.x) / sm.parts;
+    const int k0 = sm.first(rank), steps = sm.first(rank + 1) - k0;     // of every tile
     if (threadIdx.x == 0) {
-        for (int s = 0; s < T::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&ready[s], 4);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < T::W_STAGES; ++s) {
+            mbar_init(&w_full[s], 1);
+            mbar_init(&w_empty[s], 4);
+        }
+        for (int s = 0; s < T::T_STAGES; ++s) {
+            mbar_init(&ready[s], 5);                           // the tokens' copy and four widening warps
+            mbar_init(&used[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -688,89 +677,90 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         mbar_init(&drained, 1);
         fence_barrier_init();
     }
-    if (warp == 17) tmem_alloc<1>(&tmem_slot, 512);
+    if (warp == 18) tmem_alloc<1>(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    grid_wait();                                               // the widened tokens, the cleared sums
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     // Every wait gives up after its limit, as in tile_kernel.
-    if (warp == 16) {
+    if (warp == 16 || warp == 17) {
         if (elect_one()) {
-            prefetch_tensormap(&map_w);
-            prefetch_tensormap(&map_t);
-            int64_t tile = u0 / sm.ksteps;
-            int k = int(u0 - tile * sm.ksteps), s = 0, issued = 0;
+            const bool weights = warp == 16;
+            const int stages = weights ? T::W_STAGES : T::T_STAGES;
+            uint64_t *full = weights ? w_full : ready, *empty = weights ? w_empty : used;
+            prefetch_tensormap(weights ? &map_w : &map_t);
+            // B in place does not depend on the kernel before
+            if (!weights || !b_in_place) grid_wait();
+            int s = 0, issued = 0;
             uint32_t phase = 1;
             bool ok = true;
-            for (int64_t u = u0; u < u1; ++u, ++issued) {
-                if (!mbar_wait_bounded(&empty[s], phase)) {
-                    ok = false;
-                    break;
-                }
-                const int ch = int(tile / sm.tiles_t), tok = int(tile - int64_t(ch) * sm.tiles_t);
-                uint8_t *st = stages + s * T::STAGE_BYTES;
-                mbar_arrive_expect_tx(&full[s], T::STAGE_BYTES);
-                tma_load_2d(st, &map_w, &full[s], k * kStreamK, ch * BM);
-                tma_load_2d(st + T::W_BYTES, &map_t, &full[s], k * kStreamK, tok * BT);
-                tma_load_2d(st + T::W_BYTES + T::BOX_BYTES, &map_t, &full[s], k * kStreamK + 64, tok * BT);
-                if (++k == sm.ksteps) {
-                    k = 0;
-                    ++tile;
-                }
-                if (++s == T::STAGES) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (!ok) {
-                atomicOr(status, 1u);
-                for (int i = max(0, issued - T::STAGES); i < issued; ++i)
-                    mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
-            }
-        }
-    } else if (warp == 17) {
-        if (elect_one()) {
-            constexpr uint32_t idesc = idesc_f16(BM, BT);
-            const uint32_t base = smem_addr(stages) + T::W_BYTES;
-            int s = 0, b = 0, k = int(u0 % sm.ksteps);
-            uint32_t phase = 0, acc_phase = 1;
-            bool ok = true;
-            for (int64_t u = u0; u < u1 && ok;) {
-                // to the end of a chunk, of the tile or of this CTA's steps
-                const int steps = int(min(min(int64_t(kStreamChunk), int64_t(sm.ksteps - k)), u1 - u));
-                if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                for (int i = 0; i < steps; ++i) {
-                    if (!mbar_wait_bounded(&full[s], phase) || !mbar_wait_bounded(&ready[s], phase)) {
+            for (int t = tile0; t < sm.tiles && ok; t += stride) {
+                const int ch = t / sm.tiles_t, tok = t - ch * sm.tiles_t;
+                for (int k = k0; k < k0 + steps; ++k, ++issued) {
+                    if (!mbar_wait_bounded(&empty[s], phase)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t a = tmem + T::A_COL + s * (kStreamK / 2);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t db = smem_desc_sw128(base + s * T::STAGE_BYTES + h * T::BOX_BYTES);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tc_mma_f16_tmem(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc, i > 0 || h > 0 || j > 0);
+                    if (weights) {
+                        mbar_arrive_expect_tx(&full[s], T::W_BYTES);
+                        tma_load_2d(w_ring + s * T::W_BYTES, &map_w, &full[s], k * kStreamK, ch * BM);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], T::T_BYTES);
+                        tma_load_3d(t_ring + s * T::T_BYTES, &map_t, &full[s], 0, tok * BT, 2 * k);
                     }
-                    tc_commit<1>(&empty[s]);
-                    if (++s == T::STAGES) {
+                    if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) tc_commit<1>(&acc_full[b]);
-                b ^= 1;
-                if (b == 0) acc_phase ^= 1u;
-                u += steps;
-                k += steps;
-                if (k == sm.ksteps) k = 0;
+            }
+            if (!ok) {
+                atomicOr(status, 1u);
+                for (int i = max(0, issued - stages); i < issued; ++i)
+                    mbar_wait_bounded(&full[i % stages], uint32_t(i / stages) & 1u);
+            }
+        }
+    } else if (warp == 18) {
+        if (elect_one()) {
+            constexpr uint32_t idesc = idesc_f16(BM, BT);
+            const uint32_t base = smem_addr(t_ring);
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int t = tile0; t < sm.tiles && ok; t += stride) {
+                for (int c = 0; c < steps && ok; c += kStreamChunk) {
+                    if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int n = min(kStreamChunk, steps - c);
+                    for (int i = 0; i < n; ++i) {
+                        if (!mbar_wait_bounded(&ready[s], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a = tmem + T::A_COL + s * (kStreamK / 2);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t db = smem_desc_sw128(base + s * T::T_BYTES + h * T::BOX_BYTES);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tc_mma_f16_tmem(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc,
+                                                i > 0 || h > 0 || j > 0);
+                        }
+                        tc_commit<1>(&used[s]);
+                        if (++s == T::T_STAGES) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) tc_commit<1>(&acc_full[b]);
+                    b ^= 1;
+                    if (b == 0) acc_phase ^= 1u;
+                }
             }
             if (!ok) {
                 atomicOr(status, 1u);
@@ -780,17 +770,17 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         }
     } else if (warp >= 8) {
         // four warps widen the even steps, four the odd: a lane its channel
-        const int row = 32 * (warp & 3) + lane, n = int(u1 - u0);
+        const int row = 32 * (warp & 3) + lane, n = steps * ((sm.tiles - tile0 + stride - 1) / stride);
         const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-        int s = (warp - 8) >> 2;
-        uint32_t phase = 0;
-        for (int i = s; i < n; i += 2) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase))) {
+        int sw = (warp - 8) >> 2, sa = sw;
+        uint32_t w_phase = 0, a_phase = 1;
+        for (int i = sw; i < n; i += 2) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&w_full[sw], w_phase) && mbar_wait_bounded(&used[sa], a_phase))) {
                 if (lane == 0) atomicOr(status, 1u);
                 break;
             }
             tc_fence_after();                                  // the products that read this stage's columns
-            const uint8_t *st = stages + s * T::STAGE_BYTES + row * kStreamK;
+            const uint8_t *st = w_ring + sw * T::W_BYTES + row * kStreamK;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t v[32];
@@ -804,16 +794,23 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                         v[8 * c + 2 * e + 1] = widen2(q[e], 0x4342u);
                     }
                 }
-                tmem_store32(tmem + lanes + T::A_COL + s * (kStreamK / 2) + 32 * h, v);
+                tmem_store32(tmem + lanes + T::A_COL + sa * (kStreamK / 2) + 32 * h, v);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[sw]);          // the warp has read its rows
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ready[s]);
-            s += 2;
-            if (s >= T::STAGES) {
-                s -= T::STAGES;
-                phase ^= 1u;
+            if (lane == 0) mbar_arrive(&ready[sa]);
+            sw += 2;
+            if (sw >= T::W_STAGES) {
+                sw -= T::W_STAGES;
+                w_phase ^= 1u;
+            }
+            sa += 2;
+            if (sa >= T::T_STAGES) {
+                sa -= T::T_STAGES;
+                a_phase ^= 1u;
             }
         }
     } else {
@@ -822,21 +819,20 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         int b = 0;
         uint32_t phase = 0;
         bool ok = true;
-        // a warp that gave up still meets the others at their barriers
-        for (int64_t u = u0; u < u1;) {
-            const int64_t tile = u / sm.ksteps, start = tile * sm.ksteps;
-            const int steps = int(min(start + sm.ksteps, u1) - u);
-            const int ch = int(tile / sm.tiles_t), tok = int(tile - int64_t(ch) * sm.tiles_t);
+        for (int t = tile0; t < sm.tiles; t += stride) {
+            const int ch = t / sm.tiles_t, tok = t - ch * sm.tiles_t;
             const int64_t n = int64_t(ch) * BM + 32 * (warp & 3) + lane, m0 = int64_t(tok) * BT + half * T::COLS;
+            const int64_t nn = min(n, p.N - 1);                // past the end: not stored
+            const float sb = __ldg(p.sb + nn), bias = p.bias ? __ldg(p.bias + nn) : 0.0f;
+            float sa[T::COLS / 32];
+#pragma unroll
+            for (int i = 0; i < T::COLS / 32; ++i) sa[i] = __ldg(p.sa + min(m0 + 32 * i + lane, p.M - 1));
             int acc[T::COLS];
 #pragma unroll
             for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
-            for (int c = 0; c < steps && ok; c += kStreamChunk) {
+            for (int c = 0; c < steps; c += kStreamChunk) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], phase));
-                if (!ok) {
-                    if (lane == 0) atomicOr(status, 1u);
-                    break;
-                }
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < T::COLS; j += 16) {
@@ -851,42 +847,83 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                 b ^= 1;
                 if (b == 0) phase ^= 1u;
             }
-            u += steps;
-            if (steps < sm.ksteps) {
-                const int slot = sm.owner(start);
-                int *sum = ws.sums + (int64_t(slot) * BT + half * T::COLS) * BM + 32 * (warp & 3) + lane;
-                if (ok) {
-#pragma unroll
-                    for (int i = 0; i < T::COLS; ++i) atomicAdd(sum + i * BM, acc[i]);
-                }
-                __threadfence();
-                epilogue_sync();
-                if (threadIdx.x == 0) last = atomicAdd(ws.counts + slot, steps) + steps == sm.ksteps;
-                epilogue_sync();
-                if (!last) continue;
-                __threadfence();
-#pragma unroll
-                for (int i = 0; i < T::COLS; ++i) acc[i] = __ldcg(sum + i * BM);
+            if (!ok) {
+                if (lane == 0) atomicOr(status, 1u);
+                break;
             }
-            if (!ok) continue;
-            float sa[T::COLS / 32];
+            if (sm.parts > 1) {
+                // the only tile: every copy into the ring of B has been read
+                int *sum = reinterpret_cast<int *>(w_ring) + half * T::COLS * BM + 32 * (warp & 3) + lane;
 #pragma unroll
-            for (int i = 0; i < T::COLS / 32; ++i) sa[i] = __ldg(p.sa + min(m0 + 32 * i + lane, p.M - 1));
-            const int64_t nn = min(n, p.N - 1);                // past the end: not stored
-            const float sb = __ldg(p.sb + nn), bias = p.bias ? __ldg(p.bias + nn) : 0.0f;
+                for (int i = 0; i < T::COLS; ++i) sum[i * BM] = acc[i];
+                break;
+            }
+            const int rows = n < p.N ? int(min(p.M - m0, int64_t(T::COLS))) : 0;
+            using E = typename std::conditional<TY == REPOPS_TYPE_F32, float, uint16_t>::type;
+            E *out = static_cast<E *>(p.C) + m0 * p.ldc + n;
+            const bool add = p.bias != nullptr;
 #pragma unroll
             for (int i = 0; i < T::COLS; ++i) {
                 float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i]), __shfl_sync(0xffffffffu, sa[i / 32], i % 32)), sb);
-                if (p.bias) v = __fadd_rn(v, bias);
-                if (n < p.N && m0 + i < p.M) store_c<TY>(p.C, (m0 + i) * p.ldc + n, v);
+                const float w = __fadd_rn(v, bias);
+                v = add ? w : v;
+                if (i < rows) store_c<TY>(out, 0, v);
+                out += p.ldc;
             }
         }
+    }
+    if (sm.parts > 1) {
+        // this CTA's tokens of the tile: rank, rank + parts, ...; a warp a token,
+        // four channels a lane
+        const int ch = tile0 / sm.tiles_t, tok = tile0 - ch * sm.tiles_t;
+        const int64_t n = int64_t(ch) * BM + 4 * lane, m0 = int64_t(tok) * BT;
+        float sb[4], bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t nn = min(n + i, p.N - 1);
+            sb[i] = __ldg(p.sb + nn);
+            bias[i] = p.bias ? __ldg(p.bias + nn) : 0.0f;
+        }
+        __syncwarp();
+        cluster_sync();
+        for (int i = rank + sm.parts * warp; i < BT && m0 + i < p.M; i += sm.parts * (kStreamThreads / 32)) {
+            const uint32_t at = uint32_t(i * BM + 4 * lane) * 4u;
+            int4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < sm.parts) v[r] = load_cluster16(cluster_addr(w_ring, uint32_t(r)) + at);
+            const float sa = __ldg(p.sa + m0 + i);
+            int4 a = v[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < sm.parts) a = make_int4(a.x + v[r].x, a.y + v[r].y, a.z + v[r].z, a.w + v[r].w);
+            float f[4] = {__int2float_rn(a.x), __int2float_rn(a.y), __int2float_rn(a.z), __int2float_rn(a.w)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[j] = __fmul_rn(__fmul_rn(f[j], sa), sb[j]);
+                if (p.bias) f[j] = __fadd_rn(f[j], bias[j]);
+            }
+            const int64_t o = (m0 + i) * p.ldc + n;
+            if (c_vec && n + 4 <= p.N) {
+                if constexpr (TY == REPOPS_TYPE_F32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + o) = make_float4(f[0], f[1], f[2], f[3]);
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + o) =
+                        make_uint2(pack_c<TY>(f[0], f[1]), pack_c<TY>(f[2], f[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < p.N) store_c<TY>(p.C, o + j, f[j]);
+            }
+        }
+        __syncwarp();
+        cluster_sync();                                        // no CTA leaves while another reads its sums
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 17) tmem_free<1>(tmem, 512);
+    if (warp == 18) tmem_free<1>(tmem, 512);
 }
 
 // ------------------------------------------------------------------- host ----
@@ -1022,27 +1059,42 @@ int64_t stream_k(int64_t K) { return ceil_div(K, kStreamK) * kStreamK; }
 // Tokens a tile.
 int stream_tokens(int64_t M) { return M <= 64 ? 64 : 128; }
 
+// The largest cluster whose CTAs are all resident at once for every tile, and no
+// more than one a k-step.  Clusters of one size that fit on the chip together:
+// measured, and fixed so that a product's split does not depend on the device.
+int stream_parts(int64_t tiles, int64_t ksteps) {
+    constexpr int64_t fit[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    int p = 1;
+    for (int i = 2; i <= 8; ++i)
+        if (tiles <= fit[i] && i <= ksteps) p = i;
+    return p;
+}
+
 StreamMap stream_map(int64_t M, int64_t N, int64_t K) {
     StreamMap sm;
     sm.tiles_t = int(ceil_div(M, stream_tokens(M)));
     sm.ksteps = int(ceil_div(K, kStreamK));
-    sm.total = ceil_div(N, BM) * sm.tiles_t * sm.ksteps;
-    sm.ctas = int(std::min<int64_t>(kStreamCtas, sm.total));
+    sm.tiles = int(ceil_div(N, BM) * sm.tiles_t);
+    sm.parts = stream_parts(sm.tiles, sm.ksteps);
     return sm;
 }
 
-// Offsets of the scratch's parts in bytes; the last is its size.
-struct StreamLayout {
-    uint64_t sums, counts, copy, bytes;
-};
-StreamLayout stream_layout(int64_t M, int64_t N, int64_t K) {
-    const uint64_t kp = uint64_t(stream_k(K)), ctas = uint64_t(stream_map(M, N, K).ctas);
-    StreamLayout l;
-    l.sums = uint64_t(M) * kp * 2u;
-    l.counts = l.sums + ctas * BM * uint64_t(stream_tokens(M)) * 4u;
-    l.copy = l.counts + (ctas * 4u + 15u) / 16u * 16u;
-    l.bytes = l.copy + uint64_t(N) * kp;
-    return l;
+// The tokens in binary16, then B at a 16-byte pitch where TMA cannot read it in place.
+uint64_t stream_copy_at(int64_t M, int64_t K) { return uint64_t(M) * uint64_t(stream_k(K)) * 2u; }
+uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
+    return stream_copy_at(M, K) + uint64_t(N) * uint64_t(stream_k(K));
+}
+
+// The widened tokens as 64-k blocks: a box is BT tokens of two blocks, each with
+// rows of 128 bytes under the 128-byte swizzle.
+bool make_token_map(CUtensorMap *map, const __half *base, int64_t M, int64_t Kp, int box_rows) {
+    gemm::EncodeTiledFn enc = gemm::tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {64u, cuuint64_t(M), cuuint64_t(Kp / 64)}, strides[2] = {cuuint64_t(Kp) * 2u, 128u};
+    const cuuint32_t box[3] = {64u, cuuint32_t(box_rows), 2u}, estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int TY, int BT>
@@ -1050,14 +1102,13 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
     using T = StreamCfg<BT>;
     const int64_t Kp = stream_k(a.K);
     const StreamMap sm = stream_map(a.M, a.N, a.K);
-    const StreamLayout l = stream_layout(a.M, a.N, a.K);
-    const StreamScratch w{reinterpret_cast<__half *>(ws), reinterpret_cast<int *>(ws + l.sums),
-                          reinterpret_cast<int *>(ws + l.counts), reinterpret_cast<int8_t *>(ws + l.copy)};
+    __half *tokens = reinterpret_cast<__half *>(ws);
+    int8_t *copy = reinterpret_cast<int8_t *>(ws + stream_copy_at(a.M, a.K));
     const bool in_place = operand_vec(a.B, a.ldb) && a.ldb < (int64_t(1) << 39), vec = operand_vec(a.A, a.lda);
     CUtensorMap mt, mw;
-    if (!make_map(&mt, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, w.tokens, Kp, a.M, Kp, 64, BT) ||
+    if (!make_token_map(&mt, tokens, a.M, Kp, BT) ||
         !(in_place ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.B, a.K, a.N, a.ldb, kStreamK, BM)
-                   : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.copy, Kp, a.N, Kp, kStreamK, BM)))
+                   : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, copy, Kp, a.N, Kp, kStreamK, BM)))
         return REPOPS_ERR_UNSUPPORTED;
     unsigned *status = nullptr;
     int rc = status_word_address(&status);
@@ -1066,15 +1117,18 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return set_cuda_error(e);
     // nothing has been launched so far: from here on only a launch can fail
-    const int64_t clear16 = int64_t((l.copy - l.sums) / 16);
-    const int64_t items = std::max({a.M * (Kp / 8), clear16, in_place ? int64_t(0) : a.N * (Kp / 16)});
-    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 8));
+    const int64_t items = std::max(a.M * (Kp / 8), in_place ? int64_t(0) : a.N * (Kp / 16));
+    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 4));
     auto prep = in_place ? vec ? stream_prepare_kernel<true, false> : stream_prepare_kernel<false, false>
                          : vec ? stream_prepare_kernel<true, true> : stream_prepare_kernel<false, true>;
-    prep<<<grid, 256, 0, s>>>(a, Kp, w, clear16);
+    prep<<<grid, 256, 0, s>>>(a, Kp, tokens, copy);
     rc = check_launch();
     if (rc != REPOPS_OK) return rc;
-    return launch_behind(kern, dim3(unsigned(sm.ctas)), kStreamThreads, T::SMEM, s, mt, mw, a, sm, w, status);
+    constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
+    const int c_vec = reinterpret_cast<uintptr_t>(a.C) % (4 * csize) == 0 && a.ldc % 4 == 0;
+    const unsigned ctas = unsigned(sm.parts > 1 ? sm.tiles * sm.parts : std::min(sm.tiles, sm_count()));
+    return launch_behind_cluster(kern, dim3(ctas), unsigned(sm.parts), kStreamThreads, T::SMEM, s, mt, mw, a, sm,
+                                 int(in_place), c_vec, status);
 }
 
 template <int TY>
@@ -1107,7 +1161,7 @@ extern "C" uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_
         return 0;
     if (config == CFG_AUTO) config = auto_config(M, N, K);
     return config == CFG_ROWS     ? 0
-           : config == CFG_STREAM ? stream_layout(M, N, K).bytes
+           : config == CFG_STREAM ? stream_workspace(M, N, K)
                                   : tile_workspace(M, N, K);
 }
 

@@ -121,19 +121,28 @@ __device__ __forceinline__ bool dbg_smem(uint64_t need, unsigned *status) {
 // (grid_wait, before they read or write anything of it) until it has ended and
 // its writes are visible.  The earlier kernel calls grid_release.
 template <class... Params, class... Args>
-int launch_behind(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+int launch_behind_cluster(void (*kern)(Params...), dim3 grid, unsigned cluster, unsigned threads, size_t smem,
+                          cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, Params(args)...);
     return e == cudaSuccess ? REPOPS_OK : set_cuda_error(e);
+}
+// The same without an explicit cluster.
+template <class... Params, class... Args>
+int launch_behind(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
+    return launch_behind_cluster(kern, grid, 1, threads, smem, stream, args...);
 }
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
