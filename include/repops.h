@@ -1030,9 +1030,8 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
  * the scaled zero (+ bias).
  * config -1 chooses by size; 0 .. repops_gemm_i8_config_count() - 1 force a
  * kernel (the same bits): 0 splits k between the lanes and warps of a CTA and
- * suits few rows of A; 1 (tiles of 256 x 256, a pair of CTAs each), 2 (128 x 128)
- * and 3 (128 x 64) run on the tensor cores from operands widened to binary16 in
- * scratch.
+ * suits few rows of A; 1 runs on the tensor cores in binary16, A widened in
+ * scratch, B on its way into tensor memory.
  * ws: device scratch of repops_gemm_i8_workspace_bytes(config, M, N, K) bytes
  * (0 for config 0) on a 16-byte boundary, or NULL to take it from the scratch
  * pool on `stream` (ALLOC when refused).

@@ -54,7 +54,7 @@ SIZES = [(1, 1, 1), (1, 16, 64), (3, 5, 7), (8, 33, 64), (9, 130, 100), (16, 64,
          (1000, 100, 2048)]
 
 
-@pytest.mark.parametrize("config", [-1, 0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [-1, 0, 1])
 @pytest.mark.parametrize("M,N,K", SIZES)
 def test_every_kernel_is_exact(rp, M, N, K, config):
     a, b, sa, sb, got, _ = check(rp, M, N, K, config)
@@ -62,13 +62,13 @@ def test_every_kernel_is_exact(rp, M, N, K, config):
         assert torch.equal(rp.gemm_i8(a, b.t(), sa, sb, config=config, out_dtype=dt), got.to(dt))
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [0, 1])
 @pytest.mark.parametrize("off,pad", [(0, 16), (1, 0), (2, 2), (4, 4), (3, 13), (15, 1)])
 def test_alignment_and_pitch(rp, off, pad, config):
     check(rp, 21, 70, 203, config, off, pad, bias=True)
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [0, 1])
 @pytest.mark.parametrize("K", [512, 1024, 8192, 131071])
 @pytest.mark.parametrize("va,vb", [(-128, -128), (-128, 127), (127, 127), (1, -1)])
 def test_extreme_sums(rp, config, K, va, vb):
@@ -84,7 +84,7 @@ def test_extreme_sums(rp, config, K, va, vb):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [0, 1])
 def test_large_random_rows(rp, config):
     """A sample of rows of a product with several tiles a CTA."""
     M, N, K = 3000, 2100, 1600
@@ -98,7 +98,7 @@ def test_large_random_rows(rp, config):
     assert torch.equal(got, ref)
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [0, 1])
 def test_rows_outside_are_left(rp, config):
     A, B = ints((70, 200), 3).to(DEV), ints((90, 200), 4).to(DEV)
     sa, sb = torch.ones(70, device=DEV), torch.ones(90, device=DEV)
@@ -122,7 +122,7 @@ def test_empty_and_zero_k(rp):
         assert torch.equal(y, bias.expand(3, 5))
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("config", [0, 1])
 def test_scales_with_nan_and_infinity(rp, config):
     A, B = ints((4, 64), 6, 1, 100).to(DEV), ints((6, 64), 7, 1, 100).to(DEV)
     sa, sb = torch.ones(4, device=DEV), torch.ones(6, device=DEV)

@@ -20,18 +20,31 @@
 // in registers for the faster-looking m16n8k16.f16 took 31 us where this takes
 // 13 (16384 channels, 2048 k, 13 tokens).
 //
-// Many rows: the operands are widened once to binary16 (exact: 8 bits fit its
-// 11) in scratch and multiplied by tcgen05 with binary32 accumulators in tensor
-// memory.  Every product and every partial sum of up to 1024 of them is a whole
-// number of at most 2^24, so binary32 accumulation is exact whatever its order;
-// after each 1024 of k the accumulators are added to 32-bit integers in
-// registers while the tensor core fills the other half of tensor memory.  (A
-// conversion to integer takes 8 cycles a warp: 2300 cycles for a drain, against
-// 8200 of products.)  Two CTAs share a tile of 256 x 256 where there are enough
-// (cta_group::2: each reads half of B from its shared memory).  8192 x 8192 x
-// 8192 takes 662 us: 59 to widen (6.8 TB/s), then 1.82 PFLOP/s in the products,
-// bound by the tensor cores at the clock the power limit leaves; 2048 x 16384 x
-// 2048 takes 100 us, 16 of them to widen, 512 tiles in 7 rounds of 76 pairs.
+// More rows: tcgen05 on binary16 (8 bits fit its 11) with binary32 accumulators
+// in tensor memory.  Every product and every partial sum of up to 1024 of them is
+// a whole number of at most 2^24, so binary32 accumulation is exact whatever its
+// order; after each 1024 of k the accumulators are added to 32-bit integers in
+// registers while the tensor core fills the other half of the accumulators'
+// tensor memory.  (A conversion to integer takes 8 cycles a warp: 1000 cycles for
+// a drain, against 4500 of products.)
+//
+// B streams through once as bytes and is widened on its way into tensor memory,
+// where it is the product's first operand (128 channels x k): its binary16 form
+// never passes through shared memory or DRAM.  (Widening both operands to scratch
+// first reads and writes 5 bytes for each of B's: with that, 8192 x 8192 took 64
+// us at 128 tokens and 214 at 2048, where this takes 21 and 178; at 8192 tokens,
+// where pairs of CTAs could share 256 x 256 tiles and read less shared memory,
+// both took 700.)  The tokens are widened to scratch before and loaded by TMA.
+// Where there are fewer tiles than SMs a cluster shares a tile's k: each CTA
+// leaves its 32-bit sums in shared memory, and after the cluster's barrier each
+// adds and stores its share of the tokens.  (Adding parts by atomics in scratch
+// took 23 us for 8192 x 8192, 64 tokens; this takes 18.)
+//
+// Bound: at 64 tokens by what is not the products, 7 us of launches, the tokens'
+// widening, first loads and last stores, then by the issue of a step's products
+// (0.33 us for 128 of k, 128 channels and 64 tokens; B at 5 TB/s); with many by
+// the tensor cores at the clock the power limit leaves and by widening each
+// channel once for every 128 tokens (8192 x 8192 x 8192: 1.58 PFLOP/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -232,10 +245,12 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
     }
 }
 
-// --------------------------------------------------------------- many rows ----
+// --------------------------------------------------------------- more rows ----
 
-constexpr int BM = 128, BK = 64;          // BK binary16 = one 128-byte swizzled row
-constexpr int kChunkSteps = 16;           // k-steps between two drains: 1024 of k, the most that stays exact
+constexpr int BM = 128;                   // channels of a tile
+constexpr int kStreamK = 128;             // k of a step: a 128-byte row of B
+constexpr int kStreamChunk = 1024 / kStreamK;        // steps between two drains: the most that stays exact
+constexpr int kStreamThreads = 608;       // 8 epilogue warps, 8 widening warps, a TMA warp each for B and tokens, an MMA warp
 
 // Bytes k .. k+7 of a row (zeros from `n` on), as load_k16 loads sixteen.
 template <bool VEC>
@@ -262,52 +277,8 @@ __device__ __forceinline__ uint2 load_k8(const int8_t *__restrict__ row, int64_t
     return make_uint2(r[0], r[1]);
 }
 
-// The rows of A, then those of B, as binary16 rows of Kp (a multiple of 64)
-// values, zeros past K.  An item is 8 values, so that a warp's store covers 512
-// consecutive bytes (16 values an item, stored as two halves of each 32-byte
-// sector, took a third longer); two items a thread are in flight.
-template <bool VEC>
-__global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half *__restrict__ out) {
-    grid_release();
-    const uint32_t per = uint32_t(Kp / 8);
-    const int64_t items = (p.M + p.N) * per, stride = int64_t(gridDim.x) * 512;
-    for (int64_t i0 = blockIdx.x * int64_t(512) + threadIdx.x; i0 < items; i0 += stride) {
-        uint2 w[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t it = min(i0 + 256 * j, items - 1);       // past the end: the last one again
-            const int64_t r = items <= UINT32_MAX ? uint32_t(it) / per : it / per;
-            const int64_t k = (it - r * per) * 8;
-            w[j] = r < p.M ? load_k8<VEC>(p.A + r * p.lda, k, p.K, p.A, p.a_end)
-                           : load_k8<VEC>(p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (i0 + 256 * j >= items) continue;
-            const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
-            *reinterpret_cast<uint4 *>(out + (i0 + 256 * j) * 8) =
-                make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
-        }
-    }
-}
-
-// CTAS CTAs (1, or a pair) multiply a tile of CTAS * 128 rows by BN columns,
-// each holding 128 rows of A and BN / CTAS of B in a stage.
-template <int BN, int CTAS>
-struct TileCfg {
-    static constexpr int B_ROWS = BN / CTAS;
-    static constexpr int STAGE_BYTES = (BM + B_ROWS) * BK * 2;
-    static constexpr int STAGES = 196608 / STAGE_BYTES;          // 4, 6 or 8
-    static constexpr int WARP_STAGE = 32 * 128;                  // an epilogue warp's block: 32 rows of 128 bytes
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * WARP_STAGE;
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
-    static constexpr int COLS = BN / 2;                          // an epilogue warp's columns
-};
-
-constexpr int kTileThreads = 320;         // 8 epilogue warps, a TMA warp, an MMA warp
-
 struct TileMap {
-    int tiles_m, tiles_n, band;           // band: tile rows walked together, for L2 reuse
+    int tiles_m, tiles_n, band;           // m: token tiles, walked `band` at a time for L2 reuse; n: channel tiles
     __device__ __forceinline__ void at(int t, int &m, int &n) const {
         const int per = band * tiles_n, b = t / per, first = b * band, rows = min(band, tiles_m - first);
         const int r = t - b * per;
@@ -315,291 +286,6 @@ struct TileMap {
         m = first + r - n * rows;
     }
 };
-
-// C's tile: sums x scales, through the warp's block of shared memory.  Lane l
-// holds the scales (and biases) of columns l, l + 32, ...  c_tma: C can be
-// stored by TMA (a block of 32 rows x 128 bytes at a time, clipped at C's
-// edges); else lanes store single values.
-template <int TY, int COLS>
-__device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *map_c, const int (&acc)[COLS], float sa,
-                                           const float (&sb)[COLS / 32], const float (&bias)[COLS / 32], int64_t row0,
-                                           int64_t col0, uint8_t *block, bool c_tma) {
-    constexpr int W = TY == REPOPS_TYPE_F32 ? 32 : COLS < 64 ? COLS : 64;    // columns of a block
-    const int lane = threadIdx.x & 31;
-    uint4 *chunk = reinterpret_cast<uint4 *>(block);           // 16-byte chunk c of row r in slot c ^ (r & 7)
-#pragma unroll
-    for (int j = 0; j < COLS; j += W) {
-        if (col0 + j >= p.N) break;
-        if (c_tma && lane == 0) tma_store_wait_read();         // the block's previous contents have left
-        __syncwarp();
-#pragma unroll
-        for (int c = j; c < j + W; c += 8) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = __fmul_rn(__fmul_rn(__int2float_rn(acc[c + i]), sa),
-                                 __shfl_sync(0xffffffffu, sb[c / 32], (c + i) % 32));
-            if (p.bias) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = __fadd_rn(v[i], __shfl_sync(0xffffffffu, bias[c / 32], (c + i) % 32));
-            }
-            if constexpr (TY == REPOPS_TYPE_F32) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    chunk[lane * 8 + (((c - j) / 4 + h) ^ (lane & 7))] =
-                        make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                                   __float_as_uint(v[4 * h + 3]));
-            } else {
-                chunk[lane * 8 + (((c - j) / 8) ^ (lane & 7))] = make_uint4(
-                    pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]), pack_c<TY>(v[4], v[5]), pack_c<TY>(v[6], v[7]));
-            }
-        }
-        if (c_tma) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0 && row0 < p.M) tma_store_2d(map_c, block, int32_t(col0 + j), int32_t(row0));
-        } else {
-            __syncwarp();
-            using E = typename std::conditional<TY == REPOPS_TYPE_F32, float, uint16_t>::type;
-            constexpr int PER = 16 / int(sizeof(E));           // values of a chunk
-            const E *e = reinterpret_cast<const E *>(block);
-            const int rows = int(min(p.M - row0, int64_t(32)));
-#pragma unroll
-            for (int h = 0; h < W; h += 32) {
-                const int c = h + lane;
-                E *out = static_cast<E *>(p.C) + row0 * p.ldc + col0 + j + c;
-                const bool mine = col0 + j + c < p.N;
-#pragma unroll 8
-                for (int r = 0; r < 32; ++r) {
-                    const E v = e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
-                    if (mine && r < rows) out[r * p.ldc] = v;
-                }
-            }
-            __syncwarp();
-        }
-    }
-}
-
-template <int TY, int BN, int CTAS>
-__device__ __forceinline__ void tile_kernel(const CUtensorMap &map_a, const CUtensorMap &map_b, const CUtensorMap &map_c,
-                                            const I8Args &p, const TileMap &tm, int ksteps, int c_tma, unsigned *status) {
-    using T = TileCfg<BN, CTAS>;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
-    __shared__ uint32_t tmem_slot;
-    uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-    // from a shuffle the compiler knows that a warp's role is uniform: a product
-    // then takes its 64 (128 columns) or 128 cycles instead of the 111 that
-    // issuing it from a branch it must assume divergent costs
-    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = CTAS == 1 ? 0u : cluster_rank();
-    const int tiles = tm.tiles_m * tm.tiles_n, first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
-    const int chunks = (ksteps + kChunkSteps - 1) / kChunkSteps;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < T::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8 * CTAS);
-        }
-        mbar_init(&drained, 1);
-        fence_barrier_init();
-    }
-    if (warp == 9) tmem_alloc<CTAS>(&tmem_slot, T::TMEM_COLS);
-    tc_fence_before();
-    __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-    grid_wait();                                               // the widened operands
-
-    // Every wait gives up after its limit: the role that gave up sets the
-    // status word, waits (again with a limit) for its own copies or products in
-    // flight and leaves; the others run into their own limits.
-    if (warp == 8) {
-        if (elect_one()) {
-            prefetch_tensormap(&map_a);
-            prefetch_tensormap(&map_b);
-            int issued = 0, s = 0;
-            uint32_t phase = 1;                                // the wait before the ring's first use passes
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += stride) {
-                int m, n;
-                tm.at(t, m, n);
-                const int row_a = (m * CTAS + int(rank)) * BM, row_b = n * BN + int(rank) * T::B_ROWS;
-                for (int k = 0; k < ksteps; ++k, ++issued) {
-                    if (!mbar_wait_bounded(&empty[s], phase)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *st = stages + s * T::STAGE_BYTES;
-                    // a pair's four copies all signal the first CTA, whose
-                    // barrier is armed for both CTAs' bytes; a copy of the other
-                    // CTA that lands before that leaves the phase open, as the
-                    // arming arrival is still missing
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * T::STAGE_BYTES);
-                    if constexpr (CTAS == 1) {
-                        tma_load_2d(st, &map_a, &full[s], k * BK, row_a);
-                        tma_load_2d(st + BM * BK * 2, &map_b, &full[s], k * BK, row_b);
-                    } else {
-                        const uint32_t bar = cluster_addr(&full[s], 0);
-                        tma_load_2d_pair(st, &map_a, bar, k * BK, row_a);
-                        tma_load_2d_pair(st + BM * BK * 2, &map_b, bar, k * BK, row_b);
-                    }
-                    if (++s == T::STAGES) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            if (!ok) {
-                atomicOr(status, 1u);
-                if (rank == 0) {
-                    for (int i = max(0, issued - T::STAGES); i < issued; ++i)
-                        mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
-                } else {
-                    // these copies signal the other CTA: give them the time of
-                    // a copy a thousand times over
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 2000000u) {}
-                }
-            }
-        }
-    } else if (warp == 9) {
-        if (rank == 0 && elect_one()) {
-            constexpr uint32_t idesc = idesc_f16(BM * CTAS, BN);
-            const uint32_t base = smem_addr(stages);
-            int s = 0, b = 0;
-            uint32_t phase = 0, acc_phase = 1;
-            bool ok = true;
-            for (int t = first; t < tiles && ok; t += stride) {
-                for (int c = 0; c < chunks && ok; ++c) {
-                    if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
-                        ok = false;
-                        break;
-                    }
-                    if constexpr (CTAS == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                    tc_fence_after();
-                    const int steps = min(kChunkSteps, ksteps - c * kChunkSteps);
-                    for (int k = 0; k < steps; ++k) {
-                        if (!mbar_wait_bounded(&full[s], phase)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t st = base + s * T::STAGE_BYTES;
-                        const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + BM * BK * 2);
-#pragma unroll
-                        for (int j = 0; j < BK / 16; ++j)      // 32 bytes of k a step within the swizzled row
-                            tc_mma_f16<CTAS>(tmem + b * BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
-                        tc_commit<CTAS>(&empty[s]);
-                        if (++s == T::STAGES) {
-                            s = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                    if (ok) tc_commit<CTAS>(&acc_full[b]);
-                    b ^= 1;
-                    if (b == 0) acc_phase ^= 1u;
-                }
-            }
-            if (!ok) {
-                atomicOr(status, 1u);
-                tc_commit<CTAS>(&drained);
-                mbar_wait_bounded(&drained, 0u);
-            }
-        }
-    } else {
-        const int half = warp >> 2;                            // columns half * COLS .. of the tile
-        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-        uint8_t *block = stages + T::STAGES * T::STAGE_BYTES + warp * T::WARP_STAGE;
-        int b = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int t = first; t < tiles && ok; t += stride) {
-            int tile_m, tile_n;
-            tm.at(t, tile_m, tile_n);
-            const int64_t row0 = (int64_t(tile_m) * CTAS + rank) * BM + 32 * (warp & 3),
-                          col0 = int64_t(tile_n) * BN + half * T::COLS;
-            const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
-            float sb[T::COLS / 32], bias[T::COLS / 32];
-#pragma unroll
-            for (int i = 0; i < T::COLS / 32; ++i) {
-                const int64_t col = min(col0 + 32 * i + lane, p.N - 1);    // past the end: not stored
-                sb[i] = __ldg(p.sb + col);
-                bias[i] = p.bias ? __ldg(p.bias + col) : 0.0f;
-            }
-            int acc[T::COLS];
-#pragma unroll
-            for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
-            for (int c = 0; c < chunks; ++c) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], phase));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < T::COLS; j += 16) {
-                    uint32_t v[16];
-                    tmem_load16(tmem + lanes + b * BN + half * T::COLS + j, v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CTAS == 1) mbar_arrive(&acc_empty[b]);
-                    else mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
-                }
-                b ^= 1;
-                if (b == 0) phase ^= 1u;
-            }
-            if (!ok) {
-                if (lane == 0) atomicOr(status, 1u);
-                break;
-            }
-            store_tile<TY, T::COLS>(p, &map_c, acc, sa, sb, bias, row0, col0, block, c_tma != 0);
-        }
-        if (c_tma && lane == 0) tma_store_wait();
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if constexpr (CTAS == 2) cluster_sync();                   // no CTA leaves while the other may signal it
-    tc_fence_after();
-    if (warp == 9) tmem_free<CTAS>(tmem, T::TMEM_COLS);
-}
-
-template <int TY, int BN>
-__global__ void __launch_bounds__(kTileThreads, 1)
-gemm_i8_tile_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
-                    unsigned *status) {
-    tile_kernel<TY, BN, 1>(map_a, map_b, map_c, p, tm, ksteps, c_tma, status);
-}
-
-template <int TY>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
-gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
-                    unsigned *status) {
-    tile_kernel<TY, 256, 2>(map_a, map_b, map_c, p, tm, ksteps, c_tma, status);
-}
-
-// ------------------------------------------------------------ middling rows ----
-
-// Tokens from a couple of dozen to a thousand or so: B streams through once as
-// bytes and is widened on its way into tensor memory, where it is the product's
-// first operand (128 channels x k), so that its binary16 form never passes
-// through shared memory or DRAM.  The tokens, few, are widened to scratch before
-// and loaded by TMA.  Where there are fewer tiles than SMs a cluster shares a
-// tile's k: each CTA leaves its 32-bit sums in shared memory, and after the
-// cluster's barrier each adds and stores its share of the tokens (whole numbers:
-// any split gives the same bits).
-constexpr int kStreamK = 128;             // k of a step: a 128-byte row of B
-constexpr int kStreamChunk = 1024 / kStreamK;
-constexpr int kStreamThreads = 608;       // 8 epilogue warps, 8 widening warps, a TMA warp each for B and tokens, an MMA warp
 
 // BT tokens a tile.  Three rings: B's bytes (freed once widened), the tokens in
 // shared memory and the widened channels in tensor memory (both freed by the
@@ -616,33 +302,63 @@ struct StreamCfg {
     static_assert(A_COL + T_STAGES * kStreamK / 2 <= 512 && W_STAGES % 2 == 0 && T_STAGES % 2 == 0);
 };
 
-// Tile t = channel tile * tiles_t + token tile; `parts` CTAs share a tile (its
-// cluster), CTA r the k-steps [first(r), first(r + 1)).
+// `parts` CTAs share a tile (its cluster), CTA r the k-steps [first(r), first(r + 1)).
 struct StreamMap {
-    int tiles, tiles_t, ksteps, parts;
+    TileMap order;
+    int tiles, ksteps, parts;
+    int copies, rows;                  // of the widened tokens, and a copy's rows
     __device__ __forceinline__ int first(int r) const { return int(int64_t(ksteps) * r / parts); }
 };
 
-// Widens the tokens (rows of Kp) and copies B to rows of Kp where COPY.
+// Item `it` of rows of `per` items each: its row, and its place there in `c`.
+__device__ __forceinline__ int64_t item_row(int64_t it, uint32_t per, bool small, uint32_t &c) {
+    const int64_t r = small ? int64_t(uint32_t(it) / per) : it / per;
+    c = uint32_t(it - r * per);
+    return r;
+}
+
+// Widens the tokens (rows of Kp, `copies` times) and copies B to rows of Kp where
+// COPY.  An item is 8 values (a warp's store then covers 512 consecutive bytes), or
+// 16 bytes of B; two items a thread are in flight.
 template <bool VEC, bool COPY>
 __global__ void __launch_bounds__(256)
-stream_prepare_kernel(I8Args p, int64_t Kp, __half *__restrict__ tokens, int8_t *__restrict__ copy) {
+stream_prepare_kernel(I8Args p, int64_t Kp, int copies, __half *__restrict__ tokens, int8_t *__restrict__ copy) {
     grid_release();
-    const int64_t i0 = blockIdx.x * int64_t(256) + threadIdx.x, stride = int64_t(gridDim.x) * 256;
-    const int64_t per = Kp / 8;
-    for (int64_t i = i0; i < p.M * per; i += stride) {
-        const int64_t r = i / per;
-        const uint2 v = load_k8<VEC>(p.A + r * p.lda, (i - r * per) * 8, p.K, p.A, p.a_end);
-        const uint32_t a = v.x ^ 0x80808080u, b = v.y ^ 0x80808080u;
-        *reinterpret_cast<uint4 *>(tokens + i * 8) =
-            make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+    const int64_t i0 = blockIdx.x * int64_t(512) + threadIdx.x, stride = int64_t(gridDim.x) * 512;
+    const uint32_t per = uint32_t(Kp / 8);
+    const int64_t items = p.M * per;
+    const bool small = items <= UINT32_MAX;
+    for (int64_t i = i0; i < items; i += stride) {
+        uint2 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t c;                                        // past the end: the last one again
+            const int64_t r = item_row(min(i + 256 * j, items - 1), per, small, c);
+            w[j] = load_k8<VEC>(p.A + r * p.lda, int64_t(c) * 8, p.K, p.A, p.a_end);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i + 256 * j >= items) continue;
+            const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
+            const uint4 h = make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+            for (int64_t c = 0; c < copies; ++c) *reinterpret_cast<uint4 *>(tokens + (i + 256 * j + c * items) * 8) = h;
+        }
     }
     if constexpr (COPY) {
-        const int64_t per16 = Kp / 16;
-        for (int64_t i = i0; i < p.N * per16; i += stride) {
-            const int64_t r = i / per16;
-            reinterpret_cast<uint4 *>(copy)[i] =
-                load_k16<false>(p.B + r * p.ldb, (i - r * per16) * 16, p.K, p.B, p.b_end);
+        const uint32_t per16 = uint32_t(Kp / 16);
+        const int64_t chunks = p.N * per16;
+        const bool few = chunks <= UINT32_MAX;
+        for (int64_t i = i0; i < chunks; i += stride) {
+            uint4 w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t c;
+                const int64_t r = item_row(min(i + 256 * j, chunks - 1), per16, few, c);
+                w[j] = load_k16<false>(p.B + r * p.ldb, int64_t(c) * 16, p.K, p.B, p.b_end);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (i + 256 * j < chunks) reinterpret_cast<uint4 *>(copy)[i + 256 * j] = w[j];
         }
     }
 }
@@ -657,6 +373,9 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
     __shared__ uint64_t ready[T::T_STAGES], used[T::T_STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *w_ring = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u), *t_ring = w_ring + T::W_STAGES * T::W_BYTES;
+    // from a shuffle the compiler knows that a warp's role is uniform: a product
+    // is then issued in its own time, not in the 111 cycles that a branch it must
+    // assume divergent costs
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = sm.parts == 1 ? 0 : int(cluster_rank());
     const int tile0 = int(blockIdx.x) / sm.parts, stride = int(gridDim.x) / sm.parts;
@@ -677,13 +396,15 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         mbar_init(&drained, 1);
         fence_barrier_init();
     }
-    if (warp == 18) tmem_alloc<1>(&tmem_slot, 512);
+    if (warp == 18) tmem_alloc(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
-    // Every wait gives up after its limit, as in tile_kernel.
+    // Every wait gives up after its limit: the role that gave up sets the
+    // status word, waits (again with a limit) for its own copies or products in
+    // flight and leaves; the others run into their own limits.
     if (warp == 16 || warp == 17) {
         if (elect_one()) {
             const bool weights = warp == 16;
@@ -696,8 +417,10 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
             uint32_t phase = 1;
             bool ok = true;
             for (int t = tile0; t < sm.tiles && ok; t += stride) {
-                const int ch = t / sm.tiles_t, tok = t - ch * sm.tiles_t;
-                for (int k = k0; k < k0 + steps; ++k, ++issued) {
+                int ch, tok;
+                sm.order.at(t, tok, ch);
+                int k = k0 + ch % steps;                       // channels apart in k: not all on the same tokens
+                for (int i = 0; i < steps; ++i, ++issued) {
                     if (!mbar_wait_bounded(&empty[s], phase)) {
                         ok = false;
                         break;
@@ -707,8 +430,9 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                         tma_load_2d(w_ring + s * T::W_BYTES, &map_w, &full[s], k * kStreamK, ch * BM);
                     } else {
                         mbar_arrive_expect_tx(&full[s], T::T_BYTES);
-                        tma_load_3d(t_ring + s * T::T_BYTES, &map_t, &full[s], 0, tok * BT, 2 * k);
+                        tma_load_3d(t_ring + s * T::T_BYTES, &map_t, &full[s], 0, tok * BT + int(blockIdx.x % sm.copies) * sm.rows, 2 * k);
                     }
+                    if (++k == k0 + steps) k = k0;
                     if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
@@ -748,23 +472,23 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                             const uint64_t db = smem_desc_sw128(base + s * T::T_BYTES + h * T::BOX_BYTES);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                tc_mma_f16_tmem(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc,
+                                tc_mma_f16(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc,
                                                 i > 0 || h > 0 || j > 0);
                         }
-                        tc_commit<1>(&used[s]);
+                        tc_commit(&used[s]);
                         if (++s == T::T_STAGES) {
                             s = 0;
                             phase ^= 1u;
                         }
                     }
-                    if (ok) tc_commit<1>(&acc_full[b]);
+                    if (ok) tc_commit(&acc_full[b]);
                     b ^= 1;
                     if (b == 0) acc_phase ^= 1u;
                 }
             }
             if (!ok) {
                 atomicOr(status, 1u);
-                tc_commit<1>(&drained);
+                tc_commit(&drained);
                 mbar_wait_bounded(&drained, 0u);
             }
         }
@@ -820,7 +544,8 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         uint32_t phase = 0;
         bool ok = true;
         for (int t = tile0; t < sm.tiles; t += stride) {
-            const int ch = t / sm.tiles_t, tok = t - ch * sm.tiles_t;
+            int ch, tok;
+            sm.order.at(t, tok, ch);
             const int64_t n = int64_t(ch) * BM + 32 * (warp & 3) + lane, m0 = int64_t(tok) * BT + half * T::COLS;
             const int64_t nn = min(n, p.N - 1);                // past the end: not stored
             const float sb = __ldg(p.sb + nn), bias = p.bias ? __ldg(p.bias + nn) : 0.0f;
@@ -875,7 +600,8 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
     if (sm.parts > 1) {
         // this CTA's tokens of the tile: rank, rank + parts, ...; a warp a token,
         // four channels a lane
-        const int ch = tile0 / sm.tiles_t, tok = tile0 - ch * sm.tiles_t;
+        int ch, tok;
+        sm.order.at(tile0, tok, ch);
         const int64_t n = int64_t(ch) * BM + 4 * lane, m0 = int64_t(tok) * BT;
         float sb[4], bias[4];
 #pragma unroll
@@ -923,12 +649,12 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 18) tmem_free<1>(tmem, 512);
+    if (warp == 18) tmem_free(tmem, 512);
 }
 
 // ------------------------------------------------------------------- host ----
 
-enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_PAIR, CFG_TILE128, CFG_TILE64, CFG_STREAM, CFG_COUNT };
+enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_TILES, CFG_COUNT };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -937,32 +663,67 @@ int sm_count() {
     return current_device_info(&di) == REPOPS_OK ? di.sms : 152;
 }
 
-int64_t padded_k(int64_t K) { return ceil_div(K, BK) * BK; }
+int64_t stream_k(int64_t K) { return ceil_div(K, kStreamK) * kStreamK; }
 
-uint64_t tile_workspace(int64_t M, int64_t N, int64_t K) { return uint64_t(M + N) * uint64_t(padded_k(K)) * 2u; }
+// Tokens a tile.
+int stream_tokens(int64_t M) { return M <= 64 ? 64 : 128; }
 
-// The kernel whose estimated time is least.  Few rows: the integer tensor rate
-// (115 TOPS in whole groups of 8 tokens) or the memory's, plus 3 us.  Tiles: 3
-// bytes for each of B's to widen it (5.5 TB/s), 6 us of launches, fill and last
-// store, and the waves of tiles x k-steps of 64 x the time of a step: 0.36 us for
-// a pair's 256 x 256, 0.22 for 128 x 128, 0.19 for 128 x 64 (below that the
-// products' issue, not their size, sets the time).  Measured either side of a
-// choice, in us: M 32, N 16384, K 2048: rows 20, tiles 29; M 64: 39, 30.
-// N = K = 2048, M 1024: pair 22, 128 x 128 16; M 8192: 61, 61.  N 16384, K 2048,
-// M 2048: pair 104, 128 x 128 121; M 128: 36, 30.  N = K = 8192, M 128: 128 x 128
-// 76, 128 x 64 71.
+// The largest cluster whose CTAs are all resident at once for every tile, and no
+// more than one a k-step.  Clusters of one size that fit on the chip together:
+// measured, and fixed so that a product's split does not depend on the device.
+int stream_parts(int64_t tiles, int64_t ksteps) {
+    constexpr int64_t fit[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+    int p = 1;
+    for (int i = 2; i <= 8; ++i)
+        if (tiles <= fit[i] && i <= ksteps) p = i;
+    return p;
+}
+
+// Copies of the widened tokens.  Every CTA reads them all: where they are fewer
+// than 128 KB they lie in too few slices of L2 (N 16384, K 2048: 12 us from 32
+// tokens on, 16 with 8, and 12 with 8 in sixteen copies, a CTA reading one).
+int stream_copies(int64_t M, int64_t K) {
+    return int(std::clamp<int64_t>((int64_t(256) << 10) / (M * stream_k(K) * 2), 1, 16));
+}
+
+StreamMap stream_map(int64_t M, int64_t N, int64_t K) {
+    StreamMap sm;
+    // a band of 8 token tiles (2 bytes a value) by 19 of channels (1) in flight
+    // on 152 SMs reads the fewest bytes
+    sm.order = TileMap{int(ceil_div(M, stream_tokens(M))), int(ceil_div(N, BM)), 8};
+    sm.ksteps = int(ceil_div(K, kStreamK));
+    sm.tiles = sm.order.tiles_m * sm.order.tiles_n;
+    sm.copies = stream_copies(M, K);
+    sm.rows = int(M);
+    sm.parts = stream_parts(sm.tiles, sm.ksteps);
+    return sm;
+}
+
+// Scratch: the tokens in binary16, then B at a 16-byte pitch where TMA cannot read it in place.
+uint64_t stream_copy_at(int64_t M, int64_t K) { return uint64_t(M) * uint64_t(stream_copies(M, K)) * uint64_t(stream_k(K)) * 2u; }
+uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
+    return stream_copy_at(M, K) + uint64_t(N) * uint64_t(stream_k(K));
+}
+
+// The kernel whose estimated time is least, in us.  Few rows: a fixed 3 and the
+// memory's rate (4.4 TB/s here) or the integer tensor rate (115 TOPS in whole
+// groups of 8 tokens), or a warp's k-steps one after another; twice that where K
+// leaves rows off a 16-byte boundary.  Tiles: 7 (9 with 128 tokens a tile) of
+// launches, fill and last store, a CTA's steps of 128 of k at 0.34 (0.38), and the
+// copy of such rows.  Measured either side, few rows and tiles: N = K = 2048: M 32
+// 7.0, 7.9; M 48 9.8, 8.2.  N 16384, K 2048: M 16 12.3, 12.1; M 24 19.7, 12.1.
+// N = K = 8192: M 8 18.2, 18.2; M 12 25.6, 18.3.  N 2048, K 8192: M 3 14.1, 10.4.
+// N 1023, K 3001: M 3 12.5, 9.1.  One or two tokens have a kernel of their own.
 int auto_config(int64_t M, int64_t N, int64_t K) {
-    if (K == 0) return CFG_ROWS;
-    const double nk = double(N) * double(K), sms = 152;
-    const double steps = double(padded_k(K) / BK);
-    auto tiles = [&](int64_t bm, int64_t bn, double slots, double step_us) {
-        return std::ceil(double(ceil_div(M, bm)) * double(ceil_div(N, bn)) / slots) * steps * step_us;
-    };
-    const double t[3] = {tiles(256, 256, sms / 2, 0.36), tiles(128, 128, sms, 0.22), tiles(128, 64, sms, 0.19)};
-    const int best = t[0] <= t[1] && t[0] <= t[2] ? 0 : t[1] <= t[2] ? 1 : 2;
-    const double few = std::max(nk / 6.5e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
-    const double many = 3.0 * (nk + double(M) * double(K)) / 5.5e6 + 6.0 + t[best];
-    return few <= many ? CFG_ROWS : CFG_PAIR + best;
+    if (K == 0 || M <= 2) return CFG_ROWS;
+    const double nk = double(N) * double(K), tiles = double(ceil_div(N, BM)) * double(ceil_div(M, stream_tokens(M)));
+    const double parts = stream_parts(int64_t(std::min(tiles, 1e6)), ceil_div(K, kStreamK));
+    const double steps = std::ceil(tiles * parts / 152.0) * std::ceil(double(ceil_div(K, kStreamK)) / parts);
+    const double rate = std::max(nk / 4.4e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
+    const double serial = 1.5 + 0.8 * double(ceil_div(K, 512)) * std::max(1.0, 0.8 + double(M) / 32.0);
+    const double few = std::max(rate, serial) * (K % 16 ? 2.0 : 1.0);
+    const double many = (stream_tokens(M) == 64 ? 7.2 + 0.34 * steps : 9.0 + 0.38 * steps) + (K % 16 ? nk / 2.5e6 : 0.0);
+    return few <= many ? CFG_ROWS : CFG_TILES;
 }
 
 bool operand_vec(const int8_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
@@ -1016,75 +777,6 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, unsigned size, const v
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TY, int BN, int CTAS>
-int launch_tile(const I8Args &a, __half *ws, cudaStream_t s) {
-    using T = TileCfg<BN, CTAS>;
-    const int64_t Kp = padded_k(a.K);
-    constexpr CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap ma, mb, mc;
-    if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, T::B_ROWS))
-        return REPOPS_ERR_UNSUPPORTED;
-    // C by TMA where its rows start on 16 bytes and a block's rows fill 128 bytes
-    constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
-    constexpr CUtensorMapDataType ctype = TY == REPOPS_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                          : TY == REPOPS_TYPE_F16 ? F16
-                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    constexpr int wide = 128 / int(csize);                             // columns of a stored block
-    const int c_tma = wide <= T::COLS && reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && uint64_t(a.ldc) * csize % 16 == 0 &&
-                      a.ldc < (int64_t(1) << 37) && make_map(&mc, ctype, csize, a.C, a.N, a.M, a.ldc, wide, 32);
-    if (!c_tma) mc = ma;
-    unsigned *status = nullptr;
-    int rc = status_word_address(&status);
-    if (rc != REPOPS_OK) return rc;
-    auto kern = CTAS == 2 ? gemm_i8_pair_kernel<TY> : gemm_i8_tile_kernel<TY, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    // nothing has been launched so far: from here on only a launch can fail
-    const int64_t items = (a.M + a.N) * (Kp / 8);
-    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
-    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) widen_kernel<true><<<wgrid, 256, 0, s>>>(a, Kp, ws);
-    else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
-    rc = check_launch();
-    if (rc != REPOPS_OK) return rc;
-    const TileMap tm{int(ceil_div(a.M, BM * CTAS)), int(ceil_div(a.N, BN)), 16 / CTAS};
-    const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
-    return launch_behind(kern, dim3(unsigned(std::min<int64_t>(tiles, sm_count() / CTAS) * CTAS)), kTileThreads,
-                         T::SMEM, s, ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
-}
-
-// ---- middling rows
-
-int64_t stream_k(int64_t K) { return ceil_div(K, kStreamK) * kStreamK; }
-
-// Tokens a tile.
-int stream_tokens(int64_t M) { return M <= 64 ? 64 : 128; }
-
-// The largest cluster whose CTAs are all resident at once for every tile, and no
-// more than one a k-step.  Clusters of one size that fit on the chip together:
-// measured, and fixed so that a product's split does not depend on the device.
-int stream_parts(int64_t tiles, int64_t ksteps) {
-    constexpr int64_t fit[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-    int p = 1;
-    for (int i = 2; i <= 8; ++i)
-        if (tiles <= fit[i] && i <= ksteps) p = i;
-    return p;
-}
-
-StreamMap stream_map(int64_t M, int64_t N, int64_t K) {
-    StreamMap sm;
-    sm.tiles_t = int(ceil_div(M, stream_tokens(M)));
-    sm.ksteps = int(ceil_div(K, kStreamK));
-    sm.tiles = int(ceil_div(N, BM) * sm.tiles_t);
-    sm.parts = stream_parts(sm.tiles, sm.ksteps);
-    return sm;
-}
-
-// The tokens in binary16, then B at a 16-byte pitch where TMA cannot read it in place.
-uint64_t stream_copy_at(int64_t M, int64_t K) { return uint64_t(M) * uint64_t(stream_k(K)) * 2u; }
-uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
-    return stream_copy_at(M, K) + uint64_t(N) * uint64_t(stream_k(K));
-}
-
 // The widened tokens as 64-k blocks: a box is BT tokens of two blocks, each with
 // rows of 128 bytes under the 128-byte swizzle.
 bool make_token_map(CUtensorMap *map, const __half *base, int64_t M, int64_t Kp, int box_rows) {
@@ -1106,7 +798,7 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
     int8_t *copy = reinterpret_cast<int8_t *>(ws + stream_copy_at(a.M, a.K));
     const bool in_place = operand_vec(a.B, a.ldb) && a.ldb < (int64_t(1) << 39), vec = operand_vec(a.A, a.lda);
     CUtensorMap mt, mw;
-    if (!make_token_map(&mt, tokens, a.M, Kp, BT) ||
+    if (!make_token_map(&mt, tokens, a.M * sm.copies, Kp, BT) ||
         !(in_place ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.B, a.K, a.N, a.ldb, kStreamK, BM)
                    : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, copy, Kp, a.N, Kp, kStreamK, BM)))
         return REPOPS_ERR_UNSUPPORTED;
@@ -1118,10 +810,10 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
     if (e != cudaSuccess) return set_cuda_error(e);
     // nothing has been launched so far: from here on only a launch can fail
     const int64_t items = std::max(a.M * (Kp / 8), in_place ? int64_t(0) : a.N * (Kp / 16));
-    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(items, 256), int64_t(sm_count()) * 4));
+    const unsigned grid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
     auto prep = in_place ? vec ? stream_prepare_kernel<true, false> : stream_prepare_kernel<false, false>
                          : vec ? stream_prepare_kernel<true, true> : stream_prepare_kernel<false, true>;
-    prep<<<grid, 256, 0, s>>>(a, Kp, tokens, copy);
+    prep<<<grid, 256, 0, s>>>(a, Kp, sm.copies, tokens, copy);
     rc = check_launch();
     if (rc != REPOPS_OK) return rc;
     constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
@@ -1135,9 +827,6 @@ template <int TY>
 int run_i8(int cfg, const I8Args &a, void *ws, cudaStream_t s) {
     switch (cfg) {
         case CFG_ROWS: return launch_rows<TY>(a, s);
-        case CFG_PAIR: return launch_tile<TY, 256, 2>(a, static_cast<__half *>(ws), s);
-        case CFG_TILE128: return launch_tile<TY, 128, 1>(a, static_cast<__half *>(ws), s);
-        case CFG_TILE64: return launch_tile<TY, 64, 1>(a, static_cast<__half *>(ws), s);
         default:
             return stream_tokens(a.M) == 64 ? launch_stream<TY, 64>(a, static_cast<uint8_t *>(ws), s)
                                             : launch_stream<TY, 128>(a, static_cast<uint8_t *>(ws), s);
@@ -1160,9 +849,7 @@ extern "C" uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_
         M > (int64_t(1) << 40) || N > (int64_t(1) << 40))
         return 0;
     if (config == CFG_AUTO) config = auto_config(M, N, K);
-    return config == CFG_ROWS     ? 0
-           : config == CFG_STREAM ? stream_workspace(M, N, K)
-                                  : tile_workspace(M, N, K);
+    return config == CFG_ROWS ? 0 : stream_workspace(M, N, K);
 }
 
 extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
