@@ -1030,8 +1030,9 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
  * the scaled zero (+ bias).
  * config -1 chooses by size; 0 .. repops_gemm_i8_config_count() - 1 force a
  * kernel (the same bits): 0 splits k between the lanes and warps of a CTA and
- * suits few rows of A; 1 runs on the tensor cores in binary16, A widened in
- * scratch, B on its way into tensor memory.
+ * suits few rows of A; 1 and 2 run on the tensor cores in binary16: 1 with A
+ * widened in scratch and B on its way into tensor memory, 2 (thousands of rows)
+ * with both widened in scratch.
  * ws: device scratch of repops_gemm_i8_workspace_bytes(config, M, N, K) bytes
  * (0 for config 0) on a 16-byte boundary, or NULL to take it from the scratch
  * pool on `stream` (ALLOC when refused).

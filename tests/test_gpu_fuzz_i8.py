@@ -52,7 +52,7 @@ def test_products(rp, seed):
     if bias is not None:
         want = want + bias
     dt = rng.choice(DTYPES)
-    for cfg in (-1, 0, 1):
+    for cfg in (-1, 0, 1, 2):
         pad, off = rng.choice([0, 1, 3, 4, 16]), rng.choice([0, 1, 4])
         whole = torch.full((M, off + N + pad), 7.0, device=DEV, dtype=dt)
         out = whole[:, off:off + N]

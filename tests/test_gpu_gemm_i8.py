@@ -54,7 +54,7 @@ SIZES = [(1, 1, 1), (1, 16, 64), (3, 5, 7), (8, 33, 64), (9, 130, 100), (16, 64,
          (1000, 100, 2048)]
 
 
-@pytest.mark.parametrize("config", [-1, 0, 1])
+@pytest.mark.parametrize("config", [-1, 0, 1, 2])
 @pytest.mark.parametrize("M,N,K", SIZES)
 def test_every_kernel_is_exact(rp, M, N, K, config):
     a, b, sa, sb, got, _ = check(rp, M, N, K, config)
@@ -62,13 +62,13 @@ def test_every_kernel_is_exact(rp, M, N, K, config):
         assert torch.equal(rp.gemm_i8(a, b.t(), sa, sb, config=config, out_dtype=dt), got.to(dt))
 
 
-@pytest.mark.parametrize("config", [0, 1])
+@pytest.mark.parametrize("config", [0, 1, 2])
 @pytest.mark.parametrize("off,pad", [(0, 16), (1, 0), (2, 2), (4, 4), (3, 13), (15, 1)])
 def test_alignment_and_pitch(rp, off, pad, config):
     check(rp, 21, 70, 203, config, off, pad, bias=True)
 
 
-@pytest.mark.parametrize("config", [0, 1])
+@pytest.mark.parametrize("config", [0, 1, 2])
 @pytest.mark.parametrize("K", [512, 1024, 8192, 131071])
 @pytest.mark.parametrize("va,vb", [(-128, -128), (-128, 127), (127, 127), (1, -1)])
 def test_extreme_sums(rp, config, K, va, vb):
@@ -84,7 +84,7 @@ def test_extreme_sums(rp, config, K, va, vb):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
-@pytest.mark.parametrize("config", [0, 1])
+@pytest.mark.parametrize("config", [0, 1, 2])
 def test_large_random_rows(rp, config):
     """A sample of rows of a product with several tiles a CTA."""
     M, N, K = 3000, 2100, 1600
@@ -98,7 +98,7 @@ def test_large_random_rows(rp, config):
     assert torch.equal(got, ref)
 
 
-@pytest.mark.parametrize("config", [0, 1])
+@pytest.mark.parametrize("config", [0, 1, 2])
 def test_rows_outside_are_left(rp, config):
     A, B = ints((70, 200), 3).to(DEV), ints((90, 200), 4).to(DEV)
     sa, sb = torch.ones(70, device=DEV), torch.ones(90, device=DEV)
@@ -111,18 +111,32 @@ def test_rows_outside_are_left(rp, config):
         assert (buf == 9.0).all()
 
 
+@pytest.mark.parametrize("config", [0, 1, 2])
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("N", [1, 9, 11, 131, 257, 260])
+def test_values_behind_a_row_are_left(rp, N, dt, config):
+    """Rows that start on 16 bytes and end between them, in a wider tensor."""
+    M, K = 150, 96
+    A, B = ints((M, K), 5).to(DEV), ints((N, K), 6).to(DEV)
+    sa, sb = torch.ones(M, device=DEV), torch.ones(N, device=DEV)
+    buf = torch.full((M, (N + 31) // 16 * 16), 9.0, dtype=dt, device=DEV)
+    rp.gemm_i8(A, B.t(), sa, sb, out=buf[:, :N], config=config)
+    assert torch.equal(buf[:, :N], (A.double() @ B.double().t()).to(dt))
+    assert (buf[:, N:] == 9.0).all()
+
+
 def test_empty_and_zero_k(rp):
     e = torch.empty(0, 8, dtype=torch.int8, device=DEV)
     w = ints((5, 8), 5).to(DEV)
     assert rp.gemm_i8(e, w.t(), torch.empty(0, device=DEV), torch.ones(5, device=DEV)).shape == (0, 5)
     a, b = torch.empty(3, 0, dtype=torch.int8, device=DEV), torch.empty(5, 0, dtype=torch.int8, device=DEV)
     bias = torch.arange(5, device=DEV, dtype=torch.float32)
-    for cfg in (-1, 0, 1):
+    for cfg in (-1, 0, 1, 2):
         y = rp.gemm_i8(a, b.t(), torch.ones(3, device=DEV), torch.ones(5, device=DEV), bias=bias, config=cfg)
         assert torch.equal(y, bias.expand(3, 5))
 
 
-@pytest.mark.parametrize("config", [0, 1])
+@pytest.mark.parametrize("config", [0, 1, 2])
 def test_scales_with_nan_and_infinity(rp, config):
     A, B = ints((4, 64), 6, 1, 100).to(DEV), ints((6, 64), 7, 1, 100).to(DEV)
     sa, sb = torch.ones(4, device=DEV), torch.ones(6, device=DEV)

@@ -201,7 +201,7 @@ def test_reference_format_on_known_values():
 
 def test_gemm_i8_refusals(L):
     s = L.repops_gemm_i8
-    assert L.repops_gemm_i8_config_count() == 2
+    assert L.repops_gemm_i8_config_count() == 3
     ws_bytes = L.repops_gemm_i8_workspace_bytes
     need = ws_bytes(1, 4, 6, 64)
     assert need > 0 and ws_bytes(0, 4, 6, 64) == 0 and ws_bytes(9, 4, 6, 64) == 0 and ws_bytes(1, 0, 6, 64) == 0
@@ -213,7 +213,7 @@ def test_gemm_i8_refusals(L):
         return s(*a.values(), None)
 
     assert call(M=-1) == -1 and call(N=-1) == -1 and call(K=-1) == -1
-    assert call(cfg=2) == -1 and call(cfg=-2) == -1 and call(tc=3) == -1
+    assert call(cfg=3) == -1 and call(cfg=-2) == -1 and call(tc=3) == -1
     for k in ("A", "sa", "B", "sb", "C"):
         assert call(**{k: None}) == -1
     assert call(lda=63) == -1 and call(ldb=63) == -1 and call(ldc=5) == -1

@@ -32,19 +32,23 @@
 // where it is the product's first operand (128 channels x k): its binary16 form
 // never passes through shared memory or DRAM.  (Widening both operands to scratch
 // first reads and writes 5 bytes for each of B's: with that, 8192 x 8192 took 64
-// us at 128 tokens and 214 at 2048, where this takes 21 and 178; at 8192 tokens,
-// where pairs of CTAs could share 256 x 256 tiles and read less shared memory,
-// both took 700.)  The tokens are widened to scratch before and loaded by TMA.
-// Where there are fewer tiles than SMs a cluster shares a tile's k: each CTA
-// leaves its 32-bit sums in shared memory, and after the cluster's barrier each
-// adds and stores its share of the tokens.  (Adding parts by atomics in scratch
-// took 23 us for 8192 x 8192, 64 tokens; this takes 18.)
+// us at 128 tokens and 214 at 2048, where this takes 22 and 180.)  The tokens are
+// widened to scratch before and loaded by TMA.  Where there are fewer tiles than
+// SMs a cluster shares a tile's k: each CTA leaves its 32-bit sums in shared
+// memory, and after the cluster's barrier each adds and stores its share of the
+// tokens.  (Adding parts by atomics in scratch took 23 us for 8192 x 8192, 64
+// tokens; this takes 19.)  Bound: at 64 tokens by what is not the products, 7 us
+// of launches, the tokens' widening, first loads and last stores, then by a step
+// of the products (0.33 us for 128 of k, 128 channels and 64 tokens; B at 5 TB/s);
+// at 2048 by the tensor cores (2048 x 16384 x 2048: 92 us, tensor pipe 71% active,
+// 224 steps of 128 x 128 x 128 at 0.37 us).
 //
-// Bound: at 64 tokens by what is not the products, 7 us of launches, the tokens'
-// widening, first loads and last stores, then by the issue of a step's products
-// (0.33 us for 128 of k, 128 channels and 64 tokens; B at 5 TB/s); with many by
-// the tensor cores at the clock the power limit leaves and by widening each
-// channel once for every 128 tokens (8192 x 8192 x 8192: 1.58 PFLOP/s).
+// Thousands of rows: widening each channel once for every 128 tokens costs more
+// than widening it once to scratch, above all in power.  Pairs of CTAs
+// (cta_group::2, each reads half of B from its shared memory) multiply tiles of
+// 256 x 256 from widened copies.  8192 x 8192 x 8192 takes 670 us: 59 to widen
+// (6.8 TB/s), then 1.8 PFLOP/s, bound by the tensor cores at the clock the power
+// limit leaves; the kernel above takes 690 (740 against 700 where L2 is cold).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -396,7 +400,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
         mbar_init(&drained, 1);
         fence_barrier_init();
     }
-    if (warp == 18) tmem_alloc(&tmem_slot, 512);
+    if (warp == 18) tmem_alloc<1>(&tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -472,23 +476,23 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                             const uint64_t db = smem_desc_sw128(base + s * T::T_BYTES + h * T::BOX_BYTES);
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                tc_mma_f16(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc,
+                                tc_mma_f16_tmem(tmem + b * BT, a + 32 * h + 8 * j, db + 2 * j, idesc,
                                                 i > 0 || h > 0 || j > 0);
                         }
-                        tc_commit(&used[s]);
+                        tc_commit<1>(&used[s]);
                         if (++s == T::T_STAGES) {
                             s = 0;
                             phase ^= 1u;
                         }
                     }
-                    if (ok) tc_commit(&acc_full[b]);
+                    if (ok) tc_commit<1>(&acc_full[b]);
                     b ^= 1;
                     if (b == 0) acc_phase ^= 1u;
                 }
             }
             if (!ok) {
                 atomicOr(status, 1u);
-                tc_commit(&drained);
+                tc_commit<1>(&drained);
                 mbar_wait_bounded(&drained, 0u);
             }
         }
@@ -649,12 +653,304 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 18) tmem_free(tmem, 512);
+    if (warp == 18) tmem_free<1>(tmem, 512);
+}
+
+// ------------------------------------------------------------ thousands of rows ----
+
+// With thousands of tokens the widening of B pays even through DRAM: a pair of CTAs
+// multiplies a tile of 256 tokens x 256 channels from widened copies of both
+// operands, and a stage's 64 KB feed twice the products that they feed above.
+constexpr int BK = 64;                    // BK binary16 = one 128-byte swizzled row
+constexpr int kPairChunk = 1024 / BK;     // k-steps between two drains
+constexpr int kPairThreads = 320;         // 8 epilogue warps, a TMA warp, an MMA warp
+
+struct PairCfg {
+    static constexpr int BN = 256, B_ROWS = BN / 2;
+    static constexpr int STAGE_BYTES = (BM + B_ROWS) * BK * 2;
+    static constexpr int STAGES = 6;
+    static constexpr int WARP_STAGE = 32 * 128;                  // an epilogue warp's block: 32 rows of 128 bytes
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 8 * WARP_STAGE;
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+    static constexpr int COLS = BN / 2;                          // an epilogue warp's columns
+};
+
+// The rows of A, then those of B, as binary16 rows of Kp (a multiple of 64)
+// values, zeros past K.  An item is 8 values, so that a warp's store covers 512
+// consecutive bytes (16 values an item, stored as two halves of each 32-byte
+// sector, took a third longer); two items a thread are in flight.
+template <bool VEC>
+__global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half *__restrict__ out) {
+    grid_release();
+    const uint32_t per = uint32_t(Kp / 8);
+    const int64_t items = (p.M + p.N) * per, stride = int64_t(gridDim.x) * 512;
+    for (int64_t i0 = blockIdx.x * int64_t(512) + threadIdx.x; i0 < items; i0 += stride) {
+        uint2 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t it = min(i0 + 256 * j, items - 1);       // past the end: the last one again
+            const int64_t r = items <= UINT32_MAX ? uint32_t(it) / per : it / per;
+            const int64_t k = (it - r * per) * 8;
+            w[j] = r < p.M ? load_k8<VEC>(p.A + r * p.lda, k, p.K, p.A, p.a_end)
+                           : load_k8<VEC>(p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (i0 + 256 * j >= items) continue;
+            const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
+            *reinterpret_cast<uint4 *>(out + (i0 + 256 * j) * 8) =
+                make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+        }
+    }
+}
+
+// C's tile: sums x scales, through the warp's block of shared memory.  Lane l
+// holds the scales (and biases) of columns l, l + 32, ...  c_tma: C can be
+// stored by TMA (a block of 32 rows x 128 bytes at a time, clipped at C's
+// edges); else lanes store single values.
+template <int TY, int COLS>
+__device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *map_c, const int (&acc)[COLS], float sa,
+                                           const float (&sb)[COLS / 32], const float (&bias)[COLS / 32], int64_t row0,
+                                           int64_t col0, uint8_t *block, bool c_tma) {
+    constexpr int W = TY == REPOPS_TYPE_F32 ? 32 : 64;         // columns of a block
+    const int lane = threadIdx.x & 31;
+    uint4 *chunk = reinterpret_cast<uint4 *>(block);           // 16-byte chunk c of row r in slot c ^ (r & 7)
+#pragma unroll
+    for (int j = 0; j < COLS; j += W) {
+        if (col0 + j >= p.N) break;
+        if (c_tma && lane == 0) tma_store_wait_read();         // the block's previous contents have left
+        __syncwarp();
+#pragma unroll
+        for (int c = j; c < j + W; c += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = __fmul_rn(__fmul_rn(__int2float_rn(acc[c + i]), sa),
+                                 __shfl_sync(0xffffffffu, sb[c / 32], (c + i) % 32));
+            if (p.bias) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = __fadd_rn(v[i], __shfl_sync(0xffffffffu, bias[c / 32], (c + i) % 32));
+            }
+            if constexpr (TY == REPOPS_TYPE_F32) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    chunk[lane * 8 + (((c - j) / 4 + h) ^ (lane & 7))] =
+                        make_uint4(__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                                   __float_as_uint(v[4 * h + 3]));
+            } else {
+                chunk[lane * 8 + (((c - j) / 8) ^ (lane & 7))] = make_uint4(
+                    pack_c<TY>(v[0], v[1]), pack_c<TY>(v[2], v[3]), pack_c<TY>(v[4], v[5]), pack_c<TY>(v[6], v[7]));
+            }
+        }
+        if (c_tma) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && row0 < p.M) tma_store_2d(map_c, block, int32_t(col0 + j), int32_t(row0));
+        } else {
+            __syncwarp();
+            using E = typename std::conditional<TY == REPOPS_TYPE_F32, float, uint16_t>::type;
+            constexpr int PER = 16 / int(sizeof(E));           // values of a chunk
+            const E *e = reinterpret_cast<const E *>(block);
+            const int rows = int(min(p.M - row0, int64_t(32)));
+#pragma unroll
+            for (int h = 0; h < W; h += 32) {
+                const int c = h + lane;
+                E *out = static_cast<E *>(p.C) + row0 * p.ldc + col0 + j + c;
+                const bool mine = col0 + j + c < p.N;
+#pragma unroll 8
+                for (int r = 0; r < 32; ++r) {
+                    const E v = e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
+                    if (mine && r < rows) out[r * p.ldc] = v;
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+template <int TY>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                    const __grid_constant__ CUtensorMap map_c, I8Args p, TileMap tm, int ksteps, int c_tma,
+                    unsigned *status) {
+    using T = PairCfg;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int tiles = tm.tiles_m * tm.tiles_n, first = blockIdx.x / 2, stride = gridDim.x / 2;
+    const int chunks = (ksteps + kPairChunk - 1) / kPairChunk;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < T::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 16);
+        }
+        mbar_init(&drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc<2>(&tmem_slot, T::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    grid_wait();                                               // the widened operands
+
+    // Every wait gives up after its limit, as in the kernel above.
+    if (warp == 8) {
+        if (elect_one()) {
+            prefetch_tensormap(&map_a);
+            prefetch_tensormap(&map_b);
+            int issued = 0, s = 0;
+            uint32_t phase = 1;                                // the wait before the ring's first use passes
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += stride) {
+                int m, n;
+                tm.at(t, m, n);
+                const int row_a = (m * 2 + int(rank)) * BM, row_b = n * T::BN + int(rank) * T::B_ROWS;
+                for (int k = 0; k < ksteps; ++k, ++issued) {
+                    if (!mbar_wait_bounded(&empty[s], phase)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = stages + s * T::STAGE_BYTES;
+                    // a pair's four copies all signal the first CTA, whose
+                    // barrier is armed for both CTAs' bytes; a copy of the other
+                    // CTA that lands before that leaves the phase open, as the
+                    // arming arrival is still missing
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * T::STAGE_BYTES);
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    tma_load_2d_pair(st, &map_a, bar, k * BK, row_a);
+                    tma_load_2d_pair(st + BM * BK * 2, &map_b, bar, k * BK, row_b);
+                    if (++s == T::STAGES) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                atomicOr(status, 1u);
+                if (rank == 0) {
+                    for (int i = max(0, issued - T::STAGES); i < issued; ++i)
+                        mbar_wait_bounded(&full[i % T::STAGES], uint32_t(i / T::STAGES) & 1u);
+                } else {
+                    // these copies signal the other CTA: give them the time of
+                    // a copy a thousand times over
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 2000000u) {}
+                }
+            }
+        }
+    } else if (warp == 9) {
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = idesc_f16(2 * BM, T::BN);
+            const uint32_t base = smem_addr(stages);
+            int s = 0, b = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += stride) {
+                for (int c = 0; c < chunks && ok; ++c) {
+                    if (!mbar_wait_bounded(&acc_empty[b], acc_phase)) {
+                        ok = false;
+                        break;
+                    }
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    tc_fence_after();
+                    const int steps = min(kPairChunk, ksteps - c * kPairChunk);
+                    for (int k = 0; k < steps; ++k) {
+                        if (!mbar_wait_bounded(&full[s], phase)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = base + s * T::STAGE_BYTES;
+                        const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + BM * BK * 2);
+#pragma unroll
+                        for (int j = 0; j < BK / 16; ++j)      // 32 bytes of k a step within the swizzled row
+                            tc_mma_f16_pair(tmem + b * T::BN, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+                        tc_commit<2>(&empty[s]);
+                        if (++s == T::STAGES) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (ok) tc_commit<2>(&acc_full[b]);
+                    b ^= 1;
+                    if (b == 0) acc_phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                atomicOr(status, 1u);
+                tc_commit<2>(&drained);
+                mbar_wait_bounded(&drained, 0u);
+            }
+        }
+    } else {
+        const int half = warp >> 2;                            // columns half * COLS .. of the tile
+        const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+        uint8_t *block = stages + T::STAGES * T::STAGE_BYTES + warp * T::WARP_STAGE;
+        int b = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += stride) {
+            int tile_m, tile_n;
+            tm.at(t, tile_m, tile_n);
+            const int64_t row0 = (int64_t(tile_m) * 2 + rank) * BM + 32 * (warp & 3),
+                          col0 = int64_t(tile_n) * T::BN + half * T::COLS;
+            const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
+            float sb[T::COLS / 32], bias[T::COLS / 32];
+#pragma unroll
+            for (int i = 0; i < T::COLS / 32; ++i) {
+                const int64_t col = min(col0 + 32 * i + lane, p.N - 1);    // past the end: not stored
+                sb[i] = __ldg(p.sb + col);
+                bias[i] = p.bias ? __ldg(p.bias + col) : 0.0f;
+            }
+            int acc[T::COLS];
+#pragma unroll
+            for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
+            for (int c = 0; c < chunks; ++c) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[b], phase));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < T::COLS; j += 16) {
+                    uint32_t v[16];
+                    tmem_load16(tmem + lanes + b * T::BN + half * T::COLS + j, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[j + i] += __float2int_rn(__uint_as_float(v[i]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+                b ^= 1;
+                if (b == 0) phase ^= 1u;
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(status, 1u);
+                break;
+            }
+            store_tile<TY, T::COLS>(p, &map_c, acc, sa, sb, bias, row0, col0, block, c_tma != 0);
+        }
+        if (c_tma && lane == 0) tma_store_wait();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                   // no CTA leaves while the other may signal it
+    tc_fence_after();
+    if (warp == 9) tmem_free<2>(tmem, T::TMEM_COLS);
 }
 
 // ------------------------------------------------------------------- host ----
 
-enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_TILES, CFG_COUNT };
+enum I8Config { CFG_AUTO = -1, CFG_ROWS, CFG_TILES, CFG_PAIR, CFG_COUNT };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -662,6 +958,10 @@ int sm_count() {
     DeviceInfo di;
     return current_device_info(&di) == REPOPS_OK ? di.sms : 152;
 }
+
+int64_t padded_k(int64_t K) { return ceil_div(K, BK) * BK; }
+
+uint64_t pair_workspace(int64_t M, int64_t N, int64_t K) { return uint64_t(M + N) * uint64_t(padded_k(K)) * 2u; }
 
 int64_t stream_k(int64_t K) { return ceil_div(K, kStreamK) * kStreamK; }
 
@@ -705,25 +1005,35 @@ uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
     return stream_copy_at(M, K) + uint64_t(N) * uint64_t(stream_k(K));
 }
 
-// The kernel whose estimated time is least, in us.  Few rows: a fixed 3 and the
-// memory's rate (4.4 TB/s here) or the integer tensor rate (115 TOPS in whole
-// groups of 8 tokens), or a warp's k-steps one after another; twice that where K
-// leaves rows off a 16-byte boundary.  Tiles: 7 (9 with 128 tokens a tile) of
-// launches, fill and last store, a CTA's steps of 128 of k at 0.34 (0.38), and the
-// copy of such rows.  Measured either side, few rows and tiles: N = K = 2048: M 32
-// 7.0, 7.9; M 48 9.8, 8.2.  N 16384, K 2048: M 16 12.3, 12.1; M 24 19.7, 12.1.
-// N = K = 8192: M 8 18.2, 18.2; M 12 25.6, 18.3.  N 2048, K 8192: M 3 14.1, 10.4.
-// N 1023, K 3001: M 3 12.5, 9.1.  One or two tokens have a kernel of their own.
+// The kernel whose estimated time is least, in us.
+// Few rows: a fixed 3 and the memory's rate (4.4 TB/s here) or the integer tensor
+// rate (115 TOPS in whole groups of 8 tokens), or a warp's k-steps one after
+// another; twice that where K leaves rows off a 16-byte boundary.  Tiles: 7 (9 with
+// 128 tokens a tile) of launches, fill and last store, a CTA's steps of 128 of k at
+// 0.34 (0.38 with 128), the widening of many tokens and the copy of such rows of B.
+// Pairs: 8, the widening, and the waves of tiles x steps of 64 of k at 0.342.
+// Measured either side, few rows and tiles: N = K = 2048: M 32 7.0, 7.9; M 48 9.8,
+// 8.2.  N 16384, K 2048: M 16 12.3, 12.1; M 24 19.7, 12.1.  N = K = 8192: M 8 18.2,
+// 18.2; M 12 25.6, 18.3.  N 2048, K 8192: M 3 14.1, 10.4.  N 1023, K 3001: M 3 12.5,
+// 9.1.  Tiles and pairs: N = K = 8192: M 2048 179, 214; M 4096 352, 363; M 8192 690,
+// 669.  N 16384, K 2048: M 2048 92, 100; M 8192 356, 350.  N 1023, K 3001: M 4097
+// 35.5, 36.5.  One or two tokens have a kernel of their own.
 int auto_config(int64_t M, int64_t N, int64_t K) {
     if (K == 0 || M <= 2) return CFG_ROWS;
-    const double nk = double(N) * double(K), tiles = double(ceil_div(N, BM)) * double(ceil_div(M, stream_tokens(M)));
-    const double parts = stream_parts(int64_t(std::min(tiles, 1e6)), ceil_div(K, kStreamK));
-    const double steps = std::ceil(tiles * parts / 152.0) * std::ceil(double(ceil_div(K, kStreamK)) / parts);
+    const double nk = double(N) * double(K), mk = double(M) * double(K), bt = stream_tokens(M);
+    const double odd = K % 16 ? 1.0 : 0.0;
     const double rate = std::max(nk / 4.4e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
     const double serial = 1.5 + 0.8 * double(ceil_div(K, 512)) * std::max(1.0, 0.8 + double(M) / 32.0);
-    const double few = std::max(rate, serial) * (K % 16 ? 2.0 : 1.0);
-    const double many = (stream_tokens(M) == 64 ? 7.2 + 0.34 * steps : 9.0 + 0.38 * steps) + (K % 16 ? nk / 2.5e6 : 0.0);
-    return few <= many ? CFG_ROWS : CFG_TILES;
+    const double few = std::max(rate, serial) * (1.0 + odd);
+    const double tiles = double(ceil_div(N, BM)) * std::ceil(double(M) / bt);
+    const double parts = stream_parts(int64_t(std::min(tiles, 1e6)), ceil_div(K, kStreamK));
+    const double steps = std::ceil(tiles * parts / 152.0) * std::ceil(double(ceil_div(K, kStreamK)) / parts);
+    const double many = (bt == 64 ? 7.2 + 0.34 * steps : 9.0 + 0.38 * steps) + std::max(0.0, 3.0 * mk / 5.5e6 - 3.0) +
+                        odd * nk / 2.5e6;
+    const double waves = std::ceil(double(ceil_div(M, 256)) * double(ceil_div(N, 256)) / 76.0);
+    const double pairs = 8.0 + 3.0 * (nk + mk) / 5.5e6 + 0.342 * waves * double(ceil_div(K, BK)) + odd * (nk + mk) / 2.5e6;
+    if (few <= many && few <= pairs) return CFG_ROWS;
+    return many <= pairs ? CFG_TILES : CFG_PAIR;
 }
 
 bool operand_vec(const int8_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
@@ -824,9 +1134,48 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
 }
 
 template <int TY>
+int launch_pair(const I8Args &a, __half *ws, cudaStream_t s) {
+    using T = PairCfg;
+    const int64_t Kp = padded_k(a.K);
+    constexpr CUtensorMapDataType F16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap ma, mb, mc;
+    if (!make_map(&ma, F16, 2, ws, Kp, a.M, Kp, BK, BM) || !make_map(&mb, F16, 2, ws + a.M * Kp, Kp, a.N, Kp, BK, T::B_ROWS))
+        return REPOPS_ERR_UNSUPPORTED;
+    // C by TMA where its rows start on 16 bytes and end on them: a store clips at
+    // C's edge in units of 16 bytes, and what is behind a row is not C's
+    constexpr unsigned csize = TY == REPOPS_TYPE_F32 ? 4u : 2u;
+    constexpr CUtensorMapDataType ctype = TY == REPOPS_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                          : TY == REPOPS_TYPE_F16 ? F16
+                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr int wide = 128 / int(csize);                             // columns of a stored block
+    const int c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && uint64_t(a.ldc) * csize % 16 == 0 &&
+                      uint64_t(a.N) * csize % 16 == 0 &&
+                      a.ldc < (int64_t(1) << 37) && make_map(&mc, ctype, csize, a.C, a.N, a.M, a.ldc, wide, 32);
+    if (!c_tma) mc = ma;
+    unsigned *status = nullptr;
+    int rc = status_word_address(&status);
+    if (rc != REPOPS_OK) return rc;
+    auto kern = gemm_i8_pair_kernel<TY>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    // nothing has been launched so far: from here on only a launch can fail
+    const int64_t items = (a.M + a.N) * (Kp / 8);
+    const unsigned wgrid = unsigned(std::min<int64_t>(ceil_div(items, 512), int64_t(sm_count()) * 32));
+    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) widen_kernel<true><<<wgrid, 256, 0, s>>>(a, Kp, ws);
+    else widen_kernel<false><<<wgrid, 256, 0, s>>>(a, Kp, ws);
+    rc = check_launch();
+    if (rc != REPOPS_OK) return rc;
+    const TileMap tm{int(ceil_div(a.M, 2 * BM)), int(ceil_div(a.N, T::BN)), 8};
+    const int64_t tiles = int64_t(tm.tiles_m) * tm.tiles_n;
+    return launch_behind(kern, dim3(unsigned(std::min<int64_t>(tiles, sm_count() / 2) * 2)), kPairThreads,
+                         T::SMEM, s, ma, mb, mc, a, tm, int(Kp / BK), c_tma, status);
+}
+
+template <int TY>
 int run_i8(int cfg, const I8Args &a, void *ws, cudaStream_t s) {
     switch (cfg) {
         case CFG_ROWS: return launch_rows<TY>(a, s);
+        case CFG_PAIR: return launch_pair<TY>(a, static_cast<__half *>(ws), s);
         default:
             return stream_tokens(a.M) == 64 ? launch_stream<TY, 64>(a, static_cast<uint8_t *>(ws), s)
                                             : launch_stream<TY, 128>(a, static_cast<uint8_t *>(ws), s);
@@ -849,7 +1198,7 @@ extern "C" uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_
         M > (int64_t(1) << 40) || N > (int64_t(1) << 40))
         return 0;
     if (config == CFG_AUTO) config = auto_config(M, N, K);
-    return config == CFG_ROWS ? 0 : stream_workspace(M, N, K);
+    return config == CFG_ROWS ? 0 : config == CFG_PAIR ? pair_workspace(M, N, K) : stream_workspace(M, N, K);
 }
 
 extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,

@@ -1,6 +1,9 @@
 // tcgen05.cuh -- inline PTX of the fifth-generation tensor core: tensor memory,
-// the product of 128 rows in it with an operand in shared memory, writing and
-// reading it, and the shared memory of a cluster's other CTAs.
+// products into it and reading it back, for one CTA (CTAS = 1, cta_group::1) or a
+// pair of a cluster (CTAS = 2): the pair multiplies 256 rows, each CTA holding its
+// half of both operands in its shared memory and its half of the rows in its
+// tensor memory; the CTA of rank 0 issues the products.  And the shared memory of
+// a cluster's other CTAs.
 #pragma once
 
 #include "internal.cuh"
@@ -8,15 +11,27 @@
 namespace repops {
 
 // Columns of tensor memory (a power of two, 32 .. 512) for this CTA; the
-// address lands in *slot (shared memory).  One whole warp calls it; the same warp
-// releases them.
+// address lands in *slot (shared memory).  One whole warp calls it (of each CTA
+// of a pair); the same warp releases them.
+template <int CTAS>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (CTAS == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
 }
+
+template <int CTAS>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    if constexpr (CTAS == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -47,6 +62,20 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// A TMA load into this CTA's shared memory that signals the mbarrier at cluster
+// address `bar`, which may be the pair's other CTA's.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
 // One lane of a converged warp, the same each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -69,10 +98,19 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
 // accumulators, an m x n product.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 
-// D = A * B^T (+ D when accumulate), 16 of k: D and the 128 rows of A in tensor
-// memory (A's k in the 8 columns from `a` on, each holding two, the lower k in the
-// lower half), B in shared memory.  One thread.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D (tensor memory) = A * B^T (+ D when accumulate), 16 of k, by a pair with both
+// operands in shared memory.  One thread.
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+
+// The same by one CTA with the 128 rows of A in tensor memory, 16 of k in the 8
+// columns from `a` on (each holds two, the lower k in the lower half).
+__device__ __forceinline__ void tc_mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
@@ -80,10 +118,20 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, u
         : "memory");
 }
 
-// Arrives on `bar` once every product this thread has issued is complete.
+// Arrives on `bar` (of both CTAs of a pair) once every product this thread has
+// issued is complete.
+template <int CTAS>
 __device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    if constexpr (CTAS == 1) {
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(bar)),
+            "h"(uint16_t(3))
+            : "memory");
+    }
 }
 
 // 16 consecutive columns of the warp's 32 lanes: v[i] = column i of the lane.
@@ -115,5 +163,18 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&v)[
         : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Starts the store of a tile in shared memory to the map's box at (c0, c1);
+// what lies outside the tensor is not written.  One thread, which also waits:
+// for the tile to have been read, or for everything to have been written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace repops
