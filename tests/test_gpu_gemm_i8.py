@@ -63,7 +63,7 @@ def test_every_kernel_is_exact(rp, M, N, K, config):
 
 
 @pytest.mark.parametrize("config", [0, 1, 2])
-@pytest.mark.parametrize("off,pad", [(0, 16), (1, 0), (2, 2), (4, 4), (3, 13), (15, 1)])
+@pytest.mark.parametrize("off,pad", [(0, 5), (0, 16), (1, 0), (2, 2), (4, 4), (3, 13), (15, 1)])
 def test_alignment_and_pitch(rp, off, pad, config):
     check(rp, 21, 70, 203, config, off, pad, bias=True)
 

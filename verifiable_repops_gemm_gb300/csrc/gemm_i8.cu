@@ -1106,6 +1106,7 @@ int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
     const StreamMap sm = stream_map(a.M, a.N, a.K);
     __half *tokens = reinterpret_cast<__half *>(ws);
     int8_t *copy = reinterpret_cast<int8_t *>(ws + stream_copy_at(a.M, a.K));
+    // bytes that a 16-byte unit brings along behind K meet the tokens' zeros there
     const bool in_place = operand_vec(a.B, a.ldb) && a.ldb < (int64_t(1) << 39), vec = operand_vec(a.A, a.lda);
     CUtensorMap mt, mw;
     if (!make_token_map(&mt, tokens, a.M * sm.copies, Kp, BT) ||
