@@ -111,6 +111,23 @@ def test_rows_outside_are_left(rp, config):
         assert (buf == 9.0).all()
 
 
+@pytest.mark.parametrize("M", [40, 100])
+@pytest.mark.parametrize("K", [300, 900, 3500])
+@pytest.mark.parametrize("tiles", [7, 15, 16, 23, 24, 28, 29, 36, 37, 46, 47, 76, 77, 200])
+def test_every_split_of_k(rp, tiles, K, M):
+    """Either side of each number of tiles at which the CTAs that share one change,
+    with fewer k-steps than CTAs and more; both tile heights; C aligned and not."""
+    N = 128 * tiles - 3
+    g = torch.Generator(device=DEV).manual_seed(tiles)
+    A, B = (torch.randint(-128, 128, (r, K), generator=g, device=DEV, dtype=torch.int8) for r in (M, N))
+    sa, sb, bias = torch.rand(M, device=DEV), torch.rand(N, device=DEV), torch.randn(N, device=DEV)
+    want = (A.double() @ B.double().t()).float() * sa[:, None] * sb + bias
+    for ldc in (N, N + 3):
+        out = torch.empty(M, ldc, device=DEV)[:, :N]
+        assert torch.equal(rp.gemm_i8(A, B.t(), sa, sb, out=out, bias=bias, config=1), want)
+    assert rp.device_status() == 0
+
+
 @pytest.mark.parametrize("config", [0, 1, 2])
 @pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("N", [1, 9, 11, 131, 257, 260])
