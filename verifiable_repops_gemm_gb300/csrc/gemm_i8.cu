@@ -18,7 +18,7 @@
 // add their sums in shared memory.  The instruction's rate here is 130 TOPS
 // (measured), enough for 8 tokens at the memory's rate; widening to binary16
 // in registers for the faster-looking m16n8k16.f16 took 31 us where this takes
-// 13 (16384 channels, 2048 k, 13 tokens).
+// 12 (16384 channels, 2048 k, 13 tokens).
 //
 // More rows: tcgen05 on binary16 (8 bits fit its 11) with binary32 accumulators
 // in tensor memory.  Every product and every partial sum of up to 1024 of them is
@@ -108,6 +108,27 @@ __device__ __forceinline__ uint4 load_k16(const int8_t *__restrict__ row, int64_
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// 16 or 8 bytes that all lie within a row, without a branch: a guard around a load
+// makes the loads of a loop wait for one another.  Where the address is not
+// aligned, every word read holds at least one of the bytes asked for.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_full16(const int8_t *__restrict__ p) {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u), s = 8 * off;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - off);
+    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3), e = __ldg(w + (off ? 4 : 3));
+    return make_uint4(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s), __funnelshift_r(c, d, s),
+                      __funnelshift_r(d, e, s));
+}
+template <bool VEC>
+__device__ __forceinline__ uint2 load_full8(const int8_t *__restrict__ p) {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u), s = 8 * off;
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - off);
+    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + (off ? 2 : 1));
+    return make_uint2(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s));
+}
+
 // ---------------------------------------------------------------- epilogue ----
 
 template <int TY>
@@ -162,15 +183,13 @@ __global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int m = 0; m < NT; ++m) acc[r][m] = 0;
-    const int K = int(p.K);
-#pragma unroll 8 / R
-    for (int k = 16 * lane; k < K; k += 512) {
-        uint4 w[R], x[NT];
-        // a channel or token past the end repeats the last one, and is not stored
+    // a channel or token past the end repeats the last one, and is not stored
+    const int8_t *rw[R], *rx[NT];
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = load_k16<VEC>(p.B + min(j0 + r, p.N - 1) * p.ldb, k, K, p.B, p.b_end);
+    for (int r = 0; r < R; ++r) rw[r] = p.B + min(j0 + r, p.N - 1) * p.ldb;
 #pragma unroll
-        for (int m = 0; m < NT; ++m) x[m] = load_k16<VEC>(p.A + min(int64_t(m), p.M - 1) * p.lda, k, K, p.A, p.a_end);
+    for (int m = 0; m < NT; ++m) rx[m] = p.A + min(int64_t(m), p.M - 1) * p.lda;
+    auto multiply = [&](const uint4 (&w)[R], const uint4 (&x)[NT]) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -180,6 +199,25 @@ __global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
                 acc[r][m] = __dp4a(int(w[r].z), int(x[m].z), acc[r][m]);
                 acc[r][m] = __dp4a(int(w[r].w), int(x[m].w), acc[r][m]);
             }
+    };
+    const int K = int(p.K);
+    int k = 16 * lane;
+#pragma unroll 8 / R
+    for (; k + 16 <= K; k += 512) {
+        uint4 w[R], x[NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = load_full16<VEC>(rw[r] + k);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) x[m] = load_full16<VEC>(rx[m] + k);
+        multiply(w, x);
+    }
+    if (k < K) {
+        uint4 w[R], x[NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = load_k16<VEC>(rw[r], k, K, p.B, p.b_end);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) x[m] = load_k16<VEC>(rx[m], k, K, p.A, p.a_end);
+        multiply(w, x);
     }
     int mine = 0;                      // lane r * NT + m keeps channel r, token m
 #pragma unroll
@@ -197,41 +235,70 @@ __global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
 }
 
 // 16 channels x 8 * NT tokens a CTA of 8 warps; warp w takes the 64-k steps w,
-// w + 8, ...  (Two tiles of channels a warp were slower at every size but one.)
+// w + 8, ...  (Two tiles of channels a warp were slower at every size but one.)  The
+// instruction's latency is long: a step's two go to accumulators of their own (2048
+// channels of 8192, 8 tokens: 12.2 -> 8.7 us), and with more than 8 tokens a step's
+// loads in flight are enough (two or four took a warp's place on the SM: 16384 x
+// 2048, 32 tokens 19.7, with two 23).
 template <int TY, int NT, bool VEC>
 __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
     constexpr int CH = 16, TK = 8 * NT, PITCH = CH + 4;         // 2 * PITCH = 8 (mod 32): the adds hit 32 banks
-    constexpr int UNROLL = NT <= 2 ? 4 : 2;
+    constexpr int UNROLL = NT == 1 ? 4 : 1;           // k-steps whose loads are in flight
     __shared__ int sum[TK][PITCH];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int64_t n0 = int64_t(blockIdx.x) * CH, m0 = int64_t(blockIdx.y) * TK;
     for (int i = threadIdx.x; i < TK * PITCH; i += 256) (&sum[0][0])[i] = 0;
-    int d[NT][4];
+    int d[NT][4], d2[NT][4];
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[u][i] = 0;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const int steps = int((p.K + 63) / 64);
-#pragma unroll UNROLL
-    for (int s = warp; s < steps; s += 8) {
-        const int64_t k = int64_t(s) * 64 + 16 * q;
-        uint4 w[2], x[NT];
+        for (int i = 0; i < 4; ++i) d[u][i] = d2[u][i] = 0;
+    // a channel or token past the end repeats the last one, and is not stored
+    const int8_t *rw[2], *rx[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t j = n0 + 8 * h + g;
-            w[h] = j < p.N && k < p.K ? load_k16<VEC>(p.B + j * p.ldb, k, p.K, p.B, p.b_end) : zero;
-        }
+    for (int h = 0; h < 2; ++h) rw[h] = p.B + min(n0 + 8 * h + g, p.N - 1) * p.ldb;
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const int64_t i = m0 + 8 * u + g;
-            x[u] = i < p.M && k < p.K ? load_k16<VEC>(p.A + i * p.lda, k, p.K, p.A, p.a_end) : zero;
-        }
+    for (int u = 0; u < NT; ++u) rx[u] = p.A + min(m0 + 8 * u + g, p.M - 1) * p.lda;
+    const int full = int(p.K / 64);
+    auto multiply = [&](const uint4 (&w)[2], const uint4 (&x)[NT]) {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             mma_s8(d[u], w[0].x, w[1].x, w[0].y, w[1].y, x[u].x, x[u].y);
-            mma_s8(d[u], w[0].z, w[1].z, w[0].w, w[1].w, x[u].z, x[u].w);
+            mma_s8(d2[u], w[0].z, w[1].z, w[0].w, w[1].w, x[u].z, x[u].w);
         }
+    };
+    const int ahead = full - 8 * (UNROLL - 1);
+    int s = warp;
+    for (; s < ahead; s += 8 * UNROLL) {
+        uint4 w[UNROLL][2], x[UNROLL][NT];
+#pragma unroll
+        for (int e = 0; e < UNROLL; ++e) {
+            const int k = (s + 8 * e) * 64 + 16 * q;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) w[e][h] = load_full16<VEC>(rw[h] + k);
+#pragma unroll
+            for (int u = 0; u < NT; ++u) x[e][u] = load_full16<VEC>(rx[u] + k);
+        }
+#pragma unroll
+        for (int e = 0; e < UNROLL; ++e) multiply(w[e], x[e]);
+    }
+    for (; s < full; s += 8) {
+        const int k = s * 64 + 16 * q;
+        uint4 w[2], x[NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[h] = load_full16<VEC>(rw[h] + k);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) x[u] = load_full16<VEC>(rx[u] + k);
+        multiply(w, x);
+    }
+    if (s == full && p.K % 64) {                               // the last step, in part behind K
+        const int64_t k = int64_t(s) * 64 + 16 * q;
+        uint4 w[2], x[NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[h] = load_k16<VEC>(rw[h], k, p.K, p.B, p.b_end);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) x[u] = load_k16<VEC>(rx[u], k, p.K, p.A, p.a_end);
+        multiply(w, x);
     }
     __syncthreads();
     // lane: channels g and g + 8, tokens 2q and 2q + 1 of each tile
@@ -239,7 +306,7 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
     for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            atomicAdd(&sum[8 * u + 2 * q + (i & 1)][8 * (i >> 1) + g], d[u][i]);
+            atomicAdd(&sum[8 * u + 2 * q + (i & 1)][8 * (i >> 1) + g], d[u][i] + d2[u][i]);
     __syncthreads();
     for (int i = threadIdx.x; i < TK * CH; i += 256) {
         const int64_t m = m0 + i / CH, n = n0 + i % CH;
@@ -1006,25 +1073,28 @@ uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
 }
 
 // The kernel whose estimated time is least, in us.
-// Few rows: a fixed 3 and the memory's rate (4.4 TB/s here) or the integer tensor
+// Few rows: a fixed 3 and the memory's rate (5.9 TB/s here) or the integer tensor
 // rate (115 TOPS in whole groups of 8 tokens), or a warp's k-steps one after
-// another; twice that where K leaves rows off a 16-byte boundary.  Tiles: 7 (9 with
-// 128 tokens a tile) of launches, fill and last store, a CTA's steps of 128 of k at
-// 0.34 (0.38 with 128), the widening of many tokens and the copy of such rows of B.
-// Pairs: 8, the widening, and the waves of tiles x steps of 64 of k at 0.342.
-// Measured either side, few rows and tiles: N = K = 2048: M 32 7.0, 7.9; M 48 9.8,
-// 8.2.  N 16384, K 2048: M 16 12.3, 12.1; M 24 19.7, 12.1.  N = K = 8192: M 8 18.2,
-// 18.2; M 12 25.6, 18.3.  N 2048, K 8192: M 3 14.1, 10.4.  N 1023, K 3001: M 3 12.5,
-// 9.1.  Tiles and pairs: N = K = 8192: M 2048 179, 214; M 4096 352, 363; M 8192 690,
-// 669.  N 16384, K 2048: M 2048 92, 100; M 8192 356, 350.  N 1023, K 3001: M 4097
-// 35.5, 36.5.  One or two tokens have a kernel of their own.
+// another (0.45 each, longer with more tokens); 1.8 times that where K leaves rows
+// off a 16-byte boundary.  Tiles: 7 (9 with 128 tokens a tile) of launches, fill and
+// last store, a CTA's steps of 128 of k at 0.34 (0.38 with 128), the widening of
+// many tokens and the copy of such rows of B.  Pairs: 8, the widening, and the
+// waves of tiles x steps of 64 of k at 0.342.
+// Measured either side, few rows and tiles: N = K = 2048: M 32 5.3, 7.9; M 64 9.6,
+// 8.5.  N 16384, K 2048: M 16 11.9, 12.1; M 24 19.7, 12.1.  N = K = 8192: M 8 14.3,
+// 18.2; M 16 24.3, 18.4.  N 2048, K 8192: M 8 8.7, 10.5; M 16 14.5, 10.7.  N 1023, K
+// 3001: M 8 7.7, 9.0; M 16 10.2, 9.1.  Tiles and pairs: N = K = 8192: M 2048 179,
+// 214; M 4096 352, 363; M 8192 690, 669.  N 16384, K 2048: M 2048 92, 100; M 8192
+// 356, 350.  N 1023, K 3001: M 4097 35.5, 36.5.  One or two tokens have a kernel of
+// their own.
 int auto_config(int64_t M, int64_t N, int64_t K) {
     if (K == 0 || M <= 2) return CFG_ROWS;
     const double nk = double(N) * double(K), mk = double(M) * double(K), bt = stream_tokens(M);
     const double odd = K % 16 ? 1.0 : 0.0;
-    const double rate = std::max(nk / 4.4e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
-    const double serial = 1.5 + 0.8 * double(ceil_div(K, 512)) * std::max(1.0, 0.8 + double(M) / 32.0);
-    const double few = std::max(rate, serial) * (1.0 + odd);
+    const double rate = std::max(nk / 5.9e6, 2.0 * nk * double(ceil_div(M, 8) * 8) / 115e6) + 3.0;
+    const double slower = M <= 8 ? 1.0 : M <= 16 ? 1.8 : M <= 32 ? 2.1 : 4.2 * double(ceil_div(M, 64));
+    const double serial = 1.5 + 0.45 * double(ceil_div(K, 512)) * slower;
+    const double few = std::max(rate, serial) * (1.0 + 0.8 * odd);
     const double tiles = double(ceil_div(N, BM)) * std::ceil(double(M) / bt);
     const double parts = stream_parts(int64_t(std::min(tiles, 1e6)), ceil_div(K, kStreamK));
     const double steps = std::ceil(tiles * parts / 152.0) * std::ceil(double(ceil_div(K, kStreamK)) / parts);
