@@ -969,10 +969,12 @@ int repops_rope_f32(int64_t rows, int64_t heads, int64_t pairs, float *x, int64_
 /* q, scale <- the rows of x (stored as x_type, widened exactly), for every
  * group, each step one binary32 rounding:
  *   amax = max |x|,  a = max(amax, 2^-100),
- *   scale = fl(a / 127),  q = rint(fl(x * fl(127 / a))), ties to even.
- * A group that holds an infinity or a NaN gets scale NaN and q = 0.  A finite
- * value comes back within scale * (1/2 + 2^-14) (the floor 2^-100 keeps 127 / a
- * finite; a group of zeros stays zeros).  x, q, scale: device, row pitches ldx, ldq >= cols and
+ *   scale = min(fl(a / 127), S),  q = rint(fl(x * fl(127 / a))), ties to even,
+ * where S = 0x1.020406p+121 is the largest scale that 127 times is finite (only
+ * the largest binary32 value's fl(a / 127) is above it).  A group that holds an
+ * infinity or a NaN gets scale NaN and q = 0.  A finite value comes back finite,
+ * within scale * (1/2 + 2^-14) (the floor 2^-100 keeps 127 / a finite; a group
+ * of zeros stays zeros).  x, q, scale: device, row pitches ldx, ldq >= cols and
  * lds; outputs must not overlap x or each other (ALIAS).  INVALID_ARG for
  * negative sizes, cols above 2^30, unknown types or groups, null pointers
  * or short pitches. */

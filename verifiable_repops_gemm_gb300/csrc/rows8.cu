@@ -3,11 +3,15 @@
 //
 // Format, for every group of a row, each step one binary32 rounding:
 //   amax = max |x|,  a = max(amax, 2^-100),
-//   scale = fl(a / 127),  q = rint(fl(x * fl(127 / a))) (ties to even);
+//   scale = min(fl(a / 127), S),  q = rint(fl(x * fl(127 / a))) (ties to even);
 // |x| <= a, so fl(x * fl(127 / a)) <= 127 * (1 + 2^-23) and rint gives at most
-// 127: no clamp.  The floor keeps 127 / a finite: a group below it becomes
-// zeros, an error of at most 2^-100.  A group holding an infinity or a NaN gets
-// scale NaN and q = 0, so it comes back as NaN instead of as wrong numbers.
+// 127: no clamp.  The floor keeps 127 / a finite: a group below it is kept in
+// whole parts of the floor's scale, an error of at most half of one.  S is the
+// largest scale that 127 times is finite, and only the largest binary32 value
+// meets it: fl(a / 127) rounds up there, and it would come back as an infinity.
+// S is one unit of the last place less, which moves 127 of it by 2^-16 of a scale.
+// A group holding an infinity or a NaN gets scale NaN and q = 0, so it comes back
+// as NaN instead of as wrong numbers.
 // The maximum does not depend on the order it is taken in, so neither does any
 // bit here.
 //
@@ -27,6 +31,7 @@ namespace repops {
 namespace {
 
 constexpr float kScaleFloor = 0x1p-100f;
+constexpr float kScaleMost = 0x1.020406p+121f;
 
 template <int TY>
 __device__ __forceinline__ float load_one(const void *p, int64_t i) {
@@ -92,7 +97,7 @@ struct GroupScale {
 __device__ __forceinline__ GroupScale group_scale(float amax) {
     if (!(amax <= 3.402823466e38f)) return {__uint_as_float(0x7fffffffu), 0.0f, 0u};
     const float a = fmaxf(amax, kScaleFloor);
-    return {__fdiv_rn(a, 127.0f), __fdiv_rn(127.0f, a), 0xffffffffu};
+    return {fminf(__fdiv_rn(a, 127.0f), kScaleMost), __fdiv_rn(127.0f, a), 0xffffffffu};
 }
 
 // rint(fl(x * inv)) in the low byte: adding 1.5 * 2^23 rounds to a whole number
