@@ -974,10 +974,10 @@ int repops_rope_f32(int64_t rows, int64_t heads, int64_t pairs, float *x, int64_
  * the largest binary32 value's fl(a / 127) is above it).  A group that holds an
  * infinity or a NaN gets scale NaN and q = 0.  A finite value comes back finite,
  * within scale * (1/2 + 2^-14) (the floor 2^-100 keeps 127 / a finite; a group
- * of zeros stays zeros).  x, q, scale: device, row pitches ldx, ldq >= cols and
- * lds; outputs must not overlap x or each other (ALIAS).  INVALID_ARG for
- * negative sizes, cols above 2^30, unknown types or groups, null pointers
- * or short pitches. */
+ * of zeros stays zeros).  With group 0 a row without columns gets the floor's
+ * scale.  x, q, scale: device, row pitches ldx, ldq >= cols and lds; outputs must
+ * not overlap x or each other (ALIAS).  INVALID_ARG for negative sizes, cols
+ * above 2^30, unknown types or groups, null pointers or short pitches. */
 int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
                             int64_t group, int8_t *q, int64_t ldq, float *scale, int64_t lds,
                             cudaStream_t stream);

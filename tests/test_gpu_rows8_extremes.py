@@ -1,5 +1,5 @@
-"""Rows in 8 bits at the ends of their range: the largest binary32 value and
-groups whose largest magnitude is below the scale's floor."""
+"""Rows in 8 bits at the ends of their range: the largest binary32 value, groups
+whose largest magnitude is below the scale's floor, and rows without a column."""
 import numpy as np
 import pytest
 import torch
@@ -52,3 +52,13 @@ def test_groups_below_the_floor_are_whole_parts_of_it(rp, group):
     assert q[1, [0, 40]].tolist() == [1, 2]             # 127/128 and 127/64
     assert q[2:].abs().max() == 0                       # 127/256 < 1/2
     assert q.ne(0).sum() == 4
+
+
+def test_rows_without_columns_have_the_floor_as_their_scale(rp):
+    """group 0 keeps a scale a row, also of rows without a column: the maximum of
+    nothing is 0.  It reaches gemm_i8, whose empty sums it must not spoil."""
+    s = torch.full((5, 1), float("nan"), device=DEV)
+    q, got = rp.quantize_rows(torch.empty(5, 0, device=DEV), scale=s)
+    assert got is s and (s == np.float32(2.0 ** -100) / np.float32(127)).all()
+    w, ws = rp.quantize_rows(torch.empty(3, 0, device=DEV))
+    assert q.shape == (5, 0) and (rp.gemm_i8(q, w.t(), s.view(-1), ws.view(-1)) == 0).all()

@@ -416,8 +416,9 @@ extern "C" int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x
                                        cudaStream_t stream) {
     if (rows < 0 || cols < 0 || cols > (int64_t(1) << 30) || !known_storage(x_type) || !known_group(group))
         return REPOPS_ERR_INVALID_ARG;
-    if (rows == 0 || cols == 0) return REPOPS_OK;
-    if (!x || !q || !scale) return REPOPS_ERR_INVALID_ARG;
+    // a row without columns still has its scale where it has one for the row
+    if (rows == 0 || group_count(cols, group) == 0) return REPOPS_OK;
+    if ((cols > 0 && (!x || !q)) || !scale) return REPOPS_ERR_INVALID_ARG;
     uint64_t xb, qb, sb;
     if (!span_bytes(rows, cols, ldx, storage_size(x_type), &xb) || !span_bytes(rows, cols, ldq, 1, &qb) ||
         !span_bytes(rows, group_count(cols, group), lds, 4, &sb))
