@@ -1006,8 +1006,8 @@ int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_t *g, int64
  * ..._workspace_bytes(rows, cols) bytes on a 16-byte boundary (a shorter one is
  * INVALID_ARG), or NULL to take it from the scratch pool on `stream` (ALLOC
  * when refused); its contents before and after mean nothing.  dx may be res
- * itself (same pitch); any other overlap is ALIAS.  cols up to 393216
- * (UNSUPPORTED beyond). */
+ * itself (same pitch); any other overlap is ALIAS.  rows == 0 or cols == 0:
+ * no-op, dgamma is not written either.  cols up to 393216 (UNSUPPORTED beyond). */
 uint64_t repops_rmsnorm_backward_i8_workspace_bytes(int64_t rows, int64_t cols);
 int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int64_t ldx,
                                const float *x_scale, int64_t lds, int64_t group, const float *gamma,
@@ -1086,7 +1086,8 @@ int repops_rmsnorm_residual_f32(int64_t rows, int64_t cols, const float *x, int6
  * pitch lddgate (NULL exactly when gate is).  ws as
  * repops_rmsnorm_backward_i8, of ..._workspace_bytes(rows, cols, gate rows)
  * bytes (0 gate rows without a gate).  dx may be dy itself (same pitch); any
- * other overlap is ALIAS.  Limits as the forward's. */
+ * other overlap is ALIAS.  rows == 0 or cols == 0: no-op, the sums are not
+ * written either.  Limits as the forward's. */
 uint64_t repops_rmsnorm_residual_backward_workspace_bytes(int64_t rows, int64_t cols, int64_t gates);
 int repops_rmsnorm_residual_backward_f32(
     int64_t rows, int64_t cols, const float *dy, int64_t lddy, const float *dh, int64_t lddh,

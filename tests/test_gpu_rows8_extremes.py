@@ -1,5 +1,6 @@
 """Rows in 8 bits at the ends of their range: the largest binary32 value, groups
-whose largest magnitude is below the scale's floor, and rows without a column."""
+whose largest magnitude is below the scale's floor, rows without a column, and
+gradients of no rows on a stream of their own."""
 import numpy as np
 import pytest
 import torch
@@ -62,3 +63,29 @@ def test_rows_without_columns_have_the_floor_as_their_scale(rp):
     assert got is s and (s == np.float32(2.0 ** -100) / np.float32(127)).all()
     w, ws = rp.quantize_rows(torch.empty(3, 0, device=DEV))
     assert q.shape == (5, 0) and (rp.gemm_i8(q, w.t(), s.view(-1), ws.view(-1)) == 0).all()
+
+
+def test_gradients_of_no_rows_are_zeroed_on_the_stream_of_the_call(rp):
+    """Without rows a gain's gradient is +0 (an empty column sum), written where the
+    call runs: not behind work queued on the current stream."""
+    cols, side = 40, torch.cuda.Stream()
+    e = torch.empty(0, cols, device=DEV)
+    gain = torch.ones(cols, device=DEV)
+    for handle in (side, side.cuda_stream):
+        dg, dpre, dpost = (torch.full((cols,), 7.0, device=DEV) for _ in range(3))
+        dgate = torch.full((3, cols + 2), 7.0, device=DEV)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(400_000_000)                   # a fifth of a second on the current stream
+        rp.rmsnorm_backward_i8(e.to(torch.int8), torch.empty(0, 1, device=DEV), gain, 1e-5, e, group=0, dgamma=dg,
+                               stream=handle)
+        rp.rmsnorm_residual_backward(e, e, e, e, gain, post_gain=gain, gate=torch.ones(3, cols, device=DEV), dpre=dpre,
+                                     dpost=dpost, dgate=dgate[:, :cols], stream=handle)
+        with torch.cuda.stream(side):
+            got = torch.cat([dg, dpre, dpost, dgate.view(-1)]).cpu()
+        torch.cuda.synchronize()
+        assert (got[:3 * cols] == 0).all()
+        assert (got[3 * cols:].view(3, -1)[:, :cols] == 0).all() and (got[3 * cols:].view(3, -1)[:, cols:] == 7).all()
+    with pytest.raises(ValueError):                      # the arguments are looked at without rows too
+        rp.rmsnorm_backward_i8(e.to(torch.int8), torch.empty(0, 1, device=DEV), gain, 1e-5, e, group=0, dgamma=gain[1:])
+    with pytest.raises(ValueError):
+        rp.rmsnorm_residual_backward(e, e, e, e, gain, dpre=gain[1:])

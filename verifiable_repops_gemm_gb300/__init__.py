@@ -1157,6 +1157,15 @@ def swiglu_backward_i8(g, g_scale, u, u_scale, dh, dg=None, du=None, *, group: i
     return dg, du
 
 
+def _zero_gradients(handle, *tensors):
+    """+0 into each given gradient (None skipped) of a call without rows, on its
+    stream: the column sums of no rows."""
+    L = load()
+    for t in tensors:
+        for row in () if t is None else t.unsqueeze(0) if t.dim() == 1 else t:
+            _capi.check(L.repops_colsum_f32(0, row.numel(), None, row.numel(), row.data_ptr(), handle), "repops_colsum_f32")
+
+
 def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, group: int, res=None, h=None, stream=None):
     """(dx, dgamma) of RMSNorm rows whose input x is kept in 8 bits: the bits of
     rmsnorm_backward on the restored rows and of colsum(dy * xhat)
@@ -1171,15 +1180,15 @@ def rmsnorm_backward_i8(x, x_scale, gamma, eps, dy, dx=None, dgamma=None, *, gro
     dgamma = torch.empty(cols, dtype=torch.float32, device=x.device) if dgamma is None else dgamma
     ph, ldh = _row_like(h, x.shape, "h")
     handle = _stream_on_device(stream, x, x_scale, gamma, dy, res, dx, h, dgamma)
+    pg, pdg = _gain(gamma, cols, "gamma"), _gain(dgamma, cols, "dgamma")
     if rows == 0 or cols == 0:
-        return dx, dgamma.zero_()
+        _zero_gradients(handle, dgamma)
+        return dx, dgamma
     L = load()
     need = L.repops_rmsnorm_backward_i8_workspace_bytes(rows, cols)
     ws = _workspace(need, x.device, stream)
-    rc = L.repops_rmsnorm_backward_i8(rows, cols, px, ldx, pxs, lds, group, _gain(gamma, cols, "gamma"),
-                                      ctypes.c_float(eps), pd, ldd, pr, ldr, pdx, lddx, ph, ldh,
-                                      _gain(dgamma, cols, "dgamma"), ws.data_ptr() if ws is not None else None, need,
-                                      handle)
+    rc = L.repops_rmsnorm_backward_i8(rows, cols, px, ldx, pxs, lds, group, pg, ctypes.c_float(eps), pd, ldd, pr, ldr,
+                                      pdx, lddx, ph, ldh, pdg, ws.data_ptr() if ws is not None else None, need, handle)
     if rc:
         _capi.check(rc, "repops_rmsnorm_backward_i8")
     return dx, dgamma
@@ -1267,19 +1276,18 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
         raise ValueError("dgate must have the shape of gate")
     pdg, lddg, _, _ = _gate_rows(dgate, rows, cols)
     handle = _stream_on_device(stream, dy, dh, y, f, pre_gain, post_gain, gate, dx, df, dpre, dpost, dgate)
+    p_post, p_pre = _gain(post_gain, cols, "post_gain"), _gain(pre_gain, cols, "pre_gain")
+    p_dpre, p_dpost = _gain(dpre, cols, "dpre"), _gain(dpost, cols, "dpost")
     if rows == 0 or cols == 0:
-        for t in (dpre, dpost, dgate):
-            if t is not None:
-                t.zero_()
+        _zero_gradients(handle, dpre, dpost, dgate)
         return dx, df, dpre, dpost, dgate
     L = load()
     need = L.repops_rmsnorm_residual_backward_workspace_bytes(rows, cols, gates)
     ws = _workspace(need, f.device, stream)
     rc = L.repops_rmsnorm_residual_backward_f32(
-        rows, cols, pdy, lddy, pdh, lddh, py, ldy, pf, ldf, _gain(post_gain, cols, "post_gain"), pg, ldg, per,
-        ctypes.c_float(alpha), _gain(pre_gain, cols, "pre_gain"), ctypes.c_float(eps), pdx, lddx, pdf, lddf,
-        _gain(dpre, cols, "dpre"), _gain(dpost, cols, "dpost"), pdg, lddg, ws.data_ptr() if ws is not None else None,
-        need, handle)
+        rows, cols, pdy, lddy, pdh, lddh, py, ldy, pf, ldf, p_post, pg, ldg, per, ctypes.c_float(alpha), p_pre,
+        ctypes.c_float(eps), pdx, lddx, pdf, lddf, p_dpre, p_dpost, pdg, lddg,
+        ws.data_ptr() if ws is not None else None, need, handle)
     if rc:
         _capi.check(rc, "repops_rmsnorm_residual_backward_f32")
     return dx, df, dpre, dpost, dgate
