@@ -129,16 +129,18 @@ def gemm(A, B, out=None, *, config: int = -1, loader: int = LOADER_AUTO, stream=
 
 
 def _workspace(nbytes, device, stream):
-    """A byte buffer from torch's caching allocator for a call on `stream`,
-    kept from reuse until that stream's work is done; None when the stream is
-    a raw handle the allocator cannot track (the library's pool is used)."""
+    """A byte buffer from torch's caching allocator for a call on `stream`, out
+    of that stream's own memory: a freed block is handed on in the order of one
+    stream's work, so that no call on another can still be using it.  None when
+    the stream is a raw handle the allocator cannot track (the library's pool is
+    used)."""
     import torch
     if isinstance(stream, int):
         return None
-    ws = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        ws.record_stream(stream)
-    return ws
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(int(nbytes), dtype=torch.uint8, device=device)
 
 
 def gemm_chained(A, B, out=None, *, config: int = -1, workers: int = 0, stream=None):
