@@ -1037,7 +1037,10 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
  * with both widened in scratch.
  * ws: device scratch of repops_gemm_i8_workspace_bytes(config, M, N, K) bytes
  * (0 for config 0) on a 16-byte boundary, or NULL to take it from the scratch
- * pool on `stream` (ALLOC when refused).
+ * pool on `stream` (ALLOC when refused).  Config 1 reads B where it lies when B
+ * and ldb are multiples of 16 bytes; otherwise it copies it, into ws where that
+ * has repops_gemm_i8_operand_workspace_bytes(.., B, ldb) bytes (B is looked at for
+ * its alignment only), else into memory from the pool.
  * INVALID_ARG for negative sizes, unknown types or configs, null pointers,
  * short pitches or scratch; ALIAS when C or ws overlaps an operand or each
  * other; UNSUPPORTED for K above 131071 (acc would leave 32 bits), M or N above
@@ -1045,6 +1048,8 @@ int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8_t *x, int6
 int repops_gemm_i8_config_count(void);
 int repops_gemm_i8_auto_config(int64_t M, int64_t N, int64_t K);
 uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_t N, int64_t K);
+uint64_t repops_gemm_i8_operand_workspace_bytes(int config, int64_t M, int64_t N, int64_t K,
+                                                const int8_t *B, int64_t ldb);
 int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
                    const float *a_scale, const int8_t *B, int64_t ldb, const float *b_scale,
                    const float *bias, void *C, int typeC, int64_t ldc, void *ws, uint64_t ws_bytes,

@@ -1060,8 +1060,9 @@ def _scale_vector(t, n, name):
 
 
 @functools.lru_cache(maxsize=1024)
-def _gemm_i8_workspace(config, M, N, K):
-    return load().repops_gemm_i8_workspace_bytes(config, M, N, K)
+def _gemm_i8_workspace(config, M, N, K, off):
+    # `off`: how far B's rows are from 16-byte boundaries, all that is asked of B
+    return load().repops_gemm_i8_operand_workspace_bytes(config, M, N, K, off, off)
 
 
 def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, config: int = -1, stream=None):
@@ -1091,10 +1092,11 @@ def gemm_i8(A, B, a_scale, b_scale, out=None, *, out_dtype=None, bias=None, conf
     else:
         ldc = _pitch(out, "out")
     handle = _stream_on_device(stream, A, B, a_scale, b_scale, bias, out)
-    need = _gemm_i8_workspace(config, M, N, K)
+    pb, ldb = B.data_ptr(), max(ldb, K)
+    need = _gemm_i8_workspace(config, M, N, K, (pb | ldb) & 15)
     ws = _workspace(need, A.device, stream) if need else None
     rc = load().repops_gemm_i8(config, M, N, K, A.data_ptr(), max(lda, K), _scale_vector(a_scale, M, "a_scale"),
-                               B.data_ptr(), max(ldb, K), _scale_vector(b_scale, N, "b_scale"),
+                               pb, ldb, _scale_vector(b_scale, N, "b_scale"),
                                None if bias is None else _scale_vector(bias, N, "bias"), out.data_ptr(),
                                _storage_type(out.dtype), ldc, ws.data_ptr() if ws is not None else None, need, handle)
     if rc:

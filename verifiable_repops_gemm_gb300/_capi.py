@@ -47,6 +47,7 @@ SIGNATURES = {
     "repops_gemm_i8_config_count": (_i32, []),
     "repops_gemm_i8_auto_config": (_i32, [_i64, _i64, _i64]),
     "repops_gemm_i8_workspace_bytes": (_u64, [_i32, _i64, _i64, _i64]),
+    "repops_gemm_i8_operand_workspace_bytes": (_u64, [_i32, _i64, _i64, _i64, _vp, _i64]),
     "repops_gemm_i8": (_i32, [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _u64,
                               _vp]),
     "repops_rmsnorm_residual_f32": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f32, _vp, _f32,

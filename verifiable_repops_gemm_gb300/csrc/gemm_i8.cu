@@ -1066,11 +1066,12 @@ StreamMap stream_map(int64_t M, int64_t N, int64_t K) {
     return sm;
 }
 
-// Scratch: the tokens in binary16, then B at a 16-byte pitch where TMA cannot read it in place.
-uint64_t stream_copy_at(int64_t M, int64_t K) { return uint64_t(M) * uint64_t(stream_copies(M, K)) * uint64_t(stream_k(K)) * 2u; }
-uint64_t stream_workspace(int64_t M, int64_t N, int64_t K) {
-    return stream_copy_at(M, K) + uint64_t(N) * uint64_t(stream_k(K));
+// Scratch: the tokens in binary16; and a copy of B at a 16-byte pitch where TMA
+// cannot read it in place.
+uint64_t stream_workspace(int64_t M, int64_t K) {
+    return uint64_t(M) * uint64_t(stream_copies(M, K)) * uint64_t(stream_k(K)) * 2u;
 }
+uint64_t stream_copy_bytes(int64_t N, int64_t K) { return uint64_t(N) * uint64_t(stream_k(K)); }
 
 // The kernel whose estimated time is least, in us.
 // Few rows: a fixed 3 and the memory's rate (5.9 TB/s here) or the integer tensor
@@ -1106,7 +1107,19 @@ int auto_config(int64_t M, int64_t N, int64_t K) {
     return many <= pairs ? CFG_TILES : CFG_PAIR;
 }
 
+// The kernel that a call runs, CFG_ROWS where there is nothing to multiply or
+// the call is refused.
+int run_config(int config, int64_t M, int64_t N, int64_t K) {
+    if (config < CFG_AUTO || config >= CFG_COUNT || M <= 0 || N <= 0 || K <= 0 || K > kMaxK ||
+        M > (int64_t(1) << 40) || N > (int64_t(1) << 40))
+        return CFG_ROWS;
+    return config == CFG_AUTO ? auto_config(M, N, K) : config;
+}
+
 bool operand_vec(const int8_t *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0; }
+
+// TMA reads B where it lies.
+bool read_in_place(const int8_t *B, int64_t ldb) { return operand_vec(B, ldb) && ldb < (int64_t(1) << 39); }
 
 template <int TY, int R, int NT>
 int launch_dot(const I8Args &a, cudaStream_t s) {
@@ -1170,14 +1183,12 @@ bool make_token_map(CUtensorMap *map, const __half *base, int64_t M, int64_t Kp,
 }
 
 template <int TY, int BT>
-int launch_stream(const I8Args &a, uint8_t *ws, cudaStream_t s) {
+int launch_stream(const I8Args &a, __half *tokens, int8_t *copy, cudaStream_t s) {
     using T = StreamCfg<BT>;
     const int64_t Kp = stream_k(a.K);
     const StreamMap sm = stream_map(a.M, a.N, a.K);
-    __half *tokens = reinterpret_cast<__half *>(ws);
-    int8_t *copy = reinterpret_cast<int8_t *>(ws + stream_copy_at(a.M, a.K));
     // bytes that a 16-byte unit brings along behind K meet the tokens' zeros there
-    const bool in_place = operand_vec(a.B, a.ldb) && a.ldb < (int64_t(1) << 39), vec = operand_vec(a.A, a.lda);
+    const bool in_place = read_in_place(a.B, a.ldb), vec = operand_vec(a.A, a.lda);
     CUtensorMap mt, mw;
     if (!make_token_map(&mt, tokens, a.M * sm.copies, Kp, BT) ||
         !(in_place ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.B, a.K, a.N, a.ldb, kStreamK, BM)
@@ -1243,13 +1254,11 @@ int launch_pair(const I8Args &a, __half *ws, cudaStream_t s) {
 }
 
 template <int TY>
-int run_i8(int cfg, const I8Args &a, void *ws, cudaStream_t s) {
+int run_i8(int cfg, const I8Args &a, __half *ws, int8_t *copy, cudaStream_t s) {
     switch (cfg) {
         case CFG_ROWS: return launch_rows<TY>(a, s);
-        case CFG_PAIR: return launch_pair<TY>(a, static_cast<__half *>(ws), s);
-        default:
-            return stream_tokens(a.M) == 64 ? launch_stream<TY, 64>(a, static_cast<uint8_t *>(ws), s)
-                                            : launch_stream<TY, 128>(a, static_cast<uint8_t *>(ws), s);
+        case CFG_PAIR: return launch_pair<TY>(a, ws, s);
+        default: return stream_tokens(a.M) == 64 ? launch_stream<TY, 64>(a, ws, copy, s) : launch_stream<TY, 128>(a, ws, copy, s);
     }
 }
 
@@ -1265,11 +1274,14 @@ extern "C" int repops_gemm_i8_auto_config(int64_t M, int64_t N, int64_t K) {
 }
 
 extern "C" uint64_t repops_gemm_i8_workspace_bytes(int config, int64_t M, int64_t N, int64_t K) {
-    if (config < CFG_AUTO || config >= CFG_COUNT || M <= 0 || N <= 0 || K <= 0 || K > kMaxK ||
-        M > (int64_t(1) << 40) || N > (int64_t(1) << 40))
-        return 0;
-    if (config == CFG_AUTO) config = auto_config(M, N, K);
-    return config == CFG_ROWS ? 0 : config == CFG_PAIR ? pair_workspace(M, N, K) : stream_workspace(M, N, K);
+    config = run_config(config, M, N, K);
+    return config == CFG_ROWS ? 0 : config == CFG_PAIR ? pair_workspace(M, N, K) : stream_workspace(M, K);
+}
+
+extern "C" uint64_t repops_gemm_i8_operand_workspace_bytes(int config, int64_t M, int64_t N, int64_t K, const int8_t *B,
+                                                           int64_t ldb) {
+    return repops_gemm_i8_workspace_bytes(config, M, N, K) +
+           (run_config(config, M, N, K) == CFG_TILES && !read_in_place(B, ldb) ? stream_copy_bytes(N, K) : 0u);
 }
 
 extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
@@ -1294,27 +1306,30 @@ extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const
     // the grids' limits: tile indices are 32-bit, and a grid's y is at most 65535
     if (ceil_div(M, BM) * ceil_div(N, 16) > INT32_MAX / 2 || (config == CFG_ROWS && ceil_div(M, 64) > 65535))
         return REPOPS_ERR_UNSUPPORTED;
+    // scratch: `need` bytes from the caller or the pool, a copy of B (where one is
+    // made) behind them where the caller's are that long, else from the pool
     const uint64_t need = repops_gemm_i8_workspace_bytes(config, M, N, K);
-    void *own = nullptr;
-    if (need > 0) {
-        if (ws) {
-            if (ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return REPOPS_ERR_INVALID_ARG;
-            if (ranges_overlap(ws, need, A, ab) || ranges_overlap(ws, need, B, bb) || ranges_overlap(ws, need, C, cb) ||
-                ranges_overlap(ws, need, a_scale, sab) || ranges_overlap(ws, need, b_scale, sbb) ||
-                (bias && ranges_overlap(ws, need, bias, sbb)))
-                return REPOPS_ERR_ALIAS;
-        } else {
-            if (scratch_malloc(&own, size_t(need), stream) != cudaSuccess) {
-                cudaGetLastError();
-                return REPOPS_ERR_ALLOC;
-            }
-            ws = own;
-        }
+    const uint64_t all = repops_gemm_i8_operand_workspace_bytes(config, M, N, K, B, ldb);
+    if (ws && need > 0) {
+        if (ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % 16 != 0) return REPOPS_ERR_INVALID_ARG;
+        const uint64_t used = ws_bytes >= all ? all : need;
+        if (ranges_overlap(ws, used, A, ab) || ranges_overlap(ws, used, B, bb) || ranges_overlap(ws, used, C, cb) ||
+            ranges_overlap(ws, used, a_scale, sab) || ranges_overlap(ws, used, b_scale, sbb) ||
+            (bias && ranges_overlap(ws, used, bias, sbb)))
+            return REPOPS_ERR_ALIAS;
     }
+    const uint64_t pool = !ws ? all : ws_bytes >= all ? 0 : all - need;
+    void *own = nullptr;
+    if (pool > 0 && scratch_malloc(&own, size_t(pool), stream) != cudaSuccess) {
+        cudaGetLastError();
+        return REPOPS_ERR_ALLOC;
+    }
+    __half *wide = static_cast<__half *>(ws ? ws : own);
+    int8_t *copy = ws && own ? static_cast<int8_t *>(own) : reinterpret_cast<int8_t *>(wide + need / 2);
     const I8Args a{M, N, K, A, B, lda, ldb, a_scale, b_scale, bias, C, ldc, A + ab, B + bb};
-    int rc = typeC == REPOPS_TYPE_F32   ? run_i8<REPOPS_TYPE_F32>(config, a, ws, stream)
-             : typeC == REPOPS_TYPE_F16 ? run_i8<REPOPS_TYPE_F16>(config, a, ws, stream)
-                                        : run_i8<REPOPS_TYPE_BF16>(config, a, ws, stream);
+    int rc = typeC == REPOPS_TYPE_F32   ? run_i8<REPOPS_TYPE_F32>(config, a, wide, copy, stream)
+             : typeC == REPOPS_TYPE_F16 ? run_i8<REPOPS_TYPE_F16>(config, a, wide, copy, stream)
+                                        : run_i8<REPOPS_TYPE_BF16>(config, a, wide, copy, stream);
     if (own) {
         const cudaError_t e = cudaFreeAsync(own, stream);
         if (rc == REPOPS_OK && e != cudaSuccess) rc = set_cuda_error(e);
