@@ -1,5 +1,6 @@
-"""The 8-bit product with scratch of exactly the size asked for, whatever the
-weights' alignment."""
+"""The 8-bit product at the limits of its arguments: scratch of exactly the size
+asked for, whatever the weights' alignment, and more tokens than a grid's y
+dimension has tiles."""
 import pytest
 import torch
 
@@ -54,3 +55,24 @@ def test_the_bindings_scratch_does_not_hold_aligned_weights(rp):
     before = torch.cuda.memory_allocated()
     rp.gemm_i8(a, b.t(), sa, sb, out=out)
     assert torch.cuda.max_memory_allocated() - before < 4 << 20
+
+
+@pytest.mark.parametrize("config", [-1, 0, 1, 2])
+def test_empty_sums_of_many_tokens(rp, config):
+    M = 65535 * 64 + 77
+    a, b = torch.empty(M, 0, dtype=torch.int8, device=DEV), torch.empty(2, 0, dtype=torch.int8, device=DEV)
+    bias = torch.tensor([3.0, -4.0], device=DEV)
+    y = rp.gemm_i8(a, b.t(), torch.ones(M, device=DEV), torch.ones(2, device=DEV), bias=bias, config=config)
+    assert torch.equal(y, bias.expand(M, 2))
+
+
+@pytest.mark.parametrize("K", [16, 21])
+def test_few_row_kernel_with_many_tokens(rp, K):
+    M, N = 65535 * 64 + 77, 2
+    a, b = ints((M, K), 5), ints((N, K), 6)
+    sa = torch.rand(M, device=DEV) + 0.5
+    sb = torch.rand(N, device=DEV) + 0.5
+    y = rp.gemm_i8(a, b.t(), sa, sb, config=0)
+    want = (a.double() @ b.double().t()).float() * sa[:, None] * sb
+    assert torch.equal(y, want)
+    assert torch.equal(rp.gemm_i8(a, b.t(), sa, sb), want)

@@ -1134,12 +1134,22 @@ int launch_dot_r(const I8Args &a, cudaStream_t s) {
     return a.M == 1 ? launch_dot<TY, R, 1>(a, s) : launch_dot<TY, R, 2>(a, s);
 }
 
+// As many launches as a grid's 65535 token tiles make of M.
 template <int TY, int NT>
-int launch_rows_nt(const I8Args &a, cudaStream_t s) {
-    const dim3 grid(unsigned(ceil_div(a.N, 16)), unsigned(ceil_div(a.M, 8 * NT)));
-    if (operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb)) gemm_i8_rows_kernel<TY, NT, true><<<grid, 256, 0, s>>>(a);
-    else gemm_i8_rows_kernel<TY, NT, false><<<grid, 256, 0, s>>>(a);
-    return check_launch();
+int launch_rows_nt(I8Args a, cudaStream_t s) {
+    constexpr int64_t most = int64_t(65535) * 8 * NT;
+    const bool vec = operand_vec(a.A, a.lda) && operand_vec(a.B, a.ldb);
+    for (int64_t left = a.M;; left -= most) {
+        a.M = std::min(left, most);
+        const dim3 grid(unsigned(ceil_div(a.N, 16)), unsigned(ceil_div(a.M, 8 * NT)));
+        if (vec) gemm_i8_rows_kernel<TY, NT, true><<<grid, 256, 0, s>>>(a);
+        else gemm_i8_rows_kernel<TY, NT, false><<<grid, 256, 0, s>>>(a);
+        const int rc = check_launch();
+        if (rc != REPOPS_OK || left <= most) return rc;
+        if (a.A) a.A += most * a.lda;                          // null without k
+        a.sa += most;
+        a.C = static_cast<uint8_t *>(a.C) + most * a.ldc * int64_t(storage_size(TY));
+    }
 }
 
 template <int TY>
@@ -1303,9 +1313,7 @@ extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const
         return REPOPS_ERR_ALIAS;
     if (config == CFG_AUTO) config = auto_config(M, N, K);
     if (K == 0) config = CFG_ROWS;
-    // the grids' limits: tile indices are 32-bit, and a grid's y is at most 65535
-    if (ceil_div(M, BM) * ceil_div(N, 16) > INT32_MAX / 2 || (config == CFG_ROWS && ceil_div(M, 64) > 65535))
-        return REPOPS_ERR_UNSUPPORTED;
+    if (ceil_div(M, BM) * ceil_div(N, 16) > INT32_MAX / 2) return REPOPS_ERR_UNSUPPORTED;     // tile indices are 32-bit
     // scratch: `need` bytes from the caller or the pool, a copy of B (where one is
     // made) behind them where the caller's are that long, else from the pool
     const uint64_t need = repops_gemm_i8_workspace_bytes(config, M, N, K);
