@@ -1,0 +1,61 @@
+"""The decoder's buffers: no layer's scratch holds what nothing reads."""
+import pytest
+import torch
+
+from verifiable_repops_gemm_gb300 import decoder, inputs
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+KINDS = {"llama": dict(mlp="swiglu"), "gelu": dict(mlp="gelu"),
+         "sandwich": dict(mlp="swiglu", post_norm=True, gated=True, residual_scale=0.5),
+         "sandwich_gelu": dict(mlp="gelu", post_norm=True, gated=True, residual_scale=0.5),
+         "gated": dict(mlp="swiglu", gated=True), "scaled": dict(mlp="gelu", residual_scale=0.25)}
+
+
+def config(kind):
+    return decoder.DecoderConfig(d=128, heads=4, kv_heads=2, ffn=192, seq_len=24, **KINDS[kind])
+
+
+def layer(kind, seqs=2):
+    cfg = config(kind)
+    w = decoder.init_weights(cfg, 7, DEV)
+    return cfg, w, inputs.normal((seqs * cfg.seq_len, cfg.d), 1.0, 8, DEV)
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.int32), b.contiguous().view(torch.int32))
+
+
+def tensors(d):
+    return [t for t in d.values() if torch.is_tensor(t)]
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_scratch_holds_nothing_that_is_not_read(rp, kind):
+    cfg, w, x = layer(kind)
+    T = x.shape[0]
+    ws = decoder.workspace(cfg, T, DEV)
+    assert "pre" not in ws
+    # the buffers that a backward pass from 8-bit checkpoints does not need share
+    # those that it does
+    b32, b8 = decoder.backward_workspace(cfg, T, DEV), decoder.backward_workspace(cfg, T, DEV, bits=8)
+    stores = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in tensors(b8)}
+    needs = {"t_ffn": cfg.ffn, "t_d": cfg.d, "dqkv": cfg.qkv_width, "h": cfg.d, "a": cfg.ffn, "qkv": cfg.qkv_width,
+             "attn": cfg.d, ("gu" if cfg.mlp == "swiglu" else "pre"): cfg.ffn * (2 if cfg.mlp == "swiglu" else 1)}
+    if cfg.sandwich:
+        needs.update(t_e=cfg.d, t_f=cfg.d)
+    scores = 2 * (T // cfg.seq_len) * cfg.heads * cfg.seq_len ** 2
+    assert sum(stores.values()) == 4 * (T * sum(needs.values()) + scores)
+    # every 8-bit pass runs in them, and a binary32 one in scratch made for 8 bits
+    save8 = decoder.activations(cfg, T, DEV, bits=8)
+    y = decoder.forward(x.clone(), w, cfg, work=ws, save=save8)
+    assert same(y, decoder.forward(x.clone(), w, cfg))
+    save = decoder.activations(cfg, T, DEV)
+    dy = inputs.normal(x.shape, 1.0, 9, DEV)
+    got = []
+    for work in (b32, b8):
+        decoder.forward(x.clone(), w, cfg, work=ws, save=save)
+        dx, g = decoder.backward(dy.clone(), w, cfg, save, work=work)
+        got.append((dx.clone(), {k: v.clone() for k, v in g.items()}))
+    assert same(got[0][0], got[1][0]) and all(same(got[0][1][k], got[1][1][k]) for k in got[0][1])

@@ -335,16 +335,20 @@ def _edge(x, f, w, cfg: DecoderConfig, k: int, h=None):
 
 def _mlp(h, w, cfg: DecoderConfig, ws, save, out):
     """The MLP of h (without the residual) into `out`, its activations where
-    `save` keeps them."""
+    `save` keeps them (in 8 bits only GeLU's input, which GeLU then replaces)."""
     f = cfg.ffn
-    a = save["a"] if save is not None else ws["a"]
+    kept8 = save is not None and save.get("bits") == 8
+    keep = ws if save is None or kept8 else save
+    a = keep["a"]
     if cfg.mlp == "swiglu":
-        gu = save["gu"] if save is not None else ws["gu"]
+        gu = keep["gu"]
         gemm(h, w["w_gu"], out=gu)
         swiglu(gu[:, :f], gu[:, f:], out=a)
         return gemm(a, w["w_down"], out=out)
-    pre = save["pre"] if save is not None else a
+    pre = a if keep is ws else save["pre"]
     gemm_batched(h, w["w_up"], out=pre, bias=w["b_up"])
+    if kept8:
+        _keep(save, "pre", pre)
     gelu(pre, out=a)
     return gemm_batched(a, w["w_down"], out=out, bias=w["b_down"])
 
@@ -380,7 +384,7 @@ def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused_attention):
         rmsnorm_rows(x, w["g2"], cfg.eps, out=h)
     _keep(save, "x1", x)
     if cfg.sandwich:
-        f2 = _mlp(h, w, cfg, ws, None if cfg.mlp == "swiglu" else {"a": ws["a"], "pre": ws["pre"]}, tmp)
+        f2 = _mlp(h, w, cfg, ws, save, tmp)
         _keep(save, "f2", f2)
         _edge(x, f2, w, cfg, 2)
     elif cfg.mlp == "swiglu":
@@ -388,14 +392,13 @@ def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused_attention):
         swiglu(ws["gu"][:, :cfg.ffn], ws["gu"][:, cfg.ffn:], out=ws["a"])
         gemm_batched(ws["a"], w["w_down"], out=x, residual=x)
     else:
-        gemm_batched(h, w["w_up"], out=ws["pre"], bias=w["b_up"])
-        gelu(ws["pre"], out=ws["a"])
+        gemm_batched(h, w["w_up"], out=ws["a"], bias=w["b_up"])
+        _keep(save, "pre", ws["a"])
+        gelu(ws["a"], out=ws["a"])
         gemm_batched(ws["a"], w["w_down"], out=x, bias=w["b_down"], residual=x)
     if cfg.mlp == "swiglu":
         _keep(save, "g", ws["gu"][:, :cfg.ffn])
         _keep(save, "u", ws["gu"][:, cfg.ffn:])
-    else:
-        _keep(save, "pre", ws["pre"])
     return x
 
 
@@ -700,14 +703,16 @@ def backward_workspace(cfg: DecoderConfig, tokens: int, device, bits: int = 32) 
     e = dict(dtype=torch.float32, device=device)
     group, S = cfg.heads // cfg.kv_heads, cfg.seq_len
     seqs = tokens // S
-    out = {"t_ffn": torch.empty(tokens, cfg.ffn, **e), "t_d": torch.empty(tokens, cfg.d, **e),
-           "t_d2": torch.empty(tokens, cfg.d, **e), "dqkv": torch.empty(tokens, cfg.qkv_width, **e),
+    t_d2 = torch.empty(tokens, cfg.d, **e)
+    out = {"t_ffn": torch.empty(tokens, cfg.ffn, **e), "t_d": torch.empty(tokens, cfg.d, **e), "t_d2": t_d2,
+           "dqkv": torch.empty(tokens, cfg.qkv_width, **e),
            "dp": torch.empty(seqs * cfg.kv_heads, group, S, S, **e), "rope": rope_tables(cfg, device),
            "streams": side_streams(cfg, tokens, device)}
     if cfg.sandwich:
         out["t_e"] = torch.empty(tokens, cfg.d, **e)
     if bits == 8:
-        out.update(h=torch.empty(tokens, cfg.d, **e), a=torch.empty(tokens, cfg.ffn, **e),
+        # h in t_d2's memory, which only the binary32 norms' backward uses
+        out.update(h=t_d2, a=torch.empty(tokens, cfg.ffn, **e),
                    qkv=torch.empty(tokens, cfg.qkv_width, **e), attn=torch.empty(tokens, cfg.d, **e),
                    probs=torch.empty(seqs * cfg.kv_heads, group, S, S, **e))
         if cfg.mlp == "swiglu":
@@ -730,6 +735,4 @@ def workspace(cfg: DecoderConfig, tokens: int, device) -> dict:
            "streams": side_streams(cfg, tokens, device)}
     if cfg.mlp == "swiglu":
         out["gu"] = torch.empty(tokens, 2 * cfg.ffn, **e)
-    else:
-        out["pre"] = torch.empty(tokens, cfg.ffn, **e)
     return out
