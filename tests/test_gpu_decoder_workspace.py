@@ -1,4 +1,5 @@
-"""The decoder's buffers: no layer's scratch holds what nothing reads."""
+"""The decoder's buffers: no layer's scratch holds what nothing reads, and a
+backward pass refuses scratch made for the other kind of checkpoint."""
 import pytest
 import torch
 
@@ -59,3 +60,15 @@ def test_scratch_holds_nothing_that_is_not_read(rp, kind):
         dx, g = decoder.backward(dy.clone(), w, cfg, save, work=work)
         got.append((dx.clone(), {k: v.clone() for k, v in g.items()}))
     assert same(got[0][0], got[1][0]) and all(same(got[0][1][k], got[1][1][k]) for k in got[0][1])
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_backward_refuses_scratch_without_the_buffers_of_8_bits(rp, kind):
+    cfg, w, x = layer(kind)
+    save = decoder.activations(cfg, x.shape[0], DEV, bits=8)
+    decoder.forward(x.clone(), w, cfg, save=save)
+    dy = inputs.normal(x.shape, 1.0, 9, DEV)
+    keep = dy.clone()
+    with pytest.raises(ValueError, match="bits=8"):
+        decoder.backward(dy, w, cfg, save, work=decoder.backward_workspace(cfg, x.shape[0], DEV))
+    assert same(dy, keep)                                 # nothing was done to it

@@ -518,6 +518,8 @@ def backward(dy, w: dict, cfg: DecoderConfig, saved: dict, *, work: dict = None,
     T, f = dy.shape[0], cfg.ffn
     kept8 = saved.get("bits") == 8
     ws = work if work is not None else backward_workspace(cfg, T, dy.device, bits=8 if kept8 else 32)
+    if kept8 and "h" not in ws:
+        raise ValueError("a backward pass from 8-bit checkpoints needs scratch of backward_workspace(bits=8)")
     g = {}
     o = grads if grads is not None else {}
     dm = dy                                  # the MLP's gradient
