@@ -1,5 +1,6 @@
-"""The decoder's buffers: no layer's scratch holds what nothing reads, and a
-backward pass refuses scratch made for the other kind of checkpoint."""
+"""The decoder's buffers and switches: no layer's scratch holds what nothing
+reads, a backward pass refuses scratch made for the other kind of checkpoint,
+and the switches of forward reach sandwich and checkpointed layers."""
 import pytest
 import torch
 
@@ -72,3 +73,48 @@ def test_backward_refuses_scratch_without_the_buffers_of_8_bits(rp, kind):
     with pytest.raises(ValueError, match="bits=8"):
         decoder.backward(dy, w, cfg, save, work=decoder.backward_workspace(cfg, x.shape[0], DEV))
     assert same(dy, keep)                                 # nothing was done to it
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("bits", [0, 32, 8])
+def test_separate_steps_give_the_same_bits(rp, monkeypatch, kind, bits):
+    """fused=False: the residual sums (and in a sandwich layer the edges' norm, gate
+    and scale) as steps of their own."""
+    cfg, w, x = layer(kind)
+
+    def run(fused):
+        save = decoder.activations(cfg, x.shape[0], DEV, bits=bits) if bits else None
+        y = decoder.forward(x.clone(), w, cfg, save=save, fused=fused)
+        kept = []
+        for name, v in sorted(save.items()) if save else []:
+            if name == "probs":                           # defined below the diagonal only
+                continue
+            kept += [t for t in (v if isinstance(v, tuple) else (v,)) if torch.is_tensor(t)]
+        return y, kept
+
+    want, kept = run(True)
+    if cfg.sandwich:
+        def no_edge(*a, **k):
+            raise AssertionError("the fused edge ran")
+        monkeypatch.setattr(decoder, "rmsnorm_residual", no_edge)
+    else:
+        real = decoder.gemm_batched
+
+        def no_residual(*a, **k):
+            assert cfg.mlp == "gelu" and bits or k.get("residual") is None, "a fused residual sum ran"
+            return real(*a, **k)
+        monkeypatch.setattr(decoder, "gemm_batched", no_residual)
+    got, kept2 = run(False)
+    assert same(got, want) and len(kept) == len(kept2)
+    for a, b in zip(kept, kept2):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_gelu_in_the_products_epilogue_in_a_sandwich_layer(rp, monkeypatch):
+    cfg, w, x = layer("sandwich_gelu")
+    want = decoder.forward(x.clone(), w, cfg)
+
+    def no_gelu(*a, **k):
+        raise AssertionError("gelu ran as a kernel of its own")
+    monkeypatch.setattr(decoder, "gelu", no_gelu)
+    assert same(decoder.forward(x.clone(), w, cfg, gelu_epilogue=True), want)

@@ -259,16 +259,19 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
             work: dict = None, save: dict = None, fused_attention: bool = False):
     """Runs the layer on x (T x d, T a multiple of seq_len) in place and
     returns it.  `work`: reusable buffers from `workspace` (allocated when
-    absent).  `save`: a dict (from `activations`) that receives what
-    `backward` needs; a GeLU layer then keeps its GeLU input and runs GeLU as
-    its own kernel."""
+    absent).  `fused`: biases and residual sums in the products' epilogues, a
+    sandwich layer's edges in one call; without it they are steps of their own.
+    `gelu_epilogue`: GeLU in the product's epilogue too.  `save`: a dict (from
+    `activations`) that receives what `backward` needs; a GeLU layer's MLP then
+    keeps its GeLU input and runs GeLU as its own kernel, whatever these two
+    say.  The bits are the same each way."""
     T = x.shape[0]
     if T % cfg.seq_len:
         raise ValueError("tokens must be a whole number of sequences")
     ws = work if work is not None else workspace(cfg, T, x.device)
     f = cfg.ffn
     if save is not None and save.get("bits") == 8:
-        return _forward_checkpointed(x, w, cfg, ws, save, fused_attention)
+        return _forward_checkpointed(x, w, cfg, ws, save, fused, fused_attention)
     if save is not None:
         save["x0"].copy_(x)
         h, qkv, attn, a = save["h1"], save["qkv"], save["attn"], save["a"]
@@ -282,11 +285,12 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
     if cfg.sandwich:
         f1 = gemm(attn, w["w_o"], out=save["f1"] if save is not None else ws["tmp_d"])
         h = save["h2"] if save is not None else h
-        _edge(x, f1, w, cfg, 1, h)
+        steps = None if fused else ws["tmp_d"]
+        _edge(x, f1, w, cfg, 1, h, steps)
         if save is not None:
             save["x1"].copy_(x)
-        f2 = _mlp(h, w, cfg, ws, save, save["f2"] if save is not None else ws["tmp_d"])
-        _edge(x, f2, w, cfg, 2)
+        f2 = _mlp(h, w, cfg, ws, save, save["f2"] if save is not None else ws["tmp_d"], fused, gelu_epilogue)
+        _edge(x, f2, w, cfg, 2, steps=steps)
         return x
     if fused:
         gemm_batched(attn, w["w_o"], out=x, residual=x)
@@ -326,14 +330,23 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
     return x
 
 
-def _edge(x, f, w, cfg: DecoderConfig, k: int, h=None):
+def _edge(x, f, w, cfg: DecoderConfig, k: int, h=None, steps=None):
     """The edge after block k (1 attention, 2 MLP) in place on x; with h, the
-    norm before the MLP into it."""
-    rmsnorm_residual(x, f, w["g2"] if h is not None else None, cfg.eps, post_gain=w.get("p%d" % k),
-                     gate=w.get("a%d" % k), alpha=cfg.residual_scale, y=x, h=h)
+    norm before the MLP into it.  steps: scratch like x (f's own memory is fine)
+    to take the edge in as operators of their own."""
+    post, gate = w.get("p%d" % k), w.get("a%d" % k)
+    if steps is None:
+        rmsnorm_residual(x, f, w["g2"] if h is not None else None, cfg.eps, post_gain=post, gate=gate,
+                         alpha=cfg.residual_scale, y=x, h=h)
+        return
+    t = f if post is None else rmsnorm_rows(f, post, cfg.eps, out=steps)
+    t = t if gate is None else torch.mul(t, gate, out=steps)
+    x += torch.mul(t, cfg.residual_scale, out=steps)
+    if h is not None:
+        rmsnorm_rows(x, w["g2"], cfg.eps, out=h)
 
 
-def _mlp(h, w, cfg: DecoderConfig, ws, save, out):
+def _mlp(h, w, cfg: DecoderConfig, ws, save, out, fused: bool = True, gelu_epilogue: bool = False):
     """The MLP of h (without the residual) into `out`, its activations where
     `save` keeps them (in 8 bits only GeLU's input, which GeLU then replaces)."""
     f = cfg.ffn
@@ -345,6 +358,15 @@ def _mlp(h, w, cfg: DecoderConfig, ws, save, out):
         gemm(h, w["w_gu"], out=gu)
         swiglu(gu[:, :f], gu[:, f:], out=a)
         return gemm(a, w["w_down"], out=out)
+    if save is None and not fused:
+        gemm(h, w["w_up"], out=a)
+        a += w["b_up"]
+        y = gemm(gelu(a, out=a), w["w_down"], out=out)
+        y += w["b_down"]
+        return y
+    if save is None and gelu_epilogue:
+        gemm_batched(h, w["w_up"], out=a, bias=w["b_up"], act=ACT_GELU)
+        return gemm_batched(a, w["w_down"], out=out, bias=w["b_down"])
     pre = a if keep is ws else save["pre"]
     gemm_batched(h, w["w_up"], out=pre, bias=w["b_up"])
     if kept8:
@@ -364,7 +386,7 @@ def _restore(save, name, out):
     return dequantize_rows(q, s, group=CHECKPOINT_GROUP, out=out)
 
 
-def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused_attention):
+def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused, fused_attention):
     """forward(save=...) for activations(bits=8): the same x, the activations
     quantised as they are made."""
     h, qkv, attn, tmp = ws["h"], ws["qkv"], ws["attn"], ws["tmp_d"]
@@ -378,19 +400,25 @@ def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused_attention):
     if cfg.sandwich:
         f1 = gemm(attn, w["w_o"], out=tmp)
         _keep(save, "f1", f1)
-        _edge(x, f1, w, cfg, 1, h)
+        _edge(x, f1, w, cfg, 1, h, None if fused else tmp)
     else:
-        gemm_batched(attn, w["w_o"], out=x, residual=x)
+        if fused:
+            gemm_batched(attn, w["w_o"], out=x, residual=x)
+        else:
+            x += gemm(attn, w["w_o"], out=tmp)
         rmsnorm_rows(x, w["g2"], cfg.eps, out=h)
     _keep(save, "x1", x)
     if cfg.sandwich:
         f2 = _mlp(h, w, cfg, ws, save, tmp)
         _keep(save, "f2", f2)
-        _edge(x, f2, w, cfg, 2)
+        _edge(x, f2, w, cfg, 2, steps=None if fused else tmp)
     elif cfg.mlp == "swiglu":
         gemm(h, w["w_gu"], out=ws["gu"])
         swiglu(ws["gu"][:, :cfg.ffn], ws["gu"][:, cfg.ffn:], out=ws["a"])
-        gemm_batched(ws["a"], w["w_down"], out=x, residual=x)
+        if fused:
+            gemm_batched(ws["a"], w["w_down"], out=x, residual=x)
+        else:
+            x += gemm(ws["a"], w["w_down"], out=tmp)
     else:
         gemm_batched(h, w["w_up"], out=ws["a"], bias=w["b_up"])
         _keep(save, "pre", ws["a"])
