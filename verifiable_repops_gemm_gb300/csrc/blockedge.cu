@@ -60,13 +60,13 @@ __device__ __forceinline__ int slab_col(int slab, int k, int t) {
 // past the row's end reads column 0 instead, and its result is never stored or
 // folded.  n is a multiple of 4 with VEC.
 template <bool VEC>
-__device__ __forceinline__ float4 row_load(const float *__restrict__ row, int slab, int k, int n) {
+__device__ __forceinline__ float4 row_load(const DbgAccess &d, const float *__restrict__ row, int slab, int k, int n) {
     const int c = slab_col<VEC>(slab, k, 0);
     if constexpr (VEC) {
-        return __ldg(reinterpret_cast<const float4 *>(row + (c < n ? c : 0)));
+        return load_const(d, reinterpret_cast<const float4 *>(row + (c < n ? c : 0)));
     } else {
-        return make_float4(__ldg(row + (c < n ? c : 0)), __ldg(row + (c + 32 < n ? c + 32 : 0)),
-                           __ldg(row + (c + 64 < n ? c + 64 : 0)), __ldg(row + (c + 96 < n ? c + 96 : 0)));
+        return make_float4(load_const(d, row + (c < n ? c : 0)), load_const(d, row + (c + 32 < n ? c + 32 : 0)),
+                           load_const(d, row + (c + 64 < n ? c + 64 : 0)), load_const(d, row + (c + 96 < n ? c + 96 : 0)));
     }
 }
 
@@ -80,19 +80,19 @@ __device__ __forceinline__ void row_prefetch(const float *row, int slab, int n) 
 // KEEP: the row is read again soon (by the column sums); else its lines make
 // way first.
 template <bool VEC, bool KEEP = true>
-__device__ __forceinline__ void row_store(float *row, int slab, int k, int n, float4 v) {
+__device__ __forceinline__ void row_store(const DbgAccess &d, float *row, int slab, int k, int n, float4 v) {
     const int c = slab_col<VEC>(slab, k, 0);
     if constexpr (VEC) {
         if constexpr (KEEP) {
-            if (c < n) *reinterpret_cast<float4 *>(row + c) = v;
+            if (c < n) store_global(d, reinterpret_cast<float4 *>(row + c), v);
         } else {
-            if (c < n) __stcs(reinterpret_cast<float4 *>(row + c), v);
+            if (c < n) store_once(d, reinterpret_cast<float4 *>(row + c), v);
         }
     } else {
-        if (c < n) row[c] = v.x;
-        if (c + 32 < n) row[c + 32] = v.y;
-        if (c + 64 < n) row[c + 64] = v.z;
-        if (c + 96 < n) row[c + 96] = v.w;
+        if (c < n) store_global(d, row + c, v.x);
+        if (c + 32 < n) store_global(d, row + c + 32, v.y);
+        if (c + 64 < n) store_global(d, row + c + 64, v.z);
+        if (c + 96 < n) store_global(d, row + c + 96, v.w);
     }
 }
 
@@ -128,18 +128,18 @@ __device__ __forceinline__ void stage_store(float4 *stage, int slab, int k, floa
 
 // Starts the copy of the warp's slab of a row into the stage.
 template <bool VEC, int KS>
-__device__ __forceinline__ void stage_row(float4 *stage, const float *row, int slab, int n) {
+__device__ __forceinline__ void stage_row(const DbgAccess &d, float4 *stage, const float *row, int slab, int n) {
     float *s = reinterpret_cast<float *>(stage);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
         if constexpr (VEC) {
             const int c = slab_col<VEC>(slab, k, 0);
-            if (c < n) cp_async_16(s + stage_float<VEC>(slab, k, 0), row + c, 16u);
+            if (c < n && REPOPS_DBG_READ(d, row + c, 16)) cp_async_16(s + stage_float<VEC>(slab, k, 0), row + c, 16u);
         } else {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int c = slab_col<VEC>(slab, k, t);
-                if (c < n) cp_async_4(s + stage_float<VEC>(slab, k, t), row + c, 4u);
+                if (c < n && REPOPS_DBG_READ(d, row + c, 4)) cp_async_4(s + stage_float<VEC>(slab, k, t), row + c, 4u);
             }
         }
     }
@@ -148,9 +148,9 @@ __device__ __forceinline__ void stage_row(float4 *stage, const float *row, int s
 // The CTA's copy of a parameter row (null: none), in memory order, and a slab
 // step of it.  A barrier follows the copies.
 template <int LEN>
-__device__ __forceinline__ void param_copy(float *dst, const float *src, int n) {
+__device__ __forceinline__ void param_copy(const DbgAccess &d, float *dst, const float *src, int n) {
     if (!src) return;
-    for (int c = threadIdx.x; c < LEN; c += blockDim.x) dst[c] = c < n ? __ldg(src + c) : 0.0f;
+    for (int c = threadIdx.x; c < LEN; c += blockDim.x) dst[c] = c < n ? load_const(d, src + c) : 0.0f;
 }
 
 template <bool VEC>
@@ -257,7 +257,7 @@ constexpr size_t kTeamSmem = size_t(T) * KS * 16 * (PARAMS + STAGES * TEAMS);
 
 // --------------------------------------------------------------- forward ----
 
-struct EdgeArgs {
+struct EdgeArgs : DbgAccess {
     int64_t rows, n;
     const float *x, *f;
     int64_t ldx, ldf;
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
     extern __shared__ float4 stage_mem[];
     __shared__ float roots[2][2][8];
     __shared__ float4 lane_mem[T / 4];
+    if (!REPOPS_DBG_SMEM_OK(size_t(T) * KS * 16 * (kEdgePrefetch<T> ? 4 : 2), p.status)) return;
     float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
     const int slab = (threadIdx.x >> 5) * 1024;
     int phase = 0;
@@ -287,8 +288,8 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
     int cur = 0;
     int64_t row = blockIdx.x;
     if (row < p.rows) {
-        stage_row<VEC, KS>(stage_mem, p.f + row * p.ldf, slab, n);
-        stage_row<VEC, KS>(stage_mem + Q, p.x + row * p.ldx, slab, n);
+        stage_row<VEC, KS>(p, stage_mem, p.f + row * p.ldf, slab, n);
+        stage_row<VEC, KS>(p, stage_mem + Q, p.x + row * p.ldx, slab, n);
     }
     cp_async_commit();
     for (; row < p.rows; row += gridDim.x) {
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
         if constexpr (PF) {
             cur ^= 1;
             if (next < p.rows) {
-                stage_row<VEC, KS>(stage_mem + cur * 2 * Q, p.f + next * p.ldf, slab, n);
-                stage_row<VEC, KS>(stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, slab, n);
+                stage_row<VEC, KS>(p, stage_mem + cur * 2 * Q, p.f + next * p.ldf, slab, n);
+                stage_row<VEC, KS>(p, stage_mem + cur * 2 * Q + Q, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
@@ -322,11 +323,11 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
             float4 w[KB], g[KB];
             if (p.post) {
 #pragma unroll
-                for (int k = 0; k < KB; ++k) w[k] = row_load<VEC>(p.post, slab, b + k, n);
+                for (int k = 0; k < KB; ++k) w[k] = row_load<VEC>(p, p.post, slab, b + k, n);
             }
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < KB; ++k) g[k] = row_load<VEC>(gate, slab, b + k, n);
+                for (int k = 0; k < KB; ++k) g[k] = row_load<VEC>(p, gate, slab, b + k, n);
             }
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
                 if (p.post) v = mul4(mul4(v, inv_f), w[k]);
                 if (gate) v = mul4(v, g[k]);
                 v = add4(stage_load<VEC>(sx, slab, b + k), mul4(v, p.alpha));
-                row_store<VEC>(yr, slab, b + k, n, v);
+                row_store<VEC>(p, yr, slab, b + k, n, v);
                 if (p.pre) stage_store<VEC>(sx, slab, b + k, v);
             }
         }
@@ -346,15 +347,15 @@ __global__ void __launch_bounds__(T, 512 / T) edge_forward_kernel(EdgeArgs p) {
             float *hr = p.h + row * p.ldh;
             float4 w[KS];
 #pragma unroll
-            for (int k = 0; k < KS; ++k) w[k] = row_load<VEC>(p.pre, slab, k, n);
+            for (int k = 0; k < KS; ++k) w[k] = row_load<VEC>(p, p.pre, slab, k, n);
 #pragma unroll
-            for (int k = 0; k < KS; ++k) row_store<VEC>(hr, slab, k, n, mul4(mul4(stage_load<VEC>(sx, slab, k), inv_y), w[k]));
+            for (int k = 0; k < KS; ++k) row_store<VEC>(p, hr, slab, k, n, mul4(mul4(stage_load<VEC>(sx, slab, k), inv_y), w[k]));
         }
         __syncwarp();                       // the stage is read before it is filled again
         if constexpr (!PF) {
             if (next < p.rows) {
-                stage_row<VEC, KS>(sf, p.f + next * p.ldf, slab, n);
-                stage_row<VEC, KS>(sx, p.x + next * p.ldx, slab, n);
+                stage_row<VEC, KS>(p, sf, p.f + next * p.ldf, slab, n);
+                stage_row<VEC, KS>(p, sx, p.x + next * p.ldx, slab, n);
             }
             cp_async_commit();
         }
@@ -367,8 +368,10 @@ __global__ void __launch_bounds__(256) edge_forward_long_kernel(EdgeArgs p) {
     extern __shared__ float buf[];
     __shared__ float bcast;
     const int runs = int((p.n + RUN - 1) / RUN);
+    if (!REPOPS_DBG_SMEM_OK(uint64_t(runs + (runs + RUN - 1) / RUN) * sizeof(float), p.status)) return;
     float *buf2 = buf + runs;
     const float nf = float(p.n);
+    auto at = [&](const float *v) { return load_global(p, v); };
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const float *xr = p.x + row * p.ldx, *fr = p.f + row * p.ldf;
         const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
@@ -376,21 +379,24 @@ __global__ void __launch_bounds__(256) edge_forward_long_kernel(EdgeArgs p) {
         float inv_f = 0.0f;
         if (p.post)
             inv_f = rms_inv(generic_reduce_idx<Op::Sum>(
-                                p.n, [&](int64_t i) { return __fmul_rn(fr[i], fr[i]); }, buf, buf2, &bcast),
+                                p.n, [&](int64_t i) { const float v = at(fr + i); return __fmul_rn(v, v); }, buf, buf2,
+                                &bcast),
                             nf, p.eps);
         for (int64_t i = threadIdx.x; i < p.n; i += 256) {
-            float v = fr[i];
-            if (p.post) v = __fmul_rn(__fmul_rn(v, inv_f), p.post[i]);
-            if (gate) v = __fmul_rn(v, gate[i]);
-            yr[i] = __fadd_rn(xr[i], __fmul_rn(p.alpha, v));
+            float v = at(fr + i);
+            if (p.post) v = __fmul_rn(__fmul_rn(v, inv_f), at(p.post + i));
+            if (gate) v = __fmul_rn(v, at(gate + i));
+            store_global(p, yr + i, __fadd_rn(at(xr + i), __fmul_rn(p.alpha, v)));
         }
         __syncthreads();
         if (p.pre) {
             const float inv_y = rms_inv(generic_reduce_idx<Op::Sum>(
-                                            p.n, [&](int64_t i) { return __fmul_rn(yr[i], yr[i]); }, buf, buf2, &bcast),
+                                            p.n, [&](int64_t i) { const float v = at(yr + i); return __fmul_rn(v, v); }, buf,
+                                            buf2, &bcast),
                                         nf, p.eps);
             float *hr = p.h + row * p.ldh;
-            for (int64_t i = threadIdx.x; i < p.n; i += 256) hr[i] = __fmul_rn(__fmul_rn(yr[i], inv_y), p.pre[i]);
+            for (int64_t i = threadIdx.x; i < p.n; i += 256) 
+                store_global(p, hr + i, __fmul_rn(__fmul_rn(at(yr + i), inv_y), at(p.pre + i)));
         }
         __syncthreads();
     }
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(256) edge_forward_long_kernel(EdgeArgs p) {
 
 // -------------------------------------------------------------- backward ----
 
-struct EdgeBackArgs {
+struct EdgeBackArgs : DbgAccess {
     int64_t rows, n;
     // the norm before the next block: its input y (or q, s: 8 bits), the
     // gradient dh of its output, and the gradient dy arriving past it
@@ -430,13 +436,13 @@ __device__ __forceinline__ float4 row8_load(const EdgeBackArgs &p, int64_t row, 
     const float *s = p.s + row * p.lds;
     if constexpr (VEC) {                   // a group is a multiple of 4 columns
         const int i = c < n ? c : 0;
-        return unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(q + i)), __ldg(s + (i >> p.shift)));
+        return unpack_q4(load_const(p, reinterpret_cast<const uint32_t *>(q + i)), load_const(p, s + (i >> p.shift)));
     } else {
         float v[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int i = c + 32 * t < n ? c + 32 * t : 0;
-            v[t] = unpack_q1(__ldg(q + i), __ldg(s + (i >> p.shift)));
+            v[t] = unpack_q1(load_const(p, q + i), load_const(p, s + (i >> p.shift)));
         }
         return make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -455,28 +461,29 @@ __global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kern
     extern __shared__ float4 smem[];
     __shared__ float roots[TEAMS][2][2][8];
     __shared__ float4 lane_mem[TEAMS * T / 4];
+    if (!REPOPS_DBG_SMEM_OK((F ? kTeamSmem<T, KS, 4, 3, TEAMS> : kTeamSmem<T, KS, 3, 1, TEAMS>), p.status)) return;
     const int n = int(p.n), team = threadIdx.x / T, slab = ((threadIdx.x % T) >> 5) * 1024;
     const float nf = float(p.n);
     float *pre = reinterpret_cast<float *>(smem), *post = pre + 4 * Q, *gate1 = post + 4 * Q;
     float4 *sy = smem + (F ? 3 : 1) * Q + team * Q * (F ? 4 : 3), *sh = sy + Q, *sr = sh + Q, *sf = sr + Q;
     float4 *lanes = lane_mem + (threadIdx.x >> 5) * 8;
     const bool one_gate = F && p.gate && p.gate_rows >= p.rows;
-    param_copy<4 * Q>(pre, p.pre, n);
+    param_copy<4 * Q>(p, pre, p.pre, n);
     if constexpr (F) {
-        param_copy<4 * Q>(post, p.post, n);
-        param_copy<4 * Q>(gate1, one_gate ? p.gate : nullptr, n);
+        param_copy<4 * Q>(p, post, p.post, n);
+        param_copy<4 * Q>(p, gate1, one_gate ? p.gate : nullptr, n);
     }
     __syncthreads();
     int phase = 0;
     // rows go to the SMs first, then to their teams
     for (int64_t row = int64_t(team) * gridDim.x + blockIdx.x; row < p.rows; row += int64_t(gridDim.x) * TEAMS) {
         if (p.dh) {
-            if constexpr (!Q8) stage_row<VEC, KS>(sy, p.y + row * p.ldy, slab, n);
-            stage_row<VEC, KS>(sh, p.dh + row * p.lddh, slab, n);
+            if constexpr (!Q8) stage_row<VEC, KS>(p, sy, p.y + row * p.ldy, slab, n);
+            stage_row<VEC, KS>(p, sh, p.dh + row * p.lddh, slab, n);
         }
-        if constexpr (F) stage_row<VEC, KS>(sf, p.f + row * p.ldf, slab, n);
+        if constexpr (F) stage_row<VEC, KS>(p, sf, p.f + row * p.ldf, slab, n);
         cp_async_commit();
-        if (p.dy) stage_row<VEC, KS>(sr, p.dy + row * p.lddy, slab, n);
+        if (p.dy) stage_row<VEC, KS>(p, sr, p.dy + row * p.lddy, slab, n);
         cp_async_commit();
         if constexpr (Q8) {
 #pragma unroll
@@ -492,9 +499,9 @@ __global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kern
         slab_roots<T, 2>(r2, roots[team], phase, team, n);
         const float inv_y = rms_inv(r2[0], nf, p.eps), inv_f = rms_inv(r2[1], nf, p.eps);
         if (threadIdx.x % T == 0) {
-            if (p.dh) p.inv_y[row] = inv_y;
+            if (p.dh) store_global(p, p.inv_y + row, inv_y);
             if constexpr (F) {
-                if (p.post) p.inv_f[row] = inv_f;
+                if (p.post) store_global(p, p.inv_f + row, inv_f);
             }
         }
         float4 e[KS];                             // dx
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kern
                 g[k] = param_load<VEC>(pre, slab, k);
                 e[k] = mul4(stage_load<VEC>(sy, slab, k), inv_y);
                 if constexpr (Q8) {
-                    if (p.h) row_store<VEC, false>(p.h + row * p.ldh, slab, k, n, mul4(e[k], g[k]));
+                    if (p.h) row_store<VEC, false>(p, p.h + row * p.ldh, slab, k, n, mul4(e[k], g[k]));
                 }
                 g[k] = mul4(stage_load<VEC>(sh, slab, k), g[k]);
                 stage_store<VEC>(sh, slab, k, mul4(g[k], e[k]));
@@ -529,14 +536,14 @@ __global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kern
         }
         float *dxr = p.dx + row * p.lddx;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) row_store<VEC>(dxr, slab, k, n, e[k]);
+        for (int k = 0; k < KS; ++k) row_store<VEC>(p, dxr, slab, k, n, e[k]);
         if constexpr (F) {
             float *dfr = p.df + row * p.lddf;
             const float *gate = p.gate && !one_gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
             float4 g[KS];
             if (gate) {
 #pragma unroll
-                for (int k = 0; k < KS; ++k) g[k] = row_load<VEC>(gate, slab, k, n);
+                for (int k = 0; k < KS; ++k) g[k] = row_load<VEC>(p, gate, slab, k, n);
             }
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(T *kBackTeams<T, KS, F>, 1) edge_backward_kern
                 for (int k = 0; k < KS; ++k) e[k] = mul4(sub4(e[k], mul4(g[k], c)), inv_f);
             }
 #pragma unroll
-            for (int k = 0; k < KS; ++k) row_store<VEC, false>(dfr, slab, k, n, e[k]);
+            for (int k = 0; k < KS; ++k) row_store<VEC, false>(p, dfr, slab, k, n, e[k]);
         }
         __syncwarp();
     }
@@ -573,12 +580,14 @@ __global__ void __launch_bounds__(256) edge_backward_long_kernel(EdgeBackArgs p)
     extern __shared__ float buf[];
     __shared__ float bcast;
     const int runs = int((p.n + RUN - 1) / RUN);
+    if (!REPOPS_DBG_SMEM_OK(uint64_t(runs + (runs + RUN - 1) / RUN) * sizeof(float), p.status)) return;
     float *buf2 = buf + runs;
     const float nf = float(p.n);
+    auto at = [&](const float *v) { return load_global(p, v); };
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         auto yv = [&](int64_t i) {
-            if constexpr (Q8) return __fmul_rn(float(p.q[row * p.ldq + i]), p.s[row * p.lds + (i >> p.shift)]);
-            else return p.y[row * p.ldy + i];
+            if constexpr (Q8) return __fmul_rn(float(load_global(p, p.q + row * p.ldq + i)), at(p.s + row * p.lds + (i >> p.shift)));
+            else return at(p.y + row * p.ldy + i);
         };
         const float *dhr = p.dh + row * p.lddh, *dyr = p.dy + row * p.lddy;
         float *dxr = p.dx + row * p.lddx;
@@ -588,21 +597,21 @@ __global__ void __launch_bounds__(256) edge_backward_long_kernel(EdgeBackArgs p)
                                 p.n, [&](int64_t i) { const float v = yv(i); return __fmul_rn(v, v); }, buf, buf2,
                                 &bcast), nf, p.eps);
             c = __fdiv_rn(generic_reduce_idx<Op::Sum>(p.n, [&](int64_t i) {
-                return __fmul_rn(__fmul_rn(dhr[i], p.pre[i]), __fmul_rn(yv(i), inv_y));
+                return __fmul_rn(__fmul_rn(at(dhr + i), at(p.pre + i)), __fmul_rn(yv(i), inv_y));
             }, buf, buf2, &bcast), nf);
-            if (threadIdx.x == 0) p.inv_y[row] = inv_y;
+            if (threadIdx.x == 0) store_global(p, p.inv_y + row, inv_y);
         }
         for (int64_t i = threadIdx.x; i < p.n; i += 256) {
             float d = 0.0f;
             if (p.dh) {
                 const float xh = __fmul_rn(yv(i), inv_y);
-                d = __fmul_rn(inv_y, __fsub_rn(__fmul_rn(dhr[i], p.pre[i]), __fmul_rn(xh, c)));
+                d = __fmul_rn(inv_y, __fsub_rn(__fmul_rn(at(dhr + i), at(p.pre + i)), __fmul_rn(xh, c)));
                 if constexpr (Q8) {
-                    if (p.h) p.h[row * p.ldh + i] = __fmul_rn(xh, p.pre[i]);
+                    if (p.h) store_global(p, p.h + row * p.ldh + i, __fmul_rn(xh, at(p.pre + i)));
                 }
             }
-            if (p.dy) d = p.dh ? __fadd_rn(d, dyr[i]) : dyr[i];
-            dxr[i] = d;
+            if (p.dy) d = p.dh ? __fadd_rn(d, at(dyr + i)) : at(dyr + i);
+            store_global(p, dxr + i, d);
         }
         __syncthreads();
         if constexpr (F) {
@@ -610,23 +619,24 @@ __global__ void __launch_bounds__(256) edge_backward_long_kernel(EdgeBackArgs p)
             const float *gate = p.gate ? p.gate + (row / p.gate_rows) * p.ldgate : nullptr;
             float *dfr = p.df + row * p.lddf;
             auto dp = [&](int64_t i) {
-                float d = __fmul_rn(dxr[i], p.alpha);
-                if (gate) d = __fmul_rn(d, gate[i]);
-                return p.post ? __fmul_rn(d, p.post[i]) : d;
+                float d = __fmul_rn(at(dxr + i), p.alpha);
+                if (gate) d = __fmul_rn(d, at(gate + i));
+                return p.post ? __fmul_rn(d, at(p.post + i)) : d;
             };
             float inv_f = 0.0f, cf = 0.0f;
             if (p.post) {
                 inv_f = rms_inv(generic_reduce_idx<Op::Sum>(
-                                    p.n, [&](int64_t i) { return __fmul_rn(fr[i], fr[i]); }, buf, buf2, &bcast),
+                                    p.n, [&](int64_t i) { const float v = at(fr + i); return __fmul_rn(v, v); }, buf, buf2,
+                                    &bcast),
                                 nf, p.eps);
                 cf = __fdiv_rn(generic_reduce_idx<Op::Sum>(
-                                   p.n, [&](int64_t i) { return __fmul_rn(dp(i), __fmul_rn(fr[i], inv_f)); }, buf, buf2,
+                                   p.n, [&](int64_t i) { return __fmul_rn(dp(i), __fmul_rn(at(fr + i), inv_f)); }, buf, buf2,
                                    &bcast), nf);
-                if (threadIdx.x == 0) p.inv_f[row] = inv_f;
+                if (threadIdx.x == 0) store_global(p, p.inv_f + row, inv_f);
             }
             for (int64_t i = threadIdx.x; i < p.n; i += 256) {
                 const float d = dp(i);
-                dfr[i] = p.post ? __fmul_rn(inv_f, __fsub_rn(d, __fmul_rn(__fmul_rn(fr[i], inv_f), cf))) : d;
+                store_global(p, dfr + i, p.post ? __fmul_rn(inv_f, __fsub_rn(d, __fmul_rn(__fmul_rn(at(fr + i), inv_f), cf))) : d);
             }
             __syncthreads();
         }
@@ -650,21 +660,21 @@ struct Cols {
 };
 
 template <int W>
-__device__ __forceinline__ Cols<W> cols_load(const float *q) {
+__device__ __forceinline__ Cols<W> cols_load(const DbgAccess &d, const float *q) {
     Cols<W> r;
     if constexpr (W == 4) {
-        const float4 w = __ldg(reinterpret_cast<const float4 *>(q));
+        const float4 w = load_const(d, reinterpret_cast<const float4 *>(q));
         r.v[0] = w.x; r.v[1] = w.y; r.v[2] = w.z; r.v[3] = w.w;
     } else {
-        r.v[0] = __ldg(q);
+        r.v[0] = load_const(d, q);
     }
     return r;
 }
 
 template <int W>
-__device__ __forceinline__ void cols_store(float *q, const Cols<W> &r) {
-    if constexpr (W == 4) *reinterpret_cast<float4 *>(q) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-    else *q = r.v[0];
+__device__ __forceinline__ void cols_store(const DbgAccess &d, float *q, const Cols<W> &r) {
+    if constexpr (W == 4) store_global(d, reinterpret_cast<float4 *>(q), make_float4(r.v[0], r.v[1], r.v[2], r.v[3]));
+    else store_global(d, q, r.v[0]);
 }
 
 // A thread forms and folds the terms of W columns over a run of 32 rows:
@@ -680,7 +690,7 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
     const int64_t c = (blockIdx.x * int64_t(128) + threadIdx.x) * W;
     if (c >= p.n) return;
     Cols<W> post{};
-    if (GATE && p.post) post = cols_load<W>(p.post + c);
+    if (GATE && p.post) post = cols_load<W>(p, p.post + c);
     // the last rows first: the row kernel has just left them in L2
     for (int64_t run = a.runs - 1 - blockIdx.y; run >= 0; run -= gridDim.y) {
         const int64_t b = run / a.block_runs, first = b * a.block_rows + (run - b * a.block_runs) * RUN;
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
         if (POST && p.gate) {
             gate_row = p.gate + (first / p.gate_rows) * p.ldgate + c;
             gate_left = p.gate_rows - first % p.gate_rows;
-            gate = cols_load<W>(gate_row);
+            gate = cols_load<W>(p, gate_row);
         }
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += B) {
@@ -702,23 +712,23 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
                 const int64_t r = first + min(r0 + i, rows - 1);     // past the run: its last row, not folded
                 if constexpr (PRE) {
                     if constexpr (Q8) {
-                        const float s = __ldg(p.s + r * p.lds + (c >> p.shift));
+                        const float s = load_const(p, p.s + r * p.lds + (c >> p.shift));
                         if constexpr (W == 4) {
-                            const float4 w = unpack_q4(__ldg(reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
+                            const float4 w = unpack_q4(load_const(p, reinterpret_cast<const uint32_t *>(p.q + r * p.ldq + c)), s);
                             y[i].v[0] = w.x; y[i].v[1] = w.y; y[i].v[2] = w.z; y[i].v[3] = w.w;
                         } else {
-                            y[i].v[0] = unpack_q1(__ldg(p.q + r * p.ldq + c), s);
+                            y[i].v[0] = unpack_q1(load_const(p, p.q + r * p.ldq + c), s);
                         }
                     } else {
-                        y[i] = cols_load<W>(p.y + r * p.ldy + c);
+                        y[i] = cols_load<W>(p, p.y + r * p.ldy + c);
                     }
-                    d[i] = cols_load<W>(p.dh + r * p.lddh + c);
-                    iy[i] = __ldg(p.inv_y + r);
+                    d[i] = cols_load<W>(p, p.dh + r * p.lddh + c);
+                    iy[i] = load_const(p, p.inv_y + r);
                 }
                 if constexpr (POST || GATE) {
-                    dx[i] = cols_load<W>(p.dx + r * p.lddx + c);
-                    f[i] = cols_load<W>(p.f + r * p.ldf + c);
-                    jf[i] = p.post ? __ldg(p.inv_f + r) : 0.0f;
+                    dx[i] = cols_load<W>(p, p.dx + r * p.lddx + c);
+                    f[i] = cols_load<W>(p, p.f + r * p.ldf + c);
+                    jf[i] = p.post ? load_const(p, p.inv_f + r) : 0.0f;
                 }
             }
 #pragma unroll
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
                     if (gate_left == 0) {
                         gate_row += p.ldgate;
                         gate_left = p.gate_rows;
-                        gate = cols_load<W>(gate_row);
+                        gate = cols_load<W>(p, gate_row);
                     }
                     --gate_left;
                 }
@@ -754,9 +764,9 @@ __global__ void __launch_bounds__(128) edge_columns_kernel(ColArgs a) {
                 }
             }
         }
-        if constexpr (PRE) cols_store<W>(a.pre + run * p.n + c, s_pre);
-        if constexpr (POST) cols_store<W>(a.post + run * p.n + c, s_post);
-        if constexpr (GATE) cols_store<W>(a.gate + run * a.ldg + c, s_gate);
+        if constexpr (PRE) cols_store<W>(p, a.pre + run * p.n + c, s_pre);
+        if constexpr (POST) cols_store<W>(p, a.post + run * p.n + c, s_post);
+        if constexpr (GATE) cols_store<W>(p, a.gate + run * a.ldg + c, s_gate);
     }
 }
 
@@ -765,7 +775,7 @@ struct FoldSet {
     float *out;             // blocks x n, pitch ldo
     int64_t blocks, runs, ldo;
 };
-struct FoldArgs {
+struct FoldArgs : DbgAccess {
     FoldSet s[3];
     int64_t n;
 };
@@ -783,13 +793,13 @@ __global__ void __launch_bounds__(1024) edge_fold_kernel(FoldArgs a) {
         const int64_t r0 = int64_t(ty) * RUN, r1 = imin64(r0 + RUN, s.runs);
         if (c < a.n && r0 < r1) {
             const float *in = s.in + (b * s.runs + r0) * a.n + c;
-            float acc = in[0];
+            float acc = load_global(a, in);
             const int m = int(r1 - r0);
             if (m == RUN) {
 #pragma unroll
-                for (int i = 1; i < RUN; ++i) acc = __fadd_rn(acc, in[int64_t(i) * a.n]);
+                for (int i = 1; i < RUN; ++i) acc = __fadd_rn(acc, load_global(a, in + int64_t(i) * a.n));
             } else {
-                for (int i = 1; i < m; ++i) acc = __fadd_rn(acc, in[int64_t(i) * a.n]);
+                for (int i = 1; i < m; ++i) acc = __fadd_rn(acc, load_global(a, in + int64_t(i) * a.n));
             }
             part[ty][tx] = acc;
         }
@@ -797,7 +807,7 @@ __global__ void __launch_bounds__(1024) edge_fold_kernel(FoldArgs a) {
         if (ty == 0 && c < a.n) {
             float acc = part[0][tx];
             for (int g = 1; g < groups; ++g) acc = __fadd_rn(acc, part[g][tx]);
-            s.out[b * s.ldo + c] = acc;
+            store_global(a, s.out + b * s.ldo + c, acc);
         }
         __syncthreads();
     }
@@ -999,7 +1009,7 @@ int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_
         rc = launch_columns<Q8, F>(c, vec, s);
         if (rc != REPOPS_OK) return rc;
     }
-    FoldArgs f{};
+    FoldArgs f{e};
     f.n = e.n;
     int sets = 0;
     int64_t blocks = 1, most = 1;
@@ -1010,7 +1020,7 @@ int run_backward(EdgeBackArgs e, float *dpre, float *dpost, float *dgate, int64_
             const int64_t up = ceil_div(runs, RUN);
             const dim3 grid(unsigned(std::min<int64_t>(ceil_div(e.n, 256), 64)), unsigned(std::min<int64_t>(up, 65535)));
             for (int64_t b = 0; b < nb && rc == REPOPS_OK; ++b) {
-                colsum_pass_kernel<<<grid, 256, 0, s>>>(runs, e.n, in + b * runs * e.n, e.n, level + b * up * e.n, e.n);
+                colsum_pass_kernel<<<grid, 256, 0, s>>>(runs, e.n, in + b * runs * e.n, e.n, level + b * up * e.n, e.n, e);
                 rc = check_launch();
             }
             in = level;
@@ -1076,8 +1086,16 @@ extern "C" int repops_rmsnorm_residual_f32(int64_t rows, int64_t cols, const flo
         if (!(o.p == f && o.ld == ldf) && ranges_overlap(o.p, o.b, f, fb)) return REPOPS_ERR_ALIAS;
     }
     if (h && ranges_overlap(y, yb, h, hb)) return REPOPS_ERR_ALIAS;
-    const EdgeArgs a{rows, cols, x, f, ldx, ldf, post_gain, gate, pre_gain, ldgate, gate ? gate_rows : 1, alpha, eps,
-                     y, h, ldy, ldh};
+    EdgeArgs a{{}, rows, cols, x, f, ldx, ldf, post_gain, gate, pre_gain, ldgate, gate ? gate_rows : 1, alpha, eps,
+               y, h, ldy, ldh};
+    a.reads(x, xb);
+    a.reads(f, fb);
+    a.reads(post_gain, vb);
+    a.reads(gate, gb);
+    a.reads(pre_gain, vb);
+    a.writes(y, yb);
+    a.writes(h, hb);
+    if (const int rc = a.arm(); rc != REPOPS_OK) return rc;
     if (cols > MAX_STAGED_COLS) return launch_long(edge_forward_long_kernel, a, rows, cols, stream);
     const bool vec = cols % 4 == 0 && vec_row(x, ldx) && vec_row(f, ldf) && vec_row(y, ldy) && (!h || vec_row(h, ldh)) &&
                      vec_row(post_gain, 0) && vec_row(pre_gain, 0) && (!gate || vec_row(gate, ldgate));
@@ -1141,6 +1159,20 @@ extern "C" int repops_rmsnorm_residual_backward_f32(
     e.post = post_gain; e.gate = gate; e.ldgate = ldgate; e.gate_rows = gate ? gate_rows : 1;
     e.alpha = alpha; e.eps = eps;
     e.dx = dx; e.lddx = lddx; e.df = df; e.lddf = lddf;
+    e.reads(dy, dyb);
+    e.reads(dh, dhb);
+    e.reads(y, yb);
+    e.reads(f, fb);
+    e.reads(post_gain, vb);
+    e.reads(gate, gb);
+    e.reads(pre_gain, vb);
+    e.writes(dx, dxb);
+    e.writes(df, dfb);
+    e.writes(dpre, vb);
+    e.writes(dpost, vb);
+    e.writes(dgate, dgb);
+    e.writes(w.p, need);
+    if (rc = e.arm(); rc != REPOPS_OK) return w.release(rc);
     const bool vec = cols % 4 == 0 && (!dy || vec_row(dy, lddy)) && (!dh || vec_row(dh, lddh)) &&
                      (!y || vec_row(y, ldy)) && vec_row(f, ldf) && vec_row(post_gain, 0) && vec_row(pre_gain, 0) &&
                      (!gate || (vec_row(gate, ldgate) && vec_row(dgate, lddgate))) && vec_row(dx, lddx) &&
@@ -1190,6 +1222,16 @@ extern "C" int repops_rmsnorm_backward_i8(int64_t rows, int64_t cols, const int8
     e.gate_rows = 1;
     e.eps = eps;
     e.dx = dx; e.lddx = lddx; e.h = h; e.ldh = ldh;
+    e.reads(x, xb);
+    e.reads(x_scale, sb);
+    e.reads(gamma, vb);
+    e.reads(dy, dyb);
+    e.reads(res, rb);
+    e.writes(dx, dxb);
+    e.writes(h, hb);
+    e.writes(dgamma, vb);
+    e.writes(w.p, need);
+    if (rc = e.arm(); rc != REPOPS_OK) return w.release(rc);
     const bool vec = cols % 4 == 0 && reinterpret_cast<uintptr_t>(x) % 4 == 0 && ldx % 4 == 0 && vec_row(gamma, 0) &&
                      vec_row(dy, lddy) && (!res || vec_row(res, ldres)) && vec_row(dx, lddx) &&
                      (!h || vec_row(h, ldh));

@@ -66,7 +66,7 @@ namespace {
 
 constexpr int64_t kMaxK = 131071;
 
-struct I8Args {
+struct I8Args : DbgAccess {
     int64_t M, N, K;
     const int8_t *A, *B;           // M x K and N x K, k contiguous
     int64_t lda, ldb;
@@ -82,53 +82,45 @@ struct I8Args {
 // VEC: the row is 16-byte aligned.  Otherwise five aligned words are shifted
 // together; where those would leave the operand [base, end), single bytes.
 template <bool VEC>
-__device__ __forceinline__ uint4 load_k16(const int8_t *__restrict__ row, int64_t k, int64_t n, const int8_t *base,
-                                          const int8_t *end) {
+__device__ __forceinline__ uint4 load_k16(const DbgAccess &d, const int8_t *__restrict__ row, int64_t k, int64_t n,
+                                          const int8_t *base, const int8_t *end) {
     const int8_t *p = row + k;
     if (k + 16 <= n) {
         if constexpr (VEC) {
-            return __ldg(reinterpret_cast<const uint4 *>(p));
+            return load_const(d, reinterpret_cast<const uint4 *>(p));
         } else {
             const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u);
             const int8_t *q = p - off;
             if (q >= base && q + (off ? 20 : 16) <= end) {
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
-                const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3),
-                               e = off ? __ldg(w + 4) : 0u;
+                const uint32_t w0 = load_const(d, w), w1 = load_const(d, w + 1), w2 = load_const(d, w + 2),
+                               w3 = load_const(d, w + 3), w4 = off ? load_const(d, w + 4) : 0u;
                 const uint32_t s = 8 * off;
-                return make_uint4(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s), __funnelshift_r(c, d, s),
-                                  __funnelshift_r(d, e, s));
+                return make_uint4(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s), __funnelshift_r(w2, w3, s),
+                                  __funnelshift_r(w3, w4, s));
             }
         }
     }
     uint32_t r[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        if (k + i < n) r[i >> 2] |= uint32_t(uint8_t(p[i])) << (8 * (i & 3));
+        if (k + i < n) r[i >> 2] |= uint32_t(uint8_t(load_global(d, p + i))) << (8 * (i & 3));
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// 16 or 8 bytes that all lie within a row, without a branch: a guard around a load
+// 16 bytes that all lie within a row, without a branch: a guard around a load
 // makes the loads of a loop wait for one another.  Where the address is not
 // aligned, every word read holds at least one of the bytes asked for.
 template <bool VEC>
-__device__ __forceinline__ uint4 load_full16(const int8_t *__restrict__ p) {
-    if constexpr (VEC) return __ldg(reinterpret_cast<const uint4 *>(p));
+__device__ __forceinline__ uint4 load_full16(const DbgAccess &d, const int8_t *__restrict__ p) {
+    if constexpr (VEC) return load_const(d, reinterpret_cast<const uint4 *>(p));
     const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u), s = 8 * off;
     const uint32_t *w = reinterpret_cast<const uint32_t *>(p - off);
-    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2), d = __ldg(w + 3), e = __ldg(w + (off ? 4 : 3));
-    return make_uint4(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s), __funnelshift_r(c, d, s),
-                      __funnelshift_r(d, e, s));
+    const uint32_t w0 = load_const(d, w), w1 = load_const(d, w + 1), w2 = load_const(d, w + 2), w3 = load_const(d, w + 3),
+                   w4 = load_const(d, w + (off ? 4 : 3));
+    return make_uint4(__funnelshift_r(w0, w1, s), __funnelshift_r(w1, w2, s), __funnelshift_r(w2, w3, s),
+                      __funnelshift_r(w3, w4, s));
 }
-template <bool VEC>
-__device__ __forceinline__ uint2 load_full8(const int8_t *__restrict__ p) {
-    if constexpr (VEC) return __ldg(reinterpret_cast<const uint2 *>(p));
-    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u), s = 8 * off;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p - off);
-    const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + (off ? 2 : 1));
-    return make_uint2(__funnelshift_r(a, b, s), __funnelshift_r(b, c, s));
-}
-
 // ---------------------------------------------------------------- epilogue ----
 
 template <int TY>
@@ -136,6 +128,13 @@ __device__ __forceinline__ void store_c(void *C, int64_t i, float v) {
     if constexpr (TY == REPOPS_TYPE_F32) static_cast<float *>(C)[i] = v;
     else if constexpr (TY == REPOPS_TYPE_F16) static_cast<__half *>(C)[i] = __float2half_rn(v);
     else static_cast<__nv_bfloat16 *>(C)[i] = __float2bfloat16_rn(v);
+}
+
+// Element i of C, in global memory.
+template <int TY>
+__device__ __forceinline__ void store_c(const DbgAccess &d, void *C, int64_t i, float v) {
+    constexpr uint32_t size = TY == REPOPS_TYPE_F32 ? 4u : 2u;
+    if (REPOPS_DBG_WRITE(d, static_cast<const uint8_t *>(C) + i * int64_t(size), size)) store_c<TY>(C, i, v);
 }
 
 template <int TY>
@@ -146,9 +145,9 @@ __device__ __forceinline__ uint32_t pack_c(float lo, float hi) {
     return h[0] | (uint32_t(h[1]) << 16);
 }
 
-__device__ __forceinline__ float scale_bias(float v, float sb, const float *bias, int64_t j) {
-    v = __fmul_rn(v, sb);
-    return bias ? __fadd_rn(v, __ldg(bias + j)) : v;
+__device__ __forceinline__ float scale_bias(const I8Args &p, float v, int64_t j) {
+    v = __fmul_rn(v, load_const(p, p.sb + j));
+    return p.bias ? __fadd_rn(v, load_const(p, p.bias + j)) : v;
 }
 
 // ---------------------------------------------------------------- few rows ----
@@ -206,17 +205,17 @@ __global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
     for (; k + 16 <= K; k += 512) {
         uint4 w[R], x[NT];
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = load_full16<VEC>(rw[r] + k);
+        for (int r = 0; r < R; ++r) w[r] = load_full16<VEC>(p, rw[r] + k);
 #pragma unroll
-        for (int m = 0; m < NT; ++m) x[m] = load_full16<VEC>(rx[m] + k);
+        for (int m = 0; m < NT; ++m) x[m] = load_full16<VEC>(p, rx[m] + k);
         multiply(w, x);
     }
     if (k < K) {
         uint4 w[R], x[NT];
 #pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = load_k16<VEC>(rw[r], k, K, p.B, p.b_end);
+        for (int r = 0; r < R; ++r) w[r] = load_k16<VEC>(p, rw[r], k, K, p.B, p.b_end);
 #pragma unroll
-        for (int m = 0; m < NT; ++m) x[m] = load_k16<VEC>(rx[m], k, K, p.A, p.a_end);
+        for (int m = 0; m < NT; ++m) x[m] = load_k16<VEC>(p, rx[m], k, K, p.A, p.a_end);
         multiply(w, x);
     }
     int mine = 0;                      // lane r * NT + m keeps channel r, token m
@@ -229,8 +228,8 @@ __global__ void __launch_bounds__(256) gemm_i8_dot_kernel(I8Args p) {
         }
     const int64_t j = j0 + lane / NT, m = lane % NT;
     if (lane < R * NT && j < p.N && m < p.M) {
-        const float v = __fmul_rn(__int2float_rn(mine), __ldg(p.sa + m));
-        store_c<TY>(p.C, m * p.ldc + j, scale_bias(v, __ldg(p.sb + j), p.bias, j));
+        const float v = __fmul_rn(__int2float_rn(mine), load_const(p, p.sa + m));
+        store_c<TY>(p, p.C, m * p.ldc + j, scale_bias(p, v, j));
     }
 }
 
@@ -275,9 +274,9 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
         for (int e = 0; e < UNROLL; ++e) {
             const int k = (s + 8 * e) * 64 + 16 * q;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[e][h] = load_full16<VEC>(rw[h] + k);
+            for (int h = 0; h < 2; ++h) w[e][h] = load_full16<VEC>(p, rw[h] + k);
 #pragma unroll
-            for (int u = 0; u < NT; ++u) x[e][u] = load_full16<VEC>(rx[u] + k);
+            for (int u = 0; u < NT; ++u) x[e][u] = load_full16<VEC>(p, rx[u] + k);
         }
 #pragma unroll
         for (int e = 0; e < UNROLL; ++e) multiply(w[e], x[e]);
@@ -286,18 +285,18 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
         const int k = s * 64 + 16 * q;
         uint4 w[2], x[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w[h] = load_full16<VEC>(rw[h] + k);
+        for (int h = 0; h < 2; ++h) w[h] = load_full16<VEC>(p, rw[h] + k);
 #pragma unroll
-        for (int u = 0; u < NT; ++u) x[u] = load_full16<VEC>(rx[u] + k);
+        for (int u = 0; u < NT; ++u) x[u] = load_full16<VEC>(p, rx[u] + k);
         multiply(w, x);
     }
     if (s == full && p.K % 64) {                               // the last step, in part behind K
         const int64_t k = int64_t(s) * 64 + 16 * q;
         uint4 w[2], x[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) w[h] = load_k16<VEC>(rw[h], k, p.K, p.B, p.b_end);
+        for (int h = 0; h < 2; ++h) w[h] = load_k16<VEC>(p, rw[h], k, p.K, p.B, p.b_end);
 #pragma unroll
-        for (int u = 0; u < NT; ++u) x[u] = load_k16<VEC>(rx[u], k, p.K, p.A, p.a_end);
+        for (int u = 0; u < NT; ++u) x[u] = load_k16<VEC>(p, rx[u], k, p.K, p.A, p.a_end);
         multiply(w, x);
     }
     __syncthreads();
@@ -311,8 +310,8 @@ __global__ void __launch_bounds__(256) gemm_i8_rows_kernel(I8Args p) {
     for (int i = threadIdx.x; i < TK * CH; i += 256) {
         const int64_t m = m0 + i / CH, n = n0 + i % CH;
         if (m >= p.M || n >= p.N) continue;
-        const float v = __fmul_rn(__int2float_rn(sum[i / CH][i % CH]), __ldg(p.sa + m));
-        store_c<TY>(p.C, m * p.ldc + n, scale_bias(v, __ldg(p.sb + n), p.bias, n));
+        const float v = __fmul_rn(__int2float_rn(sum[i / CH][i % CH]), load_const(p, p.sa + m));
+        store_c<TY>(p, p.C, m * p.ldc + n, scale_bias(p, v, n));
     }
 }
 
@@ -325,26 +324,26 @@ constexpr int kStreamThreads = 608;       // 8 epilogue warps, 8 widening warps,
 
 // Bytes k .. k+7 of a row (zeros from `n` on), as load_k16 loads sixteen.
 template <bool VEC>
-__device__ __forceinline__ uint2 load_k8(const int8_t *__restrict__ row, int64_t k, int64_t n, const int8_t *base,
-                                         const int8_t *end) {
+__device__ __forceinline__ uint2 load_k8(const DbgAccess &d, const int8_t *__restrict__ row, int64_t k, int64_t n,
+                                         const int8_t *base, const int8_t *end) {
     const int8_t *p = row + k;
     if (k + 8 <= n) {
         if constexpr (VEC) {
-            return __ldg(reinterpret_cast<const uint2 *>(p));
+            return load_const(d, reinterpret_cast<const uint2 *>(p));
         } else {
             const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p) & 3u);
             const int8_t *q = p - off;
             if (q >= base && q + (off ? 12 : 8) <= end) {
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
-                const uint32_t a = __ldg(w), b = __ldg(w + 1), c = off ? __ldg(w + 2) : 0u;
-                return make_uint2(__funnelshift_r(a, b, 8 * off), __funnelshift_r(b, c, 8 * off));
+                const uint32_t w0 = load_const(d, w), w1 = load_const(d, w + 1), w2 = off ? load_const(d, w + 2) : 0u;
+                return make_uint2(__funnelshift_r(w0, w1, 8 * off), __funnelshift_r(w1, w2, 8 * off));
             }
         }
     }
     uint32_t r[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (k + i < n) r[i >> 2] |= uint32_t(uint8_t(p[i])) << (8 * (i & 3));
+        if (k + i < n) r[i >> 2] |= uint32_t(uint8_t(load_global(d, p + i))) << (8 * (i & 3));
     return make_uint2(r[0], r[1]);
 }
 
@@ -405,14 +404,14 @@ stream_prepare_kernel(I8Args p, int64_t Kp, int copies, __half *__restrict__ tok
         for (int j = 0; j < 2; ++j) {
             uint32_t c;                                        // past the end: the last one again
             const int64_t r = item_row(min(i + 256 * j, items - 1), per, small, c);
-            w[j] = load_k8<VEC>(p.A + r * p.lda, int64_t(c) * 8, p.K, p.A, p.a_end);
+            w[j] = load_k8<VEC>(p, p.A + r * p.lda, int64_t(c) * 8, p.K, p.A, p.a_end);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (i + 256 * j >= items) continue;
             const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
             const uint4 h = make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
-            for (int64_t c = 0; c < copies; ++c) *reinterpret_cast<uint4 *>(tokens + (i + 256 * j + c * items) * 8) = h;
+            for (int64_t c = 0; c < copies; ++c) store_global(p, reinterpret_cast<uint4 *>(tokens + (i + 256 * j + c * items) * 8), h);
         }
     }
     if constexpr (COPY) {
@@ -425,11 +424,11 @@ stream_prepare_kernel(I8Args p, int64_t Kp, int copies, __half *__restrict__ tok
             for (int j = 0; j < 2; ++j) {
                 uint32_t c;
                 const int64_t r = item_row(min(i + 256 * j, chunks - 1), per16, few, c);
-                w[j] = load_k16<false>(p.B + r * p.ldb, int64_t(c) * 16, p.K, p.B, p.b_end);
+                w[j] = load_k16<false>(p, p.B + r * p.ldb, int64_t(c) * 16, p.K, p.B, p.b_end);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (i + 256 * j < chunks) reinterpret_cast<uint4 *>(copy)[i + 256 * j] = w[j];
+                if (i + 256 * j < chunks) store_global(p, reinterpret_cast<uint4 *>(copy) + i + 256 * j, w[j]);
         }
     }
 }
@@ -443,6 +442,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
     __shared__ uint64_t w_full[T::W_STAGES], w_empty[T::W_STAGES];
     __shared__ uint64_t ready[T::T_STAGES], used[T::T_STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
+    if (!REPOPS_DBG_SMEM_OK(T::SMEM, status)) return;
     uint8_t *w_ring = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u), *t_ring = w_ring + T::W_STAGES * T::W_BYTES;
     // from a shuffle the compiler knows that a warp's role is uniform: a product
     // is then issued in its own time, not in the 111 cycles that a branch it must
@@ -619,10 +619,10 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
             sm.order.at(t, tok, ch);
             const int64_t n = int64_t(ch) * BM + 32 * (warp & 3) + lane, m0 = int64_t(tok) * BT + half * T::COLS;
             const int64_t nn = min(n, p.N - 1);                // past the end: not stored
-            const float sb = __ldg(p.sb + nn), bias = p.bias ? __ldg(p.bias + nn) : 0.0f;
+            const float sb = load_const(p, p.sb + nn), bias = p.bias ? load_const(p, p.bias + nn) : 0.0f;
             float sa[T::COLS / 32];
 #pragma unroll
-            for (int i = 0; i < T::COLS / 32; ++i) sa[i] = __ldg(p.sa + min(m0 + 32 * i + lane, p.M - 1));
+            for (int i = 0; i < T::COLS / 32; ++i) sa[i] = load_const(p, p.sa + min(m0 + 32 * i + lane, p.M - 1));
             int acc[T::COLS];
 #pragma unroll
             for (int i = 0; i < T::COLS; ++i) acc[i] = 0;
@@ -663,7 +663,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
                 float v = __fmul_rn(__fmul_rn(__int2float_rn(acc[i]), __shfl_sync(0xffffffffu, sa[i / 32], i % 32)), sb);
                 const float w = __fadd_rn(v, bias);
                 v = add ? w : v;
-                if (i < rows) store_c<TY>(out, 0, v);
+                if (i < rows) store_c<TY>(p, out, 0, v);
                 out += p.ldc;
             }
         }
@@ -678,8 +678,8 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t nn = min(n + i, p.N - 1);
-            sb[i] = __ldg(p.sb + nn);
-            bias[i] = p.bias ? __ldg(p.bias + nn) : 0.0f;
+            sb[i] = load_const(p, p.sb + nn);
+            bias[i] = p.bias ? load_const(p, p.bias + nn) : 0.0f;
         }
         __syncwarp();
         cluster_sync();
@@ -689,7 +689,7 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 if (r < sm.parts) v[r] = load_cluster16(cluster_addr(w_ring, uint32_t(r)) + at);
-            const float sa = __ldg(p.sa + m0 + i);
+            const float sa = load_const(p, p.sa + m0 + i);
             int4 a = v[0];
 #pragma unroll
             for (int r = 1; r < 8; ++r)
@@ -703,14 +703,15 @@ gemm_i8_stream_kernel(const __grid_constant__ CUtensorMap map_t, const __grid_co
             const int64_t o = (m0 + i) * p.ldc + n;
             if (c_vec && n + 4 <= p.N) {
                 if constexpr (TY == REPOPS_TYPE_F32)
-                    *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + o) = make_float4(f[0], f[1], f[2], f[3]);
+                    store_global(p, reinterpret_cast<float4 *>(static_cast<float *>(p.C) + o),
+                                 make_float4(f[0], f[1], f[2], f[3]));
                 else
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + o) =
-                        make_uint2(pack_c<TY>(f[0], f[1]), pack_c<TY>(f[2], f[3]));
+                    store_global(p, reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + o),
+                                 make_uint2(pack_c<TY>(f[0], f[1]), pack_c<TY>(f[2], f[3])));
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n + j < p.N) store_c<TY>(p.C, o + j, f[j]);
+                    if (n + j < p.N) store_c<TY>(p, p.C, o + j, f[j]);
             }
         }
         __syncwarp();
@@ -758,15 +759,15 @@ __global__ void __launch_bounds__(256) widen_kernel(I8Args p, int64_t Kp, __half
             const int64_t it = min(i0 + 256 * j, items - 1);       // past the end: the last one again
             const int64_t r = items <= UINT32_MAX ? uint32_t(it) / per : it / per;
             const int64_t k = (it - r * per) * 8;
-            w[j] = r < p.M ? load_k8<VEC>(p.A + r * p.lda, k, p.K, p.A, p.a_end)
-                           : load_k8<VEC>(p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
+            w[j] = r < p.M ? load_k8<VEC>(p, p.A + r * p.lda, k, p.K, p.A, p.a_end)
+                           : load_k8<VEC>(p, p.B + (r - p.M) * p.ldb, k, p.K, p.B, p.b_end);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (i0 + 256 * j >= items) continue;
             const uint32_t a = w[j].x ^ 0x80808080u, b = w[j].y ^ 0x80808080u;
-            *reinterpret_cast<uint4 *>(out + (i0 + 256 * j) * 8) =
-                make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u));
+            store_global(p, reinterpret_cast<uint4 *>(out + (i0 + 256 * j) * 8),
+                         make_uint4(widen2(a, 0x4140u), widen2(a, 0x4342u), widen2(b, 0x4140u), widen2(b, 0x4342u)));
         }
     }
 }
@@ -828,7 +829,7 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const CUtensorMap *m
 #pragma unroll 8
                 for (int r = 0; r < 32; ++r) {
                     const E v = e[(r * 8 + ((c / PER) ^ (r & 7))) * PER + c % PER];
-                    if (mine && r < rows) out[r * p.ldc] = v;
+                    if (mine && r < rows) store_global(p, out + r * p.ldc, v);
                 }
             }
             __syncwarp();
@@ -845,6 +846,7 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[T::STAGES], empty[T::STAGES], acc_full[2], acc_empty[2], drained;
     __shared__ uint32_t tmem_slot;
+    if (!REPOPS_DBG_SMEM_OK(T::SMEM, status)) return;
     uint8_t *stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -971,13 +973,13 @@ gemm_i8_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_cons
             tm.at(t, tile_m, tile_n);
             const int64_t row0 = (int64_t(tile_m) * 2 + rank) * BM + 32 * (warp & 3),
                           col0 = int64_t(tile_n) * T::BN + half * T::COLS;
-            const float sa = __ldg(p.sa + min(row0 + lane, p.M - 1));
+            const float sa = load_const(p, p.sa + min(row0 + lane, p.M - 1));
             float sb[T::COLS / 32], bias[T::COLS / 32];
 #pragma unroll
             for (int i = 0; i < T::COLS / 32; ++i) {
                 const int64_t col = min(col0 + 32 * i + lane, p.N - 1);    // past the end: not stored
-                sb[i] = __ldg(p.sb + col);
-                bias[i] = p.bias ? __ldg(p.bias + col) : 0.0f;
+                sb[i] = load_const(p, p.sb + col);
+                bias[i] = p.bias ? load_const(p, p.bias + col) : 0.0f;
             }
             int acc[T::COLS];
 #pragma unroll
@@ -1334,8 +1336,18 @@ extern "C" int repops_gemm_i8(int config, int64_t M, int64_t N, int64_t K, const
     }
     __half *wide = static_cast<__half *>(ws ? ws : own);
     int8_t *copy = ws && own ? static_cast<int8_t *>(own) : reinterpret_cast<int8_t *>(wide + need / 2);
-    const I8Args a{M, N, K, A, B, lda, ldb, a_scale, b_scale, bias, C, ldc, A + ab, B + bb};
-    int rc = typeC == REPOPS_TYPE_F32   ? run_i8<REPOPS_TYPE_F32>(config, a, wide, copy, stream)
+    I8Args a{{}, M, N, K, A, B, lda, ldb, a_scale, b_scale, bias, C, ldc, A + ab, B + bb};
+    a.reads_words(A, ab);
+    a.reads_words(B, bb);
+    a.reads(a_scale, sab);
+    a.reads(b_scale, sbb);
+    a.reads(bias, sbb);
+    a.writes(C, cb);
+    a.writes(wide, need);
+    a.writes(copy, all - need);
+    int rc = a.arm();
+    if (rc == REPOPS_OK)
+        rc = typeC == REPOPS_TYPE_F32   ? run_i8<REPOPS_TYPE_F32>(config, a, wide, copy, stream)
              : typeC == REPOPS_TYPE_F16 ? run_i8<REPOPS_TYPE_F16>(config, a, wide, copy, stream)
                                         : run_i8<REPOPS_TYPE_BF16>(config, a, wide, copy, stream);
     if (own) {

@@ -94,6 +94,45 @@ __device__ __forceinline__ uint32_t dynamic_smem_bytes() {
     return v;
 }
 
+// The buffers of a call whose kernels have many operands: what they may read and
+// what they may write (and read).  A kernel's argument struct derives from it;
+// empty in the release build.
+struct DbgAccess {
+#ifdef REPOPS_DEBUG_BOUNDS
+    static constexpr int kMost = 12;
+    DbgSpan read_only[kMost], written[kMost];
+    int reads_n = 0, writes_n = 0;
+    unsigned *status = nullptr;      // none: nothing is tested
+    void reads(const void *p, uint64_t bytes) {
+        if (p && bytes) read_only[reads_n++] = dbg_span(p, bytes);
+    }
+    // Bytes that kernels take by aligned words holding at least one of them.
+    void reads_words(const void *p, uint64_t bytes) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = (lo + bytes + 3) / 4 * 4;
+        reads(reinterpret_cast<const void *>(lo / 4 * 4), p && bytes ? hi - lo / 4 * 4 : 0);
+    }
+    void writes(void *p, uint64_t bytes) {
+        if (p && bytes) written[writes_n++] = dbg_span(p, bytes);
+    }
+    int arm() { return status_word_address(&status); }
+    __host__ __device__ static bool holds(const DbgSpan *s, int n, const void *p, uint32_t bytes) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        for (int i = 0; i < n; ++i)
+            if (a >= s[i].lo && a <= s[i].hi && bytes <= s[i].hi - a) return true;
+        return false;
+    }
+    __host__ __device__ bool may_write(const void *p, uint32_t bytes) const { return holds(written, writes_n, p, bytes); }
+    __host__ __device__ bool may_read(const void *p, uint32_t bytes) const {
+        return holds(read_only, reads_n, p, bytes) || may_write(p, bytes);
+    }
+#else
+    void reads(const void *, uint64_t) {}
+    void reads_words(const void *, uint64_t) {}
+    void writes(void *, uint64_t) {}
+    int arm() { return REPOPS_OK; }
+#endif
+};
+
 #ifdef REPOPS_DEBUG_BOUNDS
 __device__ __forceinline__ bool dbg_in(const DbgSpan &s, const void *p, uint32_t n, unsigned *status) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
@@ -109,12 +148,43 @@ __device__ __forceinline__ bool dbg_smem(uint64_t need, unsigned *status) {
     if (status && threadIdx.x == 0) atomicOr(status, 2u);
     return false;
 }
+__device__ __forceinline__ bool dbg_access(const DbgAccess &d, const void *p, uint32_t n, bool write) {
+    if (!d.status || (write ? d.may_write(p, n) : d.may_read(p, n))) return true;
+    atomicOr(d.status, 2u);
+    return false;
+}
 #define REPOPS_DBG_OK(span, p, n, status) ::repops::dbg_in((span), (p), (n), (status))
+#define REPOPS_DBG_READ(access, p, n) ::repops::dbg_access((access), (p), (n), false)
+#define REPOPS_DBG_WRITE(access, p, n) ::repops::dbg_access((access), (p), (n), true)
 #define REPOPS_DBG_SMEM_OK(need, status) ::repops::dbg_smem((need), (status))
 #else
 #define REPOPS_DBG_OK(span, p, n, status) true
+#define REPOPS_DBG_READ(access, p, n) true
+#define REPOPS_DBG_WRITE(access, p, n) true
 #define REPOPS_DBG_SMEM_OK(need, status) true
 #endif
+
+// A load or store that the checked build tests (a skipped load gives zeros).
+template <class T>
+__device__ __forceinline__ T load_global(const DbgAccess &d, const T *p) {
+    return REPOPS_DBG_READ(d, p, sizeof(T)) ? *p : T{};
+}
+template <class T>
+__device__ __forceinline__ T load_const(const DbgAccess &d, const T *p) {
+    return REPOPS_DBG_READ(d, p, sizeof(T)) ? __ldg(p) : T{};
+}
+template <class T>
+__device__ __forceinline__ T load_once(const DbgAccess &d, const T *p) {
+    return REPOPS_DBG_READ(d, p, sizeof(T)) ? __ldcs(p) : T{};
+}
+template <class T>
+__device__ __forceinline__ void store_global(const DbgAccess &d, T *p, T v) {
+    if (REPOPS_DBG_WRITE(d, p, sizeof(T))) *p = v;
+}
+template <class T>
+__device__ __forceinline__ void store_once(const DbgAccess &d, T *p, T v) {
+    if (REPOPS_DBG_WRITE(d, p, sizeof(T))) __stcs(p, v);
+}
 
 // A kernel of one call launched behind another of the same call on `stream`:
 // its CTAs may take their places while the earlier kernel ends, and wait there

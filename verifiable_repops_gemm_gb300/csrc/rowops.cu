@@ -1143,7 +1143,11 @@ extern "C" int repops_colsum_f32(int64_t rows, int64_t cols, const float *x, int
             return REPOPS_ERR_ALLOC;
         }
     }
-    int rc = REPOPS_OK;
+    DbgAccess dbg;
+    dbg.reads(x, xb);
+    dbg.writes(y, uint64_t(cols) * 4u);
+    dbg.writes(scratch, uint64_t(need) * uint64_t(cols) * 4u);
+    int rc = dbg.arm();
     const float *in = x;
     int64_t in_rows = rows, in_ld = ldx;
     float *level = scratch;
@@ -1152,7 +1156,7 @@ extern "C" int repops_colsum_f32(int64_t rows, int64_t cols, const float *x, int
         float *out = out_rows == 1 ? y : level;   // every level is packed: pitch cols
         const int gx = int(std::min<int64_t>((cols + 255) / 256, 64));
         const int gy = int(std::min<int64_t>(out_rows, 65535));
-        colsum_pass_kernel<<<dim3(gx, gy), 256, 0, stream>>>(in_rows, cols, in, in_ld, out, cols);
+        colsum_pass_kernel<<<dim3(gx, gy), 256, 0, stream>>>(in_rows, cols, in, in_ld, out, cols, dbg);
         rc = check_launch();
         if (out_rows == 1) break;
         in = out;

@@ -34,26 +34,33 @@ constexpr float kScaleFloor = 0x1p-100f;
 constexpr float kScaleMost = 0x1.020406p+121f;
 
 template <int TY>
-__device__ __forceinline__ float load_one(const void *p, int64_t i) {
-    if constexpr (TY == REPOPS_TYPE_F32) return static_cast<const float *>(p)[i];
-    else if constexpr (TY == REPOPS_TYPE_F16) return __half2float(static_cast<const __half *>(p)[i]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+__device__ __forceinline__ float load_one(const DbgAccess &d, const void *p, int64_t i) {
+    if constexpr (TY == REPOPS_TYPE_F32) return load_global(d, static_cast<const float *>(p) + i);
+    else if constexpr (TY == REPOPS_TYPE_F16) return __half2float(load_global(d, static_cast<const __half *>(p) + i));
+    else return __bfloat162float(load_global(d, static_cast<const __nv_bfloat16 *>(p) + i));
+}
+
+// A value as it is stored: 32 bits, or 16 in the low half.
+template <int TY>
+__device__ __forceinline__ uint32_t narrowed(float v) {
+    if constexpr (TY == REPOPS_TYPE_F32) return __float_as_uint(v);
+    else if constexpr (TY == REPOPS_TYPE_F16) return __half_as_ushort(__float2half_rn(v));
+    else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 template <int TY>
-__device__ __forceinline__ void store_one(void *p, int64_t i, float v) {
-    if constexpr (TY == REPOPS_TYPE_F32) static_cast<float *>(p)[i] = v;
-    else if constexpr (TY == REPOPS_TYPE_F16) static_cast<__half *>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void store_one(const DbgAccess &d, void *p, int64_t i, float v) {
+    if constexpr (TY == REPOPS_TYPE_F32) store_global(d, static_cast<float *>(p) + i, v);
+    else store_global(d, static_cast<uint16_t *>(p) + i, uint16_t(narrowed<TY>(v)));
 }
 
 // Elements i .. i+3, i a multiple of 4 elements from an aligned base.
 template <int TY>
-__device__ __forceinline__ float4 load_four(const void *p, int64_t i) {
+__device__ __forceinline__ float4 load_four(const DbgAccess &d, const void *p, int64_t i) {
     if constexpr (TY == REPOPS_TYPE_F32) {
-        return __ldcs(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
+        return load_once(d, reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
     } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
+        const uint2 w = load_once(d, reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
         if constexpr (TY == REPOPS_TYPE_BF16) {
             return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                                __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
@@ -66,17 +73,12 @@ __device__ __forceinline__ float4 load_four(const void *p, int64_t i) {
 }
 
 template <int TY>
-__device__ __forceinline__ void store_four(void *p, int64_t i, float4 v) {
+__device__ __forceinline__ void store_four(const DbgAccess &d, void *p, int64_t i, float4 v) {
     if constexpr (TY == REPOPS_TYPE_F32) {
-        __stcs(reinterpret_cast<float4 *>(static_cast<float *>(p) + i), v);
+        store_once(d, reinterpret_cast<float4 *>(static_cast<float *>(p) + i), v);
     } else {
-        uint16_t h[4];
-        store_one<TY>(h, 0, v.x);
-        store_one<TY>(h, 1, v.y);
-        store_one<TY>(h, 2, v.z);
-        store_one<TY>(h, 3, v.w);
-        __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i),
-               make_uint2(h[0] | (unsigned(h[1]) << 16), h[2] | (unsigned(h[3]) << 16)));
+        store_once(d, reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i),
+                   make_uint2(narrowed<TY>(v.x) | (narrowed<TY>(v.y) << 16), narrowed<TY>(v.z) | (narrowed<TY>(v.w) << 16)));
     }
 }
 
@@ -121,7 +123,7 @@ __device__ __forceinline__ uint32_t quant4(float4 v, const GroupScale &g) {
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256)
 quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t ldx, int group,
-                       int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale, int64_t lds) {
+                       int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale, int64_t lds, DbgAccess dbg) {
     const int lane = threadIdx.x & 31, lanes = group / 16, l = lane & (lanes - 1);
     const int segs = (cols + 511) / 512;
     const int64_t items = rows * segs, stride = int64_t(gridDim.x) * 8;
@@ -136,13 +138,13 @@ quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64
         for (int j = 0; j < 4; ++j) {
             if constexpr (VEC) {
                 const int c = g0 + 4 * (l + lanes * j);
-                v[j] = load_four<TY>(x, base + (c < cols ? c : safe));
+                v[j] = load_four<TY>(dbg, x, base + (c < cols ? c : safe));
             } else {
                 const int c = g0 + l + 4 * lanes * j;
-                v[j].x = load_one<TY>(x, base + (c < cols ? c : safe));
-                v[j].y = load_one<TY>(x, base + (c + lanes < cols ? c + lanes : safe));
-                v[j].z = load_one<TY>(x, base + (c + 2 * lanes < cols ? c + 2 * lanes : safe));
-                v[j].w = load_one<TY>(x, base + (c + 3 * lanes < cols ? c + 3 * lanes : safe));
+                v[j].x = load_one<TY>(dbg, x, base + (c < cols ? c : safe));
+                v[j].y = load_one<TY>(dbg, x, base + (c + lanes < cols ? c + lanes : safe));
+                v[j].z = load_one<TY>(dbg, x, base + (c + 2 * lanes < cols ? c + 2 * lanes : safe));
+                v[j].w = load_one<TY>(dbg, x, base + (c + 3 * lanes < cols ? c + 3 * lanes : safe));
             }
         }
 #pragma unroll
@@ -155,16 +157,16 @@ quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64
             const uint32_t w = quant4(v[j], gs);
             if constexpr (VEC) {
                 const int c = g0 + 4 * (l + lanes * j);
-                if (c < cols) *reinterpret_cast<uint32_t *>(o + c) = w;
+                if (c < cols) store_global(dbg, reinterpret_cast<uint32_t *>(o + c), w);
             } else {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const int c = g0 + l + lanes * (4 * j + t);
-                    if (c < cols) o[c] = int8_t(w >> (8 * t));
+                    if (c < cols) store_global(dbg, o + c, int8_t(w >> (8 * t)));
                 }
             }
         }
-        if (l == 0 && g0 < cols) scale[r * lds + g0 / group] = gs.scale;
+        if (l == 0 && g0 < cols) store_global(dbg, scale + r * lds + g0 / group, gs.scale);
     }
 }
 
@@ -174,7 +176,7 @@ quantize_groups_kernel(int64_t rows, int cols, const void *__restrict__ x, int64
 template <int TY, bool VEC, int T>
 __global__ void __launch_bounds__(256)
 quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t ldx, int8_t *__restrict__ q,
-                     int64_t ldq, float *__restrict__ scale, int64_t lds) {
+                     int64_t ldq, float *__restrict__ scale, int64_t lds, DbgAccess dbg) {
     constexpr int KEEP = 8, ROWS = 256 / T;
     __shared__ float part[8];
     const int t = threadIdx.x % T;
@@ -187,13 +189,13 @@ quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t
         auto load = [&](int k) {
             if constexpr (VEC) {
                 const int c = 4 * T * k + 4 * t;
-                return load_four<TY>(x, base + (c < cols ? c : 0));
+                return load_four<TY>(dbg, x, base + (c < cols ? c : 0));
             } else {
                 const int c = 4 * T * k + t;
-                return make_float4(load_one<TY>(x, base + (c < cols ? c : 0)),
-                                   load_one<TY>(x, base + (c + T < cols ? c + T : 0)),
-                                   load_one<TY>(x, base + (c + 2 * T < cols ? c + 2 * T : 0)),
-                                   load_one<TY>(x, base + (c + 3 * T < cols ? c + 3 * T : 0)));
+                return make_float4(load_one<TY>(dbg, x, base + (c < cols ? c : 0)),
+                                   load_one<TY>(dbg, x, base + (c + T < cols ? c + T : 0)),
+                                   load_one<TY>(dbg, x, base + (c + 2 * T < cols ? c + 2 * T : 0)),
+                                   load_one<TY>(dbg, x, base + (c + 3 * T < cols ? c + 3 * T : 0)));
             }
         };
         float4 v[KEEP];
@@ -216,18 +218,18 @@ quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t
         }
         if (!live) continue;
         const GroupScale gs = group_scale(m);
-        if (t == 0) scale[r * lds] = gs.scale;
+        if (t == 0) store_global(dbg, scale + r * lds, gs.scale);
         int8_t *o = q + r * ldq;
         auto store = [&](int k, float4 f) {
             const uint32_t w = quant4(f, gs);
             if constexpr (VEC) {
                 const int c = 4 * T * k + 4 * t;
-                if (c < cols) *reinterpret_cast<uint32_t *>(o + c) = w;
+                if (c < cols) store_global(dbg, reinterpret_cast<uint32_t *>(o + c), w);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = 4 * T * k + T * j + t;
-                    if (c < cols) o[c] = int8_t(w >> (8 * j));
+                    if (c < cols) store_global(dbg, o + c, int8_t(w >> (8 * j)));
                 }
             }
         };
@@ -244,7 +246,7 @@ quantize_rows_kernel(int64_t rows, int cols, const void *__restrict__ x, int64_t
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(256)
 dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t ldq,
-                  const float *__restrict__ scale, int64_t lds, int shift, void *__restrict__ x, int64_t ldx) {
+                  const float *__restrict__ scale, int64_t lds, int shift, void *__restrict__ x, int64_t ldx, DbgAccess dbg) {
     const int units = VEC ? cols / 4 : cols;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
         const int8_t *qr = q + r * ldq;
@@ -256,21 +258,22 @@ dequantize_kernel(int64_t rows, int cols, const int8_t *__restrict__ q, int64_t 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t i = i0 + S * j < units ? i0 + S * j : 0;
-                w[j] = VEC ? __ldcs(reinterpret_cast<const uint32_t *>(qr) + i) : uint32_t(uint8_t(__ldg(qr + i)));
-                s[j] = __ldg(sr + ((VEC ? 4 * i : i) >> shift));
+                w[j] = VEC ? load_once(dbg, reinterpret_cast<const uint32_t *>(qr) + i)
+                           : uint32_t(uint8_t(load_const(dbg, qr + i)));
+                s[j] = load_const(dbg, sr + ((VEC ? 4 * i : i) >> shift));
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t i = i0 + S * j;
                 if (i >= units) continue;
-                if constexpr (VEC) store_four<TY>(x, r * ldx + 4 * i, unpack_q4(w[j], s[j]));
-                else store_one<TY>(x, r * ldx + i, unpack_q1(int8_t(w[j]), s[j]));
+                if constexpr (VEC) store_four<TY>(dbg, x, r * ldx + 4 * i, unpack_q4(w[j], s[j]));
+                else store_one<TY>(dbg, x, r * ldx + i, unpack_q1(int8_t(w[j]), s[j]));
             }
         }
     }
 }
 
-struct SwigluArgs {
+struct SwigluArgs : DbgAccess {
     int64_t rows, cols;
     const int8_t *g, *u;
     int64_t ldg, ldu;
@@ -288,38 +291,38 @@ struct SwigluArgs {
 // columns); past the row's end column 0 is read (no branch: the loads are in
 // flight together) and nothing is stored.
 template <bool VEC>
-__device__ __forceinline__ float4 four_q8(const int8_t *q, const float *s, int shift, int c, int n) {
+__device__ __forceinline__ float4 four_q8(const DbgAccess &d, const int8_t *q, const float *s, int shift, int c, int n) {
     if constexpr (VEC) {
-        return unpack_q4(__ldcs(reinterpret_cast<const uint32_t *>(q + c)), __ldg(s + (c >> shift)));
+        return unpack_q4(load_once(d, reinterpret_cast<const uint32_t *>(q + c)), load_const(d, s + (c >> shift)));
     } else {
         float v[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int i = c + int(blockDim.x) * t < n ? c + int(blockDim.x) * t : 0;
-            v[t] = unpack_q1(__ldg(q + i), __ldg(s + (i >> shift)));
+            v[t] = unpack_q1(load_const(d, q + i), load_const(d, s + (i >> shift)));
         }
         return make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ float4 four_f32(const float *p, int c, int n) {
-    if constexpr (VEC) return *reinterpret_cast<const float4 *>(p + c);
+__device__ __forceinline__ float4 four_f32(const DbgAccess &d, const float *p, int c, int n) {
+    if constexpr (VEC) return load_global(d, reinterpret_cast<const float4 *>(p + c));
     const int S = blockDim.x;
-    return make_float4(p[c < n ? c : 0], p[c + S < n ? c + S : 0], p[c + 2 * S < n ? c + 2 * S : 0],
-                       p[c + 3 * S < n ? c + 3 * S : 0]);
+    return make_float4(load_global(d, p + (c < n ? c : 0)), load_global(d, p + (c + S < n ? c + S : 0)),
+                       load_global(d, p + (c + 2 * S < n ? c + 2 * S : 0)), load_global(d, p + (c + 3 * S < n ? c + 3 * S : 0)));
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_four_f32(float *p, int c, int n, float4 v) {
+__device__ __forceinline__ void store_four_f32(const DbgAccess &d, float *p, int c, int n, float4 v) {
     if constexpr (VEC) {
-        *reinterpret_cast<float4 *>(p + c) = v;
+        store_global(d, reinterpret_cast<float4 *>(p + c), v);
     } else {
         const int S = blockDim.x;
-        if (c < n) p[c] = v.x;
-        if (c + S < n) p[c + S] = v.y;
-        if (c + 2 * S < n) p[c + 2 * S] = v.z;
-        if (c + 3 * S < n) p[c + 3 * S] = v.w;
+        if (c < n) store_global(d, p + c, v.x);
+        if (c + S < n) store_global(d, p + c + S, v.y);
+        if (c + 2 * S < n) store_global(d, p + c + 2 * S, v.z);
+        if (c + 3 * S < n) store_global(d, p + c + 3 * S, v.w);
     }
 }
 
@@ -337,19 +340,19 @@ __global__ void __launch_bounds__(256) swiglu_backward_i8_kernel(SwigluArgs p) {
         for (int c0 = blockIdx.x * blockDim.x * 4; c0 < n; c0 += gridDim.x * blockDim.x * 4) {
             const int c = c0 + (VEC ? 4 : 1) * threadIdx.x;
             if (c >= n) continue;
-            const float4 d = four_f32<VEC>(dr, c, n);
-            const float4 a = four_q8<VEC>(gr, gsr, p.shift, c, n), b = four_q8<VEC>(ur, usr, p.shift, c, n);
+            const float4 d = four_f32<VEC>(p, dr, c, n);
+            const float4 a = four_q8<VEC>(p, gr, gsr, p.shift, c, n), b = four_q8<VEC>(p, ur, usr, p.shift, c, n);
             float4 og, ou;
             const float2 s01 = sigmoid_fixed2(a.x, a.y), s23 = sigmoid_fixed2(a.z, a.w);
             swiglu_grad_s(a.x, b.x, d.x, s01.x, og.x, ou.x);
             swiglu_grad_s(a.y, b.y, d.y, s01.y, og.y, ou.y);
             swiglu_grad_s(a.z, b.z, d.z, s23.x, og.z, ou.z);
             swiglu_grad_s(a.w, b.w, d.w, s23.y, og.w, ou.w);
-            store_four_f32<VEC>(dgr, c, n, og);
-            store_four_f32<VEC>(dur, c, n, ou);
+            store_four_f32<VEC>(p, dgr, c, n, og);
+            store_four_f32<VEC>(p, dur, c, n, ou);
             if constexpr (H)
-                store_four_f32<VEC>(hr, c, n, make_float4(swiglu_s(a.x, b.x, s01.x), swiglu_s(a.y, b.y, s01.y),
-                                                          swiglu_s(a.z, b.z, s23.x), swiglu_s(a.w, b.w, s23.y)));
+                store_four_f32<VEC>(p, hr, c, n, make_float4(swiglu_s(a.x, b.x, s01.x), swiglu_s(a.y, b.y, s01.y),
+                                                             swiglu_s(a.z, b.z, s23.x), swiglu_s(a.w, b.w, s23.y)));
         }
     }
 }
@@ -370,22 +373,22 @@ int sm_count() {
 
 template <int TY>
 int launch_quantize(int64_t rows, int cols, const void *x, int64_t ldx, int64_t group, int8_t *q, int64_t ldq,
-                    float *scale, int64_t lds, cudaStream_t s) {
+                    float *scale, int64_t lds, const DbgAccess &dbg, cudaStream_t s) {
     const bool vec = cols % 4 == 0 && aligned(x, ldx, storage_size(TY), 4 * storage_size(TY)) && aligned(q, ldq, 1, 4);
     if (group > 0) {
         const int64_t items = rows * ((int64_t(cols) + 511) / 512);
         const unsigned grid = unsigned(std::min<int64_t>((items + 7) / 8, int64_t(sm_count()) * 32));
         if (vec)
-            quantize_groups_kernel<TY, true><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds);
+            quantize_groups_kernel<TY, true><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds, dbg);
         else
-            quantize_groups_kernel<TY, false><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds);
+            quantize_groups_kernel<TY, false><<<grid, 256, 0, s>>>(rows, cols, x, ldx, int(group), q, ldq, scale, lds, dbg);
         return check_launch();
     }
     // as few threads a row as hold it in registers
     auto go = [&](auto kv, auto ks, int T) {
         const unsigned grid = unsigned(std::min<int64_t>((rows + 256 / T - 1) / (256 / T), int64_t(sm_count()) * 32));
-        if (vec) kv<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
-        else ks<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds);
+        if (vec) kv<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds, dbg);
+        else ks<<<grid, 256, 0, s>>>(rows, cols, x, ldx, q, ldq, scale, lds, dbg);
         return check_launch();
     };
     if (cols <= 1024) return go(quantize_rows_kernel<TY, true, 32>, quantize_rows_kernel<TY, false, 32>, 32);
@@ -396,13 +399,13 @@ int launch_quantize(int64_t rows, int cols, const void *x, int64_t ldx, int64_t 
 
 template <int TY>
 int launch_dequantize(int64_t rows, int cols, const int8_t *q, int64_t ldq, const float *scale, int64_t lds, int shift,
-                      void *x, int64_t ldx, cudaStream_t s) {
+                      void *x, int64_t ldx, const DbgAccess &dbg, cudaStream_t s) {
     const bool vec = cols % 4 == 0 && aligned(x, ldx, storage_size(TY), 4 * storage_size(TY)) && aligned(q, ldq, 1, 4);
     const int64_t units = vec ? cols / 4 : cols;
     const unsigned threads = row_threads(units);
     const dim3 grid(unsigned((units + 4 * threads - 1) / (4 * threads)), unsigned(std::min<int64_t>(rows, 65535)));
-    if (vec) dequantize_kernel<TY, true><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
-    else dequantize_kernel<TY, false><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx);
+    if (vec) dequantize_kernel<TY, true><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx, dbg);
+    else dequantize_kernel<TY, false><<<grid, threads, 0, s>>>(rows, cols, q, ldq, scale, lds, shift, x, ldx, dbg);
     return check_launch();
 }
 
@@ -425,13 +428,18 @@ extern "C" int repops_quantize_rows_i8(int64_t rows, int64_t cols, const void *x
         return REPOPS_ERR_INVALID_ARG;
     if (ranges_overlap(q, qb, x, xb) || ranges_overlap(scale, sb, x, xb) || ranges_overlap(q, qb, scale, sb))
         return REPOPS_ERR_ALIAS;
+    DbgAccess dbg;
+    dbg.reads(x, xb);
+    dbg.writes(q, qb);
+    dbg.writes(scale, sb);
+    if (const int rc = dbg.arm(); rc != REPOPS_OK) return rc;
     switch (x_type) {
         case REPOPS_TYPE_F32:
-            return launch_quantize<REPOPS_TYPE_F32>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_F32>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, dbg, stream);
         case REPOPS_TYPE_F16:
-            return launch_quantize<REPOPS_TYPE_F16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_F16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, dbg, stream);
         default:
-            return launch_quantize<REPOPS_TYPE_BF16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, stream);
+            return launch_quantize<REPOPS_TYPE_BF16>(rows, int(cols), x, ldx, group, q, ldq, scale, lds, dbg, stream);
     }
 }
 
@@ -448,13 +456,18 @@ extern "C" int repops_dequantize_rows_i8(int64_t rows, int64_t cols, const int8_
         return REPOPS_ERR_INVALID_ARG;
     if (ranges_overlap(x, xb, q, qb) || ranges_overlap(x, xb, scale, sb)) return REPOPS_ERR_ALIAS;
     const int shift = group_shift(group);
+    DbgAccess dbg;
+    dbg.reads(q, qb);
+    dbg.reads(scale, sb);
+    dbg.writes(x, xb);
+    if (const int rc = dbg.arm(); rc != REPOPS_OK) return rc;
     switch (x_type) {
         case REPOPS_TYPE_F32:
-            return launch_dequantize<REPOPS_TYPE_F32>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_F32>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, dbg, stream);
         case REPOPS_TYPE_F16:
-            return launch_dequantize<REPOPS_TYPE_F16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_F16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, dbg, stream);
         default:
-            return launch_dequantize<REPOPS_TYPE_BF16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, stream);
+            return launch_dequantize<REPOPS_TYPE_BF16>(rows, int(cols), q, ldq, scale, lds, shift, x, ldx, dbg, stream);
     }
 }
 
@@ -487,8 +500,17 @@ extern "C" int repops_swiglu_backward_i8(int64_t rows, int64_t cols, const int8_
             if (outs[j].p && blocks_overlap(outs[i].p, outs[i].ld, outs[j].p, outs[j].ld, rows, cols))
                 return REPOPS_ERR_ALIAS;
     }
-    const SwigluArgs a{rows, cols, g, u, ldg, ldu, g_scale, u_scale, ldgs, ldus, group_shift(group), dh, lddh,
-                       dg, du, h, lddg, lddu, ldh};
+    SwigluArgs a{{}, rows, cols, g, u, ldg, ldu, g_scale, u_scale, ldgs, ldus, group_shift(group), dh, lddh,
+                 dg, du, h, lddg, lddu, ldh};
+    a.reads(g, gb);
+    a.reads(u, ub);
+    a.reads(g_scale, gsb);
+    a.reads(u_scale, usb);
+    a.reads(dh, db);
+    a.writes(dg, ogb);
+    a.writes(du, oub);
+    a.writes(h, hb);
+    if (const int rc = a.arm(); rc != REPOPS_OK) return rc;
     const bool vec = cols % 4 == 0 && aligned(g, ldg, 1, 4) && aligned(u, ldu, 1, 4) && aligned(dh, lddh, 4, 16) &&
                      aligned(dg, lddg, 4, 16) && aligned(du, lddu, 4, 16) && (!h || aligned(h, ldh, 4, 16));
     const unsigned threads = row_threads(cols);

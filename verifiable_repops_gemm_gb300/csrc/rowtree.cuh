@@ -82,15 +82,15 @@ __device__ float generic_reduce_idx(int64_t n, F f, float *buf, float *buf2, flo
 // (coalesced), the grid's y dimension along q.
 [[maybe_unused]] __global__ void __launch_bounds__(256)
 colsum_pass_kernel(int64_t rows, int64_t cols, const float *__restrict__ x, int64_t ldx, float *__restrict__ out,
-                   int64_t ldo) {
+                   int64_t ldo, DbgAccess dbg) {
     const int64_t groups = (rows + RUN - 1) / RUN;
     for (int64_t q = blockIdx.y; q < groups; q += gridDim.y) {
         const int64_t r0 = q * RUN, r1 = imin64(r0 + RUN, rows);
         for (int64_t j = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; j < cols;
              j += int64_t(gridDim.x) * blockDim.x) {
-            float acc = x[r0 * ldx + j];
-            for (int64_t i = r0 + 1; i < r1; ++i) acc = __fadd_rn(acc, x[i * ldx + j]);
-            out[q * ldo + j] = acc;
+            float acc = load_global(dbg, x + r0 * ldx + j);
+            for (int64_t i = r0 + 1; i < r1; ++i) acc = __fadd_rn(acc, load_global(dbg, x + i * ldx + j));
+            store_global(dbg, out + q * ldo + j, acc);
         }
     }
 }
