@@ -76,3 +76,39 @@ def test_few_row_kernel_with_many_tokens(rp, K):
     want = (a.double() @ b.double().t()).float() * sa[:, None] * sb
     assert torch.equal(y, want)
     assert torch.equal(rp.gemm_i8(a, b.t(), sa, sb), want)
+
+
+@pytest.mark.parametrize("offset", [0, 3])
+def test_scratch_from_the_pool_also_within_a_captured_graph(rp, offset):
+    """A raw stream handle takes all scratch from the library's pool; a caller's
+    that holds the tokens alone only the copy of unaligned weights."""
+    M, N, K = 40, 300, 640
+    L = rp.load()
+    a, b = ints((M, K), 7), ints((N, K + 16), 8)[:, offset:offset + K]
+    sa, sb = torch.rand(M, device=DEV) + 0.5, torch.rand(N, device=DEV) + 0.5
+    want = rp.gemm_i8(a, b.t(), sa, sb, config=0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for config in (1, 2):
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        rp.gemm_i8(a, b.t(), sa, sb, out=out, config=config, stream=side.cuda_stream)
+        side.synchronize()
+        assert torch.equal(out, want)
+    size = L.repops_gemm_i8_workspace_bytes(1, M, N, K)
+    graphs = []
+    for with_ws in (True, False):
+        out, ws = torch.zeros_like(want), torch.empty(size, dtype=torch.uint8, device=DEV)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            rc = L.repops_gemm_i8(1, M, N, K, a.data_ptr(), K, sa.data_ptr(), b.data_ptr(), b.stride(0), sb.data_ptr(), None,
+                                  out.data_ptr(), rp.TYPE_F32, N, ws.data_ptr() if with_ws else None,
+                                  size if with_ws else 0, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        graphs.append((gr, out, ws))
+    for _ in range(3):
+        for gr, out, _ in graphs:
+            out.zero_()
+            gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for _, out, _ in graphs)
