@@ -3,7 +3,10 @@
 Python binding of librepops (include/repops.h): the functions here only
 marshal torch CUDA tensors into pointers, sizes and strides and call the C ABI;
 every operation runs in the library's CUDA kernels.  PyTorch provides device
-memory and streams.
+memory and streams.  A call runs on the current stream, or on `stream` (a
+torch.cuda.Stream or a raw handle); results it allocates are the current
+stream's memory either way, as torch's own are, so another stream is ordered
+after the current one first, or given `out`.
 
   gemm(A, B)                        order-fixed FP32 GEMM
                                     ("Verde与RepOps" §3.2, matmul example)
