@@ -1101,6 +1101,69 @@ int repops_rmsnorm_residual_backward_f32(
     float eps, float *dx, int64_t lddx, float *df, int64_t lddf, float *dpre, float *dpost,
     float *dgate, int64_t lddgate, void *ws, uint64_t ws_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* AdamW over many tensors                                                   */
+/* "Zoo Per-LLM Chain Soundness" §2 and §5 (the fixed-order mean over the    */
+/* contributors, then the update); the pages' update is plain SGD and fixes  */
+/* no other optimiser: this is AdamW (Loshchilov and Hutter) in its place.   */
+/* ------------------------------------------------------------------------ */
+
+#define REPOPS_ADAMW_GROUP 128   /* elements that share a scale in 8-bit moments */
+
+/* The four words of a step that change from one to the next, on the host (no
+ * launch): the binary32 values of lr, lr / (1 - beta1^step) and
+ * 1 / sqrt(1 - beta2^step), computed in binary64, and the key of the step's
+ * dither, fmix32(0x9E3779B9 * step + seed).  step >= 1, 0 <= beta < 1. */
+int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, uint32_t seed,
+                         uint32_t *scalars);
+
+/* One step of `tensors` tensors, in place.  Tensor i has sizes[i] elements
+ * (0 is fine): theta[i] binary32; contributor c's gradient
+ * grads[i*contributors + c], stored as grad_type; m[i] and v[i] binary32, or,
+ * with m_scale and v_scale, one byte an element and one scale byte for every
+ * REPOPS_ADAMW_GROUP of them (the last group may be shorter).  The arrays
+ * themselves (sizes, theta, ..., decay: one weight decay a tensor, NULL for
+ * none) are host memory, what they point to is device memory, each of any
+ * alignment.  scalars: of repops_adamw_scalars, on the host, or with
+ * scalars_on_device != 0 on the device (read by the kernels, so that a captured
+ * graph can be replayed for step after step).  grad_scale: a device float that
+ * multiplies the mean gradient (clipping), or NULL.
+ * Every step one binary32 rounding, c1 = fl(1 - beta1), c2 = fl(1 - beta2),
+ * (lr, s, b) = scalars:
+ *   g = the fold of the gradients in `order` divided by their count, as
+ *       repops_fixed_order_mean_sgd;  g = fl(g * *grad_scale) with grad_scale
+ *   m = fl(fl(m * beta1) + fl(g * c1)),  v = fl(fl(v * beta2) + fl(fl(g*g) * c2))
+ *   r = fl(sqrt(v)),  u = fl(m / fl(fl(r * b) + eps))
+ *   theta = fl(fl(theta * fl(1 - fl(decay * lr))) - fl(u * s))
+ * 8-bit moments hold m and r (v is then fl(r * r) of what is kept):
+ *   m: e4m3 (bias 7, as the OCP 8-bit formats), r: E4M4 without a sign (bias 15:
+ *   code >> 4 the exponent, code & 15 the mantissa, subnormals below 16), both
+ *   times 2^(scale byte - 127); scale byte 0 stands for zeros, so zeroed memory
+ *   is a valid start.  The scale byte is the least (>= 1) under which the group's
+ *   largest magnitude is at most 448 (m) or 1.9375 (r); a group with an infinity
+ *   or a NaN gets 255 and codes 0, and counts as NaN.  A code is the value's
+ *   magnitude cut off after 3 (4) bits of mantissa, rounded up where the cut-off
+ *   part plus a dither reaches a whole code: h = fmix32(element * 0x9E3779B1 +
+ *   fmix32(scalars[3] + 0x9E3779B9 * (i + 1))) in 32 bits, of which the low half
+ *   (m) or the high half (r) plus 1/2 is the dither in units of 2^-16 of a code;
+ *   a root that is not zero (times its scale and 2^-112 in binary32) keeps a code
+ *   of at least 1.  (fmix32: MurmurHash3's finaliser.)
+ * No two tensors may share memory, nor a written tensor a gradient (ALIAS); one
+ * gradient may serve several contributors.  ORDER for an order that is not a
+ * permutation; INVALID_ARG for null pointers, unknown types, betas outside
+ * [0, 1), eps < 0, sizes above 2^40. */
+int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
+                 const void *const *grads, int grad_type, const int *order, void *const *m,
+                 void *const *v, uint8_t *const *m_scale, uint8_t *const *v_scale,
+                 const float *decay, double beta1, double beta2, double eps,
+                 const uint32_t *scalars, int scalars_on_device, const float *grad_scale,
+                 cudaStream_t stream);
+
+/* The binary32 m and v = fl(r * r) that n elements of 8-bit moments stand for.
+ * m_out and v_out must not overlap each other or an input (ALIAS). */
+int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *m_scale,
+                         const uint8_t *v_scale, float *m_out, float *v_out, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,6 +44,7 @@ after the current one first, or given `out`.
   host_empty(shape, dtype)          page-locked host memory in huge pages for the
                                     host-buffer calls (gemm_host, ..._host)
 """
+import array
 import ctypes
 import functools
 
@@ -1298,3 +1299,150 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
     if rc:
         _capi.check(rc, "repops_rmsnorm_residual_backward_f32")
     return dx, df, dpre, dpost, dgate
+
+
+ADAMW_GROUP = 128   # elements that share a scale in 8-bit moments
+
+
+def _tensor_list(ts, dtype, here, name):
+    """A list of contiguous tensors of one dtype on the current device (a single
+    tensor is a list of one)."""
+    import torch
+    if isinstance(ts, torch.Tensor):
+        ts = (ts,)
+    for t in ts:
+        if t.dtype != dtype or t.get_device() != here or not t.is_contiguous():
+            raise ValueError("%s must be contiguous %s tensors on the current CUDA device (%d)" % (name, dtype, here))
+    return ts
+
+
+def _pointers(ts):
+    return array.array("Q", [t.data_ptr() for t in ts])
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
+
+
+def adamw_scalars(step: int, lr: float, betas=(0.9, 0.999), seed: int = 0):
+    """The four words of an AdamW step that change from one to the next, as a
+    pinned int32 CPU tensor (repops_adamw_scalars): copied into a CUDA tensor and
+    given to adamw(scalars=), they let a captured graph be replayed for step after
+    step."""
+    import torch
+    out = torch.empty(4, dtype=torch.int32, pin_memory=torch.cuda.is_available())
+    _capi.check(load().repops_adamw_scalars(int(step), lr, betas[0], betas[1], int(seed) & 0xFFFFFFFF, out.data_ptr()),
+                "repops_adamw_scalars")
+    return out
+
+
+def adamw_state(params, bits: int = 32) -> dict:
+    """Zero moments of adamw() for a list of parameters (or one), as its keyword
+    arguments: m and v, with bits=8 in a byte each and m_scales, v_scales for
+    every ADAMW_GROUP elements of a tensor."""
+    import torch
+    if isinstance(params, torch.Tensor):
+        params = [params]
+    if bits == 32:
+        return {k: [torch.zeros_like(p) for p in params] for k in ("m", "v")}
+    if bits != 8:
+        raise ValueError("bits must be 32 or 8")
+
+    def zeros(n, p):
+        return torch.zeros(n, dtype=torch.uint8, device=p.device)
+
+    out = {k: [zeros(p.numel(), p) for p in params] for k in ("m", "v")}
+    out.update({k: [zeros(-(-p.numel() // ADAMW_GROUP), p) for p in params] for k in ("m_scales", "v_scales")})
+    return out
+
+
+def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9, 0.999), eps: float = 1e-8,
+          weight_decay=0.0, order=None, m_scales=None, v_scales=None, seed: int = 0, scalars=None, grad_scale=None,
+          stream=None):
+    """One AdamW step over a list of tensors at once, in place (repops_adamw).
+
+    theta: float32 CUDA tensors, contiguous.  grads: a list of gradients shaped
+    like them (float32, float16 or bfloat16), or one such list for each of several
+    contributors, whose left fold in `order` (default: as given) divided by their
+    count is the gradient.  m, v: the moments (adamw_state), float32, or uint8 with
+    m_scales and v_scales.  weight_decay: a number, or one for each tensor.
+    step counts from 1; with seed it also keys the rounding of 8-bit moments.
+    scalars: a CUDA tensor of adamw_scalars' words instead of step and lr.
+    grad_scale: a float32 CUDA tensor of one value that multiplies the gradient."""
+    import torch
+    here = torch.cuda.current_device()
+    theta = _tensor_list(theta, torch.float32, here, "theta")
+    n = len(theta)
+    if isinstance(grads, torch.Tensor) or not len(grads) or isinstance(grads[0], torch.Tensor):
+        grads = [grads]
+    first = grads[0]
+    first = first if isinstance(first, torch.Tensor) else first[0] if len(first) else None
+    gtype = torch.float32 if first is None else first.dtype
+    kind = _storage_type(gtype)
+    grads = [_tensor_list(g, gtype, here, "grads") for g in grads]
+    eight = m_scales is not None or v_scales is not None
+    kept = torch.uint8 if eight else torch.float32
+    m, v = _tensor_list(m, kept, here, "m"), _tensor_list(v, kept, here, "v")
+    sizes = [t.numel() for t in theta]
+    for what, ts in (("grads", grads), ("m", (m,)), ("v", (v,))):
+        for t in ts:
+            if [x.numel() for x in t] != sizes:
+                raise ValueError("%s must have one tensor of each of theta's sizes" % what)
+    scale_ptrs = [None, None]
+    if eight:
+        groups = [-(-k // ADAMW_GROUP) for k in sizes]
+        for i, ts in enumerate((m_scales, v_scales)):
+            ts = _tensor_list(() if ts is None else ts, torch.uint8, here, "scales")
+            if [x.numel() for x in ts] != groups:
+                raise ValueError("m_scales and v_scales must have one byte for every %d elements" % ADAMW_GROUP)
+            scale_ptrs[i] = _pointers(ts)
+    decay = array.array("f", [weight_decay] * n if isinstance(weight_decay, (int, float)) else weight_decay)
+    if len(decay) != n:
+        raise ValueError("weight_decay must be a number or one for each tensor")
+    order = array.array("i", range(len(grads)) if order is None else order)
+    if len(order) != len(grads):
+        raise ValueError("order must have one entry per contributor")
+    L = load()
+    if scalars is None:
+        if step is None or lr is None:
+            raise ValueError("step and lr, or scalars, must be given")
+        words = (ctypes.c_uint32 * 4)()
+        _capi.check(L.repops_adamw_scalars(int(step), lr, betas[0], betas[1], int(seed) & 0xFFFFFFFF, words),
+                    "repops_adamw_scalars")
+    elif scalars.numel() != 4 or scalars.element_size() != 4 or not scalars.is_contiguous():
+        raise ValueError("scalars must be a CUDA tensor of adamw_scalars' four words")
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1):
+        raise ValueError("grad_scale must be a float32 CUDA tensor of one value")
+    handle = _stream_on_device(stream, scalars, grad_scale)
+    if len(grads) == 1:
+        gp = _pointers(grads[0])
+    else:
+        gp = array.array("Q", [t.data_ptr() for ts in zip(*grads) for t in ts])
+    sizes, tp, mp, vp = array.array("q", sizes), _pointers(theta), _pointers(m), _pointers(v)
+    rc = L.repops_adamw(n, _address(sizes), _address(tp), len(grads), _address(gp), kind, _address(order), _address(mp),
+                        _address(vp), _address(scale_ptrs[0]), _address(scale_ptrs[1]), _address(decay), betas[0],
+                        betas[1], eps, ctypes.addressof(words) if scalars is None else scalars.data_ptr(),
+                        int(scalars is not None), None if grad_scale is None else grad_scale.data_ptr(), handle)
+    if rc:
+        _capi.check(rc, "repops_adamw")
+
+
+def adamw_moments(m, v, m_scale, v_scale, *, m_out=None, v_out=None, stream=None):
+    """(m, v) as the float32 values that a tensor's 8-bit moments stand for
+    (repops_adamw_moments)."""
+    import torch
+    here = torch.cuda.current_device()
+    n = m.numel()
+    m, v, m_scale, v_scale = (_tensor_list(t, torch.uint8, here, "moments and scales")[0]
+                              for t in (m, v, m_scale, v_scale))
+    if v.numel() != n or m_scale.numel() != -(-n // ADAMW_GROUP) or v_scale.numel() != m_scale.numel():
+        raise ValueError("m and v need one size, the scales one byte for every %d elements" % ADAMW_GROUP)
+    m_out, v_out = (torch.empty(m.shape, dtype=torch.float32, device=m.device) if t is None else
+                    _tensor_list(t, torch.float32, here, "m_out and v_out")[0] for t in (m_out, v_out))
+    if m_out.numel() != n or v_out.numel() != n:
+        raise ValueError("m_out and v_out must have m's size")
+    rc = load().repops_adamw_moments(n, m.data_ptr(), v.data_ptr(), m_scale.data_ptr(), v_scale.data_ptr(),
+                                     m_out.data_ptr(), v_out.data_ptr(), _stream_on_device(stream))
+    if rc:
+        _capi.check(rc, "repops_adamw_moments")
+    return m_out, v_out

@@ -117,6 +117,10 @@ SIGNATURES = {
     "repops_selftest_bounded_wait": (_i32, [_i64, _vp]),
     "repops_selftest_bounded_flag_wait": (_i32, [_i64, _vp]),
     "repops_softmax_rows_causal_f32": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp]),
+    "repops_adamw_scalars": (_i32, [_i64, ctypes.c_double, ctypes.c_double, ctypes.c_double, _u32, _vp]),
+    "repops_adamw": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_double,
+                            ctypes.c_double, ctypes.c_double, _vp, _i32, _vp, _vp]),
+    "repops_adamw_moments": (_i32, [_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "repops_gemm_f32_batched": (_i32, [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
                                        _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                        ctypes.c_float, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _i64,

@@ -1,0 +1,569 @@
+// adamw.cu -- one AdamW step over many tensors at once, from one or several
+// contributors' gradients folded in a fixed order, with the moments in 32 bits
+// or in 8.
+//
+// Per element, every step one binary32 rounding (b1' = fl(1 - beta1), b2' alike,
+// c2 = fl(1 / sqrt(1 - beta2^t)), s = fl(lr / (1 - beta1^t))):
+//   g     = mean of the contributors' gradients as the fixed-order mean + SGD
+//           (left fold in `order`, one correctly rounded divide by their count),
+//           fl(g * grad_scale) where one is given
+//   m     = fl(fl(m * beta1) + fl(g * b1')),  v = fl(fl(v * beta2) + fl(fl(g * g) * b2'))
+//   r     = fl(sqrt(v)),  u = fl(m / fl(fl(r * c2) + eps))
+//   theta = fl(fl(theta * fl(1 - fl(decay * lr))) - fl(u * s))
+// The square root is taken once: the update needs it, and the 8-bit form keeps it.
+//
+// 8-bit moments: m in e4m3 (sign, 4 bits of exponent, 3 of mantissa), the root r in
+// 4 bits of exponent and 4 of mantissa, each with a scale 2^(s-127) for every 128
+// consecutive elements of a tensor (s one byte).  The scale is the least power of
+// two under which the group's largest value still has a code, so that taking it
+// out and putting it back is exact and the one rounding is the code's.  beta2 moves
+// v by a thousandth of itself a step, far less than half a code's width: rounded
+// to the nearest code the moments would stand still.  So a value is rounded up with
+// the probability that what is cut off has of passing (16 bits of a hash of the
+// seed, the step, the tensor and the element: MurmurHash3's finaliser, Appleby),
+// which is right on average and the same bits on every machine.  A root that is
+// not zero keeps a code that is not zero: m / 0 would follow.  A group holding an
+// infinity or a NaN gets the scale 255 and is NaN from then on.
+//
+// Bytes an element: 12 + 16 with moments in 32 bits, 12 + 4 + 1/32 in 8 (binary32
+// gradients); no order is left open, as elements are independent and a group's
+// largest value does not depend on how it is found.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "storage.cuh"
+
+namespace repops {
+namespace {
+
+constexpr int kGroup = 128;          // elements that share a scale
+constexpr int kTile = 4096;          // elements of a CTA: 16 a thread
+constexpr int kThreads = 256;
+
+// One tensor of a launch, in 64-bit words: first tile | decay, elements (the top
+// bit: every array aligned for four elements an access), theta, m, v, the two
+// scales, then the gradients in the order of the fold.
+constexpr int kEntryWords = 7;
+constexpr uint64_t kAligned = uint64_t(1) << 63;
+
+struct AdamHead {
+    int tensors, stride;             // words of an entry: 7 + contributors
+    int contributors, pow2;
+    float count, inv;
+    float b1, c1, b2, c2;            // beta1, fl(1 - beta1), beta2, fl(1 - beta2)
+    float eps;
+    float lr, step, root;            // lr, s and c2 above
+    uint32_t key;
+    uint32_t first_tensor;           // of this launch, in the whole call
+    const uint32_t *scalars;         // device: lr, s, c2, key instead of those, or null
+    const float *grad_scale;         // device, or null
+    unsigned *status;                // checked build
+};
+
+// The table travels with the launch: nothing to copy, and a captured graph keeps
+// it.  Two sizes, as the whole of it is copied for each launch.
+template <int WORDS>
+struct AdamTable {
+    AdamHead h;
+    uint64_t w[WORDS];
+};
+
+struct Entry {
+    int64_t n;
+    bool vec;
+    float decay;
+    float *theta;
+    void *m, *v;
+    uint8_t *ms, *vs;
+    const uint64_t *grads;
+};
+
+__device__ __forceinline__ uint32_t mix32(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+    h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+
+#define REPOPS_ADAM_OK(base, n, size, p, bytes) \
+    REPOPS_DBG_OK((DbgSpan{reinterpret_cast<uintptr_t>(base), reinterpret_cast<uintptr_t>(base) + uint64_t(n) * (size)}), p, bytes, status)
+
+// Elements e .. e+3 of a tensor, `have` of them there (1 .. 4); the others +0.
+template <int TY>
+__device__ __forceinline__ float4 load4(const void *base, int64_t n, int64_t e, int have, bool vec,
+                                        [[maybe_unused]] unsigned *status) {
+    constexpr unsigned size = TY == REPOPS_TYPE_F32 ? 4 : 2;
+    const char *p = static_cast<const char *>(base) + e * size;
+    if (vec && have == 4) {
+        if (!REPOPS_ADAM_OK(base, n, size, p, 4 * size)) return make_float4(0, 0, 0, 0);
+        return load_four<TY>(DbgAccess{}, p, 0);
+    }
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = i < have && REPOPS_ADAM_OK(base, n, size, p + i * size, size) ? load_one<TY>(DbgAccess{}, p, i) : 0.0f;
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ void store4(float *base, int64_t n, int64_t e, int have, bool vec, float4 v,
+                                       [[maybe_unused]] unsigned *status) {
+    float *p = base + e;
+    if (vec && have == 4) {
+        if (REPOPS_ADAM_OK(base, n, 4, p, 16)) store_four<REPOPS_TYPE_F32>(DbgAccess{}, p, 0, v);
+        return;
+    }
+    const float a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < have && REPOPS_ADAM_OK(base, n, 4, p + i, 4)) p[i] = a[i];
+}
+
+__device__ __forceinline__ uint32_t load_codes(const void *base, int64_t n, int64_t e, int have, bool vec,
+                                               [[maybe_unused]] unsigned *status) {
+    const uint8_t *p = static_cast<const uint8_t *>(base) + e;
+    if (vec && have == 4) return REPOPS_ADAM_OK(base, n, 1, p, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(p)) : 0u;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < have && REPOPS_ADAM_OK(base, n, 1, p + i, 1)) w |= uint32_t(p[i]) << (8 * i);
+    return w;
+}
+
+__device__ __forceinline__ void store_codes(void *base, int64_t n, int64_t e, int have, bool vec, uint32_t w,
+                                            [[maybe_unused]] unsigned *status) {
+    uint8_t *p = static_cast<uint8_t *>(base) + e;
+    if (vec && have == 4) {
+        if (REPOPS_ADAM_OK(base, n, 1, p, 4)) __stcs(reinterpret_cast<uint32_t *>(p), w);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < have && REPOPS_ADAM_OK(base, n, 1, p + i, 1)) p[i] = uint8_t(w >> (8 * i));
+}
+
+// ------------------------------------------------------------ 8-bit codes ----
+
+// A code's bits as the exponent and mantissa of a binary32 number are the code's
+// value times a power of two, its subnormals included: exact products give it back.
+__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
+    const float y = __fmul_rn(__fmul_rn(__uint_as_float((c & 0x7fu) << 20), 0x1p+120f), scale);
+    return __uint_as_float(__float_as_uint(y) ^ ((c & 0x80u) << 24));
+}
+__device__ __forceinline__ float decode_r(uint32_t c, float scale) {
+    return __fmul_rn(__fmul_rn(__uint_as_float((c & 0xffu) << 19), 0x1p+112f), scale);
+}
+__device__ __forceinline__ float scale_of(uint32_t s) { return __uint_as_float(s << 23); }
+
+// s for a group whose largest magnitude has the bits `amax`: the largest code is
+// 1.75 * 2^8 (m) or 1.9375 (r) times the scale.  0: the group is not finite.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t group_scale(uint32_t amax) {
+    if (amax >= 0x7f800000u) return 255u;
+    const int s = int((amax + (ROOT ? 0x07ffffu : 0x1fffffu)) >> 23) - (ROOT ? 0 : 8);
+    return uint32_t(max(s, 1));
+}
+// 2^(127 - s): normal for s up to 253 (a root's s is below 192).
+__device__ __forceinline__ float inverse_scale(uint32_t s) { return s == 255u ? 0.0f : __uint_as_float((254u - s) << 23); }
+
+__device__ __forceinline__ uint32_t encode_m(float x, float inv, uint32_t dither) {
+    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(x), inv), 0x1p-120f));
+    return ((y + ((dither << 4) | 8u)) >> 20) | ((__float_as_uint(x) >> 24) & 0x80u);
+}
+__device__ __forceinline__ uint32_t encode_r(float r, float inv, uint32_t dither) {
+    const uint32_t y = __float_as_uint(__fmul_rn(__fmul_rn(r, inv), 0x1p-112f));
+    const uint32_t c = (y + ((dither << 3) | 4u)) >> 19;
+    return c == 0 && y != 0 ? 1u : c;
+}
+
+// ----------------------------------------------------------------- kernel ----
+
+struct Step {
+    float b1, c1, b2, c2, eps, keep, step, root;
+};
+
+// theta, m and v (or r with 8-bit moments) of one element.
+__device__ __forceinline__ void update(float &theta, float &m, float &v, float &r, float g, const Step &k) {
+    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
+    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
+    r = __fsqrt_rn(v);
+    const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, k.root), k.eps));
+    theta = __fsub_rn(__fmul_rn(theta, k.keep), __fmul_rn(u, k.step));
+}
+
+__device__ __forceinline__ void add4(float4 &a, float4 b) {
+    a.x = __fadd_rn(a.x, b.x);
+    a.y = __fadd_rn(a.y, b.y);
+    a.z = __fadd_rn(a.z, b.z);
+    a.w = __fadd_rn(a.w, b.w);
+}
+
+// U vectors of four elements a thread are in flight together.
+template <int TY, bool EIGHT, bool MANY, int U>
+__device__ __forceinline__ void run_tile(const AdamHead &h, const Entry &t, int64_t base, const Step &k, uint32_t key,
+                                         float gscale, bool scaled) {
+    const int lane = threadIdx.x & 31;
+    unsigned *status = h.status;
+#pragma unroll 1
+    for (int part = 0; part < kTile / (kThreads * 4 * U); ++part) {
+        const int64_t first = base + int64_t(part) * (kThreads * 4 * U) + threadIdx.x * 4;
+        if (base + int64_t(part) * (kThreads * 4 * U) >= t.n) return;      // the same for the whole CTA
+        float4 theta[U], g[U], m[U], v[U];
+        uint32_t mc[U], vc[U];
+        float ms[U], vs[U];
+        int have[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t e = first + j * (kThreads * 4);
+            have[j] = int(max(int64_t(0), min(int64_t(4), t.n - e)));
+            g[j] = load4<TY>(reinterpret_cast<const void *>(t.grads[0]), t.n, e, have[j], t.vec, status);
+            theta[j] = load4<REPOPS_TYPE_F32>(t.theta, t.n, e, have[j], t.vec, status);
+            if constexpr (EIGHT) {
+                mc[j] = load_codes(t.m, t.n, e, have[j], t.vec, status);
+                vc[j] = load_codes(t.v, t.n, e, have[j], t.vec, status);
+                [[maybe_unused]] const int64_t groups = (t.n + kGroup - 1) / kGroup;
+                const int64_t q = e / kGroup;
+                const bool in = have[j] > 0 && REPOPS_ADAM_OK(t.ms, groups, 1, t.ms + q, 1) &&
+                                REPOPS_ADAM_OK(t.vs, groups, 1, t.vs + q, 1);
+                ms[j] = scale_of(in ? t.ms[q] : 0);
+                vs[j] = scale_of(in ? t.vs[q] : 0);
+            } else {
+                m[j] = load4<REPOPS_TYPE_F32>(t.m, t.n, e, have[j], t.vec, status);
+                v[j] = load4<REPOPS_TYPE_F32>(t.v, t.n, e, have[j], t.vec, status);
+            }
+        }
+        if constexpr (MANY) {
+#pragma unroll 4
+            for (int c = 1; c < h.contributors; ++c) {
+                const void *p = reinterpret_cast<const void *>(t.grads[c]);
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    add4(g[j], load4<TY>(p, t.n, first + j * (kThreads * 4), have[j], t.vec, status));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t e = first + j * (kThreads * 4);
+            float *gj = &g[j].x, *tj = &theta[j].x, *mj = &m[j].x, *vj = &v[j].x;
+            float r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (MANY)
+                    gj[i] = h.pow2 ? __fmul_rn(gj[i], h.inv) : __fdiv_rn(gj[i], h.count);
+                if (scaled) gj[i] = __fmul_rn(gj[i], gscale);
+                if constexpr (EIGHT) {
+                    mj[i] = decode_m(mc[j] >> (8 * i), ms[j]);
+                    const float was = decode_r(vc[j] >> (8 * i), vs[j]);
+                    vj[i] = __fmul_rn(was, was);
+                }
+                update(tj[i], mj[i], vj[i], r[i], gj[i], k);
+            }
+            if (have[j]) store4(t.theta, t.n, e, have[j], t.vec, theta[j], status);
+            if constexpr (EIGHT) {
+                uint32_t am = 0, ar = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    am = max(am, i < have[j] ? __float_as_uint(mj[i]) & 0x7fffffffu : 0u);
+                    ar = max(ar, i < have[j] ? __float_as_uint(r[i]) & 0x7fffffffu : 0u);
+                }
+                const uint32_t sm = group_scale<false>(__reduce_max_sync(0xffffffffu, am));
+                const uint32_t sr = group_scale<true>(__reduce_max_sync(0xffffffffu, ar));
+                const float im = inverse_scale(sm), ir = inverse_scale(sr);
+                uint32_t cm = 0, cr = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t d = mix32(uint32_t(e + i) * 0x9E3779B1u + key);
+                    cm |= (sm == 255u ? 0u : encode_m(mj[i], im, d & 0xffffu)) << (8 * i);
+                    cr |= (sr == 255u ? 0u : encode_r(r[i], ir, d >> 16)) << (8 * i);
+                }
+                if (have[j]) {
+                    store_codes(t.m, t.n, e, have[j], t.vec, cm, status);
+                    store_codes(t.v, t.n, e, have[j], t.vec, cr, status);
+                    const int64_t q = e / kGroup;
+                    [[maybe_unused]] const int64_t groups = (t.n + kGroup - 1) / kGroup;
+                    if (lane == 0 && REPOPS_ADAM_OK(t.ms, groups, 1, t.ms + q, 1) &&
+                        REPOPS_ADAM_OK(t.vs, groups, 1, t.vs + q, 1)) {
+                        t.ms[q] = uint8_t(sm);
+                        t.vs[q] = uint8_t(sr);
+                    }
+                }
+            } else if (have[j]) {
+                store4(static_cast<float *>(t.m), t.n, e, have[j], t.vec, m[j], status);
+                store4(static_cast<float *>(t.v), t.n, e, have[j], t.vec, v[j], status);
+            }
+        }
+    }
+}
+
+template <int TY, bool EIGHT, bool MANY, int WORDS>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<WORDS> a) {
+    const AdamHead &h = a.h;
+    // the tensor whose tiles hold this one
+    int lo = 0, hi = h.tensors - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (uint32_t(a.w[mid * h.stride]) <= blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
+    const uint64_t *w = a.w + lo * h.stride;
+    Entry t;
+    t.n = int64_t(w[1] & ~kAligned);
+    t.vec = (w[1] & kAligned) != 0;
+    t.decay = __uint_as_float(uint32_t(w[0] >> 32));
+    t.theta = reinterpret_cast<float *>(w[2]);
+    t.m = reinterpret_cast<void *>(w[3]);
+    t.v = reinterpret_cast<void *>(w[4]);
+    t.ms = reinterpret_cast<uint8_t *>(w[5]);
+    t.vs = reinterpret_cast<uint8_t *>(w[6]);
+    t.grads = w + kEntryWords;
+    float lr = h.lr, step = h.step, root = h.root;
+    uint32_t key = h.key;
+    if (h.scalars) {
+        lr = __uint_as_float(__ldg(h.scalars));
+        step = __uint_as_float(__ldg(h.scalars + 1));
+        root = __uint_as_float(__ldg(h.scalars + 2));
+        key = __ldg(h.scalars + 3);
+    }
+    const Step k{h.b1, h.c1, h.b2, h.c2, h.eps, __fsub_rn(1.0f, __fmul_rn(t.decay, lr)), step, root};
+    key = mix32(key + 0x9E3779B9u * (h.first_tensor + uint32_t(lo) + 1u));
+    const float gscale = h.grad_scale ? __ldg(h.grad_scale) : 1.0f;
+    const int64_t base = int64_t(blockIdx.x - uint32_t(w[0])) * kTile;
+    run_tile<TY, EIGHT, MANY, EIGHT ? 4 : 2>(h, t, base, k, key, gscale, h.grad_scale != nullptr);
+}
+
+// m and v of 8-bit moments as the binary32 values they stand for.
+__global__ void __launch_bounds__(kThreads)
+adamw_moments_kernel(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *ms, const uint8_t *vs, float *m_out,
+                     float *v_out, int vec, unsigned *status) {
+    [[maybe_unused]] const int64_t groups = (n + kGroup - 1) / kGroup;
+    const int64_t step = int64_t(gridDim.x) * kThreads * 4;
+    for (int64_t e = (blockIdx.x * int64_t(kThreads) + threadIdx.x) * 4; e < n; e += step) {
+        const int have = int(min(int64_t(4), n - e));
+        const uint32_t mc = load_codes(m, n, e, have, vec, status), vc = load_codes(v, n, e, have, vec, status);
+        const int64_t q = e / kGroup;
+        float a = 0.0f, b = 0.0f;
+        if (REPOPS_ADAM_OK(ms, groups, 1, ms + q, 1) && REPOPS_ADAM_OK(vs, groups, 1, vs + q, 1)) {
+            a = scale_of(__ldg(ms + q));
+            b = scale_of(__ldg(vs + q));
+        }
+        float4 x, y;
+        float *px = &x.x, *py = &y.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            px[i] = decode_m(mc >> (8 * i), a);
+            const float r = decode_r(vc >> (8 * i), b);
+            py[i] = __fmul_rn(r, r);
+        }
+        store4(m_out, n, e, have, vec, x, status);
+        store4(v_out, n, e, have, vec, y, status);
+    }
+}
+
+// ------------------------------------------------------------------- host ----
+
+constexpr int kSmallWords = 448, kLargeWords = 3968;     // 3.6 and 31.1 KB of kernel parameters
+
+template <int TY, bool EIGHT, bool MANY>
+int launch(const AdamHead &h, const std::vector<uint64_t> &w, unsigned tiles, cudaStream_t s) {
+    if (w.size() <= size_t(kSmallWords)) {
+        AdamTable<kSmallWords> a;
+        a.h = h;
+        std::copy(w.begin(), w.end(), a.w);
+        adamw_kernel<TY, EIGHT, MANY, kSmallWords><<<tiles, kThreads, 0, s>>>(a);
+    } else {
+        AdamTable<kLargeWords> a;
+        a.h = h;
+        std::copy(w.begin(), w.end(), a.w);
+        adamw_kernel<TY, EIGHT, MANY, kLargeWords><<<tiles, kThreads, 0, s>>>(a);
+    }
+    return check_launch();
+}
+
+template <int TY>
+int launch_typed(const AdamHead &h, const std::vector<uint64_t> &w, unsigned tiles, bool eight, cudaStream_t s) {
+    if (eight) return h.contributors > 1 ? launch<TY, true, true>(h, w, tiles, s) : launch<TY, true, false>(h, w, tiles, s);
+    return h.contributors > 1 ? launch<TY, false, true>(h, w, tiles, s) : launch<TY, false, false>(h, w, tiles, s);
+}
+
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+    bool operator<(const Range &o) const { return lo < o.lo; }
+};
+
+// Whether a written range shares a byte with any other.
+bool ranges_clash(std::vector<Range> &r) {
+    std::sort(r.begin(), r.end());
+    uintptr_t end = 0, written_end = 0;
+    for (const Range &x : r) {
+        if (x.lo < written_end || (x.written && x.lo < end)) return true;
+        end = std::max(end, x.hi);
+        if (x.written) written_end = std::max(written_end, x.hi);
+    }
+    return false;
+}
+
+// b^n by squaring: IEEE products alone, the same bits on any host.
+double power(double b, uint64_t n) {
+    double p = 1.0;
+    for (; n; n >>= 1, b *= b)
+        if (n & 1) p *= b;
+    return p;
+}
+
+uint32_t mix32_host(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x85EBCA6Bu;
+    h = (h ^ (h >> 13)) * 0xC2B2AE35u;
+    return h ^ (h >> 16);
+}
+
+bool in_unit(double b) { return b >= 0.0 && b < 1.0; }
+
+}  // namespace
+}  // namespace repops
+
+using namespace repops;
+
+extern "C" int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, uint32_t seed,
+                                    uint32_t *scalars) {
+    if (step < 1 || !in_unit(beta1) || !in_unit(beta2) || !std::isfinite(lr) || !scalars) return REPOPS_ERR_INVALID_ARG;
+    const float f[3] = {float(lr), float(lr / (1.0 - power(beta1, uint64_t(step)))),
+                        float(1.0 / std::sqrt(1.0 - power(beta2, uint64_t(step))))};
+    std::memcpy(scalars, f, sizeof f);
+    scalars[3] = mix32_host(0x9E3779B9u * uint32_t(step) + seed);
+    return REPOPS_OK;
+}
+
+extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
+                            const void *const *grads, int grad_type, const int *order, void *const *m, void *const *v,
+                            uint8_t *const *m_scale, uint8_t *const *v_scale, const float *decay, double beta1,
+                            double beta2, double eps, const uint32_t *scalars, int scalars_on_device,
+                            const float *grad_scale, cudaStream_t stream) {
+    if (tensors < 0 || contributors < 1 || contributors > REPOPS_MEAN_MAX_CONTRIBUTORS || !known_storage(grad_type) ||
+        !in_unit(beta1) || !in_unit(beta2) || !(eps >= 0.0) || !scalars || !order ||
+        (m_scale != nullptr) != (v_scale != nullptr))
+        return REPOPS_ERR_INVALID_ARG;
+    std::vector<char> seen(size_t(contributors), 0);
+    for (int c = 0; c < contributors; ++c) {
+        if (order[c] < 0 || order[c] >= contributors || seen[size_t(order[c])]) return REPOPS_ERR_ORDER;
+        seen[size_t(order[c])] = 1;
+    }
+    if (tensors == 0) return REPOPS_OK;
+    if (!sizes || !theta || !grads || !m || !v) return REPOPS_ERR_INVALID_ARG;
+    const bool eight = m_scale != nullptr;
+    const unsigned gsize = storage_size(grad_type), ssize = eight ? 1u : 4u;
+    std::vector<Range> ranges;
+    ranges.reserve(size_t(tensors) * size_t(5 + contributors) + 2);
+    auto range = [&](const void *p, uint64_t bytes, bool written) {
+        ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
+    };
+    for (int i = 0; i < tensors; ++i) {
+        const int64_t n = sizes[i];
+        if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
+        if (n == 0) continue;
+        if (!theta[i] || !m[i] || !v[i] || (eight && (!m_scale[i] || !v_scale[i]))) return REPOPS_ERR_INVALID_ARG;
+        range(theta[i], uint64_t(n) * 4u, true);
+        range(m[i], uint64_t(n) * ssize, true);
+        range(v[i], uint64_t(n) * ssize, true);
+        if (eight) {
+            range(m_scale[i], uint64_t(n + kGroup - 1) / kGroup, true);
+            range(v_scale[i], uint64_t(n + kGroup - 1) / kGroup, true);
+        }
+        for (int c = 0; c < contributors; ++c) {
+            const void *g = grads[int64_t(i) * contributors + c];
+            if (!g) return REPOPS_ERR_INVALID_ARG;
+            range(g, uint64_t(n) * gsize, false);
+        }
+    }
+    if (scalars_on_device) range(scalars, 16, false);
+    if (grad_scale) range(grad_scale, 4, false);
+    if (ranges_clash(ranges)) return REPOPS_ERR_ALIAS;
+
+    AdamHead h{};
+    h.stride = kEntryWords + contributors;
+    h.contributors = contributors;
+    h.pow2 = (contributors & (contributors - 1)) == 0;
+    h.count = float(contributors);
+    h.inv = h.pow2 ? 1.0f / float(contributors) : 0.0f;
+    h.b1 = float(beta1);
+    h.c1 = float(1.0 - beta1);
+    h.b2 = float(beta2);
+    h.c2 = float(1.0 - beta2);
+    h.eps = float(eps);
+    if (scalars_on_device) {
+        h.scalars = scalars;
+    } else {
+        float f[3];
+        std::memcpy(f, scalars, sizeof f);
+        h.lr = f[0];
+        h.step = f[1];
+        h.root = f[2];
+        h.key = scalars[3];
+    }
+    h.grad_scale = grad_scale;
+    if (const int rc = status_word_address(&h.status); rc != REPOPS_OK) return rc;
+
+    std::vector<uint64_t> w;
+    w.reserve(size_t(std::min(int64_t(tensors) * h.stride, int64_t(kLargeWords))));
+    int64_t tiles = 0;
+    int rc = REPOPS_OK;
+    auto flush = [&](int next) {
+        if (h.tensors && rc == REPOPS_OK) {
+            switch (grad_type) {
+                case REPOPS_TYPE_F32: rc = launch_typed<REPOPS_TYPE_F32>(h, w, unsigned(tiles), eight, stream); break;
+                case REPOPS_TYPE_F16: rc = launch_typed<REPOPS_TYPE_F16>(h, w, unsigned(tiles), eight, stream); break;
+                default: rc = launch_typed<REPOPS_TYPE_BF16>(h, w, unsigned(tiles), eight, stream); break;
+            }
+        }
+        h.tensors = 0;
+        h.first_tensor = uint32_t(next);
+        w.clear();
+        tiles = 0;
+    };
+    for (int i = 0; i < tensors && rc == REPOPS_OK; ++i) {
+        const int64_t n = sizes[i], more = (n + kTile - 1) / kTile;
+        // a launch's tensors are consecutive ones of the call; an empty one keeps its place
+        if (w.size() + size_t(h.stride) > size_t(kLargeWords) || tiles + more > INT32_MAX) flush(i);
+        uintptr_t bits = reinterpret_cast<uintptr_t>(theta[i]);
+        bits |= (reinterpret_cast<uintptr_t>(m[i]) | reinterpret_cast<uintptr_t>(v[i])) * (eight ? 4u : 1u);
+        for (int c = 0; c < contributors; ++c)
+            bits |= reinterpret_cast<uintptr_t>(grads[int64_t(i) * contributors + c]) * (4u / gsize);
+        uint32_t d = 0;
+        if (decay) std::memcpy(&d, decay + i, 4);
+        w.push_back(uint64_t(uint32_t(tiles)) | (uint64_t(d) << 32));
+        w.push_back(uint64_t(n) | (bits % 16 == 0 ? kAligned : 0));
+        w.push_back(reinterpret_cast<uint64_t>(theta[i]));
+        w.push_back(reinterpret_cast<uint64_t>(m[i]));
+        w.push_back(reinterpret_cast<uint64_t>(v[i]));
+        w.push_back(eight ? reinterpret_cast<uint64_t>(m_scale[i]) : 0);
+        w.push_back(eight ? reinterpret_cast<uint64_t>(v_scale[i]) : 0);
+        for (int c = 0; c < contributors; ++c)
+            w.push_back(reinterpret_cast<uint64_t>(grads[int64_t(i) * contributors + order[c]]));
+        ++h.tensors;
+        tiles += more;
+    }
+    if (tiles) flush(tensors);
+    return rc;
+}
+
+extern "C" int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *m_scale,
+                                    const uint8_t *v_scale, float *m_out, float *v_out, cudaStream_t stream) {
+    if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
+    if (n == 0) return REPOPS_OK;
+    if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return REPOPS_ERR_INVALID_ARG;
+    const uint64_t groups = uint64_t(n + kGroup - 1) / kGroup, bytes = uint64_t(n) * 4u;
+    for (const auto &in : {std::pair<const void *, uint64_t>{m, uint64_t(n)}, {v, uint64_t(n)}, {m_scale, groups}, {v_scale, groups}})
+        if (ranges_overlap(m_out, bytes, in.first, in.second) || ranges_overlap(v_out, bytes, in.first, in.second))
+            return REPOPS_ERR_ALIAS;
+    if (ranges_overlap(m_out, bytes, v_out, bytes)) return REPOPS_ERR_ALIAS;
+    unsigned *status;
+    if (const int rc = status_word_address(&status); rc != REPOPS_OK) return rc;
+    DeviceInfo di;
+    if (const int rc = current_device_info(&di); rc != REPOPS_OK) return rc;
+    const uintptr_t bits = ((reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v)) * 4u) |
+                           reinterpret_cast<uintptr_t>(m_out) | reinterpret_cast<uintptr_t>(v_out);
+    const int64_t units = (n + 4 * kThreads - 1) / (4 * kThreads);
+    adamw_moments_kernel<<<unsigned(std::min<int64_t>(units, int64_t(di.sms) * 32)), kThreads, 0, stream>>>(
+        n, m, v, m_scale, v_scale, m_out, v_out, bits % 16 == 0, status);
+    return check_launch();
+}

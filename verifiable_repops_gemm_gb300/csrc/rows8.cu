@@ -33,55 +33,6 @@ namespace {
 constexpr float kScaleFloor = 0x1p-100f;
 constexpr float kScaleMost = 0x1.020406p+121f;
 
-template <int TY>
-__device__ __forceinline__ float load_one(const DbgAccess &d, const void *p, int64_t i) {
-    if constexpr (TY == REPOPS_TYPE_F32) return load_global(d, static_cast<const float *>(p) + i);
-    else if constexpr (TY == REPOPS_TYPE_F16) return __half2float(load_global(d, static_cast<const __half *>(p) + i));
-    else return __bfloat162float(load_global(d, static_cast<const __nv_bfloat16 *>(p) + i));
-}
-
-// A value as it is stored: 32 bits, or 16 in the low half.
-template <int TY>
-__device__ __forceinline__ uint32_t narrowed(float v) {
-    if constexpr (TY == REPOPS_TYPE_F32) return __float_as_uint(v);
-    else if constexpr (TY == REPOPS_TYPE_F16) return __half_as_ushort(__float2half_rn(v));
-    else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-template <int TY>
-__device__ __forceinline__ void store_one(const DbgAccess &d, void *p, int64_t i, float v) {
-    if constexpr (TY == REPOPS_TYPE_F32) store_global(d, static_cast<float *>(p) + i, v);
-    else store_global(d, static_cast<uint16_t *>(p) + i, uint16_t(narrowed<TY>(v)));
-}
-
-// Elements i .. i+3, i a multiple of 4 elements from an aligned base.
-template <int TY>
-__device__ __forceinline__ float4 load_four(const DbgAccess &d, const void *p, int64_t i) {
-    if constexpr (TY == REPOPS_TYPE_F32) {
-        return load_once(d, reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
-    } else {
-        const uint2 w = load_once(d, reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i));
-        if constexpr (TY == REPOPS_TYPE_BF16) {
-            return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&w.y));
-            return make_float4(a.x, a.y, b.x, b.y);
-        }
-    }
-}
-
-template <int TY>
-__device__ __forceinline__ void store_four(const DbgAccess &d, void *p, int64_t i, float4 v) {
-    if constexpr (TY == REPOPS_TYPE_F32) {
-        store_once(d, reinterpret_cast<float4 *>(static_cast<float *>(p) + i), v);
-    } else {
-        store_once(d, reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i),
-                   make_uint2(narrowed<TY>(v.x) | (narrowed<TY>(v.y) << 16), narrowed<TY>(v.z) | (narrowed<TY>(v.w) << 16)));
-    }
-}
-
 // The larger magnitude, a NaN winning over everything.
 __device__ __forceinline__ float max_mag(float m, float v) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v)));

@@ -4,10 +4,7 @@
 // write it and those that read it.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "internal.cuh"
+#include "storage.cuh"
 
 namespace repops {
 namespace {
@@ -27,22 +24,6 @@ inline bool known_group(int64_t group) {
 }
 
 inline int64_t group_count(int64_t cols, int64_t group) { return group == 0 ? 1 : (cols + group - 1) / group; }
-
-[[maybe_unused]] inline bool known_storage(int t) {
-    return t == REPOPS_TYPE_F32 || t == REPOPS_TYPE_F16 || t == REPOPS_TYPE_BF16;
-}
-[[maybe_unused]] inline unsigned storage_size(int t) { return t == REPOPS_TYPE_F32 ? 4u : 2u; }
-
-// Bytes spanned by rows x cols elements of `size` bytes at pitch ld; false
-// when ld is short or the span overflows.
-[[maybe_unused]] inline bool span_bytes(int64_t rows, int64_t cols, int64_t ld, unsigned size, uint64_t *bytes) {
-    *bytes = 0;
-    if (ld < cols) return false;
-    if (rows == 0 || cols == 0) return true;
-    if (ld > INT64_MAX / 8 || rows - 1 > (INT64_MAX / 8 - cols) / ld) return false;
-    *bytes = uint64_t((rows - 1) * ld + cols) * size;
-    return true;
-}
 
 // Four whole numbers packed in a word, lowest byte first, each as the value it
 // stands for: one rounding, fl(q * scale).  With its sign bit flipped a byte is
