@@ -1164,6 +1164,62 @@ int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int con
 int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *m_scale,
                          const uint8_t *v_scale, float *m_out, float *v_out, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Log probabilities of given tokens                                         */
+/* "Verde与RepOps" §4.3 (training: the loss and its gradient) and §3.2 (a    */
+/* fixed order for order-critical reductions).  The pages fix no loss; the   */
+/* library's definition follows, the sums' order by columns alone.           */
+/* ------------------------------------------------------------------------ */
+
+/* For every row of logits x (rows x cols, stored as x_type, widened exactly) and
+ * temperature T:
+ *   logp[r] = log softmax(x / T)[targets[r]]   (0 for a negative target: none;
+ *             NaN for one of cols or more; targets NULL: none)
+ *   lse[r] = ln sum exp(x / T),  entropy[r] = that of softmax(x / T)
+ *   top_logp, top_ids (rows x top): the `top` most likely columns in falling
+ *             order, the lower column first among equals (-0 and +0 are equal)
+ *   stats[r] (4 floats): the maximum M, fl(1 / S), fl(ln S), the entropy,
+ *             S = sum exp((x - M) / T): what the gradient takes
+ * Logits of -infinity are impossible (log probability -infinity, no part in the
+ * sums); a row of nothing else has lse -infinity, entropy 0 and 1 / S = 0.  A row
+ * with a NaN or +infinity gives NaN (its alternatives: NaN above everything).
+ * Arithmetic, binary32 with one rounding a step unless named: c = fl(log2(e) / T),
+ *   t(x; m) = max(fl(fl(x - m) * c), -127),  k = rint(t),  f = t - k,
+ *   e(x; m) = fl((1 + f*q(f) by Horner's rule) * 2^k), +0 at k = -127, with q's
+ *   coefficients (highest first) 0x1.5bba14p-10, 0x1.3cea88p-7, 0x1.c6b752p-5,
+ *   0x1.ebf9bcp-3, 0x1.62e42ap-1;
+ *   every 1024 columns: m their maximum (0 in the place of -infinity inside e and
+ *   t), s = sum e, u = sum fl(e * t): for each residue of the column modulo 256
+ *   the columns in order from +0, then residue r + residue r + 128, .. + 64, ...;
+ *   the row in binary64: S = sum w*s, Q = sum w*(u + t(m; M)*s), w = e(m; M), the
+ *   segments of a residue modulo 32 in order from +0, then r + (r + 16), ...;
+ *   ln S = E*ln2 + 2z*(1 + z^2/3 + ... + z^22/23) by Horner's rule, S = F * 2^E,
+ *   F in [sqrt(1/2), sqrt(2)], z = (F - 1) / (F + 1);
+ *   lse = M*(1/T) + ln S,  logp = (x_t - M)*(1/T) - ln S,  H = ln S - ln2*(Q/S),
+ *   rounded once to binary32.
+ * Row pitch ldx >= cols; stats on a 16-byte boundary.  1 <= cols, 0 <= top <= cols,
+ * 1e-6 <= T <= 1e6, else INVALID_ARG; UNSUPPORTED for top above 32, more than
+ * 16384000 columns or 2^27 rows; outputs must not overlap inputs or each other
+ * (ALIAS). */
+int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
+                          const int64_t *targets, double temperature, int top, float *logp,
+                          float *lse, float *entropy, float *stats, float *top_logp,
+                          int64_t *top_ids, cudaStream_t stream);
+
+/* dx, the gradient of the logits, given dlogp and dentropy (rows floats each, one
+ * of them may be NULL), with the forward's stats:
+ *   p = fl(e(x; M) * (1/S)),  i = fl(1/T)
+ *   A = -fl(i * fl(dlogp + fl(dentropy * fl(H - ln S)))),  B = -fl(fl(i * ln2) * dentropy)
+ *   dx = fl(p * fl(A + fl(B * t(x; M)))), at the target fl(dx + fl(i * dlogp))
+ * narrowed once to x_type (without dentropy: fl(p * A), A = -fl(i * dlogp)).  A
+ * negative target has dlogp 0 whatever is given; one of cols or more makes its row
+ * NaN.  A row of -infinities alone has the gradient 0.  dx may be x itself (same
+ * pitch); any other overlap with an input is ALIAS.  Limits as the forward's. */
+int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, int x_type,
+                                   int64_t ldx, const int64_t *targets, double temperature,
+                                   const float *stats, const float *dlogp, const float *dentropy,
+                                   void *dx, int64_t lddx, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,6 +47,7 @@ after the current one first, or given `out`.
 import array
 import ctypes
 import functools
+import typing
 
 from . import _capi
 from ._capi import (ACT_GELU, ACT_NONE, LOADER_AUTO, LOADER_CPASYNC, LOADER_DIRECT, LOADER_TMA,
@@ -1446,3 +1447,79 @@ def adamw_moments(m, v, m_scale, v_scale, *, m_out=None, v_out=None, stream=None
     if rc:
         _capi.check(rc, "repops_adamw_moments")
     return m_out, v_out
+
+
+class TokenLogprobs(typing.NamedTuple):
+    """What token_logprobs returns, a row for each of the logits'."""
+    logp: object       # float32 (rows,): log probability of the target (0 without one)
+    lse: object        # float32 (rows,): log of the sum of exponentials
+    entropy: object    # float32 (rows,)
+    stats: object      # float32 (rows, 4): maximum, 1 / S, ln S, entropy, for the gradient
+    top_logp: object   # float32 (rows, top), or None
+    top_ids: object    # int64 (rows, top), or None
+
+
+def _logits(x, targets, name="logits"):
+    """(rows, columns, storage type, pitch) of logits, and the targets checked."""
+    import torch
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("%s must be a 2-D CUDA tensor with unit column stride" % name)
+    rows, cols = x.shape
+    if targets is not None and (targets.dtype != torch.int64 or targets.numel() != rows or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous int64 tensor of one value a row")
+    return rows, cols, _storage_type(x.dtype), _pitch(x, name)
+
+
+def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int = 0, stream=None):
+    """TokenLogprobs of the rows of logits (2-D float32, float16 or bfloat16 CUDA,
+    unit column stride): the log probability of each row's target under
+    softmax(logits / temperature), the row's entropy and log of the sum of
+    exponentials, and its `top` (up to 32) most likely columns
+    (repops_token_logprobs).  targets: int64, a negative one for a row without;
+    logits of -inf are impossible tokens."""
+    import torch
+    rows, cols, kind, ld = _logits(logits, targets)
+    dev = logits.device
+    logp, lse, entropy = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind()
+    stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
+    top_logp = top_ids = None
+    if top > 0:
+        top_logp = torch.empty((rows, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
+    handle = _stream_on_device(stream, logits, targets)
+    rc = load().repops_token_logprobs(rows, cols, logits.data_ptr(), kind, ld,
+                                      None if targets is None else targets.data_ptr(), temperature, top,
+                                      logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), stats.data_ptr(),
+                                      top_logp.data_ptr() if top > 0 else None, top_ids.data_ptr() if top > 0 else None,
+                                      handle)
+    if rc:
+        _capi.check(rc, "repops_token_logprobs")
+    return TokenLogprobs(logp, lse, entropy, stats, top_logp, top_ids)
+
+
+def token_logprobs_backward(logits, targets, stats, dlogp=None, dentropy=None, *, temperature: float = 1.0, out=None,
+                            stream=None):
+    """The gradient of the logits given those of token_logprobs' logp and entropy
+    (float32, one value a row; one of them may be None) and its stats, in the
+    logits' dtype (repops_token_logprobs_backward).  out may be logits."""
+    import torch
+    rows, cols, kind, ld = _logits(logits, targets)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=logits.dtype, device=logits.device)
+    if out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must have the shape and dtype of logits")
+    ldd = _logits(out, None, "out")[3]
+    if stats.dtype != torch.float32 or stats.shape != (rows, 4) or not stats.is_contiguous():
+        raise ValueError("stats must be the contiguous float32 (rows, 4) tensor of token_logprobs")
+    for t in (dlogp, dentropy):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != rows or not t.is_contiguous()):
+            raise ValueError("dlogp and dentropy must be contiguous float32 tensors of one value a row")
+    handle = _stream_on_device(stream, logits, targets, stats, dlogp, dentropy, out)
+    rc = load().repops_token_logprobs_backward(rows, cols, logits.data_ptr(), kind, ld,
+                                               None if targets is None else targets.data_ptr(), temperature,
+                                               stats.data_ptr(), None if dlogp is None else dlogp.data_ptr(),
+                                               None if dentropy is None else dentropy.data_ptr(), out.data_ptr(), ldd,
+                                               handle)
+    if rc:
+        _capi.check(rc, "repops_token_logprobs_backward")
+    return out

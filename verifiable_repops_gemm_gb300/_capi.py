@@ -121,6 +121,10 @@ SIGNATURES = {
     "repops_adamw": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_double,
                             ctypes.c_double, ctypes.c_double, _vp, _i32, _vp, _vp]),
     "repops_adamw_moments": (_i32, [_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "repops_token_logprobs": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, ctypes.c_double, _i32, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _vp]),
+    "repops_token_logprobs_backward": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, ctypes.c_double, _vp, _vp, _vp, _vp,
+                                              _i64, _vp]),
     "repops_gemm_f32_batched": (_i32, [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
                                        _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                        ctypes.c_float, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
