@@ -68,6 +68,10 @@ typedef enum {
 #define REPOPS_TYPE_F16 1    /* IEEE binary16 */
 #define REPOPS_TYPE_BF16 2   /* bfloat16: the high 16 bits of a binary32 */
 
+/* How a head's columns pair up in a rotation (repops_head_norm_rope). */
+#define REPOPS_ROPE_ADJACENT 0   /* (2i, 2i + 1) */
+#define REPOPS_ROPE_HALVES 1     /* (i, i + pairs) */
+
 /* Build manifest: library version, target architecture, compile flags that
  * fix the arithmetic (-fmad=false, -ftz=false, -prec-div=true, ...), and the
  * GEMM tile configurations.  The role of a "KernelManifest" ("Zoo Per-LLM
@@ -1219,6 +1223,70 @@ int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, in
                                    int64_t ldx, const int64_t *targets, double temperature,
                                    const float *stats, const float *dlogp, const float *dentropy,
                                    void *dx, int64_t lddx, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Norms of query and key heads with the position rotation                   */
+/* "Verde与RepOps" §4.3 (Llama-style training).  Composition of the norm and */
+/* the rotation above, bit for bit, over the heads of a matrix, with what    */
+/* other models want of a rotation: halves instead of adjacent pairs, part   */
+/* of a head, positions of their own for each row, scaled frequencies.       */
+/* ------------------------------------------------------------------------ */
+
+/* freq, in place, for contexts `factor` times as long as the `original` ones:
+ * with r = original * f / (2 pi) turns in the original context,
+ *   r <= low: f / factor;  r >= high: f;  between: the mean of both weighted by
+ *   (r - low) / (high - low) on f
+ * in binary64 (the weighted sum as f/factor + w * (f - f/factor)), rounded once.
+ * original == 0: f / factor for all.  factor > 0, original >= 0, 0 <= low < high
+ * (not looked at when original is 0), else INVALID_ARG. */
+int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, double factor, double original,
+                                      double low, double high, cudaStream_t stream);
+
+/* For every row r and head h < q_heads + k_heads, the columns [h*dim, (h+1)*dim) of
+ * row r of x (stored as `type`, widened exactly; rows at pitch ldx), each step one
+ * binary32 rounding:
+ *   v = the head normed as a row of repops_rmsnorm_rows_f32 (dim columns, eps) with
+ *       q_gain, or k_gain from head q_heads on (dim floats each); both NULL: v = x
+ *   the first 2*pairs columns of v rotated as repops_rope_f32 (inverse != 0: its
+ *   inverse, without gains only) at the row's position, pairs as `layout` says
+ *   (REPOPS_ROPE_*), the others left; narrowed once into y at pitch ldy.
+ * cos_tab, sin_tab: a table as repops_rope_table_f32's of `positions` rows of
+ * `pairs`; pairs 0: no rotation (the table may be NULL).  pos: a position for each
+ * row (device; int32, or int64 with pos_wide 1), or NULL for first + (r mod
+ * period).  A row with a negative position (padding) is left alone: nothing of y's
+ * is written; one past the table gives NaN in the rotated columns.
+ * y may be x (same pitch), any other overlap is ALIAS.  INVALID_ARG for negative
+ * sizes, 2*pairs > dim, short pitches, gains for one kind of head alone where both
+ * are there, null or misaligned (to the element) pointers, first/period that leave
+ * the table; UNSUPPORTED for dim above 512, 65536 heads of a kind or 2^31
+ * positions. */
+int repops_head_norm_rope(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t dim,
+                          const void *x, int type, int64_t ldx, const float *q_gain,
+                          const float *k_gain, float eps, const float *cos_tab,
+                          const float *sin_tab, int64_t pairs, int64_t positions, int layout,
+                          int inverse, const void *pos, int pos_wide, int64_t first,
+                          int64_t period, void *y, int64_t ldy, cudaStream_t stream);
+
+/* Its backward with gains, from the forward's x: dy rotated back (the inverse), then
+ * dx as repops_rmsnorm_backward_f32 per head, narrowed once, and
+ *   dq_gain = repops_colsum_f32 over the rows (r, h) -- r outer, h < q_heads inner --
+ *             of dy_rotated_back * xhat; dk_gain alike (+0 for rows left alone, whose
+ *             dx is not written)
+ * A gain and its gradient are there exactly when the heads are.  ws: device scratch of
+ * ..._workspace_bytes on a 16-byte boundary (a shorter one is INVALID_ARG), or NULL to
+ * take it from the scratch pool.  dx may be dy (same pitch); any other overlap is
+ * ALIAS.  rows == 0: no-op, the sums are not written either.  Without gains the
+ * backward is repops_head_norm_rope with inverse. */
+uint64_t repops_head_norm_rope_backward_workspace_bytes(int64_t rows, int64_t q_heads,
+                                                        int64_t k_heads, int64_t dim);
+int repops_head_norm_rope_backward(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t dim,
+                                   const void *dy, int type, int64_t lddy, const void *x,
+                                   int64_t ldx, const float *q_gain, const float *k_gain, float eps,
+                                   const float *cos_tab, const float *sin_tab, int64_t pairs,
+                                   int64_t positions, int layout, const void *pos, int pos_wide,
+                                   int64_t first, int64_t period, void *dx, int64_t lddx,
+                                   float *dq_gain, float *dk_gain, void *ws, uint64_t ws_bytes,
+                                   cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -41,6 +41,14 @@ after the current one first, or given `out`.
   rmsnorm_backward_i8               ("Verde与RepOps" §4.3, §5.3)
   rmsnorm_residual /                the edge between two blocks in one pass: norm,
   rmsnorm_residual_backward         gate, residual scale and sum, next norm
+  head_norm_rope /                  norms of the query and key heads with the rotation
+  head_norm_rope_backward           in the same pass, adjacent pairs or halves, part
+                                    of a head, positions of their own
+  token_logprobs /                  log probabilities of given tokens, entropy, the most
+  token_logprobs_backward           likely alternatives, and the logits' gradient
+  adamw(theta, grads, m, v, ...)    AdamW over many tensors at once, contributors'
+                                    gradients in a fixed order, moments in 32 bits or 8
+                                    ("Verde与RepOps" §4.3)
   host_empty(shape, dtype)          page-locked host memory in huge pages for the
                                     host-buffer calls (gemm_host, ..._host)
 """
@@ -51,7 +59,7 @@ import typing
 
 from . import _capi
 from ._capi import (ACT_GELU, ACT_NONE, LOADER_AUTO, LOADER_CPASYNC, LOADER_DIRECT, LOADER_TMA,
-                    MEAN_MAX_CONTRIBUTORS, TYPE_BF16, TYPE_F16, TYPE_F32, RepopsError, load)
+                    MEAN_MAX_CONTRIBUTORS, ROPE_ADJACENT, ROPE_HALVES, TYPE_BF16, TYPE_F16, TYPE_F32, RepopsError, load)
 
 __all__ = ["load", "version", "scratch_set_keep_bytes", "scratch_release", "scratch_reserved_bytes", "host_empty", "gemm", "gemm_chained", "gemm_auto_chained", "fixed_order_mean_sgd_host", "merkle_sha256_host", "attention_causal", "gemm_config_occupancy", "gemm_host", "gemm_config_count", "gemm_config_info",
            "gemm_auto_config", "gemm_small_output", "sha256_rate_probe", "sort_ids", "fixed_order_mean_sgd", "merkle_sha256",
@@ -63,6 +71,8 @@ __all__ = ["load", "version", "scratch_set_keep_bytes", "scratch_release", "scra
            "quantize_rows", "dequantize_rows", "swiglu_backward_i8", "rmsnorm_backward_i8",
            "rmsnorm_residual", "rmsnorm_residual_backward",
            "swiglu", "swiglu_backward", "rope_frequencies", "rope_table", "rope",
+           "head_norm_rope", "head_norm_rope_backward", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+           "adamw", "adamw_state", "adamw_scalars", "adamw_moments", "ADAMW_GROUP",
            "device_status", "set_thread_status_word", "RepopsError", "ACT_NONE", "ACT_GELU",
            "LOADER_AUTO", "LOADER_TMA", "LOADER_CPASYNC", "LOADER_DIRECT", "MEAN_MAX_CONTRIBUTORS"]
 
@@ -927,13 +937,22 @@ def swiglu_backward(g, u, dh, dg=None, du=None, *, stream=None):
     return dg, du
 
 
-def rope_frequencies(pairs: int, ln_base: float, device="cuda", *, stream=None):
+def rope_frequencies(pairs: int, ln_base: float, device="cuda", *, factor: float = 1.0, original: float = 0.0,
+                     low: float = 1.0, high: float = 4.0, stream=None):
     """f_i = exp(-((i / pairs) * ln_base)), i < pairs, with ln_base rounded to
-    binary32 (repops_rope_frequencies_f32)."""
+    binary32 (repops_rope_frequencies_f32).  factor != 1 scales them for contexts
+    that many times as long (repops_rope_scale_frequencies_f32): all of them by
+    1 / factor, or, given the original context's length, those that make at most
+    `low` turns in it wholly, those that make `high` not at all, and those between
+    in part."""
     import torch
     out = torch.empty(pairs, dtype=torch.float32, device=device)
     rc = load().repops_rope_frequencies_f32(pairs, ctypes.c_float(ln_base), out.data_ptr(), _stream_handle(stream))
     _capi.check(rc, "repops_rope_frequencies_f32")
+    if factor != 1.0:
+        rc = load().repops_rope_scale_frequencies_f32(pairs, out.data_ptr(), factor, original, low, high,
+                                                      _stream_handle(stream))
+        _capi.check(rc, "repops_rope_scale_frequencies_f32")
     return out
 
 
@@ -1523,3 +1542,121 @@ def token_logprobs_backward(logits, targets, stats, dlogp=None, dentropy=None, *
     if rc:
         _capi.check(rc, "repops_token_logprobs_backward")
     return out
+
+
+_LAYOUTS = {"adjacent": ROPE_ADJACENT, "halves": ROPE_HALVES}
+
+
+def _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period, name="x"):
+    """(rows, head width, storage type, pitch) of the heads in x, and the rotation's
+    arguments: (cos, sin, pairs, positions), (pos, wide, first, period)."""
+    import torch
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("%s must be a 2-D CUDA tensor with unit column stride" % name)
+    rows, width = x.shape
+    heads = q_heads + k_heads
+    if heads < 1 or width % heads or width == 0:
+        raise ValueError("%s must have one column block of the same width for each head" % name)
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be 'adjacent' or 'halves'")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    table = (None, None, 0, 0)
+    if cos is not None:
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous float32 positions x pairs tables")
+        table = (cos.data_ptr(), sin.data_ptr(), cos.shape[1], cos.shape[0])
+    if positions is None:
+        where = (None, 0, int(first), int(period) if period is not None else max(rows, 1))
+    else:
+        if positions.dtype not in (torch.int32, torch.int64) or positions.numel() != rows or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 or int64 tensor of one value a row")
+        where = (positions.data_ptr(), int(positions.dtype == torch.int64), 0, 1)
+    return rows, width // heads, _storage_type(x.dtype), _pitch(x, name), table, where
+
+
+def _head_gain(t, n, dim, name):
+    """The pointer of a gain of `dim` values, which n heads share (None without)."""
+    import torch
+    if t is None or n == 0:
+        return None
+    if t.dtype != torch.float32 or t.numel() != dim or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 vector of one value for each of a head's columns" % name)
+    return t.data_ptr()
+
+
+def head_norm_rope(x, q_heads: int, k_heads: int, cos=None, sin=None, *, q_gain=None, k_gain=None, eps: float = 1e-6,
+                   layout: str = "adjacent", positions=None, first: int = 0, period: int = None, inverse: bool = False,
+                   out=None, stream=None):
+    """Every head of x (rows, (q_heads + k_heads) * width; float32, float16 or
+    bfloat16 CUDA, unit column stride: the query and key columns of a qkv matrix)
+    normed with its gain and rotated to its row's position, in one pass
+    (repops_head_norm_rope): the bits of rmsnorm_rows on the heads and rope.
+
+    Without gains the rotation alone (inverse=True: its transpose), without cos and
+    sin (a rope_table) the norms alone.  A table of fewer than width / 2 pairs
+    rotates the first columns of each head; layout "adjacent" pairs (2i, 2i + 1),
+    "halves" (i, i + pairs).  positions: one for each row (int32 or int64), a
+    negative one leaves its row of out as it is; else first + (row mod period).
+    out may be x."""
+    import torch
+    rows, dim, kind, ld, table, where = _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if positions is None else torch.zeros_like(x)
+    if out.dtype != x.dtype or out.shape != x.shape or (out.shape[1] > 1 and out.stride(1) != 1):
+        raise ValueError("out must have the shape and dtype of x and unit column stride")
+    gains = [_head_gain(t, n, dim, name) for t, n, name in ((q_gain, q_heads, "q_gain"), (k_gain, k_heads, "k_gain"))]
+    handle = _stream_on_device(stream, x, cos, sin, q_gain, k_gain, positions, out)
+    rc = load().repops_head_norm_rope(rows, q_heads, k_heads, dim, x.data_ptr(), kind, ld, *gains, eps, *table,
+                                      _LAYOUTS[layout], int(bool(inverse)), *where, out.data_ptr(), _pitch(out, "out"),
+                                      handle)
+    if rc:
+        _capi.check(rc, "repops_head_norm_rope")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _head_workspace(rows, q_heads, k_heads, dim):
+    return load().repops_head_norm_rope_backward_workspace_bytes(rows, q_heads, k_heads, dim)
+
+
+def head_norm_rope_backward(dy, x, q_heads: int, k_heads: int, cos=None, sin=None, *, q_gain=None, k_gain=None,
+                            eps: float = 1e-6, layout: str = "adjacent", positions=None, first: int = 0,
+                            period: int = None, dx=None, dq_gain=None, dk_gain=None, stream=None):
+    """(dx, dq_gain, dk_gain) of head_norm_rope with gains given dy and its x
+    (repops_head_norm_rope_backward); an entry is None where there are no heads of
+    the kind.  dx may be dy; rows without a position add nothing to the gains'
+    gradients and are left as they are in dx.  Without gains the backward is
+    head_norm_rope(dy, ..., inverse=True)."""
+    import torch
+    rows, dim, kind, ld, table, where = _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if positions is None else \
+            torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+    for t, name in ((dy, "dy"), (dx, "dx")):
+        if t.dtype != x.dtype or t.shape != x.shape or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError("%s must have the shape and dtype of x and unit column stride" % name)
+    if (q_heads and q_gain is None) or (k_heads and k_gain is None):
+        raise ValueError("every kind of head needs its gain")
+    out = []
+    for n, t, d, name in ((q_heads, q_gain, dq_gain, "dq_gain"), (k_heads, k_gain, dk_gain, "dk_gain")):
+        if n == 0:
+            d = None
+        elif d is None:
+            d = torch.empty(dim, dtype=torch.float32, device=x.device)
+        out.append((d, _head_gain(t, n, dim, name[1:]), _head_gain(d, n, dim, name)))
+    (dq_gain, pq, pdq), (dk_gain, pk, pdk) = out
+    handle = _stream_on_device(stream, dy, x, cos, sin, q_gain, k_gain, positions, dx, dq_gain, dk_gain)
+    if rows == 0:
+        _zero_gradients(handle, dq_gain, dk_gain)
+        return dx, dq_gain, dk_gain
+    need = _head_workspace(rows, q_heads, k_heads, dim)
+    ws = _workspace(need, x.device, stream) if need else None
+    rc = load().repops_head_norm_rope_backward(rows, q_heads, k_heads, dim, dy.data_ptr(), kind, _pitch(dy, "dy"),
+                                               x.data_ptr(), ld, pq, pk, eps, *table, _LAYOUTS[layout], *where,
+                                               dx.data_ptr(), _pitch(dx, "dx"), pdq, pdk,
+                                               None if ws is None else ws.data_ptr(), need, handle)
+    if rc:
+        _capi.check(rc, "repops_head_norm_rope_backward")
+    return dx, dq_gain, dk_gain

@@ -125,6 +125,14 @@ SIGNATURES = {
                                      _vp, _vp]),
     "repops_token_logprobs_backward": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, ctypes.c_double, _vp, _vp, _vp, _vp,
                                               _i64, _vp]),
+    "repops_rope_scale_frequencies_f32": (_i32, [_i64, _vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                                 ctypes.c_double, _vp]),
+    "repops_head_norm_rope": (_i32, [_i64, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _i32,
+                                     _i32, _vp, _i32, _i64, _i64, _vp, _i64, _vp]),
+    "repops_head_norm_rope_backward_workspace_bytes": (_u64, [_i64, _i64, _i64, _i64]),
+    "repops_head_norm_rope_backward": (_i32, [_i64, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _f32, _vp,
+                                              _vp, _i64, _i64, _i32, _vp, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp,
+                                              _u64, _vp]),
     "repops_gemm_f32_batched": (_i32, [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
                                        _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
                                        ctypes.c_float, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
@@ -133,6 +141,7 @@ SIGNATURES = {
 
 ACT_NONE, ACT_GELU = 0, 1
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
 
 MERKLE_NOALLOC_SCRATCH_BYTES = 1 << 20
 

@@ -179,6 +179,22 @@ rope_kernel(int64_t rows, int heads, int pairs, float *x, int64_t ldx, const flo
     }
 }
 
+// Frequencies by parts for longer contexts, binary64 steps and one rounding.
+__global__ void __launch_bounds__(256)
+rope_scale_kernel(int64_t pairs, float *__restrict__ freq, double factor, double original, double low, double high) {
+    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < pairs; i += int64_t(gridDim.x) * blockDim.x) {
+        const double f = double(freq[i]), slow = __ddiv_rn(f, factor);
+        double v = slow;
+        if (original > 0.0) {
+            const double turns = __ddiv_rn(__dmul_rn(original, f), 6.283185307179586);
+            if (turns >= high) v = f;
+            else if (turns > low)
+                v = __dadd_rn(slow, __dmul_rn(__ddiv_rn(__dadd_rn(turns, -low), __dadd_rn(high, -low)), __dadd_rn(f, -slow)));
+        }
+        freq[i] = __double2float_rn(v);
+    }
+}
+
 // ------------------------------------------------------------------- host ----
 
 bool aligned16(const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0; }
@@ -240,6 +256,16 @@ extern "C" int repops_rope_frequencies_f32(int64_t pairs, float ln_base, float *
     if (pairs < 1 || pairs > (int64_t(1) << 24) || !freq) return REPOPS_ERR_INVALID_ARG;
     const int blocks = int(std::min<int64_t>((pairs + 255) / 256, 1024));
     rope_frequencies_kernel<<<blocks, 256, 0, stream>>>(pairs, ln_base, freq);
+    return check_launch();
+}
+
+extern "C" int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, double factor, double original, double low,
+                                                 double high, cudaStream_t stream) {
+    if (pairs < 1 || pairs > (int64_t(1) << 24) || !freq || !(factor > 0.0) || !(factor <= 1e300) || !(original >= 0.0) ||
+        !(original <= 1e300) || (original > 0.0 && !(low >= 0.0 && low < high && high <= 1e300)))
+        return REPOPS_ERR_INVALID_ARG;
+    const int blocks = int(std::min<int64_t>((pairs + 255) / 256, 1024));
+    rope_scale_kernel<<<blocks, 256, 0, stream>>>(pairs, freq, factor, original, low, high);
     return check_launch();
 }
 
