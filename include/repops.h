@@ -1115,11 +1115,11 @@ int repops_rmsnorm_residual_backward_f32(
 #define REPOPS_ADAMW_GROUP 128   /* elements that share a scale in 8-bit moments */
 
 /* The four words of a step that change from one to the next, on the host (no
- * launch): the binary32 values of lr, lr / (1 - beta1^step) and
- * 1 / sqrt(1 - beta2^step), computed in binary64, and the key of the step's
- * dither, fmix32(0x9E3779B9 * step + seed).  step >= 1, 0 <= beta < 1. */
-int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, uint32_t seed,
-                         uint32_t *scalars);
+ * launch), of rates (host): lr, beta1 and beta2 in binary64: the binary32 values of
+ * lr, lr / (1 - beta1^step) and 1 / sqrt(1 - beta2^step), computed in binary64, and
+ * the key of the step's dither, fmix32(0x9E3779B9 * step + seed).  step >= 1,
+ * 0 <= beta < 1. */
+int repops_adamw_scalars(int64_t step, const double *rates, uint32_t seed, uint32_t *scalars);
 
 /* One step of `tensors` tensors, in place.  Tensor i has sizes[i] elements
  * (0 is fine): theta[i] binary32; contributor c's gradient
@@ -1128,7 +1128,7 @@ int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, ui
  * REPOPS_ADAMW_GROUP of them (the last group may be shorter).  The arrays
  * themselves (sizes, theta, ..., decay: one weight decay a tensor, NULL for
  * none) are host memory, what they point to is device memory, each of any
- * alignment.  scalars: of repops_adamw_scalars, on the host, or with
+ * alignment.  hyper (host): beta1, beta2 and eps in binary64.  scalars: of repops_adamw_scalars, on the host, or with
  * scalars_on_device != 0 on the device (read by the kernels, so that a captured
  * graph can be replayed for step after step).  grad_scale: a device float that
  * multiplies the mean gradient (clipping), or NULL.
@@ -1159,9 +1159,8 @@ int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, ui
 int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
                  const void *const *grads, int grad_type, const int *order, void *const *m,
                  void *const *v, uint8_t *const *m_scale, uint8_t *const *v_scale,
-                 const float *decay, double beta1, double beta2, double eps,
-                 const uint32_t *scalars, int scalars_on_device, const float *grad_scale,
-                 cudaStream_t stream);
+                 const float *decay, const double *hyper, const uint32_t *scalars,
+                 int scalars_on_device, const float *grad_scale, cudaStream_t stream);
 
 /* The binary32 m and v = fl(r * r) that n elements of 8-bit moments stand for.
  * m_out and v_out must not overlap each other or an input (ALIAS). */
@@ -1206,7 +1205,7 @@ int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const ui
  * 16384000 columns or 2^27 rows; outputs must not overlap inputs or each other
  * (ALIAS). */
 int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
-                          const int64_t *targets, double temperature, int top, float *logp,
+                          const int64_t *targets, float temperature, int top, float *logp,
                           float *lse, float *entropy, float *stats, float *top_logp,
                           int64_t *top_ids, cudaStream_t stream);
 
@@ -1220,7 +1219,7 @@ int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, int x_type,
  * NaN.  A row of -infinities alone has the gradient 0.  dx may be x itself (same
  * pitch); any other overlap with an input is ALIAS.  Limits as the forward's. */
 int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, int x_type,
-                                   int64_t ldx, const int64_t *targets, double temperature,
+                                   int64_t ldx, const int64_t *targets, float temperature,
                                    const float *stats, const float *dlogp, const float *dentropy,
                                    void *dx, int64_t lddx, cudaStream_t stream);
 
@@ -1239,8 +1238,8 @@ int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, in
  * in binary64 (the weighted sum as f/factor + w * (f - f/factor)), rounded once.
  * original == 0: f / factor for all.  factor > 0, original >= 0, 0 <= low < high
  * (not looked at when original is 0), else INVALID_ARG. */
-int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, double factor, double original,
-                                      double low, double high, cudaStream_t stream);
+int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, float factor, float original,
+                                      float low, float high, cudaStream_t stream);
 
 /* For every row r and head h < q_heads + k_heads, the columns [h*dim, (h+1)*dim) of
  * row r of x (stored as `type`, widened exactly; rows at pitch ldx), each step one

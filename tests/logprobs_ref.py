@@ -51,7 +51,7 @@ def ln_fixed(S):
 
 def row(x, temperature):
     """(M, S, Q, ln S) of one row of binary32 logits."""
-    c = F32(LOG2E / temperature)
+    c = F32(LOG2E / float(F32(temperature)))
     V = len(x)
     segs = -(-V // SEGMENT)
     pad = np.full(segs * SEGMENT, -np.inf, F32)
@@ -86,7 +86,7 @@ def order(x):
 
 def forward(x, targets, temperature, top):
     """The library's results, bit for bit: logp, lse, entropy, stats, top_logp, top_ids."""
-    inv = 1.0 / temperature
+    inv = 1.0 / float(F32(temperature))
     out = [[] for _ in range(6)]
     for r, v in enumerate(x):
         M, S, Qs, ln = row(v, temperature)
@@ -113,7 +113,7 @@ def forward(x, targets, temperature, top):
 
 def backward(x, targets, stats, dlogp, dentropy, temperature):
     """The gradient in binary32 before it is narrowed, bit for bit."""
-    c, inv = F32(LOG2E / temperature), F32(1.0 / temperature)
+    c, inv = F32(LOG2E / float(F32(temperature))), F32(1) / F32(temperature)
     out = np.empty(x.shape, F32)
     with np.errstate(all="ignore"):
         for r, v in enumerate(x):
@@ -140,6 +140,7 @@ def backward(x, targets, stats, dlogp, dentropy, temperature):
 def forward64(x, targets, temperature):
     """{name: (value, bound)} of logp, lse, entropy and the matrices z and ln p for
     finite-or--inf rows with something possible, in binary64."""
+    temperature = float(F32(temperature))
     x = x.astype(F64)
     M = x.max(1, keepdims=True)
     with np.errstate(all="ignore"):
@@ -168,6 +169,7 @@ def forward64(x, targets, temperature):
 
 def backward64(x, targets, dlogp, dentropy, temperature):
     """(value, bound) of the gradient in binary64."""
+    temperature = float(F32(temperature))
     _, z, e, S, ln, H, dS = forward64(x, targets, temperature)
     f, _, _, _, _, _, _ = forward64(x, targets, temperature)
     dH = f["entropy"][1]

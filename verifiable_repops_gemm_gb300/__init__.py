@@ -1344,6 +1344,10 @@ def _address(a):
     return None if a is None else a.buffer_info()[0]
 
 
+def _doubles(*values):
+    return (ctypes.c_double * len(values))(*values)
+
+
 def adamw_scalars(step: int, lr: float, betas=(0.9, 0.999), seed: int = 0):
     """The four words of an AdamW step that change from one to the next, as a
     pinned int32 CPU tensor (repops_adamw_scalars): copied into a CUDA tensor and
@@ -1351,7 +1355,7 @@ def adamw_scalars(step: int, lr: float, betas=(0.9, 0.999), seed: int = 0):
     step."""
     import torch
     out = torch.empty(4, dtype=torch.int32, pin_memory=torch.cuda.is_available())
-    _capi.check(load().repops_adamw_scalars(int(step), lr, betas[0], betas[1], int(seed) & 0xFFFFFFFF, out.data_ptr()),
+    _capi.check(load().repops_adamw_scalars(int(step), _doubles(lr, *betas), int(seed) & 0xFFFFFFFF, out.data_ptr()),
                 "repops_adamw_scalars")
     return out
 
@@ -1427,7 +1431,7 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
         if step is None or lr is None:
             raise ValueError("step and lr, or scalars, must be given")
         words = (ctypes.c_uint32 * 4)()
-        _capi.check(L.repops_adamw_scalars(int(step), lr, betas[0], betas[1], int(seed) & 0xFFFFFFFF, words),
+        _capi.check(L.repops_adamw_scalars(int(step), _doubles(lr, *betas), int(seed) & 0xFFFFFFFF, words),
                     "repops_adamw_scalars")
     elif scalars.numel() != 4 or scalars.element_size() != 4 or not scalars.is_contiguous():
         raise ValueError("scalars must be a CUDA tensor of adamw_scalars' four words")
@@ -1440,8 +1444,8 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
         gp = array.array("Q", [t.data_ptr() for ts in zip(*grads) for t in ts])
     sizes, tp, mp, vp = array.array("q", sizes), _pointers(theta), _pointers(m), _pointers(v)
     rc = L.repops_adamw(n, _address(sizes), _address(tp), len(grads), _address(gp), kind, _address(order), _address(mp),
-                        _address(vp), _address(scale_ptrs[0]), _address(scale_ptrs[1]), _address(decay), betas[0],
-                        betas[1], eps, ctypes.addressof(words) if scalars is None else scalars.data_ptr(),
+                        _address(vp), _address(scale_ptrs[0]), _address(scale_ptrs[1]), _address(decay),
+                        _doubles(*betas, eps), ctypes.addressof(words) if scalars is None else scalars.data_ptr(),
                         int(scalars is not None), None if grad_scale is None else grad_scale.data_ptr(), handle)
     if rc:
         _capi.check(rc, "repops_adamw")

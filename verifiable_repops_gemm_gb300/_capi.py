@@ -117,16 +117,12 @@ SIGNATURES = {
     "repops_selftest_bounded_wait": (_i32, [_i64, _vp]),
     "repops_selftest_bounded_flag_wait": (_i32, [_i64, _vp]),
     "repops_softmax_rows_causal_f32": (_i32, [_i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp]),
-    "repops_adamw_scalars": (_i32, [_i64, ctypes.c_double, ctypes.c_double, ctypes.c_double, _u32, _vp]),
-    "repops_adamw": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_double,
-                            ctypes.c_double, ctypes.c_double, _vp, _i32, _vp, _vp]),
+    "repops_adamw_scalars": (_i32, [_i64, _vp, _u32, _vp]),
+    "repops_adamw": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "repops_adamw_moments": (_i32, [_i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
-    "repops_token_logprobs": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, ctypes.c_double, _i32, _vp, _vp, _vp, _vp, _vp,
-                                     _vp, _vp]),
-    "repops_token_logprobs_backward": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, ctypes.c_double, _vp, _vp, _vp, _vp,
-                                              _i64, _vp]),
-    "repops_rope_scale_frequencies_f32": (_i32, [_i64, _vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
-                                                 ctypes.c_double, _vp]),
+    "repops_token_logprobs": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "repops_token_logprobs_backward": (_i32, [_i64, _i64, _vp, _i32, _i64, _vp, _f32, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "repops_rope_scale_frequencies_f32": (_i32, [_i64, _vp, _f32, _f32, _f32, _f32, _vp]),
     "repops_head_norm_rope": (_i32, [_i64, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _f32, _vp, _vp, _i64, _i64, _i32,
                                      _i32, _vp, _i32, _i64, _i64, _vp, _i64, _vp]),
     "repops_head_norm_rope_backward_workspace_bytes": (_u64, [_i64, _i64, _i64, _i64]),

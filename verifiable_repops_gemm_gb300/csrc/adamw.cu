@@ -424,8 +424,9 @@ bool in_unit(double b) { return b >= 0.0 && b < 1.0; }
 
 using namespace repops;
 
-extern "C" int repops_adamw_scalars(int64_t step, double lr, double beta1, double beta2, uint32_t seed,
-                                    uint32_t *scalars) {
+extern "C" int repops_adamw_scalars(int64_t step, const double *rates, uint32_t seed, uint32_t *scalars) {
+    if (!rates) return REPOPS_ERR_INVALID_ARG;
+    const double lr = rates[0], beta1 = rates[1], beta2 = rates[2];
     if (step < 1 || !in_unit(beta1) || !in_unit(beta2) || !std::isfinite(lr) || !scalars) return REPOPS_ERR_INVALID_ARG;
     const float f[3] = {float(lr), float(lr / (1.0 - power(beta1, uint64_t(step)))),
                         float(1.0 / std::sqrt(1.0 - power(beta2, uint64_t(step))))};
@@ -436,9 +437,11 @@ extern "C" int repops_adamw_scalars(int64_t step, double lr, double beta1, doubl
 
 extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
                             const void *const *grads, int grad_type, const int *order, void *const *m, void *const *v,
-                            uint8_t *const *m_scale, uint8_t *const *v_scale, const float *decay, double beta1,
-                            double beta2, double eps, const uint32_t *scalars, int scalars_on_device,
+                            uint8_t *const *m_scale, uint8_t *const *v_scale, const float *decay,
+                            const double *hyper, const uint32_t *scalars, int scalars_on_device,
                             const float *grad_scale, cudaStream_t stream) {
+    if (!hyper) return REPOPS_ERR_INVALID_ARG;
+    const double beta1 = hyper[0], beta2 = hyper[1], eps = hyper[2];
     if (tensors < 0 || contributors < 1 || contributors > REPOPS_MEAN_MAX_CONTRIBUTORS || !known_storage(grad_type) ||
         !in_unit(beta1) || !in_unit(beta2) || !(eps >= 0.0) || !scalars || !order ||
         (m_scale != nullptr) != (v_scale != nullptr))
@@ -475,6 +478,7 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
             range(g, uint64_t(n) * gsize, false);
         }
     }
+    if (ranges.empty()) return REPOPS_OK;
     if (scalars_on_device) range(scalars, 16, false);
     if (grad_scale) range(grad_scale, 4, false);
     if (ranges_clash(ranges)) return REPOPS_ERR_ALIAS;

@@ -572,7 +572,7 @@ int launch_backward(const LpGradArgs &a, bool vec, cudaStream_t s) {
 constexpr int64_t kMostColumns = int64_t(16000) * kSegment;      // 187.5 KB of sums
 constexpr double kLog2e = 0x1.71547652b82fep+0;
 
-bool good_temperature(double t) { return t >= 1e-6 && t <= 1e6; }
+bool good_temperature(float t) { return t >= 1e-6f && t <= 1e6f; }
 
 }  // namespace
 }  // namespace repops
@@ -580,7 +580,7 @@ bool good_temperature(double t) { return t >= 1e-6 && t <= 1e6; }
 using namespace repops;
 
 extern "C" int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
-                                     const int64_t *targets, double temperature, int top, float *logp, float *lse,
+                                     const int64_t *targets, float temperature, int top, float *logp, float *lse,
                                      float *entropy, float *stats, float *top_logp, int64_t *top_ids,
                                      cudaStream_t stream) {
     if (rows < 0 || cols < 1 || !known_storage(x_type) || !good_temperature(temperature) || top < 0 || top > cols)
@@ -607,8 +607,8 @@ extern "C" int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, 
     a.rows = rows; a.cols = cols; a.ld = ldx;
     a.x = x;
     a.targets = targets;
-    a.c = float(kLog2e / temperature);
-    a.inv = 1.0 / temperature;
+    a.c = float(kLog2e / double(temperature));
+    a.inv = 1.0 / double(temperature);
     a.logp = logp; a.lse = lse; a.entropy = entropy; a.stats = stats;
     a.top = top; a.top_logp = top_logp; a.top_ids = top_ids;
     a.segments = int((cols + kSegment - 1) / kSegment);
@@ -628,7 +628,7 @@ extern "C" int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, 
 }
 
 extern "C" int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, int x_type, int64_t ldx,
-                                              const int64_t *targets, double temperature, const float *stats,
+                                              const int64_t *targets, float temperature, const float *stats,
                                               const float *dlogp, const float *dentropy, void *dx, int64_t lddx,
                                               cudaStream_t stream) {
     if (rows < 0 || cols < 1 || !known_storage(x_type) || !good_temperature(temperature)) return REPOPS_ERR_INVALID_ARG;
@@ -650,8 +650,8 @@ extern "C" int repops_token_logprobs_backward(int64_t rows, int64_t cols, const 
     a.x = x; a.dx = dx;
     a.targets = targets;
     a.stats = stats; a.dlogp = dlogp; a.dentropy = dentropy;
-    a.c = float(kLog2e / temperature);
-    a.inv = float(1.0 / temperature);
+    a.c = float(kLog2e / double(temperature));
+    a.inv = 1.0f / temperature;
     a.reads(x, xb);
     a.reads(targets, 2 * vb);
     a.reads(stats, 4 * vb);

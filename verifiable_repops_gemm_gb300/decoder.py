@@ -9,6 +9,8 @@ Layer (pre-norm, causal, grouped-query attention):
     qkv  = h W_qkv                                  one GEMM
     q, k = rotary(q, k)                             in place, the heads' pairs
                                                     rotated to each token's position
+                                                    (qk_norm: each head normed first,
+                                                    in the same pass)
     for every sequence (each GEMM call covers every query head; the
     `group` query heads of a key/value head share its K and V):
         S = (Q K^T) / sqrt(d_head)                  batched GEMM, alpha epilogue,
@@ -42,6 +44,11 @@ through a norm of its own, a learned gate and a residual scale before the
 residual sum -- x = x + s * (gate * RMSNorm(f)) -- and the edge between the two
 blocks, with the norm before the MLP, is one call (rmsnorm_residual).
 
+Queries and keys: `qk_norm` norms each head with a gain of its own kind (gq, gk)
+before the rotation; `rope_layout`, `rope_dim` and `rope_factor` choose which
+columns of a head pair up, how many are rotated, and frequencies for longer
+contexts (head_norm_rope, which does all of it in one pass).
+
 8-bit checkpoints: `activations(bits=8)` keeps x, qkv, the attention output
 and the MLP's input to its activation as 8-bit rows with a scale for every 128
 columns (about a quarter of their bytes), and no norm outputs, activations or
@@ -69,7 +76,7 @@ import torch
 from . import (gemm, gemm_batched, gelu, rmsnorm_rows, softmax_rows, ACT_GELU, colsum, gelu_backward,
                rmsnorm_backward, softmax_backward, swiglu, swiglu_backward, rope_frequencies, rope_table, rope,
                rmsnorm_residual, rmsnorm_residual_backward, quantize_rows, dequantize_rows, swiglu_backward_i8,
-               rmsnorm_backward_i8, gemm_i8)
+               rmsnorm_backward_i8, gemm_i8, head_norm_rope, head_norm_rope_backward)
 
 CHECKPOINT_GROUP = 128   # columns that share a scale in an 8-bit checkpoint
 
@@ -87,6 +94,11 @@ class DecoderConfig:
     post_norm: bool = False    # a norm after each block (gains p1, p2)
     gated: bool = False        # a learned gate on each block's output (a1, a2)
     residual_scale: float = 1.0  # the scale of a block's output in the residual sum
+    qk_norm: bool = False      # a norm of each query and key head before its rotation (gains gq, gk)
+    rope_layout: str = "adjacent"  # a rotation's pairs: "adjacent" (2i, 2i + 1) or "halves" (i, i + pairs)
+    rope_dim: int = 0          # columns of a head that are rotated, its first ones (0: all)
+    rope_factor: float = 1.0   # contexts this many times as long: scaled frequencies
+    rope_original: float = 0.0  # the original context's tokens (0: all frequencies scaled alike)
 
     @property
     def sandwich(self) -> bool:
@@ -95,6 +107,10 @@ class DecoderConfig:
     @property
     def d_head(self) -> int:
         return self.d // self.heads
+
+    @property
+    def qk_width(self) -> int:
+        return (self.heads + self.kv_heads) * self.d_head
 
     @property
     def qkv_width(self) -> int:
@@ -126,7 +142,12 @@ def weight_shapes(cfg: DecoderConfig) -> dict:
         out.update(p1=(d,), p2=(d,))
     if cfg.gated:
         out.update(a1=(d,), a2=(d,))
+    if cfg.qk_norm:
+        out.update(gq=(cfg.d_head,), gk=(cfg.d_head,))
     return out
+
+
+GAINS = ("g1", "g2", "p1", "p2", "a1", "a2", "gq", "gk")
 
 
 def init_weights(cfg: DecoderConfig, seed: int, device) -> dict:
@@ -137,26 +158,53 @@ def init_weights(cfg: DecoderConfig, seed: int, device) -> dict:
     out = {}
     for name, shape in weight_shapes(cfg).items():
         t = torch.randn(shape, generator=g, device=device, dtype=torch.float32)
-        out[name] = t * 0.1 + 1.0 if name in ("g1", "g2", "p1", "p2", "a1", "a2") else t * 0.02
+        out[name] = t * 0.1 + 1.0 if name in GAINS else t * 0.02
     return out
 
 
 def rope_tables(cfg: DecoderConfig, device):
-    """(cos, sin), seq_len x d_head/2, of the layer's rotary embedding, or
-    None when it is off: frequencies base^(-2i/d_head) from the binary32
-    value of ln(base), angles p * f_i for positions p < seq_len."""
+    """(cos, sin), seq_len x pairs, of the layer's rotary embedding, or None when
+    it is off: pairs = rope_dim/2 (d_head/2), frequencies base^(-i/pairs) from the
+    binary32 value of ln(base), scaled where rope_factor asks for it, angles
+    p * f_i for positions p < seq_len."""
     if not cfg.rope_base:
         return None
-    freq = rope_frequencies(cfg.d_head // 2, math.log(cfg.rope_base), device)
+    freq = rope_frequencies((cfg.rope_dim or cfg.d_head) // 2, math.log(cfg.rope_base), device,
+                            factor=cfg.rope_factor, original=cfg.rope_original)
     return rope_table(cfg.seq_len, freq)
 
 
-def _rotate(qkv, cfg: DecoderConfig, tables, inverse: bool):
-    """The rotary embedding (or its transpose) of the query and key heads:
-    columns [0, (heads + kv_heads) * d_head) of every row, position = the row's
-    index within its sequence."""
-    if tables is not None:
-        rope(qkv, cfg.heads + cfg.kv_heads, tables[0], tables[1], first=0, period=cfg.seq_len, inverse=inverse)
+def _turn(cfg: DecoderConfig, tables):
+    """head_norm_rope's keyword arguments for the layer's rotation."""
+    cos, sin = tables if tables is not None else (None, None)
+    return dict(cos=cos, sin=sin, layout=cfg.rope_layout, period=cfg.seq_len)
+
+
+def _rotate(qkv, w: dict, cfg: DecoderConfig, tables):
+    """The norms (qk_norm) and the rotary embedding of the query and key heads,
+    in place: columns [0, (heads + kv_heads) * d_head) of every row, position =
+    the row's index within its sequence."""
+    if cfg.qk_norm or cfg.rope_layout != "adjacent" or cfg.rope_dim:
+        qk = qkv[:, :cfg.qk_width]
+        gains = dict(q_gain=w["gq"], k_gain=w["gk"], eps=cfg.eps) if cfg.qk_norm else {}
+        head_norm_rope(qk, cfg.heads, cfg.kv_heads, out=qk, **gains, **_turn(cfg, tables))
+    elif tables is not None:
+        rope(qkv, cfg.heads + cfg.kv_heads, tables[0], tables[1], first=0, period=cfg.seq_len)
+
+
+def _rotate_backward(dqkv, qk, w: dict, cfg: DecoderConfig, tables, g: dict, o: dict):
+    """_rotate's backward in place on dqkv; with qk_norm from the heads before
+    their norms (qk), the gains' gradients into g."""
+    if cfg.qk_norm:
+        d = dqkv[:, :cfg.qk_width]
+        _, g["gq"], g["gk"] = head_norm_rope_backward(d, qk, cfg.heads, cfg.kv_heads, q_gain=w["gq"], k_gain=w["gk"],
+                                                      eps=cfg.eps, dx=d, dq_gain=o.get("gq"), dk_gain=o.get("gk"),
+                                                      **_turn(cfg, tables))
+    elif cfg.rope_layout != "adjacent" or cfg.rope_dim:
+        d = dqkv[:, :cfg.qk_width]
+        head_norm_rope(d, cfg.heads, cfg.kv_heads, out=d, inverse=True, **_turn(cfg, tables))
+    elif tables is not None:
+        rope(dqkv, cfg.heads + cfg.kv_heads, tables[0], tables[1], first=0, period=cfg.seq_len, inverse=True)
 
 
 def _after(stream, *others):
@@ -279,7 +327,9 @@ def forward(x, w: dict, cfg: DecoderConfig, *, fused: bool = True, gelu_epilogue
         h, qkv, attn, a = ws["h"], ws["qkv"], ws["attn"], ws["a"]
     rmsnorm_rows(x, w["g1"], cfg.eps, out=h)
     gemm(h, w["w_qkv"], out=qkv)
-    _rotate(qkv, cfg, ws["rope"], inverse=False)
+    if cfg.qk_norm and save is not None:
+        save["qk"].copy_(qkv[:, :cfg.qk_width])
+    _rotate(qkv, w, cfg, ws["rope"])
     attention(qkv, cfg, attn, ws["scores"], save["probs"] if save is not None else None, ws.get("streams"),
               fused=fused_attention)
     if cfg.sandwich:
@@ -393,8 +443,11 @@ def _forward_checkpointed(x, w, cfg: DecoderConfig, ws, save, fused, fused_atten
     _keep(save, "x0", x)
     rmsnorm_rows(x, w["g1"], cfg.eps, out=h)
     gemm(h, w["w_qkv"], out=qkv)
-    _rotate(qkv, cfg, ws["rope"], inverse=False)
-    _keep(save, "qkv", qkv)
+    if cfg.qk_norm:                          # the heads' norms are computed again from what they normed
+        _keep(save, "qkv", qkv)
+    _rotate(qkv, w, cfg, ws["rope"])
+    if not cfg.qk_norm:
+        _keep(save, "qkv", qkv)
     attention(qkv, cfg, attn, ws["scores"], None, ws.get("streams"), fused=fused_attention)
     _keep(save, "attn", attn)
     if cfg.sandwich:
@@ -461,7 +514,7 @@ def forward_i8(x, w: dict, w8: dict, cfg: DecoderConfig, *, work: dict = None, f
 
     h = rmsnorm_rows(x, w["g1"], cfg.eps, out=ws["h"])
     qkv = product(h, "w_qkv", ws["qkv"])
-    _rotate(qkv, cfg, ws["rope"], inverse=False)
+    _rotate(qkv, w, cfg, ws["rope"])
     attention(qkv, cfg, ws["attn"], ws["scores"], None, ws.get("streams"), fused=fused_attention)
     _edge(x, product(ws["attn"], "w_o", ws["tmp_d"]), w, cfg, 1, h)
     if cfg.mlp == "swiglu":
@@ -508,6 +561,8 @@ def activations(cfg: DecoderConfig, tokens: int, device, bits: int = 32) -> dict
         out["pre"] = torch.empty(tokens, cfg.ffn, **e)
     if cfg.sandwich:
         out.update(f1=torch.empty(tokens, cfg.d, **e), f2=torch.empty(tokens, cfg.d, **e))
+    if cfg.qk_norm:
+        out["qk"] = torch.empty(tokens, cfg.qk_width, **e)
     return out
 
 
@@ -533,7 +588,8 @@ def backward(dy, w: dict, cfg: DecoderConfig, saved: dict, *, work: dict = None,
             dS_h = causal softmax'(P_h; dP_h)
             dQ_h = s dS_h K_k (k <= i);  dK_k = sum_h s dS_h^T Q_h (head order,
             k >= i), s = 1/sqrt(d_head)
-        dq, dk rotated back (the rotary embedding's transpose)
+        dq, dk rotated back (the rotary embedding's transpose; with qk_norm the
+        heads' norms too, and dgq, dgk)
         dW_qkv = h1^T dqkv, dh1 = dqkv W_qkv^T
         dx0 = RMSNorm'(x0; dh1) + dx1, dg1 = colsum(dh1 * xhat1)
 
@@ -591,14 +647,14 @@ def backward(dy, w: dict, cfg: DecoderConfig, saved: dict, *, work: dict = None,
         g["w_gu" if cfg.mlp == "swiglu" else "w_up"] = gemm(ws["h"].t(), dgu,
                                                             out=o.get("w_gu" if cfg.mlp == "swiglu" else "w_up"))
         attn = _restore(saved, "attn", ws["attn"])
-        saved = _recomputed_attention(saved, cfg, ws)
+        saved = _recomputed_attention(saved, w, cfg, ws)
     else:
         attn = saved["attn"]
     g["w_o"] = gemm(attn.t(), dblock, out=o.get("w_o"))
     dattn = gemm(dblock, w["w_o"].t(), out=ws["t_d"])
     _attention_backward(dattn, ws["dqkv"], saved, cfg, ws["dp"], ws.get("streams"))
     dqkv = ws["dqkv"]
-    _rotate(dqkv, cfg, ws["rope"], inverse=True)
+    _rotate_backward(dqkv, saved.get("qk"), w, cfg, ws["rope"], g, o)
     if kept8:
         dh1 = gemm(dqkv, w["w_qkv"].t(), out=ws["t_d"])
         q, s = saved["x0"]
@@ -648,11 +704,15 @@ def _mlp_backward_i8(dm, w, cfg: DecoderConfig, saved, ws, g: dict, o: dict):
     return dpre, gemm(dpre, w["w_up"].t(), out=ws["t_d"]), a
 
 
-def _recomputed_attention(saved, cfg: DecoderConfig, ws):
-    """saved with qkv restored and every head's probabilities computed again
-    from it (the forward's product and causal softmax)."""
+def _recomputed_attention(saved, w: dict, cfg: DecoderConfig, ws):
+    """saved with qkv restored (its heads normed and rotated again where they were
+    kept before their norms) and every head's probabilities computed again from it
+    (the forward's product and causal softmax)."""
     S, dh, kv, H = cfg.seq_len, cfg.d_head, cfg.kv_heads, cfg.heads
     qkv = _restore(saved, "qkv", ws["qkv"])
+    if cfg.qk_norm:
+        ws["qk"].copy_(qkv[:, :cfg.qk_width])
+        _rotate(qkv, w, cfg, ws["rope"])
     for s in range(qkv.shape[0] // S):
         rows = slice(s * S, (s + 1) * S)
         sc = ws["probs"][s * kv:(s + 1) * kv].view(H, S, S)
@@ -660,7 +720,7 @@ def _recomputed_attention(saved, cfg: DecoderConfig, ws):
                      alpha=1.0 / float(dh) ** 0.5, causal_first=0)
         P = sc.view(H * S, S)
         softmax_rows(P, out=P, causal_first=0, causal_period=S)
-    return dict(saved, qkv=qkv, probs=ws["probs"])
+    return dict(saved, qkv=qkv, probs=ws["probs"], qk=ws.get("qk"))
 
 
 def _attention_backward(dattn, dqkv, saved, cfg: DecoderConfig, dp, streams):
@@ -751,6 +811,8 @@ def backward_workspace(cfg: DecoderConfig, tokens: int, device, bits: int = 32) 
             out["pre"] = torch.empty(tokens, cfg.ffn, **e)
         if cfg.sandwich:
             out["t_f"] = torch.empty(tokens, cfg.d, **e)
+        if cfg.qk_norm:
+            out["qk"] = torch.empty(tokens, cfg.qk_width, **e)
     return out
 
 
