@@ -1186,20 +1186,24 @@ int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const ui
  * Logits of -infinity are impossible (log probability -infinity, no part in the
  * sums); a row of nothing else has lse -infinity, entropy 0 and 1 / S = 0.  A row
  * with a NaN or +infinity gives NaN (its alternatives: NaN above everything).
- * Arithmetic, binary32 with one rounding a step unless named: c = fl(log2(e) / T),
- *   t(x; m) = max(fl(fl(x - m) * c), -127),  k = rint(t),  f = t - k,
- *   e(x; m) = fl((1 + f*q(f) by Horner's rule) * 2^k), +0 at k = -127, with q's
- *   coefficients (highest first) 0x1.5bba14p-10, 0x1.3cea88p-7, 0x1.c6b752p-5,
- *   0x1.ebf9bcp-3, 0x1.62e42ap-1;
- *   every 1024 columns: m their maximum (0 in the place of -infinity inside e and
- *   t), s = sum e, u = sum fl(e * t): for each residue of the column modulo 256
- *   the columns in order from +0, then residue r + residue r + 128, .. + 64, ...;
- *   the row in binary64: S = sum w*s, Q = sum w*(u + t(m; M)*s), w = e(m; M), the
- *   segments of a residue modulo 32 in order from +0, then r + (r + 16), ...;
- *   ln S = E*ln2 + 2z*(1 + z^2/3 + ... + z^22/23) by Horner's rule, S = F * 2^E,
- *   F in [sqrt(1/2), sqrt(2)], z = (F - 1) / (F + 1);
- *   lse = M*(1/T) + ln S,  logp = (x_t - M)*(1/T) - ln S,  H = ln S - ln2*(Q/S),
- *   rounded once to binary32.
+ * Arithmetic, binary32 with one rounding a step: c = fl(log2(e) / T),
+ *   t(x; m) = max(fl(fl(x - m) * c), -127),  n = rint(32 * t),  f = t - n/32,
+ *   e(x; m) = fl((1 + f*(a + f*b) by Horner's rule) * w), b = 0x1.ebfbe0p-3, a =
+ *   0x1.62e584p-1, w the value with the bits of fl(2^(j/32)), j = n mod 32, plus
+ *   (n - j)/32 in the exponent (+0 at t = -127);
+ *   every 4096 columns, in blocks of 1024 and with m the maximum so far (0 in the
+ *   place of -infinity inside e and t): where a block raises m to m', with w =
+ *   e(m; m') and d = t(m; m'), u = fl(w * fl(u + fl(d * s))) and s = fl(w * s) (no
+ *   step where it does not); then s += e, u += fl(e * t), for each residue of the
+ *   column modulo 256 the columns in order, all from +0; at the end residue r +
+ *   residue r + 128, .. + 64, ...;
+ *   the row: S = sum w*s, Q = sum w*(u + t(m; M)*s), w = e(m; M), the 4096s of a
+ *   residue modulo 32 in order from +0, then r + (r + 16), ...;
+ *   ln S = E*0x1.62e4p-1 + ((r + r*(zz*p)) + E*0x1.7f7d1cp-20), S = F * 2^E, F at most
+ *   0x1.6a09e6p+0 and more than half of that, z = (F - 1) / (F + 1), r = z + z, zz = z*z,
+ *   p = 1/3 + zz*(1/5 + zz*(1/7 + zz*(1/9))) by Horner's rule;
+ *   i = fl(1/T), lse = M*i + ln S,  logp = (x_t - M)*i - ln S,  H = ln S -
+ *   0x1.62e43p-1*(Q/S).
  * Row pitch ldx >= cols; stats on a 16-byte boundary.  1 <= cols, 0 <= top <= cols,
  * 1e-6 <= T <= 1e6, else INVALID_ARG; UNSUPPORTED for top above 32, more than
  * 16384000 columns or 2^27 rows; outputs must not overlap inputs or each other
@@ -1211,10 +1215,10 @@ int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, int x_type,
 
 /* dx, the gradient of the logits, given dlogp and dentropy (rows floats each, one
  * of them may be NULL), with the forward's stats:
- *   p = fl(e(x; M) * (1/S)),  i = fl(1/T)
- *   A = -fl(i * fl(dlogp + fl(dentropy * fl(H - ln S)))),  B = -fl(fl(i * ln2) * dentropy)
- *   dx = fl(p * fl(A + fl(B * t(x; M)))), at the target fl(dx + fl(i * dlogp))
- * narrowed once to x_type (without dentropy: fl(p * A), A = -fl(i * dlogp)).  A
+ *   i = fl(1/T),  A = -fl(fl(i * fl(dlogp + fl(dentropy * fl(H - ln S)))) * 1/S),
+ *   B = -fl(fl(fl(i * 0x1.62e43p-1) * dentropy) * 1/S)
+ *   dx = fl(e(x; M) * fl(A + fl(B * t(x; M)))), at the target fl(dx + fl(i * dlogp))
+ * narrowed once to x_type (without dentropy: fl(e * A), A = -fl(fl(i * dlogp) * 1/S)).  A
  * negative target has dlogp 0 whatever is given; one of cols or more makes its row
  * NaN.  A row of -infinities alone has the gradient 0.  dx may be x itself (same
  * pitch); any other overlap with an input is ALIAS.  Limits as the forward's. */

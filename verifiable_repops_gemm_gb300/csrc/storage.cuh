@@ -42,6 +42,18 @@ __device__ __forceinline__ uint32_t narrowed(float v) {
     else return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Two half-precision values in a word, the first in the low half.
+template <int TY>
+__device__ __forceinline__ uint32_t narrowed2(float lo, float hi) {
+    if constexpr (TY == REPOPS_TYPE_F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
 template <int TY>
 __device__ __forceinline__ void store_one(const DbgAccess &d, void *p, int64_t i, float v) {
     if constexpr (TY == REPOPS_TYPE_F32) store_global(d, static_cast<float *>(p) + i, v);
