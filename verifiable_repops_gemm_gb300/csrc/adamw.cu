@@ -27,7 +27,11 @@
 //
 // Bytes an element: 12 + 16 with moments in 32 bits, 12 + 4 + 1/32 in 8 (binary32
 // gradients); no order is left open, as elements are independent and a group's
-// largest value does not depend on how it is found.
+// largest value does not depend on how it is found.  32-bit moments run at the
+// memory's rate (60.8 M elements 245 us, 6.9 TB/s); 8-bit ones are bound by the
+// instructions of a square root, a quotient, two codes and their dither (about 120 an
+// element with four gradients, 79% of the issue rate): 183 us with one gradient,
+// 254 with four in bfloat16.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -86,69 +90,81 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
     return h ^ (h >> 16);
 }
 
-#define REPOPS_ADAM_OK(base, n, size, p, bytes) \
-    REPOPS_DBG_OK((DbgSpan{reinterpret_cast<uintptr_t>(base), reinterpret_cast<uintptr_t>(base) + uint64_t(n) * (size)}), p, bytes, status)
+// A span of a tensor: what a tile may touch of one of its arrays (checked build).
+struct Tile {
+    int left;                        // elements of the tensor from the tile's first on
+    bool vec;                        // four elements an access
+    unsigned *status;
+};
+#define REPOPS_ADAM_OK(tile, base, size, p, bytes)                                                             \
+    REPOPS_DBG_OK((DbgSpan{reinterpret_cast<uintptr_t>(base), reinterpret_cast<uintptr_t>(base) + uint64_t((tile).left) * (size)}), \
+                  p, bytes, (tile).status)
 
-// Elements e .. e+3 of a tensor, `have` of them there (1 .. 4); the others +0.
-template <int TY>
-__device__ __forceinline__ float4 load4(const void *base, int64_t n, int64_t e, int have, bool vec,
-                                        [[maybe_unused]] unsigned *status) {
+// Elements e .. e+3 of a tile, `have` of them there (0 .. 4); the others +0.  FULL: all
+// four, aligned, asked about once for the tile.
+template <int TY, bool FULL>
+__device__ __forceinline__ float4 load4(const Tile &t, const void *base, int e, int have) {
     constexpr unsigned size = TY == REPOPS_TYPE_F32 ? 4 : 2;
-    const char *p = static_cast<const char *>(base) + e * size;
-    if (vec && have == 4) {
-        if (!REPOPS_ADAM_OK(base, n, size, p, 4 * size)) return make_float4(0, 0, 0, 0);
+    const char *p = static_cast<const char *>(base) + e * int(size);
+    if (FULL || (t.vec && have == 4)) {
+        if (!REPOPS_ADAM_OK(t, base, size, p, 4 * size)) return make_float4(0, 0, 0, 0);
         return load_four<TY>(DbgAccess{}, p, 0);
     }
-    float v[4];
+    float v[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = i < have && REPOPS_ADAM_OK(base, n, size, p + i * size, size) ? load_one<TY>(DbgAccess{}, p, i) : 0.0f;
+    for (int i = 0; i < (FULL ? 0 : 4); ++i)
+        if (i < have && REPOPS_ADAM_OK(t, base, size, p + i * size, size)) v[i] = load_one<TY>(DbgAccess{}, p, i);
     return make_float4(v[0], v[1], v[2], v[3]);
 }
 
-__device__ __forceinline__ void store4(float *base, int64_t n, int64_t e, int have, bool vec, float4 v,
-                                       [[maybe_unused]] unsigned *status) {
+template <bool FULL>
+__device__ __forceinline__ void store4(const Tile &t, float *base, int e, int have, float4 v) {
     float *p = base + e;
-    if (vec && have == 4) {
-        if (REPOPS_ADAM_OK(base, n, 4, p, 16)) store_four<REPOPS_TYPE_F32>(DbgAccess{}, p, 0, v);
+    if (FULL || (t.vec && have == 4)) {
+        if (REPOPS_ADAM_OK(t, base, 4, p, 16)) store_four<REPOPS_TYPE_F32>(DbgAccess{}, p, 0, v);
         return;
     }
     const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(base, n, 4, p + i, 4)) p[i] = a[i];
+        if (i < have && REPOPS_ADAM_OK(t, base, 4, p + i, 4)) p[i] = a[i];
 }
 
-__device__ __forceinline__ uint32_t load_codes(const void *base, int64_t n, int64_t e, int have, bool vec,
-                                               [[maybe_unused]] unsigned *status) {
-    const uint8_t *p = static_cast<const uint8_t *>(base) + e;
-    if (vec && have == 4) return REPOPS_ADAM_OK(base, n, 1, p, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(p)) : 0u;
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const Tile &t, const uint8_t *base, int e, int have) {
+    const uint8_t *p = base + e;
+    if (FULL || (t.vec && have == 4))
+        return REPOPS_ADAM_OK(t, base, 1, p, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(p)) : 0u;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(base, n, 1, p + i, 1)) w |= uint32_t(p[i]) << (8 * i);
+        if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) w |= uint32_t(p[i]) << (8 * i);
     return w;
 }
 
-__device__ __forceinline__ void store_codes(void *base, int64_t n, int64_t e, int have, bool vec, uint32_t w,
-                                            [[maybe_unused]] unsigned *status) {
-    uint8_t *p = static_cast<uint8_t *>(base) + e;
-    if (vec && have == 4) {
-        if (REPOPS_ADAM_OK(base, n, 1, p, 4)) __stcs(reinterpret_cast<uint32_t *>(p), w);
+template <bool FULL>
+__device__ __forceinline__ void store_codes(const Tile &t, uint8_t *base, int e, int have, uint32_t w) {
+    uint8_t *p = base + e;
+    if (FULL || (t.vec && have == 4)) {
+        if (REPOPS_ADAM_OK(t, base, 1, p, 4)) __stcs(reinterpret_cast<uint32_t *>(p), w);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(base, n, 1, p + i, 1)) p[i] = uint8_t(w >> (8 * i));
+        if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) p[i] = uint8_t(w >> (8 * i));
 }
 
 // ------------------------------------------------------------ 8-bit codes ----
 
 // A code's bits as the exponent and mantissa of a binary32 number are the code's
 // value times a power of two, its subnormals included: exact products give it back.
-__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
-    const float y = __fmul_rn(__fmul_rn(__uint_as_float((c & 0x7fu) << 20), 0x1p+120f), scale);
-    return __uint_as_float(__float_as_uint(y) ^ ((c & 0x80u) << 24));
+// (e4m3 has conversion instructions, its values are binary16's as well.)
+__device__ __forceinline__ void decode_m(uint32_t c, float scale, float4 &v) {
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(uint16_t(c)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(uint16_t(c >> 16)));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    v = make_float4(__fmul_rn(a.x, scale), __fmul_rn(a.y, scale), __fmul_rn(b.x, scale), __fmul_rn(b.y, scale));
 }
 __device__ __forceinline__ float decode_r(uint32_t c, float scale) {
     return __fmul_rn(__fmul_rn(__uint_as_float((c & 0xffu) << 19), 0x1p+112f), scale);
@@ -176,6 +192,10 @@ __device__ __forceinline__ uint32_t encode_r(float r, float inv, uint32_t dither
     return c == 0 && y != 0 ? 1u : c;
 }
 
+__device__ __forceinline__ uint32_t packed(const uint32_t (&c)[4]) {
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+
 // ----------------------------------------------------------------- kernel ----
 
 struct Step {
@@ -198,105 +218,149 @@ __device__ __forceinline__ void add4(float4 &a, float4 b) {
     a.w = __fadd_rn(a.w, b.w);
 }
 
-// U vectors of four elements a thread are in flight together.
-template <int TY, bool EIGHT, bool MANY, int U>
+// CTAs an SM: 8-bit moments and several gradients hide their loads behind many warps of
+// one vector a thread (60.8 M elements, four binary32 gradients: 343 us with 32-bit
+// moments, 250 with 8-bit; two vectors and four CTAs: 359 and 274); one gradient and
+// 32-bit moments behind two vectors (245 us either way).
+template <bool EIGHT, bool MANY>
+constexpr int kCtas = EIGHT || MANY ? 5 : 1;
+
+// U vectors of four elements a thread are in flight together, and with several
+// contributors those of four of them.  FULL: a whole tile of aligned tensors.
+template <int TY, bool EIGHT, bool MANY, bool FULL>
 __device__ __forceinline__ void run_tile(const AdamHead &h, const Entry &t, int64_t base, const Step &k, uint32_t key,
                                          float gscale, bool scaled) {
+    constexpr int U = EIGHT || MANY ? 1 : 2, kPart = kThreads * 4 * U;
+    constexpr unsigned gsize = TY == REPOPS_TYPE_F32 ? 4 : 2;
     const int lane = threadIdx.x & 31;
-    unsigned *status = h.status;
+    const Tile tile{int(min(int64_t(kTile), t.n - base)), t.vec, h.status};
+    float *theta_at = t.theta + base;
+    char *m_at = static_cast<char *>(t.m) + base * (EIGHT ? 1 : 4), *v_at = static_cast<char *>(t.v) + base * (EIGHT ? 1 : 4);
+    uint8_t *ms_at = t.ms + base / kGroup, *vs_at = t.vs + base / kGroup;
+    // a tile's scales, read and written at once: a byte here and there of lines that other
+    // CTAs write to as well cost microseconds each
+    constexpr int kScales = kTile / kGroup;
+    __shared__ uint32_t scales[2][kScales];
+    const int groups = (tile.left + kGroup - 1) / kGroup;
+    if constexpr (EIGHT) {
+        if (int(threadIdx.x) < 2 * kScales) {
+            const int i = threadIdx.x % kScales;
+            scales[threadIdx.x / kScales][i] = i < groups ? (int(threadIdx.x) < kScales ? ms_at : vs_at)[i] : 0;
+        }
+        __syncthreads();
+    }
+    const int64_t gradient_at = base * gsize;
+    auto gradient = [&](int c) { return reinterpret_cast<const char *>(t.grads[c]) + gradient_at; };
 #pragma unroll 1
-    for (int part = 0; part < kTile / (kThreads * 4 * U); ++part) {
-        const int64_t first = base + int64_t(part) * (kThreads * 4 * U) + threadIdx.x * 4;
-        if (base + int64_t(part) * (kThreads * 4 * U) >= t.n) return;      // the same for the whole CTA
+    for (int part = 0; part < kTile; part += kPart) {
+        if (!FULL && part >= tile.left) break;                   // the same for the whole CTA
+        const int first = part + int(threadIdx.x) * 4;
         float4 theta[U], g[U], m[U], v[U];
-        uint32_t mc[U], vc[U];
-        float ms[U], vs[U];
+        uint32_t mc[U], vc[U], ms[U], vs[U];
         int have[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int64_t e = first + j * (kThreads * 4);
-            have[j] = int(max(int64_t(0), min(int64_t(4), t.n - e)));
-            g[j] = load4<TY>(reinterpret_cast<const void *>(t.grads[0]), t.n, e, have[j], t.vec, status);
-            theta[j] = load4<REPOPS_TYPE_F32>(t.theta, t.n, e, have[j], t.vec, status);
+            const int e = first + j * (kThreads * 4);
+            have[j] = FULL ? 4 : max(0, min(4, tile.left - e));
+            g[j] = load4<TY, FULL>(tile, gradient(0), e, have[j]);
+            theta[j] = load4<REPOPS_TYPE_F32, FULL>(tile, theta_at, e, have[j]);
             if constexpr (EIGHT) {
-                mc[j] = load_codes(t.m, t.n, e, have[j], t.vec, status);
-                vc[j] = load_codes(t.v, t.n, e, have[j], t.vec, status);
-                [[maybe_unused]] const int64_t groups = (t.n + kGroup - 1) / kGroup;
-                const int64_t q = e / kGroup;
-                const bool in = have[j] > 0 && REPOPS_ADAM_OK(t.ms, groups, 1, t.ms + q, 1) &&
-                                REPOPS_ADAM_OK(t.vs, groups, 1, t.vs + q, 1);
-                ms[j] = scale_of(in ? t.ms[q] : 0);
-                vs[j] = scale_of(in ? t.vs[q] : 0);
+                mc[j] = load_codes<FULL>(tile, reinterpret_cast<uint8_t *>(m_at), e, have[j]);
+                vc[j] = load_codes<FULL>(tile, reinterpret_cast<uint8_t *>(v_at), e, have[j]);
+                ms[j] = scales[0][e / kGroup];
+                vs[j] = scales[1][e / kGroup];
             } else {
-                m[j] = load4<REPOPS_TYPE_F32>(t.m, t.n, e, have[j], t.vec, status);
-                v[j] = load4<REPOPS_TYPE_F32>(t.v, t.n, e, have[j], t.vec, status);
+                m[j] = load4<REPOPS_TYPE_F32, FULL>(tile, m_at, e, have[j]);
+                v[j] = load4<REPOPS_TYPE_F32, FULL>(tile, v_at, e, have[j]);
             }
         }
         if constexpr (MANY) {
-#pragma unroll 4
-            for (int c = 1; c < h.contributors; ++c) {
-                const void *p = reinterpret_cast<const void *>(t.grads[c]);
+            constexpr int B = 4;
+            for (int c = 1; c < h.contributors; c += B) {
+                float4 w[B][U];
 #pragma unroll
-                for (int j = 0; j < U; ++j)
-                    add4(g[j], load4<TY>(p, t.n, first + j * (kThreads * 4), have[j], t.vec, status));
+                for (int i = 0; i < B; ++i)
+                    if (c + i < h.contributors)
+#pragma unroll
+                        for (int j = 0; j < U; ++j)
+                            w[i][j] = load4<TY, FULL>(tile, gradient(c + i), first + j * (kThreads * 4), have[j]);
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+                    if (c + i < h.contributors)
+#pragma unroll
+                        for (int j = 0; j < U; ++j) add4(g[j], w[i][j]);
             }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const int64_t e = first + j * (kThreads * 4);
+            const int e = first + j * (kThreads * 4);
             float *gj = &g[j].x, *tj = &theta[j].x, *mj = &m[j].x, *vj = &v[j].x;
             float r[4];
+            if constexpr (EIGHT) {
+                decode_m(mc[j], scale_of(ms[j]), m[j]);
+                const float rs = scale_of(vs[j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (MANY)
-                    gj[i] = h.pow2 ? __fmul_rn(gj[i], h.inv) : __fdiv_rn(gj[i], h.count);
-                if (scaled) gj[i] = __fmul_rn(gj[i], gscale);
-                if constexpr (EIGHT) {
-                    mj[i] = decode_m(mc[j] >> (8 * i), ms[j]);
-                    const float was = decode_r(vc[j] >> (8 * i), vs[j]);
+                for (int i = 0; i < 4; ++i) {
+                    const float was = decode_r(vc[j] >> (8 * i), rs);
                     vj[i] = __fmul_rn(was, was);
                 }
-                update(tj[i], mj[i], vj[i], r[i], gj[i], k);
             }
-            if (have[j]) store4(t.theta, t.n, e, have[j], t.vec, theta[j], status);
+            if (MANY && !h.pow2) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gj[i] = __fdiv_rn(gj[i], h.count);
+            } else if (MANY) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gj[i] = __fmul_rn(gj[i], h.inv);
+            }
+            if (scaled) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gj[i] = __fmul_rn(gj[i], gscale);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) update(tj[i], mj[i], vj[i], r[i], gj[i], k);
+            if (FULL || have[j]) store4<FULL>(tile, theta_at, e, have[j], theta[j]);
             if constexpr (EIGHT) {
                 uint32_t am = 0, ar = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    am = max(am, i < have[j] ? __float_as_uint(mj[i]) & 0x7fffffffu : 0u);
-                    ar = max(ar, i < have[j] ? __float_as_uint(r[i]) & 0x7fffffffu : 0u);
+                    am = max(am, FULL || i < have[j] ? __float_as_uint(mj[i]) & 0x7fffffffu : 0u);
+                    ar = max(ar, FULL || i < have[j] ? __float_as_uint(r[i]) & 0x7fffffffu : 0u);
                 }
                 const uint32_t sm = group_scale<false>(__reduce_max_sync(0xffffffffu, am));
                 const uint32_t sr = group_scale<true>(__reduce_max_sync(0xffffffffu, ar));
                 const float im = inverse_scale(sm), ir = inverse_scale(sr);
-                uint32_t cm = 0, cr = 0;
+                uint32_t cm[4], cr[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t d = mix32(uint32_t(e + i) * 0x9E3779B1u + key);
-                    cm |= (sm == 255u ? 0u : encode_m(mj[i], im, d & 0xffffu)) << (8 * i);
-                    cr |= (sr == 255u ? 0u : encode_r(r[i], ir, d >> 16)) << (8 * i);
+                    const uint32_t d = mix32(uint32_t(base + e + i) * 0x9E3779B1u + key);
+                    cm[i] = encode_m(mj[i], im, d & 0xffffu);
+                    cr[i] = encode_r(r[i], ir, d >> 16);
                 }
-                if (have[j]) {
-                    store_codes(t.m, t.n, e, have[j], t.vec, cm, status);
-                    store_codes(t.v, t.n, e, have[j], t.vec, cr, status);
-                    const int64_t q = e / kGroup;
-                    [[maybe_unused]] const int64_t groups = (t.n + kGroup - 1) / kGroup;
-                    if (lane == 0 && REPOPS_ADAM_OK(t.ms, groups, 1, t.ms + q, 1) &&
-                        REPOPS_ADAM_OK(t.vs, groups, 1, t.vs + q, 1)) {
-                        t.ms[q] = uint8_t(sm);
-                        t.vs[q] = uint8_t(sr);
+                if (FULL || have[j]) {
+                    store_codes<FULL>(tile, reinterpret_cast<uint8_t *>(m_at), e, have[j], sm == 255u ? 0u : packed(cm));
+                    store_codes<FULL>(tile, reinterpret_cast<uint8_t *>(v_at), e, have[j], sr == 255u ? 0u : packed(cr));
+                    if (lane == 0) {         // read by this warp alone, which has its own groups
+                        scales[0][e / kGroup] = sm;
+                        scales[1][e / kGroup] = sr;
                     }
                 }
-            } else if (have[j]) {
-                store4(static_cast<float *>(t.m), t.n, e, have[j], t.vec, m[j], status);
-                store4(static_cast<float *>(t.v), t.n, e, have[j], t.vec, v[j], status);
+            } else if (FULL || have[j]) {
+                store4<FULL>(tile, reinterpret_cast<float *>(m_at), e, have[j], m[j]);
+                store4<FULL>(tile, reinterpret_cast<float *>(v_at), e, have[j], v[j]);
             }
+        }
+    }
+    if constexpr (EIGHT) {
+        __syncthreads();
+        if (int(threadIdx.x) < 2 * kScales) {
+            const int i = threadIdx.x % kScales;
+            if (i < groups) (int(threadIdx.x) < kScales ? ms_at : vs_at)[i] = uint8_t(scales[threadIdx.x / kScales][i]);
         }
     }
 }
 
 template <int TY, bool EIGHT, bool MANY, int WORDS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamTable<WORDS> a) {
+__global__ void __launch_bounds__(kThreads, kCtas<EIGHT, MANY>) adamw_kernel(const __grid_constant__ AdamTable<WORDS> a) {
     const AdamHead &h = a.h;
     // the tensor whose tiles hold this one
     int lo = 0, hi = h.tensors - 1;
@@ -328,34 +392,30 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     key = mix32(key + 0x9E3779B9u * (h.first_tensor + uint32_t(lo) + 1u));
     const float gscale = h.grad_scale ? __ldg(h.grad_scale) : 1.0f;
     const int64_t base = int64_t(blockIdx.x - uint32_t(w[0])) * kTile;
-    run_tile<TY, EIGHT, MANY, EIGHT ? 4 : 2>(h, t, base, k, key, gscale, h.grad_scale != nullptr);
+    if (t.vec && base + kTile <= t.n) run_tile<TY, EIGHT, MANY, true>(h, t, base, k, key, gscale, h.grad_scale != nullptr);
+    else run_tile<TY, EIGHT, MANY, false>(h, t, base, k, key, gscale, h.grad_scale != nullptr);
 }
 
 // m and v of 8-bit moments as the binary32 values they stand for.
 __global__ void __launch_bounds__(kThreads)
 adamw_moments_kernel(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *ms, const uint8_t *vs, float *m_out,
                      float *v_out, int vec, unsigned *status) {
-    [[maybe_unused]] const int64_t groups = (n + kGroup - 1) / kGroup;
     const int64_t step = int64_t(gridDim.x) * kThreads * 4;
     for (int64_t e = (blockIdx.x * int64_t(kThreads) + threadIdx.x) * 4; e < n; e += step) {
         const int have = int(min(int64_t(4), n - e));
-        const uint32_t mc = load_codes(m, n, e, have, vec, status), vc = load_codes(v, n, e, have, vec, status);
-        const int64_t q = e / kGroup;
-        float a = 0.0f, b = 0.0f;
-        if (REPOPS_ADAM_OK(ms, groups, 1, ms + q, 1) && REPOPS_ADAM_OK(vs, groups, 1, vs + q, 1)) {
-            a = scale_of(__ldg(ms + q));
-            b = scale_of(__ldg(vs + q));
-        }
+        const Tile t{int(min(n - e, int64_t(1) << 20)), vec != 0, status};
+        const uint32_t mc = load_codes<false>(t, m + e, 0, have), vc = load_codes<false>(t, v + e, 0, have);
         float4 x, y;
-        float *px = &x.x, *py = &y.x;
+        decode_m(mc, scale_of(__ldg(ms + e / kGroup)), x);
+        const float rs = scale_of(__ldg(vs + e / kGroup));
+        float *py = &y.x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            px[i] = decode_m(mc >> (8 * i), a);
-            const float r = decode_r(vc >> (8 * i), b);
+            const float r = decode_r(vc >> (8 * i), rs);
             py[i] = __fmul_rn(r, r);
         }
-        store4(m_out, n, e, have, vec, x, status);
-        store4(v_out, n, e, have, vec, y, status);
+        store4<false>(t, m_out + e, 0, have, x);
+        store4<false>(t, v_out + e, 0, have, y);
     }
 }
 
