@@ -168,7 +168,7 @@ def test_equals_the_separate_operators(rp, rows, q, k, dim):
 
 def test_long_sums(rp):
     """More than 1024 and more than 32768 runs of a gain's sum: the further levels."""
-    for rows, q, k, dim in ((5000, 8, 8, 8), (34000, 33, 1, 4)):
+    for rows, q, k, dim in ((5000, 8, 8, 8), (34000, 33, 1, 4), (36000, 33, 31, 2)):
         o = problem(rows, q, k, dim, dim // 2, "f32", 5, padded=False)
         d = rp.head_norm_rope_backward(o["dy"], o["x"], q, k, o["cos"], o["sin"], q_gain=o["q_gain"], k_gain=o["k_gain"],
                                        eps=EPS, positions=o["pos"])

@@ -148,11 +148,12 @@ def test_head_norm_rope_refuses(L):
         assert back(**bad) == ALIAS, bad
     need = L.repops_head_norm_rope_backward_workspace_bytes
     assert need(-1, 2, 1, 64) == 0 and need(4, 2, 1, 64) == 2 * 64 * 4
-    # every level of the sums fits: at most a 32nd of the one below, rounded up
-    for rows in (1, 31, 5000, 40000, 1 << 20):
+    # every level of the sums above the 32768 results the last fold takes fits: a 32nd of
+    # the one below, rounded up
+    for rows in (1, 31, 5000, 40000, 140000, 1 << 20, 1 << 26):
         q, total = -(-rows * 8 // 32), 0
         n = q
-        while n > 1024:
+        while n > 32768:
             n = -(-n // 32)
             total += n
         assert need(rows, 8, 0, 64) >= (q + total) * 64 * 4

@@ -1503,7 +1503,7 @@ def token_logprobs(logits, targets=None, *, temperature: float = 1.0, top: int =
     import torch
     rows, cols, kind, ld = _logits(logits, targets)
     dev = logits.device
-    logp, lse, entropy = torch.empty((3, rows), dtype=torch.float32, device=dev).unbind()
+    logp, lse, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(3))
     stats = torch.empty((rows, 4), dtype=torch.float32, device=dev)
     top_logp = top_ids = None
     if top > 0:

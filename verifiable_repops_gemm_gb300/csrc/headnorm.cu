@@ -14,9 +14,16 @@
 // whose first level folds 32 neighbouring values one after another, so heads pass
 // through shared memory: neighbouring lanes copy neighbouring chunks, then a lane
 // folds a run (the swizzle of rowtree.cuh serves both without conflicts), then
-// neighbouring lanes write neighbouring chunks.  The backward's CTA takes 32 heads of
-// one gain, a run of the gain's column sum, and so leaves a 32nd of the terms as
-// run results instead of writing them all.
+// neighbouring lanes write neighbouring chunks.  A warp takes the heads of 32 runs (16
+// of 64 columns) by itself, 4 KB, and no CTA waits for another warp's.  The backward's
+// CTA takes 32 heads of one gain, a run of the gain's column sum, and so leaves a 32nd
+// of the terms as run results instead of writing them all.
+//
+// Measured, 4096 rows of 32 query and 8 key heads of 64 in float32, graph-replayed: 20.7
+// us forward (4.1 TB/s; a CTA's heads in common, barriers between the phases: 24.8), 42
+// us with the gains' gradients backward (3.0 TB/s; 47 with a CTA's in common).  What
+// bounds them now is the issue of some 30 instructions a value forward and 65 backward,
+// most of them addresses, swizzles and the trees' additions one by one.
 #include <algorithm>
 
 #include "colfold.cuh"
@@ -25,9 +32,17 @@
 namespace repops {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;            // of a forward CTA
 constexpr int kMostDim = 512;
 constexpr float kNaN = __builtin_nanf("");
+
+// i / d for i < 2^16 and d <= 2^11 by one multiplication.
+struct Divisor {
+    int d;
+    uint32_t magic;
+};
+inline Divisor divisor(int64_t d) { return {int(d), d > 1 ? uint32_t(((uint64_t(1) << 32) + uint64_t(d) - 1) / uint64_t(d)) : 0}; }
+__device__ __forceinline__ int quotient(int i, const Divisor &d) { return d.d == 1 ? i : int(__umulhi(uint32_t(i), d.magic)); }
 
 struct HeadArgs : DbgAccess {
     int64_t rows;
@@ -47,39 +62,68 @@ struct HeadArgs : DbgAccess {
     int pos_wide;
     int64_t first, period;
     float *part[2];                  // backward: run results of the two gains
+    Divisor runs;                    // runs of a head
+    int units;                       // heads of a warp: 32 / runs
+    int whole, per;                  // chunks (or values) of a head; those rotated together as one
+    int whole_shift, per_shift;      // 2^shift lanes take a head's
 };
 
 // Where a head lies and where it stands: offsets in elements, the row of the table
 // (-1: the row is left alone, -2: past the table).
-struct Unit {
-    int64_t x, dy, y;
+struct alignas(16) Unit {
+    int64_t x, y, dy;
     int pos, key;
 };
 
-__device__ __forceinline__ Unit unit_of(const HeadArgs &a, int64_t row, int head) {
+__device__ __forceinline__ void place(const HeadArgs &a, Unit &u, int64_t row, int head) {
+    u.x = row * a.ldx + int64_t(head) * a.dim;
+    u.y = row * a.ldy + int64_t(head) * a.dim;
+    u.dy = row * a.lddy + int64_t(head) * a.dim;
+    u.key = head >= a.q;
+}
+__device__ __forceinline__ int position_of(const HeadArgs &a, int64_t row) {
     int64_t p;
-    if (!a.pos) p = a.first + row % a.period;
+    if (!a.pos) p = a.first + (row < a.period ? row : row % a.period);
     else if (a.pos_wide) p = load_const(a, static_cast<const int64_t *>(a.pos) + row);
     else p = load_const(a, static_cast<const int *>(a.pos) + row);
-    Unit u;
-    u.x = row * a.ldx + int64_t(head) * a.dim;
-    u.dy = row * a.lddy + int64_t(head) * a.dim;
-    u.y = row * a.ldy + int64_t(head) * a.dim;
-    u.pos = p < 0 ? -1 : !a.pairs ? 0 : p >= a.positions ? -2 : int(p);
-    u.key = head >= a.q;
-    return u;
+    return p < 0 ? -1 : !a.pairs ? 0 : p >= a.positions ? -2 : int(p);
+}
+// The row of head n of `heads` a row.
+__device__ __forceinline__ int64_t row_of(int64_t n, int heads) {
+    return n < (int64_t(1) << 32) ? int64_t(uint32_t(n) / uint32_t(heads)) : n / heads;
 }
 
-// cos and sin of pair i at a position (NaN past the table).
 __device__ __forceinline__ float2 turn(const HeadArgs &a, int pos, int i) {
     if (pos < 0) return make_float2(kNaN, kNaN);
     const int64_t at = int64_t(pos) * a.pairs + i;
     return make_float2(load_const(a, a.cosv + at), load_const(a, a.sinv + at));
 }
-__device__ __forceinline__ float4 table4(const HeadArgs &a, const float *t, int pos, int i) {
-    if (pos < 0) return make_float4(kNaN, kNaN, kNaN, kNaN);
-    return load_const(a, reinterpret_cast<const float4 *>(t + int64_t(pos) * a.pairs + i));
-}
+
+// The cos and sin of a lane's pairs, kept while the position stays the same: a warp's
+// heads are of one row or two.
+struct Turn {
+    int pos = -3;
+    float4 c, s;                     // halves: of pairs i .. i + 3; adjacent: of i and i + 1
+    __device__ __forceinline__ void halves(const HeadArgs &a, int p, int i) {
+        if (p == pos) return;
+        pos = p;
+        c = s = make_float4(kNaN, kNaN, kNaN, kNaN);         // past the table
+        if (p < 0) return;
+        const int64_t at = int64_t(p) * a.pairs + i;
+        c = load_const(a, reinterpret_cast<const float4 *>(a.cosv + at));
+        s = load_const(a, reinterpret_cast<const float4 *>(a.sinv + at));
+    }
+    __device__ __forceinline__ void adjacent(const HeadArgs &a, int p, int i) {
+        if (p == pos) return;
+        pos = p;
+        float2 u = turn(a, p, i), v = make_float2(0.0f, 0.0f);
+        if (i + 1 < a.pairs) v = turn(a, p, i + 1);
+        c.x = u.x;
+        s.x = u.y;
+        c.y = v.x;
+        s.y = v.y;
+    }
+};
 
 template <bool BACK>
 __device__ __forceinline__ void rotate(float &u, float &v, float c, float s) {
@@ -95,25 +139,21 @@ __device__ __forceinline__ void rotate(float &u, float &v, float c, float s) {
 
 // Four neighbouring values in adjacent pairs, the first of column 4 * chunk.
 template <bool BACK>
-__device__ __forceinline__ void rotate_adjacent(const HeadArgs &a, int pos, int chunk, float4 &v) {
+__device__ __forceinline__ void rotate_adjacent(const HeadArgs &a, Turn &t, int pos, int chunk, float4 &v) {
     const int i = 2 * chunk;
-    if (i < a.pairs) {
-        const float2 t = turn(a, pos, i);
-        rotate<BACK>(v.x, v.y, t.x, t.y);
-    }
-    if (i + 1 < a.pairs) {
-        const float2 t = turn(a, pos, i + 1);
-        rotate<BACK>(v.z, v.w, t.x, t.y);
-    }
+    if (i >= a.pairs) return;
+    t.adjacent(a, pos, i);
+    rotate<BACK>(v.x, v.y, t.c.x, t.s.x);
+    if (i + 1 < a.pairs) rotate<BACK>(v.z, v.w, t.c.y, t.s.y);
 }
 // Four pairs of two halves, the first of pair i.
 template <bool BACK>
-__device__ __forceinline__ void rotate_halves(const HeadArgs &a, int pos, int i, float4 &u, float4 &v) {
-    const float4 c = table4(a, a.cosv, pos, i), s = table4(a, a.sinv, pos, i);
-    rotate<BACK>(u.x, v.x, c.x, s.x);
-    rotate<BACK>(u.y, v.y, c.y, s.y);
-    rotate<BACK>(u.z, v.z, c.z, s.z);
-    rotate<BACK>(u.w, v.w, c.w, s.w);
+__device__ __forceinline__ void rotate_halves(const HeadArgs &a, Turn &t, int pos, int i, float4 &u, float4 &v) {
+    t.halves(a, pos, i);
+    rotate<BACK>(u.x, v.x, t.c.x, t.s.x);
+    rotate<BACK>(u.y, v.y, t.c.y, t.s.y);
+    rotate<BACK>(u.z, v.z, t.c.z, t.s.z);
+    rotate<BACK>(u.w, v.w, t.c.w, t.s.w);
 }
 // Value j of a head alone; `at` gives any of the head's values.
 template <bool BACK, class F>
@@ -155,10 +195,17 @@ __device__ __forceinline__ float fold_run(const float4 *stage, int run, int firs
     return acc;
 }
 
-__device__ __forceinline__ float fold_head(const float *red, int runs) {
-    float acc = red[0];
-    for (int i = 1; i < runs; ++i) acc = __fadd_rn(acc, red[i]);
-    return acc;
+// The fold of a head's run results, which the lanes from u * runs on hold.
+__device__ __forceinline__ float fold_head(const HeadArgs &a, float acc) {
+    const int base = quotient(threadIdx.x & 31, a.runs) * a.runs.d;
+    float sum = __shfl_sync(0xffffffffu, acc, base);
+    for (int r = 1; r < a.runs.d; ++r) sum = __fadd_rn(sum, __shfl_sync(0xffffffffu, acc, base + r));
+    return sum;
+}
+// Column of the first value of this lane's run in its head, and the run's length.
+__device__ __forceinline__ int run_first(const HeadArgs &a) {
+    const int lane = threadIdx.x & 31;
+    return (lane - quotient(lane, a.runs) * a.runs.d) * RUN;
 }
 __device__ __forceinline__ float inv_rms(float sum, float n, float eps) {
     return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps)));
@@ -174,118 +221,150 @@ __device__ __forceinline__ float4 gain4(const HeadArgs &a, int key, int c) {
     return load_const(a, reinterpret_cast<const float4 *>(key ? a.k_gain : a.q_gain) + c);
 }
 
-size_t stage_bytes(int units, int runs) { return size_t(units) * runs * RUN * 4; }
+// A warp's heads: 32 runs of 32 values, and where the heads lie.
+struct WarpHeads {
+    float4 x[RUN * 8];
+    Unit unit[RUN];
+    float inv[RUN];
+};
+
+// f(head, w, kept) for w < per of every head u < here, 2^shift lanes to a head, so that a
+// lane meets the same w in each, and what f keeps for it is its own.
+template <class Kept, int UNROLL, class F>
+__device__ __forceinline__ void each_part(int here, int per, int shift, F f) {
+    const int lane = threadIdx.x & 31, sub = lane & ((1 << shift) - 1), from = lane >> shift, step = 32 >> shift;
+    for (int w = sub; w < per; w += 1 << shift) {
+        Kept kept;
+#pragma unroll UNROLL
+        for (int u = from; u < here; u += step) f(u, w, kept);
+    }
+}
+struct Nothing {};
 
 // ---------------------------------------------------------------- forward ----
 
-// `units` heads a CTA, in the order of rows and heads.  VEC: four values an access
-// everywhere.  NORM off: the rotation alone (BACK: its transpose), nothing staged
-// but by the halves of pairs.
+// VEC: four values an access everywhere.  NORM off: the rotation alone (BACK: its
+// transpose).
 template <int TY, bool VEC, bool NORM, bool BACK>
-__global__ void __launch_bounds__(kThreads) head_forward_kernel(const HeadArgs a, int units, int runs) {
-    extern __shared__ __align__(16) float4 stage[];
-    float *flat = reinterpret_cast<float *>(stage);
-    float *red = flat + size_t(units) * runs * RUN;             // units x runs, then 1/rms
-    Unit *info = reinterpret_cast<Unit *>(red + (units * runs + 1) / 2 * 2);
-    const int heads = a.q + a.k;
-    const int64_t total = a.rows * heads, u0 = blockIdx.x * int64_t(units);
-    const int here = int(imin64(units, total - u0));
-    for (int u = threadIdx.x; u < here; u += kThreads) {
-        const int64_t row = (u0 + u) / heads;
-        info[u] = unit_of(a, row, int(u0 + u - row * heads));
+__global__ void __launch_bounds__(kWarps * 32, 10) head_forward_kernel(const HeadArgs a) {
+    __shared__ WarpHeads heads[kWarps];
+    WarpHeads &h = heads[threadIdx.x >> 5];
+    float *flat = reinterpret_cast<float *>(h.x);
+    const int lane = threadIdx.x & 31, runs = a.runs.d, per_row = a.q + a.k;
+    const int64_t total = a.rows * per_row, u0 = (blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5)) * a.units;
+    if (u0 >= total) return;
+    const int here = int(imin64(a.units, total - u0));
+    int pos_of = -1;
+    if (lane < here) {
+        const int64_t row = row_of(u0 + lane, per_row);
+        place(a, h.unit[lane], row, int(u0 + lane - row * per_row));
+        pos_of = position_of(a, row);
     }
-    __syncthreads();
-    const int chunks = a.dim / 4;
+    __syncwarp();
+    // a head has `per` chunks (halves: pairs of chunks that are rotated together, and
+    // the rest), or without VEC values
+    const int turned = a.halves ? a.pairs / 4 : 0;
     if constexpr (VEC) {
-        for (int i = threadIdx.x; i < here * chunks; i += kThreads) {
-            const int u = i / chunks, c = i - u * chunks;
-            stage[chunk_at(u * runs, c)] = load_four<TY>(a, a.x, info[u].x + 4 * c);
-        }
+        each_part<Nothing, 8>(here, a.whole, a.whole_shift, [&](int u, int c, Nothing &) {
+            h.x[chunk_at(u * runs, c)] = load_four<TY>(a, a.x, h.unit[u].x + 4 * c);
+        });
     } else {
-        for (int i = threadIdx.x; i < here * a.dim; i += kThreads) {
-            const int u = i / a.dim, j = i - u * a.dim;
-            flat[value_at(u * runs, j)] = load_one<TY>(a, a.x, info[u].x + j);
-        }
+        each_part<Nothing, 4>(here, a.whole, a.whole_shift, [&](int u, int j, Nothing &) {
+            flat[value_at(u * runs, j)] = load_one<TY>(a, a.x, h.unit[u].x + j);
+        });
     }
-    __syncthreads();
+    if (lane < here) h.unit[lane].pos = pos_of;      // asked for before the values, wanted after them
+    __syncwarp();
     if constexpr (NORM) {
-        for (int t = threadIdx.x; t < here * runs; t += kThreads) {
-            const int first = (t % runs) * RUN;
-            red[t] = fold_run(stage, t, first, min(RUN, a.dim - first), [](float v, int) { return __fmul_rn(v, v); });
-        }
-        __syncthreads();
-        float inv = 0.0f;
-        // at most one head a thread: a CTA has at least as many threads
-        if (threadIdx.x < here) inv = inv_rms(fold_head(red + threadIdx.x * runs, runs), float(a.dim), a.eps);
-        __syncthreads();
-        if (threadIdx.x < here) red[threadIdx.x] = inv;
-        __syncthreads();
+        const int first = run_first(a);
+        float acc = 0.0f;
+        if (lane < here * runs)
+            acc = fold_run(h.x, lane, first, min(RUN, a.dim - first), [](float v, int) { return __fmul_rn(v, v); });
+        const float inv = inv_rms(fold_head(a, acc), float(a.dim), a.eps);
+        if (first == 0) h.inv[quotient(lane, a.runs)] = inv;
+        __syncwarp();
     }
     if constexpr (VEC) {
-        const int turned = a.halves ? a.pairs / 4 : 0, items = chunks - turned;
-        for (int i = threadIdx.x; i < here * items; i += kThreads) {
-            const int u = i / items, w = i - u * items;
-            const Unit t = info[u];
-            if (t.pos == -1) continue;
-            const int c = w < turned ? w : w + turned;      // halves: the first half stands for both
-            float4 v = stage[chunk_at(u * runs, c)];
-            if constexpr (NORM) v = mul4(scale4(v, red[u]), gain4(a, t.key, c));
-            if (w < turned) {
-                float4 v2 = stage[chunk_at(u * runs, c + turned)];
-                if constexpr (NORM) v2 = mul4(scale4(v2, red[u]), gain4(a, t.key, c + turned));
-                rotate_halves<BACK>(a, t.pos, 4 * c, v, v2);
-                store_four<TY>(a, a.y, t.y + 4 * (c + turned), v2);
-            } else if (!a.halves) {
-                rotate_adjacent<BACK>(a, t.pos, c, v);
+        struct Kept {
+            Turn turn;
+            int key = -1;
+            float4 g, g2;
+        };
+        each_part<Kept, 1>(here, a.per, a.per_shift, [&](int u, int w, Kept &k) {
+            const int c = w < turned ? w : w + turned;
+            const int64_t y = h.unit[u].y;
+            const int pos = h.unit[u].pos, key = h.unit[u].key;
+            if (pos == -1) return;
+            const float iv = NORM ? h.inv[u] : 0.0f;
+            if (NORM && key != k.key) {
+                k.key = key;
+                k.g = gain4(a, key, c);
+                if (w < turned) k.g2 = gain4(a, key, c + turned);
             }
-            store_four<TY>(a, a.y, t.y + 4 * c, v);
-        }
+            float4 v = h.x[chunk_at(u * runs, c)];
+            if constexpr (NORM) v = mul4(scale4(v, iv), k.g);
+            if (w < turned) {
+                float4 v2 = h.x[chunk_at(u * runs, c + turned)];
+                if constexpr (NORM) v2 = mul4(scale4(v2, iv), k.g2);
+                rotate_halves<BACK>(a, k.turn, pos, 4 * c, v, v2);
+                store_four<TY>(a, a.y, y + 4 * (c + turned), v2);
+            } else if (!a.halves) {
+                rotate_adjacent<BACK>(a, k.turn, pos, c, v);
+            }
+            store_four<TY>(a, a.y, y + 4 * c, v);
+        });
     } else {
-        for (int i = threadIdx.x; i < here * a.dim; i += kThreads) {
-            const int u = i / a.dim, j = i - u * a.dim;
-            const Unit t = info[u];
-            if (t.pos == -1) continue;
+        each_part<Nothing, 1>(here, a.per, a.per_shift, [&](int u, int j, Nothing &) {
+            const Unit t = h.unit[u];
+            if (t.pos == -1) return;
             const float *gain = t.key ? a.k_gain : a.q_gain;
             const float v = rotate_one<BACK>(a, t.pos, j, [&](int c) {
                 const float x = flat[value_at(u * runs, c)];
-                return NORM ? __fmul_rn(__fmul_rn(x, red[u]), load_const(a, gain + c)) : x;
+                return NORM ? __fmul_rn(__fmul_rn(x, h.inv[u]), load_const(a, gain + c)) : x;
             });
             store_one<TY>(a, a.y, t.y + j, v);
-        }
+        });
     }
 }
 
 // --------------------------------------------------------------- backward ----
 
-// A run of 32 heads of one gain: the queries' runs first, then the keys'.
+// A run of 32 heads of one gain: the queries' runs first, then the keys'.  Each warp
+// takes the heads of 32 of its runs of columns; the terms of the gain's gradient
+// replace the turned dy in shared memory, where the CTA folds them.
+struct WarpHeadsBack {
+    float4 x[RUN * 8], g[RUN * 8];
+    Unit unit[RUN];
+    float inv[RUN], mean[RUN];
+};
+
 template <int TY, bool VEC>
-__global__ void __launch_bounds__(kThreads) head_backward_kernel(const HeadArgs a, int64_t q_runs, int runs) {
-    extern __shared__ __align__(16) float4 stage[];
-    float4 *gs = stage + RUN * runs * 8;
-    float *fx = reinterpret_cast<float *>(stage), *fg = reinterpret_cast<float *>(gs);
-    float *red = fg + size_t(RUN) * runs * RUN;                  // 32 x runs
-    float *inv = red + RUN * runs, *mean = inv + RUN;
-    Unit *info = reinterpret_cast<Unit *>(mean + RUN);
+__global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, int64_t q_runs) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    WarpHeadsBack *all = reinterpret_cast<WarpHeadsBack *>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, runs = a.runs.d;
+    WarpHeadsBack &h = all[warp];
+    float *fx = reinterpret_cast<float *>(h.x), *fg = reinterpret_cast<float *>(h.g);
     const int key = blockIdx.x >= q_runs;
     const int64_t run = blockIdx.x - (key ? q_runs : 0);
-    const int heads = key ? a.k : a.q;
-    const int64_t total = a.rows * heads, u0 = run * RUN;
-    const int here = int(imin64(RUN, total - u0));
-    if (int(threadIdx.x) < here) {
-        const int64_t row = (u0 + threadIdx.x) / heads;
-        info[threadIdx.x] = unit_of(a, row, int(u0 + threadIdx.x - row * heads) + (key ? a.q : 0));
+    const int per_row = key ? a.k : a.q;
+    const int64_t total = a.rows * per_row, u0 = run * RUN;
+    const int in_run = int(imin64(RUN, total - u0));
+    const int here = max(0, min(a.units, in_run - warp * a.units));
+    if (lane < here) {
+        const int64_t at = u0 + warp * a.units + lane, row = row_of(at, per_row);
+        place(a, h.unit[lane], row, int(at - row * per_row) + (key ? a.q : 0));
+        h.unit[lane].pos = position_of(a, row);
     }
-    __syncthreads();
+    __syncwarp();
     const float *gain = key ? a.k_gain : a.q_gain;
-    const int chunks = a.dim / 4;
+    const int turned = a.halves ? a.pairs / 4 : 0;
     if constexpr (VEC) {
-        const int turned = a.halves ? a.pairs / 4 : 0, items = chunks - turned;
         const float4 zero = make_float4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < here * items; i += kThreads) {
-            const int u = i / items, w = i - u * items;
-            const Unit t = info[u];
-            const bool live = t.pos != -1;
+        each_part<Turn, 4>(here, a.per, a.per_shift, [&](int u, int w, Turn &kept) {
             const int c = w < turned ? w : w + turned;
+            const Unit t = h.unit[u];
+            const bool live = t.pos != -1;
             float4 g = zero, x = zero;
             if (live) {
                 g = load_four<TY>(a, a.dy, t.dy + 4 * c);
@@ -296,20 +375,19 @@ __global__ void __launch_bounds__(kThreads) head_backward_kernel(const HeadArgs 
                 if (live) {
                     g2 = load_four<TY>(a, a.dy, t.dy + 4 * (c + turned));
                     x2 = load_four<TY>(a, a.x, t.x + 4 * (c + turned));
-                    rotate_halves<true>(a, t.pos, 4 * c, g, g2);
+                    rotate_halves<true>(a, kept, t.pos, 4 * c, g, g2);
                 }
-                stage[chunk_at(u * runs, c + turned)] = x2;
-                gs[chunk_at(u * runs, c + turned)] = g2;
+                h.x[chunk_at(u * runs, c + turned)] = x2;
+                h.g[chunk_at(u * runs, c + turned)] = g2;
             } else if (live && !a.halves) {
-                rotate_adjacent<true>(a, t.pos, c, g);
+                rotate_adjacent<true>(a, kept, t.pos, c, g);
             }
-            stage[chunk_at(u * runs, c)] = x;
-            gs[chunk_at(u * runs, c)] = g;
-        }
+            h.x[chunk_at(u * runs, c)] = x;
+            h.g[chunk_at(u * runs, c)] = g;
+        });
     } else {
-        for (int i = threadIdx.x; i < here * a.dim; i += kThreads) {
-            const int u = i / a.dim, j = i - u * a.dim;
-            const Unit t = info[u];
+        each_part<Nothing, 1>(here, a.per, a.per_shift, [&](int u, int j, Nothing &) {
+            const Unit t = h.unit[u];
             float g = 0.0f, x = 0.0f;
             if (t.pos != -1) {
                 x = load_one<TY>(a, a.x, t.x + j);
@@ -317,85 +395,146 @@ __global__ void __launch_bounds__(kThreads) head_backward_kernel(const HeadArgs 
             }
             fx[value_at(u * runs, j)] = x;
             fg[value_at(u * runs, j)] = g;
-        }
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < here * runs; t += kThreads) {
-        const int first = (t % runs) * RUN;
-        red[t] = fold_run(stage, t, first, min(RUN, a.dim - first), [](float v, int) { return __fmul_rn(v, v); });
-    }
-    __syncthreads();
-    if (int(threadIdx.x) < here)        // a row left alone adds +0, whatever eps
-        inv[threadIdx.x] = info[threadIdx.x].pos == -1
-                               ? 0.0f
-                               : inv_rms(fold_head(red + threadIdx.x * runs, runs), float(a.dim), a.eps);
-    __syncthreads();
-    for (int t = threadIdx.x; t < here * runs; t += kThreads) {
-        const int u = t / runs, first = (t - u * runs) * RUN;
-        const float iv = inv[u];
-        const float *g = fg;
-        red[t] = fold_run(stage, t, first, min(RUN, a.dim - first), [&](float v, int j) {
-            const float gy = __fmul_rn(g[value_at(u * runs, j)], load_const(a, gain + j));
-            return __fmul_rn(gy, __fmul_rn(v, iv));
         });
     }
-    __syncthreads();
-    if (int(threadIdx.x) < here)
-        mean[threadIdx.x] = __fdiv_rn(fold_head(red + threadIdx.x * runs, runs), float(a.dim));
-    __syncthreads();
+    __syncwarp();
+    const int first = run_first(a), length = min(RUN, a.dim - first), mine = quotient(lane, a.runs);
+    const bool folds = lane < here * runs;
+    float acc = 0.0f;
+    if (folds) acc = fold_run(h.x, lane, first, length, [](float v, int) { return __fmul_rn(v, v); });
+    float inv = inv_rms(fold_head(a, acc), float(a.dim), a.eps);
+    if (folds && h.unit[mine].pos == -1) inv = 0.0f;             // a row left alone adds +0, whatever eps
+    if (folds) {
+        auto term = [&](float x, float g, float w) { return __fmul_rn(__fmul_rn(g, w), __fmul_rn(x, inv)); };
+        if (VEC && length == RUN) {
+            const float4 *w4 = reinterpret_cast<const float4 *>(gain + first);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float4 x = h.x[stage_slot(lane, c)], g = h.g[stage_slot(lane, c)], w = load_const(a, w4 + c);
+                acc = c == 0 ? term(x.x, g.x, w.x) : __fadd_rn(acc, term(x.x, g.x, w.x));
+                acc = __fadd_rn(acc, term(x.y, g.y, w.y));
+                acc = __fadd_rn(acc, term(x.z, g.z, w.z));
+                acc = __fadd_rn(acc, term(x.w, g.w, w.w));
+            }
+        } else {
+            for (int i = 0; i < length; ++i) {
+                const int at = 4 * stage_slot(lane, i >> 2) + (i & 3);
+                const float t = term(fx[at], fg[at], load_const(a, gain + first + i));
+                acc = i == 0 ? t : __fadd_rn(acc, t);
+            }
+        }
+    }
+    const float mean = __fdiv_rn(fold_head(a, acc), float(a.dim));
+    if (first == 0) {
+        h.inv[mine] = inv;
+        h.mean[mine] = mean;
+    }
+    __syncwarp();
     auto grad = [&](float x, float g, float w, float iv, float m, float &term) {
         const float xh = __fmul_rn(x, iv);
         term = __fmul_rn(g, xh);
         return __fmul_rn(iv, __fsub_rn(__fmul_rn(g, w), __fmul_rn(xh, m)));
     };
-    if constexpr (VEC) {
-        for (int i = threadIdx.x; i < here * chunks; i += kThreads) {
-            const int u = i / chunks, c = i - u * chunks, at = chunk_at(u * runs, c);
-            const float4 x = stage[at], g = gs[at], w = load_const(a, reinterpret_cast<const float4 *>(gain) + c);
-            const float iv = inv[u], m = mean[u];
+    struct Kept {
+        bool there = false;
+        float4 w;
+    };
+    each_part<Kept, 2>(here, a.whole, a.whole_shift, [&](int u, int c, Kept &k) {
+        const float iv = h.inv[u], mu = h.mean[u];
+        const bool live = h.unit[u].pos != -1;
+        if constexpr (VEC) {
+            const int at = chunk_at(u * runs, c);
+            if (!k.there) k.w = load_const(a, reinterpret_cast<const float4 *>(gain) + c);
+            k.there = true;
+            const float4 x = h.x[at], g = h.g[at], w = k.w;
             float4 d, t;
-            d.x = grad(x.x, g.x, w.x, iv, m, t.x);
-            d.y = grad(x.y, g.y, w.y, iv, m, t.y);
-            d.z = grad(x.z, g.z, w.z, iv, m, t.z);
-            d.w = grad(x.w, g.w, w.w, iv, m, t.w);
-            gs[at] = t;
-            if (info[u].pos != -1) store_four<TY>(a, a.y, info[u].y + 4 * c, d);
-        }
-    } else {
-        for (int i = threadIdx.x; i < here * a.dim; i += kThreads) {
-            const int u = i / a.dim, j = i - u * a.dim, at = value_at(u * runs, j);
+            d.x = grad(x.x, g.x, w.x, iv, mu, t.x);
+            d.y = grad(x.y, g.y, w.y, iv, mu, t.y);
+            d.z = grad(x.z, g.z, w.z, iv, mu, t.z);
+            d.w = grad(x.w, g.w, w.w, iv, mu, t.w);
+            h.g[at] = t;
+            if (live) store_four<TY>(a, a.y, h.unit[u].y + 4 * c, d);
+        } else {
+            const int at = value_at(u * runs, c);
             float t;
-            const float d = grad(fx[at], fg[at], load_const(a, gain + j), inv[u], mean[u], t);
+            const float d = grad(fx[at], fg[at], load_const(a, gain + c), iv, mu, t);
             fg[at] = t;
-            if (info[u].pos != -1) store_one<TY>(a, a.y, info[u].y + j, d);
+            if (live) store_one<TY>(a, a.y, h.unit[u].y + c, d);
         }
+    });
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.dim; j += blockDim.x) {
+        const int chunk = j >> 2;
+        float sum = 0.0f;
+        for (int w = 0, done = 0; done < in_run; ++w) {
+            const float *g = reinterpret_cast<const float *>(all[w].g) + (j & 3);
+            const int of = min(a.units, in_run - done);
+#pragma unroll 4
+            for (int u = 0; u < of; ++u) {
+                const float v = g[4 * chunk_at(u * runs, chunk)];
+                sum = done + u == 0 ? v : __fadd_rn(sum, v);
+            }
+            done += of;
+        }
+        store_global(a, a.part[key] + run * a.dim + j, sum);
+    }
+}
+
+// The last levels of the gains' sums: 8 columns a CTA, a thread for each group of 32 run
+// results (up to 1024 groups), then two levels in shared memory.
+struct GainFold : DbgAccess {
+    const float *in[2];
+    float *out[2];
+    int runs[2];
+    int dim;
+};
+__global__ void __launch_bounds__(1024) gain_fold_kernel(const GainFold a) {
+    __shared__ float part[RUN * RUN][9];
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, set = blockIdx.y, c = blockIdx.x * 8 + tx;
+    int n = a.runs[set];
+    grid_wait();
+    if (n == 0) return;
+    int groups = (n + RUN - 1) / RUN;
+    if (c < a.dim) {
+        for (int g = ty; g < groups; g += 128) {
+            const float *in = a.in[set] + int64_t(g) * RUN * a.dim + c;
+            const int m = min(RUN, n - g * RUN);
+            float v[RUN];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i)
+                if (i < m) v[i] = load_global(a, in + int64_t(i) * a.dim);
+            float acc = v[0];
+#pragma unroll
+            for (int i = 1; i < RUN; ++i)
+                if (i < m) acc = __fadd_rn(acc, v[i]);
+            part[g][tx] = acc;
+        }
+    }
+    while (groups > 1) {
+        __syncthreads();
+        n = groups;
+        groups = (n + RUN - 1) / RUN;
+        float acc = 0.0f;
+        if (ty < groups) {
+            acc = part[ty * RUN][tx];
+            for (int i = 1; i < min(RUN, n - ty * RUN); ++i) acc = __fadd_rn(acc, part[ty * RUN + i][tx]);
+        }
+        __syncthreads();
+        if (ty < groups) part[ty][tx] = acc;
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < a.dim; j += kThreads) {
-        float acc = fg[value_at(0, j)];
-        for (int u = 1; u < here; ++u) acc = __fadd_rn(acc, fg[value_at(u * runs, j)]);
-        store_global(a, a.part[key] + run * a.dim + j, acc);
-    }
+    if (ty == 0 && c < a.dim) store_global(a, a.out[set] + c, part[0][tx]);
 }
 
 // ------------------------------------------------------------------- host ----
 
-size_t forward_smem(int units, int runs) {
-    return stage_bytes(units, runs) + size_t((units * runs + 1) / 2 * 2) * 4 + size_t(units) * sizeof(Unit);
-}
-size_t backward_smem(int runs) { return 2 * stage_bytes(RUN, runs) + size_t(RUN) * (runs + 2) * 4 + RUN * sizeof(Unit); }
+constexpr int64_t kMostFolded = RUN * RUN * RUN;     // run results the last fold takes
 
 template <int TY, bool VEC, bool NORM, bool BACK>
 int launch_forward(const HeadArgs &a, cudaStream_t s) {
-    DeviceInfo di;
-    if (const int rc = current_device_info(&di); rc != REPOPS_OK) return rc;
-    const int runs = int(ceil_div(a.dim, RUN));
-    const int64_t total = a.rows * (a.q + a.k);
-    // 16 KB of heads a CTA, fewer where there are too few to give every SM two CTAs
-    const int units = int(std::max<int64_t>(1, std::min<int64_t>(128 / runs, ceil_div(total, 2 * di.sms))));
-    if (ceil_div(total, units) > INT32_MAX) return REPOPS_ERR_UNSUPPORTED;
-    head_forward_kernel<TY, VEC, NORM, BACK>
-        <<<unsigned(ceil_div(total, units)), kThreads, forward_smem(units, runs), s>>>(a, units, runs);
+    const int64_t blocks = ceil_div(a.rows * (a.q + a.k), int64_t(a.units) * kWarps);
+    if (blocks > INT32_MAX) return REPOPS_ERR_UNSUPPORTED;
+    head_forward_kernel<TY, VEC, NORM, BACK><<<unsigned(blocks), kWarps * 32, 0, s>>>(a);
     return check_launch();
 }
 
@@ -406,7 +545,28 @@ int forward_typed(const HeadArgs &a, bool vec, cudaStream_t s) {
     return vec ? launch_forward<TY, true, false, false>(a, s) : launch_forward<TY, false, false, false>(a, s);
 }
 
-int forward_any(const HeadArgs &a, int type, bool vec, cudaStream_t s) {
+// How a warp's lanes share its heads.
+void share(HeadArgs &a, bool vec) {
+    auto lanes = [](int n) {
+        int s = 0;
+        while (s < 5 && (1 << s) < n) ++s;
+        return s;
+    };
+    a.runs = divisor(ceil_div(a.dim, RUN));
+    a.units = RUN / a.runs.d;
+    a.whole = vec ? a.dim / 4 : a.dim;
+    a.per = vec && a.halves ? a.dim / 4 - a.pairs / 4 : a.whole;
+    a.whole_shift = lanes(a.whole);
+    a.per_shift = lanes(a.per);
+}
+
+int forward_any(HeadArgs a, int type, bool vec, cudaStream_t s) {
+    DeviceInfo di;
+    if (const int rc = current_device_info(&di); rc != REPOPS_OK) return rc;
+    share(a, vec);
+    // fewer heads a warp where a CTA for every SM needs it (one row of 40 heads: 6.2 us
+    // against 8.5 with all 16 in a warp)
+    while (a.units > 1 && a.rows * (a.q + a.k) < int64_t(a.units) * kWarps * di.sms) a.units = (a.units + 1) / 2;
     switch (type) {
         case REPOPS_TYPE_F32: return forward_typed<REPOPS_TYPE_F32>(a, vec, s);
         case REPOPS_TYPE_F16: return forward_typed<REPOPS_TYPE_F16>(a, vec, s);
@@ -415,22 +575,22 @@ int forward_any(const HeadArgs &a, int type, bool vec, cudaStream_t s) {
 }
 
 template <int TY, bool VEC>
-int launch_backward(const HeadArgs &a, int64_t q_runs, int64_t k_runs, cudaStream_t s) {
-    const int runs = int(ceil_div(a.dim, RUN));
-    const size_t smem = backward_smem(runs);
+int launch_backward(HeadArgs a, int64_t q_runs, int64_t k_runs, cudaStream_t s) {
+    share(a, VEC);
+    const int warps = (RUN + a.units - 1) / a.units;
+    const size_t smem = size_t(warps) * sizeof(WarpHeadsBack);
     auto kern = head_backward_kernel<TY, VEC>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return set_cuda_error(e);
     }
-    kern<<<unsigned(q_runs + k_runs), kThreads, smem, s>>>(a, q_runs, runs);
+    kern<<<unsigned(q_runs + k_runs), unsigned(warps * 32), smem, s>>>(a, q_runs);
     return check_launch();
 }
 
-// Run results of a gain's sum, and those of its further level where there are more
-// than the last fold takes (a 32nd of them, of more than 1024; twice and so on).
-int64_t level_rows(int64_t runs) { return runs > MAX_FOLD_ROWS ? 2 * ceil_div(runs, RUN) + 8 : 0; }
-
+// Run results of the further levels of a gain's sum where there are more than the last
+// fold takes (a 32nd of them, and so on).
+int64_t level_rows(int64_t runs) { return runs > kMostFolded ? 2 * ceil_div(runs, RUN) + 8 : 0; }
 
 // The checks both directions share; what they return is REPOPS_OK with sizes of
 // nothing to do (rows or heads of 0), which the callers look at first.
@@ -633,13 +793,11 @@ extern "C" int repops_head_norm_rope_backward(int64_t rows, int64_t q_heads, int
             rc = vec ? launch_backward<REPOPS_TYPE_BF16, true>(a, q_runs, k_runs, stream)
                      : launch_backward<REPOPS_TYPE_BF16, false>(a, q_runs, k_runs, stream);
     }
-    FoldArgs f{a};
-    f.n = dim;
+    GainFold f{a};
+    f.dim = int(dim);
     float *level = a.part[1] + k_runs * dim;
-    int sets = 0;
-    int64_t most = 1;
-    auto add = [&](const float *in, float *out, int64_t n) {
-        while (rc == REPOPS_OK && n > MAX_FOLD_ROWS) {
+    auto add = [&](int set, const float *in, float *out, int64_t n) {
+        while (rc == REPOPS_OK && n > kMostFolded) {
             const int64_t up = ceil_div(n, RUN);
             const dim3 grid(unsigned(ceil_div(dim, 256)), unsigned(std::min<int64_t>(up, 65535)));
             colsum_pass_kernel<<<grid, 256, 0, stream>>>(n, dim, in, dim, level, dim, a);
@@ -648,13 +806,13 @@ extern "C" int repops_head_norm_rope_backward(int64_t rows, int64_t q_heads, int
             level += up * dim;
             n = up;
         }
-        f.s[sets++] = FoldSet{in, out, 1, n, dim};
-        most = std::max(most, n);
+        f.in[set] = in;
+        f.out[set] = out;
+        f.runs[set] = int(n);
     };
-    if (q_runs) add(a.part[0], dq_gain, q_runs);
-    if (k_runs) add(a.part[1], dk_gain, k_runs);
+    add(0, a.part[0], dq_gain, q_runs);
+    add(1, a.part[1], dk_gain, k_runs);
     if (rc == REPOPS_OK)
-        rc = launch_behind(column_fold_kernel, dim3(unsigned(ceil_div(dim, RUN)), 1, unsigned(sets)),
-                           unsigned(ceil_div(most, RUN) * 32), 0, stream, f);
+        rc = launch_behind(gain_fold_kernel, dim3(unsigned(ceil_div(dim, 8)), 2), 1024, 0, stream, f);
     return w.release(rc);
 }
