@@ -55,6 +55,7 @@ after the current one first, or given `out`.
 import array
 import ctypes
 import functools
+import operator
 import typing
 
 from . import _capi
@@ -1330,14 +1331,21 @@ def _tensor_list(ts, dtype, here, name):
     import torch
     if isinstance(ts, torch.Tensor):
         ts = (ts,)
-    for t in ts:
-        if t.dtype != dtype or t.get_device() != here or not t.is_contiguous():
-            raise ValueError("%s must be contiguous %s tensors on the current CUDA device (%d)" % (name, dtype, here))
+    kind = torch.Tensor          # maps over its methods: lists of hundreds of tensors take microseconds here
+    if not ({*map(operator.attrgetter("dtype"), ts)} <= {dtype} and {*map(kind.get_device, ts)} <= {here} and
+            all(map(kind.is_contiguous, ts))):
+        raise ValueError("%s must be contiguous %s tensors on the current CUDA device (%d)" % (name, dtype, here))
     return ts
 
 
+def _sizes(ts):
+    import torch
+    return list(map(torch.Tensor.numel, ts))
+
+
 def _pointers(ts):
-    return array.array("Q", [t.data_ptr() for t in ts])
+    import torch
+    return array.array("Q", list(map(torch.Tensor.data_ptr, ts)))
 
 
 def _address(a):
@@ -1407,17 +1415,17 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
     eight = m_scales is not None or v_scales is not None
     kept = torch.uint8 if eight else torch.float32
     m, v = _tensor_list(m, kept, here, "m"), _tensor_list(v, kept, here, "v")
-    sizes = [t.numel() for t in theta]
+    sizes = _sizes(theta)
     for what, ts in (("grads", grads), ("m", (m,)), ("v", (v,))):
         for t in ts:
-            if [x.numel() for x in t] != sizes:
+            if _sizes(t) != sizes:
                 raise ValueError("%s must have one tensor of each of theta's sizes" % what)
     scale_ptrs = [None, None]
     if eight:
         groups = [-(-k // ADAMW_GROUP) for k in sizes]
         for i, ts in enumerate((m_scales, v_scales)):
             ts = _tensor_list(() if ts is None else ts, torch.uint8, here, "scales")
-            if [x.numel() for x in ts] != groups:
+            if _sizes(ts) != groups:
                 raise ValueError("m_scales and v_scales must have one byte for every %d elements" % ADAMW_GROUP)
             scale_ptrs[i] = _pointers(ts)
     decay = array.array("f", [weight_decay] * n if isinstance(weight_decay, (int, float)) else weight_decay)
@@ -1441,7 +1449,7 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
     if len(grads) == 1:
         gp = _pointers(grads[0])
     else:
-        gp = array.array("Q", [t.data_ptr() for ts in zip(*grads) for t in ts])
+        gp = _pointers([t for ts in zip(*grads) for t in ts])
     sizes, tp, mp, vp = array.array("q", sizes), _pointers(theta), _pointers(m), _pointers(v)
     rc = L.repops_adamw(n, _address(sizes), _address(tp), len(grads), _address(gp), kind, _address(order), _address(mp),
                         _address(vp), _address(scale_ptrs[0]), _address(scale_ptrs[1]), _address(decay),

@@ -453,7 +453,22 @@ struct Range {
 
 // Whether a written range shares a byte with any other.
 bool ranges_clash(std::vector<Range> &r) {
-    std::sort(r.begin(), r.end());
+    // lists of tensors mostly come in a few ascending stretches, which merge quicker than
+    // they sort
+    std::vector<size_t> cut{0}, next;
+    for (size_t i = 1; i < r.size(); ++i)
+        if (r[i] < r[i - 1]) cut.push_back(i);
+    cut.push_back(r.size());
+    while (cut.size() > 2) {
+        next.assign(1, 0);
+        for (size_t k = 0; k + 1 < cut.size(); k += 2) {
+            const size_t last = std::min(k + 2, cut.size() - 1);
+            if (last == k + 2)
+                std::inplace_merge(r.begin() + ptrdiff_t(cut[k]), r.begin() + ptrdiff_t(cut[k + 1]), r.begin() + ptrdiff_t(cut[last]));
+            next.push_back(cut[last]);
+        }
+        cut.swap(next);
+    }
     uintptr_t end = 0, written_end = 0;
     for (const Range &x : r) {
         if (x.lo < written_end || (x.written && x.lo < end)) return true;
@@ -525,19 +540,22 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
         if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
         if (n == 0) continue;
         if (!theta[i] || !m[i] || !v[i] || (eight && (!m_scale[i] || !v_scale[i]))) return REPOPS_ERR_INVALID_ARG;
-        range(theta[i], uint64_t(n) * 4u, true);
-        range(m[i], uint64_t(n) * ssize, true);
-        range(v[i], uint64_t(n) * ssize, true);
-        if (eight) {
-            range(m_scale[i], uint64_t(n + kGroup - 1) / kGroup, true);
-            range(v_scale[i], uint64_t(n + kGroup - 1) / kGroup, true);
-        }
-        for (int c = 0; c < contributors; ++c) {
-            const void *g = grads[int64_t(i) * contributors + c];
-            if (!g) return REPOPS_ERR_INVALID_ARG;
-            range(g, uint64_t(n) * gsize, false);
-        }
+        for (int c = 0; c < contributors; ++c)
+            if (!grads[int64_t(i) * contributors + c]) return REPOPS_ERR_INVALID_ARG;
     }
+    auto list = [&](auto p, int stride, bool written, auto bytes) {
+        for (int i = 0; i < tensors; ++i)
+            if (sizes[i]) range(p[int64_t(i) * stride], bytes(uint64_t(sizes[i])), written);
+    };
+    auto group_bytes = [](uint64_t n) { return (n + kGroup - 1) / kGroup; };
+    list(theta, 1, true, [](uint64_t n) { return n * 4u; });
+    list(m, 1, true, [&](uint64_t n) { return n * ssize; });
+    list(v, 1, true, [&](uint64_t n) { return n * ssize; });
+    if (eight) {
+        list(m_scale, 1, true, group_bytes);
+        list(v_scale, 1, true, group_bytes);
+    }
+    for (int c = 0; c < contributors; ++c) list(grads + c, contributors, false, [&](uint64_t n) { return n * gsize; });
     if (ranges.empty()) return REPOPS_OK;
     if (scalars_on_device) range(scalars, 16, false);
     if (grad_scale) range(grad_scale, 4, false);
