@@ -1127,11 +1127,12 @@ int repops_adamw_scalars(int64_t step, const double *rates, uint32_t seed, uint3
  * with m_scale and v_scale, one byte an element and one scale byte for every
  * REPOPS_ADAMW_GROUP of them (the last group may be shorter).  The arrays
  * themselves (sizes, theta, ..., decay: one weight decay a tensor, NULL for
- * none) are host memory, what they point to is device memory, each of any
- * alignment.  hyper (host): beta1, beta2 and eps in binary64.  scalars: of repops_adamw_scalars, on the host, or with
- * scalars_on_device != 0 on the device (read by the kernels, so that a captured
- * graph can be replayed for step after step).  grad_scale: a device float that
- * multiplies the mean gradient (clipping), or NULL.
+ * none) are host memory, what they point to is device memory, aligned to its
+ * elements and no further.  hyper (host): beta1, beta2 and eps in binary64.
+ * scalars: of repops_adamw_scalars, on the host, or with scalars_on_device != 0 on
+ * the device (read by the kernels, so that a captured graph can be replayed for
+ * step after step).  grad_scale: a device float that multiplies the mean gradient
+ * (clipping), or NULL.
  * Every step one binary32 rounding, c1 = fl(1 - beta1), c2 = fl(1 - beta2),
  * (lr, s, b) = scalars:
  *   g = the fold of the gradients in `order` divided by their count, as
@@ -1154,8 +1155,8 @@ int repops_adamw_scalars(int64_t step, const double *rates, uint32_t seed, uint3
  *   of at least 1.  (fmix32: MurmurHash3's finaliser.)
  * No two tensors may share memory, nor a written tensor a gradient (ALIAS); one
  * gradient may serve several contributors.  ORDER for an order that is not a
- * permutation; INVALID_ARG for null pointers, unknown types, betas outside
- * [0, 1), eps < 0, sizes above 2^40. */
+ * permutation; INVALID_ARG for null or misaligned (to the element) pointers,
+ * unknown types, betas outside [0, 1), eps < 0, sizes above 2^40. */
 int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
                  const void *const *grads, int grad_type, const int *order, void *const *m,
                  void *const *v, uint8_t *const *m_scale, uint8_t *const *v_scale,
@@ -1204,7 +1205,8 @@ int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const ui
  *   p = 1/3 + zz*(1/5 + zz*(1/7 + zz*(1/9))) by Horner's rule;
  *   i = fl(1/T), lse = M*i + ln S,  logp = (x_t - M)*i - ln S,  H = ln S -
  *   0x1.62e43p-1*(Q/S).
- * Row pitch ldx >= cols; stats on a 16-byte boundary.  1 <= cols, 0 <= top <= cols,
+ * Row pitch ldx >= cols; stats on a 16-byte boundary, the others on their
+ * elements'.  1 <= cols, 0 <= top <= cols,
  * 1e-6 <= T <= 1e6, else INVALID_ARG; UNSUPPORTED for top above 32, more than
  * 16384000 columns or 2^27 rows; outputs must not overlap inputs or each other
  * (ALIAS). */

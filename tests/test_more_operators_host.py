@@ -67,6 +67,9 @@ def test_adamw_refuses(L):
     assert call(m=ptrs(E, 0)) == INVALID
     assert call(ms=ptrs(G, G + 1)) == INVALID                          # one scale without the other
     assert call(scalars=None) == INVALID
+    assert call(theta=ptrs(A + 2, B)) == INVALID                       # off its elements' boundary
+    assert call(m=ptrs(E, E + 402)) == INVALID and call(v=ptrs(F + 1, F + 400)) == INVALID
+    assert call(grads=ptrs(C, D + 1), kind=1) == INVALID and call(grads=ptrs(C + 2, D)) == INVALID
     assert call(eps=-1.0) == INVALID
     assert call(eps=float("nan")) == INVALID
     assert call(b1=1.0) == INVALID
@@ -88,6 +91,7 @@ def test_adamw_refuses(L):
     assert mo(0, None, None, None, None, None, None, None) == OK
     assert mo(-1, A, B, C, D, E, F, None) == INVALID
     assert mo(10, A, B, C, None, E, F, None) == INVALID
+    assert mo(10, A, B, C, D, E + 2, F, None) == INVALID
     assert mo(10, A, B, C, D, E, E + 36, None) == ALIAS
     assert mo(10, A, B, C, D, A + 8, F, None) == ALIAS
 
@@ -100,7 +104,9 @@ def test_logprobs_refuse(L):
     assert call(rows=0) == OK
     for bad in (dict(rows=-1), dict(cols=0), dict(kind=9), dict(ld=99), dict(x=None), dict(x=A + 2), dict(logp=None),
                 dict(stats=None), dict(stats=D + 4), dict(T=0.0), dict(T=-1.0), dict(T=float("nan")), dict(T=1e7),
-                dict(top=-1), dict(top=101), dict(top=3), dict(top=3, tl=E), dict(ld=1 << 62)):
+                dict(top=-1), dict(top=101), dict(top=3), dict(top=3, tl=E), dict(ld=1 << 62), dict(t=B + 4),
+                dict(logp=C + 2), dict(lse=C + 17), dict(ent=C + 34), dict(top=2, tl=E + 1, ti=F),
+                dict(top=2, tl=E, ti=F + 4)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(top=33, tl=E, ti=F), dict(cols=16384001, ld=16384001), dict(rows=(1 << 27) + 1)):
         assert call(**bad) == UNSUPPORTED, bad
@@ -112,7 +118,7 @@ def test_logprobs_refuse(L):
 
     assert back(rows=0) == OK
     for bad in (dict(rows=-1), dict(cols=0), dict(kind=-1), dict(dl=None), dict(t=None), dict(st=None), dict(st=D + 8),
-                dict(dx=None), dict(dx=F + 1), dict(ldd=99), dict(T=0.0)):
+                dict(dx=None), dict(dx=F + 1), dict(ldd=99), dict(T=0.0), dict(t=B + 2), dict(dl=E + 1), dict(de=G + 2)):
         assert back(**bad) == INVALID, bad
     for bad in (dict(dx=A, ldd=101), dict(dx=A + 400), dict(dx=D), dict(dx=E), dict(dx=B), dict(de=F + 16)):
         assert back(**bad) == ALIAS, bad
@@ -128,7 +134,8 @@ def test_head_norm_rope_refuses(L):
     for bad in (dict(rows=-1), dict(q=-1), dict(dim=0), dict(kind=4), dict(ldx=191), dict(ldy=191), dict(x=None),
                 dict(y=None), dict(x=A + 2), dict(qg=None), dict(kg=None), dict(inverse=1), dict(pairs=33), dict(pairs=-1),
                 dict(cos=None), dict(positions=0), dict(layout=2), dict(first=-1), dict(period=0), dict(first=47),
-                dict(pos=F, wide=2)):
+                dict(pos=F, wide=2), dict(pos=F + 2), dict(pos=F + 4, wide=1), dict(qg=B + 2), dict(kg=B + 258),
+                dict(cos=C + 1), dict(sin=D + 2)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(dim=513, ldx=1539, ldy=1539), dict(positions=1 << 31), dict(q=65537, ldx=1 << 24, ldy=1 << 24)):
         assert call(**bad) == UNSUPPORTED, bad
@@ -194,3 +201,18 @@ def test_the_references_agree_with_their_formats():
     for s in (0.5, 1.0, 1.4142135623730951, 1.5, 2.0, 131072.7, 3e38):
         want = np.log(np.float64(np.float32(s)))
         assert abs(logprobs_ref.ln_fixed(s) - want) <= 2.0 ** -22 * abs(want)
+
+
+def test_models_refuse_what_they_lack():
+    import torch
+    from verifiable_repops_gemm_gb300 import decoder, train
+    cfg = decoder.DecoderConfig(d=32, heads=2, kv_heads=2, ffn=32, seq_len=8)
+    model = train.Model(cfg, 1, "cpu")
+    with pytest.raises(ValueError):
+        train.token_gradient(model, torch.zeros(8, 32), torch.zeros(8, dtype=torch.int64), model.gradient_buffer(), None)
+    with pytest.raises(ValueError):
+        train.AdamW(model, 1e-3, bits=16)
+    for bad in (-2, 3, 18):
+        with pytest.raises(ValueError):
+            decoder.rope_tables(decoder.DecoderConfig(d=32, heads=2, kv_heads=2, ffn=32, seq_len=8, rope_base=10000.0,
+                                                      rope_dim=bad), "cpu")

@@ -540,9 +540,13 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
         if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
         if (n == 0) continue;
         if (!theta[i] || !m[i] || !v[i] || (eight && (!m_scale[i] || !v_scale[i]))) return REPOPS_ERR_INVALID_ARG;
-        for (int c = 0; c < contributors; ++c)
-            if (!grads[int64_t(i) * contributors + c]) return REPOPS_ERR_INVALID_ARG;
+        if (misaligned(theta[i], 4) || misaligned(m[i], ssize) || misaligned(v[i], ssize)) return REPOPS_ERR_INVALID_ARG;
+        for (int c = 0; c < contributors; ++c) {
+            const void *g = grads[int64_t(i) * contributors + c];
+            if (!g || misaligned(g, gsize)) return REPOPS_ERR_INVALID_ARG;
+        }
     }
+    if (misaligned(scalars, 4) || misaligned(grad_scale, 4)) return REPOPS_ERR_INVALID_ARG;
     auto list = [&](auto p, int stride, bool written, auto bytes) {
         for (int i = 0; i < tensors; ++i)
             if (sizes[i]) range(p[int64_t(i) * stride], bytes(uint64_t(sizes[i])), written);
@@ -632,7 +636,8 @@ extern "C" int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *
                                     const uint8_t *v_scale, float *m_out, float *v_out, cudaStream_t stream) {
     if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
     if (n == 0) return REPOPS_OK;
-    if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return REPOPS_ERR_INVALID_ARG;
+    if (!m || !v || !m_scale || !v_scale || !m_out || !v_out || misaligned(m_out, 4) || misaligned(v_out, 4))
+        return REPOPS_ERR_INVALID_ARG;
     const uint64_t groups = uint64_t(n + kGroup - 1) / kGroup, bytes = uint64_t(n) * 4u;
     for (const auto &in : {std::pair<const void *, uint64_t>{m, uint64_t(n)}, {v, uint64_t(n)}, {m_scale, groups}, {v_scale, groups}})
         if (ranges_overlap(m_out, bytes, in.first, in.second) || ranges_overlap(v_out, bytes, in.first, in.second))

@@ -602,6 +602,9 @@ int check_shape(int64_t rows, int64_t q, int64_t k, int64_t dim, int type) {
 
 int check_table(const HeadArgs &a, int64_t rows) {
     if (a.pairs < 0 || 2 * int64_t(a.pairs) > a.dim || (a.pos_wide != 0 && a.pos_wide != 1)) return REPOPS_ERR_INVALID_ARG;
+    if (misaligned(a.q_gain, 4) || misaligned(a.k_gain, 4) || misaligned(a.pos, a.pos_wide ? 8 : 4) ||
+        (a.pairs && (misaligned(a.cosv, 4) || misaligned(a.sinv, 4))))
+        return REPOPS_ERR_INVALID_ARG;
     if (a.pairs && (!a.cosv || !a.sinv || a.positions < 1 || a.positions > INT64_MAX / 8 / a.pairs))
         return REPOPS_ERR_INVALID_ARG;
     if (a.positions > INT32_MAX) return REPOPS_ERR_UNSUPPORTED;
@@ -682,8 +685,7 @@ extern "C" int repops_head_norm_rope(int64_t rows, int64_t q_heads, int64_t k_he
     uint64_t xb, yb;
     if (!span_bytes(rows, width, ldx, size, &xb) || !span_bytes(rows, width, ldy, size, &yb)) return REPOPS_ERR_INVALID_ARG;
     if (rows == 0 || width == 0) return REPOPS_OK;
-    if (!x || !y || reinterpret_cast<uintptr_t>(x) % size != 0 || reinterpret_cast<uintptr_t>(y) % size != 0)
-        return REPOPS_ERR_INVALID_ARG;
+    if (!x || !y || misaligned(x, size) || misaligned(y, size)) return REPOPS_ERR_INVALID_ARG;
     const uint64_t tb = pairs ? uint64_t(positions) * uint64_t(pairs) * 4u : 0, gb = uint64_t(dim) * 4u,
                    pb = uint64_t(rows) * (pos_wide ? 8u : 4u);
     const Span out{y, yb};
@@ -735,8 +737,8 @@ extern "C" int repops_head_norm_rope_backward(int64_t rows, int64_t q_heads, int
         !span_bytes(rows, width, lddx, size, &dxb))
         return REPOPS_ERR_INVALID_ARG;
     if (rows == 0 || width == 0) return REPOPS_OK;
-    if (!x || !dy || !dx || reinterpret_cast<uintptr_t>(x) % size != 0 || reinterpret_cast<uintptr_t>(dy) % size != 0 ||
-        reinterpret_cast<uintptr_t>(dx) % size != 0)
+    if (!x || !dy || !dx || misaligned(x, size) || misaligned(dy, size) || misaligned(dx, size) || misaligned(dq_gain, 4) ||
+        misaligned(dk_gain, 4))
         return REPOPS_ERR_INVALID_ARG;
     const int64_t q_runs = ceil_div(rows * q_heads, RUN), k_runs = ceil_div(rows * k_heads, RUN);
     if (q_runs + k_runs > INT32_MAX) return REPOPS_ERR_UNSUPPORTED;

@@ -840,7 +840,8 @@ extern "C" int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, 
     if (rows == 0) return REPOPS_OK;
     uint64_t xb;
     if (!x || !logp || !lse || !entropy || !stats || (top && (!top_logp || !top_ids)) ||
-        reinterpret_cast<uintptr_t>(stats) % 16 != 0 || reinterpret_cast<uintptr_t>(x) % storage_size(x_type) != 0 ||
+        misaligned(stats, 16) || misaligned(x, storage_size(x_type)) || misaligned(targets, 8) || misaligned(logp, 4) ||
+        misaligned(lse, 4) || misaligned(entropy, 4) || (top && (misaligned(top_logp, 4) || misaligned(top_ids, 8))) ||
         !span_bytes(rows, cols, ldx, storage_size(x_type), &xb))
         return REPOPS_ERR_INVALID_ARG;
     const uint64_t vb = uint64_t(rows) * 4u, tb = uint64_t(rows) * uint64_t(top);
@@ -888,8 +889,8 @@ extern "C" int repops_token_logprobs_backward(int64_t rows, int64_t cols, const 
     if (rows == 0) return REPOPS_OK;
     const unsigned size = storage_size(x_type);
     uint64_t xb, db;
-    if (!x || !dx || !stats || (!dlogp && !dentropy) || (dlogp && !targets) || reinterpret_cast<uintptr_t>(stats) % 16 != 0 ||
-        reinterpret_cast<uintptr_t>(x) % size != 0 || reinterpret_cast<uintptr_t>(dx) % size != 0 ||
+    if (!x || !dx || !stats || (!dlogp && !dentropy) || (dlogp && !targets) || misaligned(stats, 16) ||
+        misaligned(x, size) || misaligned(dx, size) || misaligned(targets, 8) || misaligned(dlogp, 4) || misaligned(dentropy, 4) ||
         !span_bytes(rows, cols, ldx, size, &xb) || !span_bytes(rows, cols, lddx, size, &db))
         return REPOPS_ERR_INVALID_ARG;
     const uint64_t vb = uint64_t(rows) * 4u;

@@ -16,6 +16,9 @@ namespace {
 }
 [[maybe_unused]] inline unsigned storage_size(int t) { return t == REPOPS_TYPE_F32 ? 4u : 2u; }
 
+// Whether an address is no multiple of `size` bytes (null is).
+[[maybe_unused]] inline bool misaligned(const void *p, unsigned size) { return reinterpret_cast<uintptr_t>(p) % size != 0; }
+
 // Bytes spanned by rows x cols elements of `size` bytes at pitch ld; false
 // when ld is short or the span overflows.
 [[maybe_unused]] inline bool span_bytes(int64_t rows, int64_t cols, int64_t ld, unsigned size, uint64_t *bytes) {
