@@ -116,6 +116,32 @@ def test_gradient_against_binary64(rp, name):
         assert (a - b).norm() <= 2e-5 * b.norm(), (layer, key)
 
 
+def test_upstream_gradients_leave_the_vocabulary_at_zero(rp):
+    """A buffer that held another gradient before: every weight's part is written."""
+    cfg = CFGS["adjacent"]
+    model = train.Model(cfg, 1, DEV, seed=3, vocab=VOCAB)
+    ws = train.Workspace(model, T, DEV)
+    dy = torch.randn(T, cfg.d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(12))
+    clean = train.contributor_gradient(model, batch(4, cfg)[0], dy, model.gradient_buffer(), ws)
+    used = train.contributor_gradient(model, batch(4, cfg)[0], dy, model.gradient_buffer().fill_(float("nan")), ws)
+    for layer, key, off, shape in model.slots:
+        part = slice(off, off + math.prod(shape))
+        assert torch.equal(clean[part], used[part]), (layer, key)
+        assert layer < model.layers or not used[part].any()
+
+
+def test_a_refused_step_counts_for_nothing(rp):
+    cfg = CFGS["adjacent"]
+    model = train.Model(cfg, 1, DEV, seed=3)
+    opt = train.AdamW(model, 1e-3)
+    g = model.gradient_buffer()
+    with pytest.raises(Exception):
+        opt.step([g, g], [0, 0])
+    assert opt.steps == 0
+    opt.step([g, g], [1, 0])
+    assert opt.steps == 1
+
+
 def contributions(seed, cfg):
     return [(did, *batch(seed + i, cfg)) for i, did in enumerate((b"did:zoo:charlie", b"did:zoo:alice", b"did:zoo:bob"))]
 

@@ -169,6 +169,8 @@ def rope_tables(cfg: DecoderConfig, device):
     p * f_i for positions p < seq_len."""
     if not cfg.rope_base:
         return None
+    if cfg.rope_dim % 2 or not 0 <= cfg.rope_dim <= cfg.d_head:
+        raise ValueError("rope_dim must be even and at most a head's width")
     freq = rope_frequencies((cfg.rope_dim or cfg.d_head) // 2, math.log(cfg.rope_base), device,
                             factor=cfg.rope_factor, original=cfg.rope_original)
     return rope_table(cfg.seq_len, freq)

@@ -115,10 +115,15 @@ def _backward(model: Model, gviews, ws: Workspace):
 
 def contributor_gradient(model: Model, x, dy, grad_flat, ws: Workspace):
     """grad_flat <- the gradient of the model's parameters for input x and
-    upstream gradient dy (both T x d); returns grad_flat."""
+    upstream gradient dy (both T x d: of the last layer's output, so that a
+    vocabulary's norm and weights get 0); returns grad_flat."""
     _forward(model, x, ws)
     ws.d.copy_(dy)
-    _backward(model, model.views(grad_flat), ws)
+    gviews = model.views(grad_flat)
+    for g in gviews[model.layers:]:
+        for v in g.values():
+            v.zero_()
+    _backward(model, gviews, ws)
     return grad_flat
 
 
@@ -126,6 +131,8 @@ def token_gradient(model: Model, x, targets, grad_flat, ws: Workspace):
     """grad_flat <- the gradient, for input x (T x d), of the mean negative log
     probability of targets (int64, T; a negative one is no target) under a model
     with a vocabulary; returns (grad_flat, the targets' log probabilities)."""
+    if not model.vocab:
+        raise ValueError("the model has no vocabulary to take targets from")
     cfg, out = model.cfg, model.weights[model.layers]
     _forward(model, x, ws)
     h = rmsnorm_rows(ws.h, out["g_out"], cfg.eps, out=ws.t)
@@ -172,9 +179,9 @@ class AdamW:
 
     def step(self, grads, order) -> None:
         """One step of theta from the contributors' flat gradients, folded in `order`."""
-        self.steps += 1
-        adamw(self._slots(self.model.theta), [self._slots(g) for g in grads], step=self.steps, lr=self.lr,
+        adamw(self._slots(self.model.theta), [self._slots(g) for g in grads], step=self.steps + 1, lr=self.lr,
               betas=self.betas, eps=self.eps, weight_decay=self.decay, order=order, seed=self.seed, **self.views)
+        self.steps += 1
 
     def roots(self):
         """The Merkle root of each of the moments' buffers: what, with theta's, a
