@@ -96,8 +96,9 @@ int repops_last_cuda_error(void);
  * kernel's bounded wait on its own asynchronous copies gave up since the last
  * read (the output of that kernel is then undefined), or -- in the checked
  * build librepops_debug.so only, whose hot-path kernels (GEMM, mean + SGD,
- * Merkle) test every global access against its buffer's span and skip one
- * outside it -- REPOPS_ERR_BOUNDS if such an access was skipped.  Returns REPOPS_OK or
+ * Merkle; the 8-bit, block-edge, log-probability, head-norm and AdamW ones) test
+ * every global access against its buffer's span and skip one outside it --
+ * REPOPS_ERR_BOUNDS if such an access was skipped.  Returns REPOPS_OK or
  * REPOPS_ERR_CUDA / REPOPS_ERR_INVALID_ARG (null status_out). */
 int repops_device_status(cudaStream_t stream, int *status_out);
 

@@ -99,6 +99,10 @@ struct Tile {
 #define REPOPS_ADAM_OK(tile, base, size, p, bytes)                                                             \
     REPOPS_DBG_OK((DbgSpan{reinterpret_cast<uintptr_t>(base), reinterpret_cast<uintptr_t>(base) + uint64_t((tile).left) * (size)}), \
                   p, bytes, (tile).status)
+// The same for a byte of the scales of n elements.
+#define REPOPS_ADAM_SCALE_OK(base, n, p, status)                                                                          \
+    REPOPS_DBG_OK((DbgSpan{reinterpret_cast<uintptr_t>(base), reinterpret_cast<uintptr_t>(base) + uint64_t((n) + kGroup - 1) / kGroup}), \
+                  p, 1, status)
 
 // Elements e .. e+3 of a tile, `have` of them there (0 .. 4); the others +0.  FULL: all
 // four, aligned, asked about once for the tile.
@@ -111,9 +115,11 @@ __device__ __forceinline__ float4 load4(const Tile &t, const void *base, int e, 
         return load_four<TY>(DbgAccess{}, p, 0);
     }
     float v[4] = {0, 0, 0, 0};
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int i = 0; i < (FULL ? 0 : 4); ++i)
-        if (i < have && REPOPS_ADAM_OK(t, base, size, p + i * size, size)) v[i] = load_one<TY>(DbgAccess{}, p, i);
+        for (int i = 0; i < 4; ++i)
+            if (i < have && REPOPS_ADAM_OK(t, base, size, p + i * size, size)) v[i] = load_one<TY>(DbgAccess{}, p, i);
+    }
     return make_float4(v[0], v[1], v[2], v[3]);
 }
 
@@ -124,10 +130,12 @@ __device__ __forceinline__ void store4(const Tile &t, float *base, int e, int ha
         if (REPOPS_ADAM_OK(t, base, 4, p, 16)) store_four<REPOPS_TYPE_F32>(DbgAccess{}, p, 0, v);
         return;
     }
-    const float a[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (!FULL) {
+        const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(t, base, 4, p + i, 4)) p[i] = a[i];
+        for (int i = 0; i < 4; ++i)
+            if (i < have && REPOPS_ADAM_OK(t, base, 4, p + i, 4)) p[i] = a[i];
+    }
 }
 
 template <bool FULL>
@@ -136,9 +144,11 @@ __device__ __forceinline__ uint32_t load_codes(const Tile &t, const uint8_t *bas
     if (FULL || (t.vec && have == 4))
         return REPOPS_ADAM_OK(t, base, 1, p, 4) ? __ldcs(reinterpret_cast<const uint32_t *>(p)) : 0u;
     uint32_t w = 0;
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) w |= uint32_t(p[i]) << (8 * i);
+        for (int i = 0; i < 4; ++i)
+            if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) w |= uint32_t(p[i]) << (8 * i);
+    }
     return w;
 }
 
@@ -149,9 +159,11 @@ __device__ __forceinline__ void store_codes(const Tile &t, uint8_t *base, int e,
         if (REPOPS_ADAM_OK(t, base, 1, p, 4)) __stcs(reinterpret_cast<uint32_t *>(p), w);
         return;
     }
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) p[i] = uint8_t(w >> (8 * i));
+        for (int i = 0; i < 4; ++i)
+            if (i < have && REPOPS_ADAM_OK(t, base, 1, p + i, 1)) p[i] = uint8_t(w >> (8 * i));
+    }
 }
 
 // ------------------------------------------------------------ 8-bit codes ----
@@ -245,7 +257,9 @@ __device__ __forceinline__ void run_tile(const AdamHead &h, const Entry &t, int6
     if constexpr (EIGHT) {
         if (int(threadIdx.x) < 2 * kScales) {
             const int i = threadIdx.x % kScales;
-            scales[threadIdx.x / kScales][i] = i < groups ? (int(threadIdx.x) < kScales ? ms_at : vs_at)[i] : 0;
+            const uint8_t *p = (int(threadIdx.x) < kScales ? ms_at : vs_at) + i;
+            scales[threadIdx.x / kScales][i] =
+                i < groups && REPOPS_ADAM_SCALE_OK(int(threadIdx.x) < kScales ? t.ms : t.vs, t.n, p, h.status) ? *p : 0;
         }
         __syncthreads();
     }
@@ -354,7 +368,9 @@ __device__ __forceinline__ void run_tile(const AdamHead &h, const Entry &t, int6
         __syncthreads();
         if (int(threadIdx.x) < 2 * kScales) {
             const int i = threadIdx.x % kScales;
-            if (i < groups) (int(threadIdx.x) < kScales ? ms_at : vs_at)[i] = uint8_t(scales[threadIdx.x / kScales][i]);
+            uint8_t *p = (int(threadIdx.x) < kScales ? ms_at : vs_at) + i;
+            if (i < groups && REPOPS_ADAM_SCALE_OK(int(threadIdx.x) < kScales ? t.ms : t.vs, t.n, p, h.status))
+                *p = uint8_t(scales[threadIdx.x / kScales][i]);
         }
     }
 }
@@ -406,8 +422,9 @@ adamw_moments_kernel(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_
         const Tile t{int(min(n - e, int64_t(1) << 20)), vec != 0, status};
         const uint32_t mc = load_codes<false>(t, m + e, 0, have), vc = load_codes<false>(t, v + e, 0, have);
         float4 x, y;
-        decode_m(mc, scale_of(__ldg(ms + e / kGroup)), x);
-        const float rs = scale_of(__ldg(vs + e / kGroup));
+        const bool in = REPOPS_ADAM_SCALE_OK(ms, n, ms + e / kGroup, status) && REPOPS_ADAM_SCALE_OK(vs, n, vs + e / kGroup, status);
+        decode_m(mc, in ? scale_of(__ldg(ms + e / kGroup)) : 0.0f, x);
+        const float rs = in ? scale_of(__ldg(vs + e / kGroup)) : 0.0f;
         float *py = &y.x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
