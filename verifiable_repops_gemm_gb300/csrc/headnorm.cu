@@ -20,10 +20,11 @@
 // of the terms as run results instead of writing them all.
 //
 // Measured, 4096 rows of 32 query and 8 key heads of 64 in float32, graph-replayed: 20.7
-// us forward (4.1 TB/s; a CTA's heads in common, barriers between the phases: 24.8), 42
-// us with the gains' gradients backward (3.0 TB/s; 47 with a CTA's in common).  What
-// bounds them now is the issue of some 30 instructions a value forward and 65 backward,
-// most of them addresses, swizzles and the trees' additions one by one.
+// us forward (4.1 TB/s; a CTA's heads in common, barriers between the phases: 24.8), 39
+// us with the gains' gradients backward (3.2 TB/s; 47 with a CTA's in common, 42 with
+// each head's loads behind the one's before).  What bounds them now are the latencies of
+// a warp's phases together with the issue of some 37 instructions a value forward and 60
+// backward, most of them addresses, swizzles and the trees' additions one by one.
 #include <algorithm>
 
 #include "colfold.cuh"
@@ -338,6 +339,49 @@ struct WarpHeadsBack {
     float inv[RUN], mean[RUN];
 };
 
+// Chunk c of heads from, from + step, .. into shared memory, dy turned back; N heads'
+// loads in flight.  PAIR: chunk c + turned with it, its partner in a rotation of halves.
+constexpr int kBatch = 4;
+template <int TY, int N, bool PAIR>
+__device__ __forceinline__ void load_heads(const HeadArgs &a, WarpHeadsBack &h, int here, int from, int step, int c,
+                                           int turned, Turn &kept) {
+    constexpr int P = PAIR ? 2 : 1;
+    const int runs = a.runs.d;
+    for (int u0 = from; u0 < here; u0 += N * step) {
+        float4 x[N][P], g[N][P];
+        int pos[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = u0 + i * step;
+            pos[i] = u < here ? h.unit[u].pos : -1;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                x[i][p] = g[i][p] = make_float4(0, 0, 0, 0);
+                if (pos[i] != -1) {
+                    g[i][p] = load_four<TY>(a, a.dy, h.unit[u].dy + 4 * (c + p * turned));
+                    x[i][p] = load_four<TY>(a, a.x, h.unit[u].x + 4 * (c + p * turned));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = u0 + i * step;
+            if (pos[i] != -1) {
+                if constexpr (PAIR) rotate_halves<true>(a, kept, pos[i], 4 * c, g[i][0], g[i][P - 1]);
+                else if (!a.halves) rotate_adjacent<true>(a, kept, pos[i], c, g[i][0]);
+            }
+            if (u < here) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int at = chunk_at(u * runs, c + p * turned);
+                    h.x[at] = x[i][p];
+                    h.g[at] = g[i][p];
+                }
+            }
+        }
+    }
+}
+
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, int64_t q_runs) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -360,31 +404,12 @@ __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, in
     const float *gain = key ? a.k_gain : a.q_gain;
     const int turned = a.halves ? a.pairs / 4 : 0;
     if constexpr (VEC) {
-        const float4 zero = make_float4(0, 0, 0, 0);
-        each_part<Turn, 4>(here, a.per, a.per_shift, [&](int u, int w, Turn &kept) {
-            const int c = w < turned ? w : w + turned;
-            const Unit t = h.unit[u];
-            const bool live = t.pos != -1;
-            float4 g = zero, x = zero;
-            if (live) {
-                g = load_four<TY>(a, a.dy, t.dy + 4 * c);
-                x = load_four<TY>(a, a.x, t.x + 4 * c);
-            }
-            if (w < turned) {
-                float4 g2 = zero, x2 = zero;
-                if (live) {
-                    g2 = load_four<TY>(a, a.dy, t.dy + 4 * (c + turned));
-                    x2 = load_four<TY>(a, a.x, t.x + 4 * (c + turned));
-                    rotate_halves<true>(a, kept, t.pos, 4 * c, g, g2);
-                }
-                h.x[chunk_at(u * runs, c + turned)] = x2;
-                h.g[chunk_at(u * runs, c + turned)] = g2;
-            } else if (live && !a.halves) {
-                rotate_adjacent<true>(a, kept, t.pos, c, g);
-            }
-            h.x[chunk_at(u * runs, c)] = x;
-            h.g[chunk_at(u * runs, c)] = g;
-        });
+        const int sub = lane & ((1 << a.per_shift) - 1), from = lane >> a.per_shift, step = 32 >> a.per_shift;
+        for (int w = sub; w < a.per; w += 1 << a.per_shift) {
+            Turn kept;
+            if (w < turned) load_heads<TY, kBatch / 2, true>(a, h, here, from, step, w, turned, kept);
+            else load_heads<TY, kBatch, false>(a, h, here, from, step, w + turned, turned, kept);
+        }
     } else {
         each_part<Nothing, 1>(here, a.per, a.per_shift, [&](int u, int j, Nothing &) {
             const Unit t = h.unit[u];
@@ -517,7 +542,9 @@ __global__ void __launch_bounds__(1024) gain_fold_kernel(const GainFold a) {
         float acc = 0.0f;
         if (ty < groups) {
             acc = part[ty * RUN][tx];
-            for (int i = 1; i < min(RUN, n - ty * RUN); ++i) acc = __fadd_rn(acc, part[ty * RUN + i][tx]);
+            const int m = min(RUN, n - ty * RUN);
+#pragma unroll 8
+            for (int i = 1; i < m; ++i) acc = __fadd_rn(acc, part[ty * RUN + i][tx]);
         }
         __syncthreads();
         if (ty < groups) part[ty][tx] = acc;
