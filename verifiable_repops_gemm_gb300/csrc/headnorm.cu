@@ -334,16 +334,30 @@ __global__ void __launch_bounds__(kWarps * 32, 10) head_forward_kernel(const Hea
 // takes the heads of 32 of its runs of columns; the terms of the gain's gradient
 // replace the turned dy in shared memory, where the CTA folds them.
 struct WarpHeadsBack {
-    float4 x[RUN * 8], g[RUN * 8];
-    Unit unit[RUN];
-    float inv[RUN], mean[RUN];
+    float4 *x, *g;                   // 32 runs of 32 values each
+    Unit *unit;                      // where its heads lie; no more than there are: heads of
+    float *inv, *mean;               // 64 leave room for 12 CTAs an SM so, for 11 with 32
 };
+constexpr size_t kStage = RUN * 8 * sizeof(float4);
+__host__ __device__ constexpr size_t back_bytes(int units) {
+    return 2 * kStage + (size_t(units) * (sizeof(Unit) + 2 * sizeof(float)) + 15) / 16 * 16;
+}
+__device__ __forceinline__ WarpHeadsBack back_heads(unsigned char *smem, int warp, int units) {
+    unsigned char *p = smem + size_t(warp) * back_bytes(units);
+    WarpHeadsBack h;
+    h.x = reinterpret_cast<float4 *>(p);
+    h.g = reinterpret_cast<float4 *>(p + kStage);
+    h.unit = reinterpret_cast<Unit *>(p + 2 * kStage);
+    h.inv = reinterpret_cast<float *>(h.unit + units);
+    h.mean = h.inv + units;
+    return h;
+}
 
 // Chunk c of heads from, from + step, .. into shared memory, dy turned back; N heads'
 // loads in flight.  PAIR: chunk c + turned with it, its partner in a rotation of halves.
 constexpr int kBatch = 4;
 template <int TY, int N, bool PAIR>
-__device__ __forceinline__ void load_heads(const HeadArgs &a, WarpHeadsBack &h, int here, int from, int step, int c,
+__device__ __forceinline__ void load_heads(const HeadArgs &a, const WarpHeadsBack &h, int here, int from, int step, int c,
                                            int turned, Turn &kept) {
     constexpr int P = PAIR ? 2 : 1;
     const int runs = a.runs.d;
@@ -385,9 +399,8 @@ __device__ __forceinline__ void load_heads(const HeadArgs &a, WarpHeadsBack &h, 
 template <int TY, bool VEC>
 __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, int64_t q_runs) {
     extern __shared__ __align__(16) unsigned char smem[];
-    WarpHeadsBack *all = reinterpret_cast<WarpHeadsBack *>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, runs = a.runs.d;
-    WarpHeadsBack &h = all[warp];
+    const WarpHeadsBack h = back_heads(smem, warp, a.units);
     float *fx = reinterpret_cast<float *>(h.x), *fg = reinterpret_cast<float *>(h.g);
     const int key = blockIdx.x >= q_runs;
     const int64_t run = blockIdx.x - (key ? q_runs : 0);
@@ -450,7 +463,7 @@ __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, in
         }
     }
     const float mean = __fdiv_rn(fold_head(a, acc), float(a.dim));
-    if (first == 0) {
+    if (first == 0 && mine < a.units) {
         h.inv[mine] = inv;
         h.mean[mine] = mean;
     }
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, in
         const int chunk = j >> 2;
         float sum = 0.0f;
         for (int w = 0, done = 0; done < in_run; ++w) {
-            const float *g = reinterpret_cast<const float *>(all[w].g) + (j & 3);
+            const float *g = reinterpret_cast<const float *>(back_heads(smem, w, a.units).g) + (j & 3);
             const int of = min(a.units, in_run - done);
 #pragma unroll 4
             for (int u = 0; u < of; ++u) {
@@ -605,7 +618,7 @@ template <int TY, bool VEC>
 int launch_backward(HeadArgs a, int64_t q_runs, int64_t k_runs, cudaStream_t s) {
     share(a, VEC);
     const int warps = (RUN + a.units - 1) / a.units;
-    const size_t smem = size_t(warps) * sizeof(WarpHeadsBack);
+    const size_t smem = size_t(warps) * back_bytes(a.units);
     auto kern = head_backward_kernel<TY, VEC>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
