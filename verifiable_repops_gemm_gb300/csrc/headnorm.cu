@@ -174,24 +174,32 @@ __device__ __forceinline__ float rotate_one(const HeadArgs &a, int pos, int j, F
 __device__ __forceinline__ int chunk_at(int r0, int c) { return stage_slot(r0 + (c >> 3), c & 7); }
 __device__ __forceinline__ int value_at(int r0, int j) { return 4 * chunk_at(r0, j >> 2) + (j & 3); }
 
-// The fold of run `run` of n values: f(value, column in the head).
-template <class F>
-__device__ __forceinline__ float fold_run(const float4 *stage, int run, int first, int n, F f) {
-    float acc;
-    if (n == RUN) {
+// The sum of the squares of run `run` of n values.  VEC: n is a multiple of four; with
+// heads of whole runs no lane is asked where its run ends (heads of 80 otherwise: value
+// by value the shorter runs' lanes cost 5% of the backward).
+template <bool VEC>
+__device__ __forceinline__ float fold_squares(const HeadArgs &a, const float4 *stage, int run, int n) {
+    float acc = 0.0f;
+    auto chunk = [&](int c) {
+        const float4 v = stage[stage_slot(run, c)];
+        acc = c == 0 ? __fmul_rn(v.x, v.x) : __fadd_rn(acc, __fmul_rn(v.x, v.x));
+        acc = __fadd_rn(acc, __fmul_rn(v.y, v.y));
+        acc = __fadd_rn(acc, __fmul_rn(v.z, v.z));
+        acc = __fadd_rn(acc, __fmul_rn(v.w, v.w));
+    };
+    if (VEC && a.dim % RUN == 0) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float4 v = stage[stage_slot(run, c)];
-            const int j = first + 4 * c;
-            acc = c == 0 ? f(v.x, j) : __fadd_rn(acc, f(v.x, j));
-            acc = __fadd_rn(acc, f(v.y, j + 1));
-            acc = __fadd_rn(acc, f(v.z, j + 2));
-            acc = __fadd_rn(acc, f(v.w, j + 3));
-        }
+        for (int c = 0; c < 8; ++c) chunk(c);
+    } else if (VEC) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (4 * c < n) chunk(c);
     } else {
         const float *s = reinterpret_cast<const float *>(stage);
-        acc = f(s[4 * stage_slot(run, 0)], first);
-        for (int i = 1; i < n; ++i) acc = __fadd_rn(acc, f(s[4 * stage_slot(run, i >> 2) + (i & 3)], first + i));
+        for (int i = 0; i < n; ++i) {
+            const float v = s[4 * stage_slot(run, i >> 2) + (i & 3)], q = __fmul_rn(v, v);
+            acc = i == 0 ? q : __fadd_rn(acc, q);
+        }
     }
     return acc;
 }
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, 10) head_forward_kernel(const Hea
         const int first = run_first(a);
         float acc = 0.0f;
         if (lane < here * runs)
-            acc = fold_run(h.x, lane, first, min(RUN, a.dim - first), [](float v, int) { return __fmul_rn(v, v); });
+            acc = fold_squares<VEC>(a, h.x, lane, min(RUN, a.dim - first));
         const float inv = inv_rms(fold_head(a, acc), float(a.dim), a.eps);
         if (first == 0) h.inv[quotient(lane, a.runs)] = inv;
         __syncwarp();
@@ -439,21 +447,26 @@ __global__ void __launch_bounds__(512) head_backward_kernel(const HeadArgs a, in
     const int first = run_first(a), length = min(RUN, a.dim - first), mine = quotient(lane, a.runs);
     const bool folds = lane < here * runs;
     float acc = 0.0f;
-    if (folds) acc = fold_run(h.x, lane, first, length, [](float v, int) { return __fmul_rn(v, v); });
+    if (folds) acc = fold_squares<VEC>(a, h.x, lane, length);
     float inv = inv_rms(fold_head(a, acc), float(a.dim), a.eps);
     if (folds && h.unit[mine].pos == -1) inv = 0.0f;             // a row left alone adds +0, whatever eps
     if (folds) {
         auto term = [&](float x, float g, float w) { return __fmul_rn(__fmul_rn(g, w), __fmul_rn(x, inv)); };
-        if (VEC && length == RUN) {
-            const float4 *w4 = reinterpret_cast<const float4 *>(gain + first);
+        auto chunk = [&](int c) {
+            const float4 x = h.x[stage_slot(lane, c)], g = h.g[stage_slot(lane, c)];
+            const float4 w = load_const(a, reinterpret_cast<const float4 *>(gain + first) + c);
+            acc = c == 0 ? term(x.x, g.x, w.x) : __fadd_rn(acc, term(x.x, g.x, w.x));
+            acc = __fadd_rn(acc, term(x.y, g.y, w.y));
+            acc = __fadd_rn(acc, term(x.z, g.z, w.z));
+            acc = __fadd_rn(acc, term(x.w, g.w, w.w));
+        };
+        if (VEC && a.dim % RUN == 0) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float4 x = h.x[stage_slot(lane, c)], g = h.g[stage_slot(lane, c)], w = load_const(a, w4 + c);
-                acc = c == 0 ? term(x.x, g.x, w.x) : __fadd_rn(acc, term(x.x, g.x, w.x));
-                acc = __fadd_rn(acc, term(x.y, g.y, w.y));
-                acc = __fadd_rn(acc, term(x.z, g.z, w.z));
-                acc = __fadd_rn(acc, term(x.w, g.w, w.w));
-            }
+            for (int c = 0; c < 8; ++c) chunk(c);
+        } else if (VEC) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (4 * c < length) chunk(c);
         } else {
             for (int i = 0; i < length; ++i) {
                 const int at = 4 * stage_slot(lane, i >> 2) + (i & 3);
@@ -618,6 +631,7 @@ template <int TY, bool VEC>
 int launch_backward(HeadArgs a, int64_t q_runs, int64_t k_runs, cudaStream_t s) {
     share(a, VEC);
     const int warps = (RUN + a.units - 1) / a.units;
+    a.units = (RUN + warps - 1) / warps;             // as many heads for each: 8, not 10 and 2
     const size_t smem = size_t(warps) * back_bytes(a.units);
     auto kern = head_backward_kernel<TY, VEC>;
     if (smem > 48 * 1024) {
