@@ -481,9 +481,9 @@ __device__ __forceinline__ void store_first(float *p, float v) {
 
 // A cluster a row; its warps take the segments in turn, a block of 1024 columns in
 // registers at a time: its maximum first, then its exponentials.  Bound by the issue of
-// instructions in bfloat16 (4096 x 131072 in 346 us, 3.1 TB/s: 17 a value, of which 4.5
-// work on pairs and take two slots, 87% of the issue rate), nearer to memory in binary32
-// (4096 x 32768 in 99 us, 5.4 TB/s); few rows by latencies one after another (12.0 us
+// instructions in bfloat16 (4096 x 131072 in 322 us, 3.3 TB/s: 17 a value, of which 4.5
+// work on pairs and take two slots, 92% of the issue rate), nearer to memory in binary32
+// (4096 x 32768 in 92 us, 5.8 TB/s); few rows by latencies one after another (12.0 us
 // for one of 131072 with 8 alternatives).
 template <int TY, bool SHIFT>
 __global__ void __launch_bounds__(256) logprobs_kernel(const LpArgs a) {
@@ -782,11 +782,14 @@ template <int TY, bool SHIFT>
 int launch_logprobs(const LpArgs &a, cudaStream_t s) {
     DeviceInfo di;
     if (const int rc = current_device_info(&di); rc != REPOPS_OK) return rc;
-    // 32 warps an SM where there are segments for them, a CTA's first, then, for few
-    // rows, those of a cluster's CTAs; as few as take the same number of turns.  4096 rows
-    // of 131072 in bfloat16, graph-replayed: one warp a row 586 us, two 349; 1024 rows:
-    // two 107 us, eight 94; one row by eight warps of one CTA 30 us, by four CTAs 12.6
-    int warps = 1;
+    // Four warps a row of four segments or more: rows then end at more times than one, and
+    // the others' sums fill the time (4096 rows of 131072 in bfloat16, graph-replayed: one
+    // warp a row 586 us, two 346, three 335, four 322, five 332, eight 335; 4096 of 65536
+    // in binary32 two 180, four 170; 20000 of 8192, two segments, one 107, two 111).  More
+    // up to 32 warps an SM, a CTA's first, then, for few rows, those of a cluster's CTAs
+    // (1024 rows of 131072: two 107 us, eight 94; one row by eight warps of one CTA 30 us,
+    // by four CTAs 12); as few as take the same number of turns.
+    int warps = a.segments >= 4 ? 4 : 1;
     unsigned ctas = 1;
     while (warps < 8 && warps < a.segments && a.rows * warps < int64_t(32) * di.sms) warps *= 2;
     while (ctas < 8 && int(ctas) * warps < a.segments && a.rows * warps * ctas < int64_t(32) * di.sms) ctas *= 2;
@@ -879,7 +882,7 @@ extern "C" int repops_token_logprobs(int64_t rows, int64_t cols, const void *x, 
     a.reads(targets, uint64_t(rows) * 8u);
     for (const auto &o : outs) a.writes(o.p, o.b);
     if (const int rc = a.arm(); rc != REPOPS_OK) return rc;
-    // rows that all start on 16 bytes need no shifting (in bfloat16 347 us instead of 356)
+    // rows that all start on 16 bytes need no shifting (in bfloat16 9 us of 356 less)
     const bool aligned = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * storage_size(x_type) % 16 == 0;
     switch (x_type) {
         case REPOPS_TYPE_F32:
@@ -924,7 +927,7 @@ extern "C" int repops_token_logprobs_backward(int64_t rows, int64_t cols, const 
     a.writes(dx, db);
     if (const int rc = a.arm(); rc != REPOPS_OK) return rc;
     // every row of dx as far from a 16-byte boundary as the same row of x: 16 bytes an
-    // access (loss and gradient of 4096 x 32768 257 us, value by value 290)
+    // access (156 us for 4096 x 32768, value by value 32 more)
     const bool vec = (reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(dx)) % 16 == 0 &&
                      (ldx - lddx) * int64_t(size) % 16 == 0;
     switch (x_type) {
