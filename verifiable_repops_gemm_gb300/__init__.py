@@ -1559,6 +1559,18 @@ def token_logprobs_backward(logits, targets, stats, dlogp=None, dentropy=None, *
 _LAYOUTS = {"adjacent": ROPE_ADJACENT, "halves": ROPE_HALVES}
 
 
+def _zeroed(t, stream):
+    """t with +0 in every value, written in the order of the call's stream: on the current
+    one the zeros could land on what the call has written."""
+    import torch
+    if stream is None:
+        return t.zero_()
+    if isinstance(stream, int):              # 1: the runtime's other name of the default stream
+        stream = torch.cuda.ExternalStream(0 if stream == 1 else stream, device=t.device)
+    with torch.cuda.stream(stream):
+        return t.zero_()
+
+
 def _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period, name="x"):
     """(rows, head width, storage type, pitch) of the heads in x, and the rotation's
     arguments: (cos, sin, pairs, positions), (pos, wide, first, period)."""
@@ -1610,16 +1622,19 @@ def head_norm_rope(x, q_heads: int, k_heads: int, cos=None, sin=None, *, q_gain=
     sin (a rope_table) the norms alone.  A table of fewer than width / 2 pairs
     rotates the first columns of each head; layout "adjacent" pairs (2i, 2i + 1),
     "halves" (i, i + pairs).  positions: one for each row (int32 or int64), a
-    negative one leaves its row of out as it is; else first + (row mod period).
-    out may be x."""
+    negative one leaves its row of out as it is (0 without out); else first + (row mod
+    period).  out may be x."""
     import torch
     rows, dim, kind, ld, table, where = _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period)
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if positions is None else torch.zeros_like(x)
+    made = out is None
+    if made:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if out.dtype != x.dtype or out.shape != x.shape or (out.shape[1] > 1 and out.stride(1) != 1):
         raise ValueError("out must have the shape and dtype of x and unit column stride")
     gains = [_head_gain(t, n, dim, name) for t, n, name in ((q_gain, q_heads, "q_gain"), (k_gain, k_heads, "k_gain"))]
     handle = _stream_on_device(stream, x, cos, sin, q_gain, k_gain, positions, out)
+    if made and positions is not None:
+        _zeroed(out, stream)                 # rows without a position
     rc = load().repops_head_norm_rope(rows, q_heads, k_heads, dim, x.data_ptr(), kind, ld, *gains, eps, *table,
                                       _LAYOUTS[layout], int(bool(inverse)), *where, out.data_ptr(), _pitch(out, "out"),
                                       handle)
@@ -1639,13 +1654,13 @@ def head_norm_rope_backward(dy, x, q_heads: int, k_heads: int, cos=None, sin=Non
     """(dx, dq_gain, dk_gain) of head_norm_rope with gains given dy and its x
     (repops_head_norm_rope_backward); an entry is None where there are no heads of
     the kind.  dx may be dy; rows without a position add nothing to the gains'
-    gradients and are left as they are in dx.  Without gains the backward is
+    gradients and are left as they are in dx (0 without it).  Without gains the backward is
     head_norm_rope(dy, ..., inverse=True)."""
     import torch
     rows, dim, kind, ld, table, where = _heads_of(x, q_heads, k_heads, cos, sin, layout, positions, first, period)
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if positions is None else \
-            torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+    made = dx is None
+    if made:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     for t, name in ((dy, "dy"), (dx, "dx")):
         if t.dtype != x.dtype or t.shape != x.shape or (t.shape[1] > 1 and t.stride(1) != 1):
             raise ValueError("%s must have the shape and dtype of x and unit column stride" % name)
@@ -1663,6 +1678,8 @@ def head_norm_rope_backward(dy, x, q_heads: int, k_heads: int, cos=None, sin=Non
     if rows == 0:
         _zero_gradients(handle, dq_gain, dk_gain)
         return dx, dq_gain, dk_gain
+    if made and positions is not None:
+        _zeroed(dx, stream)                  # rows without a position
     need = _head_workspace(rows, q_heads, k_heads, dim)
     ws = _workspace(need, x.device, stream) if need else None
     rc = load().repops_head_norm_rope_backward(rows, q_heads, k_heads, dim, dy.data_ptr(), kind, _pitch(dy, "dy"),
