@@ -615,7 +615,7 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
     int64_t tiles = 0;
     int rc = REPOPS_OK;
     auto flush = [&](int next) {
-        if (h.tensors && rc == REPOPS_OK) {
+        if (tiles && rc == REPOPS_OK) {      // a table may hold empty tensors alone
             switch (grad_type) {
                 case REPOPS_TYPE_F32: rc = launch_typed<REPOPS_TYPE_F32>(h, w, unsigned(tiles), eight, stream); break;
                 case REPOPS_TYPE_F16: rc = launch_typed<REPOPS_TYPE_F16>(h, w, unsigned(tiles), eight, stream); break;
