@@ -1157,7 +1157,8 @@ int repops_adamw_scalars(int64_t step, const double *rates, uint32_t seed, uint3
  * No two tensors may share memory, nor a written tensor a gradient (ALIAS); one
  * gradient may serve several contributors.  ORDER for an order that is not a
  * permutation; INVALID_ARG for null or misaligned (to the element) pointers,
- * unknown types, betas outside [0, 1), eps < 0, sizes above 2^40. */
+ * unknown types, betas outside [0, 1), eps < 0, sizes above 2^40; ALLOC where the host
+ * has no memory for the list's ranges.  Nothing is launched then. */
 int repops_adamw(int tensors, const int64_t *sizes, float *const *theta, int contributors,
                  const void *const *grads, int grad_type, const int *order, void *const *m,
                  void *const *v, uint8_t *const *m_scale, uint8_t *const *v_scale,

@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
 #include <vector>
 
 #include "storage.cuh"
@@ -535,7 +536,7 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
                             const void *const *grads, int grad_type, const int *order, void *const *m, void *const *v,
                             uint8_t *const *m_scale, uint8_t *const *v_scale, const float *decay,
                             const double *hyper, const uint32_t *scalars, int scalars_on_device,
-                            const float *grad_scale, cudaStream_t stream) {
+                            const float *grad_scale, cudaStream_t stream) try {
     if (!hyper) return REPOPS_ERR_INVALID_ARG;
     const double beta1 = hyper[0], beta2 = hyper[1], eps = hyper[2];
     if (tensors < 0 || contributors < 1 || contributors > REPOPS_MEAN_MAX_CONTRIBUTORS || !known_storage(grad_type) ||
@@ -551,11 +552,6 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
     if (!sizes || !theta || !grads || !m || !v) return REPOPS_ERR_INVALID_ARG;
     const bool eight = m_scale != nullptr;
     const unsigned gsize = storage_size(grad_type), ssize = eight ? 1u : 4u;
-    std::vector<Range> ranges;
-    ranges.reserve(size_t(tensors) * size_t(5 + contributors) + 2);
-    auto range = [&](const void *p, uint64_t bytes, bool written) {
-        ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
-    };
     for (int i = 0; i < tensors; ++i) {
         const int64_t n = sizes[i];
         if (n < 0 || n > (int64_t(1) << 40)) return REPOPS_ERR_INVALID_ARG;
@@ -568,6 +564,11 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
         }
     }
     if (misaligned(scalars, 4) || misaligned(grad_scale, 4)) return REPOPS_ERR_INVALID_ARG;
+    std::vector<Range> ranges;
+    ranges.reserve(size_t(tensors) * size_t(5 + contributors) + 2);
+    auto range = [&](const void *p, uint64_t bytes, bool written) {
+        ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
+    };
     auto list = [&](auto p, int stride, bool written, auto bytes) {
         for (int i = 0; i < tensors; ++i)
             if (sizes[i]) range(p[int64_t(i) * stride], bytes(uint64_t(sizes[i])), written);
@@ -651,6 +652,8 @@ extern "C" int repops_adamw(int tensors, const int64_t *sizes, float *const *the
     }
     if (tiles) flush(tensors);
     return rc;
+} catch (const std::bad_alloc &) {       // before the first launch: the table is reserved in full
+    return REPOPS_ERR_ALLOC;
 }
 
 extern "C" int repops_adamw_moments(int64_t n, const uint8_t *m, const uint8_t *v, const uint8_t *m_scale,
