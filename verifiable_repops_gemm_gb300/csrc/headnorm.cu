@@ -351,6 +351,7 @@ constexpr size_t kStage = RUN * 8 * sizeof(float4);
 __host__ __device__ constexpr size_t back_bytes(int units) {
     return 2 * kStage + (size_t(units) * (sizeof(Unit) + 2 * sizeof(float)) + 15) / 16 * 16;
 }
+constexpr size_t kMostBack = RUN / 2 * back_bytes(2);         // heads of more than 320: two a warp
 __device__ __forceinline__ WarpHeadsBack back_heads(unsigned char *smem, int warp, int units) {
     unsigned char *p = smem + size_t(warp) * back_bytes(units);
     WarpHeadsBack h;
@@ -635,10 +636,8 @@ int launch_backward(HeadArgs a, int64_t q_runs, int64_t k_runs, cudaStream_t s) 
     a.units = (RUN + warps - 1) / warps;             // as many heads for each: 8, not 10 and 2
     const size_t smem = size_t(warps) * back_bytes(a.units);
     auto kern = head_backward_kernel<TY, VEC>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return set_cuda_error(e);
-    }
+    if (smem > 48 * 1024)
+        if (const int rc = allow_shared(kern, kMostBack); rc != REPOPS_OK) return rc;
     kern<<<unsigned(q_runs + k_runs), unsigned(warps * 32), smem, s>>>(a, q_runs);
     return check_launch();
 }

@@ -24,6 +24,16 @@ inline int check_launch() {
     return e == cudaSuccess ? REPOPS_OK : set_cuda_error(e);
 }
 
+// Lets a kernel take up to `most` bytes of dynamic shared memory a CTA: what the
+// largest of its launches takes, not what this one needs.  The limit belongs to the
+// kernel, so a smaller one, set by another host thread between this call and the
+// launch, would have the launch refused.
+template <class Kern>
+int allow_shared(Kern kern, size_t most) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+    return e == cudaSuccess ? REPOPS_OK : set_cuda_error(e);
+}
+
 struct DeviceInfo {
     int device = -1;
     int sms = 0;               // multiProcessorCount

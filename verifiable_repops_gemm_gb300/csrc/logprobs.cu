@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kBlock = 1024;         // columns a warp holds at once
 constexpr int kSegment = 4 * kBlock; // columns whose sums are folded together
+constexpr int64_t kMostColumns = int64_t(16000) * kBlock;        // 114 KB of sums and maxima
 constexpr int kMostTop = 32;         // alternatives: one a lane
 constexpr int kMostListed = 256;     // values ranked by counting
 constexpr float kMagic = 393216.0f;   // 1.5 * 2^18: adding it rounds to a 32nd
@@ -799,10 +800,9 @@ int launch_logprobs(const LpArgs &a, cudaStream_t s) {
     }
     const size_t smem = lp_smem(a.segments, a.blocks);
     auto kern = logprobs_kernel<TY, SHIFT>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return set_cuda_error(e);
-    }
+    if (smem > 48 * 1024)
+        if (const int rc = allow_shared(kern, lp_smem(int(kMostColumns / kSegment), int(kMostColumns / kBlock))); rc != REPOPS_OK)
+            return rc;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = ctas;
@@ -833,7 +833,6 @@ int launch_backward(const LpGradArgs &a, bool vec, cudaStream_t s) {
     return check_launch();
 }
 
-constexpr int64_t kMostColumns = int64_t(16000) * kBlock;        // 114 KB of sums and maxima
 constexpr double kLog2e = 0x1.71547652b82fep+0;
 
 bool good_temperature(float t) { return t >= 1e-6f && t <= 1e6f; }
