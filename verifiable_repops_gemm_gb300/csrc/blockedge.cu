@@ -852,16 +852,10 @@ int launch_forward(const EdgeArgs &a, cudaStream_t s) {
     return launch_forward_t<256, 8, VEC>(a, s);
 }
 
-size_t long_row_smem(int64_t n) {
-    const int64_t runs = ceil_div(n, RUN);
-    return size_t(runs + ceil_div(runs, RUN)) * sizeof(float);
-}
-
 template <class Kern, class Args>
 int launch_long(Kern kern, const Args &a, int64_t rows, int64_t n, cudaStream_t s) {
-    const size_t smem = long_row_smem(n);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
+    const size_t smem = run_results_bytes(ceil_div(n, RUN));
+    if (const int rc = allow_shared(kern, run_results_bytes(MAX_GENERIC_RUNS)); rc != REPOPS_OK) return rc;
     kern<<<grid_for_rows(rows), 256, smem, s>>>(a);
     return check_launch();
 }

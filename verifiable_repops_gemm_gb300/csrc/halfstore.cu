@@ -190,6 +190,11 @@ constexpr int ROLL_OSTAGE = 32 * ROLL_OROW;                // 8-byte slots per w
 constexpr int64_t ROLL_MAX_STAGED_WINDOW = 1024;
 static_assert(ROLL_CHUNK % ROLL_GROUP == 0, "whole groups");
 
+constexpr size_t roll_stage_bytes(int64_t window) {        // of a CTA: outputs, then padded words
+    const int64_t words = ROLL_SEG + window - 1;
+    return size_t(ROLL_WARPS) * (size_t(ROLL_OSTAGE) * 8u + size_t(words + words / ROLL_CHUNK + 1) * 4u);
+}
+
 __device__ __forceinline__ int padded(int j) { return j + j / ROLL_CHUNK; }
 
 __global__ void __launch_bounds__(32 * ROLL_WARPS)
@@ -333,13 +338,11 @@ extern "C" int repops_rolling_hash_u32(int64_t rows, int64_t width, const uint32
     const uint64_t bw = powmod61_host(REPOPS_ROLLING_HASH_BASE, window);   // B^W mod P
     if (window <= ROLL_MAX_STAGED_WINDOW) {
         const int64_t segs = (n + ROLL_SEG - 1) / ROLL_SEG;
-        const int wcap = int(ROLL_SEG + window - 1) + int((ROLL_SEG + window - 1) / ROLL_CHUNK) + 1;
-        const size_t smem = size_t(ROLL_WARPS) * (size_t(ROLL_OSTAGE) * 8u + size_t(wcap) * 4u);
-        cudaError_t e = cudaFuncSetAttribute(rolling_hash_staged_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return set_cuda_error(e);
+        const size_t smem = roll_stage_bytes(window);
+        if (const int rc = allow_shared(rolling_hash_staged_kernel, roll_stage_bytes(ROLL_MAX_STAGED_WINDOW)); rc != REPOPS_OK)
+            return rc;
         int per_sm = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rolling_hash_staged_kernel, 32 * ROLL_WARPS, smem);
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rolling_hash_staged_kernel, 32 * ROLL_WARPS, smem);
         if (e != cudaSuccess) return set_cuda_error(e);
         const int blocks = int(std::min<int64_t>((rows * segs + ROLL_WARPS - 1) / ROLL_WARPS,
                                                  int64_t(std::max(per_sm, 1)) * sms));

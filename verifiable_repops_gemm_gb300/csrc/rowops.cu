@@ -894,18 +894,18 @@ int launch_fast(int kind, int64_t rows, int64_t n, const float *x, int64_t ldx, 
     const int pvec = reinterpret_cast<uintptr_t>(gamma) % 16 == 0 && reinterpret_cast<uintptr_t>(beta) % 16 == 0;
     const size_t smem = kStageBytes<T, R>;
     if (kind == 0 && first >= 0)
-        return launch_persistent(softmax_causal_rows_kernel<T, R>, T, smem, rows, s, rows, n, x, ldx, y, ldy,
+        return launch_persistent(softmax_causal_rows_kernel<T, R>, T, smem, smem, rows, s, rows, n, x, ldx, y, ldy,
                                  first, period);
     if (kind == 0)
-        return launch_persistent(softmax_rows_kernel<T, R>, T, smem, rows, s, rows, n, x, ldx, y, ldy);
+        return launch_persistent(softmax_rows_kernel<T, R>, T, smem, smem, rows, s, rows, n, x, ldx, y, ldy);
     if (kind == 1) {
         const size_t p = pvec ? kParamBytes<T, R, 2> : 0;
-        return launch_persistent(layernorm_rows_kernel<T, R>, T, smem + p, rows, s, rows, n, x, ldx, gamma, beta,
-                                 eps, y, ldy, pvec, int(p != 0));
+        return launch_persistent(layernorm_rows_kernel<T, R>, T, smem + p, smem + kParamBytes<T, R, 2>, rows, s, rows, n,
+                                 x, ldx, gamma, beta, eps, y, ldy, pvec, int(p != 0));
     }
     const size_t p = pvec ? kParamBytes<T, R, 1> : 0;
-    return launch_persistent(rmsnorm_rows_kernel<T, R>, T, smem + p, rows, s, rows, n, x, ldx, gamma, eps, y, ldy,
-                             pvec, int(p != 0));
+    return launch_persistent(rmsnorm_rows_kernel<T, R>, T, smem + p, smem + kParamBytes<T, R, 1>, rows, s, rows, n, x, ldx,
+                             gamma, eps, y, ldy, pvec, int(p != 0));
 }
 
 int run_rows(int kind, int64_t rows, int64_t n, const float *x, int64_t ldx, const float *gamma, const float *beta,
@@ -925,11 +925,11 @@ int run_rows(int kind, int64_t rows, int64_t n, const float *x, int64_t ldx, con
     }
     // its shared buffer holds the row's run results and their group results:
     // sized from the row's own run count, whatever the path choice
-    const size_t smem = size_t(runs + (runs + RUN - 1) / RUN) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(rows_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
+    const size_t smem = run_results_bytes(runs);
+    int rc = allow_shared(rows_generic_kernel, run_results_bytes(MAX_GENERIC_RUNS));
+    if (rc != REPOPS_OK) return rc;
     unsigned *status = nullptr;
-    int rc = status_word_address(&status);
+    rc = status_word_address(&status);
     if (rc != REPOPS_OK) return rc;
     rows_generic_kernel<<<grid_for_rows(rows), 256, smem, s>>>(kind, rows, n, x, ldx, gamma, beta, eps, y, ldy,
                                                                first, period, status);
@@ -960,6 +960,7 @@ extern "C" int repops_softmax_rows_causal_f32(int64_t rows, int64_t cols, const 
         unsigned *status = nullptr;
         if ((rc = status_word_address(&status)) != REPOPS_OK) return rc;
         return launch_persistent(softmax_causal_warp_kernel, 32 * WARP_CAUSAL_WARPS, smem,
+                                 size_t(WARP_CAUSAL_WARPS) * WARP_CAUSAL_MAX_COLS * sizeof(float),
                                  (rows + WARP_CAUSAL_WARPS - 1) / WARP_CAUSAL_WARPS, stream, rows, int(cols), x, ldx,
                                  y, ldy, first, period, row_floats, status);
     }
@@ -1054,7 +1055,8 @@ extern "C" int repops_rmsnorm_backward_f32(int64_t rows, int64_t cols, const flo
                         reinterpret_cast<uintptr_t>(gamma) % 16 == 0 && (!res || rows_vec_ok(res, ldres, dx, lddx));
     if (staged) {
         auto go = [&](auto kern, int T) {
-            return launch_persistent(kern, T, size_t(4) * T * RUN * sizeof(float), rows, stream, rows, cols, x, ldx,
+            const size_t smem = size_t(4) * T * RUN * sizeof(float);
+            return launch_persistent(kern, T, smem, smem, rows, stream, rows, cols, x, ldx,
                                      gamma, eps, dy, lddy, res, ldres, dx, lddx, dyxh, ldp);
         };
         if (runs <= 32) return go(rmsnorm_backward_staged_kernel<32>, 32);
@@ -1062,9 +1064,8 @@ extern "C" int repops_rmsnorm_backward_f32(int64_t rows, int64_t cols, const flo
         if (runs <= 128) return go(rmsnorm_backward_staged_kernel<128>, 128);
         return go(rmsnorm_backward_staged_kernel<256>, 256);
     }
-    const size_t smem = size_t(runs + (runs + RUN - 1) / RUN) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(rmsnorm_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
+    const size_t smem = run_results_bytes(runs);
+    if (const int rc = allow_shared(rmsnorm_backward_kernel, run_results_bytes(MAX_GENERIC_RUNS)); rc != REPOPS_OK) return rc;
     unsigned *status = nullptr;
     if (status_word_address(&status) != REPOPS_OK) status = nullptr;
     rmsnorm_backward_kernel<<<grid_for_rows(rows), 256, smem, stream>>>(rows, cols, x, ldx, gamma, eps, dy, lddy, res,
@@ -1089,7 +1090,8 @@ int softmax_backward(int64_t rows, int64_t cols, const float *p, int64_t ldp, co
     const bool staged = runs <= 256 && rows_vec_ok(p, ldp, ds, ldds) && rows_vec_ok(dp, lddp, ds, ldds);
     if (staged) {
         auto go = [&](auto kern, int T) {
-            return launch_persistent(kern, T, size_t(2) * T * RUN * sizeof(float), rows, stream, rows, cols, p,
+            const size_t smem = size_t(2) * T * RUN * sizeof(float);
+            return launch_persistent(kern, T, smem, smem, rows, stream, rows, cols, p,
                                      ldp, dp, lddp, ds, ldds, first, period);
         };
         if (runs <= 32) return go(softmax_backward_staged_kernel<32>, 32);
@@ -1097,9 +1099,8 @@ int softmax_backward(int64_t rows, int64_t cols, const float *p, int64_t ldp, co
         if (runs <= 128) return go(softmax_backward_staged_kernel<128>, 128);
         return go(softmax_backward_staged_kernel<256>, 256);
     }
-    const size_t smem = size_t(runs + (runs + RUN - 1) / RUN) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(softmax_backward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
+    const size_t smem = run_results_bytes(runs);
+    if (const int rc = allow_shared(softmax_backward_kernel, run_results_bytes(MAX_GENERIC_RUNS)); rc != REPOPS_OK) return rc;
     unsigned *status = nullptr;
     if (status_word_address(&status) != REPOPS_OK) status = nullptr;
     softmax_backward_kernel<<<grid_for_rows(rows), 256, smem, stream>>>(rows, cols, p, ldp, dp, lddp, ds, ldds,

@@ -103,14 +103,17 @@ colsum_pass_kernel(int64_t rows, int64_t cols, const float *__restrict__ x, int6
     return int(std::min<int64_t>(rows, int64_t(sms) * 32));
 }
 
+// Bytes of a row's run results and their groups' results.
+constexpr size_t run_results_bytes(int64_t runs) { return size_t(runs + (runs + RUN - 1) / RUN) * sizeof(float); }
+
 // Launches `kern` with as many CTAs as fit on the device at once (at most one
-// per row); each CTA then strides over the rows.
+// per row); each CTA then strides over the rows.  `most`: the dynamic shared memory
+// of the kernel's largest launch.
 template <class Kern, class... Args>
-int launch_persistent(Kern kern, int threads, size_t smem, int64_t rows, cudaStream_t s, Args... args) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return set_cuda_error(e);
+int launch_persistent(Kern kern, int threads, size_t smem, size_t most, int64_t rows, cudaStream_t s, Args... args) {
+    if (const int rc = allow_shared(kern, most); rc != REPOPS_OK) return rc;
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
     if (e != cudaSuccess) return set_cuda_error(e);
     DeviceInfo di;
     const int sms = current_device_info(&di) == REPOPS_OK ? di.sms : 152;
