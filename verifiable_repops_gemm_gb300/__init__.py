@@ -1325,12 +1325,17 @@ def rmsnorm_residual_backward(dy, dh, y, f, pre_gain, eps: float = 1e-5, *, post
 ADAMW_GROUP = 128   # elements that share a scale in 8-bit moments
 
 
-def _tensor_list(ts, dtype, here, name):
-    """A list of contiguous tensors of one dtype on the current device (a single
-    tensor is a list of one)."""
+def _listed(ts):
+    """Tensors given one by one, as a list or by an iterator, as what can be gone
+    through more than once (a single tensor: a list of one)."""
     import torch
-    if isinstance(ts, torch.Tensor):
-        ts = (ts,)
+    return (ts,) if isinstance(ts, torch.Tensor) else ts if isinstance(ts, (list, tuple)) else list(ts)
+
+
+def _tensor_list(ts, dtype, here, name):
+    """A list of contiguous tensors of one dtype on the current device."""
+    import torch
+    ts = _listed(ts)
     kind = torch.Tensor          # maps over its methods: lists of hundreds of tensors take microseconds here
     if not ({*map(operator.attrgetter("dtype"), ts)} <= {dtype} and {*map(kind.get_device, ts)} <= {here} and
             all(map(kind.is_contiguous, ts))):
@@ -1369,12 +1374,11 @@ def adamw_scalars(step: int, lr: float, betas=(0.9, 0.999), seed: int = 0):
 
 
 def adamw_state(params, bits: int = 32) -> dict:
-    """Zero moments of adamw() for a list of parameters (or one), as its keyword
-    arguments: m and v, with bits=8 in a byte each and m_scales, v_scales for
-    every ADAMW_GROUP elements of a tensor."""
+    """Zero moments of adamw() for parameters (a list, an iterator of them or one), as
+    its keyword arguments: m and v, with bits=8 in a byte each and m_scales, v_scales
+    for every ADAMW_GROUP elements of a tensor."""
     import torch
-    if isinstance(params, torch.Tensor):
-        params = [params]
+    params = _listed(params)
     if bits == 32:
         return {k: [torch.zeros_like(p) for p in params] for k in ("m", "v")}
     if bits != 8:
@@ -1393,9 +1397,9 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
           stream=None):
     """One AdamW step over a list of tensors at once, in place (repops_adamw).
 
-    theta: float32 CUDA tensors, contiguous.  grads: a list of gradients shaped
-    like them (float32, float16 or bfloat16), or one such list for each of several
-    contributors, whose left fold in `order` (default: as given) divided by their
+    theta: float32 CUDA tensors, contiguous (a list, or an iterator of them, as
+    everywhere here).  grads: a list of gradients shaped like them (float32, float16
+    or bfloat16), or one such list for each of several contributors, whose left fold in `order` (default: as given) divided by their
     count is the gradient.  m, v: the moments (adamw_state), float32, or uint8 with
     m_scales and v_scales.  weight_decay: a number, or one for each tensor.
     step counts from 1; with seed it also keys the rounding of 8-bit moments.
@@ -1405,10 +1409,9 @@ def adamw(theta, grads, m, v, *, step: int = None, lr: float = None, betas=(0.9,
     here = torch.cuda.current_device()
     theta = _tensor_list(theta, torch.float32, here, "theta")
     n = len(theta)
-    if isinstance(grads, torch.Tensor) or not len(grads) or isinstance(grads[0], torch.Tensor):
-        grads = [grads]
-    first = grads[0]
-    first = first if isinstance(first, torch.Tensor) else first[0] if len(first) else None
+    grads = _listed(grads)
+    grads = [grads] if not grads or isinstance(grads[0], torch.Tensor) else [_listed(g) for g in grads]
+    first = grads[0][0] if grads[0] else None
     gtype = torch.float32 if first is None else first.dtype
     kind = _storage_type(gtype)
     grads = [_tensor_list(g, gtype, here, "grads") for g in grads]
