@@ -194,6 +194,8 @@ def train_step(model: Model, contributions, eta: float, ws: Workspace, grads=Non
     int64 targets)], in any order.  Computes every contributor's gradient, folds
     them in DID order into the mean, applies SGD with eta (or the optimizer's step)
     to theta in place and returns (root of the new theta, the order)."""
+    if model.vocab and any(not d.is_floating_point() and d.dtype != torch.int64 for _, _, d in contributions):
+        raise ValueError("targets must be int64")    # not an upstream gradient of whole numbers
     if grads is None:
         grads = [model.gradient_buffer() for _ in contributions]
     for (did, x, d), g in zip(contributions, grads):
