@@ -1244,8 +1244,9 @@ int repops_token_logprobs_backward(int64_t rows, int64_t cols, const void *x, in
  *   r <= low: f / factor;  r >= high: f;  between: the mean of both weighted by
  *   (r - low) / (high - low) on f
  * in binary64 (the weighted sum as f/factor + w * (f - f/factor)), rounded once.
- * original == 0: f / factor for all.  factor > 0, original >= 0, 0 <= low < high
- * (not looked at when original is 0), else INVALID_ARG. */
+ * original == 0: f / factor for all.  1 to 2^24 pairs, 0 < factor <= 1e30, 0 <=
+ * original <= 1e30, 0 <= low < high <= 1e30 (not looked at when original is 0), freq on
+ * its elements' boundary, else INVALID_ARG. */
 int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, float factor, float original,
                                       float low, float high, cudaStream_t stream);
 

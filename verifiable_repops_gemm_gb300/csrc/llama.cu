@@ -261,8 +261,9 @@ extern "C" int repops_rope_frequencies_f32(int64_t pairs, float ln_base, float *
 
 extern "C" int repops_rope_scale_frequencies_f32(int64_t pairs, float *freq, float factor, float original, float low,
                                                  float high, cudaStream_t stream) {
-    if (pairs < 1 || pairs > (int64_t(1) << 24) || !freq || !(factor > 0.0f) || !(factor <= 1e30f) || !(original >= 0.0f) ||
-        !(original <= 1e30f) || (original > 0.0f && !(low >= 0.0f && low < high && high <= 1e30f)))
+    if (pairs < 1 || pairs > (int64_t(1) << 24) || !freq || reinterpret_cast<uintptr_t>(freq) % 4 != 0 ||
+        !(factor > 0.0f) || !(factor <= 1e30f) || !(original >= 0.0f) || !(original <= 1e30f) ||
+        (original > 0.0f && !(low >= 0.0f && low < high && high <= 1e30f)))
         return REPOPS_ERR_INVALID_ARG;
     const int blocks = int(std::min<int64_t>((pairs + 255) / 256, 1024));
     rope_scale_kernel<<<blocks, 256, 0, stream>>>(pairs, freq, factor, original, low, high);
