@@ -184,8 +184,10 @@ class AdamW:
         self.steps += 1
 
     def roots(self):
-        """The Merkle root of each of the moments' buffers: what, with theta's, a
-        replay of later steps has to start from."""
+        """The Merkle root of each of the moments' buffers.  A replay of later steps has to
+        start from these and theta's, and from what they do not hold: `steps` (the bias
+        corrections and the dither hang on it) and the constructor's arguments.  An
+        optimiser built alike goes on where `state` is copied in and `steps` set."""
         return {name: merkle_sha256(t) for name, t in self.state.items()}
 
 
