@@ -19,11 +19,13 @@
 // CTA takes 32 heads of one gain, a run of the gain's column sum, and so leaves a 32nd
 // of the terms as run results instead of writing them all.
 //
-// Measured, 4096 rows of 32 query and 8 key heads of 64 in float32, graph-replayed: 20.7
-// us forward (4.1 TB/s; a CTA's heads in common, barriers between the phases: 24.8), 39
-// us with the gains' gradients backward (3.2 TB/s; 47 with a CTA's in common, 42 with
-// each head's loads behind the one's before).  What bounds them now are the latencies of
-// a warp's phases together with the issue of some 37 instructions a value forward and 60
+// Measured, 4096 rows of 32 query and 8 key heads of 64 in float32, a ninth of them
+// without a position, graph-replayed: 20.7 us forward (24.8 with a CTA's heads in common
+// and barriers between the phases), 39 us with the gains' gradients backward (47 with a
+// CTA's in common, 42 with each head's loads behind the one's before); with all rows
+// live 24.7 and 43 (3.4 and 2.9 TB/s), in bfloat16 22.5 and 41, the rotation alone 17.8
+// and 16.5.  What bounds them now are the latencies of
+// a warp's phases together with the issue of some 37 instructions a value forward and 65
 // backward, most of them addresses, swizzles and the trees' additions one by one.
 #include <algorithm>
 

@@ -430,7 +430,7 @@ __device__ __forceinline__ float ln_fixed(float S) {
     p = __fadd_rn(__fmul_rn(p, zz), 1.0f / 5);
     p = __fadd_rn(__fmul_rn(p, zz), 1.0f / 3);
     const float lnF = __fadd_rn(r, __fmul_rn(r, __fmul_rn(zz, p)));
-    // E * kLn2High is exact: 13 bits by 8
+    // E * kLn2High is exact: 15 bits by 8
     return __fadd_rn(__fmul_rn(float(E), kLn2High), __fadd_rn(lnF, __fmul_rn(float(E), kLn2Low)));
 }
 
@@ -577,9 +577,9 @@ __global__ void __launch_bounds__(256) logprobs_kernel(const LpArgs a) {
     if (!a.top) return;
     // which blocks hold the alternatives: by counting, a thread of the warps that have no
     // sums to end for each block, or one after another by the last warp.  A step of the
-    // count takes about a twelfth of finding one.  1024 rows of 32 blocks, 20 wanted, 33.7
-    // us and 40.7; one row of 128 blocks, 8 wanted, 12.2 and 10.8; 4096 rows of 128 by two
-    // warps each, 20 wanted, 386 and 371
+    // count takes about a twelfth of finding one.  1024 rows of 32 blocks, 20 wanted, 35 us
+    // and 43; 4096 such rows 109 and 119; one row of 128 blocks, 8 wanted, 12.3 either way;
+    // 4096 rows of 128, 20 wanted, 350 and 345, one wanted 334 and 322
     const int chosen = min(a.top, a.blocks);
     const int others = 32;           // threads of the first warp, which has the sums
     if (warps > 1 && a.blocks < 12 * kMostTop &&
